@@ -11,12 +11,15 @@ imported without a GPU or a built library.
 """
 import importlib
 
-__all__ = ["SharedKVPool", "DecoderTails", "PrefixPages", "splitkv_merge", "native", "workloads", "build"]
+__all__ = ["SharedKVPool", "QuantizedKVPool", "DecoderTails", "PrefixPages", "splitkv_merge", "native", "workloads",
+           "build"]
 
 
 def __getattr__(name):
     if name in ("SharedKVPool", "DecoderTails", "PrefixPages", "splitkv_merge"):
         return getattr(importlib.import_module(".pool", __name__), name)
+    if name == "QuantizedKVPool":
+        return importlib.import_module(".q8", __name__).QuantizedKVPool
     if name == "native":
         return importlib.import_module("._native", __name__)
     if name in ("workloads", "build"):

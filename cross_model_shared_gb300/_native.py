@@ -37,7 +37,9 @@ EXPORTS = [
     "shkv_decode_attention_tails", "shkv_pages_create", "shkv_pages_destroy", "shkv_pages_acquire",
     "shkv_pages_publish", "shkv_pages_release", "shkv_pages_alloc_transfer", "shkv_pages_stats",
     "shkv_pages_refcount", "shkv_prefill_attention", "shkv_pool_set_decode_consumer",
-    "shkv_partition_requests", "shkv_selftest_bounded_wait",
+    "shkv_partition_requests", "shkv_selftest_bounded_wait", "shkv_q8_pool_create", "shkv_q8_pool_destroy",
+    "shkv_q8_pool_set_seq_lens", "shkv_q8_pool_get_seq_lens", "shkv_q8_check_errors", "shkv_q8_append_kv",
+    "shkv_q8_read_kv", "shkv_q8_workspace_size", "shkv_q8_decode_attention", "shkv_q8_chunk_attention",
 ]
 
 SHKV_CONSUMER_AUTO = -1
@@ -58,6 +60,24 @@ class shkv_pool_config(ctypes.Structure):
         ("max_pages_per_seq", ctypes.c_int32),
         ("k_pages", ctypes.c_void_p),
         ("v_pages", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p),
+        ("error_word", ctypes.c_void_p),
+        ("initial_seq_lens", ctypes.c_void_p),
+    ]
+
+
+class shkv_q8_pool_config(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("max_batch", ctypes.c_int32),
+        ("max_pages_per_seq", ctypes.c_int32),
+        ("k_pages", ctypes.c_void_p),
+        ("v_pages", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
         ("block_table", ctypes.c_void_p),
         ("seq_lens", ctypes.c_void_p),
         ("error_word", ctypes.c_void_p),
@@ -140,6 +160,17 @@ def load() -> ctypes.CDLL:
         "shkv_pages_stats": [vp, ctypes.POINTER(shkv_pages_info)],
         "shkv_pages_refcount": [vp, i32, ctypes.POINTER(i32)],
         "shkv_prefill_attention": [vp, i32, i32, i32, vp, ctypes.c_float, vp, vp, vp],
+        "shkv_q8_pool_create": [ctypes.POINTER(shkv_q8_pool_config), ctypes.POINTER(vp)],
+        "shkv_q8_pool_destroy": [vp],
+        "shkv_q8_pool_set_seq_lens": [vp, i32, i32p, vp],
+        "shkv_q8_pool_get_seq_lens": [vp, i32, i32p],
+        "shkv_q8_check_errors": [vp, vp, u32p],
+        "shkv_q8_append_kv": [vp, i32, i32p, i32p, vp, ctypes.c_int64, vp, ctypes.c_int64, vp],
+        "shkv_q8_read_kv": [vp, i32, i32p, i32p, vp, ctypes.c_int64, vp, ctypes.c_int64, vp],
+        "shkv_q8_workspace_size": [vp, ctypes.POINTER(ctypes.c_size_t)],
+        "shkv_q8_decode_attention": [vp, i32, i32, i32, vp, ctypes.c_float, vp, vp, vp, ctypes.c_size_t, vp],
+        "shkv_q8_chunk_attention": [vp, i32, i32p, i32, vp, ctypes.c_int64, ctypes.c_float, vp, vp, vp,
+                                    ctypes.c_size_t, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -311,3 +342,60 @@ def shkv_prefill_attention(pool: int, batch: int, n_new: int, hq: int, q: int, s
                            lse_out: int, stream: int) -> None:
     _check(load().shkv_prefill_attention(pool, batch, n_new, hq, q, scale, out, lse_out, stream),
            "shkv_prefill_attention")
+
+
+def shkv_q8_pool_create(cfg: shkv_q8_pool_config) -> int:
+    h = ctypes.c_void_p()
+    _check(load().shkv_q8_pool_create(ctypes.byref(cfg), ctypes.byref(h)), "shkv_q8_pool_create")
+    return h.value
+
+
+def shkv_q8_pool_destroy(pool: int) -> None:
+    _check(load().shkv_q8_pool_destroy(pool), "shkv_q8_pool_destroy")
+
+
+def shkv_q8_pool_set_seq_lens(pool: int, batch: int, lens_ptr: int, stream: int) -> None:
+    _check(load().shkv_q8_pool_set_seq_lens(pool, batch, lens_ptr, stream), "shkv_q8_pool_set_seq_lens")
+
+
+def shkv_q8_pool_get_seq_lens(pool: int, batch: int, lens_ptr: int) -> None:
+    _check(load().shkv_q8_pool_get_seq_lens(pool, batch, lens_ptr), "shkv_q8_pool_get_seq_lens")
+
+
+def shkv_q8_check_errors(pool: int, stream: int) -> int:
+    """Returns the device error bits (0 if none); raises only on CUDA errors."""
+    flags = ctypes.c_uint32()
+    st = load().shkv_q8_check_errors(pool, stream, ctypes.byref(flags))
+    if st not in (SHKV_OK, SHKV_ERR_DEVICE):
+        raise ShkvError(st, "shkv_q8_check_errors")
+    return flags.value
+
+
+def shkv_q8_append_kv(pool: int, batch: int, start: int, new_lens: int, k_new: int, k_stride: int, v_new: int,
+                      v_stride: int, stream: int) -> None:
+    _check(load().shkv_q8_append_kv(pool, batch, start, new_lens, k_new, k_stride, v_new, v_stride, stream),
+           "shkv_q8_append_kv")
+
+
+def shkv_q8_read_kv(pool: int, batch: int, start: int, lens: int, k_out: int, k_stride: int, v_out: int,
+                    v_stride: int, stream: int) -> None:
+    _check(load().shkv_q8_read_kv(pool, batch, start, lens, k_out, k_stride, v_out, v_stride, stream),
+           "shkv_q8_read_kv")
+
+
+def shkv_q8_workspace_size(pool: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().shkv_q8_workspace_size(pool, ctypes.byref(n)), "shkv_q8_workspace_size")
+    return n.value
+
+
+def shkv_q8_decode_attention(pool: int, batch: int, n_models: int, hq: int, q: int, scale: float, out: int,
+                             lse_out: int, workspace: int, workspace_bytes: int, stream: int) -> None:
+    _check(load().shkv_q8_decode_attention(pool, batch, n_models, hq, q, scale, out, lse_out, workspace,
+                                           workspace_bytes, stream), "shkv_q8_decode_attention")
+
+
+def shkv_q8_chunk_attention(pool: int, batch: int, new_lens: int, hq: int, q: int, q_stride: int, scale: float,
+                            out: int, lse_out: int, workspace: int, workspace_bytes: int, stream: int) -> None:
+    _check(load().shkv_q8_chunk_attention(pool, batch, new_lens, hq, q, q_stride, scale, out, lse_out, workspace,
+                                          workspace_bytes, stream), "shkv_q8_chunk_attention")

@@ -1,0 +1,343 @@
+// q8_host.cu -- the C ABI of the 8-bit KV cache: argument checks and kernel
+// launches.  Declarations and their contracts are in include/shkv.h.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <algorithm>
+#include <new>
+#include <vector>
+
+#include "host_shared.h"
+#include "q8.cuh"
+#include "shkv.h"
+
+namespace shkv {
+cudaError_t launch_q8_cache(const Q8CacheParams &p, bool read, int num_sms, cudaStream_t stream);
+cudaError_t launch_q8_attn(const Q8AttnParams &p, int max_rows, cudaStream_t stream);
+}  // namespace shkv
+
+using namespace shkv;
+
+struct shkv_q8_pool {
+    shkv_q8_pool_config cfg;
+    int device;
+    int num_sms;
+    std::vector<int32_t> lens;       // host copy of seq_lens
+};
+
+namespace {
+
+bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+shkv_status status_of(cudaError_t e) { return e == cudaSuccess ? SHKV_OK : SHKV_ERR_CUDA; }
+
+bool on_pool_device(const shkv_q8_pool *pool)
+{
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess && dev == pool->device;
+}
+
+int64_t capacity(const shkv_q8_pool *pool) { return (int64_t)pool->cfg.max_pages_per_seq * pool->cfg.page_size; }
+
+// Checks and parameters common to append and read.
+shkv_status cache_params(const shkv_q8_pool *pool, int32_t batch, const int32_t *start, const int32_t *lens,
+                         const void *k, int64_t k_stride, const void *v, int64_t v_stride, Q8CacheParams &p)
+{
+    const shkv_q8_pool_config &c = pool->cfg;
+    const int64_t row = (int64_t)c.num_kv_heads * c.head_dim;
+    if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8)
+        return SHKV_ERR_INVALID_ARG;
+    memset(&p, 0, sizeof p);
+    int64_t total = 0;
+    for (int b = 0; b < batch; ++b) {
+        if (lens[b] < 0 || (start && start[b] < 0))
+            return SHKV_ERR_INVALID_ARG;
+        p.tok0[b] = (int32_t)total;
+        p.start[b] = start ? start[b] : pool->lens[b];
+        p.old_len[b] = pool->lens[b];
+        total += lens[b];
+        if (total * 2 * c.num_kv_heads > INT32_MAX)
+            return SHKV_ERR_UNSUPPORTED;
+    }
+    p.tok0[batch] = (int32_t)total;
+    if (total > 0 && (!k || !v || !aligned(k, 16) || !aligned(v, 16)))
+        return SHKV_ERR_INVALID_ARG;
+    p.k = static_cast<__nv_bfloat16 *>(const_cast<void *>(k));
+    p.v = static_cast<__nv_bfloat16 *>(const_cast<void *>(v));
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.k_pages = static_cast<uint8_t *>(c.k_pages);
+    p.v_pages = static_cast<uint8_t *>(c.v_pages);
+    p.scales = static_cast<uint8_t *>(c.scales);
+    p.block_table = c.block_table;
+    p.seq_lens = c.seq_lens;
+    p.err = c.error_word;
+    p.batch = batch;
+    p.hkv = c.num_kv_heads;
+    p.head_dim = c.head_dim;
+    p.page_size = c.page_size;
+    p.max_pages = c.max_pages_per_seq;
+    p.num_pages = c.num_pages;
+    return SHKV_OK;
+}
+
+shkv_status launch_cache(const shkv_q8_pool *pool, const Q8CacheParams &p, bool read, void *stream)
+{
+    if (launch_q8_cache(p, read, pool->num_sms, (cudaStream_t)stream) != cudaSuccess)
+        return SHKV_ERR_CUDA;
+    const size_t tokens = (size_t)p.tok0[p.batch];
+    const size_t row = (size_t)p.hkv * p.head_dim;
+    const size_t kb = tokens ? ((tokens - 1) * p.k_stride + row) * 2 : 0;
+    const size_t vb = tokens ? ((tokens - 1) * p.v_stride + row) * 2 : 0;
+    record_stream_use(stream, {span_of(p.k, kb), span_of(p.v, vb)});
+    return SHKV_OK;
+}
+
+constexpr int32_t kMaxDecodeRows = 64;     // stacked rows per KV head of a decode
+
+size_t workspace_need(const shkv_q8_pool *) { return 256; }
+
+// Both attentions: n_q query tokens of request b start at query token q0[b].
+shkv_status attention(shkv_q8_pool *pool, Q8AttnParams &p, int32_t hq, const void *q, int64_t q_stride, float scale,
+                      void *out, float *lse_out, void *workspace, size_t ws_bytes, void *stream)
+{
+    const shkv_q8_pool_config &c = pool->cfg;
+    if (!q || !out || !workspace || !aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) ||
+        !aligned(lse_out, 4) || q_stride < (int64_t)hq * c.head_dim || q_stride % 8 || !isfinite(scale) ||
+        ws_bytes < workspace_need(pool))
+        return SHKV_ERR_INVALID_ARG;
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.q_stride = q_stride;
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.lse_out = lse_out;
+    p.k_pages = static_cast<const uint8_t *>(c.k_pages);
+    p.v_pages = static_cast<const uint8_t *>(c.v_pages);
+    p.scales = static_cast<const uint8_t *>(c.scales);
+    p.block_table = c.block_table;
+    p.seq_lens = c.seq_lens;
+    p.err = c.error_word;
+    p.hq = hq;
+    p.hkv = c.num_kv_heads;
+    p.group = hq / c.num_kv_heads;
+    p.head_dim = c.head_dim;
+    p.page_size = c.page_size;
+    p.max_pages = c.max_pages_per_seq;
+    p.num_pages = c.num_pages;
+    p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    int max_rows = 0;
+    int64_t tokens = 0;
+    for (int b = 0; b < p.batch; ++b) {
+        max_rows = std::max(max_rows, p.n_q[b] * p.group);
+        tokens += p.n_q[b];
+    }
+    if (launch_q8_attn(p, max_rows, (cudaStream_t)stream) != cudaSuccess)
+        return SHKV_ERR_CUDA;
+    const size_t row = (size_t)hq * c.head_dim;
+    record_stream_use(stream, {span_of(workspace, workspace_need(pool)),
+                               span_of(q, ((size_t)(tokens - 1) * q_stride + row) * 2),
+                               span_of(out, (size_t)tokens * row * 2), span_of(lse_out, (size_t)tokens * hq * 4)});
+    return SHKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+shkv_status shkv_q8_pool_create(const shkv_q8_pool_config *cfg, shkv_q8_pool **out)
+{
+    if (!cfg || !out)
+        return SHKV_ERR_INVALID_ARG;
+    *out = nullptr;
+    const shkv_q8_pool_config &c = *cfg;
+    if (c.num_pages <= 0 || c.num_kv_heads <= 0 || c.max_batch <= 0 || c.max_pages_per_seq <= 0 || !c.k_pages ||
+        !c.v_pages || !c.scales || !c.block_table || !c.seq_lens || !c.error_word)
+        return SHKV_ERR_INVALID_ARG;
+    if (!aligned(c.k_pages, 16) || !aligned(c.v_pages, 16) || !aligned(c.scales, 16) || !aligned(c.block_table, 4) ||
+        !aligned(c.seq_lens, 4) || !aligned(c.error_word, 4))
+        return SHKV_ERR_INVALID_ARG;
+    if ((c.page_size != 16 && c.page_size != 32) || (c.head_dim != 64 && c.head_dim != 128) ||
+        c.max_batch > SHKV_MAX_BATCH || (int64_t)c.num_pages * c.num_kv_heads * c.page_size > INT32_MAX ||
+        (int64_t)c.max_pages_per_seq * c.page_size > INT32_MAX)
+        return SHKV_ERR_UNSUPPORTED;
+    if (c.initial_seq_lens)
+        for (int b = 0; b < c.max_batch; ++b)
+            if (c.initial_seq_lens[b] < 0 ||
+                (int64_t)c.initial_seq_lens[b] > (int64_t)c.max_pages_per_seq * c.page_size)
+                return SHKV_ERR_CAPACITY;
+    shkv_q8_pool *pool = new (std::nothrow) shkv_q8_pool();
+    if (!pool)
+        return SHKV_ERR_INVALID_ARG;
+    pool->cfg = c;
+    pool->cfg.initial_seq_lens = nullptr;
+    pool->lens.assign(c.max_batch, 0);
+    if (c.initial_seq_lens)
+        memcpy(pool->lens.data(), c.initial_seq_lens, sizeof(int32_t) * c.max_batch);
+    if (cudaGetDevice(&pool->device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&pool->num_sms, cudaDevAttrMultiProcessorCount, pool->device) != cudaSuccess ||
+        cudaMemcpy(c.seq_lens, pool->lens.data(), sizeof(int32_t) * c.max_batch, cudaMemcpyHostToDevice) !=
+            cudaSuccess ||
+        cudaMemset(c.error_word, 0, sizeof(uint32_t)) != cudaSuccess) {
+        delete pool;
+        return SHKV_ERR_CUDA;
+    }
+    *out = pool;
+    return SHKV_OK;
+}
+
+shkv_status shkv_q8_pool_destroy(shkv_q8_pool *pool)
+{
+    if (!pool)
+        return SHKV_ERR_INVALID_ARG;
+    delete pool;
+    return SHKV_OK;
+}
+
+shkv_status shkv_q8_pool_set_seq_lens(shkv_q8_pool *pool, int32_t batch, const int32_t *lens, void *stream)
+{
+    if (!pool || !lens || batch < 0 || batch > pool->cfg.max_batch || !on_pool_device(pool))
+        return SHKV_ERR_INVALID_ARG;
+    for (int b = 0; b < batch; ++b)
+        if (lens[b] < 0 || lens[b] > capacity(pool))
+            return SHKV_ERR_CAPACITY;
+    if (batch == 0)
+        return SHKV_OK;
+    memcpy(pool->lens.data(), lens, sizeof(int32_t) * batch);
+    cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e =
+        cudaMemcpyAsync(pool->cfg.seq_lens, pool->lens.data(), sizeof(int32_t) * batch, cudaMemcpyHostToDevice, st);
+    if (e == cudaSuccess)
+        e = cudaStreamSynchronize(st);
+    return status_of(e);
+}
+
+shkv_status shkv_q8_pool_get_seq_lens(const shkv_q8_pool *pool, int32_t batch, int32_t *lens)
+{
+    if (!pool || !lens || batch < 0 || batch > pool->cfg.max_batch)
+        return SHKV_ERR_INVALID_ARG;
+    memcpy(lens, pool->lens.data(), sizeof(int32_t) * batch);
+    return SHKV_OK;
+}
+
+shkv_status shkv_q8_append_kv(shkv_q8_pool *pool, int32_t batch, const int32_t *start, const int32_t *new_lens,
+                              const void *k_new, int64_t k_stride, const void *v_new, int64_t v_stride, void *stream)
+{
+    if (!pool || !new_lens || batch < 0 || batch > pool->cfg.max_batch || !on_pool_device(pool))
+        return SHKV_ERR_INVALID_ARG;
+    Q8CacheParams p;
+    const shkv_status st = cache_params(pool, batch, start, new_lens, k_new, k_stride, v_new, v_stride, p);
+    if (st != SHKV_OK)
+        return st;
+    bool moves = false;
+    for (int b = 0; b < batch; ++b) {
+        if (p.start[b] > pool->lens[b])
+            return SHKV_ERR_INVALID_ARG;     // would leave a gap of unwritten tokens
+        if ((int64_t)p.start[b] + new_lens[b] > capacity(pool))
+            return SHKV_ERR_CAPACITY;
+        moves = moves || p.start[b] != pool->lens[b] || new_lens[b] > 0;
+    }
+    if (!moves)
+        return SHKV_OK;
+    const shkv_status ls = launch_cache(pool, p, false, stream);
+    if (ls == SHKV_OK)
+        for (int b = 0; b < batch; ++b)
+            pool->lens[b] = p.start[b] + new_lens[b];
+    return ls;
+}
+
+shkv_status shkv_q8_read_kv(shkv_q8_pool *pool, int32_t batch, const int32_t *start, const int32_t *lens, void *k_out,
+                            int64_t k_stride, void *v_out, int64_t v_stride, void *stream)
+{
+    if (!pool || !start || !lens || batch < 0 || batch > pool->cfg.max_batch || !on_pool_device(pool))
+        return SHKV_ERR_INVALID_ARG;
+    Q8CacheParams p;
+    const shkv_status st = cache_params(pool, batch, start, lens, k_out, k_stride, v_out, v_stride, p);
+    if (st != SHKV_OK)
+        return st;
+    for (int b = 0; b < batch; ++b)
+        if ((int64_t)start[b] + lens[b] > pool->lens[b])
+            return SHKV_ERR_INVALID_ARG;
+    if (p.tok0[batch] == 0)
+        return SHKV_OK;
+    return launch_cache(pool, p, true, stream);
+}
+
+shkv_status shkv_q8_workspace_size(const shkv_q8_pool *pool, size_t *bytes)
+{
+    if (!pool || !bytes)
+        return SHKV_ERR_INVALID_ARG;
+    *bytes = workspace_need(pool);
+    return SHKV_OK;
+}
+
+shkv_status shkv_q8_decode_attention(shkv_q8_pool *pool, int32_t batch, int32_t n_models, int32_t hq_per_model,
+                                     const void *q, float scale, void *out, float *lse_out, void *workspace,
+                                     size_t workspace_bytes, void *stream)
+{
+    if (!pool || batch < 1 || batch > pool->cfg.max_batch || n_models < 1 || hq_per_model < 1 ||
+        !on_pool_device(pool))
+        return SHKV_ERR_INVALID_ARG;
+    const int32_t hkv = pool->cfg.num_kv_heads;
+    if (hq_per_model % hkv || (int64_t)n_models * (hq_per_model / hkv) > kMaxDecodeRows)
+        return SHKV_ERR_UNSUPPORTED;
+    Q8AttnParams p;
+    memset(&p, 0, sizeof p);
+    p.batch = batch;
+    p.causal = 0;
+    for (int b = 0; b < batch; ++b) {
+        p.lens[b] = pool->lens[b];
+        p.n_q[b] = n_models;
+        p.q0[b] = b * n_models;
+    }
+    return attention(pool, p, hq_per_model, q, (int64_t)hq_per_model * pool->cfg.head_dim, scale, out, lse_out,
+                     workspace, workspace_bytes, stream);
+}
+
+shkv_status shkv_q8_chunk_attention(shkv_q8_pool *pool, int32_t batch, const int32_t *new_lens, int32_t hq,
+                                    const void *q, int64_t q_stride, float scale, void *out, float *lse_out,
+                                    void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!pool || !new_lens || batch < 1 || batch > pool->cfg.max_batch || hq < 1 || !on_pool_device(pool))
+        return SHKV_ERR_INVALID_ARG;
+    const int32_t hkv = pool->cfg.num_kv_heads;
+    if (hq % hkv || hq / hkv > 128)
+        return SHKV_ERR_UNSUPPORTED;
+    Q8AttnParams p;
+    memset(&p, 0, sizeof p);
+    p.batch = batch;
+    p.causal = 1;
+    int64_t tokens = 0;
+    for (int b = 0; b < batch; ++b) {
+        if (new_lens[b] < 0 || new_lens[b] > pool->lens[b])
+            return SHKV_ERR_INVALID_ARG;     // the new tokens must already be in the pool
+        p.lens[b] = pool->lens[b];
+        p.n_q[b] = new_lens[b];
+        p.q0[b] = (int32_t)tokens;
+        tokens += new_lens[b];
+        if (tokens * hq > INT32_MAX)
+            return SHKV_ERR_UNSUPPORTED;
+    }
+    if (tokens == 0)
+        return SHKV_OK;
+    return attention(pool, p, hq, q, q_stride, scale, out, lse_out, workspace, workspace_bytes, stream);
+}
+
+shkv_status shkv_q8_check_errors(shkv_q8_pool *pool, void *stream, uint32_t *flags)
+{
+    if (!pool || !flags || !on_pool_device(pool))
+        return SHKV_ERR_INVALID_ARG;
+    *flags = 0;
+    if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess)
+        return SHKV_ERR_CUDA;
+    uint32_t v = 0;
+    if (cudaMemcpy(&v, pool->cfg.error_word, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess)
+        return SHKV_ERR_CUDA;
+    if (v && cudaMemset(pool->cfg.error_word, 0, sizeof v) != cudaSuccess)
+        return SHKV_ERR_CUDA;
+    *flags = v;
+    return v ? SHKV_ERR_DEVICE : SHKV_OK;
+}
+
+}  // extern "C"

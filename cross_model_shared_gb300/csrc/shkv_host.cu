@@ -15,6 +15,7 @@
 
 #include "shkv.h"
 #include "shkv_device.cuh"
+#include "host_shared.h"
 #include "prefill.cuh"
 #include "tails.cuh"
 
@@ -34,6 +35,30 @@ cudaError_t launch_prefill_umma(const CUtensorMap &tmK, const CUtensorMap &tmV, 
                                 int grid, cudaStream_t stream);
 cudaError_t launch_merge(int n_splits, int batch, int rows, int head_dim, const float *o_part,
                          const float *lse_part, __nv_bfloat16 *out, float *lse_out, cudaStream_t stream);
+}  // namespace shkv
+
+namespace shkv {
+
+EncodeTiledFn encode_tiled_fn()
+{
+    static EncodeTiledFn fn = nullptr;
+    if (!fn) {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(ptr);
+    }
+    return fn;
+}
+
+Span span_of(const void *p, size_t bytes)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    return {a, p ? a + bytes : a};
+}
+
 }  // namespace shkv
 
 using namespace shkv;
@@ -65,24 +90,6 @@ namespace {
 constexpr int64_t kMinChunksPerCta = 8;
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled_fn()
-{
-    static EncodeTiledFn fn = nullptr;
-    if (!fn) {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(ptr);
-    }
-    return fn;
-}
 
 // 3-D view of a [num_pages, Hkv, P, D] bf16 pool: dim0 = 64 columns
 // (128 bytes, the swizzle span), dim1 = rows (num_pages*Hkv*P, stride D*2
@@ -407,17 +414,6 @@ size_t workspace_bytes_for(int32_t batch, int32_t hkv, int32_t rows, int32_t hea
 
 shkv_status cuda_status(cudaError_t e) { return e == cudaSuccess ? SHKV_OK : SHKV_ERR_CUDA; }
 
-// Device bytes [lo, hi).
-struct Span {
-    uintptr_t lo, hi;
-};
-
-Span span_of(const void *p, size_t bytes)
-{
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return {a, p ? a + bytes : a};
-}
-
 // The device bytes that the library's last kernel-launching call on each
 // stream reads or writes (its workspace bytes, queries, outputs, tables).
 // Every library kernel lets the next kernel of its stream start once it has
@@ -500,6 +496,16 @@ struct StreamUse {
     }
 };
 StreamUse g_stream_use;
+
+}  // namespace
+
+namespace shkv {
+
+void record_stream_use(const void *stream, std::initializer_list<Span> spans) { g_stream_use.record(stream, spans); }
+
+}  // namespace shkv
+
+namespace {
 
 // Launch shape of the decode kernel for R stacked rows per KV head.
 struct DecodeShape {

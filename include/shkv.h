@@ -506,6 +506,128 @@ shkv_status shkv_decode_attention_noalloc(shkv_pool *pool, int32_t batch, int32_
 shkv_status shkv_partition_requests(int32_t batch, const int32_t *seq_lens, int32_t page_size,
                                     int32_t world_size, int32_t *owner, int64_t *rank_pages);
 
+/*
+ * The 8-bit shared KV cache: the paged cache of shkv_pool with every
+ * (token, KV head) row of K and of V held as e4m3 codes and one power-of-two
+ * scale.  It takes head_dim + 1 bytes a row where the bf16 cache takes
+ * 2 * head_dim, so a decode step reads about half the bytes.
+ *
+ *   row x[0 .. D):  e = the least integer >= -127 with max|x| <= 448 * 2^e,
+ *                   code i = e4m3(x_i * 2^-e), round to nearest even,
+ *                   scale byte = e + 127 (e8m0);  the row stands for code_i * 2^e
+ *   A row with an infinity or a NaN is stored as NaN (scale byte 255, codes
+ *   0x7f; NaN codes occur in no other row); a zero row has scale byte 0.
+ *   code_i * 2^e is exact in bf16 (its smallest subnormals aside), and
+ *   quantising a row that was read back gives the same values.
+ *
+ *   k_pages, v_pages  device e4m3 [num_pages, num_kv_heads, page_size, head_dim]
+ *   scales            device e8m0 [num_pages, num_kv_heads, 2, page_size]: K's
+ *                     scales of the page's tokens, then V's
+ *   the other fields  as in shkv_pool_config (max_batch <= SHKV_MAX_BATCH)
+ *
+ * The conventions at the top of this file hold; besides, the current device
+ * of every call that enqueues work must be the one the pool was created on
+ * (SHKV_ERR_INVALID_ARG).  Arguments named start, lens and new_lens are host
+ * arrays [batch], read before the call returns.  Requests may be of any
+ * length from zero on.  A call captured into a CUDA graph replays with the
+ * lengths and positions of its capture; SHKV_ERRF_SEQ_LEN is set where the
+ * device copy of a length then differs.
+ */
+typedef struct shkv_q8_pool shkv_q8_pool;
+
+typedef struct {
+    int32_t num_pages;
+    int32_t page_size;        /* 16 or 32 tokens */
+    int32_t num_kv_heads;
+    int32_t head_dim;         /* 64 or 128 */
+    int32_t max_batch;
+    int32_t max_pages_per_seq;
+    void *k_pages;
+    void *v_pages;
+    void *scales;
+    int32_t *block_table;
+    int32_t *seq_lens;
+    uint32_t *error_word;
+    const int32_t *initial_seq_lens; /* host, nullable */
+} shkv_q8_pool_config;
+
+/* As their shkv_pool counterparts, for an 8-bit pool. */
+shkv_status shkv_q8_pool_create(const shkv_q8_pool_config *cfg, shkv_q8_pool **out);
+shkv_status shkv_q8_pool_destroy(shkv_q8_pool *pool);
+shkv_status shkv_q8_pool_set_seq_lens(shkv_q8_pool *pool, int32_t batch, const int32_t *lens, void *stream);
+shkv_status shkv_q8_pool_get_seq_lens(const shkv_q8_pool *pool, int32_t batch, int32_t *lens);
+shkv_status shkv_q8_check_errors(shkv_q8_pool *pool, void *stream, uint32_t *flags);
+
+/*
+ * Quantise the K/V of new tokens as they are written.  Request b takes the
+ * next new_lens[b] tokens (0 allowed) of the packed inputs, at positions
+ * start[b] .. start[b] + new_lens[b] - 1, and its length becomes
+ * start[b] + new_lens[b].  start = NULL appends at the current lengths; a
+ * start below the length drops the tokens from there on first (rejected
+ * drafts), also with new_lens[b] = 0.  The block table must already map the
+ * pages, and no two written tokens may share a slot.
+ *   k_new, v_new   device bf16, token t's rows [num_kv_heads, head_dim] at
+ *                  element t * k_stride (v_stride): a multiple of 8, at least
+ *                  num_kv_heads * head_dim, so slices of one projection serve
+ * Errors: SHKV_ERR_INVALID_ARG (also start[b] above the length),
+ * SHKV_ERR_CAPACITY, SHKV_ERR_UNSUPPORTED (more than INT32_MAX rows),
+ * SHKV_ERR_CUDA.  A block-table entry outside the pool sets
+ * SHKV_ERRF_PAGE_OOB and that token is not written.
+ */
+shkv_status shkv_q8_append_kv(shkv_q8_pool *pool, int32_t batch, const int32_t *start, const int32_t *new_lens,
+                              const void *k_new, int64_t k_stride, const void *v_new, int64_t v_stride, void *stream);
+
+/*
+ * Read tokens start[b] .. start[b] + lens[b] - 1 of every request back as
+ * bf16, packed request after request (a handoff to a 16-bit consumer).
+ * k_out / v_out as k_new / v_new above; nothing is written behind the last
+ * token.  Errors: SHKV_ERR_INVALID_ARG (also a range past the length),
+ * SHKV_ERR_UNSUPPORTED, SHKV_ERR_CUDA.  A token on a page outside the pool
+ * sets SHKV_ERRF_PAGE_OOB and reads as zero.
+ */
+shkv_status shkv_q8_read_kv(shkv_q8_pool *pool, int32_t batch, const int32_t *start, const int32_t *lens, void *k_out,
+                            int64_t k_stride, void *v_out, int64_t v_stride, void *stream);
+
+/*
+ * Bytes of device workspace that one attention call on this pool needs, for
+ * any shape.  It must be zero before its first use and is left ready for the
+ * next call (of any shape) by every call that completes without device error
+ * bits.  Calls sharing one workspace must not overlap on the GPU.
+ */
+shkv_status shkv_q8_workspace_size(const shkv_q8_pool *pool, size_t *bytes);
+
+/*
+ * shkv_decode_attention over the 8-bit cache: same rows, layouts, limits
+ * (n_models * hq_per_model / num_kv_heads <= 64, head_dim 64 or 128) and
+ * formulas, K and V standing for code * 2^e.  A request of length 0 gives
+ * out = 0 and lse = -inf.  A NaN row of K or V makes out and lse of the rows
+ * that attend it NaN.  Errors: SHKV_ERR_INVALID_ARG, SHKV_ERR_UNSUPPORTED,
+ * SHKV_ERR_CUDA; device error bits as in shkv_decode_attention.
+ */
+shkv_status shkv_q8_decode_attention(shkv_q8_pool *pool, int32_t batch, int32_t n_models, int32_t hq_per_model,
+                                     const void *q, float scale, void *out, float *lse_out, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
+/*
+ * Causal attention of a ragged chunk of new tokens over the 8-bit cache
+ * (partial prefill, verification of drafted tokens).  Call it after
+ * shkv_q8_append_kv has put the tokens into the pool: new token i of the
+ * new_lens[b] last of request b (0 allowed) sits at position
+ * L_b - new_lens[b] + i and attends every key at a position <= its own.
+ *   q        device bf16, query token t's rows [hq, head_dim] at element
+ *            t * q_stride (a multiple of 8, at least hq * head_dim); the
+ *            requests' new tokens are packed one after another
+ *   out      device bf16 [tokens, hq, head_dim];  lse_out device fp32
+ *            [tokens, hq] (natural log) or NULL
+ * Supported: hq % num_kv_heads == 0, hq / num_kv_heads <= 128, head_dim 64 or
+ * 128.  Errors: SHKV_ERR_INVALID_ARG (also new_lens[b] above the length),
+ * SHKV_ERR_UNSUPPORTED, SHKV_ERR_CUDA; device error bits as in
+ * shkv_prefill_attention, NaN rows as in shkv_q8_decode_attention.
+ */
+shkv_status shkv_q8_chunk_attention(shkv_q8_pool *pool, int32_t batch, const int32_t *new_lens, int32_t hq,
+                                    const void *q, int64_t q_stride, float scale, void *out, float *lse_out,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
 /* Static description of a status code. */
 const char *shkv_status_string(shkv_status status);
 
