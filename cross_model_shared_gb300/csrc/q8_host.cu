@@ -12,11 +12,13 @@
 
 #include "host_shared.h"
 #include "q8.cuh"
+#include "q8_decode.cuh"
 #include "shkv.h"
 
 namespace shkv {
 cudaError_t launch_q8_cache(const Q8CacheParams &p, bool read, int num_sms, cudaStream_t stream);
 cudaError_t launch_q8_attn(const Q8AttnParams &p, int max_rows, cudaStream_t stream);
+cudaError_t launch_q8_decode(const CUtensorMap &tmK, const CUtensorMap &tmV, Q8DecodeParams &q, cudaStream_t stream);
 }  // namespace shkv
 
 using namespace shkv;
@@ -25,6 +27,7 @@ struct shkv_q8_pool {
     shkv_q8_pool_config cfg;
     int device;
     int num_sms;
+    CUtensorMap tm_k, tm_v;          // one page of one KV head a box
     std::vector<int32_t> lens;       // host copy of seq_lens
 };
 
@@ -96,9 +99,82 @@ shkv_status launch_cache(const shkv_q8_pool *pool, const Q8CacheParams &p, bool 
     return SHKV_OK;
 }
 
-constexpr int32_t kMaxDecodeRows = 64;     // stacked rows per KV head of a decode
+// 2-D view of a code pool: dim0 = head_dim bytes, dim1 = the (page, KV head,
+// slot) rows.  One box {128, P} with 128-byte swizzle is one page of one KV
+// head; at head_dim 64 its upper half lies outside the tensor and is filled
+// with zeros, so that the kernels see 128-byte rows.
+bool make_map(CUtensorMap *tm, void *base, const shkv_q8_pool_config &c)
+{
+    EncodeTiledFn enc = encode_tiled_fn();
+    if (!enc)
+        return false;
+    cuuint64_t dims[2] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.num_pages * c.num_kv_heads * c.page_size};
+    cuuint64_t strides[1] = {(cuuint64_t)c.head_dim};
+    cuuint32_t box[2] = {128u, (cuuint32_t)c.page_size};
+    cuuint32_t estr[2] = {1u, 1u};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
-size_t workspace_need(const shkv_q8_pool *) { return 256; }
+constexpr int32_t kMaxDecodeRows = 64;     // stacked rows per KV head that one decode launch takes
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+// The workspace: an arrival counter per (request, KV head) of the pool's
+// largest batch, then two partials per SM of up to 64 rows: their
+// log-sum-exps and rows.  Nothing else is ever written over the counters.
+size_t count_bytes(const shkv_q8_pool *p) { return align256((size_t)p->cfg.max_batch * p->cfg.num_kv_heads * 4); }
+size_t lse_bytes(const shkv_q8_pool *p) { return align256((size_t)2 * p->num_sms * kMaxDecodeRows * 4); }
+size_t workspace_need(const shkv_q8_pool *p)
+{
+    return count_bytes(p) + lse_bytes(p) + (size_t)2 * p->num_sms * kMaxDecodeRows * p->cfg.head_dim * 4;
+}
+
+// Up to 64 stacked rows per (request, KV head).
+shkv_status launch_stacked(shkv_q8_pool *pool, const Q8AttnParams &a, int max_rows, void *workspace, cudaStream_t stream)
+{
+    Q8DecodeParams q;
+    memset(&q, 0, sizeof q);
+    DecodeParams &d = q.d;
+    int32_t keys[SHKV_MAX_BATCH];           // of the requests that have rows
+    for (int b = 0; b < a.batch; ++b) {
+        keys[b] = a.n_q[b] ? a.lens[b] : 0;
+        q.n_q[b] = a.n_q[b];
+        q.q0[b] = a.q0[b];
+        q.has_empty |= a.n_q[b] && !keys[b];
+    }
+    const int64_t r = max_rows;
+    const shkv_status st =
+        plan_pages(a.batch, keys, a.page_size, a.hkv, pool->num_sms < kMaxCtas ? pool->num_sms : kMaxCtas, 128, 24 * r,
+                   10 * r, 56 * r, d.page_prefix, d.last_fill, d.cta_cut, &d.total_chunks, &d.num_ctas);
+    if (st != SHKV_OK)
+        return st;
+    d.q = a.q;
+    d.out = a.out;
+    d.lse_out = a.lse_out;
+    d.block_table = a.block_table;
+    d.seq_lens = a.seq_lens;
+    d.err = a.err;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    d.ws_count = reinterpret_cast<uint32_t *>(ws);
+    d.ws_lse = reinterpret_cast<float *>(ws + count_bytes(pool));
+    d.ws_part = reinterpret_cast<float *>(ws + count_bytes(pool) + lse_bytes(pool));
+    d.batch = a.batch;
+    d.hq = a.hq;
+    d.hkv = a.hkv;
+    d.group = a.group;
+    d.rows = max_rows;
+    d.page_size = a.page_size;
+    d.max_pages = a.max_pages;
+    d.num_pages = a.num_pages;
+    d.scale_log2 = a.scale_log2;
+    q.scales = a.scales;
+    q.q_stride = a.q_stride;
+    q.head_dim = a.head_dim;
+    q.causal = a.causal;
+    return status_of(launch_q8_decode(pool->tm_k, pool->tm_v, q, stream));
+}
 
 // Both attentions: n_q query tokens of request b start at query token q0[b].
 shkv_status attention(shkv_q8_pool *pool, Q8AttnParams &p, int32_t hq, const void *q, int64_t q_stride, float scale,
@@ -133,8 +209,11 @@ shkv_status attention(shkv_q8_pool *pool, Q8AttnParams &p, int32_t hq, const voi
         max_rows = std::max(max_rows, p.n_q[b] * p.group);
         tokens += p.n_q[b];
     }
-    if (launch_q8_attn(p, max_rows, (cudaStream_t)stream) != cudaSuccess)
-        return SHKV_ERR_CUDA;
+    const shkv_status st = max_rows <= kMaxDecodeRows
+                               ? launch_stacked(pool, p, max_rows, workspace, (cudaStream_t)stream)
+                               : status_of(launch_q8_attn(p, max_rows, (cudaStream_t)stream));
+    if (st != SHKV_OK)
+        return st;
     const size_t row = (size_t)hq * c.head_dim;
     record_stream_use(stream, {span_of(workspace, workspace_need(pool)),
                                span_of(q, ((size_t)(tokens - 1) * q_stride + row) * 2),
@@ -177,6 +256,7 @@ shkv_status shkv_q8_pool_create(const shkv_q8_pool_config *cfg, shkv_q8_pool **o
         memcpy(pool->lens.data(), c.initial_seq_lens, sizeof(int32_t) * c.max_batch);
     if (cudaGetDevice(&pool->device) != cudaSuccess ||
         cudaDeviceGetAttribute(&pool->num_sms, cudaDevAttrMultiProcessorCount, pool->device) != cudaSuccess ||
+        !make_map(&pool->tm_k, c.k_pages, c) || !make_map(&pool->tm_v, c.v_pages, c) ||
         cudaMemcpy(c.seq_lens, pool->lens.data(), sizeof(int32_t) * c.max_batch, cudaMemcpyHostToDevice) !=
             cudaSuccess ||
         cudaMemset(c.error_word, 0, sizeof(uint32_t)) != cudaSuccess) {

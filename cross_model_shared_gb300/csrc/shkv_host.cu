@@ -503,6 +503,14 @@ namespace shkv {
 
 void record_stream_use(const void *stream, std::initializer_list<Span> spans) { g_stream_use.record(stream, spans); }
 
+shkv_status plan_pages(int32_t batch, const int32_t *lens, int32_t page_size, int32_t hkv, int32_t max_ctas,
+                       int64_t stage, int64_t seg, int64_t first, int64_t last, int32_t *prefix, uint8_t *last_fill,
+                       int32_t *cuts, int64_t *total_chunks, int32_t *num_ctas)
+{
+    return build_plan(batch, lens, page_size, hkv, max_ctas, PlanCosts{stage, seg, first, last}, prefix, last_fill,
+                      cuts, total_chunks, num_ctas, true);
+}
+
 }  // namespace shkv
 
 namespace {

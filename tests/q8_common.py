@@ -11,6 +11,8 @@ A = sum_t p_t |v_t| and L keys:
     2 ds of itself (numerator and sum), so 2 ds A;
   * sums over the keys in fp32: L * 2^-24 A, and 2^-18 A for the exponentials,
     the running maximum's rescaling and the join of pieces;
+  * a weight under 2^-126 of the row's largest is no normal fp32 number and may
+    count as zero: sum_t 2^-126 |v_t| (it matters only beside values 2^100 larger);
   * one rounding to bf16: half a step, 2^-8 of the value.
 The log-sum-exp is off by ds + L * 2^-24 + 2^-18 and its own fp32 rounding.
 """
@@ -123,6 +125,7 @@ def attend(q, k, v, scale, limit=None):
     ds = abs(scale) * (d * 2.0 ** -24 + 2.0 ** -18) * q.abs().amax(1) * k.abs().sum(1).max()
     a = p @ v.abs()
     tol = a * (2.0 ** -11 + 2 * ds[:, None] + L * 2.0 ** -24 + 2.0 ** -18) + out.abs() * 2.0 ** -8
+    tol = tol + 2.0 ** -126 * v.abs().sum(0)
     return out, lse, tol, ds + L * 2.0 ** -24 + 2.0 ** -18 + lse.abs() * 2.0 ** -23
 
 
