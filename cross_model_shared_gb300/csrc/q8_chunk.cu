@@ -1,0 +1,992 @@
+// q8_chunk.cu -- causal attention of ragged chunks of new tokens over the
+// 8-bit KV cache on the 5th-generation tensor cores.
+//
+// A query tile is TPT = floor(128 / G) new tokens x the G query heads of one
+// KV head, 128 MMA rows (row r = i * G + j).  A unit is two consecutive tiles
+// X = A, B of one (request, KV head); its 128-key stages of K and V are loaded
+// once for both.  Persistent CTAs take contiguous ranges of equal cost over
+// all units' stages; a unit that straddles a cut leaves normalised partials
+// and log-sum-exps that a second kernel joins (few units, many rows: joined
+// by all SMs at once).  Per stage and tile:
+//
+//   S_X[r, key]  = sum_d (qh + ql)[r, d] k8[key, d]               kind::f8f6f4
+//   P_X[r, key]  = 2^(S 2^eq[r] 2^ek[key] scale log2(e) - m[r] + 7)   fp16, over S in TMEM
+//   O_X[r, d]   += sum_key P_X[r, key] V16[key, d]                kind::f16
+//
+// The query's two e4m3 terms are as in the stacked kernel (q8_decode.cu); the
+// factor of a key is a column factor here, read as a vector from shared
+// memory.  V is widened to fp16 in shared memory with its scale relative to
+// E, a running upper bound of the unit's V exponents: V16 = v8 * 2^(ev - E + 6),
+// exact.  O is rescaled where m or E moves.  From the first stage on that
+// holds a scale under 2^-8 of the largest so far (or far above it) the piece
+// is `wide`: it is summed with V16 = v8 * 2^-14, the factor 2^(ev - E + 20) in
+// P, and P relative to m2[r], a running maximum of x + ev apart from l's m: so
+// fp16 holds 11 bits of every token that matters to the sum, whatever the
+// magnitudes of weights and values apart.  That takes two exponentials a
+// score.  (While V's scales are alike, P relative to the largest weight does
+// the same: fp16's least step is 2^-31 of it, 2^-21 of the least V scale.)  A
+// V row of the least scale (values under 2^-118) beside ordinary ones takes
+// part as zero.  Sums and O are fp32.
+//
+// As in the bf16 kernel, a stage whose scores are all visible is
+// exponentiated against the running maximum without taking its own; a row
+// whose sum of P exceeds 2^15 (fp16's range) or is no number sends its warp
+// through the exact path.
+//
+// Roles (512 threads): warps 0-3 softmax of tile A, 4-7 of tile B (row = TMEM
+// lane), 8 QK issuer, 9 PV issuer, 10 producer of K, 11 producer of V and its
+// scale bytes, 12-15 V conversion, one key a thread: also the column factors.
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "launch.cuh"
+#include "q8.cuh"
+#include "q8_chunk.cuh"
+#include "shkv_device.cuh"
+
+namespace shkv {
+
+namespace {
+
+constexpr int kKT = 128;                 // keys per stage
+constexpr int kThreads = 512;
+constexpr int kQkWarp = 8, kPvWarp = 9, kKWarp = 10, kVWarp = 11, kConvWarp0 = 12, kConvWarps = 4;
+constexpr int kGroupWarps = 4;           // softmax warps per tile
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescaleLog2 = 8.f;      // m lags the maximum by at most this
+constexpr float kPLog2 = 7.f;            // P at the running maximum
+constexpr float kMaxPart = 32768.f;      // largest stage sum of P taken without the stage's maximum
+constexpr int kVLog2 = 6;                // V16 of the largest scale is 448 * 2^6 at most
+constexpr int kVExact = 10;              // V exponents further under E than this make a piece wide
+constexpr int kVWide = 20;               // ... and V16 is then v8 * 2^(6 - 20) for all tokens
+constexpr int kZeroRowE = 60;            // from E = 2^(60 - 127) on a V row of scale byte 0 counts as zero
+constexpr int kEHeadroom = 2;            // E moves to this much above a stage's largest V exponent
+constexpr int kKS = 3, kVS = 3;          // ring slots of 16 KB (K) and 32 KB (V)
+constexpr uint32_t kKSlotBytes = kKT * 128;
+constexpr uint32_t kVSlotBytes = 2 * kKT * 128;
+constexpr uint32_t kQTermBytes = 128 * 128;      // one e4m3 term of a tile [128 rows][128 B]
+constexpr uint32_t kSoftmaxRegs = 200, kOtherRegs = 56;
+static_assert(kSoftmaxRegs * 256 + kOtherRegs * 256 == 128 * kThreads, "register split");
+
+__device__ __forceinline__ uint32_t col_s(int x) { return (uint32_t)(x * 128); }
+__device__ __forceinline__ uint32_t col_o(int x) { return (uint32_t)(256 + x * 128); }
+
+struct Smem {
+    uint32_t qtile, kring, vring, scales, factor, pfactor, info, bars, misc, tslot, total;
+};
+
+// Query tiles [tile][qh | ql][128 rows][128 B], K ring, V ring (slots
+// [half][128 keys][128 B], the codes in the upper half until they are
+// converted), all 128-byte swizzled; per V slot its scale bytes, the keys'
+// score factors and P factors, and four words (valid pages, E, wide).
+__host__ __device__ inline Smem smem_layout()
+{
+    Smem u;
+    u.qtile = 0;
+    u.kring = u.qtile + 4 * kQTermBytes;
+    u.vring = u.kring + kKS * kKSlotBytes;
+    u.scales = u.vring + kVS * kVSlotBytes;
+    u.factor = u.scales + kVS * 2 * kKT;
+    u.pfactor = u.factor + kVS * kKT * 4;
+    u.info = u.pfactor + kVS * kKT * 4;
+    u.bars = u.info + kVS * 16;
+    u.misc = u.bars + (uint32_t)(2 * kKS + 3 * kVS + 9) * 8u;
+    u.tslot = u.misc + 8;
+    u.total = u.misc + 16 + 1024;
+    return u;
+}
+
+struct Ctx {
+    uint8_t *smem;
+    uint32_t base;
+    Smem lay;
+    volatile uint32_t *abort_flag;
+};
+
+__device__ __forceinline__ uint32_t bar_at(const Ctx &c, int i) { return c.base + c.lay.bars + 8u * i; }
+__device__ __forceinline__ uint32_t full_k(const Ctx &c, int s) { return bar_at(c, s); }
+__device__ __forceinline__ uint32_t empty_k(const Ctx &c, int s) { return bar_at(c, kKS + s); }
+__device__ __forceinline__ uint32_t full_v(const Ctx &c, int s) { return bar_at(c, 2 * kKS + s); }
+__device__ __forceinline__ uint32_t conv_v(const Ctx &c, int s) { return bar_at(c, 2 * kKS + kVS + s); }
+__device__ __forceinline__ uint32_t empty_v(const Ctx &c, int s) { return bar_at(c, 2 * kKS + 2 * kVS + s); }
+constexpr int kBar0 = 2 * kKS + 3 * kVS;
+__device__ __forceinline__ uint32_t s_full(const Ctx &c, int x) { return bar_at(c, kBar0 + x); }
+__device__ __forceinline__ uint32_t p_full(const Ctx &c, int x) { return bar_at(c, kBar0 + 2 + x); }
+__device__ __forceinline__ uint32_t pv_done(const Ctx &c, int x) { return bar_at(c, kBar0 + 4 + x); }
+__device__ __forceinline__ uint32_t q_ready(const Ctx &c) { return bar_at(c, kBar0 + 6); }
+__device__ __forceinline__ uint32_t q_free(const Ctx &c) { return bar_at(c, kBar0 + 7); }
+__device__ __forceinline__ uint32_t fin_b(const Ctx &c) { return bar_at(c, kBar0 + 8); }
+__device__ __forceinline__ uint32_t k_slot(const Ctx &c, int s) { return c.base + c.lay.kring + (uint32_t)s * kKSlotBytes; }
+__device__ __forceinline__ uint32_t v_slot(const Ctx &c, int s) { return c.base + c.lay.vring + (uint32_t)s * kVSlotBytes; }
+__device__ __forceinline__ uint32_t ring_par(int k, int n) { return (uint32_t)((k / n) & 1); }
+
+// Bounded wait that sleeps on the barrier (issuers, producers): the waiting
+// warps leave the issue slots to the softmax warps.
+__device__ __forceinline__ bool try_wait_sleep(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ bool wait_sleep(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag, uint32_t *err)
+{
+    if (try_wait_sleep(bar, parity))
+        return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (try_wait_sleep(bar, parity))
+            return true;
+        if (*abort_flag)
+            return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            *abort_flag = 1u;
+            atomicOr(err, SHKV_ERRF_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// A piece of a unit: its key stages [s0, s1).
+struct Piece {
+    int u, b, g;
+    int L, prefix;               // request length, cached tokens before the new ones
+    int i0[2], ntok[2];          // first new token and new tokens of tiles A and B (B may be empty)
+    int nst[2], nst_all;         // key stages each tile attends, and the larger
+    int s0, s1;
+};
+
+__device__ __forceinline__ void set_unit(const Q8ChunkParams &p, Piece &t)
+{
+    int lo = 0, hi = p.batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.units[mid] <= t.u)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    t.b = lo;
+    const int pairs = (p.units[lo + 1] - p.units[lo]) / p.hkv;
+    const int rem = t.u - p.units[lo];
+    t.g = rem / pairs;
+    const int tp = rem - t.g * pairs;
+    const int n = p.n_q[lo];
+    t.L = p.lens[lo];
+    t.prefix = t.L - n;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        t.i0[x] = (2 * tp + x) * p.tpt;
+        t.ntok[x] = max(0, min(p.tpt, n - t.i0[x]));
+        t.nst[x] = t.ntok[x] > 0 ? (t.prefix + t.i0[x] + t.ntok[x] + kKT - 1) / kKT : 0;
+    }
+    t.nst_all = max(t.nst[0], t.nst[1]);
+}
+
+// The CTA's pieces in order; false when there are no more.
+__device__ __forceinline__ bool first_piece(const Q8ChunkParams &p, Piece &t)
+{
+    const int c = blockIdx.x;
+    t.u = p.cut_unit[c];
+    t.s0 = p.cut_stage[c];
+    if (t.u > p.cut_unit[c + 1] || (t.u == p.cut_unit[c + 1] && t.s0 >= p.cut_stage[c + 1]))
+        return false;
+    set_unit(p, t);
+    t.s1 = t.u == p.cut_unit[c + 1] ? p.cut_stage[c + 1] : t.nst_all;
+    return true;
+}
+
+__device__ __forceinline__ bool next_piece(const Q8ChunkParams &p, Piece &t)
+{
+    const int c = blockIdx.x;
+    ++t.u;
+    t.s0 = 0;
+    if (t.u > p.cut_unit[c + 1] || (t.u == p.cut_unit[c + 1] && p.cut_stage[c + 1] == 0))
+        return false;
+    set_unit(p, t);
+    t.s1 = t.u == p.cut_unit[c + 1] ? p.cut_stage[c + 1] : t.nst_all;
+    return true;
+}
+
+// Partial slot of the piece of unit u that CTA c holds: 0 if it opens the CTA's range.
+__device__ __forceinline__ int piece_slot(const Q8ChunkParams &p, int c, int u)
+{
+    return 2 * c + (u == p.cut_unit[c] ? 0 : 1);
+}
+
+// ---------------------------------------------------------------------------
+// producers
+// ---------------------------------------------------------------------------
+// One lane copies one page: a box of P rows x 128 bytes (at head_dim 64 the
+// upper half of the rows is filled with zeros).  The V warp also copies the
+// page's 2P scale bytes and publishes the stage's valid pages.
+template <bool kIsV>
+__device__ void chunk_producer(const CUtensorMap *tm, const Q8ChunkParams &p, const Ctx &c)
+{
+    constexpr int S = kIsV ? kVS : kKS;
+    const int lane = threadIdx.x & 31;
+    const int P = p.page_size, RB = kKT / P;
+    const uint64_t pol = l2_evict_first_policy();
+    if (lane == 0)
+        prefetch_tensormap(tm);
+    bool alive = true;
+    int kbase = 0, last_issued = -1;
+    Piece t;
+    for (bool more = first_piece(p, t); more; more = next_piece(p, t)) {
+        if (kIsV && lane == 0 && __ldg(p.seq_lens + t.b) != t.L)
+            atomicOr(p.err, SHKV_ERRF_SEQ_LEN);
+        const int npages = (t.L + P - 1) / P;
+        const int32_t *row = p.block_table + (int64_t)t.b * p.max_pages;
+        auto entry = [&](int j) {                        // the lane's page of stage j
+            const int pg = j * RB + lane;
+            return lane < RB && j < t.s1 && pg < npages ? __ldg(row + pg) : -1;
+        };
+        int nxt = entry(t.s0);
+        for (int j = t.s0; j < t.s1; ++j) {
+            const int k = kbase + j - t.s0, slot = k % S;
+            const int id = nxt;
+            nxt = entry(j + 1);                          // read one stage ahead
+            bool ok = true;
+            if (alive && lane == 0)
+                ok = wait_sleep(kIsV ? empty_v(c, slot) : empty_k(c, slot), ring_par(k, S) ^ 1u, c.abort_flag, p.err);
+            alive = alive && __all_sync(0xffffffffu, ok);
+            const bool inside = lane < RB && j * RB + lane < npages;
+            const bool valid = inside && id >= 0 && id < p.num_pages;
+            const uint32_t mask = __ballot_sync(0xffffffffu, valid);
+            const uint32_t bar = kIsV ? full_v(c, slot) : full_k(c, slot);
+            if (kIsV && alive && inside && !valid)
+                atomicOr(p.err, SHKV_ERRF_PAGE_OOB);
+            if (alive && lane == 0) {
+                if (kIsV)
+                    reinterpret_cast<volatile uint32_t *>(c.smem + c.lay.info)[slot * 4] = mask;
+                mbar_arrive_expect_tx(bar, (uint32_t)__popc(mask) * (uint32_t)P * (kIsV ? 130u : 128u));
+            }
+            __syncwarp();
+            if (alive && valid) {
+                const int unit = id * p.hkv + t.g;
+                tma_load_2d((kIsV ? v_slot(c, slot) + kKT * 128u : k_slot(c, slot)) + (uint32_t)(lane * P) * 128u, tm, 0,
+                            unit * P, bar, pol);
+                if (kIsV)
+                    bulk_load(c.base + c.lay.scales + (uint32_t)(slot * 2 * kKT + lane * 2 * P),
+                              p.scales + (int64_t)unit * 2 * P, 2u * (uint32_t)P, bar);
+            }
+            if (alive)
+                last_issued = k;
+            __syncwarp();
+        }
+        kbase += t.s1 - t.s0;
+    }
+    if (!alive && lane == 0)
+        for (int k = last_issued - S + 1; k <= last_issued; ++k)
+            if (k >= 0)
+                mbar_drain_bounded(kIsV ? full_v(c, k % S) : full_k(c, k % S), ring_par(k, S));
+}
+
+// ---------------------------------------------------------------------------
+// V conversion and the keys' factors, one key a thread
+// ---------------------------------------------------------------------------
+__device__ void chunk_convert(const Q8ChunkParams &p, const Ctx &c)
+{
+    const int t = threadIdx.x - kConvWarp0 * 32, lane = t & 31;
+    const int P = p.page_size, log2P = 31 - __clz(P);
+    const int groups = p.head_dim / 64;                  // 64-column halves
+    bool alive = true;
+    int kbase = 0;
+    Piece u;
+    for (bool more = first_piece(p, u); more; more = next_piece(p, u)) {
+        int e = 0;                                       // E as a scale byte
+        bool wide = false;
+        for (int j = u.s0; j < u.s1; ++j) {
+            const int k = kbase + j - u.s0, slot = k % kVS;
+            bool ok = false;
+            if (alive)
+                ok = mbar_wait_bounded(full_v(c, slot), ring_par(k, kVS), c.abort_flag, p.err);
+            alive = __all_sync(0xffffffffu, ok);
+            if (alive) {
+                volatile uint32_t *info = reinterpret_cast<volatile uint32_t *>(c.smem + c.lay.info) + slot * 4;
+                const uint32_t mask = info[0];
+                const int n = u.L - j * kKT;
+                const uint8_t *sc = c.smem + c.lay.scales + slot * 2 * kKT;
+                // the stage's largest and least V scale, by each warp for itself
+                {
+                    const int t4 = 4 * lane;
+                    const uint32_t w = *reinterpret_cast<const volatile uint32_t *>(
+                        sc + ((t4 >> log2P) << (log2P + 1)) + P + (t4 & (P - 1)));
+                    const int in = ((mask >> (t4 >> log2P)) & 1u) ? n - t4 : 0;
+                    uint32_t b[4], top = 0, low = 255;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        b[i] = i < in ? (w >> (8 * i)) & 0xffu : 255u;
+                        top = max(top, b[i] == 255u ? 0u : b[i]);
+                    }
+                    top = __reduce_max_sync(0xffffffffu, top);
+                    if ((int)top > e) {
+                        wide = wide || (j > u.s0 && (int)top > e + kVExact);
+                        e = min((int)top + kEHeadroom, 254);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        low = min(low, b[i] == 0u && e > kZeroRowE ? 255u : b[i]);
+                    wide = wide || (int)__reduce_min_sync(0xffffffffu, low) < e - kVExact;
+                }
+                const bool valid = t < n && ((mask >> (t >> log2P)) & 1u);
+                const uint8_t *mine = sc + ((t >> log2P) << (log2P + 1)) + (t & (P - 1));
+                const int kb = *reinterpret_cast<const volatile uint8_t *>(mine);
+                const int vb = *reinterpret_cast<const volatile uint8_t *>(mine + P);
+                // a NaN row of V counts as zero and makes its key's scores NaN
+                // instead, so that only rows that attend it see it
+                const bool live = valid && vb != 255 && !(vb == 0 && e > kZeroRowE);
+                const float nan = __uint_as_float(0x7fc00000u);
+                reinterpret_cast<float *>(c.smem + c.lay.factor)[slot * kKT + t] =
+                    !valid ? 0.f : vb == 255 ? nan : q8_scale((uint32_t)kb) * p.scale_log2;
+                const int under = live ? e - vb : 0;      // >= 0
+                // (where V counts as zero P may be zero too, and stays out of its reference)
+                reinterpret_cast<float *>(c.smem + c.lay.pfactor)[slot * kKT + t] = live ? (float)(kVWide - under) : -1e30f;
+                if (t == 0) {
+                    info[1] = (uint32_t)e;
+                    info[2] = wide ? 1u : 0u;
+                }
+                const unsigned short hb = (unsigned short)((kVLog2 - (wide ? kVWide : under) + 15) << 10);   // >= 2^-14
+                const __half2 f = __halves2half2(__ushort_as_half(hb), __ushort_as_half(hb));
+                uint8_t *row = c.smem + c.lay.vring + (uint32_t)slot * kVSlotBytes + (uint32_t)t * 128u;
+                // the codes of half h are read before its fp16 values are
+                // written; only half 1's land on codes, and those were read
+#pragma unroll 1
+                for (int h = 0; h < groups; ++h) {
+                    uint4 raw[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        raw[i] = *reinterpret_cast<const uint4 *>(row + kKT * 128 + (((4 * h + i) ^ (t & 7)) << 4));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int v = 0; v < 8; ++v) {
+                            const __half2 x = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+                                                          (__nv_fp8x2_storage_t)(w[v >> 1] >> (16 * (v & 1))), __NV_E4M3)), f);
+                            o[v] = live ? *reinterpret_cast<const uint32_t *>(&x) : 0u;
+                        }
+                        uint8_t *dst = row + h * (kKT * 128);
+                        *reinterpret_cast<uint4 *>(dst + (((2 * i) ^ (t & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4 *>(dst + (((2 * i + 1) ^ (t & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(conv_v(c, slot));
+        }
+        kbase += u.s1 - u.s0;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// MMA issuers (one lane each)
+// ---------------------------------------------------------------------------
+constexpr uint32_t idesc_of(int M, int N, bool a_mn, bool b_mn)   // formats 0: e4m3 (f8f6f4), fp16 (f16)
+{
+    return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void umma_f8(uint32_t d_taddr, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_taddr),
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// A from TMEM: 128 lanes (rows) x K columns of packed fp16 pairs.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_taddr, uint32_t a_taddr, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_taddr),
+                 "r"(a_taddr), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// S_X of each tile that attends the stage, once its previous PV has read the
+// P written over S_X.
+__device__ void chunk_qk(const Q8ChunkParams &p, const Ctx &c, uint32_t tmem)
+{
+    constexpr uint32_t idesc = idesc_of(128, kKT, false, false);
+    const int steps = p.head_dim / 32;
+    const uint64_t qd0 = umma_sdesc_sw128(c.base + c.lay.qtile, 16u, 1024u);
+    const uint64_t kd0 = umma_sdesc_sw128(k_slot(c, 0), 16u, 1024u);
+    bool alive = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (alive)
+            alive = wait_sleep(bar, parity, c.abort_flag, p.err);
+    };
+    int kbase = 0, seg = 0, done[2] = {0, 0};            // stages each tile has attended
+    Piece t;
+    for (bool more = first_piece(p, t); more; more = next_piece(p, t)) {
+        wait(q_ready(c), (uint32_t)(seg & 1));
+        for (int j = t.s0; j < t.s1; ++j) {
+            const int k = kbase + j - t.s0, slot = k % kKS;
+            const uint64_t kd = kd0 + (((uint32_t)slot * kKSlotBytes) >> 4);
+            wait(full_k(c, slot), ring_par(k, kKS));
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (j >= t.nst[x])
+                    continue;
+                if (done[x] > 0)
+                    wait(pv_done(c, x), (uint32_t)((done[x] - 1) & 1));
+                ++done[x];
+                if (alive) {
+                    tc_fence_after();
+                    const uint64_t qd = qd0 + ((2u * (uint32_t)x * kQTermBytes) >> 4);
+                    for (int i = 0; i < steps; ++i) {
+                        umma_f8(tmem + col_s(x), qd + (uint64_t)(2 * i), kd + (uint64_t)(2 * i), idesc, i ? 1u : 0u);
+                        umma_f8(tmem + col_s(x), qd + (kQTermBytes >> 4) + (uint64_t)(2 * i), kd + (uint64_t)(2 * i),
+                                idesc, 1u);
+                    }
+                }
+                umma_commit(s_full(c, x));
+            }
+            umma_commit(empty_k(c, slot));
+        }
+        umma_commit(q_free(c));
+        kbase += t.s1 - t.s0;
+        ++seg;
+    }
+    umma_commit(fin_b(c));
+    mbar_drain_bounded(fin_b(c), 0u);
+}
+
+__device__ void chunk_pv(const Q8ChunkParams &p, const Ctx &c, uint32_t tmem)
+{
+    const uint32_t idesc = p.head_dim == 64 ? idesc_of(128, 64, false, true) : idesc_of(128, 128, false, true);
+    const uint64_t vd0 = umma_sdesc_sw128(v_slot(c, 0), (uint32_t)(kKT * 128), 1024u);
+    bool alive = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (alive)
+            alive = wait_sleep(bar, parity, c.abort_flag, p.err);
+    };
+    int kbase = 0, done[2] = {0, 0};
+    Piece t;
+    for (bool more = first_piece(p, t); more; more = next_piece(p, t)) {
+        for (int j = t.s0; j < t.s1; ++j) {
+            const int k = kbase + j - t.s0, slot = k % kVS;
+            const uint64_t vd = vd0 + (((uint32_t)slot * kVSlotBytes) >> 4);
+            wait(conv_v(c, slot), ring_par(k, kVS));
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (j >= t.nst[x])
+                    continue;
+                wait(p_full(c, x), (uint32_t)(done[x] & 1));
+                ++done[x];
+                if (alive) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < kKT / 16; ++ks)
+                        umma_f16_ts(tmem + col_o(x), tmem + col_s(x) + (uint32_t)(ks * 8), vd + (uint64_t)(ks * 128), idesc,
+                                    (j == t.s0 && ks == 0) ? 0u : 1u);
+                }
+                umma_commit(pv_done(c, x));
+            }
+            umma_commit(empty_v(c, slot));
+        }
+        kbase += t.s1 - t.s0;
+    }
+    umma_commit(fin_b(c));
+    mbar_drain_bounded(fin_b(c), 0u);
+}
+
+// ---------------------------------------------------------------------------
+// softmax warps of tile x: thread r = MMA row r = (new token i0 + r / G, head r % G)
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
+{
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// This row of the query as two e4m3 terms in its tile; returns the row's scale.
+__device__ __forceinline__ float stage_row(const Q8ChunkParams &p, const Ctx &c, const __nv_bfloat16 *src, int x, int r)
+{
+    const int D = p.head_dim;
+    const uint4 *s4 = reinterpret_cast<const uint4 *>(src);
+    uint32_t a = 0;
+    for (int ch = 0; ch < D / 8; ++ch) {
+        const uint4 v = src ? __ldg(s4 + ch) : make_uint4(0u, 0u, 0u, 0u);
+        a = __vmaxu2(__vmaxu2(a, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)),
+                     __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    }
+    a = max(a & 0xffffu, a >> 16);
+    int byte = (int)(a >> 7) - 8 + ((a & 0x7fu) > 0x60u ? 1 : 0);
+    byte = byte < 0 ? 0 : byte;
+    const float inv = __uint_as_float((uint32_t)(254 - byte) << 23);
+    const bool bad = a >= 0x7f80u;                       // an infinity or a NaN: the row's scores are NaN
+    uint8_t *dst = c.smem + c.lay.qtile + 2u * (uint32_t)x * kQTermBytes + (uint32_t)r * 128u;
+    for (int ch = 0; ch < D / 16; ++ch) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const uint4 v = src ? __ldg(s4 + 2 * ch + half) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t xs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = make_float2(__uint_as_float(xs[i] << 16) * inv,
+                                             __uint_as_float(xs[i] & 0xffff0000u) * inv);
+                const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+                const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+                const __nv_fp8x2_storage_t d = __nv_cvt_float2_to_fp8x2(make_float2(f.x - hf.x, f.y - hf.y),
+                                                                        __NV_SATFINITE, __NV_E4M3);
+                const int w = 2 * half + (i >> 1);
+                hi[w] = (i & 1) ? hi[w] | ((uint32_t)h << 16) : h;
+                lo[w] = (i & 1) ? lo[w] | ((uint32_t)d << 16) : d;
+            }
+        }
+        const uint32_t off = (uint32_t)((ch ^ (r & 7)) << 4);
+        const uint32_t n = 0x7f7f7f7fu;
+        *reinterpret_cast<uint4 *>(dst + off) = bad ? make_uint4(n, n, n, n) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(dst + kQTermBytes + off) =
+            bad ? make_uint4(n, n, n, n) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    return bad ? 1.f : q8_scale((uint32_t)byte);
+}
+
+__device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tmem, int x)
+{
+    const int r = threadIdx.x - x * 128;
+    const int lane = r & 31, warp = r >> 5;
+    const int ti = r / p.group, tj = r - ti * p.group;
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    const uint32_t orow = tmem + lane_base + col_o(x);
+    const uint32_t srow = tmem + lane_base + col_s(x);
+    const int P = p.page_size, D = p.head_dim;
+    const uint32_t all_pages = (1u << (kKT / P)) - 1u;
+    bool alive = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        bool ok = false;
+        if (alive)
+            ok = mbar_wait_bounded(bar, parity, c.abort_flag, p.err);
+        alive = __all_sync(0xffffffffu, ok) && alive;
+        return alive;
+    };
+    int kbase = 0, seg = 0, done = 0;                    // done: stages this tile has attended
+    Piece t;
+    for (bool more = first_piece(p, t); more; more = next_piece(p, t)) {
+        const bool row_ok = ti < t.ntok[x];
+        const int pos = t.prefix + t.i0[x] + ti;         // keys 0 .. pos
+        const int64_t tok = (int64_t)p.q0[t.b] + t.i0[x] + ti;
+        const int head = t.g * p.group + tj;
+        if (seg > 0)
+            wait(q_free(c), (uint32_t)((seg - 1) & 1));
+        const float rq = stage_row(p, c, row_ok ? p.q + tok * p.q_stride + (int64_t)head * D : nullptr, x, r);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(q_ready(c));
+
+        float m_use = -INFINITY, lsum = 0.f;
+        float m2 = 0.f;                                  // P's reference once the piece is wide; m + E until then
+        bool apart = false;
+        int e = 0;                                       // E as a scale byte
+        const int s1 = min(t.s1, t.nst[x]);
+        for (int j = t.s0; j < s1; ++j) {
+            const int k = kbase + j - t.s0, vs = k % kVS;
+            const int key0 = j * kKT;
+            wait(conv_v(c, vs), ring_par(k, kVS));
+            const volatile uint32_t *info = reinterpret_cast<const volatile uint32_t *>(c.smem + c.lay.info) + vs * 4;
+            const uint32_t pmask = alive ? info[0] : 0u;
+            const int e_new = alive ? (int)info[1] : e;
+            const bool wide = info[2] != 0u;
+            const float4 *fac = reinterpret_cast<const float4 *>(c.smem + c.lay.factor + vs * kKT * 4);
+            // keys this row may see: [key0, key0 + nvis), on pages that were copied
+            // (padding rows see all: their scores only reach their own row of O, which is not stored)
+            const int nvis = row_ok ? min(kKT, pos - key0 + 1) : kKT;
+            const bool dense = pmask == all_pages && nvis == kKT;
+            wait(s_full(c, x), (uint32_t)(done & 1));
+            if (alive)
+                tc_fence_after();
+            uint32_t sv[4][32];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                tmem_ld32_nowait(srow + (uint32_t)(q * 32), sv[q]);
+            tmem_wait_ld();
+            // Common case (see the top): P against the running maximum.
+            float part = 0.f;
+            bool fast = __all_sync(0xffffffffu, dense && alive && m_use != -INFINITY && e_new == e && !wide);
+            if (fast) {
+                const float nmu = kPLog2 - m_use;
+                const float2 rq2 = make_float2(rq, rq), nmu2 = make_float2(nmu, nmu);
+                float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 f = fac[q * 8 + i];
+                        const float2 x0 = __ffma2_rn(__fmul2_rn(make_float2(__uint_as_float(sv[q][4 * i]),
+                                                                            __uint_as_float(sv[q][4 * i + 1])),
+                                                                make_float2(f.x, f.y)), rq2, nmu2);
+                        const float2 x1 = __ffma2_rn(__fmul2_rn(make_float2(__uint_as_float(sv[q][4 * i + 2]),
+                                                                            __uint_as_float(sv[q][4 * i + 3])),
+                                                                make_float2(f.z, f.w)), rq2, nmu2);
+                        const float2 p0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
+                        const float2 p1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
+                        acc[0] = __fadd2_rn(acc[0], p0);
+                        acc[1] = __fadd2_rn(acc[1], p1);
+                        pk[2 * i] = pack_half2(p0.x, p0.y);
+                        pk[2 * i + 1] = pack_half2(p1.x, p1.y);
+                    }
+                    tmem_st16_nowait(srow + (uint32_t)(q * 16), pk);
+                }
+                part = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+                if (__any_sync(0xffffffffu, !(part <= kMaxPart))) {
+                    tmem_wait_st();
+                    fast = false;
+                }
+            }
+            if (!fast) {
+                // the exact path: scores, masked; the stage's maximum
+                float cm = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    // bit i: column 32q + i is visible (before this row's end, on a copied page)
+                    const int n = alive ? min(max(nvis - q * 32, 0), 32) : 0;
+                    uint32_t vis = n >= 32 ? 0xffffffffu : ((1u << n) - 1u);
+                    uint32_t pages = 0u;
+                    for (int pg = 0; pg < 32 / P; ++pg)
+                        if ((pmask >> (q * (32 / P) + pg)) & 1u)
+                            pages |= (P >= 32 ? 0xffffffffu : ((1u << P) - 1u)) << (pg * P);
+                    vis &= pages;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 f = fac[q * 8 + i];
+                        const float fs[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            const int col = 4 * i + v;
+                            const float s = ((vis >> col) & 1u) ? __uint_as_float(sv[q][col]) * (fs[v] * rq) : -INFINITY;
+                            sv[q][col] = __float_as_uint(s);
+                            cm = fmaxf(cm, s);
+                        }
+                    }
+                }
+                const int de = e_new - e;
+                if (wide && !apart) {
+                    apart = true;
+                    m2 = m_use + (float)e;
+                }
+                e = e_new;
+                float scale_o = 1.f;
+                if (m_use == -INFINITY) {
+                    m_use = cm;
+                } else if (cm > m_use + kRescaleLog2) {
+                    scale_o = ex2_approx(m_use - cm);
+                    lsum *= scale_o;
+                    m_use = cm;
+                }
+                const float4 *pf = reinterpret_cast<const float4 *>(c.smem + c.lay.pfactor + vs * kKT * 4);
+                if (apart) {
+                    float cy = -INFINITY;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 f = pf[q * 8 + i];
+                            cy = fmaxf(fmaxf(cy, fmaxf(__uint_as_float(sv[q][4 * i]) + f.x,
+                                                       __uint_as_float(sv[q][4 * i + 1]) + f.y)),
+                                       fmaxf(__uint_as_float(sv[q][4 * i + 2]) + f.z,
+                                             __uint_as_float(sv[q][4 * i + 3]) + f.w));
+                        }
+                    cy += (float)e;
+                    scale_o = 1.f;
+                    if (m2 == -INFINITY) {
+                        m2 = cy;
+                    } else if (cy > m2 + kRescaleLog2) {
+                        scale_o = ex2_approx(m2 - cy);
+                        m2 = cy;
+                    }
+                } else {
+                    scale_o *= __uint_as_float((uint32_t)(127 - min(de, 126)) << 23);   // (de > 10 only at the first stage)
+                }
+                if (j > t.s0 && __any_sync(0xffffffffu, scale_o != 1.f)) {
+                    // tcgen05.ld/st are warp-wide: lanes that keep their references scale by 1
+                    wait(pv_done(c, x), (uint32_t)((done - 1) & 1));
+                    if (alive) {
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c16 = 0; c16 < D / 16; ++c16) {
+                            uint32_t ov[16];
+                            tmem_ld16_nowait(orow + (uint32_t)(c16 * 16), ov);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                ov[i] = __float_as_uint(__uint_as_float(ov[i]) * scale_o);
+                            tmem_st16_nowait(orow + (uint32_t)(c16 * 16), ov);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                const float mu = m_use == -INFINITY ? 0.f : m_use - kPLog2;
+                const float mu2 = m2 == -INFINITY ? 0.f : m2 - (float)e - kPLog2;
+                part = 0.f;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float w[4];
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            w[v] = ex2_approx(__uint_as_float(sv[q][4 * i + v]) - mu);
+                            part += w[v];
+                        }
+                        if (apart) {
+                            const float4 f = pf[q * 8 + i];
+                            const float fs[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                            for (int v = 0; v < 4; ++v)
+                                w[v] = ex2_approx(__uint_as_float(sv[q][4 * i + v]) + fs[v] - mu2);
+                        }
+                        pk[2 * i] = pack_half2(w[0], w[1]);
+                        pk[2 * i + 1] = pack_half2(w[2], w[3]);
+                    }
+                    tmem_st16_nowait(srow + (uint32_t)(q * 16), pk);
+                }
+            }
+            lsum += part;
+            tmem_wait_st();
+            tc_fence_before();
+            ++done;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(p_full(c, x));
+        }
+
+        // --- this row of O_x, normalised, and its log-sum-exp
+        const bool whole = t.s0 == 0 && t.s1 == t.nst_all;
+        const bool any = s1 > t.s0;                      // this tile attends a stage of the piece
+        if (any)
+            wait(pv_done(c, x), (uint32_t)((done - 1) & 1));
+        if (alive && t.ntok[x] > 0) {
+            tc_fence_after();
+            const float inv = lsum != 0.f ? __frcp_rn(lsum) : 0.f;       // (a NaN sum stays NaN)
+            const float ef = apart ? ex2_approx(m2 - m_use - (float)(kVLog2 + 127))
+                                   : q8_scale((uint32_t)e) * (1.f / (1 << kVLog2));
+            const int64_t orr = tok * p.hq + head;
+            const int slot = piece_slot(p, blockIdx.x, t.u);
+            const int64_t prow = (int64_t)slot * kChunkRows + x * 128 + r;
+#pragma unroll 1
+            for (int c16 = 0; c16 < D / 16; ++c16) {
+                uint32_t ov[16];
+                tmem_ld16_nowait(orow + (uint32_t)(c16 * 16), ov);
+                tmem_wait_ld();
+                float o[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[i] = any && lsum != 0.f ? __uint_as_float(ov[i]) * inv * ef : 0.f;
+                if (row_ok && whole) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + orr * D + c16 * 16);
+#pragma unroll
+                    for (int v = 0; v < 2; ++v)
+                        dst[v] = make_uint4(pack_bf16x2(o[8 * v], o[8 * v + 1]), pack_bf16x2(o[8 * v + 2], o[8 * v + 3]),
+                                            pack_bf16x2(o[8 * v + 4], o[8 * v + 5]), pack_bf16x2(o[8 * v + 6], o[8 * v + 7]));
+                } else if (row_ok) {
+                    float4 *dst = reinterpret_cast<float4 *>(p.ws_part + prow * D + c16 * 16);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        dst[v] = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+                }
+            }
+            if (row_ok) {
+                const float lse = lsum != 0.f ? ((m_use == -INFINITY ? 0.f : m_use - kPLog2) + log2f(lsum)) *
+                                                    0.6931471805599453f
+                                              : -INFINITY;
+                if (!whole)
+                    p.ws_lse[prow] = lse;
+                else if (p.lse_out)
+                    p.lse_out[orr] = lse;
+            }
+        }
+        tc_fence_before();
+        kbase += t.s1 - t.s0;
+        ++seg;
+    }
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kThreads, 1)
+    shkv_q8_chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                         const __grid_constant__ Q8ChunkParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    Ctx c;
+    {
+        const uint32_t raw = smem_u32(smem_raw);
+        const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+        c.smem = smem_raw + pad;
+        c.base = raw + pad;
+    }
+    c.lay = smem_layout();
+    c.abort_flag = reinterpret_cast<volatile uint32_t *>(c.smem + c.lay.misc);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kKS; ++i) {
+            mbar_init(full_k(c, i), 1);
+            mbar_init(empty_k(c, i), 1);
+        }
+        for (int i = 0; i < kVS; ++i) {
+            mbar_init(full_v(c, i), 1);
+            mbar_init(conv_v(c, i), kConvWarps);
+            mbar_init(empty_v(c, i), 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(s_full(c, x), 1);
+            mbar_init(p_full(c, x), kGroupWarps);
+            mbar_init(pv_done(c, x), 1);
+        }
+        mbar_init(q_ready(c), 2 * kGroupWarps);
+        mbar_init(q_free(c), 1);
+        mbar_init(fin_b(c), 2);
+        *c.abort_flag = 0u;
+        fence_barrier_init();
+    }
+    if (warp == 0)
+        tmem_alloc(c.base + c.lay.tslot, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(c.smem + c.lay.tslot);
+    pdl_wait_prior();
+    pdl_launch_dependents();
+
+    if (warp < 2 * kGroupWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        chunk_softmax(p, c, tmem, warp / kGroupWarps);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kKWarp)
+            chunk_producer<false>(&tmK, p, c);
+        else if (warp == kVWarp)
+            chunk_producer<true>(&tmV, p, c);
+        else if (warp == kQkWarp) {
+            if ((threadIdx.x & 31) == 0)
+                chunk_qk(p, c, tmem);
+        } else if (warp == kPvWarp) {
+            if ((threadIdx.x & 31) == 0)
+                chunk_pv(p, c, tmem);
+        } else {
+            chunk_convert(p, c);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0)
+        tmem_dealloc(tmem, kTmemCols);
+}
+
+// Joins the pieces of split units: a warp per row.  Block y takes the unit
+// that cut y (the start of CTA y + 1) falls inside, if it is the first cut in it.
+__global__ void __launch_bounds__(256) shkv_q8_chunk_join_kernel(const __grid_constant__ Q8ChunkParams p)
+{
+    pdl_wait_prior();
+    pdl_launch_dependents();
+    const int cut = blockIdx.y + 1;
+    const int u = p.cut_unit[cut];
+    if (p.cut_stage[cut] == 0 || (p.cut_unit[cut - 1] == u && p.cut_stage[cut - 1] > 0))
+        return;
+    Piece t;
+    t.u = u;
+    set_unit(p, t);
+    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int x = row >> 7, r = row & 127;
+    const int ti = r / p.group, tj = r - ti * p.group;
+    if (ti >= t.ntok[x])
+        return;
+    int last = cut;                              // last CTA that holds a piece
+    while (last + 1 < p.num_ctas && p.cut_unit[last + 1] == u && p.cut_stage[last + 1] > 0)
+        ++last;
+    float M = -INFINITY;
+    bool nan = false;
+    for (int i = cut - 1 + lane; i <= last; i += 32) {
+        const float v = p.ws_lse[(int64_t)piece_slot(p, i, u) * kChunkRows + row];
+        nan = nan || v != v;
+        M = fmaxf(M, v);
+    }
+    nan = __any_sync(0xffffffffu, nan);
+    for (int o = 16; o > 0; o >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const int D = p.head_dim;
+    float wsum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (nan) {
+        wsum = acc.x = acc.y = acc.z = acc.w = __uint_as_float(0x7fc00000u);
+    } else if (M != -INFINITY) {
+        for (int i = cut - 1; i <= last; ++i) {
+            const int64_t pr = (int64_t)piece_slot(p, i, u) * kChunkRows + row;
+            const float w = ex2_approx((p.ws_lse[pr] - M) * 1.4426950408889634f);
+            wsum += w;
+            if (lane < D / 4) {
+                const float4 v = reinterpret_cast<const float4 *>(p.ws_part + pr * D)[lane];
+                acc.x += w * v.x;
+                acc.y += w * v.y;
+                acc.z += w * v.z;
+                acc.w += w * v.w;
+            }
+        }
+    }
+    const float winv = wsum != 0.f ? 1.f / wsum : 0.f;
+    const int64_t orr = ((int64_t)p.q0[t.b] + t.i0[x] + ti) * p.hq + (int64_t)t.g * p.group + tj;
+    if (lane < D / 4)
+        *reinterpret_cast<uint2 *>(p.out + orr * D + lane * 4) =
+            make_uint2(pack_bf16x2(acc.x * winv, acc.y * winv), pack_bf16x2(acc.z * winv, acc.w * winv));
+    if (lane == 0 && p.lse_out)
+        p.lse_out[orr] = wsum != 0.f ? M + logf(wsum) : -INFINITY;
+}
+
+// tmK, tmV: 2-D maps of the code pools (box of 128 bytes x P rows, 128-byte swizzle).
+cudaError_t launch_q8_chunk(const CUtensorMap &tmK, const CUtensorMap &tmV, const Q8ChunkParams &p, bool splits,
+                            cudaStream_t stream)
+{
+    static int regs = -1;      // the register split hands out exactly the launch's 128 a thread
+    if (regs < 0) {
+        cudaFuncAttributes fa;
+        const cudaError_t e = cudaFuncGetAttributes(&fa, shkv_q8_chunk_kernel);
+        if (e != cudaSuccess)
+            return e;
+        regs = fa.numRegs;
+    }
+    if ((uint32_t)regs * kThreads != kSoftmaxRegs * 256 + kOtherRegs * 256)
+        return cudaErrorInvalidConfiguration;
+    const uint32_t smem = smem_layout().total;
+    cudaError_t e = cudaFuncSetAttribute(shkv_q8_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess)
+        e = launch_pdl(shkv_q8_chunk_kernel, p.num_ctas, kThreads, smem, stream, tmK, tmV, p);
+    if (e != cudaSuccess || !splits)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kChunkRows / 8, (unsigned)(p.num_ctas - 1));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, shkv_q8_chunk_join_kernel, p);
+}
+
+}  // namespace shkv

@@ -25,11 +25,12 @@
 // 11 bits of every token that matters to the sum, whatever the magnitudes of
 // weights and values apart: fp16's least step, 2^-24, is 2^-31 of that
 // largest, and 2^20 tokens below it are lost to 2^-12 of it.  E, a running
-// upper bound of the segment's V exponents, keeps the fp32 sums l at 2^7 or
-// more.  A token whose V exponent is under E - 60 takes part with V = 0 and
-// that exponent, which bounds l's terms by 2^75; where E rises over tokens
-// already summed, m is kept high enough for 2^97 (b[r] is that bound).  Sums
-// and O are fp32.
+// upper bound (at least 2^-67) of the V exponents of the segment's keys that
+// every row sees, keeps the fp32 sums l at 2^7 or more; a draft's key, which
+// some rows only see, may exceed it by 2^100.  A token whose V exponent is
+// under E - 60 takes part with V = 0 and that exponent, which bounds l's terms
+// by 2^75; where E rises over tokens already summed, m is kept high enough for
+// 2^97 (b[r] is that bound).  Sums and O are fp32.
 //
 // Roles (512 threads):
 //   warps 0-7    softmax: warp w owns tokens 32*(w%4) .. +31 and half w/4 of
@@ -76,6 +77,7 @@ constexpr uint32_t kColS = 0;               // S^T buffers at columns 0 and 64
 constexpr uint32_t kColO = 128;             // O^T
 constexpr float kRescaleLog2 = 8.f;         // m lags the maximum by at most this
 constexpr float kPLog2 = 7.f;               // P is 2^7 at the running maximum: 2^15 at most
+constexpr int kMinE = 60;                   // scale byte of the least E
 constexpr int kEHeadroom = 4;               // E moves to this much above a stage's largest V exponent
 constexpr int kVWindow = 60;                // V exponents under E - 60 count as zero values
 constexpr float kTermLog2 = kVWindow + kRescaleLog2;   // a new term of l is at most 2^(this + 7)
@@ -183,8 +185,15 @@ __device__ __forceinline__ int stage_top_scale(const Ctx4 &c, int k, int n, uint
     return (int)__reduce_max_sync(0xffffffffu, top);
 }
 
+// Keys below this are seen by every row of the unit.
+__device__ __forceinline__ int keys_all_see(const Q8DecodeParams &q, const Segment &s)
+{
+    const int L = plan_len(q.d, s);
+    return q.causal ? L - q.n_q[s.b] + 1 : L;
+}
+
 // E (as a scale byte) from the one before and a stage's largest scale byte.
-__device__ __forceinline__ int next_e(int e, int top) { return top > e ? top + kEHeadroom : e; }
+__device__ __forceinline__ int next_e(int e, int top) { return top > e ? min(top + kEHeadroom, 254) : e; }
 
 // D[tmem] (+)= A[smem] . B[smem]^T on e4m3 / on fp16 operands, fp32 accumulate.
 __device__ __forceinline__ void umma_f8(uint32_t d_taddr, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -359,7 +368,8 @@ __device__ void convert_v(const Q8DecodeParams &q, const Ctx4 &c)
     for (;;) {
         const int nst = stages_of(s, P);
         const int lim = min(plan_len(p, s), s.p1 * P);
-        int e = 0;
+        const int all_see = keys_all_see(q, s);
+        int e = kMinE;
         for (int j = 0; j < nst; ++j) {
             const int k = kbase + j, slot = k % c.vs;
             bool ok = false;
@@ -369,8 +379,8 @@ __device__ void convert_v(const Q8DecodeParams &q, const Ctx4 &c)
             alive = __all_sync(0xffffffffu, ok);
             if (alive) {
                 const uint32_t mask = reinterpret_cast<volatile uint32_t *>(c.smem + c.lay.meta)[k % kScaleRing] & 0xffu;
-                const int n = lim - (s.p0 * P + j * kTT);          // tokens of the stage that count
-                e = next_e(e, stage_top_scale(c, k, n, mask, log2P));
+                const int tok0 = s.p0 * P + j * kTT, n = lim - tok0;   // tokens of the stage that count
+                e = next_e(e, stage_top_scale(c, k, min(n, all_see - tok0), mask, log2P));
                 const int vb = (int)scale_at(c, k, t, log2P, 1);
                 // a row that does not count, and a NaN row (its key's score is
                 // made NaN instead, so that only rows that attend it see it), is zero
@@ -590,8 +600,8 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
         const int L = plan_len(p, s);
         const int R = q.n_q[s.b] * p.group;
         const int lim = min(L, s.p1 * P);
-        const int all_see = q.causal ? L - q.n_q[s.b] + 1 : L;      // keys below this are seen by every row
-        int e = 0;                              // scale byte of E
+        const int all_see = keys_all_see(q, s);
+        int e = kMinE;                          // scale byte of E
         float m_use[NH], l[NH];                 // m, and this token's share of l
 #pragma unroll
         for (int i = 0; i < NH; ++i) {
@@ -621,7 +631,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                 alive = false;
             }
             const int tok0 = s.p0 * P + j * kTT;
-            const int de = next_e(e, stage_top_scale(c, k, lim - tok0, tagged & 0xffu, log2P)) - e;
+            const int de = next_e(e, stage_top_scale(c, k, min(lim, all_see) - tok0, tagged & 0xffu, log2P)) - e;
             e += de;
             const bool valid = alive && (((tagged & 0xffu) >> (t >> log2P)) & 1u) && tok0 + t < lim;
             // the token's factor of the scores (NaN where its K or V row is),
@@ -631,7 +641,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                                        : q8_scale(scale_at(c, k, t, log2P, 0)) * p.scale_log2;
             const int ve = !valid || vb == 255 ? e : max(vb, e - kVWindow);
             const float ev = (float)(ve - 127);
-            const float undo = __uint_as_float((uint32_t)(127 + e - ve) << 23);
+            const float undo = __uint_as_float((uint32_t)max(127 + e - ve, 1) << 23);
             tc_fence_before();
             __syncwarp();
             if (lane == 0)

@@ -12,12 +12,14 @@
 
 #include "host_shared.h"
 #include "q8.cuh"
+#include "q8_chunk.cuh"
 #include "q8_decode.cuh"
 #include "shkv.h"
 
 namespace shkv {
 cudaError_t launch_q8_cache(const Q8CacheParams &p, bool read, int num_sms, cudaStream_t stream);
-cudaError_t launch_q8_attn(const Q8AttnParams &p, int max_rows, cudaStream_t stream);
+cudaError_t launch_q8_chunk(const CUtensorMap &tmK, const CUtensorMap &tmV, const Q8ChunkParams &p, bool splits,
+                            cudaStream_t stream);
 cudaError_t launch_q8_decode(const CUtensorMap &tmK, const CUtensorMap &tmV, Q8DecodeParams &q, cudaStream_t stream);
 }  // namespace shkv
 
@@ -122,14 +124,17 @@ constexpr int32_t kMaxDecodeRows = 64;     // stacked rows per KV head that one 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // The workspace: an arrival counter per (request, KV head) of the pool's
-// largest batch, then two partials per SM of up to 64 rows: their
-// log-sum-exps and rows.  Nothing else is ever written over the counters.
+// largest batch, then two partials per SM, log-sum-exps and rows, of up to 64
+// (stacked) or kChunkRows (chunk) rows.  Nothing else is ever written over the
+// counters; the two kernels of a call use the partials one after the other.
 size_t count_bytes(const shkv_q8_pool *p) { return align256((size_t)p->cfg.max_batch * p->cfg.num_kv_heads * 4); }
-size_t lse_bytes(const shkv_q8_pool *p) { return align256((size_t)2 * p->num_sms * kMaxDecodeRows * 4); }
+size_t lse_bytes(const shkv_q8_pool *p) { return align256((size_t)2 * p->num_sms * kChunkRows * 4); }
 size_t workspace_need(const shkv_q8_pool *p)
 {
-    return count_bytes(p) + lse_bytes(p) + (size_t)2 * p->num_sms * kMaxDecodeRows * p->cfg.head_dim * 4;
+    return count_bytes(p) + lse_bytes(p) + (size_t)2 * p->num_sms * kChunkRows * p->cfg.head_dim * 4;
 }
+
+int max_ctas(const shkv_q8_pool *p) { return std::min(p->num_sms, std::min(kMaxCtas, kChunkMaxCtas)); }
 
 // Up to 64 stacked rows per (request, KV head).
 shkv_status launch_stacked(shkv_q8_pool *pool, const Q8AttnParams &a, int max_rows, void *workspace, cudaStream_t stream)
@@ -146,8 +151,8 @@ shkv_status launch_stacked(shkv_q8_pool *pool, const Q8AttnParams &a, int max_ro
     }
     const int64_t r = max_rows;
     const shkv_status st =
-        plan_pages(a.batch, keys, a.page_size, a.hkv, pool->num_sms < kMaxCtas ? pool->num_sms : kMaxCtas, 128, 24 * r,
-                   10 * r, 56 * r, d.page_prefix, d.last_fill, d.cta_cut, &d.total_chunks, &d.num_ctas);
+        plan_pages(a.batch, keys, a.page_size, a.hkv, max_ctas(pool), 128, 24 * r, 10 * r, 56 * r,
+                   d.page_prefix, d.last_fill, d.cta_cut, &d.total_chunks, &d.num_ctas);
     if (st != SHKV_OK)
         return st;
     d.q = a.q;
@@ -174,6 +179,118 @@ shkv_status launch_stacked(shkv_q8_pool *pool, const Q8AttnParams &a, int max_ro
     q.head_dim = a.head_dim;
     q.causal = a.causal;
     return status_of(launch_q8_decode(pool->tm_k, pool->tm_v, q, stream));
+}
+
+// Cuts the units' stages into at most `limit` contiguous ranges so that the
+// costliest is as cheap as a greedy fill makes it (bisection over the bound).
+// In fifths of a stage of both tiles: a piece pays kPiece for its query rows,
+// the pipeline's fill and drain and its output, a stage 5 (3 with one tile).
+constexpr int64_t kPiece = 20, kPair = 5, kSingle = 3;
+constexpr int64_t kMinPiece = 2;            // stages; smaller pieces are not cut off
+
+bool plan_chunks(Q8ChunkParams &p, int limit)
+{
+    const int hkv = p.hkv, tpt = p.tpt;
+    int64_t total = 0, stages = 0;
+    for (int b = 0; b < p.batch; ++b) {
+        const int tiles = (p.n_q[b] + tpt - 1) / tpt;
+        for (int tp = 0; 2 * tp < tiles; ++tp) {
+            const int64_t nst = chunk_stages(p.lens[b], p.n_q[b], tpt, tp);
+            total += hkv * (kPiece + nst * (2 * tp + 1 < tiles ? kPair : kSingle));
+            stages += hkv * nst;
+        }
+    }
+    const int64_t C = std::max<int64_t>(1, std::min<int64_t>(limit, stages / kMinPiece));
+    auto fill = [&](int64_t bound, bool out) -> int64_t {
+        int64_t acc = 0;
+        int c = 0, u = 0;
+        for (int b = 0; b < p.batch; ++b) {
+            const int tiles = (p.n_q[b] + tpt - 1) / tpt;
+            for (int g = 0; g < hkv; ++g)
+                for (int tp = 0; 2 * tp < tiles; ++tp, ++u) {
+                    const int64_t w = 2 * tp + 1 < tiles ? kPair : kSingle;
+                    int64_t rest = chunk_stages(p.lens[b], p.n_q[b], tpt, tp), s = 0;
+                    while (acc + kPiece + rest * w > bound) {
+                        int64_t m = std::min((bound - acc - kPiece) / w, rest - kMinPiece);
+                        if (m < kMinPiece)
+                            m = 0;
+                        if ((m == 0 && acc == 0) || ++c >= C)
+                            return C + 1;
+                        s += m;
+                        rest -= m;
+                        acc = 0;
+                        if (out) {
+                            p.cut_unit[c] = u;
+                            p.cut_stage[c] = (int32_t)s;
+                        }
+                    }
+                    acc += kPiece + rest * w;
+                }
+        }
+        if (out) {
+            p.cut_unit[0] = p.cut_stage[0] = 0;
+            p.cut_unit[c + 1] = u;
+            p.cut_stage[c + 1] = 0;
+        }
+        return c + 1;
+    };
+    int64_t lo = total / C - 1, hi = total / C + 2 * kPiece;
+    while (fill(hi, false) > C)
+        hi += hi - lo;
+    const int64_t tol = std::max<int64_t>(1, total / C / 256);
+    while (hi - lo > tol) {
+        const int64_t mid = lo + (hi - lo) / 2;
+        if (fill(mid, false) <= C)
+            hi = mid;
+        else
+            lo = mid;
+    }
+    p.num_ctas = (int32_t)fill(hi, true);
+    for (int c = 1; c < p.num_ctas; ++c)
+        if (p.cut_stage[c] > 0)
+            return true;
+    return false;
+}
+
+shkv_status launch_chunk(shkv_q8_pool *pool, const Q8AttnParams &a, void *workspace, cudaStream_t stream)
+{
+    Q8ChunkParams p;
+    memset(&p, 0, sizeof p);
+    p.q = a.q;
+    p.q_stride = a.q_stride;
+    p.out = a.out;
+    p.lse_out = a.lse_out;
+    p.scales = a.scales;
+    p.block_table = a.block_table;
+    p.seq_lens = a.seq_lens;
+    p.err = a.err;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.ws_lse = reinterpret_cast<float *>(ws + count_bytes(pool));
+    p.ws_part = reinterpret_cast<float *>(ws + count_bytes(pool) + lse_bytes(pool));
+    p.batch = a.batch;
+    p.hq = a.hq;
+    p.hkv = a.hkv;
+    p.group = a.group;
+    p.head_dim = a.head_dim;
+    p.page_size = a.page_size;
+    p.max_pages = a.max_pages;
+    p.num_pages = a.num_pages;
+    p.tpt = 128 / a.group;
+    p.scale_log2 = a.scale_log2;
+    int64_t units = 0;
+    for (int b = 0; b < a.batch; ++b) {
+        p.units[b] = (int32_t)units;
+        p.lens[b] = a.lens[b];
+        p.n_q[b] = a.n_q[b];
+        p.q0[b] = a.q0[b];
+        const int tiles = (a.n_q[b] + p.tpt - 1) / p.tpt;
+        units += (int64_t)a.hkv * ((tiles + 1) / 2);
+        if (units > INT32_MAX)
+            return SHKV_ERR_UNSUPPORTED;
+    }
+    p.units[a.batch] = (int32_t)units;
+    const bool splits = plan_chunks(p, max_ctas(pool));
+    return status_of(launch_q8_chunk(pool->tm_k, pool->tm_v, p, splits, stream));
 }
 
 // Both attentions: n_q query tokens of request b start at query token q0[b].
@@ -203,15 +320,27 @@ shkv_status attention(shkv_q8_pool *pool, Q8AttnParams &p, int32_t hq, const voi
     p.max_pages = c.max_pages_per_seq;
     p.num_pages = c.num_pages;
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    // requests of up to kMaxDecodeRows rows per KV head go to the stacked
+    // kernel, which is bound by the pages' bytes, the others to the chunk kernel
     int max_rows = 0;
     int64_t tokens = 0;
+    Q8AttnParams large = p;
+    bool any_large = false;
     for (int b = 0; b < p.batch; ++b) {
-        max_rows = std::max(max_rows, p.n_q[b] * p.group);
         tokens += p.n_q[b];
+        if ((int64_t)p.n_q[b] * p.group > kMaxDecodeRows) {
+            p.n_q[b] = 0;
+            any_large = true;
+        } else {
+            large.n_q[b] = 0;
+            max_rows = std::max(max_rows, p.n_q[b] * p.group);
+        }
     }
-    const shkv_status st = max_rows <= kMaxDecodeRows
-                               ? launch_stacked(pool, p, max_rows, workspace, (cudaStream_t)stream)
-                               : status_of(launch_q8_attn(p, max_rows, (cudaStream_t)stream));
+    shkv_status st = SHKV_OK;
+    if (any_large)
+        st = launch_chunk(pool, large, workspace, (cudaStream_t)stream);
+    if (st == SHKV_OK && max_rows > 0)
+        st = launch_stacked(pool, p, max_rows, workspace, (cudaStream_t)stream);
     if (st != SHKV_OK)
         return st;
     const size_t row = (size_t)hq * c.head_dim;

@@ -351,6 +351,25 @@ def test_chunk_of_uneven_magnitudes(new):
     check_chunk(c, q, new, 0.02, out, lse)
 
 
+@pytest.mark.parametrize("new", [150, 5])
+def test_a_later_tokens_magnitude_has_no_effect_on_earlier_rows(new):
+    c = Cache([300], 2, 128, 16, seed=26)
+    for t, j, byte in ((299, 1, 240), (298, 0, 200), (297, 1, 170)):
+        c.sc[int(c.table[0, t // 16]), :, j, t % 16] = byte
+    pool = c.pool()
+    q = c.q(new, 8)
+    out, lse = pool.chunk_attention(q, [new], scale=0.01, return_lse=True)
+    no_errors(pool)
+    k, v = c.rows(0)
+    n = new - 3                                              # the rows that see none of the three
+    limit = (torch.arange(n, device="cuda") + 300 - new + 1).repeat_interleave(4)
+    for h in range(2):
+        s = slice(4 * h, 4 * h + 4)
+        o, e, to, te = attend(q[:n, s].reshape(4 * n, -1), k[:297, h], v[:297, h], 0.01, limit)
+        check(out[:n, s].reshape(4 * n, -1), o, to, "out")
+        check(lse[:n, s].reshape(-1), e, te, "lse")
+
+
 def test_chunk_reads_strided_queries_and_writes_no_row_behind_the_last():
     c = Cache([200, 90], 2, 128, 16, seed=17)
     pool = c.pool()
