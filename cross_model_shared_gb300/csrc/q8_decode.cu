@@ -93,8 +93,8 @@ constexpr uint32_t kSoftmaxRegs = 168, kOtherRegs = 88;
 static_assert(kSoftmaxRegs * 256 + kOtherRegs * 256 == 128 * kThreads, "register split");
 
 // scratch rows of 64 words
-constexpr int kScrMax = 0, kScrNew = 4, kScrAlpha = 5, kScrL = 6, kScrM = 10, kScrInv = 11, kScrQ = 12, kScrLim = 13,
-              kScrOff = 14, kScrAlphaL = 15, kScrB = 16, kScrRows = 17;
+constexpr int kScrMax = 0, kScrNew = 4, kScrAlpha = 5, kScrL = 6, kScrM = 10, kScrInv = 11, kScrQ = 12, kScrOff = 13,
+              kScrAlphaL = 14, kScrB = 15, kScrRows = 16;
 
 __host__ __device__ constexpr int q_nr(int rows) { return (rows + 15) / 16 * 16; }
 // N of the PV MMA: 48 is rounded up to a whole 64-column swizzle span.
@@ -214,6 +214,13 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
 {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Two e4m3 codes (low 16 bits) as fp16.
+__device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t codes)
+{
+    const __half2 h(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3));
+    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // ---------------------------------------------------------------------------
@@ -389,17 +396,15 @@ __device__ void convert_v(const Q8DecodeParams &q, const Ctx4 &c)
                 uint4 raw[8];
 #pragma unroll
                 for (int ch = 0; ch < 8; ++ch)
-                    raw[ch] = *reinterpret_cast<const uint4 *>(row + kTT * 128 + ((ch ^ (t & 7)) << 4));
+                    raw[ch] = live ? *reinterpret_cast<const uint4 *>(row + kTT * 128 + ((ch ^ (t & 7)) << 4))
+                                   : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                 for (int ch = 0; ch < 8; ++ch) {
                     const uint32_t w[4] = {raw[ch].x, raw[ch].y, raw[ch].z, raw[ch].w};
                     uint32_t o[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const __half2 h(__nv_cvt_fp8x2_to_halfraw2(
-                            (__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3));
-                        o[i] = live ? *reinterpret_cast<const uint32_t *>(&h) : 0u;
-                    }
+                    for (int i = 0; i < 8; ++i)
+                        o[i] = widen_e4m3x2(w[i >> 1] >> (16 * (i & 1)));
                     uint8_t *dst = row + (ch >> 2) * (kTT * 128);
                     const int c0 = (2 * ch) & 7;
                     *reinterpret_cast<uint4 *>(dst + ((c0 ^ (t & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -536,7 +541,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
 
     // Query rows of segment `sg`: bf16 staging buffer -> the two swizzled
     // e4m3 tiles and the rows' scales; D/8 lanes a row.  Rows past the unit's
-    // are zero.  Also the rows' key limits.
+    // are zero.
     auto stage_q = [&](int sg, const Segment &u) {
         wait(qfull(c), (uint32_t)(sg & 1));
         const int LR = D / 8, log2LR = 31 - __clz(LR);
@@ -580,10 +585,6 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                     scr[kScrQ * 64 + r] = bad ? 1.f : q8_scale((uint32_t)byte);
             }
         }
-        if (threadIdx.x < 64) {
-            const int L = plan_len(p, u);
-            scr_i[kScrLim * 64 + threadIdx.x] = q.causal ? L - q.n_q[u.b] + (int)threadIdx.x / p.group + 1 : L;
-        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -597,30 +598,21 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
     stage_q(0, s);
     for (;;) {
         const int nst = stages_of(s, P);
-        const int L = plan_len(p, s);
         const int R = q.n_q[s.b] * p.group;
-        const int lim = min(L, s.p1 * P);
+        const int lim = min(plan_len(p, s), s.p1 * P);
         const int all_see = keys_all_see(q, s);
         int e = kMinE;                          // scale byte of E
-        float m_use[NH], l[NH];                 // m, and this token's share of l
+        float2 nmu[NH / 2], l[NH / 2];          // 7 - m (1e30: no key yet), and this token's share of l
 #pragma unroll
-        for (int i = 0; i < NH; ++i) {
-            m_use[i] = -INFINITY;
-            l[i] = 0.f;
+        for (int i = 0; i < NH / 2; ++i) {
+            nmu[i] = make_float2(1e30f, 1e30f);
+            l[i] = make_float2(0.f, 0.f);
         }
-        named_barrier(1, kSoftmaxThreads);      // the rows' scales and limits are in place
+        named_barrier(1, kSoftmaxThreads);      // the rows' scales are in place
 
         for (int j = 0; j < nst; ++j) {
             const int k = kbase + j, buf = k & 1;
-            uint32_t sv[NH];
-            if (wait(s_full(c, buf), (uint32_t)((k >> 1) & 1))) {
-                tc_fence_after();
-                tmem_ld_half<NH>(tmem + lane_base + kColS + (uint32_t)(buf * 64), hh, sv);
-            } else {
-#pragma unroll
-                for (int i = 0; i < NH; ++i)
-                    sv[i] = 0u;
-            }
+            // --- the token's scales, which come with K
             wait(scale_b(c, k % kScaleRing), ring_par(k, kScaleRing));
             const uint32_t tagged = alive ? meta[k % kScaleRing] : 0u;
             if (alive && (tagged >> 8) != ((uint32_t)k & 0xffffffu)) {
@@ -642,28 +634,52 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
             const int ve = !valid || vb == 255 ? e : max(vb, e - kVWindow);
             const float ev = (float)(ve - 127);
             const float undo = __uint_as_float((uint32_t)max(127 + e - ve, 1) << 23);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(s_free(c, buf));
-            float xs[NH];
-            bool need = false;
-            const bool masked = tok0 + kTT > all_see;
+            // rows from this one on see the token (new token i from position L - n + i on)
+            const int row_min = valid ? max(0, (tok0 + t - all_see + 1) * p.group) : 64;
+            const bool masked = __any_sync(0xffffffffu, row_min > 0);
+            // y - m + 7 of this thread's rows (nm = 7 - m), -inf where not seen
+            float2 d[NH / 2];
+            auto scores = [&](const float2 (&nm)[NH / 2]) {
+                uint32_t sv[NH];
+                tmem_ld_half<NH>(tmem + lane_base + kColS + (uint32_t)(buf * 64), hh, sv);
+                const float2 ts2 = make_float2(ts, ts), ev2 = make_float2(ev, ev);
 #pragma unroll
-            for (int i = 0; i < NH; ++i) {
-                const int r = half_row(hh, i);
-                const bool sees = valid && (!masked || tok0 + t < scr_i[kScrLim * 64 + r]);
-                xs[i] = sees ? fmaf(__uint_as_float(sv[i]), ts * scr[kScrQ * 64 + r], ev) : -INFINITY;
-                need = need || (xs[i] > m_use[i] + kRescaleLog2);
-            }
+                for (int ch = 0; ch < NH / 8; ++ch) {
+                    const float4 *rq = reinterpret_cast<const float4 *>(scr + kScrQ * 64 + 16 * ch + 8 * hh);
+                    const float4 qa = rq[0], qb = rq[1];
+                    const float2 q2[4] = {make_float2(qa.x, qa.y), make_float2(qa.z, qa.w), make_float2(qb.x, qb.y),
+                                          make_float2(qb.z, qb.w)};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int o = 4 * ch + i;
+                        const float2 s2 = make_float2(__uint_as_float(sv[2 * o]), __uint_as_float(sv[2 * o + 1]));
+                        d[o] = __ffma2_rn(s2, __fmul2_rn(ts2, q2[i]), __fadd2_rn(ev2, nm[o]));
+                        if (masked) {
+                            if (half_row(hh, 2 * o) < row_min)
+                                d[o].x = -INFINITY;
+                            if (half_row(hh, 2 * o + 1) < row_min)
+                                d[o].y = -INFINITY;
+                        }
+                    }
+                }
+            };
+            if (wait(s_full(c, buf), (uint32_t)((k >> 1) & 1)))
+                tc_fence_after();
+            scores(nmu);
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < NH / 2; ++i)
+                top = fmaxf(top, fmaxf(d[i].x, d[i].y));
             // --- lazy refresh of the maxima: all warps agree
-            if (bar_red_or(1, kSoftmaxThreads, need || de > 0)) {
+            if (bar_red_or(1, kSoftmaxThreads, top > kPLog2 + kRescaleLog2 || de > 0)) {
+                const float2 none[NH / 2] = {};
+                scores(none);                   // y
                 {
                     constexpr int M = pow2_at_least(NH);
                     float v[M];
 #pragma unroll
                     for (int i = 0; i < M; ++i)
-                        v[i] = i < NH ? xs[i] : -INFINITY;
+                        v[i] = i < NH ? ((i & 1) ? d[(i < NH ? i : 0) / 2].y : d[(i < NH ? i : 0) / 2].x) : -INFINITY;
                     ReduceScatter<M, 16, true>::run(v, lane);
                     const int base = rs_base<M>(lane);
                     if (rs_owner<M>(lane))
@@ -685,7 +701,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                         mn = fmaxf(mn, mo + (b - kMaxTermLog2));
                         scr[kScrB * 64 + r] = fmaxf(b - (mn - mo), kTermLog2);
                     }
-                    scr[kScrNew * 64 + r] = mn;
+                    scr[kScrNew * 64 + r] = mn == -INFINITY ? 1e30f : kPLog2 - mn;
                     scr[kScrAlpha * 64 + r] = mn == -INFINITY ? 1.f : ex2_approx(mo - mn);
                     scr[kScrAlphaL * 64 + r] = mn == -INFINITY ? 1.f : ex2_approx(mo - mn + (float)de);
                     scr[kScrM * 64 + r] = mn;
@@ -706,21 +722,23 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < NH; ++i) {
-                    m_use[i] = scr[kScrNew * 64 + half_row(hh, i)];
-                    l[i] *= scr[kScrAlphaL * 64 + half_row(hh, i)];
+                for (int i = 0; i < NH / 2; ++i) {
+                    const int r = half_row(hh, 2 * i);
+                    nmu[i] = make_float2(scr[kScrNew * 64 + r], scr[kScrNew * 64 + r + 1]);
+                    d[i] = __fadd2_rn(d[i], nmu[i]);
+                    l[i] = __fmul2_rn(l[i], make_float2(scr[kScrAlphaL * 64 + r], scr[kScrAlphaL * 64 + r + 1]));
                 }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(s_free(c, buf));
             uint32_t pk[NH / 2];
 #pragma unroll
-            for (int i = 0; i < NH; i += 2) {
-                const float mu0 = m_use[i] == -INFINITY ? 0.f : m_use[i] - kPLog2;
-                const float mu1 = m_use[i + 1] == -INFINITY ? 0.f : m_use[i + 1] - kPLog2;
-                const float p0 = ex2_approx(xs[i] - mu0);
-                const float p1 = ex2_approx(xs[i + 1] - mu1);
-                l[i] = fmaf(p0, undo, l[i]);
-                l[i + 1] = fmaf(p1, undo, l[i + 1]);
-                pk[i / 2] = pack_half2(p0, p1);
+            for (int i = 0; i < NH / 2; ++i) {
+                const float2 pe = make_float2(ex2_approx(d[i].x), ex2_approx(d[i].y));
+                l[i] = __ffma2_rn(pe, make_float2(undo, undo), l[i]);
+                pk[i] = pack_half2(pe.x, pe.y);
             }
             // --- P^T, once the previous stage's product has read the buffer
             if (k > 0)
@@ -745,7 +763,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
         if (has_next) {
             sn = next_segment(p, s, c.cta_end);
             wait(q_tile_free(c), (uint32_t)(seg & 1));
-            named_barrier(1, kSoftmaxThreads);  // every warp is past its last use of the rows' scales and limits
+            named_barrier(1, kSoftmaxThreads);  // every warp is past its last use of the rows' scales
             stage_q(seg + 1, sn);
         }
 
@@ -755,7 +773,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
             float v[M];
 #pragma unroll
             for (int i = 0; i < M; ++i)
-                v[i] = i < NH ? l[i] : 0.f;
+                v[i] = i < NH ? ((i & 1) ? l[(i < NH ? i : 0) / 2].y : l[(i < NH ? i : 0) / 2].x) : 0.f;
             ReduceScatter<M, 16, false>::run(v, lane);
             const int base = rs_base<M>(lane);
             if (rs_owner<M>(lane))
