@@ -46,6 +46,7 @@
 #include "launch.cuh"
 #include "q8.cuh"
 #include "q8_chunk.cuh"
+#include "q8_wait.cuh"
 #include "shkv_device.cuh"
 
 namespace shkv {
@@ -123,39 +124,6 @@ __device__ __forceinline__ uint32_t fin_b(const Ctx &c) { return bar_at(c, kBar0
 __device__ __forceinline__ uint32_t k_slot(const Ctx &c, int s) { return c.base + c.lay.kring + (uint32_t)s * kKSlotBytes; }
 __device__ __forceinline__ uint32_t v_slot(const Ctx &c, int s) { return c.base + c.lay.vring + (uint32_t)s * kVSlotBytes; }
 __device__ __forceinline__ uint32_t ring_par(int k, int n) { return (uint32_t)((k / n) & 1); }
-
-// Bounded wait that sleeps on the barrier (issuers, producers): the waiting
-// warps leave the issue slots to the softmax warps.
-__device__ __forceinline__ bool try_wait_sleep(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(20000u)
-        : "memory");
-    return ok != 0;
-}
-
-__device__ bool wait_sleep(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag, uint32_t *err)
-{
-    if (try_wait_sleep(bar, parity))
-        return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (;;) {
-        if (try_wait_sleep(bar, parity))
-            return true;
-        if (*abort_flag)
-            return false;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
-            *abort_flag = 1u;
-            atomicOr(err, SHKV_ERRF_TIMEOUT);
-            return false;
-        }
-    }
-}
 
 // A piece of a unit: its key stages [s0, s1).
 struct Piece {
@@ -242,6 +210,7 @@ __device__ void chunk_producer(const CUtensorMap *tm, const Q8ChunkParams &p, co
     bool alive = true;
     int kbase = 0, last_issued = -1;
     Piece t;
+#pragma unroll 1
     for (bool more = first_piece(p, t); more; more = next_piece(p, t)) {
         if (kIsV && lane == 0 && __ldg(p.seq_lens + t.b) != t.L)
             atomicOr(p.err, SHKV_ERRF_SEQ_LEN);
@@ -252,13 +221,14 @@ __device__ void chunk_producer(const CUtensorMap *tm, const Q8ChunkParams &p, co
             return lane < RB && j < t.s1 && pg < npages ? __ldg(row + pg) : -1;
         };
         int nxt = entry(t.s0);
+#pragma unroll 1
         for (int j = t.s0; j < t.s1; ++j) {
             const int k = kbase + j - t.s0, slot = k % S;
             const int id = nxt;
             nxt = entry(j + 1);                          // read one stage ahead
             bool ok = true;
             if (alive && lane == 0)
-                ok = wait_sleep(kIsV ? empty_v(c, slot) : empty_k(c, slot), ring_par(k, S) ^ 1u, c.abort_flag, p.err);
+                ok = q8_wait<true>(kIsV ? empty_v(c, slot) : empty_k(c, slot), ring_par(k, S) ^ 1u, c.abort_flag, p.err);
             alive = alive && __all_sync(0xffffffffu, ok);
             const bool inside = lane < RB && j * RB + lane < npages;
             const bool valid = inside && id >= 0 && id < p.num_pages;
@@ -303,14 +273,16 @@ __device__ void chunk_convert(const Q8ChunkParams &p, const Ctx &c)
     bool alive = true;
     int kbase = 0;
     Piece u;
+#pragma unroll 1
     for (bool more = first_piece(p, u); more; more = next_piece(p, u)) {
         int e = 0;                                       // E as a scale byte
         bool wide = false;
+#pragma unroll 1
         for (int j = u.s0; j < u.s1; ++j) {
             const int k = kbase + j - u.s0, slot = k % kVS;
             bool ok = false;
             if (alive)
-                ok = mbar_wait_bounded(full_v(c, slot), ring_par(k, kVS), c.abort_flag, p.err);
+                ok = q8_wait<false>(full_v(c, slot), ring_par(k, kVS), c.abort_flag, p.err);
             alive = __all_sync(0xffffffffu, ok);
             if (alive) {
                 volatile uint32_t *info = reinterpret_cast<volatile uint32_t *>(c.smem + c.lay.info) + slot * 4;
@@ -431,12 +403,14 @@ __device__ void chunk_qk(const Q8ChunkParams &p, const Ctx &c, uint32_t tmem)
     bool alive = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (alive)
-            alive = wait_sleep(bar, parity, c.abort_flag, p.err);
+            alive = q8_wait<true>(bar, parity, c.abort_flag, p.err);
     };
     int kbase = 0, seg = 0, done[2] = {0, 0};            // stages each tile has attended
     Piece t;
+#pragma unroll 1
     for (bool more = first_piece(p, t); more; more = next_piece(p, t)) {
         wait(q_ready(c), (uint32_t)(seg & 1));
+#pragma unroll 1
         for (int j = t.s0; j < t.s1; ++j) {
             const int k = kbase + j - t.s0, slot = k % kKS;
             const uint64_t kd = kd0 + (((uint32_t)slot * kKSlotBytes) >> 4);
@@ -451,6 +425,7 @@ __device__ void chunk_qk(const Q8ChunkParams &p, const Ctx &c, uint32_t tmem)
                 if (alive) {
                     tc_fence_after();
                     const uint64_t qd = qd0 + ((2u * (uint32_t)x * kQTermBytes) >> 4);
+#pragma unroll 1
                     for (int i = 0; i < steps; ++i) {
                         umma_f8(tmem + col_s(x), qd + (uint64_t)(2 * i), kd + (uint64_t)(2 * i), idesc, i ? 1u : 0u);
                         umma_f8(tmem + col_s(x), qd + (kQTermBytes >> 4) + (uint64_t)(2 * i), kd + (uint64_t)(2 * i),
@@ -476,11 +451,13 @@ __device__ void chunk_pv(const Q8ChunkParams &p, const Ctx &c, uint32_t tmem)
     bool alive = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (alive)
-            alive = wait_sleep(bar, parity, c.abort_flag, p.err);
+            alive = q8_wait<true>(bar, parity, c.abort_flag, p.err);
     };
     int kbase = 0, done[2] = {0, 0};
     Piece t;
+#pragma unroll 1
     for (bool more = first_piece(p, t); more; more = next_piece(p, t)) {
+#pragma unroll 1
         for (int j = t.s0; j < t.s1; ++j) {
             const int k = kbase + j - t.s0, slot = k % kVS;
             const uint64_t vd = vd0 + (((uint32_t)slot * kVSlotBytes) >> 4);
@@ -523,6 +500,7 @@ __device__ __forceinline__ float stage_row(const Q8ChunkParams &p, const Ctx &c,
     const int D = p.head_dim;
     const uint4 *s4 = reinterpret_cast<const uint4 *>(src);
     uint32_t a = 0;
+#pragma unroll 4
     for (int ch = 0; ch < D / 8; ++ch) {
         const uint4 v = src ? __ldg(s4 + ch) : make_uint4(0u, 0u, 0u, 0u);
         a = __vmaxu2(__vmaxu2(a, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)),
@@ -534,6 +512,7 @@ __device__ __forceinline__ float stage_row(const Q8ChunkParams &p, const Ctx &c,
     const float inv = __uint_as_float((uint32_t)(254 - byte) << 23);
     const bool bad = a >= 0x7f80u;                       // an infinity or a NaN: the row's scores are NaN
     uint8_t *dst = c.smem + c.lay.qtile + 2u * (uint32_t)x * kQTermBytes + (uint32_t)r * 128u;
+#pragma unroll 1
     for (int ch = 0; ch < D / 16; ++ch) {
         uint32_t hi[4], lo[4];
 #pragma unroll
@@ -576,12 +555,13 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
     auto wait = [&](uint32_t bar, uint32_t parity) {
         bool ok = false;
         if (alive)
-            ok = mbar_wait_bounded(bar, parity, c.abort_flag, p.err);
+            ok = q8_wait<false>(bar, parity, c.abort_flag, p.err);
         alive = __all_sync(0xffffffffu, ok) && alive;
         return alive;
     };
     int kbase = 0, seg = 0, done = 0;                    // done: stages this tile has attended
     Piece t;
+#pragma unroll 1
     for (bool more = first_piece(p, t); more; more = next_piece(p, t)) {
         const bool row_ok = ti < t.ntok[x];
         const int pos = t.prefix + t.i0[x] + ti;         // keys 0 .. pos
@@ -600,6 +580,7 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
         bool apart = false;
         int e = 0;                                       // E as a scale byte
         const int s1 = min(t.s1, t.nst[x]);
+#pragma unroll 1
         for (int j = t.s0; j < s1; ++j) {
             const int k = kbase + j - t.s0, vs = k % kVS;
             const int key0 = j * kKT;

@@ -12,15 +12,15 @@
 //   S^T[t, r]  = sum_d k8[t, d] (qh[r, d] + ql[r, d])             kind::f8f6f4
 //   y[t, r]    = S^T[t, r] * 2^ek[t] * 2^eq[r] * scale * log2(e) + ev[t]
 //   P^T[t, r]  = 2^(y - m[r] + 7),  m[r] a running maximum of y    fp16
-//   O^T[d, r] += sum_t v8[t, d] P^T[t, r]                         kind::f16
+//   O^T[d, r] += sum_t 2^-8 v8[t, d] P^T[t, r]                    kind::f16
 //   l[r]      += sum_t P^T[t, r] * 2^(E - ev[t])                  (P before its rounding)
-//   out = O^T * 2^E / l,   lse = ln2 * (m - 7 - E + log2(l))
+//   out = O^T * 2^(E + 8) / l,   lse = ln2 * (m - 7 - E + log2(l))
 //
 // K's codes go to the tensor cores as they lie in the page.  A bf16 query has
 // 8 significant bits: its row is scaled by a power of two to at most 448 and
 // split into two e4m3 terms, qh nearest and ql = q - qh, which is exact but
-// for values under 2^-15 of the row's largest.  V's codes are widened to fp16
-// in shared memory, exactly.  With the token's V exponent inside y, P is
+// for values under 2^-15 of the row's largest.  V's codes are moved to fp16
+// in shared memory (sign and seven bits, exponent bias and all: v8 * 2^-8, exactly).  With the token's V exponent inside y, P is
 // relative to the row's largest weight times value scale, so that fp16 holds
 // 11 bits of every token that matters to the sum, whatever the magnitudes of
 // weights and values apart: fp16's least step, 2^-24, is 2^-31 of that
@@ -32,17 +32,23 @@
 // by 2^75; where E rises over tokens already summed, m is kept high enough for
 // 2^97 (b[r] is that bound).  Sums and O are fp32.
 //
+// Up to 32 rows the softmax is bound by the latency of its chain, not by its
+// instructions: its two groups of four warps then take alternate stages, each
+// with all rows, a running maximum, sums and O of its own, joined at the
+// segment's end.  Above, both groups work on every stage, on half the rows.
+//
 // Roles (512 threads):
-//   warps 0-7    softmax: warp w owns tokens 32*(w%4) .. +31 and half w/4 of
-//                the rows; also stages the query rows and reads O^T out
+//   warps 0-7    softmax: warp w owns tokens 32*(w%4) .. +31 of its stages;
+//                also stages the query rows and reads O^T out
 //   warp 8       QK issuer (one lane)
 //   warp 9       producer of K pages, scales, query rows and validity words
 //   warp 10      PV issuer (one lane)
 //   warp 11      producer of V pages
-//   warps 12-15  V conversion, one token a thread: the codes land in the upper
-//                16 KB of a 32 KB slot, where the thread reads its row and
-//                writes it back as fp16 over both halves (row t's codes lie
-//                inside row t's fp16 bytes, so no thread waits for another)
+//   warps 12-15  one token a thread: the token's factors for the softmax, and
+//                V's conversion: the codes land in the upper 16 KB of a 32 KB
+//                slot, where the thread reads its row and writes it back as
+//                fp16 over both halves (row t's codes lie inside row t's fp16
+//                bytes, so no thread waits for another)
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -53,6 +59,7 @@
 #include "decode_common.cuh"
 #include "launch.cuh"
 #include "q8_decode.cuh"
+#include "q8_wait.cuh"
 #include "umma_rows.cuh"
 
 namespace shkv {
@@ -84,97 +91,107 @@ constexpr float kTermLog2 = kVWindow + kRescaleLog2;   // a new term of l is at 
 constexpr float kMaxTermLog2 = 90.f;        // ... and stays at most 2^(this + 7): 2^20 of them fit fp32
 constexpr uint32_t kKSlotBytes = kTT * 128;
 constexpr uint32_t kVSlotBytes = 2 * kTT * 128;
-constexpr int kScaleRing = 8;               // see the note at the producer
-constexpr int kMaxKSlots = 4;
-static_assert(kMaxKSlots + 4 <= kScaleRing, "scales of a stage live until its V is converted");
+constexpr uint32_t kPBytes = kTT * 128;
+constexpr int kScaleRing = 8;               // stages of scale bytes, see the note at the producer
 // registers: 168 for the softmax warpgroups, 88 for the other two, of the
 // launch's 128 a thread
 constexpr uint32_t kSoftmaxRegs = 168, kOtherRegs = 88;
 static_assert(kSoftmaxRegs * 256 + kOtherRegs * 256 == 128 * kThreads, "register split");
 
-// scratch rows of 64 words
-constexpr int kScrMax = 0, kScrNew = 4, kScrAlpha = 5, kScrL = 6, kScrM = 10, kScrInv = 11, kScrQ = 12, kScrOff = 13,
-              kScrAlphaL = 14, kScrB = 15, kScrRows = 16;
+// scratch rows of 64 words: per softmax group the stage maxima and the sums
+// [token group], the new 7 - m, the rescaling of O and of l, m, the bound b;
+// then the factors of the two groups at the segment's end, the queries' scales
+// and the rows' output offsets
+constexpr int kScrMax = 0, kScrNew = 4, kScrAlpha = 5, kScrAlphaL = 6, kScrM = 7, kScrB = 8, kScrGroup = 9;
+constexpr int kScrEnd = 2 * kScrGroup, kScrQ = kScrEnd + 2, kScrOff = kScrQ + 1, kScrRows = kScrOff + 1;
 
 __host__ __device__ constexpr int q_nr(int rows) { return (rows + 15) / 16 * 16; }
 // N of the PV MMA: 48 is rounded up to a whole 64-column swizzle span.
 __host__ __device__ constexpr int q_npv(int nr) { return nr == 48 ? 64 : nr; }
+// The softmax groups take alternate stages.
+__host__ __device__ constexpr bool q_pingpong(int nr) { return nr <= 32; }
+
+constexpr int kKS = 4, kVS = 3;             // ring slots
+constexpr int kInfo = kVS + 1;              // stages of token factors (see convert_v)
+static_assert(kKS <= kScaleRing, "scales of a stage live until its factors are taken");
 
 struct Smem {
-    uint32_t kring, vring, pbuf, qtile, qhalf, qbuf, scr, scales, bars, meta, misc, tslot, total;
+    uint32_t vring, pbuf, qtile, qhalf, qbuf, scr, scales, info, bars, meta, misc, tslot, total;
 };
 
-// K ring, V ring (slots [half][128 tokens][128 B]), P^T [128 tokens][128 B]
-// and the query tiles [qh | ql][NR rows][128 B] are 128-byte swizzled; qbuf
-// holds the next segment's bf16 query rows.
-__host__ __device__ inline Smem smem_layout(int rows, int head_dim, int ks, int vs)
+// From offset 0: the K ring, the V ring (slots [half][128 tokens][128 B]), P^T
+// [128 tokens][128 B] of each group that has its own, and the query tiles
+// [qh | ql][NR rows][128 B], all 128-byte swizzled; qbuf holds the next
+// segment's bf16 query rows; info a stage's token factors (score factor, V
+// exponent, l factor, first row that sees the token).
+__host__ __device__ constexpr Smem smem_layout(int nr)
 {
-    Smem u;
-    u.kring = 0;
-    u.vring = u.kring + (uint32_t)ks * kKSlotBytes;
-    u.pbuf = u.vring + (uint32_t)vs * kVSlotBytes;
-    u.qtile = u.pbuf + kTT * 128;
-    u.qhalf = (uint32_t)q_nr(rows) * 128u;
+    Smem u{};
+    u.vring = kKS * kKSlotBytes;
+    u.pbuf = u.vring + kVS * kVSlotBytes;
+    u.qtile = u.pbuf + (q_pingpong(nr) ? 2u : 1u) * kPBytes;
+    u.qhalf = (uint32_t)nr * 128u;
     u.qbuf = u.qtile + 2 * u.qhalf;
-    u.scr = align_up(u.qbuf + (uint32_t)(rows * head_dim * 2), 128);
+    u.scr = u.qbuf + (uint32_t)nr * 256u;
     u.scales = u.scr + kScrRows * 64 * 4;
-    u.bars = u.scales + kScaleRing * 2 * kTT;
-    // full_k[ks], empty_k[ks], full_v[vs], conv[vs], empty_v[vs], scale[ring],
-    // p_full, pv_done, qfull, qempty, s_full[2], s_free[2], q_ready, q_tile_free, fin
-    u.meta = u.bars + (uint32_t)(2 * ks + 3 * vs + kScaleRing + 11) * 8u;
-    u.misc = u.meta + kScaleRing * 4;
+    u.info = u.scales + kScaleRing * 2 * kTT;
+    u.bars = u.info + kInfo * kTT * 16u;
+    u.meta = u.bars + 48 * 8u;
+    u.misc = u.meta + (kScaleRing + kInfo) * 4u;       // validity words, then each info stage's E
     u.tslot = u.misc + 8;
     u.total = u.misc + 16 + 1024;           // + slack to align the base to 1024 bytes
     return u;
 }
+static_assert(smem_layout(64).total <= (uint32_t)kSmemLimit && smem_layout(32).total <= (uint32_t)kSmemLimit, "fits");
 
 struct Ctx4 {
     uint8_t *smem;
-    uint32_t base;
-    Smem lay;
-    int ks, vs;
+    uint32_t base, bars;
     volatile uint32_t *abort_flag;
     uint32_t *bcast;
     int64_t cta_begin, cta_end;
 };
 
-__device__ __forceinline__ uint32_t bar_at(const Ctx4 &c, int i) { return c.base + c.lay.bars + 8u * i; }
-__device__ __forceinline__ uint32_t full_k(const Ctx4 &c, int s) { return bar_at(c, s); }
-__device__ __forceinline__ uint32_t empty_k(const Ctx4 &c, int s) { return bar_at(c, c.ks + s); }
-__device__ __forceinline__ uint32_t full_v(const Ctx4 &c, int s) { return bar_at(c, 2 * c.ks + s); }
-__device__ __forceinline__ uint32_t conv_v(const Ctx4 &c, int s) { return bar_at(c, 2 * c.ks + c.vs + s); }
-__device__ __forceinline__ uint32_t empty_v(const Ctx4 &c, int s) { return bar_at(c, 2 * c.ks + 2 * c.vs + s); }
-__device__ __forceinline__ uint32_t scale_b(const Ctx4 &c, int i) { return bar_at(c, 2 * c.ks + 3 * c.vs + i); }
-__device__ __forceinline__ uint32_t tail_b(const Ctx4 &c, int i) { return scale_b(c, kScaleRing + i); }
-__device__ __forceinline__ uint32_t p_full(const Ctx4 &c) { return tail_b(c, 0); }
-__device__ __forceinline__ uint32_t pv_done(const Ctx4 &c) { return tail_b(c, 1); }
-__device__ __forceinline__ uint32_t qfull(const Ctx4 &c) { return tail_b(c, 2); }
-__device__ __forceinline__ uint32_t qempty(const Ctx4 &c) { return tail_b(c, 3); }
-__device__ __forceinline__ uint32_t s_full(const Ctx4 &c, int b) { return tail_b(c, 4 + b); }
-__device__ __forceinline__ uint32_t s_free(const Ctx4 &c, int b) { return tail_b(c, 6 + b); }
-__device__ __forceinline__ uint32_t q_ready(const Ctx4 &c) { return tail_b(c, 8); }
-__device__ __forceinline__ uint32_t q_tile_free(const Ctx4 &c) { return tail_b(c, 9); }
-__device__ __forceinline__ uint32_t fin_b(const Ctx4 &c) { return tail_b(c, 10); }
-__device__ __forceinline__ uint32_t k_slot(const Ctx4 &c, int s) { return c.base + c.lay.kring + (uint32_t)s * kKSlotBytes; }
-__device__ __forceinline__ uint32_t v_slot(const Ctx4 &c, int s) { return c.base + c.lay.vring + (uint32_t)s * kVSlotBytes; }
-__device__ __forceinline__ uint32_t ring_par(int k, int n) { return (uint32_t)((k / n) & 1); }
+// Barriers.
+constexpr int kFullK = 0, kEmptyK = kFullK + kKS, kFullV = kEmptyK + kKS, kConvV = kFullV + kVS, kEmptyV = kConvV + kVS,
+              kScaleB = kEmptyV + kVS, kInfoB = kScaleB + kScaleRing, kPFull = kInfoB + kInfo, kPvDone = kPFull + 2,
+              kQFull = kPvDone + 2, kQEmpty = kQFull + 1, kSFull = kQEmpty + 1, kSFree = kSFull + 2, kQReady = kSFree + 2,
+              kQTileFree = kQReady + 1, kFin = kQTileFree + 1, kBars = kFin + 1;
+static_assert(kBars <= 48, "room for the barriers");
+__device__ __forceinline__ uint32_t bar_at(const Ctx4 &c, int i) { return c.bars + 8u * (uint32_t)i; }
 
+// A ring position that advances with the stages: its slot and the parity of
+// the slot's current use.
+template <int N>
+struct Ring {
+    int slot = 0;
+    uint32_t par = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++slot == N) {
+            slot = 0;
+            par ^= 1u;
+        }
+    }
+};
+
+// Stages of a segment.
 __device__ __forceinline__ int stages_of(const Segment &s, int P) { return ((s.p1 - s.p0) * P + kTT - 1) / kTT; }
 
-// The stage's scale bytes of token t: K's and V's ([page][K, V][P] as in the pool).
-__device__ __forceinline__ uint32_t scale_at(const Ctx4 &c, int k, int t, int log2P, int kv)
+// Offset of token t's K scale byte in a stage's ([page][K, V][P] as in the
+// pool); V's is P further on.
+__device__ __forceinline__ uint32_t scale_off(int t, int log2P)
 {
-    const uint32_t off = (uint32_t)(((t >> log2P) << (log2P + 1)) + (kv << log2P) + (t & ((1 << log2P) - 1)));
-    return reinterpret_cast<const volatile uint8_t *>(c.smem + c.lay.scales)[(k % kScaleRing) * 2 * kTT + off];
+    return (uint32_t)(((t >> log2P) << (log2P + 1)) + (t & ((1 << log2P) - 1)));
 }
 
 // Largest V scale byte of the stage's tokens below `n` on copied pages (NaN
-// rows, 255, aside), by a warp; 0 if there are none.
-__device__ __forceinline__ int stage_top_scale(const Ctx4 &c, int k, int n, uint32_t mask, int log2P)
+// rows, 255, aside), by a warp; 0 if there are none.  vs4 points at the V
+// scales of the lane's four tokens.
+__device__ __forceinline__ int stage_top_scale(const uint8_t *vs4, int n, uint32_t mask, int log2P)
 {
     const int t = 4 * (threadIdx.x & 31);
-    const uint32_t off = (uint32_t)(((t >> log2P) << (log2P + 1)) + (1 << log2P) + (t & ((1 << log2P) - 1)));
-    const uint32_t w = *reinterpret_cast<const volatile uint32_t *>(c.smem + c.lay.scales + (k % kScaleRing) * 2 * kTT + off);
+    const uint32_t w = *reinterpret_cast<const volatile uint32_t *>(vs4);
     const int in = ((mask >> (t >> log2P)) & 1u) ? n - t : 0;
     uint32_t top = 0;
 #pragma unroll
@@ -216,11 +233,16 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// Two e4m3 codes (low 16 bits) as fp16.
-__device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t codes)
+// Two e4m3 codes of w (the low or the high half) as fp16 pairs, times 2^-8:
+// each code's byte with its sign above it, moved so that the sign and the
+// exponent and mantissa bits come to lie in fp16's places.  Three full-rate
+// integer instructions; the conversion instruction measured slower here.
+template <bool kHigh>
+__device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t w)
 {
-    const __half2 h(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3));
-    return *reinterpret_cast<const uint32_t *>(&h);
+    uint32_t r;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(w), "n"(kHigh ? 0xB3A2 : 0x9180));
+    return (r << 7) & 0xBF80BF80u;
 }
 
 // ---------------------------------------------------------------------------
@@ -230,25 +252,27 @@ __device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t codes)
 // one page (a box of P rows x 128 bytes; at head_dim 64 the box's upper half
 // is outside the tensor and filled with zeros).  The K warp also copies each
 // page's 2P scale bytes and publishes the stage's validity word, on barriers
-// of a ring of their own: a stage's scales are read by the softmax and by the
-// V conversion, after its K slot may have been refilled.  The K warp writes
-// entry k once QK(k - KS) is complete; QK(i) is issued after the softmax has
-// read S and the scales of stage i - 2, and its P of stage i - 3 waits for
-// PV(i - 4), whose V was converted: entries up to k - KS - 4 are free.
-template <bool kIsK>
+// of a ring of their own, so that they wait for no V slot.  The K warp writes
+// entry k once QK(k - KS) is complete, and QK(i) waits for the factors that
+// the V conversion's warps take from the scales of stage i: entries up to
+// k - KS are free.
+template <int NR, bool kIsK>
 __device__ void producer_q8(const CUtensorMap *tm, const Q8DecodeParams &q, const Ctx4 &c)
 {
+    constexpr Smem L = smem_layout(NR);
+    constexpr int kSlots = kIsK ? kKS : kVS;
     const DecodeParams &p = q.d;
     const int lane = threadIdx.x & 31;
-    const int P = p.page_size, RB = kTT / P, log2P = 31 - __clz(P);
-    const int slots = kIsK ? c.ks : c.vs;
+    const int P = p.page_size, RB = kTT / P;
     const uint64_t pol = l2_evict_first_policy();
     if (lane == 0)
         prefetch_tensormap(tm);
     bool alive = true;
-    int kbase = 0, seg = 0, last_issued = -1, q_issued = -1;
+    int k = 0, seg = 0, q_issued = -1;
+    Ring<kSlots> ring;
     Segment s = locate(p, c.cta_begin, c.cta_end);
     int pre = unit_entry(p.block_table, p, s.b, s.p0 + lane, s.p1);
+#pragma unroll 1
     for (;;) {
         const bool has_next = s.seg_end < c.cta_end;
         Segment sn;
@@ -260,89 +284,92 @@ __device__ void producer_q8(const CUtensorMap *tm, const Q8DecodeParams &q, cons
         const int dev_len = kIsK && lane == 0 ? __ldg(p.seq_lens + s.b) : 0;
         if (kIsK) {
             if (alive) {
-                const bool ok = mbar_wait_bounded(qempty(c), (uint32_t)((seg & 1) ^ 1), c.abort_flag, p.err);
+                const bool ok = q8_wait<true>(bar_at(c, kQEmpty), (uint32_t)((seg & 1) ^ 1), c.abort_flag, p.err);
                 alive = __all_sync(0xffffffffu, ok);
             }
             if (alive) {
                 const int n = q.n_q[s.b];
                 const uint32_t bytes = (uint32_t)(p.group * q.head_dim * 2);
                 if (lane == 0)
-                    mbar_arrive_expect_tx(qfull(c), bytes * (uint32_t)n);
+                    mbar_arrive_expect_tx(bar_at(c, kQFull), bytes * (uint32_t)n);
                 __syncwarp();
                 const __nv_bfloat16 *src = p.q + (int64_t)q.q0[s.b] * q.q_stride + (int64_t)s.g * p.group * q.head_dim;
+#pragma unroll 1
                 for (int i = lane; i < n; i += 32)
-                    bulk_load(c.base + c.lay.qbuf + (uint32_t)i * bytes, src + (int64_t)i * q.q_stride, bytes, qfull(c));
+                    bulk_load(c.base + L.qbuf + (uint32_t)i * bytes, src + (int64_t)i * q.q_stride, bytes,
+                              bar_at(c, kQFull));
                 q_issued = seg;
             }
         }
-        const int nst = stages_of(s, P);
-        int w0 = s.p0;                                   // block-table window [w0, w0+32)
+        int left = s.p1 - s.p0;                          // pages still to copy
+        int w = 0;                                       // position in the window of 32 table entries
         int cur = pre;
-        int nxt = unit_entry(p.block_table, p, s.b, w0 + 32 + lane, s.p1);
-        for (int j = 0; j < nst; ++j) {
-            const int k = kbase + j, slot = k % slots;
-            const int page0 = s.p0 + j * RB;
-            if (page0 >= w0 + 32) {                      // a stage's pages never straddle a window
-                w0 += 32;
+        int next_j = s.p0 + 32 + lane;
+        int nxt = unit_entry(p.block_table, p, s.b, next_j, s.p1);
+#pragma unroll 1
+        for (; left > 0; left -= RB) {
+            if (w == 32) {                               // a stage's pages never straddle a window
+                w = 0;
                 cur = nxt;
-                nxt = unit_entry(p.block_table, p, s.b, w0 + 32 + lane, s.p1);
+                next_j += 32;
+                nxt = unit_entry(p.block_table, p, s.b, next_j, s.p1);
             }
-            const int id = __shfl_sync(0xffffffffu, cur, (page0 + lane - w0) & 31);
+            const int id = __shfl_sync(0xffffffffu, cur, (w + lane) & 31);
+            w += RB;
             bool ok = true;
             if (alive)
-                ok = mbar_wait_bounded(kIsK ? empty_k(c, slot) : empty_v(c, slot), ring_par(k, slots) ^ 1u,
-                                       c.abort_flag, p.err);
+                ok = q8_wait<true>(bar_at(c, (kIsK ? kEmptyK : kEmptyV) + ring.slot), ring.par ^ 1u, c.abort_flag, p.err);
             alive = alive && __all_sync(0xffffffffu, ok);
-            const bool inside = lane < RB && page0 + lane < s.p1;
-            const bool valid = inside && id >= 0 && id < p.num_pages;
+            const bool inside = lane < RB && lane < left;
+            const bool valid = inside && (uint32_t)id < (uint32_t)p.num_pages;
             const uint32_t mask = __ballot_sync(0xffffffffu, valid);
             if (kIsK && alive && inside && !valid)
                 atomicOr(p.err, SHKV_ERRF_PAGE_OOB);
-            const uint32_t bar = kIsK ? full_k(c, slot) : full_v(c, slot);
-            const uint32_t sbar = scale_b(c, k % kScaleRing);
+            const uint32_t bar = bar_at(c, (kIsK ? kFullK : kFullV) + ring.slot);
+            const uint32_t sbar = bar_at(c, kScaleB + k % kScaleRing);
             if (alive && lane == 0) {
-                const uint32_t pages = (uint32_t)__popc(mask);
+                const uint32_t rows = (uint32_t)(__popc(mask) * P);
                 if (kIsK) {
-                    reinterpret_cast<volatile uint32_t *>(c.smem + c.lay.meta)[k % kScaleRing] =
+                    reinterpret_cast<volatile uint32_t *>(c.smem + L.meta)[k % kScaleRing] =
                         mask | ((uint32_t)k << 8);       // valid pages + stage tag
-                    mbar_arrive_expect_tx(sbar, pages * 2u * (uint32_t)P);
+                    mbar_arrive_expect_tx(sbar, 2u * rows);
                 }
-                mbar_arrive_expect_tx(bar, pages * (uint32_t)P * 128u);
+                mbar_arrive_expect_tx(bar, 128u * rows);
             }
             __syncwarp();
             if (alive && valid) {
                 const int unit = id * p.hkv + s.g;
-                const uint32_t dst = (kIsK ? k_slot(c, slot) : v_slot(c, slot) + kTT * 128u) + (uint32_t)(lane * P) * 128u;
-                tma_load_2d(dst, tm, 0, unit * P, bar, pol);
+                const uint32_t dst = c.base + (kIsK ? (uint32_t)ring.slot * kKSlotBytes
+                                                    : L.vring + (uint32_t)ring.slot * kVSlotBytes + kTT * 128u);
+                tma_load_2d(dst + (uint32_t)(lane * P) * 128u, tm, 0, unit * P, bar, pol);
                 if (kIsK)
-                    bulk_load(c.base + c.lay.scales + (uint32_t)((k % kScaleRing) * 2 * kTT + lane * 2 * P),
+                    bulk_load(c.base + L.scales + (uint32_t)((k % kScaleRing) * 2 * kTT + lane * 2 * P),
                               q.scales + (int64_t)unit * 2 * P, 2u * (uint32_t)P, sbar);
             }
-            if (alive)
-                last_issued = k;
             __syncwarp();
+            if (alive) {
+                ++k;
+                ring.next();
+            }
         }
         if (kIsK && lane == 0 && dev_len != plan_len(p, s))
             atomicOr(p.err, SHKV_ERRF_SEQ_LEN);
-        kbase += nst;
         ++seg;
         if (!has_next)
             break;
         s = sn;
         pre = pre_next;
     }
-    // After an abort, wait (bounded) for the copies still in flight so no
-    // copy lands after the CTA exits.
+    // After an abort, wait (bounded) for the copies still in flight (stages up
+    // to k - 1) so no copy lands after the CTA exits.
     if (!alive && lane == 0) {
-        for (int k = last_issued - slots + 1; k <= last_issued; ++k)
-            if (k >= 0)
-                mbar_drain_bounded(kIsK ? full_k(c, k % slots) : full_v(c, k % slots), ring_par(k, slots));
+        for (int i = max(0, k - kSlots); i < k; ++i)
+            mbar_drain_bounded(bar_at(c, (kIsK ? kFullK : kFullV) + i % kSlots), (uint32_t)((i / kSlots) & 1));
         if (kIsK) {
-            for (int k = last_issued - kScaleRing + 1; k <= last_issued; ++k)
-                if (k >= 0)
-                    mbar_drain_bounded(scale_b(c, k % kScaleRing), ring_par(k, kScaleRing));
+            for (int i = max(0, k - kScaleRing); i < k; ++i)
+                mbar_drain_bounded(bar_at(c, kScaleB + i % kScaleRing), (uint32_t)((i / kScaleRing) & 1));
             if (q_issued >= 0)
-                mbar_drain_bounded(qfull(c), (uint32_t)(q_issued & 1));
+                mbar_drain_bounded(bar_at(c, kQFull), (uint32_t)(q_issued & 1));
         }
     }
 }
@@ -364,35 +391,74 @@ __device__ void warm_l2_q8(const CUtensorMap *tm, const DecodeParams &p, const C
 // ---------------------------------------------------------------------------
 // V conversion
 // ---------------------------------------------------------------------------
+template <int NR>
 __device__ void convert_v(const Q8DecodeParams &q, const Ctx4 &c)
 {
+    constexpr Smem L = smem_layout(NR);
     const DecodeParams &p = q.d;
     const int t = threadIdx.x - kConvWarp0 * 32, lane = t & 31;
     const int P = p.page_size, log2P = 31 - __clz(P);
+    volatile uint32_t *meta = reinterpret_cast<volatile uint32_t *>(c.smem + L.meta);
+    const uint8_t *sc_mine = c.smem + L.scales + scale_off(t, log2P);
+    const uint8_t *sc_four = c.smem + L.scales + scale_off(4 * lane, log2P) + P;
+    const int page = t >> log2P;
     bool alive = true;
-    int kbase = 0;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        bool ok = false;
+        if (alive)
+            ok = q8_wait<false>(bar, parity, c.abort_flag, p.err);
+        alive = __all_sync(0xffffffffu, ok);
+    };
+    uint32_t k = 0;
+    Ring<kScaleRing> sring;
+    Ring<kVS> vring;
     Segment s = locate(p, c.cta_begin, c.cta_end);
+#pragma unroll 1
     for (;;) {
-        const int nst = stages_of(s, P);
-        const int lim = min(plan_len(p, s), s.p1 * P);
+        const int tok_end = s.p1 * P;
+        const int lim = min(plan_len(p, s), tok_end);
         const int all_see = keys_all_see(q, s);
-        int e = kMinE;
-        for (int j = 0; j < nst; ++j) {
-            const int k = kbase + j, slot = k % c.vs;
-            bool ok = false;
+        int e = kMinE;                                   // scale byte of E
+#pragma unroll 1
+        for (int tok0 = s.p0 * P; tok0 < tok_end; tok0 += kTT, ++k) {
+            // --- the token's factors.  (Entry k % kInfo was last used by stage
+            // k - kVS - 1, whose PV was done before V(k - 1) was loaded.)
+            const uint32_t entry = k % kInfo;
+            wait(bar_at(c, kScaleB + sring.slot), sring.par);
+            const uint32_t tagged = alive ? meta[sring.slot] : 0u;
+            if (alive && (tagged >> 8) != (k & 0xffffffu)) {
+                if (lane == 0) {
+                    atomicOr(p.err, SHKV_ERRF_PIPELINE);
+                    *c.abort_flag = 1u;
+                }
+                alive = false;
+            }
+            const uint32_t mask = tagged & 0xffu;
+            const int so = sring.slot * 2 * kTT;
+            const int kb = *(const volatile uint8_t *)(sc_mine + so), vb = *(const volatile uint8_t *)(sc_mine + so + P);
+            e = next_e(e, stage_top_scale(sc_four + so, min(lim, all_see) - tok0, mask, log2P));
+            const bool valid = alive && tok0 + t < lim && ((mask >> page) & 1u);
+            // a NaN row of V counts as zero and makes its key's scores NaN
+            // instead, so that only rows that attend it see it
+            const bool live = valid && vb != 255 && vb >= e - kVWindow;
+            const int ve = !valid || vb == 255 ? e : max(vb, e - kVWindow);
+            // rows from row_min on see the token (new token i from position L - n + i on)
+            const int row_min = valid ? min(64, max(0, (tok0 + t - all_see + 1) * p.group)) : 64;
+            const uint32_t masked = __any_sync(0xffffffffu, row_min > 0);
+            float4 f;
+            f.x = !valid ? 0.f : vb == 255 ? __uint_as_float(0x7fc00000u) : q8_scale((uint32_t)kb) * p.scale_log2;
+            f.y = (float)(ve - 127);
+            f.z = __uint_as_float((uint32_t)max(127 + e - ve, 1) << 23);
+            f.w = __int_as_float(row_min | (int)(masked << 8) | (e << 16));
             if (alive)
-                ok = mbar_wait_bounded(full_v(c, slot), ring_par(k, c.vs), c.abort_flag, p.err) &&
-                     mbar_wait_bounded(scale_b(c, k % kScaleRing), ring_par(k, kScaleRing), c.abort_flag, p.err);
-            alive = __all_sync(0xffffffffu, ok);
+                reinterpret_cast<float4 *>(c.smem + L.info)[entry * kTT + t] = f;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar_at(c, kInfoB + (int)entry));
+            // --- V
+            wait(bar_at(c, kFullV + vring.slot), vring.par);
             if (alive) {
-                const uint32_t mask = reinterpret_cast<volatile uint32_t *>(c.smem + c.lay.meta)[k % kScaleRing] & 0xffu;
-                const int tok0 = s.p0 * P + j * kTT, n = lim - tok0;   // tokens of the stage that count
-                e = next_e(e, stage_top_scale(c, k, min(n, all_see - tok0), mask, log2P));
-                const int vb = (int)scale_at(c, k, t, log2P, 1);
-                // a row that does not count, and a NaN row (its key's score is
-                // made NaN instead, so that only rows that attend it see it), is zero
-                const bool live = t < n && ((mask >> (t >> log2P)) & 1u) && vb != 255 && vb >= e - kVWindow;
-                uint8_t *row = c.smem + c.lay.vring + (uint32_t)slot * kVSlotBytes + (uint32_t)t * 128u;
+                uint8_t *row = c.smem + L.vring + (uint32_t)vring.slot * kVSlotBytes + (uint32_t)t * 128u;
                 uint4 raw[8];
 #pragma unroll
                 for (int ch = 0; ch < 8; ++ch)
@@ -400,23 +466,23 @@ __device__ void convert_v(const Q8DecodeParams &q, const Ctx4 &c)
                                    : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                 for (int ch = 0; ch < 8; ++ch) {
-                    const uint32_t w[4] = {raw[ch].x, raw[ch].y, raw[ch].z, raw[ch].w};
-                    uint32_t o[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        o[i] = widen_e4m3x2(w[i >> 1] >> (16 * (i & 1)));
                     uint8_t *dst = row + (ch >> 2) * (kTT * 128);
                     const int c0 = (2 * ch) & 7;
-                    *reinterpret_cast<uint4 *>(dst + ((c0 ^ (t & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4 *>(dst + (((c0 + 1) ^ (t & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    *reinterpret_cast<uint4 *>(dst + ((c0 ^ (t & 7)) << 4)) =
+                        make_uint4(widen_e4m3x2<false>(raw[ch].x), widen_e4m3x2<true>(raw[ch].x),
+                                   widen_e4m3x2<false>(raw[ch].y), widen_e4m3x2<true>(raw[ch].y));
+                    *reinterpret_cast<uint4 *>(dst + (((c0 + 1) ^ (t & 7)) << 4)) =
+                        make_uint4(widen_e4m3x2<false>(raw[ch].z), widen_e4m3x2<true>(raw[ch].z),
+                                   widen_e4m3x2<false>(raw[ch].w), widen_e4m3x2<true>(raw[ch].w));
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(conv_v(c, slot));
+                mbar_arrive(bar_at(c, kConvV + vring.slot));
+            sring.next();
+            vring.next();
         }
-        kbase += nst;
         if (s.seg_end >= c.cta_end)
             break;
         s = next_segment(p, s, c.cta_end);
@@ -429,88 +495,100 @@ __device__ void convert_v(const Q8DecodeParams &q, const Ctx4 &c)
 template <int NR>
 __device__ void qk_issuer(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem)
 {
-    const DecodeParams &p = q.d;
+    constexpr Smem L = smem_layout(NR);
     constexpr uint32_t idesc = idesc_of(128, NR, false, false);
+    const DecodeParams &p = q.d;
     const int steps = q.head_dim / 32;                   // 32 codes an MMA
-    const uint64_t kd0 = umma_sdesc_sw128(k_slot(c, 0), 16u, 1024u);
-    const uint64_t qh0 = umma_sdesc_sw128(c.base + c.lay.qtile, 16u, 1024u);
-    const uint64_t ql0 = umma_sdesc_sw128(c.base + c.lay.qtile + c.lay.qhalf, 16u, 1024u);
+    const uint64_t kd0 = umma_sdesc_sw128(c.base, 16u, 1024u);
+    const uint64_t qh0 = umma_sdesc_sw128(c.base + L.qtile, 16u, 1024u);
+    const uint64_t ql0 = umma_sdesc_sw128(c.base + L.qtile + L.qhalf, 16u, 1024u);
     bool alive = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (alive)
-            alive = mbar_wait_bounded(bar, parity, c.abort_flag, p.err);
+            alive = q8_wait<true>(bar, parity, c.abort_flag, p.err);
     };
-    int kbase = 0, seg = 0;
+    int seg = 0;
+    uint32_t k = 0;
+    Ring<kKS> ring;
     Segment s = locate(p, c.cta_begin, c.cta_end);
+#pragma unroll 1
     for (;;) {
-        const int nst = stages_of(s, p.page_size);
-        wait(q_ready(c), (uint32_t)(seg & 1));
-        for (int j = 0; j < nst; ++j) {
-            const int k = kbase + j, buf = k & 1, slot = k % c.ks;
-            const uint64_t kd = kd0 + (((uint32_t)slot * kKSlotBytes) >> 4);
-            wait(full_k(c, slot), ring_par(k, c.ks));
-            wait(s_free(c, buf), (uint32_t)(((k >> 1) & 1) ^ 1));
+        wait(bar_at(c, kQReady), (uint32_t)(seg & 1));
+#pragma unroll 1
+        for (int left = stages_of(s, p.page_size); left > 0; --left, ++k) {
+            const uint32_t buf = k & 1u;
+            const uint64_t kd = kd0 + (uint64_t)(((uint32_t)ring.slot * kKSlotBytes) >> 4);
+            wait(bar_at(c, kFullK + ring.slot), ring.par);
+            wait(bar_at(c, kInfoB + (int)(k % kInfo)), (k / kInfo) & 1u);
+            wait(bar_at(c, kSFree + (int)buf), ((k >> 1) & 1u) ^ 1u);
+            mbar_arrive(bar_at(c, kSFull + (int)buf));   // passes the factors on to the softmax
             if (alive) {
                 tc_fence_after();
-                const uint32_t d = tmem + kColS + (uint32_t)(buf * 64);
+                const uint32_t d = tmem + kColS + buf * 64u;
+#pragma unroll 1
                 for (int i = 0; i < steps; ++i) {
                     umma_f8(d, kd + (uint64_t)(2 * i), qh0 + (uint64_t)(2 * i), idesc, i ? 1u : 0u);
                     umma_f8(d, kd + (uint64_t)(2 * i), ql0 + (uint64_t)(2 * i), idesc, 1u);
                 }
             }
-            umma_commit(s_full(c, buf));
-            umma_commit(empty_k(c, slot));
-            if (j == nst - 1)
-                umma_commit(q_tile_free(c));
+            umma_commit(bar_at(c, kSFull + (int)buf));
+            umma_commit(bar_at(c, kEmptyK + ring.slot));
+            ring.next();
         }
-        kbase += nst;
+        umma_commit(bar_at(c, kQTileFree));
         ++seg;
         if (s.seg_end >= c.cta_end)
             break;
         s = next_segment(p, s, c.cta_end);
     }
-    umma_commit(fin_b(c));
-    mbar_drain_bounded(fin_b(c), 0u);
+    umma_commit(bar_at(c, kFin));
+    mbar_drain_bounded(bar_at(c, kFin), 0u);
 }
 
 template <int NR>
 __device__ void pv_issuer(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem)
 {
-    const DecodeParams &p = q.d;
+    constexpr Smem L = smem_layout(NR);
     constexpr uint32_t idesc = idesc_of(128, q_npv(NR), true, true);
-    const uint64_t vd0 = umma_sdesc_sw128(v_slot(c, 0), (uint32_t)(kTT * 128), 1024u);
-    const uint64_t pd0 = umma_sdesc_sw128(c.base + c.lay.pbuf, (uint32_t)(kTT * 128), 1024u);
+    constexpr bool kPing = q_pingpong(NR);
+    const DecodeParams &p = q.d;
+    const uint64_t vd0 = umma_sdesc_sw128(c.base + L.vring, (uint32_t)(kTT * 128), 1024u);
+    const uint64_t pd0 = umma_sdesc_sw128(c.base + L.pbuf, (uint32_t)(kTT * 128), 1024u);
     bool alive = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (alive)
-            alive = mbar_wait_bounded(bar, parity, c.abort_flag, p.err);
+            alive = q8_wait<true>(bar, parity, c.abort_flag, p.err);
     };
-    int kbase = 0;
+    uint32_t k = 0;
+    Ring<kVS> ring;
     Segment s = locate(p, c.cta_begin, c.cta_end);
+#pragma unroll 1
     for (;;) {
         const int nst = stages_of(s, p.page_size);
-        for (int j = 0; j < nst; ++j) {
-            const int k = kbase + j, slot = k % c.vs;
-            const uint64_t vd = vd0 + (((uint32_t)slot * kVSlotBytes) >> 4);
-            wait(conv_v(c, slot), ring_par(k, c.vs));
-            wait(p_full(c), (uint32_t)(k & 1));
+#pragma unroll 1
+        for (int j = 0; j < nst; ++j, ++k) {
+            const uint64_t vd = vd0 + (uint64_t)(((uint32_t)ring.slot * kVSlotBytes) >> 4);
+            const uint32_t g = kPing ? k & 1u : 0u;      // softmax group, its P and O
+            const uint64_t pd = pd0 + (uint64_t)(g * (kPBytes >> 4));
+            wait(bar_at(c, kConvV + ring.slot), ring.par);
+            wait(bar_at(c, kPFull + (int)g), (kPing ? k >> 1 : k) & 1u);
             if (alive) {
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < kTT / 16; ++ks)
-                    umma_bf16(tmem + kColO, vd + (uint64_t)(ks * 128), pd0 + (uint64_t)(ks * 128), idesc,
-                              (j == 0 && ks == 0) ? 0u : 1u);
+                    umma_bf16(tmem + kColO + g * 64u, vd + (uint64_t)(ks * 128), pd + (uint64_t)(ks * 128), idesc,
+                              (j < (kPing ? 2 : 1) && ks == 0) ? 0u : 1u);
             }
-            umma_commit(pv_done(c));
-            umma_commit(empty_v(c, slot));
+            umma_commit(bar_at(c, kPvDone + (int)g));
+            umma_commit(bar_at(c, kEmptyV + ring.slot));
+            ring.next();
         }
-        kbase += nst;
         if (s.seg_end >= c.cta_end)
             break;
         s = next_segment(p, s, c.cta_end);
     }
-    umma_commit(fin_b(c));
-    mbar_drain_bounded(fin_b(c), 0u);
+    umma_commit(bar_at(c, kFin));
+    mbar_drain_bounded(bar_at(c, kFin), 0u);
 }
 
 // ---------------------------------------------------------------------------
@@ -519,38 +597,49 @@ __device__ void pv_issuer(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem)
 template <int NR>
 __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem)
 {
-    constexpr int NH = NR / 2;                 // rows per thread
+    constexpr bool kPing = q_pingpong(NR);
+    constexpr int NH = kPing ? NR : NR / 2;    // rows per thread of a stage
+    constexpr int NE = NR / 2;                 // rows per thread at the segment's end
+    constexpr Smem L = smem_layout(NR);
     const DecodeParams &p = q.d;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tg = warp & (kTokenGroups - 1), hh = warp / kTokenGroups;
+    const int grp = kPing ? hh : 0;            // whose maxima, sums, P and O
     const int t = tg * 32 + lane;
-    const int P = p.page_size, log2P = 31 - __clz(P);
+    const int P = p.page_size;
     const int D = q.head_dim;
     const uint32_t lane_base = (uint32_t)(tg * 32) << 16;
-    const volatile uint32_t *meta = reinterpret_cast<const volatile uint32_t *>(c.smem + c.lay.meta);
-    float *scr = reinterpret_cast<float *>(c.smem + c.lay.scr);
-    int *scr_i = reinterpret_cast<int *>(scr);
+    const uint32_t bar_id = 1u + (uint32_t)grp, bar_threads = kPing ? 128u : 256u;
+    constexpr uint32_t kAllBar = 3;            // both groups
+    float *scr = reinterpret_cast<float *>(c.smem + L.scr);
+    const int *scr_i = reinterpret_cast<const int *>(scr);
+    float *mine = scr + grp * kScrGroup * 64;
     bool alive = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
         bool ok = false;
         if (alive)
-            ok = mbar_wait_bounded(bar, parity, c.abort_flag, p.err);
+            ok = q8_wait<false>(bar, parity, c.abort_flag, p.err);
         alive = __all_sync(0xffffffffu, ok) && alive;
         return alive;
     };
+    // element i of a thread's rows of a stage is stacked row row_of(i): all of
+    // them, or its half's 8-row chunks; every TMEM access is 8 columns
+    auto row_of = [&](int i) { return kPing ? i : half_row(hh, i); };
+    auto chunk_col = [&](int ch) { return kPing ? 8 * ch : 16 * ch + 8 * hh; };
 
     // Query rows of segment `sg`: bf16 staging buffer -> the two swizzled
     // e4m3 tiles and the rows' scales; D/8 lanes a row.  Rows past the unit's
     // are zero.
     auto stage_q = [&](int sg, const Segment &u) {
-        wait(qfull(c), (uint32_t)(sg & 1));
+        wait(bar_at(c, kQFull), (uint32_t)(sg & 1));
         const int LR = D / 8, log2LR = 31 - __clz(LR);
         const int rows = q.n_q[u.b] * p.group;
         const int l = threadIdx.x & (LR - 1);
+#pragma unroll 1
         for (int r = threadIdx.x >> log2LR; r < NR; r += kSoftmaxThreads >> log2LR) {
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
             if (alive && r < rows)
-                v = *reinterpret_cast<const uint4 *>(c.smem + c.lay.qbuf + r * D * 2 + l * 16);
+                v = *reinterpret_cast<const uint4 *>(c.smem + L.qbuf + r * D * 2 + l * 16);
             const uint32_t xs[4] = {v.x, v.y, v.z, v.w};
             uint32_t a = 0;
 #pragma unroll
@@ -578,9 +667,9 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
             if (bad)
                 hi[0] = hi[1] = lo[0] = lo[1] = 0x7f7f7f7fu;
             if (alive) {
-                uint8_t *dst = c.smem + c.lay.qtile + (uint32_t)r * 128u + (((l >> 1) ^ (r & 7)) << 4) + (l & 1) * 8;
+                uint8_t *dst = c.smem + L.qtile + (uint32_t)r * 128u + (((l >> 1) ^ (r & 7)) << 4) + (l & 1) * 8;
                 *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0], hi[1]);
-                *reinterpret_cast<uint2 *>(dst + c.lay.qhalf) = make_uint2(lo[0], lo[1]);
+                *reinterpret_cast<uint2 *>(dst + L.qhalf) = make_uint2(lo[0], lo[1]);
                 if (l == 0)
                     scr[kScrQ * 64 + r] = bad ? 1.f : q8_scale((uint32_t)byte);
             }
@@ -588,19 +677,18 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-            mbar_arrive(qempty(c));
-            mbar_arrive(q_ready(c));
+            mbar_arrive(bar_at(c, kQEmpty));
+            mbar_arrive(bar_at(c, kQReady));
         }
     };
 
     int kbase = 0, seg = 0;
     Segment s = locate(p, c.cta_begin, c.cta_end);
     stage_q(0, s);
+#pragma unroll 1
     for (;;) {
         const int nst = stages_of(s, P);
         const int R = q.n_q[s.b] * p.group;
-        const int lim = min(plan_len(p, s), s.p1 * P);
-        const int all_see = keys_all_see(q, s);
         int e = kMinE;                          // scale byte of E
         float2 nmu[NH / 2], l[NH / 2];          // 7 - m (1e30: no key yet), and this token's share of l
 #pragma unroll
@@ -608,44 +696,40 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
             nmu[i] = make_float2(1e30f, 1e30f);
             l[i] = make_float2(0.f, 0.f);
         }
-        named_barrier(1, kSoftmaxThreads);      // the rows' scales are in place
-
-        for (int j = 0; j < nst; ++j) {
-            const int k = kbase + j, buf = k & 1;
-            // --- the token's scales, which come with K
-            wait(scale_b(c, k % kScaleRing), ring_par(k, kScaleRing));
-            const uint32_t tagged = alive ? meta[k % kScaleRing] : 0u;
-            if (alive && (tagged >> 8) != ((uint32_t)k & 0xffffffu)) {
-                if (lane == 0) {
-                    atomicOr(p.err, SHKV_ERRF_PIPELINE);
-                    *c.abort_flag = 1u;
-                }
-                alive = false;
+        if (threadIdx.x < NR)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                scr[(g * kScrGroup + kScrM) * 64 + threadIdx.x] = -INFINITY;
+                scr[(g * kScrGroup + kScrB) * 64 + threadIdx.x] = kTermLog2;
             }
-            const int tok0 = s.p0 * P + j * kTT;
-            const int de = next_e(e, stage_top_scale(c, k, min(lim, all_see) - tok0, tagged & 0xffu, log2P)) - e;
-            e += de;
-            const bool valid = alive && (((tagged & 0xffu) >> (t >> log2P)) & 1u) && tok0 + t < lim;
-            // the token's factor of the scores (NaN where its K or V row is),
-            // its V exponent, and the factor that takes it out of l again
-            const int vb = (int)scale_at(c, k, t, log2P, 1);
-            const float ts = vb == 255 ? __uint_as_float(0x7fc00000u)
-                                       : q8_scale(scale_at(c, k, t, log2P, 0)) * p.scale_log2;
-            const int ve = !valid || vb == 255 ? e : max(vb, e - kVWindow);
-            const float ev = (float)(ve - 127);
-            const float undo = __uint_as_float((uint32_t)max(127 + e - ve, 1) << 23);
-            // rows from this one on see the token (new token i from position L - n + i on)
-            const int row_min = valid ? max(0, (tok0 + t - all_see + 1) * p.group) : 64;
-            const bool masked = __any_sync(0xffffffffu, row_min > 0);
+        named_barrier(kAllBar, kSoftmaxThreads);   // the rows' scales and initial maxima are in place
+
+        // this group's first stage of the segment
+        const int j0 = kPing ? (kbase ^ grp) & 1 : 0;
+#pragma unroll 1
+        for (int j = j0; j < nst; j += kPing ? 2 : 1) {
+            const int k = kbase + j, buf = k & 1;
+            // S^T and the token's factors
+            if (wait(bar_at(c, kSFull + buf), (uint32_t)((k >> 1) & 1)))
+                tc_fence_after();
+            const float4 f = reinterpret_cast<const float4 *>(c.smem + L.info)[(k % kInfo) * kTT + t];
+            const int w4 = alive ? __float_as_int(f.w) : 64 | 1 << 8 | e << 16;
+            const int row_min = w4 & 0xff;
+            const bool masked = (w4 & 0x100) != 0;       // for some token of the warp
+            const int de = (w4 >> 16) - e;
+            e = w4 >> 16;
             // y - m + 7 of this thread's rows (nm = 7 - m), -inf where not seen
             float2 d[NH / 2];
             auto scores = [&](const float2 (&nm)[NH / 2]) {
                 uint32_t sv[NH];
-                tmem_ld_half<NH>(tmem + lane_base + kColS + (uint32_t)(buf * 64), hh, sv);
-                const float2 ts2 = make_float2(ts, ts), ev2 = make_float2(ev, ev);
+#pragma unroll
+                for (int ch = 0; ch < NH / 8; ++ch)
+                    tmem_ld8_nowait(tmem + lane_base + kColS + (uint32_t)(buf * 64 + chunk_col(ch)), sv + 8 * ch);
+                tmem_wait_ld();
+                const float2 ts2 = make_float2(f.x, f.x), ev2 = make_float2(f.y, f.y);
 #pragma unroll
                 for (int ch = 0; ch < NH / 8; ++ch) {
-                    const float4 *rq = reinterpret_cast<const float4 *>(scr + kScrQ * 64 + 16 * ch + 8 * hh);
+                    const float4 *rq = reinterpret_cast<const float4 *>(scr + kScrQ * 64 + chunk_col(ch));
                     const float4 qa = rq[0], qb = rq[1];
                     const float2 q2[4] = {make_float2(qa.x, qa.y), make_float2(qa.z, qa.w), make_float2(qb.x, qb.y),
                                           make_float2(qb.z, qb.w)};
@@ -654,24 +738,22 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                         const int o = 4 * ch + i;
                         const float2 s2 = make_float2(__uint_as_float(sv[2 * o]), __uint_as_float(sv[2 * o + 1]));
                         d[o] = __ffma2_rn(s2, __fmul2_rn(ts2, q2[i]), __fadd2_rn(ev2, nm[o]));
-                        if (masked) {
-                            if (half_row(hh, 2 * o) < row_min)
-                                d[o].x = -INFINITY;
-                            if (half_row(hh, 2 * o + 1) < row_min)
-                                d[o].y = -INFINITY;
-                        }
                     }
                 }
+                if (masked)
+#pragma unroll
+                    for (int o = 0; o < NH / 2; ++o) {
+                        d[o].x = row_of(2 * o) < row_min ? -INFINITY : d[o].x;
+                        d[o].y = row_of(2 * o + 1) < row_min ? -INFINITY : d[o].y;
+                    }
             };
-            if (wait(s_full(c, buf), (uint32_t)((k >> 1) & 1)))
-                tc_fence_after();
             scores(nmu);
             float top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < NH / 2; ++i)
                 top = fmaxf(top, fmaxf(d[i].x, d[i].y));
-            // --- lazy refresh of the maxima: all warps agree
-            if (bar_red_or(1, kSoftmaxThreads, top > kPLog2 + kRescaleLog2 || de > 0)) {
+            // --- lazy refresh of the maxima: all warps of the stage agree
+            if (bar_red_or(bar_id, bar_threads, top > kPLog2 + kRescaleLog2 || de > 0)) {
                 const float2 none[NH / 2] = {};
                 scores(none);                   // y
                 {
@@ -686,75 +768,80 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
 #pragma unroll
                         for (int jj = 0; jj < (M >= 32 ? M / 32 : 1); ++jj)
                             if (base + jj < NH)
-                                scr[(kScrMax + tg) * 64 + half_row(hh, base + jj)] = v[jj];
+                                mine[(kScrMax + tg) * 64 + row_of(base + jj)] = v[jj];
                 }
-                named_barrier(1, kSoftmaxThreads);
-                if (threadIdx.x < NR) {
-                    const int r = threadIdx.x;
-                    const float mo = scr[kScrM * 64 + r];
+                named_barrier(bar_id, bar_threads);
+                const int r = kPing ? t : (int)threadIdx.x;
+                if (r < NR) {
+                    const float mo = mine[kScrM * 64 + r];
                     float mn = mo;
 #pragma unroll
                     for (int g = 0; g < kTokenGroups; ++g)
-                        mn = fmaxf(mn, scr[(kScrMax + g) * 64 + r]);
+                        mn = fmaxf(mn, mine[(kScrMax + g) * 64 + r]);
                     if (mo != -INFINITY) {
-                        const float b = scr[kScrB * 64 + r] + (float)de;
+                        const float b = mine[kScrB * 64 + r] + (float)de;
                         mn = fmaxf(mn, mo + (b - kMaxTermLog2));
-                        scr[kScrB * 64 + r] = fmaxf(b - (mn - mo), kTermLog2);
+                        mine[kScrB * 64 + r] = fmaxf(b - (mn - mo), kTermLog2);
                     }
-                    scr[kScrNew * 64 + r] = mn == -INFINITY ? 1e30f : kPLog2 - mn;
-                    scr[kScrAlpha * 64 + r] = mn == -INFINITY ? 1.f : ex2_approx(mo - mn);
-                    scr[kScrAlphaL * 64 + r] = mn == -INFINITY ? 1.f : ex2_approx(mo - mn + (float)de);
-                    scr[kScrM * 64 + r] = mn;
+                    mine[kScrNew * 64 + r] = mn == -INFINITY ? 1e30f : kPLog2 - mn;
+                    mine[kScrAlpha * 64 + r] = mn == -INFINITY ? 1.f : ex2_approx(mo - mn);
+                    mine[kScrAlphaL * 64 + r] = mn == -INFINITY ? 1.f : ex2_approx(mo - mn + (float)de);
+                    mine[kScrM * 64 + r] = mn;
                 }
-                named_barrier(1, kSoftmaxThreads);
-                const float *alpha = scr + kScrAlpha * 64;
-                if (j >= 1) {
-                    // O^T holds stages up to k-1: rescale this thread's part once PV(k-1) is done
-                    wait(pv_done(c), (uint32_t)((k - 1) & 1));
+                named_barrier(bar_id, bar_threads);
+                if (j > j0) {
+                    // O^T holds the group's stages before: rescale this thread's part once their PV is done
+                    wait(bar_at(c, kPvDone + grp), (uint32_t)(((kPing ? k >> 1 : k) - 1) & 1));
                     if (alive) {
                         tc_fence_after();
-                        uint32_t ov[NH];
-                        tmem_ld_half<NH>(tmem + lane_base + kColO, hh, ov);
 #pragma unroll
-                        for (int i = 0; i < NH; ++i)
-                            ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha[half_row(hh, i)]);
-                        tmem_st_half<NH>(tmem + lane_base + kColO, hh, ov);
+                        for (int ch = 0; ch < NH / 8; ++ch) {
+                            const uint32_t col = tmem + lane_base + kColO + (uint32_t)(grp * 64 + chunk_col(ch));
+                            uint32_t ov[8];
+                            tmem_ld8_nowait(col, ov);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                ov[i] = __float_as_uint(__uint_as_float(ov[i]) * mine[kScrAlpha * 64 + chunk_col(ch) + i]);
+                            tmem_st8_nowait(col, ov);
+                        }
+                        tmem_wait_st();
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < NH / 2; ++i) {
-                    const int r = half_row(hh, 2 * i);
-                    nmu[i] = make_float2(scr[kScrNew * 64 + r], scr[kScrNew * 64 + r + 1]);
+                    const int rr = row_of(2 * i);
+                    nmu[i] = make_float2(mine[kScrNew * 64 + rr], mine[kScrNew * 64 + rr + 1]);
                     d[i] = __fadd2_rn(d[i], nmu[i]);
-                    l[i] = __fmul2_rn(l[i], make_float2(scr[kScrAlphaL * 64 + r], scr[kScrAlphaL * 64 + r + 1]));
+                    l[i] = __fmul2_rn(l[i], make_float2(mine[kScrAlphaL * 64 + rr], mine[kScrAlphaL * 64 + rr + 1]));
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(s_free(c, buf));
+                mbar_arrive(bar_at(c, kSFree + buf));
             uint32_t pk[NH / 2];
 #pragma unroll
             for (int i = 0; i < NH / 2; ++i) {
                 const float2 pe = make_float2(ex2_approx(d[i].x), ex2_approx(d[i].y));
-                l[i] = __ffma2_rn(pe, make_float2(undo, undo), l[i]);
+                l[i] = __ffma2_rn(pe, make_float2(f.z, f.z), l[i]);
                 pk[i] = pack_half2(pe.x, pe.y);
             }
-            // --- P^T, once the previous stage's product has read the buffer
-            if (k > 0)
-                wait(pv_done(c), (uint32_t)((k - 1) & 1));
+            // --- P^T, once the group's previous product has read the buffer
+            if (k >= (kPing ? 2 : 1))
+                wait(bar_at(c, kPvDone + grp), (uint32_t)(((kPing ? k >> 1 : k) - 1) & 1));
             if (alive) {
-                uint8_t *prow = c.smem + c.lay.pbuf + (uint32_t)t * 128u;
+                uint8_t *prow = c.smem + L.pbuf + (uint32_t)grp * kPBytes + (uint32_t)t * 128u;
 #pragma unroll
                 for (int ch = 0; ch < NH / 8; ++ch)
-                    *reinterpret_cast<uint4 *>(prow + (((2 * ch + hh) ^ (t & 7)) << 4)) =
+                    *reinterpret_cast<uint4 *>(prow + (((chunk_col(ch) / 8) ^ (t & 7)) << 4)) =
                         make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
             }
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(p_full(c));
+                mbar_arrive(bar_at(c, kPFull + grp));
         }
 
         // --- next segment's query rows, as soon as the last QK of this one is done
@@ -762,12 +849,12 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
         Segment sn;
         if (has_next) {
             sn = next_segment(p, s, c.cta_end);
-            wait(q_tile_free(c), (uint32_t)(seg & 1));
-            named_barrier(1, kSoftmaxThreads);  // every warp is past its last use of the rows' scales
+            wait(bar_at(c, kQTileFree), (uint32_t)(seg & 1));
+            named_barrier(kAllBar, kSoftmaxThreads);  // every warp is past its last use of the rows' scales
             stage_q(seg + 1, sn);
         }
 
-        // --- segment end: row sums across the 128 tokens, log-sum-exp
+        // --- segment end: row sums across the 128 tokens
         {
             constexpr int M = pow2_at_least(NH);
             float v[M];
@@ -780,25 +867,51 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
 #pragma unroll
                 for (int jj = 0; jj < (M >= 32 ? M / 32 : 1); ++jj)
                     if (base + jj < NH)
-                        scr[(kScrL + tg) * 64 + half_row(hh, base + jj)] = v[jj];
+                        mine[(kScrMax + tg) * 64 + row_of(base + jj)] = v[jj];
         }
-        named_barrier(1, kSoftmaxThreads);
+        if (t == 0)
+            *reinterpret_cast<int *>(mine + kScrNew * 64) = e;       // the group's E (kScrNew is free)
+        named_barrier(kAllBar, kSoftmaxThreads);
         const bool whole = (s.seg_begin == s.unit_begin) && (s.seg_end == s.unit_end);
         const int slot_id = whole ? 0 : 2 * (int)blockIdx.x + (s.seg_begin == c.cta_begin ? 0 : 1);
         const int64_t row0 = (int64_t)q.q0[s.b] * p.hq + (int64_t)s.g * p.group;
         const int *rowoff = scr_i + kScrOff * 64;
         if (threadIdx.x < NR) {
             const int r = threadIdx.x;
-            float a = 0.f;
+            // the groups' parts, relative to the larger maximum and E
+            float m[2], a[2], w[2];
+            int eg[2];
 #pragma unroll
-            for (int g = 0; g < kTokenGroups; ++g)
-                a += scr[(kScrL + g) * 64 + r];
-            scr[kScrInv * 64 + r] = a != 0.f ? __frcp_rn(a) : 0.f;    // (a NaN sum stays NaN)
-            const float m = scr[kScrM * 64 + r];
-            scr[kScrM * 64 + r] = -INFINITY;        // the next segment starts afresh
-            scr[kScrB * 64 + r] = kTermLog2;
+            for (int g = 0; g < 2; ++g) {
+                const float *o = scr + g * kScrGroup * 64;
+                m[g] = kPing || g == 0 ? o[kScrM * 64 + r] : -INFINITY;
+                eg[g] = kPing || g == 0 ? reinterpret_cast<const int *>(o)[kScrNew * 64] : 0;
+                a[g] = 0.f;
+                if (kPing || g == 0)
+#pragma unroll
+                    for (int i = 0; i < kTokenGroups; ++i)
+                        a[g] += o[(kScrMax + i) * 64 + r];
+            }
+            const int ee = max(eg[0], eg[1]);
+            float mm = fmaxf(m[0], m[1]);
+#pragma unroll
+            for (int g = 0; g < 2; ++g)              // (and high enough for l's terms under the larger E)
+                mm = fmaxf(mm, m[g] + (float)(ee - eg[g] - 20));
+            float sum = 0.f;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                // (a sum of NaN keeps its weight: its m may be -inf)
+                w[g] = m[g] == -INFINITY ? (a[g] != 0.f ? 1.f : 0.f) : ex2_approx(m[g] - mm);
+                sum += m[g] == -INFINITY ? a[g] : a[g] * ex2_approx(m[g] - mm + (float)(ee - eg[g]));
+            }
+            const float inv = sum != 0.f ? __frcp_rn(sum) : 0.f;     // (a NaN sum stays NaN)
+            const float ef = q8_scale((uint32_t)ee);
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+                scr[(kScrEnd + g) * 64 + r] = w[g] * inv * ef;
             if (alive && r < R) {
-                const float lse = a != 0.f ? ((m == -INFINITY ? 0.f : m - kPLog2) - (float)(e - 127) + log2f(a)) * kLn2 : -INFINITY;
+                const float lse = sum != 0.f ? ((mm == -INFINITY ? 0.f : mm - kPLog2) - (float)(ee - 127) + log2f(sum)) * kLn2
+                                             : -INFINITY;
                 if (whole) {
                     if (p.lse_out)
                         p.lse_out[row0 + rowoff[r]] = lse;
@@ -807,31 +920,43 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                 }
             }
         }
-        named_barrier(1, kSoftmaxThreads);
+        named_barrier(kAllBar, kSoftmaxThreads);
 
-        // --- column d = t of O^T for this thread's rows, normalised
-        wait(pv_done(c), (uint32_t)((kbase + nst - 1) & 1));
-        if (alive) {
-            tc_fence_after();
-            const float ef = q8_scale((uint32_t)e);
-            uint32_t ov[NH];
-            tmem_ld_half<NH>(tmem + lane_base + kColO, hh, ov);
-            if (t < D) {
+        // --- column d = t of O^T for half the rows, normalised
+        float o[NE];
 #pragma unroll
-                for (int i = 0; i < NH; ++i) {
-                    const int r = half_row(hh, i);
-                    if (r < R) {
-                        const float o = __uint_as_float(ov[i]) * scr[kScrInv * 64 + r] * ef;
-                        if (!whole)
-                            p.ws_part[((int64_t)slot_id * p.rows + r) * D + t] = o;
-                        else
-                            p.out[(row0 + rowoff[r]) * D + t] = __float2bfloat16_rn(o);
-                    }
+        for (int i = 0; i < NE; ++i)
+            o[i] = 0.f;
+#pragma unroll
+        for (int g = 0; g < (kPing ? 2 : 1); ++g) {
+            // the group's last stage of the segment, if it had one
+            const int last = kPing ? nst - 1 - ((kbase + nst - 1 + g) & 1) : nst - 1;
+            if (last < 0)
+                continue;
+            wait(bar_at(c, kPvDone + g), (uint32_t)((kPing ? (kbase + last) >> 1 : kbase + last) & 1));
+            if (alive) {
+                tc_fence_after();
+                uint32_t ov[NE];
+                tmem_ld_half<NE>(tmem + lane_base + kColO + (uint32_t)(g * 64), hh, ov);
+#pragma unroll
+                for (int i = 0; i < NE; ++i)
+                    o[i] = fmaf(__uint_as_float(ov[i]) * 256.f, scr[(kScrEnd + g) * 64 + half_row(hh, i)], o[i]);
+            }
+        }
+        if (alive && t < D) {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) {
+                const int r = half_row(hh, i);
+                if (r < R) {
+                    if (!whole)
+                        p.ws_part[((int64_t)slot_id * p.rows + r) * D + t] = o[i];
+                    else
+                        p.out[(row0 + rowoff[r]) * D + t] = __float2bfloat16_rn(o[i]);
                 }
             }
         }
         tc_fence_before();
-        named_barrier(1, kSoftmaxThreads);
+        named_barrier(kAllBar, kSoftmaxThreads);
 
         // --- split unit: the last piece to arrive merges all pieces
         if (!whole) {
@@ -843,10 +968,11 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                 const uint32_t prev = atomicAdd(counter, 1u);
                 *c.bcast = (prev == (uint32_t)(ce - cb)) ? 1u : 0u;
             }
-            named_barrier(1, kSoftmaxThreads);
+            named_barrier(kAllBar, kSoftmaxThreads);
             if (*c.bcast) {
                 __threadfence();
                 const int dq = D / 4;
+#pragma unroll 1
                 for (int rr = warp; rr < R; rr += kSoftmaxWarps) {
                     float M = -INFINITY;
                     for (int cc = cb + lane; cc <= ce; cc += 32) {
@@ -862,6 +988,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                     if (nan) {
                         wsum = acc.x = acc.y = acc.z = acc.w = __uint_as_float(0x7fc00000u);
                     } else if (M != -INFINITY) {
+#pragma unroll 2
                         for (int cc = cb; cc <= ce; ++cc) {
                             const int sl = piece_slot(p, cc, s.unit_begin);
                             const float w = ex2_approx((__ldcg(p.ws_lse + (int64_t)sl * p.rows + rr) - M) *
@@ -891,7 +1018,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                 if (threadIdx.x == 0)
                     *counter = 0u;
             }
-            named_barrier(1, kSoftmaxThreads);
+            named_barrier(kAllBar, kSoftmaxThreads);
         }
 
         kbase += nst;
@@ -935,59 +1062,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         c.smem = smem_raw + pad;
         c.base = raw + pad;
     }
-    c.ks = q.k_slots;
-    c.vs = q.v_slots;
-    c.lay = smem_layout(p.rows, q.head_dim, c.ks, c.vs);
-    c.abort_flag = reinterpret_cast<volatile uint32_t *>(c.smem + c.lay.misc);
-    c.bcast = reinterpret_cast<uint32_t *>(c.smem + c.lay.misc + 4);
+    constexpr Smem L = smem_layout(NR);
+    c.bars = c.base + L.bars;
+    c.abort_flag = reinterpret_cast<volatile uint32_t *>(c.smem + L.misc);
+    c.bcast = reinterpret_cast<uint32_t *>(c.smem + L.misc + 4);
     c.cta_begin = p.cta_cut[blockIdx.x];
     c.cta_end = p.cta_cut[blockIdx.x + 1];
     const bool work = c.cta_begin < c.cta_end;
     const int warp = threadIdx.x >> 5;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < c.ks; ++i) {
-            mbar_init(full_k(c, i), 1);
-            mbar_init(empty_k(c, i), 1);
+        constexpr uint32_t kStageWarps = q_pingpong(NR) ? kSoftmaxWarps / 2 : kSoftmaxWarps;   // that take a stage
+#pragma unroll 1
+        for (int i = 0; i < kBars; ++i) {
+            uint32_t n = 1;
+            if (i >= kConvV && i < kEmptyV || i >= kInfoB && i < kPFull)
+                n = kConvWarps;
+            else if (i >= kPFull && i < kPvDone || i >= kSFree && i < kQReady)
+                n = kStageWarps;
+            else if (i == kQEmpty || i == kQReady)
+                n = kSoftmaxWarps;
+            else if (i >= kSFull && i < kSFree || i == kFin)
+                n = 2;                       // the QK issuer and its commit; one commit per issuer
+            mbar_init(bar_at(c, i), n);
         }
-        for (int i = 0; i < c.vs; ++i) {
-            mbar_init(full_v(c, i), 1);
-            mbar_init(conv_v(c, i), kConvWarps);
-            mbar_init(empty_v(c, i), 1);
-        }
-        for (int i = 0; i < kScaleRing; ++i)
-            mbar_init(scale_b(c, i), 1);
-        mbar_init(p_full(c), kSoftmaxWarps);
-        mbar_init(pv_done(c), 1);
-        mbar_init(qfull(c), 1);
-        mbar_init(qempty(c), kSoftmaxWarps);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(s_full(c, i), 1);
-            mbar_init(s_free(c, i), kSoftmaxWarps);
-        }
-        mbar_init(q_ready(c), kSoftmaxWarps);
-        mbar_init(q_tile_free(c), 1);
-        mbar_init(fin_b(c), 2);                              // one commit per MMA issuer
         *c.abort_flag = 0u;
         *c.bcast = 0u;
         fence_barrier_init();
     }
     if (threadIdx.x < 64) {
         const int r = threadIdx.x;
-        reinterpret_cast<float *>(c.smem + c.lay.scr)[kScrM * 64 + r] = -INFINITY;
-        reinterpret_cast<float *>(c.smem + c.lay.scr)[kScrB * 64 + r] = kTermLog2;
-        reinterpret_cast<int *>(c.smem + c.lay.scr)[kScrOff * 64 + r] = r / p.group * p.hq + r % p.group;
+        reinterpret_cast<int *>(c.smem + L.scr)[kScrOff * 64 + r] = r / p.group * p.hq + r % p.group;
     }
     if (warp == 0)
-        tmem_alloc(c.base + c.lay.tslot, kTmemCols);
+        tmem_alloc(c.base + L.tslot, kTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(c.smem + c.lay.tslot);
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(c.smem + L.tslot);
     if (work && warp == kKWarp)
-        warm_l2_q8(&tmK, p, c, c.ks);
+        warm_l2_q8(&tmK, p, c, kKS);
     else if (work && warp == kVWarp)
-        warm_l2_q8(&tmV, p, c, c.vs);
+        warm_l2_q8(&tmV, p, c, kVS);
     pdl_wait_prior();                       // global memory only from here on
     pdl_launch_dependents();                // (after the wait: see launch.cuh)
 
@@ -1001,9 +1117,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (work) {
             if (warp == kKWarp)
-                producer_q8<true>(&tmK, q, c);
+                producer_q8<NR, true>(&tmK, q, c);
             else if (warp == kVWarp)
-                producer_q8<false>(&tmV, q, c);
+                producer_q8<NR, false>(&tmV, q, c);
             else if (warp == kQkWarp) {
                 if ((threadIdx.x & 31) == 0)
                     qk_issuer<NR>(q, c, tmem);
@@ -1011,7 +1127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if ((threadIdx.x & 31) == 0)
                     pv_issuer<NR>(q, c, tmem);
             } else {
-                convert_v(q, c);
+                convert_v<NR>(q, c);
             }
         }
     }
@@ -1029,7 +1145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 namespace {
 
 template <int NR>
-cudaError_t launch_nr(const CUtensorMap &tmK, const CUtensorMap &tmV, Q8DecodeParams &q, cudaStream_t stream)
+cudaError_t launch_nr(const CUtensorMap &tmK, const CUtensorMap &tmV, const Q8DecodeParams &q, cudaStream_t stream)
 {
     static int regs = -1;      // the register split hands out exactly the launch's 128 a thread
     if (regs < 0) {
@@ -1041,11 +1157,7 @@ cudaError_t launch_nr(const CUtensorMap &tmK, const CUtensorMap &tmV, Q8DecodePa
     }
     if ((uint32_t)regs * kThreads != kSoftmaxRegs * 256 + kOtherRegs * 256)
         return cudaErrorInvalidConfiguration;
-    q.k_slots = kMaxKSlots;
-    q.v_slots = 4;
-    while (smem_layout(q.d.rows, q.head_dim, q.k_slots, q.v_slots).total > (uint32_t)kSmemLimit)
-        --q.v_slots;
-    const uint32_t smem = smem_layout(q.d.rows, q.head_dim, q.k_slots, q.v_slots).total;
+    constexpr uint32_t smem = smem_layout(NR).total;
     const cudaError_t e =
         cudaFuncSetAttribute(shkv_q8_decode_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
@@ -1056,7 +1168,7 @@ cudaError_t launch_nr(const CUtensorMap &tmK, const CUtensorMap &tmV, Q8DecodePa
 }  // namespace
 
 // tmK, tmV: 2-D maps of the code pools (box of 128 bytes x P rows, 128-byte swizzle).
-cudaError_t launch_q8_decode(const CUtensorMap &tmK, const CUtensorMap &tmV, Q8DecodeParams &q, cudaStream_t stream)
+cudaError_t launch_q8_decode(const CUtensorMap &tmK, const CUtensorMap &tmV, const Q8DecodeParams &q, cudaStream_t stream)
 {
     switch (q_nr(q.d.rows)) {
     case 16:

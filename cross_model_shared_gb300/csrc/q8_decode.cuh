@@ -15,7 +15,7 @@ struct Q8DecodeParams {
     DecodeParams d;
     const uint8_t *scales;           // [num_pages, Hkv, 2, P]
     int64_t q_stride;                // elements from a query token to the next
-    int32_t head_dim, causal, has_empty, k_slots, v_slots;
+    int32_t head_dim, causal, has_empty;
     int32_t n_q[SHKV_MAX_BATCH];     // query tokens of each request (see Q8AttnParams)
     int32_t q0[SHKV_MAX_BATCH];
 };

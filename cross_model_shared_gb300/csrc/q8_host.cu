@@ -20,7 +20,8 @@ namespace shkv {
 cudaError_t launch_q8_cache(const Q8CacheParams &p, bool read, int num_sms, cudaStream_t stream);
 cudaError_t launch_q8_chunk(const CUtensorMap &tmK, const CUtensorMap &tmV, const Q8ChunkParams &p, bool splits,
                             cudaStream_t stream);
-cudaError_t launch_q8_decode(const CUtensorMap &tmK, const CUtensorMap &tmV, Q8DecodeParams &q, cudaStream_t stream);
+cudaError_t launch_q8_decode(const CUtensorMap &tmK, const CUtensorMap &tmV, const Q8DecodeParams &q,
+                             cudaStream_t stream);
 }  // namespace shkv
 
 using namespace shkv;
