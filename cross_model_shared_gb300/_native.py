@@ -167,7 +167,7 @@ def load() -> ctypes.CDLL:
         "shkv_q8_check_errors": [vp, vp, u32p],
         "shkv_q8_append_kv": [vp, i32, i32p, i32p, vp, ctypes.c_int64, vp, ctypes.c_int64, vp],
         "shkv_q8_read_kv": [vp, i32, i32p, i32p, vp, ctypes.c_int64, vp, ctypes.c_int64, vp],
-        "shkv_q8_workspace_size": [vp, ctypes.POINTER(ctypes.c_size_t)],
+        "shkv_q8_workspace_size": [vp, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(ctypes.c_size_t)],
         "shkv_q8_decode_attention": [vp, i32, i32, i32, vp, ctypes.c_float, vp, vp, vp, ctypes.c_size_t, vp],
         "shkv_q8_chunk_attention": [vp, i32, i32p, i32, vp, ctypes.c_int64, ctypes.c_float, vp, vp, vp,
                                     ctypes.c_size_t, vp],
@@ -383,10 +383,11 @@ def shkv_q8_read_kv(pool: int, batch: int, start: int, lens: int, k_out: int, k_
            "shkv_q8_read_kv")
 
 
-def shkv_q8_workspace_size(pool: int) -> int:
-    n = ctypes.c_size_t()
-    _check(load().shkv_q8_workspace_size(pool, ctypes.byref(n)), "shkv_q8_workspace_size")
-    return n.value
+def shkv_q8_workspace_size(pool: int):
+    """(workspace bytes, bytes at its front that must be zero before the first use)."""
+    n, z = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load().shkv_q8_workspace_size(pool, ctypes.byref(n), ctypes.byref(z)), "shkv_q8_workspace_size")
+    return n.value, z.value
 
 
 def shkv_q8_decode_attention(pool: int, batch: int, n_models: int, hq: int, q: int, scale: float, out: int,

@@ -474,11 +474,12 @@ shkv_status shkv_q8_read_kv(shkv_q8_pool *pool, int32_t batch, const int32_t *st
     return launch_cache(pool, p, true, stream);
 }
 
-shkv_status shkv_q8_workspace_size(const shkv_q8_pool *pool, size_t *bytes)
+shkv_status shkv_q8_workspace_size(const shkv_q8_pool *pool, size_t *bytes, size_t *zero_bytes)
 {
-    if (!pool || !bytes)
+    if (!pool || !bytes || !zero_bytes)
         return SHKV_ERR_INVALID_ARG;
     *bytes = workspace_need(pool);
+    *zero_bytes = count_bytes(pool);
     return SHKV_OK;
 }
 

@@ -8,6 +8,8 @@ decode and by ragged causal chunks.
 """
 from __future__ import annotations
 
+import array
+import contextlib
 from typing import Dict, Optional
 
 import numpy as np
@@ -16,15 +18,32 @@ import torch
 from . import _native as N
 
 _BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+_HERE = contextlib.nullcontext()
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
 
 
-def _host_i32(x, name: str) -> np.ndarray:
-    a = np.asarray(x)
-    if a.ndim != 1 or (a.size and a.dtype.kind not in "iu"):
-        raise ValueError(f"{name} must be a one-dimensional list of integers")
-    if a.size and (a.min() < 0 or a.max() > 2 ** 31 - 1):
-        raise ValueError(f"{name} must lie in [0, 2**31)")
-    return np.ascontiguousarray(a, dtype=np.int32)
+class _HostInts:
+    """Host int32 array of a C call (a list, a numpy array or a CPU tensor of
+    non-negative integers).  A decode step makes several of these per layer:
+    no numpy on the way."""
+    __slots__ = ("n", "total", "ptr", "_keep")
+
+    def __init__(self, x, name: str):
+        if not isinstance(x, (list, tuple)):
+            if getattr(x, "ndim", 1) != 1:
+                raise ValueError(f"{name} must be a one-dimensional list of integers")
+            x = x.tolist() if hasattr(x, "tolist") else x
+        try:
+            x = list(x)
+            a = array.array("i", x)
+        except TypeError:
+            raise ValueError(f"{name} must be a one-dimensional list of integers") from None
+        except OverflowError:
+            raise ValueError(f"{name} must lie in [0, 2**31)") from None
+        if x and min(x) < 0:
+            raise ValueError(f"{name} must lie in [0, 2**31)")
+        self.n, self.total, self._keep = len(a), sum(x), a
+        self.ptr = a.buffer_info()[0] if a else None
 
 
 class QuantizedKVPool:
@@ -42,8 +61,8 @@ class QuantizedKVPool:
     which must be ordered after the work that made its inputs.  The workspace
     of the attentions is one per stream; a call that is being captured into a
     CUDA graph takes one of its own from the graph's memory, so graphs share
-    none.  ``workspace=`` names another (zeroed before its first use, see
-    ``workspace_bytes``).
+    none.  ``workspace=`` names another, of ``workspace_bytes`` bytes whose
+    first ``workspace_zero_bytes`` are zero before its first use.
     """
 
     def __init__(self, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int, max_batch: int,
@@ -72,11 +91,11 @@ class QuantizedKVPool:
             self.error_word = torch.zeros(1, dtype=torch.int32, device=device)
             init = None
             if initial_seq_lens is not None:
-                given = _host_i32(initial_seq_lens, "initial_seq_lens")
-                if len(given) > max_batch:
+                given = _HostInts(initial_seq_lens, "initial_seq_lens")
+                if given.n > max_batch:
                     raise ValueError("initial_seq_lens is longer than max_batch")
                 init = np.zeros(max_batch, dtype=np.int32)
-                init[: len(given)] = given
+                init[: given.n] = given._keep
             cfg = N.shkv_q8_pool_config(
                 num_pages=num_pages, page_size=page_size, num_kv_heads=num_kv_heads, head_dim=head_dim,
                 max_batch=max_batch, max_pages_per_seq=max_pages_per_seq, k_pages=self.k_pages.data_ptr(),
@@ -85,7 +104,7 @@ class QuantizedKVPool:
                 error_word=self.error_word.data_ptr(), initial_seq_lens=init.ctypes.data if init is not None else None)
             torch.cuda.synchronize(device)
             self.handle = N.shkv_q8_pool_create(cfg)
-        self.workspace_bytes = N.shkv_q8_workspace_size(self.handle)
+        self.workspace_bytes, self.workspace_zero_bytes = N.shkv_q8_workspace_size(self.handle)
         self._workspaces: Dict[int, torch.Tensor] = {}
 
     def _pages(self, t: Optional[torch.Tensor], shape, name: str) -> torch.Tensor:
@@ -108,11 +127,15 @@ class QuantizedKVPool:
             pass
 
     # -- arguments ------------------------------------------------------------
-    def _stream(self, stream: Optional[torch.cuda.Stream]) -> torch.cuda.Stream:
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        if s.device != self.device:
+    def _on(self, stream: Optional[torch.cuda.Stream]):
+        """(context that makes the stream and the pool's device current, raw stream)."""
+        if stream is None:
+            if _raw_stream is not None and torch.cuda.current_device() == self.device.index:
+                return _HERE, _raw_stream(self.device.index)
+            stream = torch.cuda.current_stream(self.device)
+        elif stream.device != self.device:
             raise ValueError(f"stream must be one of {self.device}")
-        return s
+        return torch.cuda.stream(stream), stream.cuda_stream
 
     def _rows(self, t: torch.Tensor, heads: Optional[int], name: str) -> int:
         """Checks a [tokens, heads, head_dim] bf16 operand whose tokens may be strided; its stride in elements."""
@@ -134,26 +157,30 @@ class QuantizedKVPool:
             raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {self.device}")
         return t
 
-    def _workspace(self, given: Optional[torch.Tensor], stream: torch.cuda.Stream) -> torch.Tensor:
+    def _workspace(self, given: Optional[torch.Tensor], stream: int) -> torch.Tensor:
         if given is not None:
             if given.device != self.device or given.dtype != _U8 or not given.is_contiguous():
                 raise ValueError(f"workspace must be a contiguous uint8 tensor on {self.device}")
             return given
         if torch.cuda.is_current_stream_capturing():
-            return torch.zeros(self.workspace_bytes, dtype=_U8, device=self.device)
-        ws = self._workspaces.get(stream.cuda_stream)
+            return self._new_workspace()
+        ws = self._workspaces.get(stream)
         if ws is None:
-            ws = self._workspaces[stream.cuda_stream] = torch.zeros(self.workspace_bytes, dtype=_U8,
-                                                                    device=self.device)
+            ws = self._workspaces[stream] = self._new_workspace()
+        return ws
+
+    def _new_workspace(self) -> torch.Tensor:
+        ws = torch.empty(self.workspace_bytes, dtype=_U8, device=self.device)
+        ws[: self.workspace_zero_bytes].zero_()
         return ws
 
     # -- lengths --------------------------------------------------------------
     def set_seq_lens(self, lens, stream=None):
         """Set the cached lengths of the first len(lens) requests (synchronises the stream)."""
-        arr = _host_i32(lens, "lens")
-        s = self._stream(stream)
-        with torch.cuda.stream(s):
-            N.shkv_q8_pool_set_seq_lens(self.handle, len(arr), arr.ctypes.data, s.cuda_stream)
+        n = _HostInts(lens, "lens")
+        ctx, s = self._on(stream)
+        with ctx:
+            N.shkv_q8_pool_set_seq_lens(self.handle, n.n, n.ptr, s)
 
     def host_seq_lens(self, batch: Optional[int] = None) -> np.ndarray:
         out = np.zeros(self.max_batch if batch is None else batch, dtype=np.int32)
@@ -166,33 +193,31 @@ class QuantizedKVPool:
         k_new / v_new (bf16 [sum(new_lens), num_kv_heads, head_dim], tokens may
         be strided).  ``start`` writes from given positions on instead of the
         current lengths (dropping what lies behind them)."""
-        new = _host_i32(new_lens, "new_lens")
-        first = _host_i32(start, "start") if start is not None else None
-        if first is not None and len(first) != len(new):
+        new = _HostInts(new_lens, "new_lens")
+        first = _HostInts(start, "start") if start is not None else None
+        if first is not None and first.n != new.n:
             raise ValueError("start and new_lens must have the same length")
         ks, vs = self._rows(k_new, self.num_kv_heads, "k_new"), self._rows(v_new, self.num_kv_heads, "v_new")
-        total = int(new.sum(dtype=np.int64))
-        if k_new.shape[0] != total or v_new.shape[0] != total:
+        if k_new.shape[0] != new.total or v_new.shape[0] != new.total:
             raise ValueError("k_new and v_new must hold sum(new_lens) tokens")
-        s = self._stream(stream)
-        with torch.cuda.stream(s):
-            N.shkv_q8_append_kv(self.handle, len(new), first.ctypes.data if first is not None else None,
-                                new.ctypes.data, k_new.data_ptr(), ks, v_new.data_ptr(), vs, s.cuda_stream)
+        ctx, s = self._on(stream)
+        with ctx:
+            N.shkv_q8_append_kv(self.handle, new.n, first.ptr if first is not None else None, new.ptr,
+                                k_new.data_ptr(), ks, v_new.data_ptr(), vs, s)
 
     def read_kv(self, start, lens, k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
                 stream=None):
         """Tokens start[b] .. start[b] + lens[b] - 1 of every request as bf16
         (K, V), each [sum(lens), num_kv_heads, head_dim]."""
-        first, n = _host_i32(start, "start"), _host_i32(lens, "lens")
-        if len(first) != len(n):
+        first, n = _HostInts(start, "start"), _HostInts(lens, "lens")
+        if first.n != n.n:
             raise ValueError("start and lens must have the same length")
-        shape = (int(n.sum(dtype=np.int64)), self.num_kv_heads, self.head_dim)
-        s = self._stream(stream)
-        with torch.cuda.stream(s):
+        shape = (n.total, self.num_kv_heads, self.head_dim)
+        row = self.num_kv_heads * self.head_dim
+        ctx, s = self._on(stream)
+        with ctx:
             k, v = self._out(k_out, shape, _BF16, "k_out"), self._out(v_out, shape, _BF16, "v_out")
-            row = self.num_kv_heads * self.head_dim
-            N.shkv_q8_read_kv(self.handle, len(n), first.ctypes.data, n.ctypes.data, k.data_ptr(), row, v.data_ptr(),
-                              row, s.cuda_stream)
+            N.shkv_q8_read_kv(self.handle, n.n, first.ptr, n.ptr, k.data_ptr(), row, v.data_ptr(), row, s)
         return k, v
 
     def decode_attention(self, q: torch.Tensor, n_models: int, scale: Optional[float] = None,
@@ -206,15 +231,14 @@ class QuantizedKVPool:
         B, rows, D = q.shape
         if n_models < 1 or rows % n_models or D != self.head_dim:
             raise ValueError("q must be [B, n_models * hq, head_dim]")
-        s = self._stream(stream)
-        with torch.cuda.stream(s):
+        ctx, s = self._on(stream)
+        with ctx:
             o = self._out(out, q.shape, _BF16, "out")
             e = self._out(lse, (B, rows), _F32, "lse") if return_lse or lse is not None else None
             ws = self._workspace(workspace, s)
             N.shkv_q8_decode_attention(self.handle, B, n_models, rows // n_models, q.data_ptr(),
                                        D ** -0.5 if scale is None else float(scale), o.data_ptr(),
-                                       e.data_ptr() if e is not None else None, ws.data_ptr(), ws.numel(),
-                                       s.cuda_stream)
+                                       e.data_ptr() if e is not None else None, ws.data_ptr(), ws.numel(), s)
         return (o, e) if e is not None else o
 
     def chunk_attention(self, q: torch.Tensor, new_lens, scale: Optional[float] = None,
@@ -224,25 +248,24 @@ class QuantizedKVPool:
         already appended: q bf16 [sum(new_lens), hq, head_dim], requests packed
         one after another (tokens may be strided).  New token i attends the
         cached prefix and the new tokens up to itself."""
-        new = _host_i32(new_lens, "new_lens")
+        new = _HostInts(new_lens, "new_lens")
         qs = self._rows(q, None, "q")
         T, hq, D = q.shape
-        if T != int(new.sum(dtype=np.int64)):
+        if T != new.total:
             raise ValueError("q must hold sum(new_lens) tokens")
-        s = self._stream(stream)
-        with torch.cuda.stream(s):
+        ctx, s = self._on(stream)
+        with ctx:
             o = self._out(out, (T, hq, D), _BF16, "out")
             e = self._out(lse, (T, hq), _F32, "lse") if return_lse or lse is not None else None
             if T:
                 ws = self._workspace(workspace, s)
-                N.shkv_q8_chunk_attention(self.handle, len(new), new.ctypes.data, hq, q.data_ptr(), qs,
+                N.shkv_q8_chunk_attention(self.handle, new.n, new.ptr, hq, q.data_ptr(), qs,
                                           D ** -0.5 if scale is None else float(scale), o.data_ptr(),
-                                          e.data_ptr() if e is not None else None, ws.data_ptr(), ws.numel(),
-                                          s.cuda_stream)
+                                          e.data_ptr() if e is not None else None, ws.data_ptr(), ws.numel(), s)
         return (o, e) if e is not None else o
 
     def check_errors(self, stream=None) -> int:
         """Synchronize and return (then clear) the device error bits."""
-        s = self._stream(stream)
-        with torch.cuda.stream(s):
-            return N.shkv_q8_check_errors(self.handle, s.cuda_stream)
+        ctx, s = self._on(stream)
+        with ctx:
+            return N.shkv_q8_check_errors(self.handle, s)

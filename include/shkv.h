@@ -590,11 +590,12 @@ shkv_status shkv_q8_read_kv(shkv_q8_pool *pool, int32_t batch, const int32_t *st
 
 /*
  * Bytes of device workspace that one attention call on this pool needs, for
- * any shape.  It must be zero before its first use and is left ready for the
- * next call (of any shape) by every call that completes without device error
- * bits.  Calls sharing one workspace must not overlap on the GPU.
+ * any shape.  Its first *zero_bytes bytes must be zero before its first use
+ * and are left so by every call that completes without device error bits;
+ * the rest may hold anything.  Calls sharing one workspace must not overlap on
+ * the GPU.
  */
-shkv_status shkv_q8_workspace_size(const shkv_q8_pool *pool, size_t *bytes);
+shkv_status shkv_q8_workspace_size(const shkv_q8_pool *pool, size_t *bytes, size_t *zero_bytes);
 
 /*
  * shkv_decode_attention over the 8-bit cache: same rows, layouts, limits
