@@ -33,15 +33,9 @@
 // whose sum of P exceeds 2^15 (fp16's range) or is no number sends its warp
 // through the exact path.
 //
-// A tile's stage is a chain, QK -> softmax -> PV -> QK, and a warp alone runs
-// its part at four clocks an instruction: a row's 128 scores are shared by two
-// threads (64 keys each, of two warps that reach the same TMEM lanes), which
-// agree on the running maximum where it moves.
-//
-// Roles (768 threads): warps 0-7 softmax of tile A, 8-15 of tile B (row = TMEM
-// lane, half of the keys by bit 2 of the warp), 16 QK issuer, 17 PV issuer, 18
-// producer of K, 19 producer of V and its scale bytes, 20-23 V conversion, one
-// key a thread: also the column factors.
+// Roles (512 threads): warps 0-3 softmax of tile A, 4-7 of tile B (row = TMEM
+// lane), 8 QK issuer, 9 PV issuer, 10 producer of K, 11 producer of V and its
+// scale bytes, 12-15 V conversion, one key a thread: also the column factors.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -60,11 +54,9 @@ namespace shkv {
 namespace {
 
 constexpr int kKT = 128;                 // keys per stage
-constexpr int kThreads = 768;
-constexpr int kGroupWarps = 8;           // softmax warps per tile
-constexpr int kSoftmaxThreads = 2 * kGroupWarps * 32;
-constexpr int kQkWarp = 16, kPvWarp = 17, kKWarp = 18, kVWarp = 19, kConvWarp0 = 20, kConvWarps = 4;
-constexpr int kHK = kKT / 2;             // keys per softmax thread of a stage
+constexpr int kThreads = 512;
+constexpr int kQkWarp = 8, kPvWarp = 9, kKWarp = 10, kVWarp = 11, kConvWarp0 = 12, kConvWarps = 4;
+constexpr int kGroupWarps = 4;           // softmax warps per tile
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.f;      // m lags the maximum by at most this
 constexpr float kPLog2 = 7.f;            // P at the running maximum
@@ -78,21 +70,20 @@ constexpr int kKS = 3, kVS = 3;          // ring slots of 16 KB (K) and 32 KB (V
 constexpr uint32_t kKSlotBytes = kKT * 128;
 constexpr uint32_t kVSlotBytes = 2 * kKT * 128;
 constexpr uint32_t kQTermBytes = 128 * 128;      // one e4m3 term of a tile [128 rows][128 B]
-constexpr uint32_t kLaunchRegs = 80, kSoftmaxRegs = 96, kOtherRegs = 48;
-static_assert(kSoftmaxRegs * kSoftmaxThreads + kOtherRegs * (kThreads - kSoftmaxThreads) == kLaunchRegs * kThreads,
-              "register split");
+constexpr uint32_t kSoftmaxRegs = 200, kOtherRegs = 56;
+static_assert(kSoftmaxRegs * 256 + kOtherRegs * 256 == 128 * kThreads, "register split");
 
 __device__ __forceinline__ uint32_t col_s(int x) { return (uint32_t)(x * 128); }
 __device__ __forceinline__ uint32_t col_o(int x) { return (uint32_t)(256 + x * 128); }
 
 struct Smem {
-    uint32_t qtile, kring, vring, scales, factor, pfactor, xch, info, bars, misc, tslot, total;
+    uint32_t qtile, kring, vring, scales, factor, pfactor, info, bars, misc, tslot, total;
 };
 
 // Query tiles [tile][qh | ql][128 rows][128 B], K ring, V ring (slots
 // [half][128 keys][128 B], the codes in the upper half until they are
 // converted), all 128-byte swizzled; per V slot its scale bytes, the keys'
-// score factors and P factors, and four words (valid pages, E, wide); xch is where the two threads of a row meet.
+// score factors and P factors, and four words (valid pages, E, wide).
 __host__ __device__ inline Smem smem_layout()
 {
     Smem u;
@@ -102,8 +93,7 @@ __host__ __device__ inline Smem smem_layout()
     u.scales = u.vring + kVS * kVSlotBytes;
     u.factor = u.scales + kVS * 2 * kKT;
     u.pfactor = u.factor + kVS * kKT * 4;
-    u.xch = u.pfactor + kVS * kKT * 4;
-    u.info = u.xch + 2 * 2 * 256 * 4;
+    u.info = u.pfactor + kVS * kKT * 4;
     u.bars = u.info + kVS * 16;
     u.misc = u.bars + (uint32_t)(2 * kKS + 3 * kVS + 9) * 8u;
     u.tslot = u.misc + 8;
@@ -348,8 +338,7 @@ __device__ void chunk_convert(const Q8ChunkParams &p, const Ctx &c)
                     uint4 raw[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        raw[i] = live ? *reinterpret_cast<const uint4 *>(row + kKT * 128 + (((4 * h + i) ^ (t & 7)) << 4))
-                                      : make_uint4(0u, 0u, 0u, 0u);
+                        raw[i] = *reinterpret_cast<const uint4 *>(row + kKT * 128 + (((4 * h + i) ^ (t & 7)) << 4));
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
@@ -358,7 +347,7 @@ __device__ void chunk_convert(const Q8ChunkParams &p, const Ctx &c)
                         for (int v = 0; v < 8; ++v) {
                             const __half2 x = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2(
                                                           (__nv_fp8x2_storage_t)(w[v >> 1] >> (16 * (v & 1))), __NV_E4M3)), f);
-                            o[v] = *reinterpret_cast<const uint32_t *>(&x);
+                            o[v] = live ? *reinterpret_cast<const uint32_t *>(&x) : 0u;
                         }
                         uint8_t *dst = row + h * (kKT * 128);
                         *reinterpret_cast<uint4 *>(dst + (((2 * i) ^ (t & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -483,8 +472,7 @@ __device__ void chunk_pv(const Q8ChunkParams &p, const Ctx &c, uint32_t tmem)
                     tc_fence_after();
 #pragma unroll
                     for (int ks = 0; ks < kKT / 16; ++ks)
-                        umma_f16_ts(tmem + col_o(x), tmem + col_s(x) + (uint32_t)((ks >> 2) * 64 + (ks & 3) * 8),
-                                    vd + (uint64_t)(ks * 128), idesc,
+                        umma_f16_ts(tmem + col_o(x), tmem + col_s(x) + (uint32_t)(ks * 8), vd + (uint64_t)(ks * 128), idesc,
                                     (j == t.s0 && ks == 0) ? 0u : 1u);
                 }
                 umma_commit(pv_done(c, x));
@@ -506,58 +494,45 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// The halves of a row's two threads meet here: each gives a value and gets the
-// other's.  The buffers alternate, so one barrier an exchange suffices.
-struct Pair {
-    float *buf;                  // this thread's places are buf[0] and buf[512], the other's 128 away
-    int other, id, turn;
-    __device__ __forceinline__ float swap(float v)
-    {
-        float *b = buf + turn * 512;
-        b[0] = v;
-        named_barrier((uint32_t)id, 64u);
-        turn ^= 1;
-        return b[other];
-    }
-};
-
-// Half h of this row of the query as two e4m3 terms in its tile; returns the
-// row's scale.
-template <int D>
-__device__ __forceinline__ float stage_row(const Ctx &c, const __nv_bfloat16 *src, int x, int r, int h, Pair &pair)
+// This row of the query as two e4m3 terms in its tile; returns the row's scale.
+__device__ __forceinline__ float stage_row(const Q8ChunkParams &p, const Ctx &c, const __nv_bfloat16 *src, int x, int r)
 {
-    constexpr int NV = D / 16;                           // vectors of 8 values
-    uint4 v[NV];
-#pragma unroll
-    for (int ch = 0; ch < NV; ++ch)
-        v[ch] = src ? __ldg(reinterpret_cast<const uint4 *>(src) + h * NV + ch) : make_uint4(0u, 0u, 0u, 0u);
+    const int D = p.head_dim;
+    const uint4 *s4 = reinterpret_cast<const uint4 *>(src);
     uint32_t a = 0;
-#pragma unroll
-    for (int ch = 0; ch < NV; ++ch)
-        a = __vmaxu2(__vmaxu2(a, __vmaxu2(v[ch].x & 0x7fff7fffu, v[ch].y & 0x7fff7fffu)),
-                     __vmaxu2(v[ch].z & 0x7fff7fffu, v[ch].w & 0x7fff7fffu));
+#pragma unroll 4
+    for (int ch = 0; ch < D / 8; ++ch) {
+        const uint4 v = src ? __ldg(s4 + ch) : make_uint4(0u, 0u, 0u, 0u);
+        a = __vmaxu2(__vmaxu2(a, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)),
+                     __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    }
     a = max(a & 0xffffu, a >> 16);
-    a = max(a, __float_as_uint(pair.swap(__uint_as_float(a))));
-    const int byte = max((int)((a + 0x1fu) >> 7) - 8, 0);
+    int byte = (int)(a >> 7) - 8 + ((a & 0x7fu) > 0x60u ? 1 : 0);
+    byte = byte < 0 ? 0 : byte;
     const float inv = __uint_as_float((uint32_t)(254 - byte) << 23);
     const bool bad = a >= 0x7f80u;                       // an infinity or a NaN: the row's scores are NaN
     uint8_t *dst = c.smem + c.lay.qtile + 2u * (uint32_t)x * kQTermBytes + (uint32_t)r * 128u;
-#pragma unroll
-    for (int ch = 0; ch < NV / 2; ++ch) {
+#pragma unroll 1
+    for (int ch = 0; ch < D / 16; ++ch) {
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint4 q = v[2 * ch + (i >> 2)];
-            const uint32_t w = (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
-            const float2 f = make_float2(__uint_as_float(w << 16) * inv, __uint_as_float(w & 0xffff0000u) * inv);
-            const __nv_fp8x2_storage_t hc = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
-            const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(hc, __NV_E4M3)));
-            const __nv_fp8x2_storage_t d = __nv_cvt_float2_to_fp8x2(make_float2(f.x - hf.x, f.y - hf.y), __NV_SATFINITE,
-                                                                    __NV_E4M3);
-            hi[i >> 1] = (i & 1) ? hi[i >> 1] | ((uint32_t)hc << 16) : hc;
-            lo[i >> 1] = (i & 1) ? lo[i >> 1] | ((uint32_t)d << 16) : d;
+        for (int half = 0; half < 2; ++half) {
+            const uint4 v = src ? __ldg(s4 + 2 * ch + half) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t xs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = make_float2(__uint_as_float(xs[i] << 16) * inv,
+                                             __uint_as_float(xs[i] & 0xffff0000u) * inv);
+                const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+                const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+                const __nv_fp8x2_storage_t d = __nv_cvt_float2_to_fp8x2(make_float2(f.x - hf.x, f.y - hf.y),
+                                                                        __NV_SATFINITE, __NV_E4M3);
+                const int w = 2 * half + (i >> 1);
+                hi[w] = (i & 1) ? hi[w] | ((uint32_t)h << 16) : h;
+                lo[w] = (i & 1) ? lo[w] | ((uint32_t)d << 16) : d;
+            }
         }
-        const uint32_t off = (uint32_t)(((h * (NV / 2) + ch) ^ (r & 7)) << 4);
+        const uint32_t off = (uint32_t)((ch ^ (r & 7)) << 4);
         const uint32_t n = 0x7f7f7f7fu;
         *reinterpret_cast<uint4 *>(dst + off) = bad ? make_uint4(n, n, n, n) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4 *>(dst + kQTermBytes + off) =
@@ -566,23 +541,16 @@ __device__ __forceinline__ float stage_row(const Ctx &c, const __nv_bfloat16 *sr
     return bad ? 1.f : q8_scale((uint32_t)byte);
 }
 
-__device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tmem, int x, int h)
+__device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tmem, int x)
 {
-    const int r = threadIdx.x & 127;
+    const int r = threadIdx.x - x * 128;
     const int lane = r & 31, warp = r >> 5;
     const int ti = r / p.group, tj = r - ti * p.group;
-    const int P = p.page_size, D = p.head_dim;
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    const uint32_t orow = tmem + lane_base + col_o(x) + (uint32_t)(h * (D / 2));   // this thread's half of O's columns
-    const uint32_t srow = tmem + lane_base + col_s(x) + (uint32_t)(h * kHK);       // ... of S's; P lies over its first 32
-    // bits of the stage's page mask in this thread's half
-    const uint32_t half_pages = (1u << (kHK / P)) - 1u;
-    const int page0 = h * (kHK / P);
-    Pair pair;
-    pair.buf = reinterpret_cast<float *>(c.smem + c.lay.xch) + x * 256 + h * 128 + r;
-    pair.other = h ? -128 : 128;
-    pair.id = 1 + x * 4 + warp;
-    pair.turn = 0;
+    const uint32_t orow = tmem + lane_base + col_o(x);
+    const uint32_t srow = tmem + lane_base + col_s(x);
+    const int P = p.page_size, D = p.head_dim;
+    const uint32_t all_pages = (1u << (kKT / P)) - 1u;
     bool alive = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
         bool ok = false;
@@ -601,14 +569,13 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
         const int head = t.g * p.group + tj;
         if (seg > 0)
             wait(q_free(c), (uint32_t)((seg - 1) & 1));
-        const __nv_bfloat16 *src = row_ok ? p.q + tok * p.q_stride + (int64_t)head * D : nullptr;
-        const float rq = D == 64 ? stage_row<64>(c, src, x, r, h, pair) : stage_row<128>(c, src, x, r, h, pair);
+        const float rq = stage_row(p, c, row_ok ? p.q + tok * p.q_stride + (int64_t)head * D : nullptr, x, r);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0)
             mbar_arrive(q_ready(c));
 
-        float m_use = -INFINITY, lsum = 0.f;             // the row's m, and this half's sum
+        float m_use = -INFINITY, lsum = 0.f;
         float m2 = 0.f;                                  // P's reference once the piece is wide; m + E until then
         bool apart = false;
         int e = 0;                                       // E as a scale byte
@@ -616,34 +583,34 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
 #pragma unroll 1
         for (int j = t.s0; j < s1; ++j) {
             const int k = kbase + j - t.s0, vs = k % kVS;
-            const int key0 = j * kKT + h * kHK;
+            const int key0 = j * kKT;
             wait(conv_v(c, vs), ring_par(k, kVS));
             const volatile uint32_t *info = reinterpret_cast<const volatile uint32_t *>(c.smem + c.lay.info) + vs * 4;
-            const uint32_t pmask = alive ? (info[0] >> page0) & half_pages : 0u;
+            const uint32_t pmask = alive ? info[0] : 0u;
             const int e_new = alive ? (int)info[1] : e;
             const bool wide = info[2] != 0u;
-            const float4 *fac = reinterpret_cast<const float4 *>(c.smem + c.lay.factor + (vs * kKT + h * kHK) * 4);
-            // keys of this half that the row may see: [key0, key0 + nvis), on pages that were copied
+            const float4 *fac = reinterpret_cast<const float4 *>(c.smem + c.lay.factor + vs * kKT * 4);
+            // keys this row may see: [key0, key0 + nvis), on pages that were copied
             // (padding rows see all: their scores only reach their own row of O, which is not stored)
-            const int nvis = row_ok ? min(kHK, max(0, pos - key0 + 1)) : kHK;
-            const bool dense = pmask == half_pages && nvis == kHK;
+            const int nvis = row_ok ? min(kKT, pos - key0 + 1) : kKT;
+            const bool dense = pmask == all_pages && nvis == kKT;
             wait(s_full(c, x), (uint32_t)(done & 1));
             if (alive)
                 tc_fence_after();
-            uint32_t sv[2][32];
+            uint32_t sv[4][32];
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+            for (int q = 0; q < 4; ++q)
                 tmem_ld32_nowait(srow + (uint32_t)(q * 32), sv[q]);
             tmem_wait_ld();
             // Common case (see the top): P against the running maximum.
             float part = 0.f;
-            bool fast = dense && alive && m_use != -INFINITY && e_new == e && !wide;
-            if (__all_sync(0xffffffffu, fast)) {
+            bool fast = __all_sync(0xffffffffu, dense && alive && m_use != -INFINITY && e_new == e && !wide);
+            if (fast) {
                 const float nmu = kPLog2 - m_use;
                 const float2 rq2 = make_float2(rq, rq), nmu2 = make_float2(nmu, nmu);
                 float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
+                for (int q = 0; q < 4; ++q) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -664,17 +631,17 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                     tmem_st16_nowait(srow + (uint32_t)(q * 16), pk);
                 }
                 part = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-                fast = part <= kMaxPart;
-            } else {
-                fast = false;
+                if (__any_sync(0xffffffffu, !(part <= kMaxPart))) {
+                    tmem_wait_st();
+                    fast = false;
+                }
             }
-            if (bar_red_or((uint32_t)pair.id, 64u, !fast)) {
-                // the exact path, by both halves: scores, masked; the stage's maximum
-                tmem_wait_st();
+            if (!fast) {
+                // the exact path: scores, masked; the stage's maximum
                 float cm = -INFINITY;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    // bit i: column 32q + i of the half is visible (before this row's end, on a copied page)
+                for (int q = 0; q < 4; ++q) {
+                    // bit i: column 32q + i is visible (before this row's end, on a copied page)
                     const int n = alive ? min(max(nvis - q * 32, 0), 32) : 0;
                     uint32_t vis = n >= 32 ? 0xffffffffu : ((1u << n) - 1u);
                     uint32_t pages = 0u;
@@ -695,7 +662,6 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                         }
                     }
                 }
-                cm = fmaxf(cm, pair.swap(cm));
                 const int de = e_new - e;
                 if (wide && !apart) {
                     apart = true;
@@ -710,11 +676,11 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                     lsum *= scale_o;
                     m_use = cm;
                 }
-                const float4 *pf = reinterpret_cast<const float4 *>(c.smem + c.lay.pfactor + (vs * kKT + h * kHK) * 4);
+                const float4 *pf = reinterpret_cast<const float4 *>(c.smem + c.lay.pfactor + vs * kKT * 4);
                 if (apart) {
                     float cy = -INFINITY;
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
+                    for (int q = 0; q < 4; ++q)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const float4 f = pf[q * 8 + i];
@@ -723,7 +689,7 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                                        fmaxf(__uint_as_float(sv[q][4 * i + 2]) + f.z,
                                              __uint_as_float(sv[q][4 * i + 3]) + f.w));
                         }
-                    cy = fmaxf(cy, pair.swap(cy)) + (float)e;
+                    cy += (float)e;
                     scale_o = 1.f;
                     if (m2 == -INFINITY) {
                         m2 = cy;
@@ -740,14 +706,14 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                     if (alive) {
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c8 = 0; c8 < D / 16; ++c8) {
-                            uint32_t ov[8];
-                            tmem_ld8_nowait(orow + (uint32_t)(c8 * 8), ov);
+                        for (int c16 = 0; c16 < D / 16; ++c16) {
+                            uint32_t ov[16];
+                            tmem_ld16_nowait(orow + (uint32_t)(c16 * 16), ov);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
+                            for (int i = 0; i < 16; ++i)
                                 ov[i] = __float_as_uint(__uint_as_float(ov[i]) * scale_o);
-                            tmem_st8_nowait(orow + (uint32_t)(c8 * 8), ov);
+                            tmem_st16_nowait(orow + (uint32_t)(c16 * 16), ov);
                         }
                         tmem_wait_st();
                     }
@@ -756,7 +722,7 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                 const float mu2 = m2 == -INFINITY ? 0.f : m2 - (float)e - kPLog2;
                 part = 0.f;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
+                for (int q = 0; q < 4; ++q) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -791,7 +757,6 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
         // --- this row of O_x, normalised, and its log-sum-exp
         const bool whole = t.s0 == 0 && t.s1 == t.nst_all;
         const bool any = s1 > t.s0;                      // this tile attends a stage of the piece
-        lsum += pair.swap(lsum);
         if (any)
             wait(pv_done(c, x), (uint32_t)((done - 1) & 1));
         if (alive && t.ntok[x] > 0) {
@@ -803,7 +768,7 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
             const int slot = piece_slot(p, blockIdx.x, t.u);
             const int64_t prow = (int64_t)slot * kChunkRows + x * 128 + r;
 #pragma unroll 1
-            for (int c16 = 0; c16 < D / 32; ++c16) {
+            for (int c16 = 0; c16 < D / 16; ++c16) {
                 uint32_t ov[16];
                 tmem_ld16_nowait(orow + (uint32_t)(c16 * 16), ov);
                 tmem_wait_ld();
@@ -811,21 +776,20 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     o[i] = any && lsum != 0.f ? __uint_as_float(ov[i]) * inv * ef : 0.f;
-                const int col = h * (D / 2) + c16 * 16;
                 if (row_ok && whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + orr * D + col);
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + orr * D + c16 * 16);
 #pragma unroll
                     for (int v = 0; v < 2; ++v)
                         dst[v] = make_uint4(pack_bf16x2(o[8 * v], o[8 * v + 1]), pack_bf16x2(o[8 * v + 2], o[8 * v + 3]),
                                             pack_bf16x2(o[8 * v + 4], o[8 * v + 5]), pack_bf16x2(o[8 * v + 6], o[8 * v + 7]));
                 } else if (row_ok) {
-                    float4 *dst = reinterpret_cast<float4 *>(p.ws_part + prow * D + col);
+                    float4 *dst = reinterpret_cast<float4 *>(p.ws_part + prow * D + c16 * 16);
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
                         dst[v] = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
                 }
             }
-            if (row_ok && h == 0) {
+            if (row_ok) {
                 const float lse = lsum != 0.f ? ((m_use == -INFINITY ? 0.f : m_use - kPLog2) + log2f(lsum)) *
                                                     0.6931471805599453f
                                               : -INFINITY;
@@ -890,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < 2 * kGroupWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        chunk_softmax(p, c, tmem, warp / kGroupWarps, (warp >> 2) & 1);
+        chunk_softmax(p, c, tmem, warp / kGroupWarps);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kKWarp)
@@ -978,7 +942,7 @@ __global__ void __launch_bounds__(256) shkv_q8_chunk_join_kernel(const __grid_co
 cudaError_t launch_q8_chunk(const CUtensorMap &tmK, const CUtensorMap &tmV, const Q8ChunkParams &p, bool splits,
                             cudaStream_t stream)
 {
-    static int regs = -1;      // the register split hands out exactly the launch's kLaunchRegs a thread
+    static int regs = -1;      // the register split hands out exactly the launch's 128 a thread
     if (regs < 0) {
         cudaFuncAttributes fa;
         const cudaError_t e = cudaFuncGetAttributes(&fa, shkv_q8_chunk_kernel);
@@ -986,7 +950,7 @@ cudaError_t launch_q8_chunk(const CUtensorMap &tmK, const CUtensorMap &tmV, cons
             return e;
         regs = fa.numRegs;
     }
-    if ((uint32_t)regs != kLaunchRegs)
+    if ((uint32_t)regs * kThreads != kSoftmaxRegs * 256 + kOtherRegs * 256)
         return cudaErrorInvalidConfiguration;
     const uint32_t smem = smem_layout().total;
     cudaError_t e = cudaFuncSetAttribute(shkv_q8_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
