@@ -338,7 +338,8 @@ __device__ void chunk_convert(const Q8ChunkParams &p, const Ctx &c)
                     uint4 raw[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        raw[i] = *reinterpret_cast<const uint4 *>(row + kKT * 128 + (((4 * h + i) ^ (t & 7)) << 4));
+                        raw[i] = live ? *reinterpret_cast<const uint4 *>(row + kKT * 128 + (((4 * h + i) ^ (t & 7)) << 4))
+                                      : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
@@ -347,7 +348,7 @@ __device__ void chunk_convert(const Q8ChunkParams &p, const Ctx &c)
                         for (int v = 0; v < 8; ++v) {
                             const __half2 x = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2(
                                                           (__nv_fp8x2_storage_t)(w[v >> 1] >> (16 * (v & 1))), __NV_E4M3)), f);
-                            o[v] = live ? *reinterpret_cast<const uint32_t *>(&x) : 0u;
+                            o[v] = *reinterpret_cast<const uint32_t *>(&x);
                         }
                         uint8_t *dst = row + h * (kKT * 128);
                         *reinterpret_cast<uint4 *>(dst + (((2 * i) ^ (t & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -494,49 +495,48 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// This row of the query as two e4m3 terms in its tile; returns the row's scale.
-__device__ __forceinline__ float stage_row(const Q8ChunkParams &p, const Ctx &c, const __nv_bfloat16 *src, int x, int r)
+// This row of the query as two e4m3 terms in its tile; returns the row's
+// scale.  (Run once a piece: what counts is its instructions, fetched cold,
+// so the row is read twice by short loops instead of held by unrolled code.)
+__device__ __forceinline__ float stage_row(const Ctx &c, const __nv_bfloat16 *src, int D, int x, int r)
 {
-    const int D = p.head_dim;
     const uint4 *s4 = reinterpret_cast<const uint4 *>(src);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     uint32_t a = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int ch = 0; ch < D / 8; ++ch) {
-        const uint4 v = src ? __ldg(s4 + ch) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 v = src ? __ldg(s4 + ch) : zero;
         a = __vmaxu2(__vmaxu2(a, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)),
                      __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
     }
     a = max(a & 0xffffu, a >> 16);
-    int byte = (int)(a >> 7) - 8 + ((a & 0x7fu) > 0x60u ? 1 : 0);
-    byte = byte < 0 ? 0 : byte;
+    const int byte = max((int)((a + 0x1fu) >> 7) - 8, 0);
     const float inv = __uint_as_float((uint32_t)(254 - byte) << 23);
     const bool bad = a >= 0x7f80u;                       // an infinity or a NaN: the row's scores are NaN
     uint8_t *dst = c.smem + c.lay.qtile + 2u * (uint32_t)x * kQTermBytes + (uint32_t)r * 128u;
+    uint4 next = src ? __ldg(s4) : zero;
 #pragma unroll 1
-    for (int ch = 0; ch < D / 16; ++ch) {
+    for (int ch = 0; ch < D / 8; ++ch) {
+        const uint4 v = next;
+        if (src && ch + 1 < D / 8)
+            next = __ldg(s4 + ch + 1);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const uint4 v = src ? __ldg(s4 + 2 * ch + half) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t xs[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = make_float2(__uint_as_float(xs[i] << 16) * inv,
-                                             __uint_as_float(xs[i] & 0xffff0000u) * inv);
-                const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
-                const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
-                const __nv_fp8x2_storage_t d = __nv_cvt_float2_to_fp8x2(make_float2(f.x - hf.x, f.y - hf.y),
-                                                                        __NV_SATFINITE, __NV_E4M3);
-                const int w = 2 * half + (i >> 1);
-                hi[w] = (i & 1) ? hi[w] | ((uint32_t)h << 16) : h;
-                lo[w] = (i & 1) ? lo[w] | ((uint32_t)d << 16) : d;
-            }
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = make_float2(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xffff0000u) * inv);
+            const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+            const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+            hi[i] = h;
+            lo[i] = __nv_cvt_float2_to_fp8x2(make_float2(f.x - hf.x, f.y - hf.y), __NV_SATFINITE, __NV_E4M3);
         }
-        const uint32_t off = (uint32_t)((ch ^ (r & 7)) << 4);
-        const uint32_t n = 0x7f7f7f7fu;
-        *reinterpret_cast<uint4 *>(dst + off) = bad ? make_uint4(n, n, n, n) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4 *>(dst + kQTermBytes + off) =
-            bad ? make_uint4(n, n, n, n) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        uint2 h2 = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+        uint2 l2 = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+        if (bad)
+            h2.x = h2.y = l2.x = l2.y = 0x7f7f7f7fu;
+        uint8_t *at = dst + (((ch >> 1) ^ (r & 7)) << 4) + (ch & 1) * 8;
+        *reinterpret_cast<uint2 *>(at) = h2;
+        *reinterpret_cast<uint2 *>(at + kQTermBytes) = l2;
     }
     return bad ? 1.f : q8_scale((uint32_t)byte);
 }
@@ -569,7 +569,8 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
         const int head = t.g * p.group + tj;
         if (seg > 0)
             wait(q_free(c), (uint32_t)((seg - 1) & 1));
-        const float rq = stage_row(p, c, row_ok ? p.q + tok * p.q_stride + (int64_t)head * D : nullptr, x, r);
+        const __nv_bfloat16 *src = row_ok ? p.q + tok * p.q_stride + (int64_t)head * D : nullptr;
+        const float rq = stage_row(c, src, D, x, r);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0)
@@ -632,33 +633,51 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                 }
                 part = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
                 if (__any_sync(0xffffffffu, !(part <= kMaxPart))) {
+                    // the scores go back for the exact path
                     tmem_wait_st();
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        tmem_st32(srow + (uint32_t)(q * 32), sv[q]);
                     fast = false;
                 }
             }
             if (!fast) {
-                // the exact path: scores, masked; the stage's maximum
-                float cm = -INFINITY;
+                // the exact path, 16 columns at a time (short loops: it runs
+                // at a piece's first stage, on the diagonal and where a
+                // maximum moves, its instructions mostly cold): the stage's
+                // masked maximum first, then P
+                const float4 *pf = reinterpret_cast<const float4 *>(c.smem + c.lay.pfactor + vs * kKT * 4);
+                const int shift = 31 - __clz(P);
+                // the scores of columns 16c .. 16c + 15, -inf where not visible
+                // (past this row's end, or on a page that was not copied)
+                auto columns = [&](int c16, float (&x16)[16]) {
+                    uint32_t raw[16];
+                    tmem_ld16_nowait(srow + (uint32_t)(c16 * 16), raw);
+                    tmem_wait_ld();
+                    const int n = alive && ((pmask >> ((c16 * 16) >> shift)) & 1u) ? nvis - c16 * 16 : 0;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    // bit i: column 32q + i is visible (before this row's end, on a copied page)
-                    const int n = alive ? min(max(nvis - q * 32, 0), 32) : 0;
-                    uint32_t vis = n >= 32 ? 0xffffffffu : ((1u << n) - 1u);
-                    uint32_t pages = 0u;
-                    for (int pg = 0; pg < 32 / P; ++pg)
-                        if ((pmask >> (q * (32 / P) + pg)) & 1u)
-                            pages |= (P >= 32 ? 0xffffffffu : ((1u << P) - 1u)) << (pg * P);
-                    vis &= pages;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 f = fac[q * 8 + i];
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 f = fac[c16 * 4 + i];
                         const float fs[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            const int col = 4 * i + v;
-                            const float s = ((vis >> col) & 1u) ? __uint_as_float(sv[q][col]) * (fs[v] * rq) : -INFINITY;
-                            sv[q][col] = __float_as_uint(s);
-                            cm = fmaxf(cm, s);
+                        for (int v = 0; v < 4; ++v)
+                            x16[4 * i + v] = 4 * i + v < n ? __uint_as_float(raw[4 * i + v]) * (fs[v] * rq) : -INFINITY;
+                    }
+                };
+                float cm = -INFINITY, cy = -INFINITY;
+#pragma unroll 1
+                for (int c16 = 0; c16 < kKT / 16; ++c16) {
+                    float x16[16];
+                    columns(c16, x16);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        cm = fmaxf(cm, x16[i]);
+                    if (wide) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 f = pf[c16 * 4 + i];
+                            cy = fmaxf(fmaxf(cy, fmaxf(x16[4 * i] + f.x, x16[4 * i + 1] + f.y)),
+                                       fmaxf(x16[4 * i + 2] + f.z, x16[4 * i + 3] + f.w));
                         }
                     }
                 }
@@ -676,19 +695,7 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                     lsum *= scale_o;
                     m_use = cm;
                 }
-                const float4 *pf = reinterpret_cast<const float4 *>(c.smem + c.lay.pfactor + vs * kKT * 4);
                 if (apart) {
-                    float cy = -INFINITY;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 f = pf[q * 8 + i];
-                            cy = fmaxf(fmaxf(cy, fmaxf(__uint_as_float(sv[q][4 * i]) + f.x,
-                                                       __uint_as_float(sv[q][4 * i + 1]) + f.y)),
-                                       fmaxf(__uint_as_float(sv[q][4 * i + 2]) + f.z,
-                                             __uint_as_float(sv[q][4 * i + 3]) + f.w));
-                        }
                     cy += (float)e;
                     scale_o = 1.f;
                     if (m2 == -INFINITY) {
@@ -721,28 +728,30 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                 const float mu = m_use == -INFINITY ? 0.f : m_use - kPLog2;
                 const float mu2 = m2 == -INFINITY ? 0.f : m2 - (float)e - kPLog2;
                 part = 0.f;
+#pragma unroll 1
+                for (int c16 = 0; c16 < kKT / 16; ++c16) {       // (P of columns 16c.. lies over columns 8c..)
+                    float x16[16];
+                    uint32_t pk[8];
+                    columns(c16, x16);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 4; ++i) {
                         float w[4];
 #pragma unroll
                         for (int v = 0; v < 4; ++v) {
-                            w[v] = ex2_approx(__uint_as_float(sv[q][4 * i + v]) - mu);
+                            w[v] = ex2_approx(x16[4 * i + v] - mu);
                             part += w[v];
                         }
                         if (apart) {
-                            const float4 f = pf[q * 8 + i];
-                            const float fs[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                            for (int v = 0; v < 4; ++v)
-                                w[v] = ex2_approx(__uint_as_float(sv[q][4 * i + v]) + fs[v] - mu2);
+                            const float4 f = pf[c16 * 4 + i];
+                            w[0] = ex2_approx(x16[4 * i] + f.x - mu2);
+                            w[1] = ex2_approx(x16[4 * i + 1] + f.y - mu2);
+                            w[2] = ex2_approx(x16[4 * i + 2] + f.z - mu2);
+                            w[3] = ex2_approx(x16[4 * i + 3] + f.w - mu2);
                         }
                         pk[2 * i] = pack_half2(w[0], w[1]);
                         pk[2 * i + 1] = pack_half2(w[2], w[3]);
                     }
-                    tmem_st16_nowait(srow + (uint32_t)(q * 16), pk);
+                    tmem_st8_nowait(srow + (uint32_t)(c16 * 8), pk);
                 }
             }
             lsum += part;
@@ -761,21 +770,23 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
             wait(pv_done(c, x), (uint32_t)((done - 1) & 1));
         if (alive && t.ntok[x] > 0) {
             tc_fence_after();
-            const float inv = lsum != 0.f ? __frcp_rn(lsum) : 0.f;       // (a NaN sum stays NaN)
-            const float ef = apart ? ex2_approx(m2 - m_use - (float)(kVLog2 + 127))
-                                   : q8_scale((uint32_t)e) * (1.f / (1 << kVLog2));
+            // (a NaN sum stays NaN; a tile with no stage here or no visible key gives zeros)
+            const float f = !any || lsum == 0.f ? 0.f
+                                                : __frcp_rn(lsum) * (apart ? ex2_approx(m2 - m_use - (float)(kVLog2 + 127))
+                                                                           : q8_scale((uint32_t)e) * (1.f / (1 << kVLog2)));
             const int64_t orr = tok * p.hq + head;
             const int slot = piece_slot(p, blockIdx.x, t.u);
             const int64_t prow = (int64_t)slot * kChunkRows + x * 128 + r;
 #pragma unroll 1
             for (int c16 = 0; c16 < D / 16; ++c16) {
-                uint32_t ov[16];
-                tmem_ld16_nowait(orow + (uint32_t)(c16 * 16), ov);
+                uint32_t ov[16] = {};
+                if (any)
+                    tmem_ld16_nowait(orow + (uint32_t)(c16 * 16), ov);
                 tmem_wait_ld();
                 float o[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    o[i] = any && lsum != 0.f ? __uint_as_float(ov[i]) * inv * ef : 0.f;
+                    o[i] = __uint_as_float(ov[i]) * f;
                 if (row_ok && whole) {
                     uint4 *dst = reinterpret_cast<uint4 *>(p.out + orr * D + c16 * 16);
 #pragma unroll
