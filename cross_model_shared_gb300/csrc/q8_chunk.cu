@@ -489,6 +489,13 @@ __device__ void chunk_pv(const Q8ChunkParams &p, const Ctx &c, uint32_t tmem)
 // ---------------------------------------------------------------------------
 // softmax warps of tile x: thread r = MMA row r = (new token i0 + r / G, head r % G)
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ float max3f(float a, float b, float c)
+{
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
 {
     const __half2 v = __floats2half2_rn(lo, hi);
@@ -514,29 +521,41 @@ __device__ __forceinline__ float stage_row(const Ctx &c, const __nv_bfloat16 *sr
     const float inv = __uint_as_float((uint32_t)(254 - byte) << 23);
     const bool bad = a >= 0x7f80u;                       // an infinity or a NaN: the row's scores are NaN
     uint8_t *dst = c.smem + c.lay.qtile + 2u * (uint32_t)x * kQTermBytes + (uint32_t)r * 128u;
-    uint4 next = src ? __ldg(s4) : zero;
+    uint4 next[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        next[i] = src ? __ldg(s4 + i) : zero;
 #pragma unroll 1
-    for (int ch = 0; ch < D / 8; ++ch) {
-        const uint4 v = next;
-        if (src && ch + 1 < D / 8)
-            next = __ldg(s4 + ch + 1);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t hi[4], lo[4];
+    for (int c4 = 0; c4 < D / 8; c4 += 4) {
+        uint4 v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 f = make_float2(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xffff0000u) * inv);
-            const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
-            const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
-            hi[i] = h;
-            lo[i] = __nv_cvt_float2_to_fp8x2(make_float2(f.x - hf.x, f.y - hf.y), __NV_SATFINITE, __NV_E4M3);
+            v[i] = next[i];
+            if (src && c4 + 4 < D / 8)
+                next[i] = __ldg(s4 + c4 + 4 + i);
         }
-        uint2 h2 = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-        uint2 l2 = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-        if (bad)
-            h2.x = h2.y = l2.x = l2.y = 0x7f7f7f7fu;
-        uint8_t *at = dst + (((ch >> 1) ^ (r & 7)) << 4) + (ch & 1) * 8;
-        *reinterpret_cast<uint2 *>(at) = h2;
-        *reinterpret_cast<uint2 *>(at + kQTermBytes) = l2;
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint4 q = v[j + (i >> 2)];
+                const uint32_t w = (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+                const float2 f = make_float2(__uint_as_float(w << 16) * inv, __uint_as_float(w & 0xffff0000u) * inv);
+                // (scaled values are exact in fp16 down to its subnormals, 2^-33 of the row's largest)
+                const __half2 f16 = __floats2half2_rn(f.x, f.y);
+                const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(f16, __NV_SATFINITE, __NV_E4M3);
+                const __half2 rest = __hsub2(f16, __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+                const __nv_fp8x2_storage_t l = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
+                hi[i >> 1] = (i & 1) ? hi[i >> 1] | ((uint32_t)h << 16) : h;
+                lo[i >> 1] = (i & 1) ? lo[i >> 1] | ((uint32_t)l << 16) : l;
+            }
+            const uint32_t off = (uint32_t)((((c4 + j) / 2) ^ (r & 7)) << 4);
+            const uint32_t n = 0x7f7f7f7fu;
+            *reinterpret_cast<uint4 *>(dst + off) = bad ? make_uint4(n, n, n, n) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(dst + kQTermBytes + off) =
+                bad ? make_uint4(n, n, n, n) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
     }
     return bad ? 1.f : q8_scale((uint32_t)byte);
 }
@@ -642,42 +661,45 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                 }
             }
             if (!fast) {
-                // the exact path, 16 columns at a time (short loops: it runs
+                // the exact path, 32 columns at a time (short loops: it runs
                 // at a piece's first stage, on the diagonal and where a
                 // maximum moves, its instructions mostly cold): the stage's
                 // masked maximum first, then P
                 const float4 *pf = reinterpret_cast<const float4 *>(c.smem + c.lay.pfactor + vs * kKT * 4);
                 const int shift = 31 - __clz(P);
-                // the scores of columns 16c .. 16c + 15, -inf where not visible
+                // the scores of columns 32c .. 32c + 31, -inf where not visible
                 // (past this row's end, or on a page that was not copied)
-                auto columns = [&](int c16, float (&x16)[16]) {
-                    uint32_t raw[16];
-                    tmem_ld16_nowait(srow + (uint32_t)(c16 * 16), raw);
+                auto columns = [&](int c32, float (&xs)[32]) {
+                    uint32_t raw[32];
+                    tmem_ld32_nowait(srow + (uint32_t)(c32 * 32), raw);
                     tmem_wait_ld();
-                    const int n = alive && ((pmask >> ((c16 * 16) >> shift)) & 1u) ? nvis - c16 * 16 : 0;
+                    const uint32_t first = (pmask >> ((c32 * 32) >> shift)) & 1u, second = (pmask >> ((c32 * 32 + 16) >> shift)) & 1u;
+                    const int n = alive ? nvis - c32 * 32 : 0;
+                    const int n0 = first ? n : 0, n1 = second ? n : 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 f = fac[c16 * 4 + i];
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 f = fac[c32 * 8 + i];
                         const float fs[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
                         for (int v = 0; v < 4; ++v)
-                            x16[4 * i + v] = 4 * i + v < n ? __uint_as_float(raw[4 * i + v]) * (fs[v] * rq) : -INFINITY;
+                            xs[4 * i + v] = 4 * i + v < (i < 4 ? n0 : n1) ? __uint_as_float(raw[4 * i + v]) * (fs[v] * rq)
+                                                                         : -INFINITY;
                     }
                 };
                 float cm = -INFINITY, cy = -INFINITY;
 #pragma unroll 1
-                for (int c16 = 0; c16 < kKT / 16; ++c16) {
-                    float x16[16];
-                    columns(c16, x16);
+                for (int c32 = 0; c32 < kKT / 32; ++c32) {
+                    float xs[32];
+                    columns(c32, xs);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        cm = fmaxf(cm, x16[i]);
+                    for (int i = 0; i < 32; i += 2)
+                        cm = max3f(cm, xs[i], xs[i + 1]);
                     if (wide) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float4 f = pf[c16 * 4 + i];
-                            cy = fmaxf(fmaxf(cy, fmaxf(x16[4 * i] + f.x, x16[4 * i + 1] + f.y)),
-                                       fmaxf(x16[4 * i + 2] + f.z, x16[4 * i + 3] + f.w));
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 f = pf[c32 * 8 + i];
+                            cy = max3f(max3f(cy, xs[4 * i] + f.x, xs[4 * i + 1] + f.y), xs[4 * i + 2] + f.z,
+                                       xs[4 * i + 3] + f.w);
                         }
                     }
                 }
@@ -727,32 +749,33 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                 }
                 const float mu = m_use == -INFINITY ? 0.f : m_use - kPLog2;
                 const float mu2 = m2 == -INFINITY ? 0.f : m2 - (float)e - kPLog2;
-                part = 0.f;
+                float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-                for (int c16 = 0; c16 < kKT / 16; ++c16) {       // (P of columns 16c.. lies over columns 8c..)
-                    float x16[16];
-                    uint32_t pk[8];
-                    columns(c16, x16);
+                for (int c32 = 0; c32 < kKT / 32; ++c32) {       // (P of columns 32c.. lies over columns 16c..)
+                    float xs[32];
+                    uint32_t pk[16];
+                    columns(c32, xs);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 8; ++i) {
                         float w[4];
 #pragma unroll
                         for (int v = 0; v < 4; ++v) {
-                            w[v] = ex2_approx(x16[4 * i + v] - mu);
-                            part += w[v];
+                            w[v] = ex2_approx(xs[4 * i + v] - mu);
+                            sums[v] += w[v];
                         }
                         if (apart) {
-                            const float4 f = pf[c16 * 4 + i];
-                            w[0] = ex2_approx(x16[4 * i] + f.x - mu2);
-                            w[1] = ex2_approx(x16[4 * i + 1] + f.y - mu2);
-                            w[2] = ex2_approx(x16[4 * i + 2] + f.z - mu2);
-                            w[3] = ex2_approx(x16[4 * i + 3] + f.w - mu2);
+                            const float4 f = pf[c32 * 8 + i];
+                            w[0] = ex2_approx(xs[4 * i] + f.x - mu2);
+                            w[1] = ex2_approx(xs[4 * i + 1] + f.y - mu2);
+                            w[2] = ex2_approx(xs[4 * i + 2] + f.z - mu2);
+                            w[3] = ex2_approx(xs[4 * i + 3] + f.w - mu2);
                         }
                         pk[2 * i] = pack_half2(w[0], w[1]);
                         pk[2 * i + 1] = pack_half2(w[2], w[3]);
                     }
-                    tmem_st8_nowait(srow + (uint32_t)(c16 * 8), pk);
+                    tmem_st16_nowait(srow + (uint32_t)(c32 * 16), pk);
                 }
+                part = (sums[0] + sums[1]) + (sums[2] + sums[3]);
             }
             lsum += part;
             tmem_wait_st();

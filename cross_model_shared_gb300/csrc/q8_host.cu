@@ -186,7 +186,7 @@ shkv_status launch_stacked(shkv_q8_pool *pool, const Q8AttnParams &a, int max_ro
 // costliest is as cheap as a greedy fill makes it (bisection over the bound).
 // In fifths of a stage of both tiles: a piece pays kPiece for its query rows,
 // the pipeline's fill and drain and its output, a stage 5 (3 with one tile).
-constexpr int64_t kPiece = 20, kPair = 5, kSingle = 3;
+constexpr int64_t kPiece = 30, kPair = 5, kSingle = 3;
 constexpr int64_t kMinPiece = 2;            // stages; smaller pieces are not cut off
 
 bool plan_chunks(Q8ChunkParams &p, int limit)
