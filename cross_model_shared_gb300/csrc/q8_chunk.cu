@@ -502,62 +502,72 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// This row of the query as two e4m3 terms in its tile; returns the row's
-// scale.  (Run once a piece: what counts is its instructions, fetched cold,
-// so the row is read twice by short loops instead of held by unrolled code.)
-__device__ __forceinline__ float stage_row(const Ctx &c, const __nv_bfloat16 *src, int D, int x, int r)
+// The warp's 32 rows of the query as two e4m3 terms in their tile; returns the
+// scale of this lane's row (a power of two).  src: this lane's row, null for a
+// padding row (zeros).  D / 8 neighbouring lanes take a row, 8 columns each,
+// and the raw row is copied to where its terms will lie (its 2 D bytes are
+// theirs): all 32 rows are in flight at once and no lane reads what another
+// copied.  A row a lane through registers, 8 loads in flight, took 10K cycles a
+// piece, four rows in flight by neighbouring lanes 15K.
+__device__ __forceinline__ float stage_rows(const Ctx &c, const __nv_bfloat16 *src, const __nv_bfloat16 *any, int D, int x,
+                                            int r0)
 {
-    const uint4 *s4 = reinterpret_cast<const uint4 *>(src);
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    uint32_t a = 0;
-#pragma unroll 8
-    for (int ch = 0; ch < D / 8; ++ch) {
-        const uint4 v = src ? __ldg(s4 + ch) : zero;
-        a = __vmaxu2(__vmaxu2(a, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)),
-                     __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-    }
-    a = max(a & 0xffffu, a >> 16);
-    const int byte = max((int)((a + 0x1fu) >> 7) - 8, 0);
-    const float inv = __uint_as_float((uint32_t)(254 - byte) << 23);
-    const bool bad = a >= 0x7f80u;                       // an infinity or a NaN: the row's scores are NaN
-    uint8_t *dst = c.smem + c.lay.qtile + 2u * (uint32_t)x * kQTermBytes + (uint32_t)r * 128u;
-    uint4 next[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        next[i] = src ? __ldg(s4 + i) : zero;
+    const int lane = threadIdx.x & 31;
+    const int shift = D == 64 ? 3 : 4;                   // log2 of a row's lanes
+    const int sub = lane & ((1 << shift) - 1), rsub = lane >> shift, rows = 32 >> shift;
+    const uint32_t tile = c.lay.qtile + 2u * (uint32_t)x * kQTermBytes;
+    // a row's columns 8 sub .. 8 sub + 7 in the first term's tile
+    auto place = [&](int row) { return tile + (uint32_t)(row * 128 + (((sub >> 1) ^ (row & 7)) << 4) + (sub & 1) * 8); };
 #pragma unroll 1
-    for (int c4 = 0; c4 < D / 8; c4 += 4) {
-        uint4 v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = next[i];
-            if (src && c4 + 4 < D / 8)
-                next[i] = __ldg(s4 + c4 + 4 + i);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint4 q = v[j + (i >> 2)];
-                const uint32_t w = (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
-                const float2 f = make_float2(__uint_as_float(w << 16) * inv, __uint_as_float(w & 0xffff0000u) * inv);
-                // (scaled values are exact in fp16 down to its subnormals, 2^-33 of the row's largest)
-                const __half2 f16 = __floats2half2_rn(f.x, f.y);
-                const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(f16, __NV_SATFINITE, __NV_E4M3);
-                const __half2 rest = __hsub2(f16, __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
-                const __nv_fp8x2_storage_t l = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
-                hi[i >> 1] = (i & 1) ? hi[i >> 1] | ((uint32_t)h << 16) : h;
-                lo[i >> 1] = (i & 1) ? lo[i >> 1] | ((uint32_t)l << 16) : l;
-            }
-            const uint32_t off = (uint32_t)((((c4 + j) / 2) ^ (r & 7)) << 4);
-            const uint32_t n = 0x7f7f7f7fu;
-            *reinterpret_cast<uint4 *>(dst + off) = bad ? make_uint4(n, n, n, n) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(dst + kQTermBytes + off) =
-                bad ? make_uint4(n, n, n, n) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
+    for (int i = 0; i < D / 8; ++i) {                    // `rows` rows at a time
+        const __nv_bfloat16 *row = reinterpret_cast<const __nv_bfloat16 *>(
+            __shfl_sync(0xffffffffu, (unsigned long long)src, i * rows + rsub));
+        const uint32_t bytes = row ? 8u : 0u;            // (0: zeros, and nothing is read)
+        const uint8_t *from = reinterpret_cast<const uint8_t *>((row ? row : any) + sub * 8);
+        const uint32_t to = c.base + place(r0 + i * rows + rsub);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + kQTermBytes), "l"(from + 8), "r"(bytes)
+                     : "memory");
     }
-    return bad ? 1.f : q8_scale((uint32_t)byte);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    int mine = 0;                                        // scale byte of this lane's row, 255: not finite
+#pragma unroll 2
+    for (int i = 0; i < D / 8; ++i) {
+        uint2 *const first = reinterpret_cast<uint2 *>(c.smem + place(r0 + i * rows + rsub));
+        uint2 *const second = reinterpret_cast<uint2 *>(reinterpret_cast<uint8_t *>(first) + kQTermBytes);
+        const uint2 v0 = *first, v1 = *second;
+        const uint32_t w[4] = {v0.x, v0.y, v1.x, v1.y};
+        uint32_t a = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                              __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+        a = max(a & 0xffffu, a >> 16);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1)
+            a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+        if (D != 64)
+            a = max(a, __shfl_xor_sync(0xffffffffu, a, 8));
+        const bool bad = a >= 0x7f80u;               // an infinity or a NaN: the row's scores are NaN
+        const int byte = bad ? 255 : max((int)((a + 0x1fu) >> 7) - 8, 0);
+        const float inv = __uint_as_float((uint32_t)(254 - min(byte, 253)) << 23);
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            // (scaled values are exact in fp16 down to its subnormals, 2^-33 of the row's largest)
+            const __half2 f16 = __floats2half2_rn(__uint_as_float(w[k] << 16) * inv,
+                                                  __uint_as_float(w[k] & 0xffff0000u) * inv);
+            const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(f16, __NV_SATFINITE, __NV_E4M3);
+            const __half2 rest = __hsub2(f16, __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+            const __nv_fp8x2_storage_t l = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
+            hi[k >> 1] = (k & 1) ? hi[k >> 1] | ((uint32_t)h << 16) : h;
+            lo[k >> 1] = (k & 1) ? lo[k >> 1] | ((uint32_t)l << 16) : l;
+        }
+        const uint32_t n = 0x7f7f7f7fu;
+        *first = bad ? make_uint2(n, n) : make_uint2(hi[0], hi[1]);
+        *second = bad ? make_uint2(n, n) : make_uint2(lo[0], lo[1]);
+        const int got = __shfl_sync(0xffffffffu, byte, (lane & (rows - 1)) << shift);
+        if ((lane >> (5 - shift)) == i)
+            mine = got;
+    }
+    return mine == 255 ? 1.f : q8_scale((uint32_t)mine);
 }
 
 __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tmem, int x)
@@ -589,7 +599,7 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
         if (seg > 0)
             wait(q_free(c), (uint32_t)((seg - 1) & 1));
         const __nv_bfloat16 *src = row_ok ? p.q + tok * p.q_stride + (int64_t)head * D : nullptr;
-        const float rq = stage_row(c, src, D, x, r);
+        const float rq = stage_rows(c, src, p.q, D, x, warp * 32);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0)
@@ -817,10 +827,12 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                         dst[v] = make_uint4(pack_bf16x2(o[8 * v], o[8 * v + 1]), pack_bf16x2(o[8 * v + 2], o[8 * v + 3]),
                                             pack_bf16x2(o[8 * v + 4], o[8 * v + 5]), pack_bf16x2(o[8 * v + 6], o[8 * v + 7]));
                 } else if (row_ok) {
-                    float4 *dst = reinterpret_cast<float4 *>(p.ws_part + prow * D + c16 * 16);
+                    // (four columns of all rows together: neighbouring lanes write neighbouring words)
+                    float4 *dst = reinterpret_cast<float4 *>(p.ws_part) +
+                                  (((int64_t)slot * 2 + x) * (D / 4) + c16 * 4) * 128 + r;
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
-                        dst[v] = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+                        dst[v * 128] = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
                 }
             }
             if (row_ok) {
@@ -913,10 +925,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the pieces of split units: a warp per row.  Block y takes the unit
-// that cut y (the start of CTA y + 1) falls inside, if it is the first cut in it.
+// The larger of two; NaN where one is.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// Joins the pieces of split units, 8 rows a block: thread = (row, four
+// columns), the rows of a column group neighbours as the pieces hold them.
+// Block y takes the unit that cut y (the start of CTA y + 1) falls inside, if
+// it is the first cut in it.
 __global__ void __launch_bounds__(256) shkv_q8_chunk_join_kernel(const __grid_constant__ Q8ChunkParams p)
 {
+    __shared__ float maxima[8][8];
     pdl_wait_prior();
     pdl_launch_dependents();
     const int cut = blockIdx.y + 1;
@@ -926,49 +949,53 @@ __global__ void __launch_bounds__(256) shkv_q8_chunk_join_kernel(const __grid_co
     Piece t;
     t.u = u;
     set_unit(p, t);
-    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int x = row >> 7, r = row & 127;
-    const int ti = r / p.group, tj = r - ti * p.group;
-    if (ti >= t.ntok[x])
+    const int x = blockIdx.x >> 4, r = (blockIdx.x & 15) * 8 + (threadIdx.x & 7), row = x * 128 + r;
+    if (((blockIdx.x & 15) * 8) / p.group >= t.ntok[x])  // the block's first row: none of its rows is in use
         return;
+    const int c4 = threadIdx.x >> 3, D = p.head_dim;
+    const int ti = r / p.group, tj = r - ti * p.group;
+    const bool row_ok = ti < t.ntok[x];
     int last = cut;                              // last CTA that holds a piece
     while (last + 1 < p.num_ctas && p.cut_unit[last + 1] == u && p.cut_stage[last + 1] > 0)
         ++last;
-    float M = -INFINITY;
-    bool nan = false;
-    for (int i = cut - 1 + lane; i <= last; i += 32) {
-        const float v = p.ws_lse[(int64_t)piece_slot(p, i, u) * kChunkRows + row];
-        nan = nan || v != v;
-        M = fmaxf(M, v);
+    float M = -INFINITY;                         // NaN as soon as a piece's log-sum-exp is
+    if (row_ok) {
+        for (int i = cut - 1 + c4; i <= last; i += 32)
+            M = max_nan(M, p.ws_lse[(int64_t)piece_slot(p, i, u) * kChunkRows + row]);
     }
-    nan = __any_sync(0xffffffffu, nan);
-    for (int o = 16; o > 0; o >>= 1)
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const int D = p.head_dim;
+    M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, 8));
+    M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, 16));
+    if ((threadIdx.x & 31) < 8)
+        maxima[threadIdx.x >> 5][threadIdx.x & 7] = M;
+    __syncthreads();
+    M = maxima[0][threadIdx.x & 7];
+#pragma unroll
+    for (int w = 1; w < 8; ++w)
+        M = max_nan(M, maxima[w][threadIdx.x & 7]);
+    if (!row_ok || c4 >= D / 4)
+        return;
     float wsum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (nan) {
-        wsum = acc.x = acc.y = acc.z = acc.w = __uint_as_float(0x7fc00000u);
+    if (M != M) {
+        wsum = acc.x = acc.y = acc.z = acc.w = M;
     } else if (M != -INFINITY) {
+#pragma unroll 2
         for (int i = cut - 1; i <= last; ++i) {
-            const int64_t pr = (int64_t)piece_slot(p, i, u) * kChunkRows + row;
-            const float w = ex2_approx((p.ws_lse[pr] - M) * 1.4426950408889634f);
+            const int64_t slot = piece_slot(p, i, u);
+            const float w = ex2_approx((p.ws_lse[slot * kChunkRows + row] - M) * 1.4426950408889634f);
+            const float4 v = reinterpret_cast<const float4 *>(p.ws_part)[((slot * 2 + x) * (D / 4) + c4) * 128 + r];
             wsum += w;
-            if (lane < D / 4) {
-                const float4 v = reinterpret_cast<const float4 *>(p.ws_part + pr * D)[lane];
-                acc.x += w * v.x;
-                acc.y += w * v.y;
-                acc.z += w * v.z;
-                acc.w += w * v.w;
-            }
+            acc.x += w * v.x;
+            acc.y += w * v.y;
+            acc.z += w * v.z;
+            acc.w += w * v.w;
         }
     }
     const float winv = wsum != 0.f ? 1.f / wsum : 0.f;
     const int64_t orr = ((int64_t)p.q0[t.b] + t.i0[x] + ti) * p.hq + (int64_t)t.g * p.group + tj;
-    if (lane < D / 4)
-        *reinterpret_cast<uint2 *>(p.out + orr * D + lane * 4) =
-            make_uint2(pack_bf16x2(acc.x * winv, acc.y * winv), pack_bf16x2(acc.z * winv, acc.w * winv));
-    if (lane == 0 && p.lse_out)
+    *reinterpret_cast<uint2 *>(p.out + orr * D + c4 * 4) =
+        make_uint2(pack_bf16x2(acc.x * winv, acc.y * winv), pack_bf16x2(acc.z * winv, acc.w * winv));
+    if (c4 == 0 && p.lse_out)
         p.lse_out[orr] = wsum != 0.f ? M + logf(wsum) : -INFINITY;
 }
 

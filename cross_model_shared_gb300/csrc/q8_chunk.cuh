@@ -25,7 +25,7 @@ struct Q8ChunkParams {
     const int32_t *block_table, *seq_lens;
     uint32_t *err;
     float *ws_lse;                   // [2 * CTAs, kChunkRows]
-    float *ws_part;                  // [2 * CTAs, kChunkRows, D]
+    float *ws_part;                  // [2 * CTAs, 2, D / 4, 128, 4]: four columns of a tile's rows together
     int32_t batch, hq, hkv, group, head_dim, page_size, max_pages, num_pages;
     int32_t tpt;                     // new tokens per tile
     int32_t num_ctas;
