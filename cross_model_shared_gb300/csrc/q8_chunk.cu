@@ -531,41 +531,57 @@ __device__ __forceinline__ float stage_rows(const Ctx &c, const __nv_bfloat16 *s
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     int mine = 0;                                        // scale byte of this lane's row, 255: not finite
-#pragma unroll 2
-    for (int i = 0; i < D / 8; ++i) {
-        uint2 *const first = reinterpret_cast<uint2 *>(c.smem + place(r0 + i * rows + rsub));
-        uint2 *const second = reinterpret_cast<uint2 *>(reinterpret_cast<uint8_t *>(first) + kQTermBytes);
-        const uint2 v0 = *first, v1 = *second;
-        const uint32_t w[4] = {v0.x, v0.y, v1.x, v1.y};
-        uint32_t a = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                              __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-        a = max(a & 0xffffu, a >> 16);
+#pragma unroll 1
+    for (int i0 = 0; i0 < D / 8; i0 += 4) {              // four at a time, their chains of shuffles and conversions side by side
+        uint8_t *to[4];
+        uint32_t w[4][4], a[4];
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1)
-            a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-        if (D != 64)
-            a = max(a, __shfl_xor_sync(0xffffffffu, a, 8));
-        const bool bad = a >= 0x7f80u;               // an infinity or a NaN: the row's scores are NaN
-        const int byte = bad ? 255 : max((int)((a + 0x1fu) >> 7) - 8, 0);
-        const float inv = __uint_as_float((uint32_t)(254 - min(byte, 253)) << 23);
-        uint32_t hi[2], lo[2];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            // (scaled values are exact in fp16 down to its subnormals, 2^-33 of the row's largest)
-            const __half2 f16 = __floats2half2_rn(__uint_as_float(w[k] << 16) * inv,
-                                                  __uint_as_float(w[k] & 0xffff0000u) * inv);
-            const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(f16, __NV_SATFINITE, __NV_E4M3);
-            const __half2 rest = __hsub2(f16, __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
-            const __nv_fp8x2_storage_t l = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
-            hi[k >> 1] = (k & 1) ? hi[k >> 1] | ((uint32_t)h << 16) : h;
-            lo[k >> 1] = (k & 1) ? lo[k >> 1] | ((uint32_t)l << 16) : l;
+        for (int i = 0; i < 4; ++i) {
+            to[i] = c.smem + place(r0 + (i0 + i) * rows + rsub);
+            const uint2 v0 = *reinterpret_cast<const uint2 *>(to[i]), v1 = *reinterpret_cast<const uint2 *>(to[i] + kQTermBytes);
+            w[i][0] = v0.x;
+            w[i][1] = v0.y;
+            w[i][2] = v1.x;
+            w[i][3] = v1.y;
+            const uint32_t m = __vmaxu2(__vmaxu2(v0.x & 0x7fff7fffu, v0.y & 0x7fff7fffu),
+                                        __vmaxu2(v1.x & 0x7fff7fffu, v1.y & 0x7fff7fffu));
+            a[i] = max(m & 0xffffu, m >> 16);
         }
-        const uint32_t n = 0x7f7f7f7fu;
-        *first = bad ? make_uint2(n, n) : make_uint2(hi[0], hi[1]);
-        *second = bad ? make_uint2(n, n) : make_uint2(lo[0], lo[1]);
-        const int got = __shfl_sync(0xffffffffu, byte, (lane & (rows - 1)) << shift);
-        if ((lane >> (5 - shift)) == i)
-            mine = got;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                a[i] = max(a[i], __shfl_xor_sync(0xffffffffu, a[i], o));
+        }
+        if (D != 64) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                a[i] = max(a[i], __shfl_xor_sync(0xffffffffu, a[i], 8));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool bad = a[i] >= 0x7f80u;            // an infinity or a NaN: the row's scores are NaN
+            const int byte = bad ? 255 : max((int)((a[i] + 0x1fu) >> 7) - 8, 0);
+            const float inv = __uint_as_float((uint32_t)(254 - min(byte, 253)) << 23);
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                // (scaled values are exact in fp16 down to its subnormals, 2^-33 of the row's largest)
+                const __half2 f16 = __floats2half2_rn(__uint_as_float(w[i][k] << 16) * inv,
+                                                      __uint_as_float(w[i][k] & 0xffff0000u) * inv);
+                const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(f16, __NV_SATFINITE, __NV_E4M3);
+                const __half2 rest = __hsub2(f16, __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+                const __nv_fp8x2_storage_t l = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
+                hi[k >> 1] = (k & 1) ? hi[k >> 1] | ((uint32_t)h << 16) : h;
+                lo[k >> 1] = (k & 1) ? lo[k >> 1] | ((uint32_t)l << 16) : l;
+            }
+            const uint32_t n = 0x7f7f7f7fu;
+            *reinterpret_cast<uint2 *>(to[i]) = bad ? make_uint2(n, n) : make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2 *>(to[i] + kQTermBytes) = bad ? make_uint2(n, n) : make_uint2(lo[0], lo[1]);
+            const int got = __shfl_sync(0xffffffffu, byte, (lane & (rows - 1)) << shift);
+            if ((lane >> (5 - shift)) == i0 + i)
+                mine = got;
+        }
     }
     return mine == 255 ? 1.f : q8_scale((uint32_t)mine);
 }
