@@ -250,12 +250,26 @@ __device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t w)
 // ---------------------------------------------------------------------------
 // Stage j of a segment is the 128 tokens from p0*P + j*128.  One lane copies
 // one page (a box of P rows x 128 bytes; at head_dim 64 the box's upper half
-// is outside the tensor and filled with zeros).  The K warp also copies each
-// page's 2P scale bytes and publishes the stage's validity word, on barriers
-// of a ring of their own, so that they wait for no V slot.  The K warp writes
+// is outside the tensor and filled with zeros).  The K warp also copies the
+// pages' scale bytes, with one 16-byte asynchronous copy a lane (a bulk copy a
+// page took as long to issue as the codes, 600 cycles a stage of 16-token
+// pages, and this warp then bounded long contexts), and publishes the stage's
+// validity word, on barriers of a ring of their own, so that they wait for no
+// V slot.  The K warp writes
 // entry k once QK(k - KS) is complete, and QK(i) waits for the factors that
 // the V conversion's warps take from the scales of stage i: entries up to
 // k - KS are free.
+__device__ __forceinline__ void cp_async16(uint32_t to, const void *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
+// One arrival on the barrier once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 template <int NR, bool kIsK>
 __device__ void producer_q8(const CUtensorMap *tm, const Q8DecodeParams &q, const Ctx4 &c)
 {
@@ -263,7 +277,7 @@ __device__ void producer_q8(const CUtensorMap *tm, const Q8DecodeParams &q, cons
     constexpr int kSlots = kIsK ? kKS : kVS;
     const DecodeParams &p = q.d;
     const int lane = threadIdx.x & 31;
-    const int P = p.page_size, RB = kTT / P;
+    const int P = p.page_size, RB = kTT / P, log2P = 31 - __clz(P);
     const uint64_t pol = l2_evict_first_policy();
     if (lane == 0)
         prefetch_tensormap(tm);
@@ -332,7 +346,7 @@ __device__ void producer_q8(const CUtensorMap *tm, const Q8DecodeParams &q, cons
                 if (kIsK) {
                     reinterpret_cast<volatile uint32_t *>(c.smem + L.meta)[k % kScaleRing] =
                         mask | ((uint32_t)k << 8);       // valid pages + stage tag
-                    mbar_arrive_expect_tx(sbar, 2u * rows);
+                    mbar_arrive(sbar);
                 }
                 mbar_arrive_expect_tx(bar, 128u * rows);
             }
@@ -342,9 +356,17 @@ __device__ void producer_q8(const CUtensorMap *tm, const Q8DecodeParams &q, cons
                 const uint32_t dst = c.base + (kIsK ? (uint32_t)ring.slot * kKSlotBytes
                                                     : L.vring + (uint32_t)ring.slot * kVSlotBytes + kTT * 128u);
                 tma_load_2d(dst + (uint32_t)(lane * P) * 128u, tm, 0, unit * P, bar, pol);
-                if (kIsK)
-                    bulk_load(c.base + L.scales + (uint32_t)((k % kScaleRing) * 2 * kTT + lane * 2 * P),
-                              q.scales + (int64_t)unit * 2 * P, 2u * (uint32_t)P, sbar);
+            }
+            if (kIsK) {
+                // 16 bytes a lane, P / 8 lanes a page
+                const int page = (lane << 3) >> log2P, in = lane & (P / 8 - 1);
+                const int pid = __shfl_sync(0xffffffffu, id, page & 31);
+                if (alive) {
+                    if (page < RB && ((mask >> page) & 1u))
+                        cp_async16(c.base + L.scales + (uint32_t)((k % kScaleRing) * 2 * kTT + lane * 16),
+                                   q.scales + ((int64_t)pid * p.hkv + s.g) * 2 * P + in * 16);
+                    cp_async_arrive(sbar);
+                }
             }
             __syncwarp();
             if (alive) {
@@ -365,13 +387,11 @@ __device__ void producer_q8(const CUtensorMap *tm, const Q8DecodeParams &q, cons
     if (!alive && lane == 0) {
         for (int i = max(0, k - kSlots); i < k; ++i)
             mbar_drain_bounded(bar_at(c, (kIsK ? kFullK : kFullV) + i % kSlots), (uint32_t)((i / kSlots) & 1));
-        if (kIsK) {
-            for (int i = max(0, k - kScaleRing); i < k; ++i)
-                mbar_drain_bounded(bar_at(c, kScaleB + i % kScaleRing), (uint32_t)((i / kScaleRing) & 1));
-            if (q_issued >= 0)
-                mbar_drain_bounded(bar_at(c, kQFull), (uint32_t)(q_issued & 1));
-        }
+        if (kIsK && q_issued >= 0)
+            mbar_drain_bounded(bar_at(c, kQFull), (uint32_t)(q_issued & 1));
     }
+    if (kIsK)
+        asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Before the previous grid is waited for: L2 prefetch of the CTA's first
@@ -388,13 +408,38 @@ __device__ void warm_l2_q8(const CUtensorMap *tm, const DecodeParams &p, const C
     }
 }
 
+// What a token brings to the softmax: (score factor, V exponent, factor of l,
+// first row that sees it | kMasked if some token of the warp is not seen by all
+// | kNoValue if its V counts as zero | E << 16).  sc: the token's K scale byte,
+// V's is P further on; at: its distance from the first key some row does not
+// see; e: E with the token's stage.  A NaN row of V makes its key's scores NaN,
+// so that only rows that attend it see it.
+constexpr int kMasked = 0x100, kNoValue = 0x200;
+__device__ __forceinline__ float4 token_factors(const DecodeParams &p, const uint8_t *sc, bool valid, int at, int e)
+{
+    const int kb = *(const volatile uint8_t *)sc, vb = *(const volatile uint8_t *)(sc + p.page_size);
+    const int ve = !valid || vb == 255 ? e : max(vb, e - kVWindow);
+    // rows from row_min on see the token (new token i from position L - n + i on)
+    const int row_min = valid ? min(64, max(0, (at + 1) * p.group)) : 64;
+    const int flags = (__any_sync(0xffffffffu, row_min > 0) ? kMasked : 0) | (ve > vb ? kNoValue : 0);
+    float4 f;
+    f.x = !valid ? 0.f : vb == 255 ? __uint_as_float(0x7fc00000u) : q8_scale((uint32_t)kb) * p.scale_log2;
+    f.y = (float)(ve - 127);
+    f.z = __uint_as_float((uint32_t)max(127 + e - ve, 1) << 23);
+    f.w = __int_as_float(row_min | flags | (e << 16));
+    return f;
+}
+
 // ---------------------------------------------------------------------------
 // V conversion
 // ---------------------------------------------------------------------------
+// Every code becomes fp16, whatever its token: the bits give finite values, and
+// where a token is not seen or its V counts as zero P is 0.
 template <int NR>
 __device__ void convert_v(const Q8DecodeParams &q, const Ctx4 &c)
 {
     constexpr Smem L = smem_layout(NR);
+    constexpr bool kPing = q_pingpong(NR);
     const DecodeParams &p = q.d;
     const int t = threadIdx.x - kConvWarp0 * 32, lane = t & 31;
     const int P = p.page_size, log2P = 31 - __clz(P);
@@ -421,40 +466,32 @@ __device__ void convert_v(const Q8DecodeParams &q, const Ctx4 &c)
         int e = kMinE;                                   // scale byte of E
 #pragma unroll 1
         for (int tok0 = s.p0 * P; tok0 < tok_end; tok0 += kTT, ++k) {
-            // --- the token's factors.  (Entry k % kInfo was last used by stage
-            // k - kVS - 1, whose PV was done before V(k - 1) was loaded.)
-            const uint32_t entry = k % kInfo;
-            wait(bar_at(c, kScaleB + sring.slot), sring.par);
-            const uint32_t tagged = alive ? meta[sring.slot] : 0u;
-            if (alive && (tagged >> 8) != (k & 0xffffffu)) {
-                if (lane == 0) {
-                    atomicOr(p.err, SHKV_ERRF_PIPELINE);
-                    *c.abort_flag = 1u;
+            if (!kPing) {
+                // --- E and the token's factors (up to 32 rows the softmax's warps
+                // have the time to find them).  (Entry k % kInfo was last used by
+                // stage k - kVS - 1, whose PV was done before V(k - 1) was loaded.)
+                const uint32_t entry = k % kInfo;
+                wait(bar_at(c, kScaleB + sring.slot), sring.par);
+                const uint32_t tagged = alive ? meta[sring.slot] : 0u;
+                if (alive && (tagged >> 8) != (k & 0xffffffu)) {
+                    if (lane == 0) {
+                        atomicOr(p.err, SHKV_ERRF_PIPELINE);
+                        *c.abort_flag = 1u;
+                    }
+                    alive = false;
                 }
-                alive = false;
+                const uint32_t mask = tagged & 0xffu;
+                const int so = sring.slot * 2 * kTT;
+                e = next_e(e, stage_top_scale(sc_four + so, min(lim, all_see) - tok0, mask, log2P));
+                const bool valid = alive && tok0 + t < lim && ((mask >> page) & 1u);
+                const float4 f = token_factors(p, sc_mine + so, valid, tok0 + t - all_see, e);
+                if (alive)
+                    reinterpret_cast<float4 *>(c.smem + L.info)[entry * kTT + t] = f;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar_at(c, kInfoB + (int)entry));
+                sring.next();
             }
-            const uint32_t mask = tagged & 0xffu;
-            const int so = sring.slot * 2 * kTT;
-            const int kb = *(const volatile uint8_t *)(sc_mine + so), vb = *(const volatile uint8_t *)(sc_mine + so + P);
-            e = next_e(e, stage_top_scale(sc_four + so, min(lim, all_see) - tok0, mask, log2P));
-            const bool valid = alive && tok0 + t < lim && ((mask >> page) & 1u);
-            // a NaN row of V counts as zero and makes its key's scores NaN
-            // instead, so that only rows that attend it see it
-            const bool live = valid && vb != 255 && vb >= e - kVWindow;
-            const int ve = !valid || vb == 255 ? e : max(vb, e - kVWindow);
-            // rows from row_min on see the token (new token i from position L - n + i on)
-            const int row_min = valid ? min(64, max(0, (tok0 + t - all_see + 1) * p.group)) : 64;
-            const uint32_t masked = __any_sync(0xffffffffu, row_min > 0);
-            float4 f;
-            f.x = !valid ? 0.f : vb == 255 ? __uint_as_float(0x7fc00000u) : q8_scale((uint32_t)kb) * p.scale_log2;
-            f.y = (float)(ve - 127);
-            f.z = __uint_as_float((uint32_t)max(127 + e - ve, 1) << 23);
-            f.w = __int_as_float(row_min | (int)(masked << 8) | (e << 16));
-            if (alive)
-                reinterpret_cast<float4 *>(c.smem + L.info)[entry * kTT + t] = f;
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bar_at(c, kInfoB + (int)entry));
             // --- V
             wait(bar_at(c, kFullV + vring.slot), vring.par);
             if (alive) {
@@ -462,8 +499,7 @@ __device__ void convert_v(const Q8DecodeParams &q, const Ctx4 &c)
                 uint4 raw[8];
 #pragma unroll
                 for (int ch = 0; ch < 8; ++ch)
-                    raw[ch] = live ? *reinterpret_cast<const uint4 *>(row + kTT * 128 + ((ch ^ (t & 7)) << 4))
-                                   : make_uint4(0u, 0u, 0u, 0u);
+                    raw[ch] = *reinterpret_cast<const uint4 *>(row + kTT * 128 + ((ch ^ (t & 7)) << 4));
 #pragma unroll
                 for (int ch = 0; ch < 8; ++ch) {
                     uint8_t *dst = row + (ch >> 2) * (kTT * 128);
@@ -480,7 +516,6 @@ __device__ void convert_v(const Q8DecodeParams &q, const Ctx4 &c)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bar_at(c, kConvV + vring.slot));
-            sring.next();
             vring.next();
         }
         if (s.seg_end >= c.cta_end)
@@ -496,6 +531,7 @@ template <int NR>
 __device__ void qk_issuer(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem)
 {
     constexpr Smem L = smem_layout(NR);
+    constexpr bool kPing = q_pingpong(NR);
     constexpr uint32_t idesc = idesc_of(128, NR, false, false);
     const DecodeParams &p = q.d;
     const int steps = q.head_dim / 32;                   // 32 codes an MMA
@@ -519,9 +555,11 @@ __device__ void qk_issuer(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem)
             const uint32_t buf = k & 1u;
             const uint64_t kd = kd0 + (uint64_t)(((uint32_t)ring.slot * kKSlotBytes) >> 4);
             wait(bar_at(c, kFullK + ring.slot), ring.par);
-            wait(bar_at(c, kInfoB + (int)(k % kInfo)), (k / kInfo) & 1u);
+            if (!kPing)
+                wait(bar_at(c, kInfoB + (int)(k % kInfo)), (k / kInfo) & 1u);
             wait(bar_at(c, kSFree + (int)buf), ((k >> 1) & 1u) ^ 1u);
-            mbar_arrive(bar_at(c, kSFull + (int)buf));   // passes the factors on to the softmax
+            if (!kPing)
+                mbar_arrive(bar_at(c, kSFull + (int)buf));   // passes the factors on to the softmax
             if (alive) {
                 tc_fence_after();
                 const uint32_t d = tmem + kColS + buf * 64u;
@@ -606,8 +644,10 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
     const int tg = warp & (kTokenGroups - 1), hh = warp / kTokenGroups;
     const int grp = kPing ? hh : 0;            // whose maxima, sums, P and O
     const int t = tg * 32 + lane;
-    const int P = p.page_size;
+    const int P = p.page_size, log2P = 31 - __clz(P);
     const int D = q.head_dim;
+    const volatile uint32_t *meta = reinterpret_cast<const volatile uint32_t *>(c.smem + L.meta);
+    const uint8_t *sc_four = c.smem + L.scales + scale_off(4 * lane, log2P) + P;
     const uint32_t lane_base = (uint32_t)(tg * 32) << 16;
     const uint32_t bar_id = 1u + (uint32_t)grp, bar_threads = kPing ? 128u : 256u;
     constexpr uint32_t kAllBar = 3;            // both groups
@@ -706,16 +746,43 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
 
         // this group's first stage of the segment
         const int j0 = kPing ? (kbase ^ grp) & 1 : 0;
+        const int tok_first = s.p0 * P, lim = min(plan_len(p, s), s.p1 * P), all_see = keys_all_see(q, s);
+        uint32_t mask = 0;
 #pragma unroll 1
         for (int j = j0; j < nst; j += kPing ? 2 : 1) {
             const int k = kbase + j, buf = k & 1;
-            // S^T and the token's factors
+            // the token's factors and S^T
+            float4 f;
+            if (kPing) {
+                // (E moves with the other group's stages too)
+                auto top = [&](int i) {
+                    const int slot = (kbase + i) % kScaleRing;
+                    wait(bar_at(c, kScaleB + slot), (uint32_t)((kbase + i) / kScaleRing) & 1u);
+                    mask = meta[slot];
+                    if (alive && (mask >> 8) != ((uint32_t)(kbase + i) & 0xffffffu)) {
+                        if (lane == 0) {
+                            atomicOr(p.err, SHKV_ERRF_PIPELINE);
+                            *c.abort_flag = 1u;
+                        }
+                        alive = false;
+                    }
+                    return stage_top_scale(sc_four + slot * 2 * kTT, min(lim, all_see) - tok_first - i * kTT, mask, log2P);
+                };
+                int e_now = e;
+                if (j > 0)
+                    e_now = next_e(e_now, top(j - 1));
+                e_now = next_e(e_now, top(j));
+                const int tok = tok_first + j * kTT + t;
+                f = token_factors(p, c.smem + L.scales + (k % kScaleRing) * 2 * kTT + scale_off(t, log2P),
+                                  tok < lim && ((mask >> (t >> log2P)) & 1u), tok - all_see, e_now);
+            }
             if (wait(bar_at(c, kSFull + buf), (uint32_t)((k >> 1) & 1)))
                 tc_fence_after();
-            const float4 f = reinterpret_cast<const float4 *>(c.smem + L.info)[(k % kInfo) * kTT + t];
-            const int w4 = alive ? __float_as_int(f.w) : 64 | 1 << 8 | e << 16;
+            if (!kPing)
+                f = reinterpret_cast<const float4 *>(c.smem + L.info)[(k % kInfo) * kTT + t];
+            const int w4 = alive ? __float_as_int(f.w) : 64 | kMasked | e << 16;
             const int row_min = w4 & 0xff;
-            const bool masked = (w4 & 0x100) != 0;       // for some token of the warp
+            const bool masked = (w4 & kMasked) != 0;     // for some token of the warp
             const int de = (w4 >> 16) - e;
             e = w4 >> 16;
             // y - m + 7 of this thread's rows (nm = 7 - m), -inf where not seen
@@ -827,6 +894,10 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                 l[i] = __ffma2_rn(pe, make_float2(f.z, f.z), l[i]);
                 pk[i] = pack_half2(pe.x, pe.y);
             }
+            if (w4 & kNoValue)
+#pragma unroll
+                for (int i = 0; i < NH / 2; ++i)
+                    pk[i] = 0u;
             // --- P^T, once the group's previous product has read the buffer
             if (k >= (kPing ? 2 : 1))
                 wait(bar_at(c, kPvDone + grp), (uint32_t)(((kPing ? k >> 1 : k) - 1) & 1));
@@ -1080,10 +1151,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 n = kConvWarps;
             else if (i >= kPFull && i < kPvDone || i >= kSFree && i < kQReady)
                 n = kStageWarps;
+            else if (i >= kScaleB && i < kInfoB)
+                n = 33;                      // the K warp's lanes' copies and the validity word
             else if (i == kQEmpty || i == kQReady)
                 n = kSoftmaxWarps;
-            else if (i >= kSFull && i < kSFree || i == kFin)
-                n = 2;                       // the QK issuer and its commit; one commit per issuer
+            else if (i >= kSFull && i < kSFree)
+                n = q_pingpong(NR) ? 1 : 2;  // the QK's commit, and its issuer where it passes factors on
+            else if (i == kFin)
+                n = 2;                       // one commit per issuer
             mbar_init(bar_at(c, i), n);
         }
         *c.abort_flag = 0u;
