@@ -63,4 +63,12 @@ __device__ __forceinline__ float q8_scale(uint32_t byte)
     return __uint_as_float(byte << 23 | (byte == 0u || byte == 255u ? 1u << 22 : 0u));
 }
 
+// The larger of two; NaN where one is.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
 }  // namespace shkv

@@ -941,14 +941,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_dealloc(tmem, kTmemCols);
 }
 
-// The larger of two; NaN where one is.
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-    return y;
-}
-
 // Joins the pieces of split units, 8 rows a block: thread = (row, four
 // columns), the rows of a column group neighbours as the pieces hold them.
 // Block y takes the unit that cut y (the start of CTA y + 1) falls inside, if

@@ -638,6 +638,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
     constexpr bool kPing = q_pingpong(NR);
     constexpr int NH = kPing ? NR : NR / 2;    // rows per thread of a stage
     constexpr int NE = NR / 2;                 // rows per thread at the segment's end
+    constexpr int kMerge = NR == 16 ? 1 : 4;   // rows a warp merges at a time
     constexpr Smem L = smem_layout(NR);
     const DecodeParams &p = q.d;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1029,74 +1030,120 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
         tc_fence_before();
         named_barrier(kAllBar, kSoftmaxThreads);
 
-        // --- split unit: the last piece to arrive merges all pieces
-        if (!whole) {
-            const int cb = cta_of(p, s.unit_begin);
-            const int ce = cta_of(p, s.unit_end - 1);
-            uint32_t *counter = p.ws_count + (int64_t)s.b * p.hkv + s.g;
-            if (threadIdx.x == 0) {
-                __threadfence();
-                const uint32_t prev = atomicAdd(counter, 1u);
-                *c.bcast = (prev == (uint32_t)(ce - cb)) ? 1u : 0u;
-            }
-            named_barrier(kAllBar, kSoftmaxThreads);
-            if (*c.bcast) {
-                __threadfence();
-                const int dq = D / 4;
-#pragma unroll 1
-                for (int rr = warp; rr < R; rr += kSoftmaxWarps) {
-                    float M = -INFINITY;
-                    for (int cc = cb + lane; cc <= ce; cc += 32) {
-                        const float x = __ldcg(p.ws_lse + (int64_t)piece_slot(p, cc, s.unit_begin) * p.rows + rr);
-                        M = x != x ? x : fmaxf(M, x);
-                    }
-                    const bool nan = __any_sync(0xffffffffu, M != M);
-#pragma unroll
-                    for (int o_ = 16; o_ > 0; o_ >>= 1)
-                        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o_));
-                    float wsum = 0.f;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (nan) {
-                        wsum = acc.x = acc.y = acc.z = acc.w = __uint_as_float(0x7fc00000u);
-                    } else if (M != -INFINITY) {
-#pragma unroll 2
-                        for (int cc = cb; cc <= ce; ++cc) {
-                            const int sl = piece_slot(p, cc, s.unit_begin);
-                            const float w = ex2_approx((__ldcg(p.ws_lse + (int64_t)sl * p.rows + rr) - M) *
-                                                       1.4426950408889634f);
-                            wsum += w;
-                            if (lane < dq) {
-                                const float4 v = __ldcg(
-                                    reinterpret_cast<const float4 *>(p.ws_part + ((int64_t)sl * p.rows + rr) * D) + lane);
-                                acc.x += w * v.x;
-                                acc.y += w * v.y;
-                                acc.z += w * v.z;
-                                acc.w += w * v.w;
-                            }
-                        }
-                    }
-                    const float winv = wsum != 0.f ? 1.f / wsum : 0.f;
-                    const int64_t orr = row0 + rowoff[rr];
-                    if (lane < dq) {
-                        uint2 packed;
-                        packed.x = pack_bf16x2(acc.x * winv, acc.y * winv);
-                        packed.y = pack_bf16x2(acc.z * winv, acc.w * winv);
-                        *reinterpret_cast<uint2 *>(p.out + orr * D + lane * 4) = packed;
-                    }
-                    if (lane == 0 && p.lse_out)
-                        p.lse_out[orr] = wsum != 0.f ? M + logf(wsum) : -INFINITY;
-                }
-                if (threadIdx.x == 0)
-                    *counter = 0u;
-            }
-            named_barrier(kAllBar, kSoftmaxThreads);
-        }
-
         kbase += nst;
         ++seg;
         if (!has_next)
             break;
         s = sn;
+    }
+
+    // --- split units: the last piece to arrive merges all pieces.  A CTA's
+    // first and last segments can be pieces; both arrive here, after the last,
+    // under one fence (3.5K cycles, which the first would pay alone before the
+    // next segment's stages).
+    const Segment first = locate(p, c.cta_begin, c.cta_end);
+    const bool split[2] = {seg > 1 && first.seg_begin != first.unit_begin,
+                           s.seg_begin != s.unit_begin || s.seg_end != s.unit_end};
+    if (!split[0] && !split[1])
+        return;
+    if (threadIdx.x == 0) {
+        uint32_t before[2] = {0u, 0u}, last = 0u;
+        __threadfence();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (split[i])
+                before[i] = atomicAdd(p.ws_count + (int64_t)(i ? s.b : first.b) * p.hkv + (i ? s.g : first.g), 1u);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const Segment &u = i ? s : first;
+            if (split[i] && before[i] == (uint32_t)(cta_of(p, u.unit_end - 1) - cta_of(p, u.unit_begin)))
+                last |= 1u << i;
+        }
+        *c.bcast = last;
+    }
+    named_barrier(kAllBar, kSoftmaxThreads);
+    const uint32_t mine_last = *c.bcast;
+    if (mine_last)
+        __threadfence();
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        if (!((mine_last >> i) & 1u))
+            continue;
+        const int b = i ? s.b : first.b, g = i ? s.g : first.g;
+        const int64_t unit_begin = i ? s.unit_begin : first.unit_begin;
+        const int cb = cta_of(p, unit_begin), ce = cta_of(p, (i ? s.unit_end : first.unit_end) - 1);
+        const int R = q.n_q[b] * p.group, dq = D / 4;
+        const int64_t row0 = (int64_t)q.q0[b] * p.hq + (int64_t)g * p.group;
+        const int *rowoff = scr_i + kScrOff * 64;
+        // kMerge rows of a warp at a time: their loads in flight together (one
+        // row at a time, 32 rows took 6 us)
+#pragma unroll 1
+        for (int r0 = warp; r0 < R; r0 += kMerge * kSoftmaxWarps) {
+            float M[kMerge];                             // NaN as soon as a piece's log-sum-exp is
+#pragma unroll
+            for (int m = 0; m < kMerge; ++m)
+                M[m] = -INFINITY;
+#pragma unroll 1
+            for (int cc = cb + lane; cc <= ce; cc += 32) {
+                const float *lse = p.ws_lse + (int64_t)piece_slot(p, cc, unit_begin) * p.rows;
+#pragma unroll
+                for (int m = 0; m < kMerge; ++m)
+                    if (r0 + m * kSoftmaxWarps < R)
+                        M[m] = max_nan(M[m], __ldcg(lse + r0 + m * kSoftmaxWarps));
+            }
+#pragma unroll
+            for (int o_ = 16; o_ > 0; o_ >>= 1)
+#pragma unroll
+                for (int m = 0; m < kMerge; ++m)
+                    M[m] = max_nan(M[m], __shfl_xor_sync(0xffffffffu, M[m], o_));
+            float wsum[kMerge];
+            float4 acc[kMerge];
+#pragma unroll
+            for (int m = 0; m < kMerge; ++m) {
+                wsum[m] = 0.f;
+                acc[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll 1
+            for (int cc = cb; cc <= ce; ++cc) {
+                const int64_t pr = (int64_t)piece_slot(p, cc, unit_begin) * p.rows + r0;
+                float x[kMerge];
+                float4 v[kMerge];
+#pragma unroll
+                for (int m = 0; m < kMerge; ++m) {
+                    const bool in = r0 + m * kSoftmaxWarps < R;
+                    x[m] = in ? __ldcg(p.ws_lse + pr + m * kSoftmaxWarps) : -INFINITY;
+                    v[m] = in && lane < dq
+                                ? __ldcg(reinterpret_cast<const float4 *>(p.ws_part + (pr + m * kSoftmaxWarps) * D) + lane)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+                for (int m = 0; m < kMerge; ++m) {
+                    // (no piece has a key the row sees: weights of 0)
+                    const float w = M[m] == -INFINITY ? 0.f : ex2_approx((x[m] - M[m]) * 1.4426950408889634f);
+                    wsum[m] += w;
+                    acc[m].x += w * v[m].x;
+                    acc[m].y += w * v[m].y;
+                    acc[m].z += w * v[m].z;
+                    acc[m].w += w * v[m].w;
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < kMerge; ++m) {
+                const int rr = r0 + m * kSoftmaxWarps;
+                if (rr >= R)
+                    continue;
+                const float winv = wsum[m] != 0.f ? 1.f / wsum[m] : 0.f;
+                const int64_t orr = row0 + rowoff[rr];
+                if (lane < dq)
+                    *reinterpret_cast<uint2 *>(p.out + orr * D + lane * 4) =
+                        make_uint2(pack_bf16x2(acc[m].x * winv, acc[m].y * winv),
+                                   pack_bf16x2(acc[m].z * winv, acc[m].w * winv));
+                if (lane == 0 && p.lse_out)
+                    p.lse_out[orr] = wsum[m] != 0.f ? M[m] + logf(wsum[m]) : -INFINITY;
+            }
+        }
+        if (threadIdx.x == 0)
+            p.ws_count[(int64_t)b * p.hkv + g] = 0u;
     }
 }
 
