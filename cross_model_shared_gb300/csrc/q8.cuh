@@ -38,7 +38,7 @@ struct Q8CacheParams {
     int32_t old_len[SHKV_MAX_BATCH]; // host copy of the lengths before the call
 };
 
-// Kernel parameters of attention.  Request b has n_q[b] query tokens (the
+// An attention call, before its requests are dealt to the kernels.  Request b has n_q[b] query tokens (the
 // decoders of a decode step, or the new tokens of a chunk) from packed query
 // token q0[b] on; row r = i * G + j of a (request, KV head g) is query token
 // i, head g * G + j.
@@ -47,7 +47,7 @@ struct Q8AttnParams {
     int64_t q_stride;                // elements from a query token to the next
     __nv_bfloat16 *out;              // [query tokens, Hq, D]
     float *lse_out;                  // [query tokens, Hq] or null
-    const uint8_t *k_pages, *v_pages, *scales;
+    const uint8_t *scales;
     const int32_t *block_table, *seq_lens;
     uint32_t *err;
     int32_t batch, hq, hkv, group, head_dim, page_size, max_pages, num_pages, causal;

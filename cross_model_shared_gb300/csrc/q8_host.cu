@@ -309,8 +309,6 @@ shkv_status attention(shkv_q8_pool *pool, Q8AttnParams &p, int32_t hq, const voi
     p.q_stride = q_stride;
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.lse_out = lse_out;
-    p.k_pages = static_cast<const uint8_t *>(c.k_pages);
-    p.v_pages = static_cast<const uint8_t *>(c.v_pages);
     p.scales = static_cast<const uint8_t *>(c.scales);
     p.block_table = c.block_table;
     p.seq_lens = c.seq_lens;

@@ -580,3 +580,52 @@ def test_refusals():
 def test_table_of_codes_matches_torch():
     codes = torch.arange(256, dtype=torch.uint8)
     assert np.array_equal(codes.view(torch.float8_e4m3fn).double().numpy(), TABLE, equal_nan=True)
+
+
+# ---------------------------------------------------------------------------
+# splits, joins and mixed batches
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("N_,hq,hkv,d,page", [(1, 16, 2, 128, 16), (3, 16, 2, 64, 32), (5, 16, 2, 128, 32), (8, 16, 2, 128, 16)])
+def test_decode_of_long_split_requests(N_, hq, hkv, d, page):
+    """Work ranges that open and close inside units, for every number of rows a kernel is built for (16 to 64)."""
+    c = Cache([20011, 0, 7, 9001, 13120], hkv, d, page, seed=40 + N_)
+    pool = c.pool()
+    q = c.q(5, N_ * hq)
+    out, lse = pool.decode_attention(q, N_, return_lse=True)
+    no_errors(pool)
+    check_decode(c, q, N_, d ** -0.5, out, lse)
+    again, lse2 = pool.decode_attention(q, N_, return_lse=True)      # the join's counters are back at zero
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("small", [24, 3])
+def test_chunk_of_few_tokens_beside_many(small):
+    """Requests of a few new tokens beside large ones: many (a launch of their own) and few (none)."""
+    lens, new = [700] * small + [900, 0, 5], [3] * small + [40, 0, 5]
+    c = Cache(lens, 8, 128, 16, seed=44)
+    pool = c.pool()
+    q = c.q(sum(new), 32)
+    out, lse = pool.chunk_attention(q, new, scale=0.05, return_lse=True)
+    no_errors(pool)
+    check_chunk(c, q, new, 0.05, out, lse)
+
+
+@pytest.mark.parametrize("n", [70, 6])
+def test_queries_that_are_no_numbers_stay_in_their_rows(n):
+    """An infinity or a NaN in a query row makes that row NaN and no other; a row of zeros weighs all keys alike."""
+    c = Cache([300], 1, 128, 16, seed=45)
+    pool = c.pool()
+    q = c.q(n, 2)
+    q[1, 0, 5], q[2, 1, 127], q[3] = float("inf"), float("nan"), 0
+    out, lse = pool.chunk_attention(q, [n], scale=0.05, return_lse=True)
+    no_errors(pool)
+    bad = torch.zeros(n, 2, dtype=torch.bool, device="cuda")
+    bad[1, 0] = bad[2, 1] = True
+    assert out[bad].isnan().all() and lse[bad].isnan().all()
+    q[1, 0], q[2, 1] = 0, 0
+    k, v = c.rows(0)
+    limit = (torch.arange(n, device="cuda") + 301 - n).repeat_interleave(2)
+    o, e, to, te = attend(q.reshape(2 * n, -1), k[:, 0], v[:, 0], 0.05, limit)
+    ok = ~bad.reshape(-1)
+    check(out.reshape(2 * n, -1)[ok], o[ok], to[ok], "out")
+    check(lse.reshape(-1)[ok], e[ok], te[ok], "lse")
