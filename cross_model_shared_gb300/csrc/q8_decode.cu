@@ -32,10 +32,10 @@
 // bounds l's terms by 2^75; where E rises over tokens already summed, m is kept high enough for
 // 2^97 (b[r] is that bound).  Sums and O are fp32.
 //
-// Up to 32 rows the softmax is bound by the latency of its chain, not by its
-// instructions: its two groups of four warps then take alternate stages, each
-// with all rows, a running maximum, sums and O of its own, joined at the
-// segment's end.  Above, both groups work on every stage, on half the rows.
+// The softmax is bound by the latency of its chain, not by its instructions:
+// up to 48 rows its two groups of four warps take alternate stages, each with
+// all rows, a running maximum, sums and O of its own, joined at the segment's
+// end.  Above (registers), both groups work on every stage, on half the rows.
 //
 // Roles (512 threads):
 //   warps 0-7    softmax: warp w owns tokens 32*(w%4) .. +31 of its stages;
@@ -48,7 +48,7 @@
 //                upper 16 KB of a 32 KB slot, where the thread reads its row
 //                and writes it back as fp16 over both halves (row t's codes
 //                lie inside row t's fp16 bytes, so no thread waits for
-//                another).  Above 32 rows also the tokens' factors; below,
+//                another).  Above 48 rows also the tokens' factors; below,
 //                the softmax's warps find them while they wait for S^T: a
 //                stage takes the conversion 1570 cycles with them, 1100
 //                without
@@ -103,16 +103,16 @@ static_assert(kSoftmaxRegs * 256 + kOtherRegs * 256 == 128 * kThreads, "register
 
 // scratch rows of 64 words: per softmax group the stage maxima and the sums
 // [token group], the new 7 - m, the rescaling of O and of l, m, the bound b;
-// then the factors of the two groups at the segment's end, the queries' scales
-// and the rows' output offsets
+// then the factors of the two groups at the segment's end, the queries'
+// scales, the rows' output offsets and the groups' E at the segment's end
 constexpr int kScrMax = 0, kScrNew = 4, kScrAlpha = 5, kScrAlphaL = 6, kScrM = 7, kScrB = 8, kScrGroup = 9;
-constexpr int kScrEnd = 2 * kScrGroup, kScrQ = kScrEnd + 2, kScrOff = kScrQ + 1, kScrRows = kScrOff + 1;
+constexpr int kScrEnd = 2 * kScrGroup, kScrQ = kScrEnd + 2, kScrOff = kScrQ + 1, kScrE = kScrOff + 1, kScrRows = kScrE + 1;
 
 __host__ __device__ constexpr int q_nr(int rows) { return (rows + 15) / 16 * 16; }
 // N of the PV MMA: 48 is rounded up to a whole 64-column swizzle span.
 __host__ __device__ constexpr int q_npv(int nr) { return nr == 48 ? 64 : nr; }
 // The softmax groups take alternate stages.
-__host__ __device__ constexpr bool q_pingpong(int nr) { return nr <= 32; }
+__host__ __device__ constexpr bool q_pingpong(int nr) { return nr <= 48; }
 
 constexpr int kKS = 4, kVS = 3;             // ring slots
 constexpr int kInfo = kVS + 1;              // stages of token factors (see convert_v)
@@ -125,7 +125,7 @@ struct Smem {
 // From offset 0: the K ring, the V ring (slots [half][128 tokens][128 B]), P^T
 // [128 tokens][128 B] of each group that has its own, and the query tiles
 // [qh | ql][NR rows][128 B], all 128-byte swizzled; qbuf holds the next
-// segment's bf16 query rows; info a stage's token factors (above 32 rows).
+// segment's bf16 query rows; info a stage's token factors (above 48 rows).
 __host__ __device__ constexpr Smem smem_layout(int nr)
 {
     Smem u{};
@@ -137,14 +137,14 @@ __host__ __device__ constexpr Smem smem_layout(int nr)
     u.scr = u.qbuf + (uint32_t)nr * 256u;
     u.scales = u.scr + kScrRows * 64 * 4;
     u.info = u.scales + kScaleRing * 2 * kTT;
-    u.bars = u.info + kInfo * kTT * 16u;
+    u.bars = u.info + (q_pingpong(nr) ? 0u : kInfo * kTT * 16u);
     u.meta = u.bars + 48 * 8u;
     u.misc = u.meta + kScaleRing * 4u;       // validity words
     u.tslot = u.misc + 8;
     u.total = u.misc + 16 + 1024;           // + slack to align the base to 1024 bytes
     return u;
 }
-static_assert(smem_layout(64).total <= (uint32_t)kSmemLimit && smem_layout(32).total <= (uint32_t)kSmemLimit, "fits");
+static_assert(smem_layout(64).total <= (uint32_t)kSmemLimit && smem_layout(48).total <= (uint32_t)kSmemLimit, "fits");
 
 struct Ctx4 {
     uint8_t *smem;
@@ -188,12 +188,11 @@ __device__ __forceinline__ uint32_t scale_off(int t, int log2P)
 }
 
 // Largest V scale byte of the stage's tokens below `n` on copied pages (NaN
-// rows, 255, aside), by a warp; 0 if there are none.  vs4 points at the V
-// scales of the lane's four tokens.
-__device__ __forceinline__ int stage_top_scale(const uint8_t *vs4, int n, uint32_t mask, int log2P)
+// rows, 255, aside), by a warp; 0 if there are none.  w: the V scales of the
+// lane's four tokens.
+__device__ __forceinline__ int stage_top_scale(uint32_t w, int n, uint32_t mask, int log2P)
 {
     const int t = 4 * (threadIdx.x & 31);
-    const uint32_t w = *reinterpret_cast<const volatile uint32_t *>(vs4);
     const int in = ((mask >> (t >> log2P)) & 1u) ? n - t : 0;
     uint32_t top = 0;
 #pragma unroll
@@ -412,14 +411,13 @@ __device__ void warm_l2_q8(const CUtensorMap *tm, const DecodeParams &p, const C
 
 // What a token brings to the softmax: (score factor, V exponent, factor of l,
 // first row that sees it | kMasked if some token of the warp is not seen by all
-// | kNoValue if its V counts as zero | E << 16).  sc: the token's K scale byte,
-// V's is P further on; at: its distance from the first key some row does not
+// | kNoValue if its V counts as zero | E << 16).  kb, vb: the token's scale
+// bytes; at: its distance from the first key some row does not
 // see; e: E with the token's stage.  A NaN row of V makes its key's scores NaN,
 // so that only rows that attend it see it.
 constexpr int kMasked = 0x100, kNoValue = 0x200;
-__device__ __forceinline__ float4 token_factors(const DecodeParams &p, const uint8_t *sc, bool valid, int at, int e)
+__device__ __forceinline__ float4 token_factors(const DecodeParams &p, int kb, int vb, bool valid, int at, int e)
 {
-    const int kb = *(const volatile uint8_t *)sc, vb = *(const volatile uint8_t *)(sc + p.page_size);
     const int ve = !valid || vb == 255 ? e : max(vb, e - kVWindow);
     // rows from row_min on see the token (new token i from position L - n + i on)
     const int row_min = valid ? min(64, max(0, (at + 1) * p.group)) : 64;
@@ -469,7 +467,7 @@ __device__ void convert_v(const Q8DecodeParams &q, const Ctx4 &c)
 #pragma unroll 1
         for (int tok0 = s.p0 * P; tok0 < tok_end; tok0 += kTT, ++k) {
             if (!kPing) {
-                // --- E and the token's factors (up to 32 rows the softmax's warps
+                // --- E and the token's factors (up to 48 rows the softmax's warps
                 // have the time to find them).  (Entry k % kInfo was last used by
                 // stage k - kVS - 1, whose PV was done before V(k - 1) was loaded.)
                 const uint32_t entry = k % kInfo;
@@ -484,9 +482,11 @@ __device__ void convert_v(const Q8DecodeParams &q, const Ctx4 &c)
                 }
                 const uint32_t mask = tagged & 0xffu;
                 const int so = sring.slot * 2 * kTT;
-                e = next_e(e, stage_top_scale(sc_four + so, min(lim, all_see) - tok0, mask, log2P));
+                const uint32_t four = *reinterpret_cast<const volatile uint32_t *>(sc_four + so);
+                const int kb = *(const volatile uint8_t *)(sc_mine + so), vb = *(const volatile uint8_t *)(sc_mine + so + P);
+                e = next_e(e, stage_top_scale(four, min(lim, all_see) - tok0, mask, log2P));
                 const bool valid = alive && tok0 + t < lim && ((mask >> page) & 1u);
-                const float4 f = token_factors(p, sc_mine + so, valid, tok0 + t - all_see, e);
+                const float4 f = token_factors(p, kb, vb, valid, tok0 + t - all_see, e);
                 if (alive)
                     reinterpret_cast<float4 *>(c.smem + L.info)[entry * kTT + t] = f;
                 __syncwarp();
@@ -640,6 +640,9 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
     constexpr bool kPing = q_pingpong(NR);
     constexpr int NH = kPing ? NR : NR / 2;    // rows per thread of a stage
     constexpr int NE = NR / 2;                 // rows per thread at the segment's end
+    // 7 - m of the rows: in registers up to 32 a thread, above read where it is used
+    constexpr bool kNmRegs = NH <= 32;
+    constexpr int kLoad = NH <= 32 ? NH / 8 : 3;   // 8-column chunks of S^T in flight
     constexpr int kMerge = NR == 16 ? 1 : 4;   // rows a warp merges at a time
     constexpr Smem L = smem_layout(NR);
     const DecodeParams &p = q.d;
@@ -733,10 +736,11 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
         const int nst = stages_of(s, P);
         const int R = q.n_q[s.b] * p.group;
         int e = kMinE;                          // scale byte of E
-        float2 nmu[NH / 2], l[NH / 2];          // 7 - m (1e30: no key yet), and this token's share of l
+        float2 nmu[kNmRegs ? NH / 2 : 1], l[NH / 2];   // 7 - m (1e30: no key yet), and this token's share of l
 #pragma unroll
         for (int i = 0; i < NH / 2; ++i) {
-            nmu[i] = make_float2(1e30f, 1e30f);
+            if (kNmRegs)
+                nmu[kNmRegs ? i : 0] = make_float2(1e30f, 1e30f);
             l[i] = make_float2(0.f, 0.f);
         }
         if (threadIdx.x < NR)
@@ -744,40 +748,41 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
             for (int g = 0; g < 2; ++g) {
                 scr[(g * kScrGroup + kScrM) * 64 + threadIdx.x] = -INFINITY;
                 scr[(g * kScrGroup + kScrB) * 64 + threadIdx.x] = kTermLog2;
+                scr[(g * kScrGroup + kScrNew) * 64 + threadIdx.x] = 1e30f;
             }
         named_barrier(kAllBar, kSoftmaxThreads);   // the rows' scales and initial maxima are in place
 
         // this group's first stage of the segment
         const int j0 = kPing ? (kbase ^ grp) & 1 : 0;
         const int tok_first = s.p0 * P, lim = min(plan_len(p, s), s.p1 * P), all_see = keys_all_see(q, s);
-        uint32_t mask = 0;
 #pragma unroll 1
         for (int j = j0; j < nst; j += kPing ? 2 : 1) {
             const int k = kbase + j, buf = k & 1;
             // the token's factors and S^T
             float4 f;
             if (kPing) {
-                // (E moves with the other group's stages too)
-                auto top = [&](int i) {
-                    const int slot = (kbase + i) % kScaleRing;
-                    wait(bar_at(c, kScaleB + slot), (uint32_t)((kbase + i) / kScaleRing) & 1u);
-                    mask = meta[slot];
-                    if (alive && (mask >> 8) != ((uint32_t)(kbase + i) & 0xffffffu)) {
-                        if (lane == 0) {
-                            atomicOr(p.err, SHKV_ERRF_PIPELINE);
-                            *c.abort_flag = 1u;
-                        }
-                        alive = false;
+                // E moves with the other group's stage before, too; its scales
+                // landed before this stage's (an arrival of the copies' waits
+                // for all copies before it)
+                const int slot = k % kScaleRing, prev = (k - 1) & (kScaleRing - 1);
+                wait(bar_at(c, kScaleB + slot), (uint32_t)(k / kScaleRing) & 1u);
+                const uint8_t *sc = c.smem + L.scales + slot * 2 * kTT + scale_off(t, log2P);
+                const uint32_t mask = meta[slot], mask0 = j > 0 ? meta[prev] : 0u;
+                const uint32_t four0 = *reinterpret_cast<const volatile uint32_t *>(sc_four + prev * 2 * kTT);
+                const uint32_t four = *reinterpret_cast<const volatile uint32_t *>(sc_four + slot * 2 * kTT);
+                const int kb = *(const volatile uint8_t *)sc, vb = *(const volatile uint8_t *)(sc + P);
+                if (alive && (mask >> 8) != ((uint32_t)k & 0xffffffu)) {
+                    if (lane == 0) {
+                        atomicOr(p.err, SHKV_ERRF_PIPELINE);
+                        *c.abort_flag = 1u;
                     }
-                    return stage_top_scale(sc_four + slot * 2 * kTT, min(lim, all_see) - tok_first - i * kTT, mask, log2P);
-                };
-                int e_now = e;
-                if (j > 0)
-                    e_now = next_e(e_now, top(j - 1));
-                e_now = next_e(e_now, top(j));
-                const int tok = tok_first + j * kTT + t;
-                f = token_factors(p, c.smem + L.scales + (k % kScaleRing) * 2 * kTT + scale_off(t, log2P),
-                                  tok < lim && ((mask >> (t >> log2P)) & 1u), tok - all_see, e_now);
+                    alive = false;
+                }
+                const int tok0 = tok_first + j * kTT, seen = min(lim, all_see) - tok0;
+                const int top0 = stage_top_scale(four0, seen + kTT, mask0 & 0xffu, log2P);
+                const int top = stage_top_scale(four, seen, mask & 0xffu, log2P);
+                f = token_factors(p, kb, vb, tok0 + t < lim && ((mask >> (t >> log2P)) & 1u), tok0 + t - all_see,
+                                  next_e(next_e(e, top0), top));
             }
             if (wait(bar_at(c, kSFull + buf), (uint32_t)((k >> 1) & 1)))
                 tc_fence_after();
@@ -790,24 +795,40 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
             e = w4 >> 16;
             // y - m + 7 of this thread's rows (nm = 7 - m), -inf where not seen
             float2 d[NH / 2];
-            auto scores = [&](const float2 (&nm)[NH / 2]) {
-                uint32_t sv[NH];
-#pragma unroll
-                for (int ch = 0; ch < NH / 8; ++ch)
-                    tmem_ld8_nowait(tmem + lane_base + kColS + (uint32_t)(buf * 64 + chunk_col(ch)), sv + 8 * ch);
-                tmem_wait_ld();
+            auto scores = [&](bool relative) {       // (or y itself)
                 const float2 ts2 = make_float2(f.x, f.x), ev2 = make_float2(f.y, f.y);
 #pragma unroll
-                for (int ch = 0; ch < NH / 8; ++ch) {
-                    const float4 *rq = reinterpret_cast<const float4 *>(scr + kScrQ * 64 + chunk_col(ch));
-                    const float4 qa = rq[0], qb = rq[1];
-                    const float2 q2[4] = {make_float2(qa.x, qa.y), make_float2(qa.z, qa.w), make_float2(qb.x, qb.y),
-                                          make_float2(qb.z, qb.w)};
+                for (int c0 = 0; c0 < NH / 8; c0 += kLoad) {
+                    uint32_t sv[8 * kLoad];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int o = 4 * ch + i;
-                        const float2 s2 = make_float2(__uint_as_float(sv[2 * o]), __uint_as_float(sv[2 * o + 1]));
-                        d[o] = __ffma2_rn(s2, __fmul2_rn(ts2, q2[i]), __fadd2_rn(ev2, nm[o]));
+                    for (int ch = 0; ch < kLoad; ++ch)
+                        tmem_ld8_nowait(tmem + lane_base + kColS + (uint32_t)(buf * 64 + chunk_col(c0 + ch)), sv + 8 * ch);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int ch = 0; ch < kLoad; ++ch) {
+                        const float4 *rq = reinterpret_cast<const float4 *>(scr + kScrQ * 64 + chunk_col(c0 + ch));
+                        const float4 qa = rq[0], qb = rq[1];
+                        const float2 q2[4] = {make_float2(qa.x, qa.y), make_float2(qa.z, qa.w), make_float2(qb.x, qb.y),
+                                              make_float2(qb.z, qb.w)};
+                        float2 nm[4];
+                        if (kNmRegs) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                nm[i] = nmu[kNmRegs ? 4 * (c0 + ch) + i : 0];
+                        } else {
+                            const float4 *sm = reinterpret_cast<const float4 *>(mine + kScrNew * 64 + chunk_col(c0 + ch));
+                            const float4 na = sm[0], nb = sm[1];
+                            nm[0] = make_float2(na.x, na.y);
+                            nm[1] = make_float2(na.z, na.w);
+                            nm[2] = make_float2(nb.x, nb.y);
+                            nm[3] = make_float2(nb.z, nb.w);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int o = 4 * ch + i;
+                            const float2 s2 = make_float2(__uint_as_float(sv[2 * o]), __uint_as_float(sv[2 * o + 1]));
+                            d[4 * c0 + o] = __ffma2_rn(s2, __fmul2_rn(ts2, q2[i]), relative ? __fadd2_rn(ev2, nm[i]) : ev2);
+                        }
                     }
                 }
                 if (masked)
@@ -817,15 +838,14 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                         d[o].y = row_of(2 * o + 1) < row_min ? -INFINITY : d[o].y;
                     }
             };
-            scores(nmu);
+            scores(true);
             float top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < NH / 2; ++i)
                 top = fmaxf(top, fmaxf(d[i].x, d[i].y));
             // --- lazy refresh of the maxima: all warps of the stage agree
             if (bar_red_or(bar_id, bar_threads, top > kPLog2 + kRescaleLog2 || de > 0)) {
-                const float2 none[NH / 2] = {};
-                scores(none);                   // y
+                scores(false);
                 {
                     constexpr int M = pow2_at_least(NH);
                     float v[M];
@@ -881,8 +901,10 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
 #pragma unroll
                 for (int i = 0; i < NH / 2; ++i) {
                     const int rr = row_of(2 * i);
-                    nmu[i] = make_float2(mine[kScrNew * 64 + rr], mine[kScrNew * 64 + rr + 1]);
-                    d[i] = __fadd2_rn(d[i], nmu[i]);
+                    const float2 nm = make_float2(mine[kScrNew * 64 + rr], mine[kScrNew * 64 + rr + 1]);
+                    if (kNmRegs)
+                        nmu[kNmRegs ? i : 0] = nm;
+                    d[i] = __fadd2_rn(d[i], nm);
                     l[i] = __fmul2_rn(l[i], make_float2(mine[kScrAlphaL * 64 + rr], mine[kScrAlphaL * 64 + rr + 1]));
                 }
             }
@@ -943,8 +965,8 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                     if (base + jj < NH)
                         mine[(kScrMax + tg) * 64 + row_of(base + jj)] = v[jj];
         }
-        if (t == 0)
-            *reinterpret_cast<int *>(mine + kScrNew * 64) = e;       // the group's E (kScrNew is free)
+        if (t == 0 && (kPing || warp == 0))
+            *reinterpret_cast<int *>(scr + kScrE * 64 + grp) = e;
         named_barrier(kAllBar, kSoftmaxThreads);
         const bool whole = (s.seg_begin == s.unit_begin) && (s.seg_end == s.unit_end);
         const int slot_id = whole ? 0 : 2 * (int)blockIdx.x + (s.seg_begin == c.cta_begin ? 0 : 1);
@@ -959,7 +981,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
             for (int g = 0; g < 2; ++g) {
                 const float *o = scr + g * kScrGroup * 64;
                 m[g] = kPing || g == 0 ? o[kScrM * 64 + r] : -INFINITY;
-                eg[g] = kPing || g == 0 ? reinterpret_cast<const int *>(o)[kScrNew * 64] : 0;
+                eg[g] = kPing || g == 0 ? scr_i[kScrE * 64 + g] : 0;
                 a[g] = 0.f;
                 if (kPing || g == 0)
 #pragma unroll
