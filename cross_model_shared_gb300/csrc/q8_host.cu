@@ -7,8 +7,8 @@
 #include <string.h>
 
 #include <algorithm>
+#include <exception>
 #include <new>
-#include <vector>
 
 #include "host_shared.h"
 #include "q8.cuh"
@@ -31,7 +31,7 @@ struct shkv_q8_pool {
     int device;
     int num_sms;
     CUtensorMap tm_k, tm_v;          // one page of one KV head a box
-    std::vector<int32_t> lens;       // host copy of seq_lens
+    int32_t lens[SHKV_MAX_BATCH];    // host copy of seq_lens
 };
 
 namespace {
@@ -90,10 +90,13 @@ shkv_status cache_params(const shkv_q8_pool *pool, int32_t batch, const int32_t 
     return SHKV_OK;
 }
 
-shkv_status launch_cache(const shkv_q8_pool *pool, const Q8CacheParams &p, bool read, void *stream)
+shkv_status launch_cache(shkv_q8_pool *pool, const Q8CacheParams &p, bool read, void *stream)
 {
     if (launch_q8_cache(p, read, pool->num_sms, (cudaStream_t)stream) != cudaSuccess)
         return SHKV_ERR_CUDA;
+    if (!read)
+        for (int b = 0; b < p.batch; ++b)
+            pool->lens[b] = p.start[b] + (p.tok0[b + 1] - p.tok0[b]);
     const size_t tokens = (size_t)p.tok0[p.batch];
     const size_t row = (size_t)p.hkv * p.head_dim;
     const size_t kb = tokens ? ((tokens - 1) * p.k_stride + row) * 2 : 0;
@@ -388,13 +391,13 @@ shkv_status shkv_q8_pool_create(const shkv_q8_pool_config *cfg, shkv_q8_pool **o
         return SHKV_ERR_INVALID_ARG;
     pool->cfg = c;
     pool->cfg.initial_seq_lens = nullptr;
-    pool->lens.assign(c.max_batch, 0);
+    memset(pool->lens, 0, sizeof pool->lens);
     if (c.initial_seq_lens)
-        memcpy(pool->lens.data(), c.initial_seq_lens, sizeof(int32_t) * c.max_batch);
+        memcpy(pool->lens, c.initial_seq_lens, sizeof(int32_t) * c.max_batch);
     if (cudaGetDevice(&pool->device) != cudaSuccess ||
         cudaDeviceGetAttribute(&pool->num_sms, cudaDevAttrMultiProcessorCount, pool->device) != cudaSuccess ||
         !make_map(&pool->tm_k, c.k_pages, c) || !make_map(&pool->tm_v, c.v_pages, c) ||
-        cudaMemcpy(c.seq_lens, pool->lens.data(), sizeof(int32_t) * c.max_batch, cudaMemcpyHostToDevice) !=
+        cudaMemcpy(c.seq_lens, pool->lens, sizeof(int32_t) * c.max_batch, cudaMemcpyHostToDevice) !=
             cudaSuccess ||
         cudaMemset(c.error_word, 0, sizeof(uint32_t)) != cudaSuccess) {
         delete pool;
@@ -421,10 +424,10 @@ shkv_status shkv_q8_pool_set_seq_lens(shkv_q8_pool *pool, int32_t batch, const i
             return SHKV_ERR_CAPACITY;
     if (batch == 0)
         return SHKV_OK;
-    memcpy(pool->lens.data(), lens, sizeof(int32_t) * batch);
+    memcpy(pool->lens, lens, sizeof(int32_t) * batch);
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e =
-        cudaMemcpyAsync(pool->cfg.seq_lens, pool->lens.data(), sizeof(int32_t) * batch, cudaMemcpyHostToDevice, st);
+        cudaMemcpyAsync(pool->cfg.seq_lens, pool->lens, sizeof(int32_t) * batch, cudaMemcpyHostToDevice, st);
     if (e == cudaSuccess)
         e = cudaStreamSynchronize(st);
     return status_of(e);
@@ -434,13 +437,13 @@ shkv_status shkv_q8_pool_get_seq_lens(const shkv_q8_pool *pool, int32_t batch, i
 {
     if (!pool || !lens || batch < 0 || batch > pool->cfg.max_batch)
         return SHKV_ERR_INVALID_ARG;
-    memcpy(lens, pool->lens.data(), sizeof(int32_t) * batch);
+    memcpy(lens, pool->lens, sizeof(int32_t) * batch);
     return SHKV_OK;
 }
 
 shkv_status shkv_q8_append_kv(shkv_q8_pool *pool, int32_t batch, const int32_t *start, const int32_t *new_lens,
                               const void *k_new, int64_t k_stride, const void *v_new, int64_t v_stride, void *stream)
-{
+try {
     if (!pool || !new_lens || batch < 0 || batch > pool->cfg.max_batch || !on_pool_device(pool))
         return SHKV_ERR_INVALID_ARG;
     Q8CacheParams p;
@@ -457,16 +460,14 @@ shkv_status shkv_q8_append_kv(shkv_q8_pool *pool, int32_t batch, const int32_t *
     }
     if (!moves)
         return SHKV_OK;
-    const shkv_status ls = launch_cache(pool, p, false, stream);
-    if (ls == SHKV_OK)
-        for (int b = 0; b < batch; ++b)
-            pool->lens[b] = p.start[b] + new_lens[b];
-    return ls;
+    return launch_cache(pool, p, false, stream);
+} catch (const std::exception &) {
+    return SHKV_ERR_CUDA;                // no host memory for the plan
 }
 
 shkv_status shkv_q8_read_kv(shkv_q8_pool *pool, int32_t batch, const int32_t *start, const int32_t *lens, void *k_out,
                             int64_t k_stride, void *v_out, int64_t v_stride, void *stream)
-{
+try {
     if (!pool || !start || !lens || batch < 0 || batch > pool->cfg.max_batch || !on_pool_device(pool))
         return SHKV_ERR_INVALID_ARG;
     Q8CacheParams p;
@@ -479,6 +480,8 @@ shkv_status shkv_q8_read_kv(shkv_q8_pool *pool, int32_t batch, const int32_t *st
     if (p.tok0[batch] == 0)
         return SHKV_OK;
     return launch_cache(pool, p, true, stream);
+} catch (const std::exception &) {
+    return SHKV_ERR_CUDA;                // no host memory for the plan
 }
 
 shkv_status shkv_q8_workspace_size(const shkv_q8_pool *pool, size_t *bytes, size_t *zero_bytes)
@@ -493,7 +496,7 @@ shkv_status shkv_q8_workspace_size(const shkv_q8_pool *pool, size_t *bytes, size
 shkv_status shkv_q8_decode_attention(shkv_q8_pool *pool, int32_t batch, int32_t n_models, int32_t hq_per_model,
                                      const void *q, float scale, void *out, float *lse_out, void *workspace,
                                      size_t workspace_bytes, void *stream)
-{
+try {
     if (!pool || batch < 1 || batch > pool->cfg.max_batch || n_models < 1 || hq_per_model < 1 ||
         !on_pool_device(pool))
         return SHKV_ERR_INVALID_ARG;
@@ -511,12 +514,14 @@ shkv_status shkv_q8_decode_attention(shkv_q8_pool *pool, int32_t batch, int32_t 
     }
     return attention(pool, p, hq_per_model, q, (int64_t)hq_per_model * pool->cfg.head_dim, scale, out, lse_out,
                      workspace, workspace_bytes, stream);
+} catch (const std::exception &) {
+    return SHKV_ERR_CUDA;                // no host memory for the plan
 }
 
 shkv_status shkv_q8_chunk_attention(shkv_q8_pool *pool, int32_t batch, const int32_t *new_lens, int32_t hq,
                                     const void *q, int64_t q_stride, float scale, void *out, float *lse_out,
                                     void *workspace, size_t workspace_bytes, void *stream)
-{
+try {
     if (!pool || !new_lens || batch < 1 || batch > pool->cfg.max_batch || hq < 1 || !on_pool_device(pool))
         return SHKV_ERR_INVALID_ARG;
     const int32_t hkv = pool->cfg.num_kv_heads;
@@ -540,6 +545,8 @@ shkv_status shkv_q8_chunk_attention(shkv_q8_pool *pool, int32_t batch, const int
     if (tokens == 0)
         return SHKV_OK;
     return attention(pool, p, hq, q, q_stride, scale, out, lse_out, workspace, workspace_bytes, stream);
+} catch (const std::exception &) {
+    return SHKV_ERR_CUDA;                // no host memory for the plan
 }
 
 shkv_status shkv_q8_check_errors(shkv_q8_pool *pool, void *stream, uint32_t *flags)
