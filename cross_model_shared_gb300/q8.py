@@ -19,7 +19,8 @@ from . import _native as N
 
 _BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
 _HERE = contextlib.nullcontext()
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 class _HostInts:
@@ -130,8 +131,9 @@ class QuantizedKVPool:
     def _on(self, stream: Optional[torch.cuda.Stream]):
         """(context that makes the stream and the pool's device current, raw stream)."""
         if stream is None:
-            if _raw_stream is not None and torch.cuda.current_device() == self.device.index:
-                return _HERE, _raw_stream(self.device.index)
+            index = self.device.index
+            if _raw_stream is not None and _current_device() == index:
+                return _HERE, _raw_stream(index)
             stream = torch.cuda.current_stream(self.device)
         elif stream.device != self.device:
             raise ValueError(f"stream must be one of {self.device}")
@@ -139,16 +141,18 @@ class QuantizedKVPool:
 
     def _rows(self, t: torch.Tensor, heads: Optional[int], name: str) -> int:
         """Checks a [tokens, heads, head_dim] bf16 operand whose tokens may be strided; its stride in elements."""
-        if t.device != self.device or t.dtype != _BF16:
+        if t.dtype is not _BF16 or t.device != self.device:
             raise ValueError(f"{name} must be bfloat16 on {self.device}")
-        if t.dim() != 3 or t.shape[2] != self.head_dim or (heads is not None and t.shape[1] != heads):
+        shape = t.shape
+        if len(shape) != 3 or shape[2] != self.head_dim or (heads is not None and shape[1] != heads):
             raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {self.head_dim}]")
-        row = t.shape[1] * self.head_dim
-        if t.shape[0] <= 1 and t.is_contiguous():
+        row = shape[1] * self.head_dim
+        if t.is_contiguous():
             return row
-        if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != self.head_dim) or t.stride(0) < row or t.stride(0) % 8:
+        token, head, one = t.stride()
+        if one != 1 or (shape[1] > 1 and head != self.head_dim) or token < row or token % 8:
             raise ValueError(f"{name}: a token's rows must be contiguous and tokens a multiple of 8 elements apart")
-        return t.stride(0)
+        return token
 
     def _out(self, t: Optional[torch.Tensor], shape, dtype, name: str) -> torch.Tensor:
         if t is None:
