@@ -17,16 +17,17 @@
 // factor of a key is a column factor here, read as a vector from shared
 // memory.  V is widened to fp16 in shared memory with its scale relative to
 // E, a running upper bound of the unit's V exponents: V16 = v8 * 2^(ev - E + 6),
-// exact.  O is rescaled where m or E moves.  From the first stage on that
-// holds a scale under 2^-8 of the largest so far (or far above it) the piece
-// is `wide`: it is summed with V16 = v8 * 2^-14, the factor 2^(ev - E + 20) in
-// P, and P relative to m2[r], a running maximum of x + ev apart from l's m: so
-// fp16 holds 11 bits of every token that matters to the sum, whatever the
-// magnitudes of weights and values apart.  That takes two exponentials a
-// score.  (While V's scales are alike, P relative to the largest weight does
-// the same: fp16's least step is 2^-31 of it, 2^-21 of the least V scale.)  A
-// V row of the least scale (values under 2^-118) beside ordinary ones takes
-// part as zero.  Sums and O are fp32.
+// exact.  O is rescaled where m or E moves.  From the first stage on by which
+// V's scales lie more than 2^12 apart the piece is `wide`: it is summed with
+// V16 = v8 * 2^-14, the factor 2^(ev - E + 20) in P, and P relative to m2[r], a
+// running maximum of x + ev apart from l's m: so fp16 holds 11 bits of every
+// token that matters to the sum, whatever the magnitudes of weights and values
+// apart.  That takes two exponentials a score, about twice the time.  (While
+// V's scales are alike, P relative to the largest weight does the same: fp16's
+// least step is 2^-31 of it, 2^-19 of the least V scale.  2^12 is past what
+// values of magnitude 2^N(0, 1) reach in 2^18 tokens.)  A V row of the least
+// scale (values under 2^-118) beside ordinary ones takes part as zero.  Sums
+// and O are fp32.
 //
 // As in the bf16 kernel, a stage whose scores are all visible is
 // exponentiated against the running maximum without taking its own; a row
@@ -62,7 +63,7 @@ constexpr float kRescaleLog2 = 8.f;      // m lags the maximum by at most this
 constexpr float kPLog2 = 7.f;            // P at the running maximum
 constexpr float kMaxPart = 32768.f;      // largest stage sum of P taken without the stage's maximum
 constexpr int kVLog2 = 6;                // V16 of the largest scale is 448 * 2^6 at most
-constexpr int kVExact = 10;              // V exponents further under E than this make a piece wide
+constexpr int kVSpread = 12;             // V exponents further apart than this make a piece wide
 constexpr int kVWide = 20;               // ... and V16 is then v8 * 2^(6 - 20) for all tokens
 constexpr int kZeroRowE = 60;            // from E = 2^(60 - 127) on a V row of scale byte 0 counts as zero
 constexpr int kEHeadroom = 2;            // E moves to this much above a stage's largest V exponent
@@ -276,6 +277,7 @@ __device__ void chunk_convert(const Q8ChunkParams &p, const Ctx &c)
 #pragma unroll 1
     for (bool more = first_piece(p, u); more; more = next_piece(p, u)) {
         int e = 0;                                       // E as a scale byte
+        int most = 0, least = 255;                       // V scale bytes of the piece so far
         bool wide = false;
 #pragma unroll 1
         for (int j = u.s0; j < u.s1; ++j) {
@@ -302,14 +304,14 @@ __device__ void chunk_convert(const Q8ChunkParams &p, const Ctx &c)
                         top = max(top, b[i] == 255u ? 0u : b[i]);
                     }
                     top = __reduce_max_sync(0xffffffffu, top);
-                    if ((int)top > e) {
-                        wide = wide || (j > u.s0 && (int)top > e + kVExact);
+                    if ((int)top > e)
                         e = min((int)top + kEHeadroom, 254);
-                    }
+                    most = max(most, (int)top);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         low = min(low, b[i] == 0u && e > kZeroRowE ? 255u : b[i]);
-                    wide = wide || (int)__reduce_min_sync(0xffffffffu, low) < e - kVExact;
+                    least = min(least, (int)__reduce_min_sync(0xffffffffu, low));
+                    wide = wide || most - least > kVSpread;
                 }
                 const bool valid = t < n && ((mask >> (t >> log2P)) & 1u);
                 const uint8_t *mine = sc + ((t >> log2P) << (log2P + 1)) + (t & (P - 1));
@@ -753,7 +755,7 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                         m2 = cy;
                     }
                 } else {
-                    scale_o *= __uint_as_float((uint32_t)(127 - min(de, 126)) << 23);   // (de > 10 only at the first stage)
+                    scale_o *= __uint_as_float((uint32_t)(127 - min(de, 126)) << 23);   // (de > 16 only at the first stage)
                 }
                 if (j > t.s0 && __any_sync(0xffffffffu, scale_o != 1.f)) {
                     // tcgen05.ld/st are warp-wide: lanes that keep their references scale by 1
