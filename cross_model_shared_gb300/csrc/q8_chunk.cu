@@ -333,6 +333,8 @@ __device__ void chunk_convert(const Q8ChunkParams &p, const Ctx &c)
                 const unsigned short hb = (unsigned short)((kVLog2 - (wide ? kVWide : under) + 15) << 10);   // >= 2^-14
                 const __half2 f = __halves2half2(__ushort_as_half(hb), __ushort_as_half(hb));
                 uint8_t *row = c.smem + c.lay.vring + (uint32_t)slot * kVSlotBytes + (uint32_t)t * 128u;
+                // (the conversion instruction and one product: the stacked
+                // kernel's integer moves are 4% of the kernel slower here)
                 // the codes of half h are read before its fp16 values are
                 // written; only half 1's land on codes, and those were read
 #pragma unroll 1
