@@ -59,7 +59,8 @@ class QuantizedKVPool:
     of two that brings the row's largest magnitude to at most 448.
 
     Every call runs on ``stream`` (the pool device's current stream if None),
-    which must be ordered after the work that made its inputs.  The workspace
+    which must be ordered after the work that made its inputs; tensors of other
+    streams may be dropped once the call has returned.  The workspace
     of the attentions is one per stream; a call that is being captured into a
     CUDA graph takes one of its own from the graph's memory, so graphs share
     none.  ``workspace=`` names another, of ``workspace_bytes`` bytes whose
@@ -139,6 +140,14 @@ class QuantizedKVPool:
             raise ValueError(f"stream must be one of {self.device}")
         return torch.cuda.stream(stream), stream.cuda_stream
 
+    @staticmethod
+    def _used_on(stream: Optional[torch.cuda.Stream], *tensors: Optional[torch.Tensor]) -> None:
+        """Keeps the memory of a call's tensors from being handed out again before `stream` is through with it."""
+        if stream is not None and not torch.cuda.is_current_stream_capturing():
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+
     def _rows(self, t: torch.Tensor, heads: Optional[int], name: str) -> int:
         """Checks a [tokens, heads, head_dim] bf16 operand whose tokens may be strided; its stride in elements."""
         if t.dtype is not _BF16 or t.device != self.device:
@@ -208,6 +217,7 @@ class QuantizedKVPool:
         with ctx:
             N.shkv_q8_append_kv(self.handle, new.n, first.ptr if first is not None else None, new.ptr,
                                 k_new.data_ptr(), ks, v_new.data_ptr(), vs, s)
+            self._used_on(stream, k_new, v_new)
 
     def read_kv(self, start, lens, k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
                 stream=None):
@@ -222,6 +232,7 @@ class QuantizedKVPool:
         with ctx:
             k, v = self._out(k_out, shape, _BF16, "k_out"), self._out(v_out, shape, _BF16, "v_out")
             N.shkv_q8_read_kv(self.handle, n.n, first.ptr, n.ptr, k.data_ptr(), row, v.data_ptr(), row, s)
+            self._used_on(stream, k_out, v_out)
         return k, v
 
     def decode_attention(self, q: torch.Tensor, n_models: int, scale: Optional[float] = None,
@@ -243,6 +254,7 @@ class QuantizedKVPool:
             N.shkv_q8_decode_attention(self.handle, B, n_models, rows // n_models, q.data_ptr(),
                                        D ** -0.5 if scale is None else float(scale), o.data_ptr(),
                                        e.data_ptr() if e is not None else None, ws.data_ptr(), ws.numel(), s)
+            self._used_on(stream, q, out, lse, workspace)
         return (o, e) if e is not None else o
 
     def chunk_attention(self, q: torch.Tensor, new_lens, scale: Optional[float] = None,
@@ -266,6 +278,7 @@ class QuantizedKVPool:
                 N.shkv_q8_chunk_attention(self.handle, new.n, new.ptr, hq, q.data_ptr(), qs,
                                           D ** -0.5 if scale is None else float(scale), o.data_ptr(),
                                           e.data_ptr() if e is not None else None, ws.data_ptr(), ws.numel(), s)
+                self._used_on(stream, q, out, lse, workspace)
         return (o, e) if e is not None else o
 
     def check_errors(self, stream=None) -> int:

@@ -629,3 +629,32 @@ def test_queries_that_are_no_numbers_stay_in_their_rows(n):
     ok = ~bad.reshape(-1)
     check(out.reshape(2 * n, -1)[ok], o[ok], to[ok], "out")
     check(lse.reshape(-1)[ok], e[ok], te[ok], "lse")
+
+def test_inputs_of_another_stream_may_be_dropped():
+    """A call waits on its stream while its inputs are freed and their memory is asked for again elsewhere."""
+    c = Cache([700, 90], 2, 128, 16, seed=46)
+    pool = c.pool(lens=[690, 90])
+    q0 = c.q(2, 16)
+    kv0 = torch.randn(2, 10, 2, 128, generator=c.g).to(torch.bfloat16).cuda()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    pool.append_kv(kv0[0], kv0[1], [10, 0], start=[690, 90], stream=s)       # kernels loaded, workspace made
+    pool.decode_attention(q0, 2, return_lse=True, stream=s)
+    torch.full_like(q0, 7.0)
+    pool.set_seq_lens([690, 90])
+    q, k, v = q0.clone(), kv0[0].clone(), kv0[1].clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)                               # some 50 ms
+    pool.append_kv(k, v, [10, 0], stream=s)
+    out, lse = pool.decode_attention(q, 2, scale=0.05, return_lse=True, stream=s)
+    del q, k, v
+    others = [torch.full_like(t, 7.0) for t in (q0, kv0[0], kv0[1]) for _ in range(3)]
+    torch.cuda.synchronize()
+    no_errors(pool)
+    del others
+    got_k, got_v = pool.read_kv([690, 0], [10, 0])
+    for got, src in ((got_k, kv0[0]), (got_v, kv0[1])):
+        codes, sc = quantise(src.double().cpu().numpy())
+        assert torch.equal(got.double().cpu(), dequantise(torch.from_numpy(codes), torch.from_numpy(sc)))
+    check_decode(c, q0, 2, 0.05, out, lse)
