@@ -191,6 +191,7 @@ shkv_status launch_stacked(shkv_q8_pool *pool, const Q8AttnParams &a, int max_ro
 // costliest is as cheap as a greedy fill makes it (bisection over the bound).
 // In fifths of a stage of both tiles: a piece pays kPiece for its query rows,
 // the pipeline's fill and drain and its output, a stage 5 (3 with one tile).
+// (Fitted to the ranges' end times; a piece at 20 was 4 to 7% slower.)
 constexpr int64_t kPiece = 30, kPair = 5, kSingle = 3;
 constexpr int64_t kMinPiece = 2;            // stages; smaller pieces are not cut off
 
@@ -325,8 +326,10 @@ shkv_status attention(shkv_q8_pool *pool, Q8AttnParams &p, int32_t hq, const voi
     p.num_pages = c.num_pages;
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
     // requests of up to kMaxDecodeRows rows per KV head go to the stacked
-    // kernel, which is bound by the pages' bytes, the others to the chunk
-    // kernel; a few small requests beside large ones go along with them, where
+    // kernel, which reads a page once for all of them (16 requests of 4000
+    // tokens, 8 KV heads: 64 rows 66 us, where the chunk kernel takes 143 for
+    // 68 rows, 155 for 128: one tile, nothing to overlap its chain with), the
+    // others to the chunk kernel; a few small requests beside large ones go along with them, where
     // that costs a CTA less than the second launch (about 12 us, the time of 6
     // stages; a mixed batch of 9 requests took 41 us with it, 24 without)
     int max_rows = 0;
