@@ -329,9 +329,10 @@ shkv_status attention(shkv_q8_pool *pool, Q8AttnParams &p, int32_t hq, const voi
     // kernel, which reads a page once for all of them (16 requests of 4000
     // tokens, 8 KV heads: 64 rows 66 us, where the chunk kernel takes 143 for
     // 68 rows, 155 for 128: one tile, nothing to overlap its chain with), the
-    // others to the chunk kernel; a few small requests beside large ones go along with them, where
-    // that costs a CTA less than the second launch (about 12 us, the time of 6
-    // stages; a mixed batch of 9 requests took 41 us with it, 24 without)
+    // others to the chunk kernel; a few small requests beside large ones go
+    // along with them, where that costs a CTA less than the second launch
+    // (about 12 us, the time of 6 stages; a mixed batch of 9 requests took
+    // 41 us with it, 24 without)
     int max_rows = 0;
     int64_t tokens = 0, small_cost = 0;
     Q8AttnParams large = p;
