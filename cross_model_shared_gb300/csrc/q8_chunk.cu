@@ -10,29 +10,38 @@
 // by all SMs at once).  Per stage and tile:
 //
 //   S_X[r, key]  = sum_d (qh + ql)[r, d] k8[key, d]               kind::f8f6f4
-//   P_X[r, key]  = 2^(S 2^eq[r] 2^ek[key] scale log2(e) - m[r] + 7)   fp16, over S in TMEM
-//   O_X[r, d]   += sum_key P_X[r, key] V16[key, d]                kind::f16
+//   x_X[r, key]  = S_X 2^eq[r] 2^ek[key] scale log2(e)
+//   w_X[r, key]  = 2^(x - m[r] + 7),  m[r] a running maximum of x + ev
+//   P_X[r, key]  = w 2^ev[key]                                    fp16, over S in TMEM
+//   O_X[r, d]   += sum_key P_X[r, key] v8[key, d]                 kind::f16
+//   l[r]        += sum_key w_X[r, key]
+//   out = O / l,   lse = ln2 * (m - 7 + log2(l))
 //
 // The query's two e4m3 terms are as in the stacked kernel (q8_decode.cu); the
-// factor of a key is a column factor here, read as a vector from shared
-// memory.  V is widened to fp16 in shared memory with its scale relative to
-// E, a running upper bound of the unit's V exponents: V16 = v8 * 2^(ev - E + 6),
-// exact.  O is rescaled where m or E moves.  From the first stage on by which
-// V's scales lie more than 2^12 apart the piece is `wide`: it is summed with
-// V16 = v8 * 2^-14, the factor 2^(ev - E + 20) in P, and P relative to m2[r], a
-// running maximum of x + ev apart from l's m: so fp16 holds 11 bits of every
-// token that matters to the sum, whatever the magnitudes of weights and values
-// apart.  That takes two exponentials a score, about twice the time.  (While
-// V's scales are alike, P relative to the largest weight does the same: fp16's
-// least step is 2^-31 of it, 2^-19 of the least V scale.  2^12 is past what
-// values of magnitude 2^N(0, 1) reach in 2^18 tokens.)  A V row of the least
-// scale (values under 2^-118) beside ordinary ones takes part as zero.  Sums
-// and O are fp32.
+// factors of a key are column factors here, read as vectors from shared
+// memory.  V's codes are exact in fp16 as they are.  With the key's V exponent
+// in m, P is relative to the row's largest weight times value scale: fp16's
+// least step, 2^-24, is 2^-31 of that, so 2^20 keys whose P rounds to zero are
+// 2^-12 of the sum's largest term.  (P relative to the largest weight alone,
+// with V's scales apart by 2^s, loses up to n 2^(s - 32): a first key of much
+// weight and little value, as an attention sink is, then lost 10% of a sum over
+// 131072 keys at s = 12.)  V exponents of -40 to 40 (row maxima of 2^-31 to 2^48)
+// keep l's terms between 2^-81 and 2^55, in fp32's range.  From the first
+// stage on that holds another one the piece is `wide`: l is then summed from a
+// second exponential, relative to a running maximum of x of its own.
+// Such a stage takes about twice the time.  Sums and O are fp32.
 //
 // As in the bf16 kernel, a stage whose scores are all visible is
-// exponentiated against the running maximum without taking its own; a row
-// whose sum of P exceeds 2^15 (fp16's range) or is no number sends its warp
-// through the exact path.
+// exponentiated against the running maximum without taking its own.  A quarter
+// of its sum of w, times the stage's largest value scale, bounds each P in the
+// quarter: a row for which that leaves fp16's range sends its warp through the
+// exact path.  (Looking at P itself, by a sum with ev in the exponent and l by
+// factors 2^-ev or by a packed maximum, costs an instruction a pair and, in the
+// first form, a vector load: turns 338 us, the document 1.80 ms, against 317 us
+// and 1.59 ms; the exact path it is spared is 2% of the time.)  Three quarters
+// of the scores are loaded at first, the last over the third: with all of them
+// in registers the kernel spilled more (324 us, 1.77 ms).  Its load and wait stay
+// next to each other: nothing may touch the registers between them.
 //
 // Roles (512 threads): warps 0-3 softmax of tile A, 4-7 of tile B (row = TMEM
 // lane), 8 QK issuer, 9 PV issuer, 10 producer of K, 11 producer of V and its
@@ -59,14 +68,10 @@ constexpr int kThreads = 512;
 constexpr int kQkWarp = 8, kPvWarp = 9, kKWarp = 10, kVWarp = 11, kConvWarp0 = 12, kConvWarps = 4;
 constexpr int kGroupWarps = 4;           // softmax warps per tile
 constexpr uint32_t kTmemCols = 512;
-constexpr float kRescaleLog2 = 8.f;      // m lags the maximum by at most this
+constexpr float kRescaleLog2 = 2.f;      // in the exact path m moves where it lags the maximum by more
 constexpr float kPLog2 = 7.f;            // P at the running maximum
-constexpr float kMaxPart = 32768.f;      // largest stage sum of P taken without the stage's maximum
-constexpr int kVLog2 = 6;                // V16 of the largest scale is 448 * 2^6 at most
-constexpr int kVSpread = 12;             // V exponents further apart than this make a piece wide
-constexpr int kVWide = 20;               // ... and V16 is then v8 * 2^(6 - 20) for all tokens
-constexpr int kZeroRowE = 60;            // from E = 2^(60 - 127) on a V row of scale byte 0 counts as zero
-constexpr int kEHeadroom = 2;            // E moves to this much above a stage's largest V exponent
+constexpr float kMaxPart = 65504.f;      // fp16's largest: bound of a stage's P taken without its maximum
+constexpr int kVWindow = 40;             // V exponents outside -kVWindow .. kVWindow make a piece wide
 constexpr int kKS = 3, kVS = 3;          // ring slots of 16 KB (K) and 32 KB (V)
 constexpr uint32_t kKSlotBytes = kKT * 128;
 constexpr uint32_t kVSlotBytes = 2 * kKT * 128;
@@ -78,13 +83,14 @@ __device__ __forceinline__ uint32_t col_s(int x) { return (uint32_t)(x * 128); }
 __device__ __forceinline__ uint32_t col_o(int x) { return (uint32_t)(256 + x * 128); }
 
 struct Smem {
-    uint32_t qtile, kring, vring, scales, factor, pfactor, info, bars, misc, tslot, total;
+    uint32_t qtile, kring, vring, scales, factor, evs, pfactor, info, bars, misc, tslot, total;
 };
 
 // Query tiles [tile][qh | ql][128 rows][128 B], K ring, V ring (slots
 // [half][128 keys][128 B], the codes in the upper half until they are
 // converted), all 128-byte swizzled; per V slot its scale bytes, the keys'
-// score factors and P factors, and four words (valid pages, E, wide).
+// score factors, V exponents and factors of P, and four words (valid pages,
+// wide, the largest sum of w that needs no look at the maximum).
 __host__ __device__ inline Smem smem_layout()
 {
     Smem u;
@@ -93,7 +99,8 @@ __host__ __device__ inline Smem smem_layout()
     u.vring = u.kring + kKS * kKSlotBytes;
     u.scales = u.vring + kVS * kVSlotBytes;
     u.factor = u.scales + kVS * 2 * kKT;
-    u.pfactor = u.factor + kVS * kKT * 4;
+    u.evs = u.factor + kVS * kKT * 4;
+    u.pfactor = u.evs + kVS * kKT * 4;
     u.info = u.pfactor + kVS * kKT * 4;
     u.bars = u.info + kVS * 16;
     u.misc = u.bars + (uint32_t)(2 * kKS + 3 * kVS + 9) * 8u;
@@ -276,8 +283,6 @@ __device__ void chunk_convert(const Q8ChunkParams &p, const Ctx &c)
     Piece u;
 #pragma unroll 1
     for (bool more = first_piece(p, u); more; more = next_piece(p, u)) {
-        int e = 0;                                       // E as a scale byte
-        int most = 0, least = 255;                       // V scale bytes of the piece so far
         bool wide = false;
 #pragma unroll 1
         for (int j = u.s0; j < u.s1; ++j) {
@@ -291,27 +296,24 @@ __device__ void chunk_convert(const Q8ChunkParams &p, const Ctx &c)
                 const uint32_t mask = info[0];
                 const int n = u.L - j * kKT;
                 const uint8_t *sc = c.smem + c.lay.scales + slot * 2 * kKT;
-                // the stage's largest and least V scale, by each warp for itself
+                int top;                                 // the stage's largest V scale byte
+                // V exponents outside the window, by each warp for itself (NaN
+                // rows aside, and the least scale, whose rows count as zero)
                 {
                     const int t4 = 4 * lane;
                     const uint32_t w = *reinterpret_cast<const volatile uint32_t *>(
                         sc + ((t4 >> log2P) << (log2P + 1)) + P + (t4 & (P - 1)));
                     const int in = ((mask >> (t4 >> log2P)) & 1u) ? n - t4 : 0;
-                    uint32_t b[4], top = 0, low = 255;
+                    bool out = false;
+                    int big = 0;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        b[i] = i < in ? (w >> (8 * i)) & 0xffu : 255u;
-                        top = max(top, b[i] == 255u ? 0u : b[i]);
+                        const int b = (int)((w >> (8 * i)) & 0xffu);
+                        big = max(big, i < in && b != 255 ? b : 0);
+                        out = out || (i < in && b != 255 && b != 0 && abs(b - 127) > kVWindow);
                     }
-                    top = __reduce_max_sync(0xffffffffu, top);
-                    if ((int)top > e)
-                        e = min((int)top + kEHeadroom, 254);
-                    most = max(most, (int)top);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        low = min(low, b[i] == 0u && e > kZeroRowE ? 255u : b[i]);
-                    least = min(least, (int)__reduce_min_sync(0xffffffffu, low));
-                    wide = wide || most - least > kVSpread;
+                    wide = wide || __any_sync(0xffffffffu, out);
+                    top = (int)__reduce_max_sync(0xffffffffu, (unsigned)big);
                 }
                 const bool valid = t < n && ((mask >> (t >> log2P)) & 1u);
                 const uint8_t *mine = sc + ((t >> log2P) << (log2P + 1)) + (t & (P - 1));
@@ -319,22 +321,22 @@ __device__ void chunk_convert(const Q8ChunkParams &p, const Ctx &c)
                 const int vb = *reinterpret_cast<const volatile uint8_t *>(mine + P);
                 // a NaN row of V counts as zero and makes its key's scores NaN
                 // instead, so that only rows that attend it see it
-                const bool live = valid && vb != 255 && !(vb == 0 && e > kZeroRowE);
+                const bool live = valid && vb != 255 && vb != 0;
                 const float nan = __uint_as_float(0x7fc00000u);
+                const int ev = live ? vb - 127 : -kVWindow;
                 reinterpret_cast<float *>(c.smem + c.lay.factor)[slot * kKT + t] =
                     !valid ? 0.f : vb == 255 ? nan : q8_scale((uint32_t)kb) * p.scale_log2;
-                const int under = live ? e - vb : 0;      // >= 0
                 // (where V counts as zero P may be zero too, and stays out of its reference)
-                reinterpret_cast<float *>(c.smem + c.lay.pfactor)[slot * kKT + t] = live ? (float)(kVWide - under) : -1e30f;
+                reinterpret_cast<float *>(c.smem + c.lay.evs)[slot * kKT + t] = wide && !live ? -INFINITY : (float)ev;
+                reinterpret_cast<float *>(c.smem + c.lay.pfactor)[slot * kKT + t] =
+                    __uint_as_float((uint32_t)(127 + ev) << 23);                 // 2^ev (of no use where wide)
                 if (t == 0) {
-                    info[1] = (uint32_t)e;
-                    info[2] = wide ? 1u : 0u;
+                    info[1] = wide ? 1u : 0u;
+                    info[2] = __float_as_uint(kMaxPart) + ((uint32_t)(127 - max(top, 127 - kVWindow)) << 23);
                 }
-                const unsigned short hb = (unsigned short)((kVLog2 - (wide ? kVWide : under) + 15) << 10);   // >= 2^-14
-                const __half2 f = __halves2half2(__ushort_as_half(hb), __ushort_as_half(hb));
                 uint8_t *row = c.smem + c.lay.vring + (uint32_t)slot * kVSlotBytes + (uint32_t)t * 128u;
-                // (the conversion instruction and one product: the stacked
-                // kernel's integer moves are 4% of the kernel slower here)
+                // (the conversion instruction: the stacked kernel's integer
+                // moves are 4% of the kernel slower here)
                 // the codes of half h are read before its fp16 values are
                 // written; only half 1's land on codes, and those were read
 #pragma unroll 1
@@ -350,9 +352,9 @@ __device__ void chunk_convert(const Q8ChunkParams &p, const Ctx &c)
                         uint32_t o[8];
 #pragma unroll
                         for (int v = 0; v < 8; ++v) {
-                            const __half2 x = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2(
-                                                          (__nv_fp8x2_storage_t)(w[v >> 1] >> (16 * (v & 1))), __NV_E4M3)), f);
-                            o[v] = *reinterpret_cast<const uint32_t *>(&x);
+                            const __half2_raw x = __nv_cvt_fp8x2_to_halfraw2(
+                                (__nv_fp8x2_storage_t)(w[v >> 1] >> (16 * (v & 1))), __NV_E4M3);
+                            o[v] = (uint32_t)x.x | (uint32_t)x.y << 16;
                         }
                         uint8_t *dst = row + h * (kKT * 128);
                         *reinterpret_cast<uint4 *>(dst + (((2 * i) ^ (t & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -626,9 +628,8 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
             mbar_arrive(q_ready(c));
 
         float m_use = -INFINITY, lsum = 0.f;
-        float m2 = 0.f;                                  // P's reference once the piece is wide; m + E until then
+        float m_l = 0.f;                                 // l's reference once the piece is wide; m_use until then
         bool apart = false;
-        int e = 0;                                       // E as a scale byte
         const int s1 = min(t.s1, t.nst[x]);
 #pragma unroll 1
         for (int j = t.s0; j < s1; ++j) {
@@ -637,9 +638,10 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
             wait(conv_v(c, vs), ring_par(k, kVS));
             const volatile uint32_t *info = reinterpret_cast<const volatile uint32_t *>(c.smem + c.lay.info) + vs * 4;
             const uint32_t pmask = alive ? info[0] : 0u;
-            const int e_new = alive ? (int)info[1] : e;
-            const bool wide = info[2] != 0u;
+            const bool wide = info[1] != 0u;
             const float4 *fac = reinterpret_cast<const float4 *>(c.smem + c.lay.factor + vs * kKT * 4);
+            const float4 *evs = reinterpret_cast<const float4 *>(c.smem + c.lay.evs + vs * kKT * 4);
+            const float4 *pfac = reinterpret_cast<const float4 *>(c.smem + c.lay.pfactor + vs * kKT * 4);
             // keys this row may see: [key0, key0 + nvis), on pages that were copied
             // (padding rows see all: their scores only reach their own row of O, which is not stored)
             const int nvis = row_ok ? min(kKT, pos - key0 + 1) : kKT;
@@ -647,41 +649,51 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
             wait(s_full(c, x), (uint32_t)(done & 1));
             if (alive)
                 tc_fence_after();
-            uint32_t sv[4][32];
+            uint32_t sv[3][32];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 3; ++q)
                 tmem_ld32_nowait(srow + (uint32_t)(q * 32), sv[q]);
             tmem_wait_ld();
             // Common case (see the top): P against the running maximum.
             float part = 0.f;
-            bool fast = __all_sync(0xffffffffu, dense && alive && m_use != -INFINITY && e_new == e && !wide);
+            bool fast = __all_sync(0xffffffffu, dense && alive && m_use != -INFINITY && !wide);
             if (fast) {
                 const float nmu = kPLog2 - m_use;
                 const float2 rq2 = make_float2(rq, rq), nmu2 = make_float2(nmu, nmu);
                 float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                // 32 columns; their P lies over 16 columns further to the left,
+                // so that the scores of the first half stay in registers
+                auto quarter = [&](int q, const uint32_t (&s)[32]) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float4 f = fac[q * 8 + i];
-                        const float2 x0 = __ffma2_rn(__fmul2_rn(make_float2(__uint_as_float(sv[q][4 * i]),
-                                                                            __uint_as_float(sv[q][4 * i + 1])),
+                        const float4 f = fac[q * 8 + i], w = pfac[q * 8 + i];
+                        const float2 x0 = __ffma2_rn(__fmul2_rn(make_float2(__uint_as_float(s[4 * i]),
+                                                                            __uint_as_float(s[4 * i + 1])),
                                                                 make_float2(f.x, f.y)), rq2, nmu2);
-                        const float2 x1 = __ffma2_rn(__fmul2_rn(make_float2(__uint_as_float(sv[q][4 * i + 2]),
-                                                                            __uint_as_float(sv[q][4 * i + 3])),
+                        const float2 x1 = __ffma2_rn(__fmul2_rn(make_float2(__uint_as_float(s[4 * i + 2]),
+                                                                            __uint_as_float(s[4 * i + 3])),
                                                                 make_float2(f.z, f.w)), rq2, nmu2);
-                        const float2 p0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
-                        const float2 p1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
+                        float2 p0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
+                        float2 p1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
                         acc[0] = __fadd2_rn(acc[0], p0);
                         acc[1] = __fadd2_rn(acc[1], p1);
+                        p0 = __fmul2_rn(p0, make_float2(w.x, w.y));
+                        p1 = __fmul2_rn(p1, make_float2(w.z, w.w));
                         pk[2 * i] = pack_half2(p0.x, p0.y);
                         pk[2 * i + 1] = pack_half2(p1.x, p1.y);
                     }
                     tmem_st16_nowait(srow + (uint32_t)(q * 16), pk);
-                }
+                };
+                quarter(2, sv[2]);
+                quarter(0, sv[0]);
+                quarter(1, sv[1]);
+                tmem_ld32_nowait(srow + 96u, sv[2]);
+                tmem_wait_ld();
+                quarter(3, sv[2]);
                 part = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-                if (__any_sync(0xffffffffu, !(part <= kMaxPart))) {
+                const float most = fmaxf(fmaxf(acc[0].x, acc[0].y), fmaxf(acc[1].x, acc[1].y));
+                if (__any_sync(0xffffffffu, row_ok && !(most <= __uint_as_float(info[2])))) {
                     // the scores go back for the exact path
                     tmem_wait_st();
 #pragma unroll
@@ -695,7 +707,6 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                 // at a piece's first stage, on the diagonal and where a
                 // maximum moves, its instructions mostly cold): the stage's
                 // masked maximum first, then P
-                const float4 *pf = reinterpret_cast<const float4 *>(c.smem + c.lay.pfactor + vs * kKT * 4);
                 const int shift = 31 - __clz(P);
                 // the scores of columns 32c .. 32c + 31, -inf where not visible
                 // (past this row's end, or on a page that was not copied)
@@ -716,48 +727,39 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                                                                          : -INFINITY;
                     }
                 };
-                float cm = -INFINITY, cy = -INFINITY;
+                float cm = -INFINITY, cy = -INFINITY;    // maxima of x and of y
 #pragma unroll 1
                 for (int c32 = 0; c32 < kKT / 32; ++c32) {
                     float xs[32];
                     columns(c32, xs);
+                    if (wide)
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2)
-                        cm = max3f(cm, xs[i], xs[i + 1]);
-                    if (wide) {
+                        for (int i = 0; i < 32; i += 2)
+                            cm = max3f(cm, xs[i], xs[i + 1]);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 f = pf[c32 * 8 + i];
-                            cy = max3f(max3f(cy, xs[4 * i] + f.x, xs[4 * i + 1] + f.y), xs[4 * i + 2] + f.z,
-                                       xs[4 * i + 3] + f.w);
-                        }
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 v = evs[c32 * 8 + i];
+                        cy = max3f(max3f(cy, xs[4 * i] + v.x, xs[4 * i + 1] + v.y), xs[4 * i + 2] + v.z, xs[4 * i + 3] + v.w);
                     }
                 }
-                const int de = e_new - e;
                 if (wide && !apart) {
                     apart = true;
-                    m2 = m_use + (float)e;
+                    m_l = m_use;
                 }
-                e = e_new;
                 float scale_o = 1.f;
                 if (m_use == -INFINITY) {
-                    m_use = cm;
-                } else if (cm > m_use + kRescaleLog2) {
-                    scale_o = ex2_approx(m_use - cm);
-                    lsum *= scale_o;
-                    m_use = cm;
+                    m_use = cy;
+                } else if (cy > m_use + kRescaleLog2) {
+                    scale_o = ex2_approx(m_use - cy);
+                    m_use = cy;
                 }
-                if (apart) {
-                    cy += (float)e;
-                    scale_o = 1.f;
-                    if (m2 == -INFINITY) {
-                        m2 = cy;
-                    } else if (cy > m2 + kRescaleLog2) {
-                        scale_o = ex2_approx(m2 - cy);
-                        m2 = cy;
-                    }
-                } else {
-                    scale_o *= __uint_as_float((uint32_t)(127 - min(de, 126)) << 23);   // (de > 16 only at the first stage)
+                if (!apart) {
+                    lsum *= scale_o;
+                } else if (m_l == -INFINITY) {
+                    m_l = cm;
+                } else if (cm > m_l + kRescaleLog2) {
+                    lsum *= ex2_approx(m_l - cm);
+                    m_l = cm;
                 }
                 if (j > t.s0 && __any_sync(0xffffffffu, scale_o != 1.f)) {
                     // tcgen05.ld/st are warp-wide: lanes that keep their references scale by 1
@@ -778,7 +780,7 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                     }
                 }
                 const float mu = m_use == -INFINITY ? 0.f : m_use - kPLog2;
-                const float mu2 = m2 == -INFINITY ? 0.f : m2 - (float)e - kPLog2;
+                const float mu_l = !apart ? mu : m_l == -INFINITY ? 0.f : m_l - kPLog2;
                 float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
                 for (int c32 = 0; c32 < kKT / 32; ++c32) {       // (P of columns 32c.. lies over columns 16c..)
@@ -787,18 +789,14 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                     columns(c32, xs);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
+                        const float4 v = (apart ? evs : pfac)[c32 * 8 + i];
+                        const float vs4[4] = {v.x, v.y, v.z, v.w};
                         float w[4];
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            w[v] = ex2_approx(xs[4 * i + v] - mu);
-                            sums[v] += w[v];
-                        }
-                        if (apart) {
-                            const float4 f = pf[c32 * 8 + i];
-                            w[0] = ex2_approx(xs[4 * i] + f.x - mu2);
-                            w[1] = ex2_approx(xs[4 * i + 1] + f.y - mu2);
-                            w[2] = ex2_approx(xs[4 * i + 2] + f.z - mu2);
-                            w[3] = ex2_approx(xs[4 * i + 3] + f.w - mu2);
+                        for (int u = 0; u < 4; ++u) {
+                            const float wl = ex2_approx(xs[4 * i + u] - mu_l);
+                            sums[u] += wl;
+                            w[u] = apart ? ex2_approx(xs[4 * i + u] + vs4[u] - mu) : wl * vs4[u];
                         }
                         pk[2 * i] = pack_half2(w[0], w[1]);
                         pk[2 * i + 1] = pack_half2(w[2], w[3]);
@@ -824,9 +822,7 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
         if (alive && t.ntok[x] > 0) {
             tc_fence_after();
             // (a NaN sum stays NaN; a tile with no stage here or no visible key gives zeros)
-            const float f = !any || lsum == 0.f ? 0.f
-                                                : __frcp_rn(lsum) * (apart ? ex2_approx(m2 - m_use - (float)(kVLog2 + 127))
-                                                                           : q8_scale((uint32_t)e) * (1.f / (1 << kVLog2)));
+            const float f = !any || lsum == 0.f ? 0.f : __frcp_rn(lsum) * (apart ? ex2_approx(m_use - m_l) : 1.f);
             const int64_t orr = tok * p.hq + head;
             const int slot = piece_slot(p, blockIdx.x, t.u);
             const int64_t prow = (int64_t)slot * kChunkRows + x * 128 + r;
@@ -856,8 +852,8 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                 }
             }
             if (row_ok) {
-                const float lse = lsum != 0.f ? ((m_use == -INFINITY ? 0.f : m_use - kPLog2) + log2f(lsum)) *
-                                                    0.6931471805599453f
+                const float m = apart ? m_l : m_use;
+                const float lse = lsum != 0.f ? ((m == -INFINITY ? 0.f : m - kPLog2) + log2f(lsum)) * 0.6931471805599453f
                                               : -INFINITY;
                 if (!whole)
                     p.ws_lse[prow] = lse;

@@ -1,0 +1,50 @@
+"""Weights and values of very different magnitudes in the 8-bit cache's attentions, against 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+from .q8_common import attend, check
+from .q8_marked import SCALE, marked, queries, share
+
+pytestmark = pytest.mark.gpu
+
+
+def chunk_some(c, new, hq, requests, heads):
+    """Chunk attention of the whole batch, checked at some requests and KV heads."""
+    pool = c.pool()
+    q = queries(c, sum(new), hq)
+    out, lse = pool.chunk_attention(q, new, scale=SCALE, return_lse=True)
+    assert pool.check_errors() == 0
+    g = hq // c.hkv
+    for b in requests:
+        n, at = new[b], sum(new[:b])
+        k, v = c.rows(b)
+        limit = (torch.arange(n, device="cuda") + c.lens[b] - n + 1).repeat_interleave(g)
+        for h in heads:
+            s = slice(h * g, h * g + g)
+            o, e, to, te = attend(q[at: at + n, s].reshape(n * g, -1), k[:, h], v[:, h], SCALE, limit)
+            check(out[at: at + n, s].reshape(n * g, -1), o, to, f"out of request {b}, head {h}")
+            check(lse[at: at + n, s].reshape(-1), e, te, f"lse of request {b}, head {h}")
+
+
+@pytest.mark.parametrize("below", [8, 10, 12, 14])
+@pytest.mark.parametrize("L", [16384, 65536])
+def test_chunk_keeps_tokens_far_below_a_key_of_small_value(L, below):
+    """A first key 2^32 above the others, with a value 2^-below of theirs: the others are a part of the sum."""
+    c = marked([L], {(0, 0): (32.0, 127 - below, 0x78)}, 1, 128, 16, seed=50 + below)
+    chunk_some(c, [128], 8, [0], [0])
+
+
+@pytest.mark.parametrize("L,below", [(16384, 8), (16384, 10), (16384, 12), (16384, 14), (65536, 8), (65536, 12)])
+def test_whole_units_keep_them_too(L, below):
+    """As above with more units than work ranges: most are not split."""
+    c = share(marked([L], {(0, 0): (32.0, 127 - below, 0x78)}, 8, 128, 32, seed=60), 40)
+    chunk_some(c, [64] * 40, 32, [0, 23, 39], [0, 5])
+
+
+def test_marked_scores_are_what_they_say():
+    c = marked([40], {(0, 7): (32.0, 120, None), (0, 9): (-60.0, 127, None)}, 1, 64, 16, seed=1)
+    k, _ = c.rows(0)
+    bits = (k[:, 0, 0] * 8.0 * SCALE * np.log2(np.e)).cpu()
+    assert abs(bits[7] / 32 - 1) <= 2.0 ** -4 and abs(bits[9] / -60 - 1) <= 2.0 ** -4
+    assert not bits[[i for i in range(40) if i not in (7, 9)]].any()
