@@ -27,9 +27,10 @@
 // weight and little value, as an attention sink is, then lost 10% of a sum over
 // 131072 keys at s = 12.)  V exponents of -40 to 40 (row maxima of 2^-31 to 2^48)
 // keep l's terms between 2^-81 and 2^55, in fp32's range.  From the first
-// stage on that holds another one the piece is `wide`: l is then summed from a
-// second exponential, relative to a running maximum of x of its own.
-// Such a stage takes about twice the time.  Sums and O are fp32.
+// stage on that holds another one, or a zero row (scale byte 0), the piece is
+// `wide`: l is then summed from a second exponential, relative to a running
+// maximum of x of its own, and a key whose V is zero stays out of m.  Such a
+// stage takes about twice the time.  Sums and O are fp32.
 //
 // As in the bf16 kernel, a stage whose scores are all visible is
 // exponentiated against the running maximum without taking its own.  A quarter
@@ -298,7 +299,7 @@ __device__ void chunk_convert(const Q8ChunkParams &p, const Ctx &c)
                 const uint8_t *sc = c.smem + c.lay.scales + slot * 2 * kKT;
                 int top;                                 // the stage's largest V scale byte
                 // V exponents outside the window, by each warp for itself (NaN
-                // rows aside, and the least scale, whose rows count as zero)
+                // rows aside; zero rows have the least scale)
                 {
                     const int t4 = 4 * lane;
                     const uint32_t w = *reinterpret_cast<const volatile uint32_t *>(
@@ -310,7 +311,7 @@ __device__ void chunk_convert(const Q8ChunkParams &p, const Ctx &c)
                     for (int i = 0; i < 4; ++i) {
                         const int b = (int)((w >> (8 * i)) & 0xffu);
                         big = max(big, i < in && b != 255 ? b : 0);
-                        out = out || (i < in && b != 255 && b != 0 && abs(b - 127) > kVWindow);
+                        out = out || (i < in && b != 255 && abs(b - 127) > kVWindow);
                     }
                     wide = wide || __any_sync(0xffffffffu, out);
                     top = (int)__reduce_max_sync(0xffffffffu, (unsigned)big);
@@ -321,12 +322,24 @@ __device__ void chunk_convert(const Q8ChunkParams &p, const Ctx &c)
                 const int vb = *reinterpret_cast<const volatile uint8_t *>(mine + P);
                 // a NaN row of V counts as zero and makes its key's scores NaN
                 // instead, so that only rows that attend it see it
-                const bool live = valid && vb != 255 && vb != 0;
+                const uint8_t *codes = c.smem + c.lay.vring + (uint32_t)slot * kVSlotBytes + (uint32_t)t * 128u + kKT * 128;
+                bool zero = false;
+                if (valid && vb == 0) {                  // a row of zeros, or one of tiny values
+                    uint32_t any = 0;
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {        // (at head_dim 64 the upper half is zero)
+                        const uint4 w = reinterpret_cast<const uint4 *>(codes)[i];
+                        any |= w.x | w.y | w.z | w.w;
+                    }
+                    zero = (any & 0x7f7f7f7fu) == 0u;
+                }
+                const bool live = valid && vb != 255 && !zero;
                 const float nan = __uint_as_float(0x7fc00000u);
                 const int ev = live ? vb - 127 : -kVWindow;
                 reinterpret_cast<float *>(c.smem + c.lay.factor)[slot * kKT + t] =
                     !valid ? 0.f : vb == 255 ? nan : q8_scale((uint32_t)kb) * p.scale_log2;
-                // (where V counts as zero P may be zero too, and stays out of its reference)
+                // (where V is zero P may be zero too, and its key stays out of
+                // P's reference: the weights of the others keep their bits)
                 reinterpret_cast<float *>(c.smem + c.lay.evs)[slot * kKT + t] = wide && !live ? -INFINITY : (float)ev;
                 reinterpret_cast<float *>(c.smem + c.lay.pfactor)[slot * kKT + t] =
                     __uint_as_float((uint32_t)(127 + ev) << 23);                 // 2^ev (of no use where wide)

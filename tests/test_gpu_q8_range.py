@@ -42,6 +42,14 @@ def test_whole_units_keep_them_too(L, below):
     chunk_some(c, [64] * 40, 32, [0, 23, 39], [0, 5])
 
 
+@pytest.mark.parametrize("bits", [28.0, 44.0, 58.0, 88.0])
+@pytest.mark.parametrize("L,new", [(300, 128), (6000, 64)])
+def test_chunk_beside_a_leading_key_without_value(L, new, bits):
+    """A V row of zeros whose key leads by up to 61 nats: all of the output is the others'."""
+    c = marked([L, L], {(0, 3): (bits, 0, 0), (1, 0): (bits, 0, 0x80)}, 2, 128, 16, seed=70)
+    chunk_some(c, [new, new], 8, [0, 1], [0, 1])
+
+
 def test_marked_scores_are_what_they_say():
     c = marked([40], {(0, 7): (32.0, 120, None), (0, 9): (-60.0, 127, None)}, 1, 64, 16, seed=1)
     k, _ = c.rows(0)
