@@ -835,7 +835,11 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
         if (alive && t.ntok[x] > 0) {
             tc_fence_after();
             // (a NaN sum stays NaN; a tile with no stage here or no visible key gives zeros)
-            const float f = !any || lsum == 0.f ? 0.f : __frcp_rn(lsum) * (apart ? ex2_approx(m_use - m_l) : 1.f);
+            // (2^(m_use - m_l) in two halves: itself it can leave fp32's range, up to 2^129 or with 1 / l
+            // under 2^-126, where its product with O does not)
+            const bool none = !any || lsum == 0.f;
+            const float half = none || !apart ? 1.f : ex2_approx(0.5f * (m_use - m_l));
+            const float f = none ? 0.f : __frcp_rn(lsum) * half;
             const int64_t orr = tok * p.hq + head;
             const int slot = piece_slot(p, blockIdx.x, t.u);
             const int64_t prow = (int64_t)slot * kChunkRows + x * 128 + r;
@@ -848,7 +852,7 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                 float o[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    o[i] = __uint_as_float(ov[i]) * f;
+                    o[i] = __uint_as_float(ov[i]) * half * f;
                 if (row_ok && whole) {
                     uint4 *dst = reinterpret_cast<uint4 *>(p.out + orr * D + c16 * 16);
 #pragma unroll

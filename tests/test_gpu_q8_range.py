@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from .q8_common import attend, check
+from .q8_common import attend, check, check_chunk
 from .q8_marked import SCALE, marked, queries, share
 
 pytestmark = pytest.mark.gpu
@@ -48,6 +48,28 @@ def test_chunk_beside_a_leading_key_without_value(L, new, bits):
     """A V row of zeros whose key leads by up to 61 nats: all of the output is the others'."""
     c = marked([L, L], {(0, 3): (bits, 0, 0), (1, 0): (bits, 0, 0x80)}, 2, 128, 16, seed=70)
     chunk_some(c, [new, new], 8, [0, 1], [0, 1])
+
+
+@pytest.mark.parametrize("byte", [241, 244, 247])
+@pytest.mark.parametrize("L,new", [(300, 128), (6000, 64)])
+def test_chunk_of_the_largest_values(L, new, byte):
+    """Outputs up to bf16's largest, beside values 2^100 and more below: finite where the sum is."""
+    c = marked([L, L], {(0, 5): (40.0, byte, 0x77), (1, L - 150): (12.0, byte, 0xF7)}, 2, 128, 16, seed=71,
+               v_byte=100)
+    chunk_some(c, [new, new], 8, [0, 1], [0, 1])
+
+
+@pytest.mark.parametrize("new", [2, 16, 128])
+@pytest.mark.parametrize("v_byte", [0, 3, 60, 200])
+def test_values_of_one_magnitude_anywhere(new, v_byte):
+    """Caches whose values are all tiny (rows of the least scale, some of them zero) or all huge."""
+    c = marked([400, 3000], {(0, 3): (10.0, v_byte, None)}, 2, 64, 32, seed=74, v_byte=v_byte)
+    c.v[:, :, 7] = 0
+    pool = c.pool()
+    q = queries(c, 2 * new, 8)
+    out, lse = pool.chunk_attention(q, [new, new], scale=SCALE, return_lse=True)
+    assert pool.check_errors() == 0
+    check_chunk(c, q, [new, new], SCALE, out, lse)
 
 
 def test_marked_scores_are_what_they_say():
