@@ -1007,7 +1007,8 @@ __global__ void __launch_bounds__(256) shkv_q8_chunk_join_kernel(const __grid_co
 #pragma unroll 2
         for (int i = cut - 1; i <= last; ++i) {
             const int64_t slot = piece_slot(p, i, u);
-            const float w = ex2_approx((p.ws_lse[slot * kChunkRows + row] - M) * 1.4426950408889634f);
+            // (weights of 2^-10 at most: sums of outputs near fp32's largest stay below it)
+            const float w = ex2_approx((p.ws_lse[slot * kChunkRows + row] - M) * 1.4426950408889634f) * 0x1p-10f;
             const float4 v = reinterpret_cast<const float4 *>(p.ws_part)[((slot * 2 + x) * (D / 4) + c4) * 128 + r];
             wsum += w;
             acc.x += w * v.x;
@@ -1021,7 +1022,7 @@ __global__ void __launch_bounds__(256) shkv_q8_chunk_join_kernel(const __grid_co
     *reinterpret_cast<uint2 *>(p.out + orr * D + c4 * 4) =
         make_uint2(pack_bf16x2(acc.x * winv, acc.y * winv), pack_bf16x2(acc.z * winv, acc.w * winv));
     if (c4 == 0 && p.lse_out)
-        p.lse_out[orr] = wsum != 0.f ? M + logf(wsum) : -INFINITY;
+        p.lse_out[orr] = wsum != 0.f ? M + logf(wsum * 0x1p10f) : -INFINITY;
 }
 
 // tmK, tmV: 2-D maps of the code pools (box of 128 bytes x P rows, 128-byte swizzle).

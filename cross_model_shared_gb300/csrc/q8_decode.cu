@@ -1142,8 +1142,9 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                 }
 #pragma unroll
                 for (int m = 0; m < kMerge; ++m) {
-                    // (no piece has a key the row sees: weights of 0)
-                    const float w = M[m] == -INFINITY ? 0.f : ex2_approx((x[m] - M[m]) * 1.4426950408889634f);
+                    // (no piece has a key the row sees: weights of 0; else of 2^-10
+                    // at most: sums of outputs near fp32's largest stay below it)
+                    const float w = M[m] == -INFINITY ? 0.f : ex2_approx((x[m] - M[m]) * 1.4426950408889634f) * 0x1p-10f;
                     wsum[m] += w;
                     acc[m].x += w * v[m].x;
                     acc[m].y += w * v[m].y;
@@ -1163,7 +1164,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                         make_uint2(pack_bf16x2(acc[m].x * winv, acc[m].y * winv),
                                    pack_bf16x2(acc[m].z * winv, acc[m].w * winv));
                 if (lane == 0 && p.lse_out)
-                    p.lse_out[orr] = wsum[m] != 0.f ? M[m] + logf(wsum[m]) : -INFINITY;
+                    p.lse_out[orr] = wsum[m] != 0.f ? M[m] + logf(wsum[m] * 0x1p10f) : -INFINITY;
             }
         }
         if (threadIdx.x == 0)

@@ -72,6 +72,14 @@ def test_values_of_one_magnitude_anywhere(new, v_byte):
     check_chunk(c, q, [new, new], SCALE, out, lse)
 
 
+@pytest.mark.parametrize("new", [4, 64])
+def test_split_units_of_the_largest_values(new):
+    """Pieces whose outputs are all near bf16's largest are joined without an overflow."""
+    c = marked([20000], {}, 1, 128, 16, seed=76, v_byte=247)
+    c.v[:] = torch.where(torch.arange(128, device="cuda") % 3 == 0, 0xF7, 0x77).to(torch.uint8)
+    chunk_some(c, [new], 8, [0], [0])
+
+
 def test_marked_scores_are_what_they_say():
     c = marked([40], {(0, 7): (32.0, 120, None), (0, 9): (-60.0, 127, None)}, 1, 64, 16, seed=1)
     k, _ = c.rows(0)
