@@ -13,8 +13,8 @@
 //   y[t, r]    = S^T[t, r] * 2^ek[t] * 2^eq[r] * scale * log2(e) + ev[t]
 //   P^T[t, r]  = 2^(y - m[r] + 7),  m[r] a running maximum of y    fp16
 //   O^T[d, r] += sum_t 2^-8 v8[t, d] P^T[t, r]                    kind::f16
-//   l[r]      += sum_t P^T[t, r] * 2^(E - ev[t])                  (P before its rounding)
-//   out = O^T * 2^(E + 8) / l,   lse = ln2 * (m - 7 - E + log2(l))
+//   l[r]      += sum_t P^T[t, r] * 2^-ev[t]                       (P before its rounding)
+//   out = 256 O^T / l,   lse = ln2 * (m - 7 + log2(l))
 //
 // K's codes go to the tensor cores as they lie in the page.  A bf16 query has
 // 8 significant bits: its row is scaled by a power of two to at most 448 and
@@ -24,13 +24,16 @@
 // relative to the row's largest weight times value scale, so that fp16 holds
 // 11 bits of every token that matters to the sum, whatever the magnitudes of
 // weights and values apart: fp16's least step, 2^-24, is 2^-31 of that
-// largest, and 2^20 tokens below it are lost to 2^-12 of it.  E, a running
-// upper bound (at least 2^-67) of the V exponents of the segment's keys that
-// every row sees, keeps the fp32 sums l at 2^7 or more; a draft's key, which
-// some rows only see, may exceed it by 2^100.  A token whose V exponent is
-// under E - 60 takes part in l with exponent E - 60 and not in O (P = 0), which
-// bounds l's terms by 2^75; where E rises over tokens already summed, m is kept high enough for
-// 2^97 (b[r] is that bound).  Sums and O are fp32.
+// largest, and 2^20 tokens below it are lost to 2^-12 of it.  V exponents of
+// -40 to 40 (row maxima of 2^-31 to 2^48) keep P before its rounding at 2^-81 and
+// more for the largest weight, and l's terms under 2^55.  From the first stage
+// on that holds another one, or a zero row (scale byte 0), the segment is `wide`
+// (each softmax group for itself): l is then summed from a second exponential,
+// relative to a running maximum of y - ev of its own, and a token whose V is
+// zero stays out of m.  Its exponents then bound nothing, however far weights
+// and values lie apart in either direction.  Such a stage is slow (loops over
+// eight rows, four meetings of the group's warps); ordinary caches have none.
+// Sums and O are fp32.
 //
 // The softmax is bound by the latency of its chain, not by its instructions:
 // up to 48 rows its two groups of four warps take alternate stages, each with
@@ -87,11 +90,7 @@ constexpr uint32_t kColS = 0;               // S^T buffers at columns 0 and 64
 constexpr uint32_t kColO = 128;             // O^T
 constexpr float kRescaleLog2 = 8.f;         // m lags the maximum by at most this
 constexpr float kPLog2 = 7.f;               // P is 2^7 at the running maximum: 2^15 at most
-constexpr int kMinE = 60;                   // scale byte of the least E
-constexpr int kEHeadroom = 4;               // E moves to this much above a stage's largest V exponent
-constexpr int kVWindow = 60;                // V exponents under E - 60 count as zero values
-constexpr float kTermLog2 = kVWindow + kRescaleLog2;   // a new term of l is at most 2^(this + 7)
-constexpr float kMaxTermLog2 = 90.f;        // ... and stays at most 2^(this + 7): 2^20 of them fit fp32
+constexpr int kVWindow = 40;                // V exponents outside -kVWindow .. kVWindow make a segment wide
 constexpr uint32_t kKSlotBytes = kTT * 128;
 constexpr uint32_t kVSlotBytes = 2 * kTT * 128;
 constexpr uint32_t kPBytes = kTT * 128;
@@ -102,11 +101,13 @@ constexpr uint32_t kSoftmaxRegs = 168, kOtherRegs = 88;
 static_assert(kSoftmaxRegs * 256 + kOtherRegs * 256 == 128 * kThreads, "register split");
 
 // scratch rows of 64 words: per softmax group the stage maxima and the sums
-// [token group], the new 7 - m, the rescaling of O and of l, m, the bound b;
-// then the factors of the two groups at the segment's end, the queries'
-// scales, the rows' output offsets and the groups' E at the segment's end
-constexpr int kScrMax = 0, kScrNew = 4, kScrAlpha = 5, kScrAlphaL = 6, kScrM = 7, kScrB = 8, kScrGroup = 9;
-constexpr int kScrEnd = 2 * kScrGroup, kScrQ = kScrEnd + 2, kScrOff = kScrQ + 1, kScrE = kScrOff + 1, kScrRows = kScrE + 1;
+// [token group], the new 7 - m, the rescaling of O and l, m, and for a wide
+// segment the sum of its wide stages, its reference, and m before them; then
+// the factors of the two groups at the segment's end (two halves each), the
+// queries' scales, the rows' output offsets and whether the groups went wide
+constexpr int kScrMax = 0, kScrNew = 4, kScrAlpha = 5, kScrM = 6, kScrL = 7, kScrMl = 8, kScrM0 = 9, kScrGroup = 10;
+constexpr int kScrEnd = 2 * kScrGroup, kScrQ = kScrEnd + 4, kScrOff = kScrQ + 1, kScrWide = kScrOff + 1,
+              kScrRows = kScrWide + 1;
 
 __host__ __device__ constexpr int q_nr(int rows) { return (rows + 15) / 16 * 16; }
 // N of the PV MMA: 48 is rounded up to a whole 64-column swizzle span.
@@ -187,20 +188,20 @@ __device__ __forceinline__ uint32_t scale_off(int t, int log2P)
     return (uint32_t)(((t >> log2P) << (log2P + 1)) + (t & ((1 << log2P) - 1)));
 }
 
-// Largest V scale byte of the stage's tokens below `n` on copied pages (NaN
-// rows, 255, aside), by a warp; 0 if there are none.  w: the V scales of the
-// lane's four tokens.
-__device__ __forceinline__ int stage_top_scale(uint32_t w, int n, uint32_t mask, int log2P)
+// Whether the stage's tokens below `n` on copied pages hold a V exponent outside
+// the window (NaN rows, 255, aside), by a warp.  w: the V scales of the lane's
+// four tokens.
+__device__ __forceinline__ bool stage_outside(uint32_t w, int n, uint32_t mask, int log2P)
 {
     const int t = 4 * (threadIdx.x & 31);
     const int in = ((mask >> (t >> log2P)) & 1u) ? n - t : 0;
-    uint32_t top = 0;
+    bool out = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t b = i < in ? (w >> (8 * i)) & 0xffu : 0u;
-        top = max(top, b == 255u ? 0u : b);
+        const int b = (int)((w >> (8 * i)) & 0xffu);
+        out = out || (i < in && b != 255 && abs(b - 127) > kVWindow);
     }
-    return (int)__reduce_max_sync(0xffffffffu, top);
+    return __any_sync(0xffffffffu, out);
 }
 
 // Keys below this are seen by every row of the unit.
@@ -209,9 +210,6 @@ __device__ __forceinline__ int keys_all_see(const Q8DecodeParams &q, const Segme
     const int L = plan_len(q.d, s);
     return q.causal ? L - q.n_q[s.b] + 1 : L;
 }
-
-// E (as a scale byte) from the one before and a stage's largest scale byte.
-__device__ __forceinline__ int next_e(int e, int top) { return top > e ? min(top + kEHeadroom, 254) : e; }
 
 // D[tmem] (+)= A[smem] . B[smem]^T on e4m3 / on fp16 operands, fp32 accumulate.
 __device__ __forceinline__ void umma_f8(uint32_t d_taddr, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -409,24 +407,24 @@ __device__ void warm_l2_q8(const CUtensorMap *tm, const DecodeParams &p, const C
     }
 }
 
-// What a token brings to the softmax: (score factor, V exponent, factor of l,
+// What a token brings to the softmax: (score factor, V exponent ev, 2^-ev,
 // first row that sees it | kMasked if some token of the warp is not seen by all
-// | kNoValue if its V counts as zero | E << 16).  kb, vb: the token's scale
-// bytes; at: its distance from the first key some row does not
-// see; e: E with the token's stage.  A NaN row of V makes its key's scores NaN,
-// so that only rows that attend it see it.
-constexpr int kMasked = 0x100, kNoValue = 0x200;
-__device__ __forceinline__ float4 token_factors(const DecodeParams &p, int kb, int vb, bool valid, int at, int e)
+// | kWide if the stage holds a V exponent outside the window).  kb, vb: the
+// token's scale bytes; at: its distance from the first key some row does not
+// see.  A NaN row of V makes its key's scores NaN, so that only rows that attend
+// it see it.
+constexpr int kMasked = 0x100, kWide = 0x200;
+__device__ __forceinline__ float4 token_factors(const DecodeParams &p, int kb, int vb, bool valid, int at, bool outside)
 {
-    const int ve = !valid || vb == 255 ? e : max(vb, e - kVWindow);
+    const int ve = !valid || vb == 255 ? 127 : vb;
     // rows from row_min on see the token (new token i from position L - n + i on)
     const int row_min = valid ? min(64, max(0, (at + 1) * p.group)) : 64;
-    const int flags = (__any_sync(0xffffffffu, row_min > 0) ? kMasked : 0) | (ve > vb ? kNoValue : 0);
+    const int flags = (__any_sync(0xffffffffu, row_min > 0) ? kMasked : 0) | (outside ? kWide : 0);
     float4 f;
     f.x = !valid ? 0.f : vb == 255 ? __uint_as_float(0x7fc00000u) : q8_scale((uint32_t)kb) * p.scale_log2;
     f.y = (float)(ve - 127);
-    f.z = __uint_as_float((uint32_t)max(127 + e - ve, 1) << 23);
-    f.w = __int_as_float(row_min | flags | (e << 16));
+    f.z = __uint_as_float((uint32_t)(254 - ve) << 23);
+    f.w = __int_as_float(row_min | flags);
     return f;
 }
 
@@ -434,7 +432,7 @@ __device__ __forceinline__ float4 token_factors(const DecodeParams &p, int kb, i
 // V conversion
 // ---------------------------------------------------------------------------
 // Every code becomes fp16, whatever its token: the bits give finite values, and
-// where a token is not seen or its V counts as zero P is 0.
+// where a token is not seen P is 0.
 template <int NR>
 __device__ void convert_v(const Q8DecodeParams &q, const Ctx4 &c)
 {
@@ -463,11 +461,10 @@ __device__ void convert_v(const Q8DecodeParams &q, const Ctx4 &c)
         const int tok_end = s.p1 * P;
         const int lim = min(plan_len(p, s), tok_end);
         const int all_see = keys_all_see(q, s);
-        int e = kMinE;                                   // scale byte of E
 #pragma unroll 1
         for (int tok0 = s.p0 * P; tok0 < tok_end; tok0 += kTT, ++k) {
             if (!kPing) {
-                // --- E and the token's factors (up to 48 rows the softmax's warps
+                // --- the token's factors (up to 48 rows the softmax's warps
                 // have the time to find them).  (Entry k % kInfo was last used by
                 // stage k - kVS - 1, whose PV was done before V(k - 1) was loaded.)
                 const uint32_t entry = k % kInfo;
@@ -484,9 +481,9 @@ __device__ void convert_v(const Q8DecodeParams &q, const Ctx4 &c)
                 const int so = sring.slot * 2 * kTT;
                 const uint32_t four = *reinterpret_cast<const volatile uint32_t *>(sc_four + so);
                 const int kb = *(const volatile uint8_t *)(sc_mine + so), vb = *(const volatile uint8_t *)(sc_mine + so + P);
-                e = next_e(e, stage_top_scale(four, min(lim, all_see) - tok0, mask, log2P));
                 const bool valid = alive && tok0 + t < lim && ((mask >> page) & 1u);
-                const float4 f = token_factors(p, kb, vb, valid, tok0 + t - all_see, e);
+                const float4 f = token_factors(p, kb, vb, valid, tok0 + t - all_see,
+                                               stage_outside(four, lim - tok0, mask, log2P));
                 if (alive)
                     reinterpret_cast<float4 *>(c.smem + L.info)[entry * kTT + t] = f;
                 __syncwarp();
@@ -728,6 +725,137 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
         }
     };
 
+    // A stage of a wide segment (see the top), eight rows at a time: short loops
+    // with their state in shared memory, as the common stage has the registers.
+    // first: the segment's first such stage of the group; has_o: O holds
+    // earlier stages; pv_par: parity of the group's previous product.
+    auto wide_stage = [&](const float4 &f, int row_min, bool first, bool has_o, int k, uint32_t pv_par, uint8_t *prow) {
+        const int r = kPing ? t : (int)threadIdx.x;      // the row this thread keeps, below NR
+        // V's codes, where the scale alone does not tell a zero row from one of tiny values
+        wait(bar_at(c, kConvV + k % kVS), (uint32_t)(k / kVS) & 1u);
+        bool zero = false;
+        if (alive && f.y == -127.f) {
+            const uint8_t *row = c.smem + L.vring + (uint32_t)(k % kVS) * kVSlotBytes + (uint32_t)t * 128u;
+            uint32_t any = 0;
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(row + (i >> 3) * (kTT * 128) + (i & 7) * 16);
+                any |= w.x | w.y | w.z | w.w;
+            }
+            zero = (any & 0x7fff7fffu) == 0u;
+        }
+        const float ev = zero ? -INFINITY : f.y;
+        // y - ev of rows chunk_col(ch) .. + 7, -inf where not seen
+        auto scores8 = [&](int ch, float (&x)[8]) {
+            uint32_t sv[8];
+            tmem_ld8_nowait(tmem + lane_base + kColS + (uint32_t)((k & 1) * 64 + chunk_col(ch)), sv);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int row = chunk_col(ch) + i;
+                x[i] = row < row_min ? -INFINITY : __uint_as_float(sv[i]) * (f.x * scr[kScrQ * 64 + row]);
+            }
+        };
+        // the warp's maxima of x + add over its tokens -> kScrMax
+        auto maxima = [&](float add) {
+#pragma unroll 1
+            for (int ch = 0; ch < NH / 8; ++ch) {
+                float x[8];
+                scores8(ch, x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[i] += add;
+                ReduceScatter<8, 16, true>::run(x, lane);
+                if (rs_owner<8>(lane))
+                    mine[(kScrMax + tg) * 64 + chunk_col(ch) + rs_base<8>(lane)] = x[0];
+            }
+        };
+        // the row's reference from the one before and kScrMax
+        auto moved = [&](float old) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < kTokenGroups; ++g)
+                top = fmaxf(top, mine[(kScrMax + g) * 64 + r]);
+            return old == -INFINITY || top > old + kRescaleLog2 ? top : old;
+        };
+        maxima(ev);
+        named_barrier(bar_id, bar_threads);
+        bool moves = false;
+        if (r < NR) {
+            const float mo = mine[kScrM * 64 + r], mn = moved(mo);
+            if (first) {
+                mine[kScrM0 * 64 + r] = mine[kScrMl * 64 + r] = mo;
+                mine[kScrL * 64 + r] = 0.f;
+            }
+            moves = mn != mo;
+            mine[kScrAlpha * 64 + r] = moves ? ex2_approx(mo - mn) : 1.f;
+            mine[kScrM * 64 + r] = mn;
+        }
+        if (bar_red_or(bar_id, bar_threads, moves) && has_o) {
+            wait(bar_at(c, kPvDone + grp), pv_par);
+            if (alive) {
+                tc_fence_after();
+#pragma unroll 1
+                for (int ch = 0; ch < NH / 8; ++ch) {
+                    const uint32_t col = tmem + lane_base + kColO + (uint32_t)(grp * 64 + chunk_col(ch));
+                    uint32_t ov[8];
+                    tmem_ld8_nowait(col, ov);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        ov[i] = __float_as_uint(__uint_as_float(ov[i]) * mine[kScrAlpha * 64 + chunk_col(ch) + i]);
+                    tmem_st8_nowait(col, ov);
+                }
+                tmem_wait_st();
+            }
+        }
+        maxima(0.f);
+        named_barrier(bar_id, bar_threads);
+        if (r < NR) {
+            const float ml = mine[kScrMl * 64 + r], mn = moved(ml);
+            if (mn != ml)
+                mine[kScrL * 64 + r] *= ex2_approx(ml - mn);
+            mine[kScrMl * 64 + r] = mn;
+        }
+        named_barrier(bar_id, bar_threads);
+        if (k >= (kPing ? 2 : 1))
+            wait(bar_at(c, kPvDone + grp), pv_par);
+#pragma unroll 1
+        for (int ch = 0; ch < NH / 8; ++ch) {
+            float x[8], w[8];
+            scores8(ch, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float m = mine[kScrM * 64 + chunk_col(ch) + i], ml = mine[kScrMl * 64 + chunk_col(ch) + i];
+                w[i] = ex2_approx(x[i] + ev - (m == -INFINITY ? 0.f : m - kPLog2));
+                x[i] = ex2_approx(x[i] - (ml == -INFINITY ? 0.f : ml - kPLog2));
+            }
+            if (alive)
+                *reinterpret_cast<uint4 *>(prow + (((chunk_col(ch) / 8) ^ (t & 7)) << 4)) =
+                    make_uint4(pack_half2(w[0], w[1]), pack_half2(w[2], w[3]), pack_half2(w[4], w[5]),
+                               pack_half2(w[6], w[7]));
+            ReduceScatter<8, 16, false>::run(x, lane);
+            if (rs_owner<8>(lane))
+                mine[(kScrMax + tg) * 64 + chunk_col(ch) + rs_base<8>(lane)] = x[0];
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(bar_at(c, kSFree + (k & 1)));
+            mbar_arrive(bar_at(c, kPFull + grp));
+        }
+        named_barrier(bar_id, bar_threads);
+        if (r < NR) {
+            float sum = mine[kScrL * 64 + r];
+#pragma unroll
+            for (int g = 0; g < kTokenGroups; ++g)
+                sum += mine[(kScrMax + g) * 64 + r];
+            mine[kScrL * 64 + r] = sum;
+        }
+        named_barrier(bar_id, bar_threads);
+    };
+
     int kbase = 0, seg = 0;
     Segment s = locate(p, c.cta_begin, c.cta_end);
     stage_q(0, s);
@@ -735,7 +863,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
     for (;;) {
         const int nst = stages_of(s, P);
         const int R = q.n_q[s.b] * p.group;
-        int e = kMinE;                          // scale byte of E
+        bool wide = false;                      // for the group's stages from here on
         float2 nmu[kNmRegs ? NH / 2 : 1], l[NH / 2];   // 7 - m (1e30: no key yet), and this token's share of l
 #pragma unroll
         for (int i = 0; i < NH / 2; ++i) {
@@ -747,7 +875,6 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 scr[(g * kScrGroup + kScrM) * 64 + threadIdx.x] = -INFINITY;
-                scr[(g * kScrGroup + kScrB) * 64 + threadIdx.x] = kTermLog2;
                 scr[(g * kScrGroup + kScrNew) * 64 + threadIdx.x] = 1e30f;
             }
         named_barrier(kAllBar, kSoftmaxThreads);   // the rows' scales and initial maxima are in place
@@ -761,14 +888,10 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
             // the token's factors and S^T
             float4 f;
             if (kPing) {
-                // E moves with the other group's stage before, too; its scales
-                // landed before this stage's (an arrival of the copies' waits
-                // for all copies before it)
-                const int slot = k % kScaleRing, prev = (k - 1) & (kScaleRing - 1);
+                const int slot = k % kScaleRing;
                 wait(bar_at(c, kScaleB + slot), (uint32_t)(k / kScaleRing) & 1u);
                 const uint8_t *sc = c.smem + L.scales + slot * 2 * kTT + scale_off(t, log2P);
-                const uint32_t mask = meta[slot], mask0 = j > 0 ? meta[prev] : 0u;
-                const uint32_t four0 = *reinterpret_cast<const volatile uint32_t *>(sc_four + prev * 2 * kTT);
+                const uint32_t mask = meta[slot];
                 const uint32_t four = *reinterpret_cast<const volatile uint32_t *>(sc_four + slot * 2 * kTT);
                 const int kb = *(const volatile uint8_t *)sc, vb = *(const volatile uint8_t *)(sc + P);
                 if (alive && (mask >> 8) != ((uint32_t)k & 0xffffffu)) {
@@ -778,21 +901,19 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                     }
                     alive = false;
                 }
-                const int tok0 = tok_first + j * kTT, seen = min(lim, all_see) - tok0;
-                const int top0 = stage_top_scale(four0, seen + kTT, mask0 & 0xffu, log2P);
-                const int top = stage_top_scale(four, seen, mask & 0xffu, log2P);
+                const int tok0 = tok_first + j * kTT;
                 f = token_factors(p, kb, vb, tok0 + t < lim && ((mask >> (t >> log2P)) & 1u), tok0 + t - all_see,
-                                  next_e(next_e(e, top0), top));
+                                  stage_outside(four, lim - tok0, mask & 0xffu, log2P));
             }
             if (wait(bar_at(c, kSFull + buf), (uint32_t)((k >> 1) & 1)))
                 tc_fence_after();
             if (!kPing)
                 f = reinterpret_cast<const float4 *>(c.smem + L.info)[(k % kInfo) * kTT + t];
-            const int w4 = alive ? __float_as_int(f.w) : 64 | kMasked | e << 16;
+            const int w4 = alive ? __float_as_int(f.w) : 64 | kMasked;
             const int row_min = w4 & 0xff;
             const bool masked = (w4 & kMasked) != 0;     // for some token of the warp
-            const int de = (w4 >> 16) - e;
-            e = w4 >> 16;
+            uint8_t *prow = c.smem + L.pbuf + (uint32_t)grp * kPBytes + (uint32_t)t * 128u;
+            const uint32_t pv_par = (uint32_t)(((kPing ? k >> 1 : k) - 1) & 1);   // of the group's previous product
             // y - m + 7 of this thread's rows (nm = 7 - m), -inf where not seen
             float2 d[NH / 2];
             auto scores = [&](bool relative) {       // (or y itself)
@@ -838,13 +959,26 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                         d[o].y = row_of(2 * o + 1) < row_min ? -INFINITY : d[o].y;
                     }
             };
-            scores(true);
-            float top = -INFINITY;
+            bool go_wide = wide, refresh = false;
+            if (!wide) {
+                scores(true);
+                float top = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < NH / 2; ++i)
-                top = fmaxf(top, fmaxf(d[i].x, d[i].y));
-            // --- lazy refresh of the maxima: all warps of the stage agree
-            if (bar_red_or(bar_id, bar_threads, top > kPLog2 + kRescaleLog2 || de > 0)) {
+                for (int i = 0; i < NH / 2; ++i)
+                    top = fmaxf(top, fmaxf(d[i].x, d[i].y));
+                // all warps of the stage agree, also where one of them gave up waiting
+                const bool outside = (w4 & kWide) != 0;
+                refresh = bar_red_or(bar_id, bar_threads, top > kPLog2 + kRescaleLog2 || outside);
+                if (refresh)
+                    go_wide = bar_red_or(bar_id, bar_threads, outside);
+            }
+            if (go_wide) {
+                wide_stage(f, row_min, !wide, j > j0, k, pv_par, prow);
+                wide = true;
+                continue;
+            }
+            // --- lazy refresh of the maxima
+            if (refresh) {
                 scores(false);
                 {
                     constexpr int M = pow2_at_least(NH);
@@ -868,20 +1002,14 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
 #pragma unroll
                     for (int g = 0; g < kTokenGroups; ++g)
                         mn = fmaxf(mn, mine[(kScrMax + g) * 64 + r]);
-                    if (mo != -INFINITY) {
-                        const float b = mine[kScrB * 64 + r] + (float)de;
-                        mn = fmaxf(mn, mo + (b - kMaxTermLog2));
-                        mine[kScrB * 64 + r] = fmaxf(b - (mn - mo), kTermLog2);
-                    }
                     mine[kScrNew * 64 + r] = mn == -INFINITY ? 1e30f : kPLog2 - mn;
                     mine[kScrAlpha * 64 + r] = mn == -INFINITY ? 1.f : ex2_approx(mo - mn);
-                    mine[kScrAlphaL * 64 + r] = mn == -INFINITY ? 1.f : ex2_approx(mo - mn + (float)de);
                     mine[kScrM * 64 + r] = mn;
                 }
                 named_barrier(bar_id, bar_threads);
                 if (j > j0) {
                     // O^T holds the group's stages before: rescale this thread's part once their PV is done
-                    wait(bar_at(c, kPvDone + grp), (uint32_t)(((kPing ? k >> 1 : k) - 1) & 1));
+                    wait(bar_at(c, kPvDone + grp), pv_par);
                     if (alive) {
                         tc_fence_after();
 #pragma unroll
@@ -905,7 +1033,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                     if (kNmRegs)
                         nmu[kNmRegs ? i : 0] = nm;
                     d[i] = __fadd2_rn(d[i], nm);
-                    l[i] = __fmul2_rn(l[i], make_float2(mine[kScrAlphaL * 64 + rr], mine[kScrAlphaL * 64 + rr + 1]));
+                    l[i] = __fmul2_rn(l[i], make_float2(mine[kScrAlpha * 64 + rr], mine[kScrAlpha * 64 + rr + 1]));
                 }
             }
             tc_fence_before();
@@ -919,15 +1047,10 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                 l[i] = __ffma2_rn(pe, make_float2(f.z, f.z), l[i]);
                 pk[i] = pack_half2(pe.x, pe.y);
             }
-            if (w4 & kNoValue)
-#pragma unroll
-                for (int i = 0; i < NH / 2; ++i)
-                    pk[i] = 0u;
             // --- P^T, once the group's previous product has read the buffer
             if (k >= (kPing ? 2 : 1))
-                wait(bar_at(c, kPvDone + grp), (uint32_t)(((kPing ? k >> 1 : k) - 1) & 1));
+                wait(bar_at(c, kPvDone + grp), pv_par);
             if (alive) {
-                uint8_t *prow = c.smem + L.pbuf + (uint32_t)grp * kPBytes + (uint32_t)t * 128u;
 #pragma unroll
                 for (int ch = 0; ch < NH / 8; ++ch)
                     *reinterpret_cast<uint4 *>(prow + (((chunk_col(ch) / 8) ^ (t & 7)) << 4)) =
@@ -966,7 +1089,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                         mine[(kScrMax + tg) * 64 + row_of(base + jj)] = v[jj];
         }
         if (t == 0 && (kPing || warp == 0))
-            *reinterpret_cast<int *>(scr + kScrE * 64 + grp) = e;
+            *reinterpret_cast<int *>(scr + kScrWide * 64 + grp) = wide;
         named_barrier(kAllBar, kSoftmaxThreads);
         const bool whole = (s.seg_begin == s.unit_begin) && (s.seg_end == s.unit_end);
         const int slot_id = whole ? 0 : 2 * (int)blockIdx.x + (s.seg_begin == c.cta_begin ? 0 : 1);
@@ -974,39 +1097,42 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
         const int *rowoff = scr_i + kScrOff * 64;
         if (threadIdx.x < NR) {
             const int r = threadIdx.x;
-            // the groups' parts, relative to the larger maximum and E
-            float m[2], a[2], w[2];
-            int eg[2];
+            // the groups' parts, relative to the larger reference of their sums
+            float m[2], a[2], ref[2];
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 const float *o = scr + g * kScrGroup * 64;
-                m[g] = kPing || g == 0 ? o[kScrM * 64 + r] : -INFINITY;
-                eg[g] = kPing || g == 0 ? scr_i[kScrE * 64 + g] : 0;
+                m[g] = ref[g] = -INFINITY;
                 a[g] = 0.f;
-                if (kPing || g == 0)
+                if (kPing || g == 0) {
+                    m[g] = ref[g] = o[kScrM * 64 + r];
 #pragma unroll
                     for (int i = 0; i < kTokenGroups; ++i)
                         a[g] += o[(kScrMax + i) * 64 + r];
+                    if (scr_i[kScrWide * 64 + g]) {
+                        // what was summed before, relative to m as it was then
+                        const float m0 = o[kScrM0 * 64 + r];
+                        ref[g] = o[kScrMl * 64 + r];
+                        a[g] = o[kScrL * 64 + r] + (m0 == -INFINITY ? a[g] : a[g] * ex2_approx(m0 - ref[g]));
+                    }
+                }
             }
-            const int ee = max(eg[0], eg[1]);
-            float mm = fmaxf(m[0], m[1]);
-#pragma unroll
-            for (int g = 0; g < 2; ++g)              // (and high enough for l's terms under the larger E)
-                mm = fmaxf(mm, m[g] + (float)(ee - eg[g] - 20));
+            const float mm = fmaxf(ref[0], ref[1]);
             float sum = 0.f;
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                // (a sum of NaN keeps its weight: its m may be -inf)
-                w[g] = m[g] == -INFINITY ? (a[g] != 0.f ? 1.f : 0.f) : ex2_approx(m[g] - mm);
-                sum += m[g] == -INFINITY ? a[g] : a[g] * ex2_approx(m[g] - mm + (float)(ee - eg[g]));
-            }
-            const float inv = sum != 0.f ? __frcp_rn(sum) : 0.f;     // (a NaN sum stays NaN)
-            const float ef = q8_scale((uint32_t)ee);
-#pragma unroll
             for (int g = 0; g < 2; ++g)
-                scr[(kScrEnd + g) * 64 + r] = w[g] * inv * ef;
+                sum += ref[g] == -INFINITY ? a[g] : a[g] * ex2_approx(ref[g] - mm);
+            const float inv = sum != 0.f ? __frcp_rn(sum) : 0.f;     // (a NaN sum stays NaN)
+            // 2^(m - mm), in two halves: itself it can leave fp32's range, up to 2^135 or under
+            // 2^-126, where its product with O does not
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const float half = m[g] == -INFINITY ? 0.f : ex2_approx(0.5f * (m[g] - mm));
+                scr[(kScrEnd + 2 * g) * 64 + r] = half * inv;
+                scr[(kScrEnd + 2 * g + 1) * 64 + r] = half;
+            }
             if (alive && r < R) {
-                const float lse = sum != 0.f ? ((mm == -INFINITY ? 0.f : mm - kPLog2) - (float)(ee - 127) + log2f(sum)) * kLn2
+                const float lse = sum != 0.f ? ((mm == -INFINITY ? 0.f : mm - kPLog2) + log2f(sum)) * kLn2
                                              : -INFINITY;
                 if (whole) {
                     if (p.lse_out)
@@ -1036,7 +1162,8 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                 tmem_ld_half<NE>(tmem + lane_base + kColO + (uint32_t)(g * 64), hh, ov);
 #pragma unroll
                 for (int i = 0; i < NE; ++i)
-                    o[i] = fmaf(__uint_as_float(ov[i]) * 256.f, scr[(kScrEnd + g) * 64 + half_row(hh, i)], o[i]);
+                    o[i] = fmaf(__uint_as_float(ov[i]) * 256.f * scr[(kScrEnd + 2 * g + 1) * 64 + half_row(hh, i)],
+                                scr[(kScrEnd + 2 * g) * 64 + half_row(hh, i)], o[i]);
             }
         }
         if (alive && t < D) {

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from .q8_common import attend, check, check_chunk
+from .q8_common import attend, check, check_chunk, check_decode
 from .q8_marked import SCALE, marked, queries, share
 
 pytestmark = pytest.mark.gpu
@@ -78,6 +78,34 @@ def test_split_units_of_the_largest_values(new):
     c = marked([20000], {}, 1, 128, 16, seed=76, v_byte=247)
     c.v[:] = torch.where(torch.arange(128, device="cuda") % 3 == 0, 0xF7, 0x77).to(torch.uint8)
     chunk_some(c, [new], 8, [0], [0])
+
+
+ROWS = [(1, 16, 2), (3, 16, 2), (5, 16, 2), (8, 16, 2)]      # 8, 24, 40 and 64 rows a KV head
+
+
+@pytest.mark.parametrize("N_,hq,hkv", ROWS)
+@pytest.mark.parametrize("bits,above", [(-30.0, 44), (-60.0, 52), (-72.0, 60), (-88.0, 70), (-100.0, 70), (-120.0, 100)])
+def test_decode_beside_a_large_value_of_little_weight(N_, hq, hkv, bits, above):
+    """A token's value is far above the others' and its weight farther below: the output is the others'."""
+    lens = [700, 9000, 260]
+    c = marked(lens, {(b, lens[b] // 2): (bits, 127 + above, None) for b in range(3)}, hkv, 128, 16, seed=72)
+    pool = c.pool()
+    q = queries(c, 3, N_ * hq)
+    out, lse = pool.decode_attention(q, N_, scale=SCALE, return_lse=True)
+    assert pool.check_errors() == 0
+    check_decode(c, q, N_, SCALE, out, lse)
+
+
+@pytest.mark.parametrize("N_,hq,hkv", ROWS)
+@pytest.mark.parametrize("bits", [28.0, 58.0, 80.0])
+def test_decode_beside_a_leading_key_without_value(N_, hq, hkv, bits):
+    lens = [700, 9000, 260]
+    c = marked(lens, {(0, 5): (bits, 0, 0), (1, 4000): (bits, 0, 0x80), (2, 259): (bits, 0, 0)}, hkv, 128, 16, seed=73)
+    pool = c.pool()
+    q = queries(c, 3, N_ * hq)
+    out, lse = pool.decode_attention(q, N_, scale=SCALE, return_lse=True)
+    assert pool.check_errors() == 0
+    check_decode(c, q, N_, SCALE, out, lse)
 
 
 def test_marked_scores_are_what_they_say():
