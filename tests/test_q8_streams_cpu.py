@@ -1,0 +1,86 @@
+"""Which tensors the 8-bit cache's Python calls hold back for the stream they run on, without a device: the C
+entry points and torch's streams are replaced by fakes."""
+import pytest
+import torch
+
+from cross_model_shared_gb300 import q8
+
+
+class Fake:
+    """Records what was held back for which stream, and when the entry points were called."""
+
+    def __init__(self):
+        self.events, self.raw, self.capturing = [], 7, False
+
+    def entry(self, name):
+        return lambda *a: self.events.append(name)
+
+    def held(self):
+        return [e[1:] for e in self.events if e[0] == "hold"]
+
+
+class Watched(torch.Tensor):
+    def record_stream(self, stream):
+        self.fake.events.append(("hold", self.label, stream))
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    f = Fake()
+    for name in ("append_kv", "read_kv", "decode_attention", "chunk_attention"):
+        monkeypatch.setattr(q8.N, f"shkv_q8_{name}", f.entry(name))
+    monkeypatch.setattr(q8, "_raw_stream", lambda index: f.raw)
+    monkeypatch.setattr(q8, "_current_device", lambda: None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: f"stream {f.raw}")
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: f.capturing)
+    return f
+
+
+@pytest.fixture
+def pool(fake):
+    p = object.__new__(q8.QuantizedKVPool)
+    p.device = torch.device("cpu")
+    p.num_kv_heads, p.head_dim, p.page_size, p.max_batch, p.max_pages_per_seq = 2, 64, 16, 4, 4
+    p.handle, p.workspace_bytes, p.workspace_zero_bytes = None, 64, 16
+    p._workspaces, p._streams = {}, {}
+    for name in ("k_pages", "v_pages", "scales", "block_table", "seq_lens", "error_word"):
+        setattr(p, name, watched(fake, name, 4))
+    return p
+
+
+def watched(fake, name, *shape, dtype=torch.bfloat16):
+    t = torch.zeros(shape, dtype=dtype).as_subclass(Watched)
+    t.fake, t.label = fake, name
+    return t
+
+
+def calls(fake, pool):
+    kv = lambda name: watched(fake, name, 3, 2, 64)             # noqa: E731
+    q = lambda name: watched(fake, name, 3, 4, 64)              # noqa: E731
+    lse = watched(fake, "lse", 3, 4, dtype=torch.float32)
+    ws = watched(fake, "workspace", 64, dtype=torch.uint8)
+    return {
+        "append_kv": (lambda: pool.append_kv(kv("k"), kv("v"), [3]), ["k", "v"]),
+        "read_kv": (lambda: pool.read_kv([0], [3], k_out=kv("k"), v_out=kv("v")), ["k", "v"]),
+        "decode_attention": (lambda: pool.decode_attention(q("q"), 2, out=q("out"), lse=lse, workspace=ws),
+                             ["q", "out", "lse", "workspace"]),
+        "chunk_attention": (lambda: pool.chunk_attention(q("q"), [3], out=q("out"), lse=lse, workspace=ws),
+                            ["q", "out", "lse", "workspace"]),
+    }
+
+
+@pytest.mark.parametrize("name", ["append_kv", "read_kv", "decode_attention", "chunk_attention"])
+@pytest.mark.parametrize("raw", [0, 7])
+def test_a_calls_tensors_are_held_for_the_stream_that_is_current(fake, pool, name, raw):
+    fake.raw = raw
+    call, tensors = calls(fake, pool)[name]
+    call()
+    assert fake.events[-1] == name                              # ... before its kernels are enqueued
+    assert set(fake.held()) >= {(t, f"stream {raw}") for t in tensors}
+
+
+def test_nothing_is_held_while_a_graph_is_captured(fake, pool):
+    fake.capturing = True
+    for call, _ in calls(fake, pool).values():
+        call()
+    assert not fake.held()
