@@ -61,7 +61,7 @@ class QuantizedKVPool:
     Every call runs on ``stream`` (the pool device's current stream if None),
     which must be ordered after the work that made its inputs; tensors of other
     streams may be dropped once the call has returned (a captured call's, as
-    the pool, have to live as long as its graph).  The workspace
+    the pool, have to live as long as its graph), the pool too.  The workspace
     of the attentions is one per stream; a call that is being captured into a
     CUDA graph takes one of its own from the graph's memory, so graphs share
     none.  ``workspace=`` names another, of ``workspace_bytes`` bytes whose
@@ -143,8 +143,8 @@ class QuantizedKVPool:
         return torch.cuda.stream(stream), stream.cuda_stream
 
     def _used_on(self, raw: int, *tensors: Optional[torch.Tensor]) -> None:
-        """Keeps the memory of a call's tensors from being handed out again
-        before the current stream, `raw`, is through with it: called before
+        """Keeps the memory of a call's tensors and of the pool from being
+        handed out again before the current stream, `raw`, is through with it: called before
         the kernels are enqueued, so that a call that fails half-way is
         covered.  (0.4 us a tensor; a Stream object costs 2.8 us to make and
         is kept.)"""
@@ -152,7 +152,11 @@ class QuantizedKVPool:
             return
         stream = self._streams.get(raw)
         if stream is None:
-            stream = self._streams[raw] = torch.cuda.current_stream(self.device)
+            # the pool's own memory, once: from here on until it is freed
+            stream = torch.cuda.current_stream(self.device)
+            for t in (self.k_pages, self.v_pages, self.scales, self.block_table, self.seq_lens, self.error_word):
+                t.record_stream(stream)
+            self._streams[raw] = stream
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)

@@ -41,3 +41,36 @@ def test_inputs_of_another_stream_may_be_dropped_where_the_calls_is_the_current_
         codes, sc = quantise(src.double().cpu().numpy())
         assert torch.equal(got.double().cpu(), dequantise(torch.from_numpy(codes), torch.from_numpy(sc)))
     check_decode(c, q0, 2, 0.05, out, lse)
+
+
+def test_a_pool_may_be_dropped_while_a_call_on_a_side_stream_waits():
+    """Its pages, scales, table and lengths are read and written to the end, though their memory is asked for again."""
+    c = Cache([700, 90], 2, 128, 16, seed=47)
+    q = c.q(2, 16)
+    kv = torch.randn(2, 10, 2, 128, generator=c.g).to(torch.bfloat16).cuda()
+    side = torch.cuda.Stream()
+    warm = c.pool()
+    with torch.cuda.stream(side):
+        warm.decode_attention(q, 2, return_lse=True)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        pages = [t.clone() for t in (c.k, c.v, c.sc)]
+        pool = c.pool.__func__(type("Own", (), dict(vars(c), k=pages[0], v=pages[1], sc=pages[2]))(), lens=[690, 90])
+        del pages
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)
+            pool.append_kv(kv[0], kv[1], [10, 0])
+            out, lse = pool.decode_attention(q, 2, scale=0.05, return_lse=True)
+        del pool
+        others = [torch.full_like(t, 7) for t in (c.k, c.v, c.sc) for _ in range(3)]
+        others += [torch.full((2, c.table.shape[1]), 7, dtype=torch.int32, device="cuda") for _ in range(4)]
+        others += [torch.full((n,), 7, dtype=torch.int32, device="cuda") for n in (1, 1, 2, 2)]
+        torch.cuda.synchronize()
+        k8, v8, sc = c.k.clone(), c.v.clone(), c.sc.clone()
+        check_pool = c.pool(lens=[690, 90])
+        check_pool.append_kv(kv[0], kv[1], [10, 0])
+        check_decode(c, q, 2, 0.05, out, lse)
+        assert all((t == 7).all() for t in others)                   # and nothing was written behind its back
+        for t, was in ((c.k, k8), (c.v, v8), (c.sc, sc)):
+            t.copy_(was)

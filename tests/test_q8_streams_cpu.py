@@ -79,6 +79,20 @@ def test_a_calls_tensors_are_held_for_the_stream_that_is_current(fake, pool, nam
     assert set(fake.held()) >= {(t, f"stream {raw}") for t in tensors}
 
 
+OWN = ("k_pages", "v_pages", "scales", "block_table", "seq_lens", "error_word")
+
+
+def test_the_pools_memory_is_held_once_for_every_stream(fake, pool):
+    for raw in (0, 7, 0, 9, 7):
+        fake.raw = raw
+        for call, _ in calls(fake, pool).values():
+            call()
+    for name in OWN:
+        assert sorted(s for t, s in fake.held() if t == name) == ["stream 0", "stream 7", "stream 9"]
+    first = fake.events.index("append_kv")
+    assert {t for t, _ in [e[1:] for e in fake.events[:first]]} >= set(OWN)
+
+
 def test_nothing_is_held_while_a_graph_is_captured(fake, pool):
     fake.capturing = True
     for call, _ in calls(fake, pool).values():
