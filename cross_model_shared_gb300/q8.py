@@ -59,9 +59,12 @@ class QuantizedKVPool:
     of two that brings the row's largest magnitude to at most 448.
 
     Every call runs on ``stream`` (the pool device's current stream if None),
-    which must be ordered after the work that made its inputs; tensors of other
-    streams may be dropped once the call has returned (a captured call's, as
-    the pool, have to live as long as its graph), the pool too.  The workspace
+    which must be ordered after the work that made its inputs.  A call on a
+    named stream, or where a side stream is current, holds its tensors back:
+    they may be dropped once it has returned, whichever stream they are of.  On
+    the default stream, unnamed, tensors of other streams are the caller's to
+    keep or record, as with torch's own operations.  The pool may be dropped at any time.  A captured call's
+    tensors, and the pool, have to live as long as the graph.  The workspace
     of the attentions is one per stream; a call that is being captured into a
     CUDA graph takes one of its own from the graph's memory, so graphs share
     none.  ``workspace=`` names another, of ``workspace_bytes`` bytes whose
@@ -142,22 +145,23 @@ class QuantizedKVPool:
             raise ValueError(f"stream must be one of {self.device}")
         return torch.cuda.stream(stream), stream.cuda_stream
 
-    def _used_on(self, raw: int, *tensors: Optional[torch.Tensor]) -> None:
-        """Keeps the memory of a call's tensors and of the pool from being
-        handed out again before the current stream, `raw`, is through with it: called before
-        the kernels are enqueued, so that a call that fails half-way is
-        covered.  (0.4 us a tensor; a Stream object costs 2.8 us to make and
-        is kept.)"""
-        if torch.cuda.is_current_stream_capturing():
-            return
+    def _used_on(self, raw: int, named: Optional[torch.cuda.Stream], *tensors: Optional[torch.Tensor]) -> None:
+        """Keeps the memory of the pool, and of the tensors of a call whose
+        stream is named or a side stream, from being handed out again before
+        the current stream, ``raw``, is through with it: called before the
+        kernels are enqueued, so that a call that fails half-way is covered.
+        (Recording the tensors of a short call costs 2 to 4 us of 20.)"""
         stream = self._streams.get(raw)
+        mine = raw == 0 and named is None
+        if mine and stream is not None or torch.cuda.is_current_stream_capturing():
+            return
         if stream is None:
             # the pool's own memory, once: from here on until it is freed
             stream = torch.cuda.current_stream(self.device)
             for t in (self.k_pages, self.v_pages, self.scales, self.block_table, self.seq_lens, self.error_word):
                 t.record_stream(stream)
             self._streams[raw] = stream
-        for t in tensors:
+        for t in () if mine else tensors:
             if t is not None:
                 t.record_stream(stream)
 
@@ -228,7 +232,7 @@ class QuantizedKVPool:
             raise ValueError("k_new and v_new must hold sum(new_lens) tokens")
         ctx, s = self._on(stream)
         with ctx:
-            self._used_on(s, k_new, v_new)
+            self._used_on(s, stream, k_new, v_new)
             N.shkv_q8_append_kv(self.handle, new.n, first.ptr if first is not None else None, new.ptr,
                                 k_new.data_ptr(), ks, v_new.data_ptr(), vs, s)
 
@@ -244,7 +248,7 @@ class QuantizedKVPool:
         ctx, s = self._on(stream)
         with ctx:
             k, v = self._out(k_out, shape, _BF16, "k_out"), self._out(v_out, shape, _BF16, "v_out")
-            self._used_on(s, k_out, v_out)
+            self._used_on(s, stream, k_out, v_out)
             N.shkv_q8_read_kv(self.handle, n.n, first.ptr, n.ptr, k.data_ptr(), row, v.data_ptr(), row, s)
         return k, v
 
@@ -264,7 +268,7 @@ class QuantizedKVPool:
             o = self._out(out, q.shape, _BF16, "out")
             e = self._out(lse, (B, rows), _F32, "lse") if return_lse or lse is not None else None
             ws = self._workspace(workspace, s)
-            self._used_on(s, q, out, lse, workspace)
+            self._used_on(s, stream, q, out, lse, workspace)
             N.shkv_q8_decode_attention(self.handle, B, n_models, rows // n_models, q.data_ptr(),
                                        D ** -0.5 if scale is None else float(scale), o.data_ptr(),
                                        e.data_ptr() if e is not None else None, ws.data_ptr(), ws.numel(), s)
@@ -288,7 +292,7 @@ class QuantizedKVPool:
             e = self._out(lse, (T, hq), _F32, "lse") if return_lse or lse is not None else None
             if T:
                 ws = self._workspace(workspace, s)
-                self._used_on(s, q, out, lse, workspace)
+                self._used_on(s, stream, q, out, lse, workspace)
                 N.shkv_q8_chunk_attention(self.handle, new.n, new.ptr, hq, q.data_ptr(), qs,
                                           D ** -0.5 if scale is None else float(scale), o.data_ptr(),
                                           e.data_ptr() if e is not None else None, ws.data_ptr(), ws.numel(), s)

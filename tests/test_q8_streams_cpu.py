@@ -6,6 +6,9 @@ import torch
 from cross_model_shared_gb300 import q8
 
 
+OWN = ("k_pages", "v_pages", "scales", "block_table", "seq_lens", "error_word")
+
+
 class Fake:
     """Records what was held back for which stream, and when the entry points were called."""
 
@@ -43,7 +46,7 @@ def pool(fake):
     p.num_kv_heads, p.head_dim, p.page_size, p.max_batch, p.max_pages_per_seq = 2, 64, 16, 4, 4
     p.handle, p.workspace_bytes, p.workspace_zero_bytes = None, 64, 16
     p._workspaces, p._streams = {}, {}
-    for name in ("k_pages", "v_pages", "scales", "block_table", "seq_lens", "error_word"):
+    for name in OWN:
         setattr(p, name, watched(fake, name, 4))
     return p
 
@@ -70,16 +73,28 @@ def calls(fake, pool):
 
 
 @pytest.mark.parametrize("name", ["append_kv", "read_kv", "decode_attention", "chunk_attention"])
-@pytest.mark.parametrize("raw", [0, 7])
-def test_a_calls_tensors_are_held_for_the_stream_that_is_current(fake, pool, name, raw):
-    fake.raw = raw
+def test_a_calls_tensors_are_held_for_the_side_stream_that_is_current(fake, pool, name):
     call, tensors = calls(fake, pool)[name]
-    call()
-    assert fake.events[-1] == name                              # ... before its kernels are enqueued
-    assert set(fake.held()) >= {(t, f"stream {raw}") for t in tensors}
+    for _ in range(2):
+        del fake.events[:]
+        call()
+        assert fake.events[-1] == name                          # ... before its kernels are enqueued
+        assert set(fake.held()) >= {(t, "stream 7") for t in tensors}
 
 
-OWN = ("k_pages", "v_pages", "scales", "block_table", "seq_lens", "error_word")
+def test_and_for_the_default_stream_where_it_is_named(fake, pool, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: q8._HERE)
+    fake.raw = 0
+    named = type("Stream", (), {"device": pool.device, "cuda_stream": 0})()
+    pool.append_kv(watched(fake, "k", 3, 2, 64), watched(fake, "v", 3, 2, 64), [3], stream=named)
+    assert {t for t, _ in fake.held()} == {"k", "v", *OWN}
+
+
+def test_on_the_default_stream_tensors_are_the_callers(fake, pool):
+    fake.raw = 0
+    for call, _ in calls(fake, pool).values():
+        call()
+    assert {t for t, _ in fake.held()} == set(OWN)
 
 
 def test_the_pools_memory_is_held_once_for_every_stream(fake, pool):
