@@ -253,6 +253,16 @@ __global__ void __launch_bounds__(kCacheThreads) shkv_q8_read_kernel(const __gri
                 atomicOr(p.err, SHKV_ERRF_SEQ_LEN);
 }
 
+// Takes reported bits out of the error word: atomically, as kernels of other
+// streams may be setting others.
+__global__ void shkv_q8_clear_errors_kernel(uint32_t *err, uint32_t bits) { atomicAnd(err, ~bits); }
+
+cudaError_t launch_q8_clear_errors(uint32_t *err, uint32_t bits, cudaStream_t stream)
+{
+    shkv_q8_clear_errors_kernel<<<1, 1, 0, stream>>>(err, bits);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_q8_cache(const Q8CacheParams &p, bool read, int num_sms, cudaStream_t stream)
 {
     int64_t blocks = ((int64_t)p.tok0[p.batch] + kCacheThreads / 32 - 1) / (kCacheThreads / 32);

@@ -18,6 +18,7 @@
 
 namespace shkv {
 cudaError_t launch_q8_cache(const Q8CacheParams &p, bool read, int num_sms, cudaStream_t stream);
+cudaError_t launch_q8_clear_errors(uint32_t *err, uint32_t bits, cudaStream_t stream);
 cudaError_t launch_q8_chunk(const CUtensorMap &tmK, const CUtensorMap &tmV, const Q8ChunkParams &p, bool splits,
                             cudaStream_t stream);
 cudaError_t launch_q8_decode(const CUtensorMap &tmK, const CUtensorMap &tmV, const Q8DecodeParams &q,
@@ -558,12 +559,15 @@ shkv_status shkv_q8_check_errors(shkv_q8_pool *pool, void *stream, uint32_t *fla
     if (!pool || !flags || !on_pool_device(pool))
         return SHKV_ERR_INVALID_ARG;
     *flags = 0;
-    if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess)
-        return SHKV_ERR_CUDA;
+    cudaStream_t st = (cudaStream_t)stream;
     uint32_t v = 0;
-    if (cudaMemcpy(&v, pool->cfg.error_word, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess)
+    if (cudaMemcpyAsync(&v, pool->cfg.error_word, sizeof v, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
         return SHKV_ERR_CUDA;
-    if (v && cudaMemset(pool->cfg.error_word, 0, sizeof v) != cudaSuccess)
+    // only what is reported is cleared, and before the call returns: a bit that
+    // a kernel of another stream sets in the meantime stays for the next check
+    if (v && (launch_q8_clear_errors(pool->cfg.error_word, v, st) != cudaSuccess ||
+              cudaStreamSynchronize(st) != cudaSuccess))
         return SHKV_ERR_CUDA;
     *flags = v;
     return v ? SHKV_ERR_DEVICE : SHKV_OK;

@@ -299,7 +299,8 @@ class QuantizedKVPool:
         return (o, e) if e is not None else o
 
     def check_errors(self, stream=None) -> int:
-        """Synchronize and return (then clear) the device error bits."""
+        """Wait for the stream and return (then clear) the device error bits;
+        those of calls on other streams are reported by this check or a later one."""
         ctx, s = self._on(stream)
         with ctx:
             return N.shkv_q8_check_errors(self.handle, s)

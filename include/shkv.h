@@ -556,6 +556,8 @@ shkv_status shkv_q8_pool_create(const shkv_q8_pool_config *cfg, shkv_q8_pool **o
 shkv_status shkv_q8_pool_destroy(shkv_q8_pool *pool);
 shkv_status shkv_q8_pool_set_seq_lens(shkv_q8_pool *pool, int32_t batch, const int32_t *lens, void *stream);
 shkv_status shkv_q8_pool_get_seq_lens(const shkv_q8_pool *pool, int32_t batch, int32_t *lens);
+/* Waits for `stream` only.  Bits that calls on other streams set are reported
+ * by this check or a later one, none is lost. */
 shkv_status shkv_q8_check_errors(shkv_q8_pool *pool, void *stream, uint32_t *flags);
 
 /*

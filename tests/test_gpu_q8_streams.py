@@ -2,6 +2,8 @@
 import pytest
 import torch
 
+from cross_model_shared_gb300 import _native as N
+
 from .q8_common import Cache, check_decode, dequantise, quantise
 
 pytestmark = pytest.mark.gpu
@@ -70,3 +72,34 @@ def test_a_pool_may_be_dropped_while_a_call_on_a_side_stream_waits():
         assert all((t == 7).all() for t in others)                   # and nothing was written behind its back
         for t, was in ((c.k, k8), (c.v, v8), (c.sc, sc)):
             t.copy_(was)
+
+
+def test_error_bits_of_another_stream_are_not_lost():
+    """A side stream's calls set one bit while the current stream's checks read and clear another."""
+    c = Cache([100, 100], 1, 64, 16, seed=48)
+    pool = c.pool()
+    q = c.q(2, 2)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        pool.decode_attention(q, 1)
+    torch.cuda.synchronize()
+    assert pool.check_errors() == 0
+    good = pool.block_table.clone()
+    lens = pool.seq_lens.clone()
+    for spin in range(20):
+        pool.block_table[1, 2] = -5                                  # PAGE_OOB on the current stream
+        pool.decode_attention(q, 1)
+        torch.cuda.synchronize()
+        pool.block_table.copy_(good)
+        pool.seq_lens.sub_(1)                                        # SEQ_LEN on the side stream
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(5_000 * spin)
+            pool.decode_attention(q, 1)
+        got = [pool.check_errors() for _ in range(3)]
+        torch.cuda.synchronize()
+        pool.seq_lens.copy_(lens)
+        got.append(pool.check_errors())
+        assert got[0] & N.SHKV_ERRF_PAGE_OOB and not any(g & N.SHKV_ERRF_PAGE_OOB for g in got[1:])
+        assert any(g & N.SHKV_ERRF_SEQ_LEN for g in got)
+        assert pool.check_errors() == 0
