@@ -25,12 +25,14 @@
 // 2^-12 of the sum's largest term.  (P relative to the largest weight alone,
 // with V's scales apart by 2^s, loses up to n 2^(s - 32): a first key of much
 // weight and little value, as an attention sink is, then lost 10% of a sum over
-// 131072 keys at s = 12.)  V exponents of -40 to 40 (row maxima of 2^-31 to 2^48)
-// keep l's terms between 2^-81 and 2^55, in fp32's range.  From the first
-// stage on that holds another one, or a zero row (scale byte 0), the piece is
-// `wide`: l is then summed from a second exponential, relative to a running
-// maximum of x of its own, and a key whose V is zero stays out of m.  Such a
-// stage takes about twice the time.  Sums and O are fp32.
+// 131072 keys at s = 12.)  l is in fp32's range while no V exponent is above 60
+// (then the row's largest w is 2^-61 or more) and no w above 2^67.  From the
+// first stage on that holds the one (for the whole piece) or the other (for its
+// warp), l is summed from a second exponential, relative to a running maximum of
+// x of its own; a key whose V is zero stays out of m at all times.  That takes
+// values above 2^60, values all below 2^-51, or a key that leads by 2^60 and has
+// next to no value; such a stage takes about twice the time.  Sums and O are
+// fp32.
 //
 // As in the bf16 kernel, a stage whose scores are all visible is
 // exponentiated against the running maximum without taking its own.  A quarter
@@ -71,8 +73,10 @@ constexpr int kGroupWarps = 4;           // softmax warps per tile
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 2.f;      // in the exact path m moves where it lags the maximum by more
 constexpr float kPLog2 = 7.f;            // P at the running maximum
+constexpr uint32_t kApart = 1, kMayLead = 2;   // a stage's needs: see the top; a key of it may lead by 2^60
 constexpr float kMaxPart = 65504.f;      // fp16's largest: bound of a stage's P taken without its maximum
-constexpr int kVWindow = 40;             // V exponents outside -kVWindow .. kVWindow make a piece wide
+constexpr int kMaxEv = 60;               // a V exponent above this needs a reference of l's own
+constexpr float kMaxLead = 60.f;         // ... as does an x this far above m
 constexpr int kKS = 3, kVS = 3;          // ring slots of 16 KB (K) and 32 KB (V)
 constexpr uint32_t kKSlotBytes = kKT * 128;
 constexpr uint32_t kVSlotBytes = 2 * kKT * 128;
@@ -91,7 +95,8 @@ struct Smem {
 // [half][128 keys][128 B], the codes in the upper half until they are
 // converted), all 128-byte swizzled; per V slot its scale bytes, the keys'
 // score factors, V exponents and factors of P, and four words (valid pages,
-// wide, the largest sum of w that needs no look at the maximum).
+// what its V exponents need, the largest sum of w that needs no look at the
+// maximum).
 __host__ __device__ inline Smem smem_layout()
 {
     Smem u;
@@ -297,24 +302,25 @@ __device__ void chunk_convert(const Q8ChunkParams &p, const Ctx &c)
                 const uint32_t mask = info[0];
                 const int n = u.L - j * kKT;
                 const uint8_t *sc = c.smem + c.lay.scales + slot * 2 * kKT;
-                int top;                                 // the stage's largest V scale byte
-                // V exponents outside the window, by each warp for itself (NaN
-                // rows aside; zero rows have the least scale)
+                uint32_t top, low;
+                // the stage's largest and least V scale byte (NaN rows aside;
+                // zero rows have the least), by each warp for itself
                 {
                     const int t4 = 4 * lane;
                     const uint32_t w = *reinterpret_cast<const volatile uint32_t *>(
                         sc + ((t4 >> log2P) << (log2P + 1)) + P + (t4 & (P - 1)));
                     const int in = ((mask >> (t4 >> log2P)) & 1u) ? n - t4 : 0;
-                    bool out = false;
-                    int big = 0;
+                    top = 0;
+                    low = 255;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int b = (int)((w >> (8 * i)) & 0xffu);
-                        big = max(big, i < in && b != 255 ? b : 0);
-                        out = out || (i < in && b != 255 && abs(b - 127) > kVWindow);
+                        const uint32_t b = (w >> (8 * i)) & 0xffu;
+                        top = max(top, i < in && b != 255u ? b : 0u);
+                        low = min(low, i < in ? b : 255u);
                     }
-                    wide = wide || __any_sync(0xffffffffu, out);
-                    top = (int)__reduce_max_sync(0xffffffffu, (unsigned)big);
+                    top = __reduce_max_sync(0xffffffffu, top);
+                    low = __reduce_min_sync(0xffffffffu, low);
+                    wide = wide || top > 127u + kMaxEv;
                 }
                 const bool valid = t < n && ((mask >> (t >> log2P)) & 1u);
                 const uint8_t *mine = sc + ((t >> log2P) << (log2P + 1)) + (t & (P - 1));
@@ -335,17 +341,16 @@ __device__ void chunk_convert(const Q8ChunkParams &p, const Ctx &c)
                 }
                 const bool live = valid && vb != 255 && !zero;
                 const float nan = __uint_as_float(0x7fc00000u);
-                const int ev = live ? vb - 127 : -kVWindow;
                 reinterpret_cast<float *>(c.smem + c.lay.factor)[slot * kKT + t] =
                     !valid ? 0.f : vb == 255 ? nan : q8_scale((uint32_t)kb) * p.scale_log2;
-                // (where V is zero P may be zero too, and its key stays out of
-                // P's reference: the weights of the others keep their bits)
-                reinterpret_cast<float *>(c.smem + c.lay.evs)[slot * kKT + t] = wide && !live ? -INFINITY : (float)ev;
-                reinterpret_cast<float *>(c.smem + c.lay.pfactor)[slot * kKT + t] =
-                    __uint_as_float((uint32_t)(127 + ev) << 23);                 // 2^ev (of no use where wide)
+                // (where V is zero P is zero, and its key stays out of P's
+                // reference: the weights of the others keep their bits)
+                reinterpret_cast<float *>(c.smem + c.lay.evs)[slot * kKT + t] = live ? (float)(vb - 127) : -INFINITY;
+                reinterpret_cast<float *>(c.smem + c.lay.pfactor)[slot * kKT + t] = live ? q8_scale((uint32_t)vb) : 0.f;
                 if (t == 0) {
-                    info[1] = wide ? 1u : 0u;
-                    info[2] = __float_as_uint(kMaxPart) + ((uint32_t)(127 - max(top, 127 - kVWindow)) << 23);
+                    info[1] = wide ? kApart : low < 127u - (uint32_t)kMaxLead ? kMayLead : 0u;
+                    // 65504 / 2^top, 2^67 at most
+                    info[2] = __float_as_uint(kMaxPart) + ((127u - max(top, 127u - 51u)) << 23);
                 }
                 uint8_t *row = c.smem + c.lay.vring + (uint32_t)slot * kVSlotBytes + (uint32_t)t * 128u;
                 // (the conversion instruction: the stacked kernel's integer
@@ -641,8 +646,8 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
             mbar_arrive(q_ready(c));
 
         float m_use = -INFINITY, lsum = 0.f;
-        float m_l = 0.f;                                 // l's reference once the piece is wide; m_use until then
-        bool apart = false;
+        float m_l = 0.f;                                 // l's reference once they are apart; m_use until then
+        bool apart = false;                              // for the warp's stages from here on
         const int s1 = min(t.s1, t.nst[x]);
 #pragma unroll 1
         for (int j = t.s0; j < s1; ++j) {
@@ -651,7 +656,7 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
             wait(conv_v(c, vs), ring_par(k, kVS));
             const volatile uint32_t *info = reinterpret_cast<const volatile uint32_t *>(c.smem + c.lay.info) + vs * 4;
             const uint32_t pmask = alive ? info[0] : 0u;
-            const bool wide = info[1] != 0u;
+            const uint32_t needs = info[1];
             const float4 *fac = reinterpret_cast<const float4 *>(c.smem + c.lay.factor + vs * kKT * 4);
             const float4 *evs = reinterpret_cast<const float4 *>(c.smem + c.lay.evs + vs * kKT * 4);
             const float4 *pfac = reinterpret_cast<const float4 *>(c.smem + c.lay.pfactor + vs * kKT * 4);
@@ -669,7 +674,7 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
             tmem_wait_ld();
             // Common case (see the top): P against the running maximum.
             float part = 0.f;
-            bool fast = __all_sync(0xffffffffu, dense && alive && m_use != -INFINITY && !wide);
+            bool fast = __all_sync(0xffffffffu, dense && alive && m_use != -INFINITY && !apart && needs != kApart);
             if (fast) {
                 const float nmu = kPLog2 - m_use;
                 const float2 rq2 = make_float2(rq, rq), nmu2 = make_float2(nmu, nmu);
@@ -745,7 +750,7 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                 for (int c32 = 0; c32 < kKT / 32; ++c32) {
                     float xs[32];
                     columns(c32, xs);
-                    if (wide)
+                    if (apart || needs != 0u)
 #pragma unroll
                         for (int i = 0; i < 32; i += 2)
                             cm = max3f(cm, xs[i], xs[i + 1]);
@@ -755,16 +760,17 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                         cy = max3f(max3f(cy, xs[4 * i] + v.x, xs[4 * i + 1] + v.y), xs[4 * i + 2] + v.z, xs[4 * i + 3] + v.w);
                     }
                 }
-                if (wide && !apart) {
-                    apart = true;
-                    m_l = m_use;
-                }
+                const float m_old = m_use;
                 float scale_o = 1.f;
                 if (m_use == -INFINITY) {
                     m_use = cy;
                 } else if (cy > m_use + kRescaleLog2) {
                     scale_o = ex2_approx(m_use - cy);
                     m_use = cy;
+                }
+                if (!apart && __any_sync(0xffffffffu, needs == kApart || cm - m_use > kMaxLead)) {
+                    apart = true;
+                    m_l = m_old;
                 }
                 if (!apart) {
                     lsum *= scale_o;

@@ -20,20 +20,22 @@
 // 8 significant bits: its row is scaled by a power of two to at most 448 and
 // split into two e4m3 terms, qh nearest and ql = q - qh, which is exact but
 // for values under 2^-15 of the row's largest.  V's codes are moved to fp16
-// in shared memory (sign and seven bits, exponent bias and all: v8 * 2^-8, exactly).  With the token's V exponent inside y, P is
-// relative to the row's largest weight times value scale, so that fp16 holds
-// 11 bits of every token that matters to the sum, whatever the magnitudes of
-// weights and values apart: fp16's least step, 2^-24, is 2^-31 of that
-// largest, and 2^20 tokens below it are lost to 2^-12 of it.  V exponents of
-// -40 to 40 (row maxima of 2^-31 to 2^48) keep P before its rounding at 2^-81 and
-// more for the largest weight, and l's terms under 2^55.  From the first stage
-// on that holds another one, or a zero row (scale byte 0), the segment is `wide`
-// (each softmax group for itself): l is then summed from a second exponential,
-// relative to a running maximum of y - ev of its own, and a token whose V is
-// zero stays out of m.  Its exponents then bound nothing, however far weights
-// and values lie apart in either direction.  Such a stage is slow (loops over
-// eight rows, four meetings of the group's warps); ordinary caches have none.
-// Sums and O are fp32.
+// in shared memory (sign and seven bits, exponent bias and all: v8 * 2^-8,
+// exactly).  With the token's V exponent inside y, P is relative to the row's
+// largest weight times value scale, so that fp16 holds 11 bits of every token
+// that matters to the sum, whatever the magnitudes of weights and values apart:
+// fp16's least step, 2^-24, is 2^-31 of that largest, and 2^20 tokens below it
+// are lost to 2^-12 of it.  V exponents of -40 to 40 (row maxima of 2^-31 to
+// 2^48) keep P before its rounding at 2^-81 and more for the largest weight, and
+// l's terms under 2^55.  A `low` token, under -40, as a zero row is, takes part in
+// l as one of -40 and not in O, while its weight is small enough (see `lead`).
+// Where it is not, and in every stage from the first exponent above 40 on, the
+// stage is `wide` (each softmax group for itself): its part of l comes from a
+// second exponential, relative to a running maximum of y - ev of its own, and a
+// token whose V is zero stays out of m.  Such a stage is slow (loops over eight
+// rows, four meetings of the group's warps): with all of a segment's wide, 31
+// requests of 1k to 8k tokens take 91 us instead of 56 at 8 rows, 266 instead of
+// 71 at 32.  Sums and O are fp32.
 //
 // The softmax is bound by the latency of its chain, not by its instructions:
 // up to 48 rows its two groups of four warps take alternate stages, each with
@@ -90,7 +92,12 @@ constexpr uint32_t kColS = 0;               // S^T buffers at columns 0 and 64
 constexpr uint32_t kColO = 128;             // O^T
 constexpr float kRescaleLog2 = 8.f;         // m lags the maximum by at most this
 constexpr float kPLog2 = 7.f;               // P is 2^7 at the running maximum: 2^15 at most
-constexpr int kVWindow = 40;                // V exponents outside -kVWindow .. kVWindow make a segment wide
+constexpr int kVWindow = 40;                // a V exponent above makes a segment wide, one below -kVWindow is low
+// A low token leads where its y - m + 7, with -kVWindow for its exponent, is above
+// this.  A row of the least scale (zeros, or values under 2^-118) may add
+// 2^(8 + kVWindow) to l: what its values would add to O is 2^-86 of the largest
+// term at most.  What others would add is under fp16's least step.
+constexpr float kLeadLeast = 8.f, kLeadLow = -24.f;
 constexpr uint32_t kKSlotBytes = kTT * 128;
 constexpr uint32_t kVSlotBytes = 2 * kTT * 128;
 constexpr uint32_t kPBytes = kTT * 128;
@@ -101,11 +108,11 @@ constexpr uint32_t kSoftmaxRegs = 168, kOtherRegs = 88;
 static_assert(kSoftmaxRegs * 256 + kOtherRegs * 256 == 128 * kThreads, "register split");
 
 // scratch rows of 64 words: per softmax group the stage maxima and the sums
-// [token group], the new 7 - m, the rescaling of O and l, m, and for a wide
-// segment the sum of its wide stages, its reference, and m before them; then
-// the factors of the two groups at the segment's end (two halves each), the
-// queries' scales, the rows' output offsets and whether the groups went wide
-constexpr int kScrMax = 0, kScrNew = 4, kScrAlpha = 5, kScrM = 6, kScrL = 7, kScrMl = 8, kScrM0 = 9, kScrGroup = 10;
+// [token group], the new 7 - m, the rescaling of O and l, m, and the wide
+// stages' part of l and its reference; then the factors of the two groups at the
+// segment's end (two halves each), the queries' scales, the rows' output offsets
+// and whether the groups had wide stages
+constexpr int kScrMax = 0, kScrNew = 4, kScrAlpha = 5, kScrM = 6, kScrL = 7, kScrMl = 8, kScrGroup = 9;
 constexpr int kScrEnd = 2 * kScrGroup, kScrQ = kScrEnd + 4, kScrOff = kScrQ + 1, kScrWide = kScrOff + 1,
               kScrRows = kScrWide + 1;
 
@@ -188,10 +195,10 @@ __device__ __forceinline__ uint32_t scale_off(int t, int log2P)
     return (uint32_t)(((t >> log2P) << (log2P + 1)) + (t & ((1 << log2P) - 1)));
 }
 
-// Whether the stage's tokens below `n` on copied pages hold a V exponent outside
+// Whether the stage's tokens below `n` on copied pages hold a V exponent above
 // the window (NaN rows, 255, aside), by a warp.  w: the V scales of the lane's
 // four tokens.
-__device__ __forceinline__ bool stage_outside(uint32_t w, int n, uint32_t mask, int log2P)
+__device__ __forceinline__ bool stage_above(uint32_t w, int n, uint32_t mask, int log2P)
 {
     const int t = 4 * (threadIdx.x & 31);
     const int in = ((mask >> (t >> log2P)) & 1u) ? n - t : 0;
@@ -199,7 +206,7 @@ __device__ __forceinline__ bool stage_outside(uint32_t w, int n, uint32_t mask, 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int b = (int)((w >> (8 * i)) & 0xffu);
-        out = out || (i < in && b != 255 && abs(b - 127) > kVWindow);
+        out = out || (i < in && b != 255 && b > 127 + kVWindow);
     }
     return __any_sync(0xffffffffu, out);
 }
@@ -407,24 +414,25 @@ __device__ void warm_l2_q8(const CUtensorMap *tm, const DecodeParams &p, const C
     }
 }
 
-// What a token brings to the softmax: (score factor, V exponent ev, 2^-ev,
-// first row that sees it | kMasked if some token of the warp is not seen by all
-// | kWide if the stage holds a V exponent outside the window).  kb, vb: the
-// token's scale bytes; at: its distance from the first key some row does not
-// see.  A NaN row of V makes its key's scores NaN, so that only rows that attend
-// it see it.
-constexpr int kMasked = 0x100, kWide = 0x200;
-__device__ __forceinline__ float4 token_factors(const DecodeParams &p, int kb, int vb, bool valid, int at, bool outside)
+// What a token brings to the softmax: (score factor, V exponent ev, -kVWindow at
+// least, 2^-ev, first row that sees it | kMasked if some token of the warp is not
+// seen by all | kWide if the stage holds a V exponent above the window | kLow if
+// the token's is below it | V's scale byte << 16).  kb, vb: the token's scale
+// bytes; at: its distance from the first key some row does not see.  A NaN row
+// of V makes its key's scores NaN, so that only rows that attend it see it.
+constexpr int kMasked = 0x100, kWide = 0x200, kLow = 0x400;
+__device__ __forceinline__ float4 token_factors(const DecodeParams &p, int kb, int vb, bool valid, int at, bool above)
 {
-    const int ve = !valid || vb == 255 ? 127 : vb;
+    const int ve = !valid || vb == 255 ? 127 : vb, vc = max(ve, 127 - kVWindow);
     // rows from row_min on see the token (new token i from position L - n + i on)
     const int row_min = valid ? min(64, max(0, (at + 1) * p.group)) : 64;
-    const int flags = (__any_sync(0xffffffffu, row_min > 0) ? kMasked : 0) | (outside ? kWide : 0);
+    const int flags = (__any_sync(0xffffffffu, row_min > 0) ? kMasked : 0) | (above ? kWide : 0) |
+                      (vc > ve ? kLow : 0);
     float4 f;
     f.x = !valid ? 0.f : vb == 255 ? __uint_as_float(0x7fc00000u) : q8_scale((uint32_t)kb) * p.scale_log2;
-    f.y = (float)(ve - 127);
-    f.z = __uint_as_float((uint32_t)(254 - ve) << 23);
-    f.w = __int_as_float(row_min | flags);
+    f.y = (float)(vc - 127);
+    f.z = __uint_as_float((uint32_t)(254 - vc) << 23);
+    f.w = __int_as_float(row_min | flags | ve << 16);
     return f;
 }
 
@@ -483,7 +491,7 @@ __device__ void convert_v(const Q8DecodeParams &q, const Ctx4 &c)
                 const int kb = *(const volatile uint8_t *)(sc_mine + so), vb = *(const volatile uint8_t *)(sc_mine + so + P);
                 const bool valid = alive && tok0 + t < lim && ((mask >> page) & 1u);
                 const float4 f = token_factors(p, kb, vb, valid, tok0 + t - all_see,
-                                               stage_outside(four, lim - tok0, mask, log2P));
+                                               stage_above(four, lim - tok0, mask, log2P));
                 if (alive)
                     reinterpret_cast<float4 *>(c.smem + L.info)[entry * kTT + t] = f;
                 __syncwarp();
@@ -725,16 +733,18 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
         }
     };
 
-    // A stage of a wide segment (see the top), eight rows at a time: short loops
-    // with their state in shared memory, as the common stage has the registers.
-    // first: the segment's first such stage of the group; has_o: O holds
-    // earlier stages; pv_par: parity of the group's previous product.
-    auto wide_stage = [&](const float4 &f, int row_min, bool first, bool has_o, int k, uint32_t pv_par, uint8_t *prow) {
+    // A wide stage (see the top), eight rows at a time: short loops with their
+    // state in shared memory, as the common stage has the registers.  first: the
+    // segment's first of the group; has_o: O holds earlier stages; pv_par: parity
+    // of the group's previous product.  Leaves the new 7 - m, and in kScrAlpha
+    // what the common stages' l takes.
+    auto wide_stage = [&](const float4 &f, int w4, bool first, bool has_o, int k, uint32_t pv_par, uint8_t *prow) {
         const int r = kPing ? t : (int)threadIdx.x;      // the row this thread keeps, below NR
+        const int row_min = w4 & 0xff, vb = w4 >> 16;
         // V's codes, where the scale alone does not tell a zero row from one of tiny values
         wait(bar_at(c, kConvV + k % kVS), (uint32_t)(k / kVS) & 1u);
         bool zero = false;
-        if (alive && f.y == -127.f) {
+        if (alive && vb == 0) {
             const uint8_t *row = c.smem + L.vring + (uint32_t)(k % kVS) * kVSlotBytes + (uint32_t)t * 128u;
             uint32_t any = 0;
 #pragma unroll 1
@@ -744,7 +754,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
             }
             zero = (any & 0x7fff7fffu) == 0u;
         }
-        const float ev = zero ? -INFINITY : f.y;
+        const float ev = zero ? -INFINITY : (float)(vb - 127);
         // y - ev of rows chunk_col(ch) .. + 7, -inf where not seen
         auto scores8 = [&](int ch, float (&x)[8]) {
             uint32_t sv[8];
@@ -784,10 +794,11 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
         if (r < NR) {
             const float mo = mine[kScrM * 64 + r], mn = moved(mo);
             if (first) {
-                mine[kScrM0 * 64 + r] = mine[kScrMl * 64 + r] = mo;
+                mine[kScrMl * 64 + r] = -INFINITY;
                 mine[kScrL * 64 + r] = 0.f;
             }
             moves = mn != mo;
+            mine[kScrNew * 64 + r] = mn == -INFINITY ? 1e30f : kPLog2 - mn;
             mine[kScrAlpha * 64 + r] = moves ? ex2_approx(mo - mn) : 1.f;
             mine[kScrM * 64 + r] = mn;
         }
@@ -863,7 +874,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
     for (;;) {
         const int nst = stages_of(s, P);
         const int R = q.n_q[s.b] * p.group;
-        bool wide = false;                      // for the group's stages from here on
+        bool wide = false, had_wide = false;    // the group's stages from here on are; some were
         float2 nmu[kNmRegs ? NH / 2 : 1], l[NH / 2];   // 7 - m (1e30: no key yet), and this token's share of l
 #pragma unroll
         for (int i = 0; i < NH / 2; ++i) {
@@ -903,13 +914,13 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                 }
                 const int tok0 = tok_first + j * kTT;
                 f = token_factors(p, kb, vb, tok0 + t < lim && ((mask >> (t >> log2P)) & 1u), tok0 + t - all_see,
-                                  stage_outside(four, lim - tok0, mask & 0xffu, log2P));
+                                  stage_above(four, lim - tok0, mask & 0xffu, log2P));
             }
             if (wait(bar_at(c, kSFull + buf), (uint32_t)((k >> 1) & 1)))
                 tc_fence_after();
             if (!kPing)
                 f = reinterpret_cast<const float4 *>(c.smem + L.info)[(k % kInfo) * kTT + t];
-            const int w4 = alive ? __float_as_int(f.w) : 64 | kMasked;
+            const int w4 = alive ? __float_as_int(f.w) : 64 | kMasked | 127 << 16;
             const int row_min = w4 & 0xff;
             const bool masked = (w4 & kMasked) != 0;     // for some token of the warp
             uint8_t *prow = c.smem + L.pbuf + (uint32_t)grp * kPBytes + (uint32_t)t * 128u;
@@ -967,14 +978,24 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                 for (int i = 0; i < NH / 2; ++i)
                     top = fmaxf(top, fmaxf(d[i].x, d[i].y));
                 // all warps of the stage agree, also where one of them gave up waiting
-                const bool outside = (w4 & kWide) != 0;
-                refresh = bar_red_or(bar_id, bar_threads, top > kPLog2 + kRescaleLog2 || outside);
+                const bool low = (w4 & kLow) != 0;
+                const bool lead = low && top > (w4 >> 16 ? kLeadLow : kLeadLeast);
+                const bool need = lead || (w4 & kWide) != 0;
+                refresh = bar_red_or(bar_id, bar_threads, need || (!low && top > kPLog2 + kRescaleLog2));
                 if (refresh)
-                    go_wide = bar_red_or(bar_id, bar_threads, outside);
+                    go_wide = bar_red_or(bar_id, bar_threads, need);
             }
             if (go_wide) {
-                wide_stage(f, row_min, !wide, j > j0, k, pv_par, prow);
-                wide = true;
+                wide_stage(f, w4, !had_wide, j > j0, k, pv_par, prow);
+                had_wide = true;
+                wide = bar_red_or(bar_id, bar_threads, wide || (w4 & kWide) != 0);
+#pragma unroll
+                for (int i = 0; i < NH / 2; ++i) {
+                    const int rr = row_of(2 * i);
+                    if (kNmRegs)
+                        nmu[kNmRegs ? i : 0] = make_float2(mine[kScrNew * 64 + rr], mine[kScrNew * 64 + rr + 1]);
+                    l[i] = __fmul2_rn(l[i], make_float2(mine[kScrAlpha * 64 + rr], mine[kScrAlpha * 64 + rr + 1]));
+                }
                 continue;
             }
             // --- lazy refresh of the maxima
@@ -1047,6 +1068,10 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                 l[i] = __ffma2_rn(pe, make_float2(f.z, f.z), l[i]);
                 pk[i] = pack_half2(pe.x, pe.y);
             }
+            if (w4 & kLow)
+#pragma unroll
+                for (int i = 0; i < NH / 2; ++i)
+                    pk[i] = 0u;
             // --- P^T, once the group's previous product has read the buffer
             if (k >= (kPing ? 2 : 1))
                 wait(bar_at(c, kPvDone + grp), pv_par);
@@ -1089,7 +1114,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                         mine[(kScrMax + tg) * 64 + row_of(base + jj)] = v[jj];
         }
         if (t == 0 && (kPing || warp == 0))
-            *reinterpret_cast<int *>(scr + kScrWide * 64 + grp) = wide;
+            *reinterpret_cast<int *>(scr + kScrWide * 64 + grp) = had_wide;
         named_barrier(kAllBar, kSoftmaxThreads);
         const bool whole = (s.seg_begin == s.unit_begin) && (s.seg_end == s.unit_end);
         const int slot_id = whole ? 0 : 2 * (int)blockIdx.x + (s.seg_begin == c.cta_begin ? 0 : 1);
@@ -1110,10 +1135,10 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                     for (int i = 0; i < kTokenGroups; ++i)
                         a[g] += o[(kScrMax + i) * 64 + r];
                     if (scr_i[kScrWide * 64 + g]) {
-                        // what was summed before, relative to m as it was then
-                        const float m0 = o[kScrM0 * 64 + r];
-                        ref[g] = o[kScrMl * 64 + r];
-                        a[g] = o[kScrL * 64 + r] + (m0 == -INFINITY ? a[g] : a[g] * ex2_approx(m0 - ref[g]));
+                        const float ml = o[kScrMl * 64 + r];
+                        ref[g] = fmaxf(m[g], ml);
+                        a[g] = (m[g] == -INFINITY ? a[g] : a[g] * ex2_approx(m[g] - ref[g])) +
+                               (ml == -INFINITY ? o[kScrL * 64 + r] : o[kScrL * 64 + r] * ex2_approx(ml - ref[g]));
                     }
                 }
             }

@@ -108,6 +108,50 @@ def test_decode_beside_a_leading_key_without_value(N_, hq, hkv, bits):
     check_decode(c, q, N_, SCALE, out, lse)
 
 
+# scale bytes of V, with the codes of the row (0: a zero row)
+KINDS = [(0, 0), (0, 0), (0, 0x78), (5, 0x78), (60, 0xF8), (80, 0x78), (100, 0x78), (127, 0xF8), (150, 0x78), (170, 0x78),
+         (200, 0xF8), (240, 0x78)]
+
+
+def mixed(lens, hkv, seed, kinds, most, v_byte=127):
+    g = torch.Generator().manual_seed(seed)
+    draw = lambda n: int(torch.randint(n, (1,), generator=g))               # noqa: E731
+    marks = {}
+    for b, n in enumerate(lens):
+        for _ in range(8):
+            byte, code = kinds[draw(len(kinds))]
+            bits = draw(2 * most) - most + 0.5
+            marks[b, draw(n) if draw(3) else min(draw(3), n - 1)] = (bits, byte, code)
+    return marked(lens, marks, hkv, 128, 16, seed=seed, v_byte=v_byte)
+
+
+@pytest.mark.parametrize("N_,hq,hkv", ROWS)
+@pytest.mark.parametrize("seed", range(4))
+@pytest.mark.parametrize("kinds,most", [(KINDS, 100), (KINDS[:2], 70), (KINDS[:6], 45), (KINDS[5:9], 100)])
+def test_decode_of_weights_and_values_of_all_magnitudes(N_, hq, hkv, seed, kinds, most):
+    """Zero rows, rows of tiny and of huge values with weights far above and below the others', anywhere."""
+    lens = [700, 9000, 260, 64, 1500]
+    c = mixed(lens, hkv, 100 + seed, kinds, most)
+    pool = c.pool()
+    q = queries(c, len(lens), N_ * hq)
+    out, lse = pool.decode_attention(q, N_, scale=SCALE, return_lse=True)
+    assert pool.check_errors() == 0
+    check_decode(c, q, N_, SCALE, out, lse)
+
+
+@pytest.mark.parametrize("n", [3, 7, 70, 200])
+@pytest.mark.parametrize("seed", range(4))
+@pytest.mark.parametrize("kinds,most", [(KINDS, 100), (KINDS[:2], 70), (KINDS[:6], 45), (KINDS[5:9], 100)])
+def test_chunks_of_weights_and_values_of_all_magnitudes(n, seed, kinds, most):
+    lens, new = [700, 5000, 260, 1500], [n, n // 2, n, n]
+    c = mixed(lens, 2, 200 + seed, kinds, most)
+    pool = c.pool()
+    q = queries(c, sum(new), 16)
+    out, lse = pool.chunk_attention(q, new, scale=SCALE, return_lse=True)
+    assert pool.check_errors() == 0
+    check_chunk(c, q, new, SCALE, out, lse)
+
+
 def test_marked_scores_are_what_they_say():
     c = marked([40], {(0, 7): (32.0, 120, None), (0, 9): (-60.0, 127, None)}, 1, 64, 16, seed=1)
     k, _ = c.rows(0)
