@@ -47,6 +47,13 @@ bool on_pool_device(const shkv_q8_pool *pool)
     return cudaGetDevice(&dev) == cudaSuccess && dev == pool->device;
 }
 
+// Calls that wait for their stream cannot be captured into a graph.
+bool capturing(cudaStream_t stream)
+{
+    cudaStreamCaptureStatus s = cudaStreamCaptureStatusNone;
+    return cudaStreamIsCapturing(stream, &s) != cudaSuccess || s != cudaStreamCaptureStatusNone;
+}
+
 int64_t capacity(const shkv_q8_pool *pool) { return (int64_t)pool->cfg.max_pages_per_seq * pool->cfg.page_size; }
 
 // Checks and parameters common to append and read.
@@ -429,8 +436,10 @@ shkv_status shkv_q8_pool_set_seq_lens(shkv_q8_pool *pool, int32_t batch, const i
             return SHKV_ERR_CAPACITY;
     if (batch == 0)
         return SHKV_OK;
-    memcpy(pool->lens, lens, sizeof(int32_t) * batch);
     cudaStream_t st = (cudaStream_t)stream;
+    if (capturing(st))
+        return SHKV_ERR_INVALID_ARG;
+    memcpy(pool->lens, lens, sizeof(int32_t) * batch);
     cudaError_t e =
         cudaMemcpyAsync(pool->cfg.seq_lens, pool->lens, sizeof(int32_t) * batch, cudaMemcpyHostToDevice, st);
     if (e == cudaSuccess)
@@ -560,6 +569,8 @@ shkv_status shkv_q8_check_errors(shkv_q8_pool *pool, void *stream, uint32_t *fla
         return SHKV_ERR_INVALID_ARG;
     *flags = 0;
     cudaStream_t st = (cudaStream_t)stream;
+    if (capturing(st))
+        return SHKV_ERR_INVALID_ARG;
     uint32_t v = 0;
     if (cudaMemcpyAsync(&v, pool->cfg.error_word, sizeof v, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
         cudaStreamSynchronize(st) != cudaSuccess)

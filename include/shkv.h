@@ -551,7 +551,9 @@ typedef struct {
     const int32_t *initial_seq_lens; /* host, nullable */
 } shkv_q8_pool_config;
 
-/* As their shkv_pool counterparts, for an 8-bit pool. */
+/* As their shkv_pool counterparts, for an 8-bit pool.  The calls that wait for
+ * their stream (set_seq_lens, check_errors) refuse one that is being captured
+ * (SHKV_ERR_INVALID_ARG) and change nothing. */
 shkv_status shkv_q8_pool_create(const shkv_q8_pool_config *cfg, shkv_q8_pool **out);
 shkv_status shkv_q8_pool_destroy(shkv_q8_pool *pool);
 shkv_status shkv_q8_pool_set_seq_lens(shkv_q8_pool *pool, int32_t batch, const int32_t *lens, void *stream);

@@ -103,3 +103,24 @@ def test_error_bits_of_another_stream_are_not_lost():
         assert got[0] & N.SHKV_ERRF_PAGE_OOB and not any(g & N.SHKV_ERRF_PAGE_OOB for g in got[1:])
         assert any(g & N.SHKV_ERRF_SEQ_LEN for g in got)
         assert pool.check_errors() == 0
+
+
+def test_calls_that_wait_are_refused_while_their_stream_is_captured():
+    """... before they change anything: the lengths stay, and the capture goes on."""
+    c = Cache([300, 77], 2, 128, 16, seed=49)
+    pool = c.pool()
+    q = c.q(2, 8)
+    pool.decode_attention(q, 1, scale=0.05)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for f in (lambda: pool.set_seq_lens([5, 6]), pool.check_errors):
+            with pytest.raises(N.ShkvError) as e:
+                f()
+            assert e.value.status == N.SHKV_ERR_INVALID_ARG
+        out, lse = pool.decode_attention(q, 1, scale=0.05, return_lse=True)
+    assert pool.host_seq_lens().tolist() == [300, 77]
+    g.replay()
+    torch.cuda.synchronize()
+    assert pool.check_errors() == 0
+    check_decode(c, q, 1, 0.05, out, lse)
