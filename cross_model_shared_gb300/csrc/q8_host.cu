@@ -313,8 +313,9 @@ shkv_status attention(shkv_q8_pool *pool, Q8AttnParams &p, int32_t hq, const voi
                       void *out, float *lse_out, void *workspace, size_t ws_bytes, void *stream)
 {
     const shkv_q8_pool_config &c = pool->cfg;
+    const float scale_log2 = (float)((double)scale * 1.4426950408889634);
     if (!q || !out || !workspace || !aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) ||
-        !aligned(lse_out, 4) || q_stride < (int64_t)hq * c.head_dim || q_stride % 8 || !isfinite(scale) ||
+        !aligned(lse_out, 4) || q_stride < (int64_t)hq * c.head_dim || q_stride % 8 || !isfinite(scale_log2) ||
         ws_bytes < workspace_need(pool))
         return SHKV_ERR_INVALID_ARG;
     p.q = static_cast<const __nv_bfloat16 *>(q);
@@ -332,7 +333,7 @@ shkv_status attention(shkv_q8_pool *pool, Q8AttnParams &p, int32_t hq, const voi
     p.page_size = c.page_size;
     p.max_pages = c.max_pages_per_seq;
     p.num_pages = c.num_pages;
-    p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    p.scale_log2 = scale_log2;
     // requests of up to kMaxDecodeRows rows per KV head go to the stacked
     // kernel, which reads a page once for all of them (16 requests of 4000
     // tokens, 8 KV heads: 64 rows 66 us, where the chunk kernel takes 143 for

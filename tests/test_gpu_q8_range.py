@@ -3,6 +3,8 @@ import numpy as np
 import pytest
 import torch
 
+from cross_model_shared_gb300 import _native as N
+
 from .q8_common import attend, check, check_chunk, check_decode
 from .q8_marked import SCALE, marked, queries, share
 
@@ -150,6 +152,17 @@ def test_chunks_of_weights_and_values_of_all_magnitudes(n, seed, kinds, most):
     out, lse = pool.chunk_attention(q, new, scale=SCALE, return_lse=True)
     assert pool.check_errors() == 0
     check_chunk(c, q, new, SCALE, out, lse)
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -3e38, float("nan"), float("-inf")])
+def test_a_scale_that_leaves_fp32_in_bits_is_refused(scale):
+    c = marked([40], {}, 1, 64, 16, seed=2)
+    pool = c.pool()
+    for call in (lambda: pool.decode_attention(c.q(1, 2), 1, scale=scale),
+                 lambda: pool.chunk_attention(c.q(4, 2), [4], scale=scale)):
+        with pytest.raises(N.ShkvError) as e:
+            call()
+        assert e.value.status == N.SHKV_ERR_INVALID_ARG
 
 
 def test_marked_scores_are_what_they_say():
