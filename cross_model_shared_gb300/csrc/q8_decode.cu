@@ -145,7 +145,7 @@ __host__ __device__ constexpr Smem smem_layout(int nr)
     u.scr = u.qbuf + (uint32_t)nr * 256u;
     u.scales = u.scr + kScrRows * 64 * 4;
     u.info = u.scales + kScaleRing * 2 * kTT;
-    u.bars = u.info + (q_pingpong(nr) ? 0u : kInfo * kTT * 16u);
+    u.bars = u.info + (q_pingpong(nr) ? 0u : kInfo * kTT * 8u);
     u.meta = u.bars + 48 * 8u;
     u.misc = u.meta + kScaleRing * 4u;       // validity words
     u.tslot = u.misc + 8;
@@ -414,26 +414,21 @@ __device__ void warm_l2_q8(const CUtensorMap *tm, const DecodeParams &p, const C
     }
 }
 
-// What a token brings to the softmax: (score factor, V exponent ev, -kVWindow at
-// least, 2^-ev, first row that sees it | kMasked if some token of the warp is not
-// seen by all | kWide if the stage holds a V exponent above the window | kLow if
-// the token's is below it | V's scale byte << 16).  kb, vb: the token's scale
-// bytes; at: its distance from the first key some row does not see.  A NaN row
-// of V makes its key's scores NaN, so that only rows that attend it see it.
-constexpr int kMasked = 0x100, kWide = 0x200, kLow = 0x400;
-__device__ __forceinline__ float4 token_factors(const DecodeParams &p, int kb, int vb, bool valid, int at, bool above)
+// What a token brings to the softmax: (score factor, first row that sees it
+// | kMasked if some token of the warp is not seen by all | kWide if the stage
+// holds a V exponent above the window | V's scale byte << 16).  kb, vb: the
+// token's scale bytes; at: its distance from the first key some row does not
+// see.  A NaN row of V makes its key's scores NaN, so that only rows that attend
+// it see it.
+constexpr int kMasked = 0x100, kWide = 0x200;
+__device__ __forceinline__ float2 token_factors(const DecodeParams &p, int kb, int vb, bool valid, int at, bool above)
 {
-    const int ve = !valid || vb == 255 ? 127 : vb, vc = max(ve, 127 - kVWindow);
+    const int ve = !valid || vb == 255 ? 127 : vb;
     // rows from row_min on see the token (new token i from position L - n + i on)
     const int row_min = valid ? min(64, max(0, (at + 1) * p.group)) : 64;
-    const int flags = (__any_sync(0xffffffffu, row_min > 0) ? kMasked : 0) | (above ? kWide : 0) |
-                      (vc > ve ? kLow : 0);
-    float4 f;
-    f.x = !valid ? 0.f : vb == 255 ? __uint_as_float(0x7fc00000u) : q8_scale((uint32_t)kb) * p.scale_log2;
-    f.y = (float)(vc - 127);
-    f.z = __uint_as_float((uint32_t)(254 - vc) << 23);
-    f.w = __int_as_float(row_min | flags | ve << 16);
-    return f;
+    const int flags = (__any_sync(0xffffffffu, row_min > 0) ? kMasked : 0) | (above ? kWide : 0);
+    return make_float2(!valid ? 0.f : vb == 255 ? __uint_as_float(0x7fc00000u) : q8_scale((uint32_t)kb) * p.scale_log2,
+                       __int_as_float(row_min | flags | ve << 16));
 }
 
 // ---------------------------------------------------------------------------
@@ -490,10 +485,10 @@ __device__ void convert_v(const Q8DecodeParams &q, const Ctx4 &c)
                 const uint32_t four = *reinterpret_cast<const volatile uint32_t *>(sc_four + so);
                 const int kb = *(const volatile uint8_t *)(sc_mine + so), vb = *(const volatile uint8_t *)(sc_mine + so + P);
                 const bool valid = alive && tok0 + t < lim && ((mask >> page) & 1u);
-                const float4 f = token_factors(p, kb, vb, valid, tok0 + t - all_see,
+                const float2 f = token_factors(p, kb, vb, valid, tok0 + t - all_see,
                                                stage_above(four, lim - tok0, mask, log2P));
                 if (alive)
-                    reinterpret_cast<float4 *>(c.smem + L.info)[entry * kTT + t] = f;
+                    reinterpret_cast<float2 *>(c.smem + L.info)[entry * kTT + t] = f;
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar_at(c, kInfoB + (int)entry));
@@ -738,7 +733,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
     // segment's first of the group; has_o: O holds earlier stages; pv_par: parity
     // of the group's previous product.  Leaves the new 7 - m, and in kScrAlpha
     // what the common stages' l takes.
-    auto wide_stage = [&](const float4 &f, int w4, bool first, bool has_o, int k, uint32_t pv_par, uint8_t *prow) {
+    auto wide_stage = [&](float k_factor, int w4, bool first, bool has_o, int k, uint32_t pv_par, uint8_t *prow) {
         const int r = kPing ? t : (int)threadIdx.x;      // the row this thread keeps, below NR
         const int row_min = w4 & 0xff, vb = w4 >> 16;
         // V's codes, where the scale alone does not tell a zero row from one of tiny values
@@ -763,7 +758,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int row = chunk_col(ch) + i;
-                x[i] = row < row_min ? -INFINITY : __uint_as_float(sv[i]) * (f.x * scr[kScrQ * 64 + row]);
+                x[i] = row < row_min ? -INFINITY : __uint_as_float(sv[i]) * (k_factor * scr[kScrQ * 64 + row]);
             }
         };
         // the warp's maxima of x + add over its tokens -> kScrMax
@@ -897,7 +892,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
         for (int j = j0; j < nst; j += kPing ? 2 : 1) {
             const int k = kbase + j, buf = k & 1;
             // the token's factors and S^T
-            float4 f;
+            float2 f;
             if (kPing) {
                 const int slot = k % kScaleRing;
                 wait(bar_at(c, kScaleB + slot), (uint32_t)(k / kScaleRing) & 1u);
@@ -919,8 +914,12 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
             if (wait(bar_at(c, kSFull + buf), (uint32_t)((k >> 1) & 1)))
                 tc_fence_after();
             if (!kPing)
-                f = reinterpret_cast<const float4 *>(c.smem + L.info)[(k % kInfo) * kTT + t];
-            const int w4 = alive ? __float_as_int(f.w) : 64 | kMasked | 127 << 16;
+                f = reinterpret_cast<const float2 *>(c.smem + L.info)[(k % kInfo) * kTT + t];
+            const int w4 = alive ? __float_as_int(f.y) : 64 | kMasked | 127 << 16;
+            // the token's V exponent (a low token's: the window's least), and 2^-ev
+            const int vc = max(w4 >> 16, 127 - kVWindow);
+            const bool low = vc > w4 >> 16;
+            const float ev = (float)(vc - 127), inv_ev = __uint_as_float((uint32_t)(254 - vc) << 23);
             const int row_min = w4 & 0xff;
             const bool masked = (w4 & kMasked) != 0;     // for some token of the warp
             uint8_t *prow = c.smem + L.pbuf + (uint32_t)grp * kPBytes + (uint32_t)t * 128u;
@@ -928,7 +927,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
             // y - m + 7 of this thread's rows (nm = 7 - m), -inf where not seen
             float2 d[NH / 2];
             auto scores = [&](bool relative) {       // (or y itself)
-                const float2 ts2 = make_float2(f.x, f.x), ev2 = make_float2(f.y, f.y);
+                const float2 ts2 = make_float2(f.x, f.x), ev2 = make_float2(ev, ev);
 #pragma unroll
                 for (int c0 = 0; c0 < NH / 8; c0 += kLoad) {
                     uint32_t sv[8 * kLoad];
@@ -978,7 +977,6 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                 for (int i = 0; i < NH / 2; ++i)
                     top = fmaxf(top, fmaxf(d[i].x, d[i].y));
                 // all warps of the stage agree, also where one of them gave up waiting
-                const bool low = (w4 & kLow) != 0;
                 const bool lead = low && top > (w4 >> 16 ? kLeadLow : kLeadLeast);
                 const bool need = lead || (w4 & kWide) != 0;
                 refresh = bar_red_or(bar_id, bar_threads, need || (!low && top > kPLog2 + kRescaleLog2));
@@ -986,7 +984,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                     go_wide = bar_red_or(bar_id, bar_threads, need);
             }
             if (go_wide) {
-                wide_stage(f, w4, !had_wide, j > j0, k, pv_par, prow);
+                wide_stage(f.x, w4, !had_wide, j > j0, k, pv_par, prow);
                 had_wide = true;
                 wide = bar_red_or(bar_id, bar_threads, wide || (w4 & kWide) != 0);
 #pragma unroll
@@ -1065,10 +1063,10 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
 #pragma unroll
             for (int i = 0; i < NH / 2; ++i) {
                 const float2 pe = make_float2(ex2_approx(d[i].x), ex2_approx(d[i].y));
-                l[i] = __ffma2_rn(pe, make_float2(f.z, f.z), l[i]);
+                l[i] = __ffma2_rn(pe, make_float2(inv_ev, inv_ev), l[i]);
                 pk[i] = pack_half2(pe.x, pe.y);
             }
-            if (w4 & kLow)
+            if (low)
 #pragma unroll
                 for (int i = 0; i < NH / 2; ++i)
                     pk[i] = 0u;
