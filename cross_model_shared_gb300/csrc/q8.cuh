@@ -9,10 +9,12 @@
 //
 // A power of two loses nothing against any other scale: dividing by it is
 // exact and e4m3 is a floating format, so only the 4-bit significands are
-// rounded (at most 2^-4 of a value; values under 2^-15 of the row's largest
-// fall on the subnormal grid).  q_i * 2^e is exact in bf16.  A row that holds
-// an infinity or a NaN has s = 255 and every code 0x7f (NaN); a zero row has
-// s = 0.
+// rounded (at most 2^-4 of a value; values under 2^-6 after scaling, 2^-14.8 to
+// 2^-13.8 of the row's largest, fall on the subnormal grid).  q_i * 2^e is exact
+// in bf16 but at its ends: its smallest subnormals, and a value of 1.9375 * 2^127
+// or more, whose code at e = 120 is 256 and which so reads back as an infinity.
+// A row that holds an infinity or a NaN has s = 255 and every code 0x7f (NaN); a
+// zero row has s = 0.
 #pragma once
 
 #include <cuda_bf16.h>

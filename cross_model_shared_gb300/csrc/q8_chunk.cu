@@ -450,6 +450,7 @@ __device__ void chunk_qk(const Q8ChunkParams &p, const Ctx &c, uint32_t tmem)
                 if (alive) {
                     tc_fence_after();
                     const uint64_t qd = qd0 + ((2u * (uint32_t)x * kQTermBytes) >> 4);
+                    // (rolled, as in q8_decode.cu)
 #pragma unroll 1
                     for (int i = 0; i < steps; ++i) {
                         umma_f8(tmem + col_s(x), qd + (uint64_t)(2 * i), kd + (uint64_t)(2 * i), idesc, i ? 1u : 0u);

@@ -18,10 +18,12 @@
 //
 // K's codes go to the tensor cores as they lie in the page.  A bf16 query has
 // 8 significant bits: its row is scaled by a power of two to at most 448 and
-// split into two e4m3 terms, qh nearest and ql = q - qh, which is exact but
-// for values under 2^-15 of the row's largest.  V's codes are moved to fp16
-// in shared memory (sign and seven bits, exponent bias and all: v8 * 2^-8,
-// exactly).  With the token's V exponent inside y, P is relative to the row's
+// split into two e4m3 terms, qh nearest and ql = q - qh.  That is exact for
+// values of 2^-2 and more after scaling (2^-9.8 of the row's largest at most);
+// smaller ones are held to 2^-10, half of e4m3's least step: 2^-17.8 of the
+// largest.  (A third term would cost half as many QK products again.)  V's codes
+// are moved to fp16 in shared memory (sign and seven bits, exponent bias and all:
+// v8 * 2^-8, exactly).  With the token's V exponent inside y, P is relative to the row's
 // largest weight times value scale, so that fp16 holds 11 bits of every token
 // that matters to the sum, whatever the magnitudes of weights and values apart:
 // fp16's least step, 2^-24, is 2^-31 of that largest, and 2^20 tokens below it
@@ -261,10 +263,11 @@ __device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t w)
 // page took as long to issue as the codes, 600 cycles a stage of 16-token
 // pages, and this warp then bounded long contexts), and publishes the stage's
 // validity word, on barriers of a ring of their own, so that they wait for no
-// V slot.  The K warp writes
-// entry k once QK(k - KS) is complete, and QK(i) waits for the factors that
-// the V conversion's warps take from the scales of stage i: entries up to
-// k - KS are free.
+// V slot.  The K warp writes entry k once QK(k - KS) is complete, and entry
+// k - 8 must be through by then.  Above 48 rows QK(i) waits for the factors that
+// the V conversion's warps take from the scales of stage i.  Up to 48 it waits for
+// the softmax to have read the scores of stage i - 2, whose group took the scales
+// of its stage i - 4 before: entries up to k - 8.
 __device__ __forceinline__ void cp_async16(uint32_t to, const void *from)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
@@ -565,6 +568,8 @@ __device__ void qk_issuer(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem)
             if (alive) {
                 tc_fence_after();
                 const uint32_t d = tmem + kColS + buf * 64u;
+                // (rolled: unrolled, with the accumulate flag a constant, the first
+                // product of a stage was added to what TMEM held before)
 #pragma unroll 1
                 for (int i = 0; i < steps; ++i) {
                     umma_f8(d, kd + (uint64_t)(2 * i), qh0 + (uint64_t)(2 * i), idesc, i ? 1u : 0u);

@@ -336,12 +336,12 @@ shkv_status attention(shkv_q8_pool *pool, Q8AttnParams &p, int32_t hq, const voi
     p.scale_log2 = scale_log2;
     // requests of up to kMaxDecodeRows rows per KV head go to the stacked
     // kernel, which reads a page once for all of them (16 requests of 4000
-    // tokens, 8 KV heads: 64 rows 66 us, where the chunk kernel takes 143 for
-    // 68 rows, 155 for 128: one tile, nothing to overlap its chain with), the
-    // others to the chunk kernel; a few small requests beside large ones go
-    // along with them, where that costs a CTA less than the second launch
-    // (about 12 us, the time of 6 stages; a mixed batch of 9 requests took
-    // 41 us with it, 24 without)
+    // tokens, 8 KV heads: 64 rows 51 us; the chunk kernel takes 69 us for 68 to
+    // 128 rows: one tile, nothing to overlap its chain with, so 68 rows cost a
+    // third more than 64), the others to the chunk kernel; a few small requests
+    // beside large ones go along with them, where that costs a CTA less than the
+    // second launch (about 12 us, the time of 6 stages; a mixed batch of 9
+    // requests took 41 us with it, 24 without)
     int max_rows = 0;
     int64_t tokens = 0, small_cost = 0;
     Q8AttnParams large = p;

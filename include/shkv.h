@@ -517,8 +517,10 @@ shkv_status shkv_partition_requests(int32_t batch, const int32_t *seq_lens, int3
  *                   scale byte = e + 127 (e8m0);  the row stands for code_i * 2^e
  *   A row with an infinity or a NaN is stored as NaN (scale byte 255, codes
  *   0x7f; NaN codes occur in no other row); a zero row has scale byte 0.
- *   code_i * 2^e is exact in bf16 (its smallest subnormals aside), and
- *   quantising a row that was read back gives the same values.
+ *   code_i * 2^e is exact in bf16 but at its ends: its smallest subnormals, and
+ *   magnitudes of 1.9375 * 2^127 and more, which become 2^128 and read back as
+ *   infinities.  Those aside, quantising a row that was read back gives the same
+ *   values.
  *
  *   k_pages, v_pages  device e4m3 [num_pages, num_kv_heads, page_size, head_dim]
  *   scales            device e8m0 [num_pages, num_kv_heads, 2, page_size]: K's
@@ -608,6 +610,15 @@ shkv_status shkv_q8_workspace_size(const shkv_q8_pool *pool, size_t *bytes, size
  * out = 0 and lse = -inf.  A NaN row of K or V makes out and lse of the rows
  * that attend it NaN.  Errors: SHKV_ERR_INVALID_ARG, SHKV_ERR_UNSUPPORTED,
  * SHKV_ERR_CUDA; device error bits as in shkv_decode_attention.
+ * Arithmetic (this call and the next): query values are held to 2^-17.8 of
+ * their row's largest magnitude (those above 2^-9.8 of it exactly), K and V as
+ * stored, scores, softmax sums and outputs in fp32 until one rounding to bf16.
+ * A softmax weight is rounded to 11 bits for its product with V, and may count
+ * as 0 there where weight times V scale is under 2^-31 of the row's largest.
+ * Weights and V scales may lie apart as far as fp32 exponents reach (a weight
+ * under 2^-126 of the row's largest counts as 0).  V scales above 2^40 (stacked
+ * rows) or 2^60 (chunks), and keys that lead the others by 2^9 with V scales under
+ * 2^-40, or by 2^41 with rows of zeros, take slower stages.
  */
 shkv_status shkv_q8_decode_attention(shkv_q8_pool *pool, int32_t batch, int32_t n_models, int32_t hq_per_model,
                                      const void *q, float scale, void *out, float *lse_out, void *workspace,

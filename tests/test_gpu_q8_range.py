@@ -154,6 +154,22 @@ def test_chunks_of_weights_and_values_of_all_magnitudes(n, seed, kinds, most):
     check_chunk(c, q, new, SCALE, out, lse)
 
 
+@pytest.mark.parametrize("new", [3, 100])
+def test_queries_with_large_channels(new):
+    """Query channels 2^13 apart (massive activations): the small ones are held to 2^-17.8 of the largest, as the
+    tolerance has it for every query."""
+    c = marked([2000], {}, 2, 128, 16, seed=75)
+    q = queries(c, new, 8)
+    q[..., 17] = 8192.0
+    q[..., 40] = -3000.0
+    c.k[..., 17] = 0x08                  # 2^-6: its product with the large channel is of ordinary size
+    c.k[..., 40] = 0
+    pool = c.pool()
+    out, lse = pool.chunk_attention(q, [new], scale=0.1, return_lse=True)
+    assert pool.check_errors() == 0
+    check_chunk(c, q, [new], 0.1, out, lse)
+
+
 @pytest.mark.parametrize("scale", [2.4e38, -3e38, float("nan"), float("-inf")])
 def test_a_scale_that_leaves_fp32_in_bits_is_refused(scale):
     c = marked([40], {}, 1, 64, 16, seed=2)
