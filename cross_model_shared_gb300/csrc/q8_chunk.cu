@@ -774,7 +774,12 @@ __device__ void chunk_softmax(const Q8ChunkParams &p, const Ctx &c, uint32_t tme
                     m_l = m_old;
                 }
                 if (!apart) {
-                    lsum *= scale_o;
+                    // (in halves: where m rises by V's exponents, up to 2^120, the weights so far can
+                    // matter past fp32's least normal number; what they brought to O does not)
+                    if (m_use != m_old && m_old != -INFINITY) {
+                        const float half = ex2_approx(0.5f * (m_old - m_use));
+                        lsum = lsum * half * half;
+                    }
                 } else if (m_l == -INFINITY) {
                     m_l = cm;
                 } else if (cm > m_l + kRescaleLog2) {

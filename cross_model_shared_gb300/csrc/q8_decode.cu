@@ -737,7 +737,9 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
     // state in shared memory, as the common stage has the registers.  first: the
     // segment's first of the group; has_o: O holds earlier stages; pv_par: parity
     // of the group's previous product.  Leaves the new 7 - m, and in kScrAlpha
-    // what the common stages' l takes.
+    // half of what the common stages' l takes (twice: where m rises by V's
+    // exponents, up to 2^167, the weights so far can matter past fp32's least
+    // normal number; what they brought to O does not).
     auto wide_stage = [&](float k_factor, int w4, bool first, bool has_o, int k, uint32_t pv_par, uint8_t *prow) {
         const int r = kPing ? t : (int)threadIdx.x;      // the row this thread keeps, below NR
         const int row_min = w4 & 0xff, vb = w4 >> 16;
@@ -791,6 +793,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
         maxima(ev);
         named_barrier(bar_id, bar_threads);
         bool moves = false;
+        float half = 1.f;
         if (r < NR) {
             const float mo = mine[kScrM * 64 + r], mn = moved(mo);
             if (first) {
@@ -800,6 +803,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
             moves = mn != mo;
             mine[kScrNew * 64 + r] = mn == -INFINITY ? 1e30f : kPLog2 - mn;
             mine[kScrAlpha * 64 + r] = moves ? ex2_approx(mo - mn) : 1.f;
+            half = moves ? ex2_approx(0.5f * (mo - mn)) : 1.f;
             mine[kScrM * 64 + r] = mn;
         }
         if (bar_red_or(bar_id, bar_threads, moves) && has_o) {
@@ -827,6 +831,7 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
             if (mn != ml)
                 mine[kScrL * 64 + r] *= ex2_approx(ml - mn);
             mine[kScrMl * 64 + r] = mn;
+            mine[kScrAlpha * 64 + r] = half;
         }
         named_barrier(bar_id, bar_threads);
         if (k >= (kPing ? 2 : 1))
@@ -997,7 +1002,8 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                     const int rr = row_of(2 * i);
                     if (kNmRegs)
                         nmu[kNmRegs ? i : 0] = make_float2(mine[kScrNew * 64 + rr], mine[kScrNew * 64 + rr + 1]);
-                    l[i] = __fmul2_rn(l[i], make_float2(mine[kScrAlpha * 64 + rr], mine[kScrAlpha * 64 + rr + 1]));
+                    const float2 half = make_float2(mine[kScrAlpha * 64 + rr], mine[kScrAlpha * 64 + rr + 1]);
+                    l[i] = __fmul2_rn(__fmul2_rn(l[i], half), half);
                 }
                 continue;
             }
@@ -1138,10 +1144,16 @@ __device__ void softmax_q8(const Q8DecodeParams &q, const Ctx4 &c, uint32_t tmem
                     for (int i = 0; i < kTokenGroups; ++i)
                         a[g] += o[(kScrMax + i) * 64 + r];
                     if (scr_i[kScrWide * 64 + g]) {
+                        // the larger of the common and the wide stages' parts decides, by its exponent (a sum may
+                        // be 2^-120 beside its reference, see the wide stage)
                         const float ml = o[kScrMl * 64 + r];
-                        ref[g] = fmaxf(m[g], ml);
-                        a[g] = (m[g] == -INFINITY ? a[g] : a[g] * ex2_approx(m[g] - ref[g])) +
-                               (ml == -INFINITY ? o[kScrL * 64 + r] : o[kScrL * 64 + r] * ex2_approx(ml - ref[g]));
+                        const float b = o[kScrL * 64 + r];
+                        const float ta = a[g] > 0.f ? m[g] + (float)ilogbf(a[g]) : -INFINITY;
+                        const float tb = b > 0.f ? ml + (float)ilogbf(b) : -INFINITY;
+                        ref[g] = fmaxf(ta, tb);
+                        const float ha = ta == -INFINITY ? 1.f : ex2_approx(0.5f * (m[g] - ref[g]));
+                        const float hb = tb == -INFINITY ? 1.f : ex2_approx(0.5f * (ml - ref[g]));
+                        a[g] = a[g] * ha * ha + b * hb * hb;     // (NaN where one is)
                     }
                 }
             }

@@ -110,6 +110,32 @@ def test_decode_beside_a_leading_key_without_value(N_, hq, hkv, bits):
     check_decode(c, q, N_, SCALE, out, lse)
 
 
+# (scale byte of the others' V, bits of the marked token's score, its byte): the reference of P rises by 2^126 and more
+# while the others keep a part of the weights
+RISES = [(127, 10.0, 247), (127, 20.0, 240), (87, 5.0, 247), (70, 18.0, 180), (68, 8.0, 187), (20, 3.0, 150), (5, 0.0, 247)]
+
+
+@pytest.mark.parametrize("N_,hq,hkv", ROWS)
+@pytest.mark.parametrize("v_byte,bits,byte", RISES)
+def test_decode_keeps_the_weights_before_a_value_of_far_larger_scale(N_, hq, hkv, v_byte, bits, byte):
+    lens = [700, 9000, 260]
+    marks = {(b, n * 2 // 3): (bits, byte, 0x70) for b, n in enumerate(lens)}
+    c = marked(lens, marks, hkv, 128, 16, seed=77, v_byte=v_byte)
+    pool = c.pool()
+    q = queries(c, 3, N_ * hq)
+    out, lse = pool.decode_attention(q, N_, scale=SCALE, return_lse=True)
+    assert pool.check_errors() == 0
+    check_decode(c, q, N_, SCALE, out, lse)
+
+
+@pytest.mark.parametrize("v_byte,bits,byte", RISES)
+@pytest.mark.parametrize("copies", [1, 160])
+def test_chunk_keeps_the_weights_before_a_value_of_far_larger_scale(v_byte, bits, byte, copies):
+    """160 requests of one unit each: none is split."""
+    c = share(marked([9000], {(0, 6000): (bits, byte, 0x70)}, 1, 128, 16, seed=78, v_byte=v_byte), copies)
+    chunk_some(c, [32] * copies, 8, [0, copies - 1], [0])
+
+
 # scale bytes of V, with the codes of the row (0: a zero row)
 KINDS = [(0, 0), (0, 0), (0, 0x78), (5, 0x78), (60, 0xF8), (80, 0x78), (100, 0x78), (127, 0xF8), (150, 0x78), (170, 0x78),
          (200, 0xF8), (240, 0x78)]
