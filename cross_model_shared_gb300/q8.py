@@ -63,14 +63,14 @@ class QuantizedKVPool:
     named stream, or where a side stream is current, holds its tensors back:
     they may be dropped once it has returned, whichever stream they are of.  On
     the default stream, unnamed, tensors of other streams are the caller's to
-    keep or record, as with torch's own operations.  The pool may be dropped at any time.  A captured call's
-    tensors, and the pool, have to live as long as the graph.  The workspace
-    of the attentions is one per stream; a call that is being captured into a
+    keep or record, as with torch's own operations.  The pool may be dropped at
+    any time.  A captured call's tensors, and the pool, have to live as long as
+    the graph.  The workspace of the attentions is one per stream; a call that is being captured into a
     CUDA graph takes one of its own from the graph's memory, so graphs share
     none.  ``workspace=`` names another, of ``workspace_bytes`` bytes (40 MB at
     head_dim 128) whose first ``workspace_zero_bytes`` are zero before its first
-    use; the layers of a model, each with a pool of its own, can share one, as
-    their calls on a stream follow one another.
+    use; pools of one shape, as the layers of a model have, can share one where
+    their calls follow one another on a stream.
     """
 
     def __init__(self, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int, max_batch: int,

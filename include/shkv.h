@@ -599,7 +599,7 @@ shkv_status shkv_q8_read_kv(shkv_q8_pool *pool, int32_t batch, const int32_t *st
  * any shape.  Its first *zero_bytes bytes must be zero before its first use
  * and are left so by every call that completes without device error bits;
  * the rest may hold anything.  Calls sharing one workspace must not overlap on
- * the GPU.
+ * the GPU, and be on pools of equal max_batch and num_kv_heads (the front's size).
  */
 shkv_status shkv_q8_workspace_size(const shkv_q8_pool *pool, size_t *bytes, size_t *zero_bytes);
 
