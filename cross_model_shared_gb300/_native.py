@@ -24,6 +24,7 @@ SHKV_ERRF_PAGE_OOB = 0x1
 SHKV_ERRF_SEQ_LEN = 0x2
 SHKV_ERRF_TIMEOUT = 0x4
 SHKV_ERRF_PIPELINE = 0x8
+SHKV_ERRF_INDEX = 0x10
 
 SHKV_MAX_BATCH = 1024
 
@@ -40,6 +41,7 @@ EXPORTS = [
     "shkv_partition_requests", "shkv_selftest_bounded_wait", "shkv_q8_pool_create", "shkv_q8_pool_destroy",
     "shkv_q8_pool_set_seq_lens", "shkv_q8_pool_get_seq_lens", "shkv_q8_check_errors", "shkv_q8_append_kv",
     "shkv_q8_read_kv", "shkv_q8_workspace_size", "shkv_q8_decode_attention", "shkv_q8_chunk_attention",
+    "shkv_decode_mass", "shkv_prefill_mass", "shkv_select_tokens", "shkv_evict_tokens",
 ]
 
 SHKV_CONSUMER_AUTO = -1
@@ -82,6 +84,14 @@ class shkv_q8_pool_config(ctypes.Structure):
         ("seq_lens", ctypes.c_void_p),
         ("error_word", ctypes.c_void_p),
         ("initial_seq_lens", ctypes.c_void_p),
+    ]
+
+
+class shkv_mass(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("request_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
     ]
 
 
@@ -128,6 +138,7 @@ def load() -> ctypes.CDLL:
                           "`python -m cross_model_shared_gb300.build` (needs nvcc)")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, u32p, i32p = ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(ctypes.c_uint32), ctypes.c_void_p
+    i64, mass = ctypes.c_int64, ctypes.POINTER(shkv_mass)
     sig = {
         "shkv_pool_create": [ctypes.POINTER(shkv_pool_config), ctypes.POINTER(vp)],
         "shkv_pool_destroy": [vp],
@@ -171,6 +182,11 @@ def load() -> ctypes.CDLL:
         "shkv_q8_decode_attention": [vp, i32, i32, i32, vp, ctypes.c_float, vp, vp, vp, ctypes.c_size_t, vp],
         "shkv_q8_chunk_attention": [vp, i32, i32p, i32, vp, ctypes.c_int64, ctypes.c_float, vp, vp, vp,
                                     ctypes.c_size_t, vp],
+        "shkv_decode_mass": [vp, i32, i32, i32, vp, ctypes.c_float, vp, ctypes.c_float, mass, mass, vp],
+        "shkv_prefill_mass": [vp, i32, i32, i32, vp, i64, i64, ctypes.c_float, vp, i64, i64, ctypes.c_float, mass,
+                              mass, vp],
+        "shkv_select_tokens": [vp, i32, mass, i32p, i32, i32, vp, i64, vp],
+        "shkv_evict_tokens": [vp, i32, i32p, vp, i64, vp, i64, vp, i64, i32p, mass, mass, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -400,3 +416,33 @@ def shkv_q8_chunk_attention(pool: int, batch: int, new_lens: int, hq: int, q: in
                             out: int, lse_out: int, workspace: int, workspace_bytes: int, stream: int) -> None:
     _check(load().shkv_q8_chunk_attention(pool, batch, new_lens, hq, q, q_stride, scale, out, lse_out, workspace,
                                           workspace_bytes, stream), "shkv_q8_chunk_attention")
+
+
+def _ref(mass):
+    return ctypes.byref(mass) if mass is not None else None
+
+
+def shkv_decode_mass(pool: int, batch: int, n_models: int, hq: int, q: int, scale: float, lse: int, decay: float,
+                     mass, out: shkv_mass, stream: int) -> None:
+    _check(load().shkv_decode_mass(pool, batch, n_models, hq, q, scale, lse, decay, _ref(mass), _ref(out), stream),
+           "shkv_decode_mass")
+
+
+def shkv_prefill_mass(pool: int, batch: int, n_new: int, hq: int, q: int, q_request_stride: int, q_token_stride: int,
+                      scale: float, lse: int, lse_request_stride: int, lse_token_stride: int, decay: float, mass,
+                      out: shkv_mass, stream: int) -> None:
+    _check(load().shkv_prefill_mass(pool, batch, n_new, hq, q, q_request_stride, q_token_stride, scale, lse,
+                                    lse_request_stride, lse_token_stride, decay, _ref(mass), _ref(out), stream),
+           "shkv_prefill_mass")
+
+
+def shkv_select_tokens(pool: int, batch: int, mass: shkv_mass, keep: int, sink: int, recent: int, index: int,
+                       index_stride: int, stream: int) -> None:
+    _check(load().shkv_select_tokens(pool, batch, _ref(mass), keep, sink, recent, index, index_stride, stream),
+           "shkv_select_tokens")
+
+
+def shkv_evict_tokens(pool: int, batch: int, keep: int, index: int, index_stride: int, new_table: int,
+                      new_table_stride: int, table: int, table_stride: int, lens: int, mass, out, stream: int) -> None:
+    _check(load().shkv_evict_tokens(pool, batch, keep, index, index_stride, new_table, new_table_stride, table,
+                                    table_stride, lens, _ref(mass), _ref(out), stream), "shkv_evict_tokens")

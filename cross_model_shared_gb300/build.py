@@ -19,7 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libshkv.so")
 SOURCES = ["decode_attn.cu", "decode_umma.cu", "prefill_umma.cu", "append_merge.cu", "selftest.cu", "shkv_host.cu",
-           "q8_cache.cu", "q8_decode.cu", "q8_chunk.cu", "q8_host.cu", "page_manager.cpp", "shard.cpp"]
+           "q8_cache.cu", "q8_decode.cu", "q8_chunk.cu", "q8_host.cu", "mass.cu", "evict.cu", "evict_host.cu",
+           "page_manager.cpp", "shard.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,312 @@
+// evict_host.cu -- the C ABI of eviction by accumulated attention weight:
+// argument checks and kernel launches.  Declarations and their contracts are in
+// include/shkv.h.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <algorithm>
+#include <exception>
+
+#include "evict.cuh"
+#include "host_shared.h"
+#include "shkv.h"
+
+namespace shkv {
+cudaError_t launch_mass(const MassParams &p, cudaStream_t stream);
+cudaError_t launch_select(const SelectParams &p, cudaStream_t stream);
+cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream);
+}  // namespace shkv
+
+using namespace shkv;
+
+namespace {
+
+bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+shkv_status status_of(cudaError_t e) { return e == cudaSuccess ? SHKV_OK : SHKV_ERR_CUDA; }
+
+// A pool, a batch that it takes, and its device current.
+bool callable(const shkv_pool *pool, int32_t batch)
+{
+    int dev = -1;
+    return pool && batch >= 0 && batch <= pool->cfg.max_batch && batch <= SHKV_MAX_BATCH &&
+           cudaGetDevice(&dev) == cudaSuccess && dev == pool->device;
+}
+
+int64_t longest(int32_t batch, const int32_t *lens)
+{
+    int64_t n = 0;
+    for (int b = 0; b < batch; ++b)
+        n = std::max<int64_t>(n, lens[b]);
+    return n;
+}
+
+// Masses that a call reads.
+bool readable(const shkv_mass *m)
+{
+    return m && m->data && aligned(m->data, 4) && m->request_stride >= 0 && m->head_stride >= 0;
+}
+
+// Masses that a call writes: the rows of `len` must not overlap, whichever of
+// requests and heads lies outside.
+bool writable(const shkv_mass *m, int32_t batch, int32_t hkv, int64_t len)
+{
+    if (!readable(m))
+        return false;
+    const int64_t r = m->request_stride, h = m->head_stride;
+    if (batch == 1 || hkv == 1)
+        return batch * hkv == 1 || (batch == 1 ? h : r) >= len;
+    return (h >= len && r >= h * (hkv - 1) + len) || (r >= len && h >= r * (batch - 1) + len);
+}
+
+// The same masses have the same strides (those that are used).
+bool same_layout(const shkv_mass *a, const shkv_mass *b, int32_t batch, int32_t hkv)
+{
+    return a->data != b->data || ((batch == 1 || a->request_stride == b->request_stride) &&
+                                  (hkv == 1 || a->head_stride == b->head_stride));
+}
+
+Span mass_span(const float *data, int64_t request_stride, int64_t head_stride, int32_t batch, int32_t hkv, int64_t len)
+{
+    return span_of(data, (size_t)((batch - 1) * request_stride + (hkv - 1) * head_stride + len) * 4);
+}
+
+// Both forms: the n_q query tokens of every request.
+shkv_status add_mass(shkv_pool *pool, int32_t batch, int32_t n_q, int32_t hq, const void *q, int64_t q_request,
+                     int64_t q_token, float scale, const float *lse, int64_t lse_request, int64_t lse_token,
+                     float decay, const shkv_mass *mass, const shkv_mass *out, bool causal, void *stream)
+{
+    const shkv_pool_config &c = pool->cfg;
+    const int64_t row = (int64_t)hq * c.head_dim;
+    if (batch == 1)                      // a stride that no step is taken along
+        q_request = n_q * q_token, lse_request = 0;
+    if (n_q == 1)
+        q_token = row, lse_token = 0;
+    const float scale_log2 = (float)((double)scale * 1.4426950408889634);
+    const int64_t len = longest(batch, pool->lens.data());
+    if (!q || !aligned(q, 16) || !lse || !aligned(lse, 4) || q_token < row || q_token % 8 || q_request <= 0 ||
+        q_request % 8 || lse_request < 0 || lse_token < 0 || !isfinite(scale_log2) || !isfinite(decay) ||
+        !writable(out, batch, c.num_kv_heads, len) ||
+        (mass && (!readable(mass) || !same_layout(mass, out, batch, c.num_kv_heads))))
+        return SHKV_ERR_INVALID_ARG;
+    MassParams p;
+    memset(&p, 0, sizeof p);
+    int64_t tiles = 0;
+    for (int b = 0; b < batch; ++b) {
+        p.lens[b] = pool->lens[b];
+        p.tile0[b] = (int32_t)tiles;
+        tiles += (pool->lens[b] + 127) / 128;
+        if (tiles * c.num_kv_heads > INT32_MAX)
+            return SHKV_ERR_UNSUPPORTED;
+    }
+    p.tile0[batch] = (int32_t)tiles;
+    if (tiles == 0)
+        return SHKV_OK;
+    p.k_pages = static_cast<const __nv_bfloat16 *>(c.k_pages);
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.lse = lse;
+    p.q_request = q_request;
+    p.q_token = q_token;
+    p.lse_request = lse_request;
+    p.lse_token = lse_token;
+    if (mass && decay != 0.f) {
+        p.mass.in = mass->data;
+        p.mass.in_request = mass->request_stride;
+        p.mass.in_head = mass->head_stride;
+    }
+    p.mass.out = out->data;
+    p.mass.out_request = out->request_stride;
+    p.mass.out_head = out->head_stride;
+    p.block_table = c.block_table;
+    p.seq_lens = c.seq_lens;
+    p.err = c.error_word;
+    p.batch = batch;
+    p.n_q = n_q;
+    p.hq = hq;
+    p.hkv = c.num_kv_heads;
+    p.group = hq / c.num_kv_heads;
+    p.head_dim = c.head_dim;
+    p.page_size = c.page_size;
+    p.max_pages = c.max_pages_per_seq;
+    p.num_pages = c.num_pages;
+    p.causal = causal;
+    p.scale_log2 = scale_log2;
+    p.decay = decay;
+    if (launch_mass(p, (cudaStream_t)stream) != cudaSuccess)
+        return SHKV_ERR_CUDA;
+    record_stream_use(stream,
+                      {span_of(q, (size_t)((batch - 1) * q_request + (n_q - 1) * q_token + row) * 2),
+                       span_of(lse, (size_t)((batch - 1) * lse_request + (n_q - 1) * lse_token + hq) * 4),
+                       mass_span(p.mass.in, p.mass.in_request, p.mass.in_head, batch, c.num_kv_heads, len),
+                       mass_span(p.mass.out, p.mass.out_request, p.mass.out_head, batch, c.num_kv_heads, len)});
+    return SHKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+shkv_status shkv_decode_mass(shkv_pool *pool, int32_t batch, int32_t n_models, int32_t hq_per_model, const void *q,
+                             float scale, const float *lse, float decay, const shkv_mass *mass, const shkv_mass *out,
+                             void *stream)
+try {
+    if (!callable(pool, batch) || batch < 1 || n_models < 1 || hq_per_model < 1)
+        return SHKV_ERR_INVALID_ARG;
+    const int32_t hkv = pool->cfg.num_kv_heads;
+    if (hq_per_model % hkv || (int64_t)n_models * (hq_per_model / hkv) > 64)
+        return SHKV_ERR_UNSUPPORTED;
+    const int64_t row = (int64_t)hq_per_model * pool->cfg.head_dim;
+    return add_mass(pool, batch, n_models, hq_per_model, q, n_models * row, row, scale, lse,
+                    (int64_t)n_models * hq_per_model, hq_per_model, decay, mass, out, false, stream);
+} catch (const std::exception &) {
+    return SHKV_ERR_CUDA;                // no host memory
+}
+
+shkv_status shkv_prefill_mass(shkv_pool *pool, int32_t batch, int32_t n_new, int32_t hq_per_model, const void *q,
+                              int64_t q_request_stride, int64_t q_token_stride, float scale, const float *lse,
+                              int64_t lse_request_stride, int64_t lse_token_stride, float decay,
+                              const shkv_mass *mass, const shkv_mass *out, void *stream)
+try {
+    if (!callable(pool, batch) || batch < 1 || n_new < 1 || hq_per_model < 1)
+        return SHKV_ERR_INVALID_ARG;
+    const int32_t hkv = pool->cfg.num_kv_heads;
+    if (hq_per_model % hkv || hq_per_model / hkv > 128)
+        return SHKV_ERR_UNSUPPORTED;
+    for (int b = 0; b < batch; ++b)
+        if (pool->lens[b] < n_new)
+            return SHKV_ERR_INVALID_ARG;     // the new tokens must already be in the pool
+    return add_mass(pool, batch, n_new, hq_per_model, q, q_request_stride, q_token_stride, scale, lse,
+                    lse_request_stride, lse_token_stride, decay, mass, out, true, stream);
+} catch (const std::exception &) {
+    return SHKV_ERR_CUDA;                // no host memory
+}
+
+shkv_status shkv_select_tokens(shkv_pool *pool, int32_t batch, const shkv_mass *mass, const int32_t *keep,
+                               int32_t sink, int32_t recent, int32_t *index, int64_t index_stride, void *stream)
+try {
+    if (!callable(pool, batch) || !keep || sink < 0 || recent < 0)
+        return SHKV_ERR_INVALID_ARG;
+    if (batch == 0)
+        return SHKV_OK;
+    if (!readable(mass) || !index || !aligned(index, 4) || index_stride < 1 || index_stride > INT32_MAX)
+        return SHKV_ERR_INVALID_ARG;
+    const int32_t hkv = pool->cfg.num_kv_heads;
+    SelectParams p;
+    memset(&p, 0, sizeof p);
+    for (int b = 0; b < batch; ++b) {
+        const int32_t L = pool->lens[b];
+        if (keep[b] < 0 || std::min(keep[b], L) > index_stride ||
+            (keep[b] < L && (int64_t)sink + recent > keep[b]))
+            return SHKV_ERR_INVALID_ARG;
+        p.lens[b] = L;
+        p.keep[b] = keep[b];
+    }
+    if ((int64_t)batch * hkv > INT32_MAX)
+        return SHKV_ERR_UNSUPPORTED;
+    p.mass = mass->data;
+    p.mass_request = mass->request_stride;
+    p.mass_head = mass->head_stride;
+    p.index = index;
+    p.index_stride = index_stride;
+    p.seq_lens = pool->cfg.seq_lens;
+    p.err = pool->cfg.error_word;
+    p.batch = batch;
+    p.hkv = hkv;
+    p.sink = sink;
+    p.recent = recent;
+    if (launch_select(p, (cudaStream_t)stream) != cudaSuccess)
+        return SHKV_ERR_CUDA;
+    record_stream_use(stream, {mass_span(p.mass, p.mass_request, p.mass_head, batch, hkv, longest(batch, p.lens)),
+                               span_of(index, (size_t)batch * hkv * index_stride * 4)});
+    return SHKV_OK;
+} catch (const std::exception &) {
+    return SHKV_ERR_CUDA;                // no host memory
+}
+
+shkv_status shkv_evict_tokens(shkv_pool *pool, int32_t batch, const int32_t *keep, const int32_t *index,
+                              int64_t index_stride, const int32_t *new_table, int64_t new_table_stride,
+                              const int32_t *table, int64_t table_stride, const int32_t *lens, const shkv_mass *mass,
+                              const shkv_mass *out, void *stream)
+try {
+    if (!callable(pool, batch) || !keep || !table != !lens || !mass != !out)
+        return SHKV_ERR_INVALID_ARG;
+    const shkv_pool_config &c = pool->cfg;
+    EvictParams p;
+    memset(&p, 0, sizeof p);
+    int64_t pages = 0, len = 0;
+    bool moves = false;
+    if (!table)
+        table_stride = c.max_pages_per_seq;
+    for (int b = 0; b < batch; ++b) {
+        const int32_t L = lens ? lens[b] : pool->lens[b];
+        if (keep[b] < 0 || L < 0 || (int64_t)L > table_stride * c.page_size)
+            return SHKV_ERR_INVALID_ARG;
+        p.lens[b] = L;
+        p.keep[b] = keep[b];
+        p.page0[b] = (int32_t)pages;
+        if (keep[b] >= L)
+            continue;
+        moves = true;
+        len = std::max<int64_t>(len, L);
+        const int64_t n = ((int64_t)keep[b] + c.page_size - 1) / c.page_size;
+        if (n > c.max_pages_per_seq)
+            return SHKV_ERR_CAPACITY;
+        if (n > new_table_stride || keep[b] > index_stride)
+            return SHKV_ERR_INVALID_ARG;
+        pages += n;
+    }
+    p.page0[batch] = (int32_t)pages;     // at most SHKV_MAX_BATCH * max_pages_per_seq; checked below
+    if (!moves)
+        return SHKV_OK;
+    if (pages > 0 && (!index || !new_table || !aligned(index, 4) || !aligned(new_table, 4) || new_table == c.block_table))
+        return SHKV_ERR_INVALID_ARG;
+    if (table && !aligned(table, 4))
+        return SHKV_ERR_INVALID_ARG;
+    if (out && (!readable(mass) || !writable(out, batch, c.num_kv_heads, len) ||
+                !same_layout(mass, out, batch, c.num_kv_heads)))
+        return SHKV_ERR_INVALID_ARG;
+    if ((pages + batch) * c.num_kv_heads > INT32_MAX)
+        return SHKV_ERR_UNSUPPORTED;
+    p.k_pages = static_cast<uint4 *>(c.k_pages);
+    p.v_pages = static_cast<uint4 *>(c.v_pages);
+    p.index = index;
+    p.index_stride = index_stride;
+    p.new_table = new_table;
+    p.new_stride = new_table_stride;
+    p.table = table ? table : c.block_table;
+    p.table_stride = table_stride;
+    if (out) {
+        p.mass.in = mass->data;
+        p.mass.in_request = mass->request_stride;
+        p.mass.in_head = mass->head_stride;
+        p.mass.out = out->data;
+        p.mass.out_request = out->request_stride;
+        p.mass.out_head = out->head_stride;
+    }
+    p.block_table = c.block_table;
+    p.seq_lens = c.seq_lens;
+    p.err = c.error_word;
+    p.batch = batch;
+    p.hkv = c.num_kv_heads;
+    p.head_dim = c.head_dim;
+    p.page_size = c.page_size;
+    p.max_pages = c.max_pages_per_seq;
+    p.num_pages = c.num_pages;
+    p.check_lens = !lens;
+    if (launch_evict(p, (cudaStream_t)stream) != cudaSuccess)
+        return SHKV_ERR_CUDA;
+    for (int b = 0; b < batch; ++b)
+        if (p.keep[b] < p.lens[b])
+            pool->lens[b] = p.keep[b];
+    // the pool's table has changed: a decode with tails right behind this call
+    // has to wait for it, as it does where no byte is free
+    record_stream_use(stream, {Span{0, UINTPTR_MAX}});
+    return SHKV_OK;
+} catch (const std::exception &) {
+    return SHKV_ERR_CUDA;                // no host memory
+}
+
+}  // extern "C"

@@ -1,13 +1,27 @@
-// host_shared.h -- host-side pieces of shkv_host.cu that the 8-bit cache's
-// entry points use as well (internal to the library).
+// host_shared.h -- host-side pieces of shkv_host.cu that the entry points of the
+// 8-bit cache and of eviction use as well (internal to the library).
 #pragma once
 
 #include <cuda.h>
 #include <stdint.h>
 
 #include <initializer_list>
+#include <vector>
 
 #include "shkv.h"
+
+struct shkv_pool {
+    shkv_pool_config cfg;
+    int device;
+    int num_sms;
+    CUtensorMap tm_k;      // 3-D maps: whole row-blocks (mma.sync consumer)
+    CUtensorMap tm_v;
+    CUtensorMap tm_k2;     // 2-D maps: one 64-column half of a page (tcgen05 consumer)
+    CUtensorMap tm_v2;
+    std::vector<int32_t> lens;   // host copy of seq_lens
+    bool tails_view = false;     // a per-decoder tail table over another pool's pages: empty lengths allowed
+    int32_t consumer = SHKV_CONSUMER_AUTO;   // decode consumer the caller asked for
+};
 
 namespace shkv {
 

@@ -63,19 +63,6 @@ Span span_of(const void *p, size_t bytes)
 
 using namespace shkv;
 
-struct shkv_pool {
-    shkv_pool_config cfg;
-    int device;
-    int num_sms;
-    CUtensorMap tm_k;      // 3-D maps: whole row-blocks (mma.sync consumer)
-    CUtensorMap tm_v;
-    CUtensorMap tm_k2;     // 2-D maps: one 64-column half of a page (tcgen05 consumer)
-    CUtensorMap tm_v2;
-    std::vector<int32_t> lens;   // host copy of seq_lens
-    bool tails_view = false;     // a per-decoder tail table over another pool's pages: empty lengths allowed
-    int32_t consumer = SHKV_CONSUMER_AUTO;   // decode consumer the caller asked for
-};
-
 // Per-decoder unique tails: a view pool over the parent's pages whose
 // "requests" are the (request, decoder) pairs, b * n_models + m.
 struct shkv_tails {

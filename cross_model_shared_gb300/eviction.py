@@ -1,0 +1,216 @@
+"""Eviction from the shared KV cache by accumulated attention weight.
+
+``SharedKVPool`` has these calls.  ``decode_mass`` and ``prefill_mass`` add the
+softmax weights that a decode step's or a chunk's rows gave every cached token
+to the token's mass, ``select_tokens`` names every KV head's tokens of most
+mass, and ``evict_tokens`` moves them into new pages.
+"""
+from __future__ import annotations
+
+import contextlib
+from typing import Dict, Optional
+
+import numpy as np
+import torch
+
+from . import _native as N
+from .q8 import _HostInts
+
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_HERE = contextlib.nullcontext()
+
+
+class EvictionCalls:
+    """Masses are fp32 [B, num_kv_heads, T], T at least the longest request's
+    length, the last dimension contiguous and the others of any stride.  A
+    request's new tokens start from the masses that the tensor holds at their
+    positions: zeros, as a rule.
+
+    Every call runs on ``stream`` (the pool device's current stream if None),
+    which must be ordered after the work that made its inputs.  A call on a
+    named stream, or where a side stream is current, holds its tensors back:
+    they may be dropped once it has returned.  A captured call's tensors, and
+    the pool, have to live as long as the graph, which replays with the lengths
+    of the capture.  Calls take no workspace.
+    """
+
+    # -- arguments ------------------------------------------------------------
+    def _enter(self, stream: Optional[torch.cuda.Stream]):
+        """(context that makes the stream and the pool's device current, raw stream)."""
+        device = self.k_pages.device
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+            if torch.cuda.current_device() == device.index:
+                return _HERE, int(stream.cuda_stream)
+        elif stream.device != device:
+            raise ValueError(f"stream must be one of {device}")
+        return torch.cuda.stream(stream), int(stream.cuda_stream)
+
+    def _hold(self, raw: int, named: Optional[torch.cuda.Stream], *tensors: Optional[torch.Tensor]) -> None:
+        """Keeps the memory of the pool, and of the tensors of a call whose
+        stream is named or a side stream, from being handed out again before
+        the current stream, ``raw``, is through with it: before the kernels are
+        enqueued."""
+        held: Dict[int, torch.cuda.Stream] = self.__dict__.setdefault("_held_for", {})
+        stream = held.get(raw)
+        mine = raw == 0 and named is None
+        if mine and stream is not None or torch.cuda.is_current_stream_capturing():
+            return
+        if stream is None:
+            # the pool's own memory, once: from here on until it is freed
+            stream = torch.cuda.current_stream(self.k_pages.device)
+            for t in (self.k_pages, self.v_pages, self.block_table, self.seq_lens, self.error_word):
+                t.record_stream(stream)
+            held[raw] = stream
+        for t in () if mine else tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+    def _mass_of(self, t: torch.Tensor, batch: int, name: str) -> N.shkv_mass:
+        if t.dtype is not _F32 or t.device != self.k_pages.device or t.dim() != 3:
+            raise ValueError(f"{name} must be float32 [B, num_kv_heads, T] on {self.k_pages.device}")
+        if t.shape[0] < batch or t.shape[1] != self.num_kv_heads or (t.shape[2] > 1 and t.stride(2) != 1):
+            raise ValueError(f"{name} must be [B, {self.num_kv_heads}, T] of at least {batch} requests, "
+                             "its last dimension contiguous")
+        return N.shkv_mass(t.data_ptr(), t.stride(0), t.stride(1))
+
+    def _masses(self, mass: Optional[torch.Tensor], out: Optional[torch.Tensor], batch: int, longest: int):
+        """Views of the masses read (or None) and written, and the tensor written."""
+        if out is None:
+            out = mass if mass is not None else torch.zeros((batch, self.num_kv_heads, longest), dtype=_F32,
+                                                            device=self.k_pages.device)
+        views = []
+        for t, name in ((mass, "mass"), (out, "out")):
+            if t is not None and t.dim() == 3 and t.shape[2] < longest:
+                raise ValueError(f"{name} must hold the longest request's {longest} tokens")
+            views.append(self._mass_of(t, batch, name) if t is not None else None)
+        return views[0], views[1], out
+
+    def _longest(self, batch: int) -> int:
+        if batch > self.max_batch:
+            raise ValueError(f"at most {self.max_batch} requests")
+        return int(self.host_seq_lens(batch).max(initial=0))
+
+    # -- the path -------------------------------------------------------------
+    def decode_mass(self, q: torch.Tensor, lse: torch.Tensor, n_models: int, mass: Optional[torch.Tensor],
+                    decay: float = 1.0, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+        """``out[b, g, t] = decay * mass[b, g, t] +`` the sum of the softmax
+        weights that the stacked rows of KV head g gave cached token t.
+
+        q: bf16 [B, n_models * hq, head_dim] and lse: fp32 [B, n_models * hq],
+        of the same ``decode_attention`` (also ``DecoderTails``').  ``out`` is
+        ``mass`` itself if None; with ``mass`` None it holds the sums alone.
+        Positions behind a request's last token are left as they are."""
+        if q.dtype is not _BF16 or q.device != self.k_pages.device or q.dim() != 3 or not q.is_contiguous():
+            raise ValueError(f"q must be a contiguous bfloat16 tensor [B, n_models * hq, head_dim] on {self.k_pages.device}")
+        B, rows, D = q.shape
+        if n_models < 1 or rows % n_models or D != self.head_dim:
+            raise ValueError("q must be [B, n_models * hq, head_dim]")
+        if lse.dtype is not _F32 or lse.device != q.device or tuple(lse.shape) != (B, rows) or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous float32 tensor {[B, rows]} on {q.device}")
+        ctx, s = self._enter(stream)
+        with ctx:
+            m, o, result = self._masses(mass, out, B, self._longest(B))
+            self._hold(s, stream, q, lse, mass, out)
+            N.shkv_decode_mass(self.handle, B, n_models, rows // n_models, q.data_ptr(),
+                               D ** -0.5 if scale is None else float(scale), lse.data_ptr(), float(decay), m, o, s)
+        return result
+
+    def prefill_mass(self, q: torch.Tensor, lse: torch.Tensor, mass: Optional[torch.Tensor], decay: float = 1.0,
+                     scale: Optional[float] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """The same for the last n_new tokens of every request, of which new
+        token i weighs the tokens up to itself: q bf16 [B, n_new, hq, head_dim]
+        and lse fp32 [B, n_new, hq] of the same ``prefill_attention``.  Slices
+        of both (``q[:, -64:]``) make the chunk's last tokens a window of
+        voters: only a token's own rows have to be contiguous."""
+        if q.dtype is not _BF16 or q.device != self.k_pages.device or q.dim() != 4 or q.shape[3] != self.head_dim:
+            raise ValueError(f"q must be bfloat16 [B, n_new, hq, head_dim] on {self.k_pages.device}")
+        B, T, H, D = q.shape
+        if (D > 1 and q.stride(3) != 1) or (H > 1 and q.stride(2) != D):
+            raise ValueError("q: a token's rows must be contiguous")
+        if lse.dtype is not _F32 or lse.device != q.device or tuple(lse.shape) != (B, T, H):
+            raise ValueError(f"lse must be float32 {[B, T, H]} on {q.device}")
+        if H > 1 and lse.stride(2) != 1:
+            raise ValueError("lse: a token's values must be contiguous")
+        ctx, s = self._enter(stream)
+        with ctx:
+            m, o, result = self._masses(mass, out, B, self._longest(B))
+            self._hold(s, stream, q, lse, mass, out)
+            N.shkv_prefill_mass(self.handle, B, T, H, q.data_ptr(), q.stride(0), q.stride(1),
+                                D ** -0.5 if scale is None else float(scale), lse.data_ptr(), lse.stride(0),
+                                lse.stride(1), float(decay), m, o, s)
+        return result
+
+    def select_tokens(self, mass: torch.Tensor, keep, sink: int = 0, recent: int = 0,
+                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Positions of the ``keep[b]`` tokens that stay, for every request and
+        KV head: the first ``sink``, the last ``recent``, and of the others
+        those of largest mass (of equals the lower position; a NaN above all).
+        int32 [B, num_kv_heads, most kept], ascending, -1 behind a request's
+        kept tokens; a request of at most ``keep[b]`` tokens keeps them all."""
+        k = _HostInts(keep, "keep")
+        longest = self._longest(k.n)
+        lens = self.host_seq_lens(k.n)
+        most = int(np.minimum(lens, np.asarray(k._keep, dtype=np.int64)).max(initial=0))
+        ctx, s = self._enter(stream)
+        with ctx:
+            if mass.dim() == 3 and mass.shape[2] < longest:
+                raise ValueError(f"mass must hold the longest request's {longest} tokens")
+            m = self._mass_of(mass, k.n, "mass")
+            shape = (k.n, self.num_kv_heads, max(most, 1))
+            if out is None:
+                index = torch.empty(shape, dtype=_I32, device=self.k_pages.device)
+            else:
+                index = out
+                if out.dtype is not _I32 or out.device != self.k_pages.device or out.dim() != 3 or \
+                        not out.is_contiguous() or out.shape[:2] != shape[:2] or out.shape[2] < most:
+                    raise ValueError(f"out must be a contiguous int32 tensor [{shape[0]}, {shape[1]}, at least {most}]")
+            if k.n:
+                self._hold(s, stream, mass, out)
+                N.shkv_select_tokens(self.handle, k.n, m, k.ptr, int(sink), int(recent), index.data_ptr(),
+                                     index.shape[2], s)
+        return index
+
+    def evict_tokens(self, index: torch.Tensor, keep, new_table: torch.Tensor, mass: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None, source=None, stream=None) -> None:
+        """Moves the kept tokens of every request longer than ``keep[b]`` to
+        the pages ``new_table[b]`` names, KV head by KV head; its row of
+        ``block_table`` and its length follow, its old pages are free once the
+        call has run.  Other requests are left alone.
+
+        index: int32 [B, num_kv_heads, K], as ``select_tokens`` returns it
+        new_table: int32 [B, W], W * page_size >= keep[b], of pages that no
+        request of the call reads; its row becomes the request's, with the pages
+        it names for tokens to come
+        mass: masses that move along: to the front of the request's row, zeros
+        behind them up to the old length, into ``out`` (``mass`` itself if None)
+        source: (table, lens) that say where the tokens are, instead of the
+        pool's own: int32 [B, W'] on the device, and a host list."""
+        k = _HostInts(keep, "keep")
+        device = self.k_pages.device
+        if index.dtype is not _I32 or index.device != device or index.dim() != 3 or not index.is_contiguous() or \
+                index.shape[0] < k.n or index.shape[1] != self.num_kv_heads:
+            raise ValueError(f"index must be a contiguous int32 tensor [{k.n}, {self.num_kv_heads}, K] on {device}")
+        if out is not None and mass is None:
+            raise ValueError("out without mass")
+        tables = [(new_table, "new_table")]
+        table = lens = None
+        if source is not None:
+            table, lens = source[0], _HostInts(source[1], "source lengths")
+            if lens.n != k.n:
+                raise ValueError("source lengths and keep must have the same length")
+            tables.append((table, "source table"))
+        for t, name in tables:
+            if t.dtype is not _I32 or t.device != device or t.dim() != 2 or not t.is_contiguous() or t.shape[0] < k.n:
+                raise ValueError(f"{name} must be a contiguous int32 tensor [{k.n}, pages] on {device}")
+        longest = max(lens._keep, default=0) if lens is not None else self._longest(k.n)
+        ctx, s = self._enter(stream)
+        with ctx:
+            m, o, _ = self._masses(mass, out, k.n, longest) if mass is not None else (None, None, None)
+            if k.n:
+                self._hold(s, stream, index, new_table, table, mass, out)
+                N.shkv_evict_tokens(self.handle, k.n, k.ptr, index.data_ptr(), index.shape[2], new_table.data_ptr(),
+                                    new_table.shape[1], table.data_ptr() if table is not None else None,
+                                    table.shape[1] if table is not None else 0, lens.ptr if lens is not None else None,
+                                    m, o, s)

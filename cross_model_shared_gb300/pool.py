@@ -15,6 +15,7 @@ import numpy as np
 import torch
 
 from . import _native as N
+from .eviction import EvictionCalls
 
 
 def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> int:
@@ -31,13 +32,16 @@ def _require(t: torch.Tensor, dtype, name: str):
         raise ValueError(f"{name} must be contiguous")
 
 
-class SharedKVPool:
+class SharedKVPool(EvictionCalls):
     """One paged KV cache shared by N decoders.
 
     k_pages / v_pages: bf16 [num_pages, num_kv_heads, page_size, head_dim]
     block_table: int32 [max_batch, max_pages_per_seq] (fill it, then call
     ``sync_block_table`` is not needed: the kernels read it in place)
     seq_lens: int32 [max_batch], owned by the pool after creation.
+
+    ``decode_mass``, ``prefill_mass``, ``select_tokens`` and ``evict_tokens``
+    (``EvictionCalls``) shrink requests to the tokens that attention weighs most.
     """
 
     def __init__(self, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int,

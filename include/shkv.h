@@ -52,6 +52,7 @@ typedef enum {
 #define SHKV_ERRF_SEQ_LEN 0x2u    /* device seq_lens disagrees with the pool's host copy */
 #define SHKV_ERRF_TIMEOUT 0x4u    /* a pipeline wait exceeded its time limit */
 #define SHKV_ERRF_PIPELINE 0x8u   /* a pipeline slot held a stage other than the one expected */
+#define SHKV_ERRF_INDEX 0x10u     /* a kept position outside its request (shkv_evict_tokens) */
 
 /* Largest batch a single decode / append call accepts. */
 #define SHKV_MAX_BATCH 1024
@@ -643,6 +644,125 @@ shkv_status shkv_q8_decode_attention(shkv_q8_pool *pool, int32_t batch, int32_t 
 shkv_status shkv_q8_chunk_attention(shkv_q8_pool *pool, int32_t batch, const int32_t *new_lens, int32_t hq,
                                     const void *q, int64_t q_stride, float scale, void *out, float *lse_out,
                                     void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Eviction by accumulated attention weight.  A cache that only grows runs out
+ * of pages; these calls shrink a request to the tokens that its readers attend
+ * to.  Every cached token has, per KV head, a mass: the softmax weights that
+ * rows gave it, added up over decode steps (shkv_decode_mass) and chunks of a
+ * prompt (shkv_prefill_mass).  shkv_select_tokens names each head's tokens of
+ * most mass, shkv_evict_tokens moves them into new pages.  KV heads keep
+ * different tokens, a request's heads equally many, so that pages, lengths and
+ * every attention call stay what they are.
+ *
+ * The conventions at the top of this file hold; besides, the current device of
+ * each call must be the pool's (SHKV_ERR_INVALID_ARG), arrays named lens and
+ * keep are host arrays [batch], read before the call returns, and requests may
+ * be of any length from zero on.  A call captured into a CUDA graph replays
+ * with the lengths of its capture; SHKV_ERRF_SEQ_LEN is set where the device
+ * copy of a length then differs.  The calls take no workspace.
+ *
+ * Masses: fp32, mass of token t of request b and KV head g at
+ * data[b * request_stride + g * head_stride + t] (strides in elements, any
+ * alignment of 4 bytes).
+ */
+typedef struct {
+    float *data;
+    int64_t request_stride, head_stride;
+} shkv_mass;
+
+/*
+ * After a decode step: for every request b, KV head g and token t < L_b
+ *   out[b, g, t] = decay * mass[b, g, t]
+ *                  + sum over the N * G stacked rows r of g of
+ *                    exp(scale <q[b, r], K_b[t, g]> - lse[b, r])
+ * where lse is what the attention call over the same q returned: the rows'
+ * softmax weights, also of a call with per-decoder tails, whose lse covers the
+ * tails as well.  A row with an lse of -inf attends nothing and adds nothing.
+ *   q      device bf16 [batch, n_models * hq_per_model, head_dim]
+ *   lse    device fp32 [batch, n_models * hq_per_model]
+ *   decay  finite; 1 adds up, less forgets.  With decay = 0, or mass NULL, old
+ *          masses are not read
+ *   mass, out   may be the same masses (updated in place), else disjoint
+ * Masses of positions t >= L_b are neither read nor written.  A token on a page
+ * outside the pool sets SHKV_ERRF_PAGE_OOB and its rows' sum is 0.
+ * Arithmetic: scores of exact products accumulated in fp32, weights and their
+ * sums in fp32; no step rounds to fewer bits, and none depends on an order
+ * between threads.
+ * Supported: n_models * hq_per_model / num_kv_heads <= 64 as in
+ * shkv_decode_attention, head_dim 64 or 128.  Errors: SHKV_ERR_INVALID_ARG,
+ * SHKV_ERR_UNSUPPORTED, SHKV_ERR_CUDA.
+ */
+shkv_status shkv_decode_mass(shkv_pool *pool, int32_t batch, int32_t n_models, int32_t hq_per_model, const void *q,
+                             float scale, const float *lse, float decay, const shkv_mass *mass, const shkv_mass *out,
+                             void *stream);
+
+/*
+ * The same for the n_new last tokens of every request, which are in the pool
+ * (shkv_prefill_attention gives their lse): row (i, h) is new token i, at
+ * position L_b - n_new + i, and weighs the tokens up to its own.  The new tokens
+ * of a larger chunk's end serve as a window of voters: q and lse may be slices.
+ *   q    device bf16, token i's rows [hq_per_model, head_dim] at element
+ *        b * q_request_stride + i * q_token_stride: multiples of 8, token
+ *        stride at least hq_per_model * head_dim, request stride above 0
+ *   lse  device fp32, token i's [hq_per_model] at element
+ *        b * lse_request_stride + i * lse_token_stride, not negative
+ * Supported: hq_per_model / num_kv_heads <= 128, head_dim 64 or 128.  Errors:
+ * as shkv_decode_mass; SHKV_ERR_INVALID_ARG where a request is shorter than
+ * n_new.
+ */
+shkv_status shkv_prefill_mass(shkv_pool *pool, int32_t batch, int32_t n_new, int32_t hq_per_model, const void *q,
+                              int64_t q_request_stride, int64_t q_token_stride, float scale, const float *lse,
+                              int64_t lse_request_stride, int64_t lse_token_stride, float decay,
+                              const shkv_mass *mass, const shkv_mass *out, void *stream);
+
+/*
+ * The tokens to keep: for every request b and KV head g the positions of the
+ * first `sink` tokens, of the last `recent` ones, and of the others those of
+ * largest mass, keep[b] in all, ascending.  Of equal masses the lower position
+ * is kept; -0 equals 0 and a NaN counts as larger than every number.  A request
+ * of at most keep[b] tokens keeps them all.
+ *   index  device int32 [batch, num_kv_heads, index_stride]; entries behind
+ *          the kept ones become -1
+ * Errors: SHKV_ERR_INVALID_ARG (also keep[b] below sink + recent where the
+ * request is longer than keep[b], index_stride below a request's kept tokens,
+ * negative counts), SHKV_ERR_CUDA.
+ */
+shkv_status shkv_select_tokens(shkv_pool *pool, int32_t batch, const shkv_mass *mass, const int32_t *keep,
+                               int32_t sink, int32_t recent, int32_t *index, int64_t index_stride, void *stream);
+
+/*
+ * Move the kept tokens of every request longer than keep[b] into new pages:
+ * for each KV head g and j < keep[b], with i = index[b, g, j],
+ *   pool[new_table[b][j/P], g, j%P, :] = pool[table[b][i/P], g, i%P, :]
+ * for K and V, a bit-exact copy; then the pool's block table holds new_table[b]
+ * (with the pages that it names behind the ceil(keep[b] / P) used ones, for
+ * tokens to come, and -1 behind its width) and L_b = keep[b].  The other
+ * requests are left alone.  The old pages are the caller's again once the
+ * call has run on `stream`: pages that requests share stay intact, as nothing is
+ * written to them.  The index need not come from shkv_select_tokens, but to
+ * move masses in place it must ascend.
+ *   index      device int32 [batch, num_kv_heads, index_stride]
+ *   new_table  device int32 [batch, new_table_stride]: pages that no request of
+ *              the call reads, each named once; not the pool's block table
+ *   table, table_stride, lens
+ *              where the tokens are: NULL, 0, NULL for the pool's own table and
+ *              lengths, else device int32 [batch, table_stride] and host [batch]
+ *              (a shared prompt, a table put aside); keep[b] is compared with
+ *              these lengths
+ *   mass, out  NULL, or masses that move along: out[b, g, j] = mass[b, g, i] for
+ *              j < keep[b], and 0 up to the old length.  The same masses (moved
+ *              in place) or disjoint
+ * Errors: SHKV_ERR_INVALID_ARG (also index_stride or new_table_stride too
+ * small, a length past table_stride pages), SHKV_ERR_CAPACITY (keep[b] of a
+ * moved request past max_pages_per_seq pages), SHKV_ERR_CUDA.  An index outside
+ * [0, the old length) sets SHKV_ERRF_INDEX, a page outside the pool
+ * SHKV_ERRF_PAGE_OOB; that token is not copied (its mass becomes 0).
+ */
+shkv_status shkv_evict_tokens(shkv_pool *pool, int32_t batch, const int32_t *keep, const int32_t *index,
+                              int64_t index_stride, const int32_t *new_table, int64_t new_table_stride,
+                              const int32_t *table, int64_t table_stride, const int32_t *lens, const shkv_mass *mass,
+                              const shkv_mass *out, void *stream);
 
 /* Static description of a status code. */
 const char *shkv_status_string(shkv_status status);
