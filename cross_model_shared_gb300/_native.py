@@ -41,7 +41,7 @@ EXPORTS = [
     "shkv_partition_requests", "shkv_selftest_bounded_wait", "shkv_q8_pool_create", "shkv_q8_pool_destroy",
     "shkv_q8_pool_set_seq_lens", "shkv_q8_pool_get_seq_lens", "shkv_q8_check_errors", "shkv_q8_append_kv",
     "shkv_q8_read_kv", "shkv_q8_workspace_size", "shkv_q8_decode_attention", "shkv_q8_chunk_attention",
-    "shkv_decode_mass", "shkv_prefill_mass", "shkv_select_tokens", "shkv_evict_tokens",
+    "shkv_decode_mass", "shkv_prefill_mass", "shkv_prefill_mass_workspace_size", "shkv_select_tokens", "shkv_evict_tokens",
 ]
 
 SHKV_CONSUMER_AUTO = -1
@@ -184,7 +184,8 @@ def load() -> ctypes.CDLL:
                                     ctypes.c_size_t, vp],
         "shkv_decode_mass": [vp, i32, i32, i32, vp, ctypes.c_float, vp, ctypes.c_float, mass, mass, vp],
         "shkv_prefill_mass": [vp, i32, i32, i32, vp, i64, i64, ctypes.c_float, vp, i64, i64, ctypes.c_float, mass,
-                              mass, vp],
+                              mass, vp, ctypes.c_size_t, vp],
+        "shkv_prefill_mass_workspace_size": [vp, ctypes.POINTER(ctypes.c_size_t)],
         "shkv_select_tokens": [vp, i32, mass, i32p, i32, i32, vp, i64, vp],
         "shkv_evict_tokens": [vp, i32, i32p, vp, i64, vp, i64, vp, i64, i32p, mass, mass, vp],
     }
@@ -430,10 +431,16 @@ def shkv_decode_mass(pool: int, batch: int, n_models: int, hq: int, q: int, scal
 
 def shkv_prefill_mass(pool: int, batch: int, n_new: int, hq: int, q: int, q_request_stride: int, q_token_stride: int,
                       scale: float, lse: int, lse_request_stride: int, lse_token_stride: int, decay: float, mass,
-                      out: shkv_mass, stream: int) -> None:
+                      out: shkv_mass, workspace: int, workspace_bytes: int, stream: int) -> None:
     _check(load().shkv_prefill_mass(pool, batch, n_new, hq, q, q_request_stride, q_token_stride, scale, lse,
-                                    lse_request_stride, lse_token_stride, decay, _ref(mass), _ref(out), stream),
-           "shkv_prefill_mass")
+                                    lse_request_stride, lse_token_stride, decay, _ref(mass), _ref(out), workspace,
+                                    workspace_bytes, stream), "shkv_prefill_mass")
+
+
+def shkv_prefill_mass_workspace_size(pool: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().shkv_prefill_mass_workspace_size(pool, ctypes.byref(n)), "shkv_prefill_mass_workspace_size")
+    return n.value
 
 
 def shkv_select_tokens(pool: int, batch: int, mass: shkv_mass, keep: int, sink: int, recent: int, index: int,

@@ -16,22 +16,39 @@ struct MassIo {
     int64_t in_request, in_head, out_request, out_head;
 };
 
+constexpr int kMassMaxCtas = 256;
+constexpr int kMassTile = 128;       // tokens of a tile: rows of an MMA
+constexpr int kMassItem = 2 * kMassTile;
+constexpr int kMassRows = 128;       // query rows of a block, at most
+
 // A decode step or a chunk: row r = i * G + j of a (request, KV head g) is
 // query token i, head g * G + j.  Causal: query token i sits at position
-// L_b - n_q + i.
+// L_b - n_q + i.  Blocks of `tpt` query tokens, `blocks` in all; an item is two
+// consecutive 128-token tiles of a (request, KV head), items are numbered
+// request-major, then by head.  CTA c takes the blocks from (cut_item[c],
+// cut_block[c]) up to (cut_item[c + 1], cut_block[c + 1]); block 0 stands for
+// the item's first.
 struct MassParams {
-    const __nv_bfloat16 *k_pages;    // [num_pages, Hkv, P, D]
-    const __nv_bfloat16 *q;          // query token i's rows [Hq, D] at b * q_request + i * q_token
-    const float *lse;                // ... and its [Hq]
-    int64_t q_request, q_token, lse_request, lse_token;
+    const float *lse;                // query token i's [Hq] at b * lse_request + i * lse_token
+    int64_t lse_request, lse_token;
     MassIo mass;
     const int32_t *block_table, *seq_lens;
     uint32_t *err;
-    int32_t batch, n_q, hq, hkv, group, head_dim, page_size, max_pages, num_pages, causal;
+    float *pieces;                   // [2 * CTAs, kMassItem]: sums of a range's first and last, cut item
+    int32_t batch, n_q, hkv, group, head_dim, page_size, max_pages, num_pages, causal;
+    int32_t tpt, blocks, num_ctas;
     float scale_log2, decay;
+    int32_t cut_item[kMassMaxCtas + 1];
+    int32_t cut_block[kMassMaxCtas + 1];
     int32_t lens[SHKV_MAX_BATCH];
-    int32_t tile0[SHKV_MAX_BATCH + 1];   // 128-token tiles of one KV head before each request
+    int32_t item0[SHKV_MAX_BATCH + 1];   // items before each request
 };
+
+// Tokens that every query token of a request sees.
+__host__ __device__ inline int mass_past(int len, int n_q, int causal) { return causal ? len - n_q : len; }
+
+// First block with a row that sees token t.
+__host__ __device__ inline int mass_block0(int t, int past, int tpt) { return t > past ? (t - past) / tpt : 0; }
 
 struct SelectParams {
     const float *mass;

@@ -15,7 +15,8 @@
 #include "shkv.h"
 
 namespace shkv {
-cudaError_t launch_mass(const MassParams &p, cudaStream_t stream);
+cudaError_t launch_mass(const CUtensorMap &tm_k, const CUtensorMap &tm_q, const MassParams &p, bool pieces,
+                        cudaStream_t stream);
 cudaError_t launch_select(const SelectParams &p, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream);
 }  // namespace shkv
@@ -74,42 +75,137 @@ Span mass_span(const float *data, int64_t request_stride, int64_t head_stride, i
     return span_of(data, (size_t)((batch - 1) * request_stride + (hkv - 1) * head_stride + len) * 4);
 }
 
+// Rows of a call: dim0 = head_dim, dim1 = heads, dim2 = query tokens of a
+// request, dim3 = requests.  A box {64, G, tpt, 1} is a column half of a block's
+// rows of one KV head, 128-byte swizzled; query tokens behind a request's last
+// are zeros.
+bool make_q_map(CUtensorMap *tm, const void *q, const shkv_pool_config &c, int32_t batch, int32_t n_q, int32_t hq,
+                int64_t q_request, int64_t q_token, int32_t tpt)
+{
+    EncodeTiledFn enc = encode_tiled_fn();
+    if (!enc)
+        return false;
+    cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)hq, (cuuint64_t)n_q, (cuuint64_t)batch};
+    cuuint64_t strides[3] = {(cuuint64_t)c.head_dim * 2, (cuuint64_t)q_token * 2, (cuuint64_t)q_request * 2};
+    cuuint32_t box[4] = {64u, (cuuint32_t)(hq / c.num_kv_heads), (cuuint32_t)tpt, 1u};
+    cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(q), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Bytes of the cut items' sums.
+size_t piece_bytes(const shkv_pool *pool)
+{
+    return (size_t)2 * std::min(pool->num_sms, kMassMaxCtas) * kMassItem * sizeof(float);
+}
+
+// Cuts the items into at most `limit` ranges of about equal cost, counted in
+// products of a tile and a block of rows, and one more an item.  An item of many
+// blocks may be cut between two of them; pieces of under kMinPiece blocks are not
+// cut off.  True if an item is cut.
+constexpr int64_t kItemCost = 1, kMinPiece = 2;
+
+bool plan_mass(MassParams &p, int limit)
+{
+    // cost of tile pair `pair` of a request, and of all of its pairs of one head
+    auto cost = [&](int L, int pair) -> int64_t {
+        const int past = mass_past(L, p.n_q, p.causal), t = pair * kMassItem;
+        int64_t k = kItemCost + p.blocks - mass_block0(t, past, p.tpt);
+        if (t + kMassTile < L)
+            k += p.blocks - mass_block0(t + kMassTile, past, p.tpt);
+        return k;
+    };
+    // the first `even` pairs take part in every block
+    auto even = [&](int L) -> int64_t { return std::max(0, std::min(L / kMassItem, mass_past(L, p.n_q, p.causal) / kMassItem)); };
+    const int64_t full = kItemCost + 2 * (int64_t)p.blocks;
+    auto head = [&](int L) -> int64_t {
+        int64_t k = even(L) * full;
+        for (int pair = (int)even(L); pair * kMassItem < L; ++pair)
+            k += cost(L, pair);
+        return k;
+    };
+    int64_t total = 0;
+    for (int b = 0; b < p.batch; ++b)
+        total += p.hkv * head(p.lens[b]);
+    const int64_t C = std::max<int64_t>(1, std::min<int64_t>(limit, p.blocks > 1 ? total / (4 * kMinPiece) : p.item0[p.batch]));
+    int n = 0, b = 0;
+    int64_t before = 0, h = head(p.lens[0]);
+    bool cut = false;
+    p.cut_item[0] = p.cut_block[0] = 0;
+    for (int64_t c = 1; c < C; ++c) {
+        const int64_t target = total * c / C;
+        while (h == 0 || target >= before + p.hkv * h) {
+            before += p.hkv * h;
+            h = head(p.lens[++b]);
+        }
+        const int L = p.lens[b], g = (int)((target - before) / h);
+        int64_t rest = (target - before) % h;
+        int pair = (int)std::min(rest / full, even(L));
+        rest -= pair * full;
+        int64_t k = cost(L, pair);
+        while (rest >= k) {
+            rest -= k;
+            k = cost(L, ++pair);
+        }
+        int item = p.item0[b] + g * ((L + kMassItem - 1) / kMassItem) + pair;
+        const int block0 = mass_block0(pair * kMassItem, mass_past(L, p.n_q, p.causal), p.tpt);
+        const int64_t steps = p.blocks - block0, at = steps * rest / k;
+        int block = 0;
+        if (steps >= 2 * kMinPiece && at >= kMinPiece && steps - at >= kMinPiece)
+            block = block0 + (int)at;
+        else if (2 * at >= steps)
+            ++item;
+        if (item > p.cut_item[n] || (item == p.cut_item[n] && block > p.cut_block[n])) {
+            if (item >= p.item0[p.batch])
+                break;
+            ++n;
+            p.cut_item[n] = item;
+            p.cut_block[n] = block;
+            cut = cut || block > 0;
+        }
+    }
+    p.num_ctas = n + 1;
+    p.cut_item[n + 1] = p.item0[p.batch];
+    p.cut_block[n + 1] = 0;
+    return cut;
+}
+
 // Both forms: the n_q query tokens of every request.
 shkv_status add_mass(shkv_pool *pool, int32_t batch, int32_t n_q, int32_t hq, const void *q, int64_t q_request,
                      int64_t q_token, float scale, const float *lse, int64_t lse_request, int64_t lse_token,
-                     float decay, const shkv_mass *mass, const shkv_mass *out, bool causal, void *stream)
+                     float decay, const shkv_mass *mass, const shkv_mass *out, bool causal, void *workspace,
+                     size_t workspace_bytes, void *stream)
 {
     const shkv_pool_config &c = pool->cfg;
     const int64_t row = (int64_t)hq * c.head_dim;
-    if (batch == 1)                      // a stride that no step is taken along
-        q_request = n_q * q_token, lse_request = 0;
-    if (n_q == 1)
+    if (n_q == 1)                        // a stride that no step is taken along
         q_token = row, lse_token = 0;
+    if (batch == 1)
+        q_request = n_q * q_token, lse_request = 0;
     const float scale_log2 = (float)((double)scale * 1.4426950408889634);
     const int64_t len = longest(batch, pool->lens.data());
-    if (!q || !aligned(q, 16) || !lse || !aligned(lse, 4) || q_token < row || q_token % 8 || q_request <= 0 ||
-        q_request % 8 || lse_request < 0 || lse_token < 0 || !isfinite(scale_log2) || !isfinite(decay) ||
+    if (!q || !aligned(q, 16) || !lse || !aligned(lse, 4) || q_token < row || q_token % c.head_dim || q_request <= 0 ||
+        q_request % q_token || lse_request < 0 || lse_token < 0 || !isfinite(scale_log2) || !isfinite(decay) ||
         !writable(out, batch, c.num_kv_heads, len) ||
         (mass && (!readable(mass) || !same_layout(mass, out, batch, c.num_kv_heads))))
         return SHKV_ERR_INVALID_ARG;
+    if (q_request >= (int64_t)1 << 39)   // a tensor map's strides are below 2^40 bytes
+        return SHKV_ERR_UNSUPPORTED;
     MassParams p;
     memset(&p, 0, sizeof p);
-    int64_t tiles = 0;
+    int64_t items = 0;
     for (int b = 0; b < batch; ++b) {
         p.lens[b] = pool->lens[b];
-        p.tile0[b] = (int32_t)tiles;
-        tiles += (pool->lens[b] + 127) / 128;
-        if (tiles * c.num_kv_heads > INT32_MAX)
+        p.item0[b] = (int32_t)items;
+        items += ((int64_t)pool->lens[b] + kMassItem - 1) / kMassItem * c.num_kv_heads;
+        if (items > INT32_MAX)
             return SHKV_ERR_UNSUPPORTED;
     }
-    p.tile0[batch] = (int32_t)tiles;
-    if (tiles == 0)
+    p.item0[batch] = (int32_t)items;
+    if (items == 0)
         return SHKV_OK;
-    p.k_pages = static_cast<const __nv_bfloat16 *>(c.k_pages);
-    p.q = static_cast<const __nv_bfloat16 *>(q);
     p.lse = lse;
-    p.q_request = q_request;
-    p.q_token = q_token;
     p.lse_request = lse_request;
     p.lse_token = lse_token;
     if (mass && decay != 0.f) {
@@ -123,9 +219,9 @@ shkv_status add_mass(shkv_pool *pool, int32_t batch, int32_t n_q, int32_t hq, co
     p.block_table = c.block_table;
     p.seq_lens = c.seq_lens;
     p.err = c.error_word;
+    p.pieces = static_cast<float *>(workspace);
     p.batch = batch;
     p.n_q = n_q;
-    p.hq = hq;
     p.hkv = c.num_kv_heads;
     p.group = hq / c.num_kv_heads;
     p.head_dim = c.head_dim;
@@ -133,13 +229,20 @@ shkv_status add_mass(shkv_pool *pool, int32_t batch, int32_t n_q, int32_t hq, co
     p.max_pages = c.max_pages_per_seq;
     p.num_pages = c.num_pages;
     p.causal = causal;
+    p.tpt = std::min(kMassRows / p.group, n_q);
+    p.blocks = (n_q + p.tpt - 1) / p.tpt;
     p.scale_log2 = scale_log2;
     p.decay = decay;
-    if (launch_mass(p, (cudaStream_t)stream) != cudaSuccess)
+    CUtensorMap tm_q;
+    if (!make_q_map(&tm_q, q, c, batch, n_q, hq, q_request, q_token, p.tpt))
+        return SHKV_ERR_CUDA;
+    const bool pieces = plan_mass(p, std::min(pool->num_sms, kMassMaxCtas));
+    if (launch_mass(pool->tm_k2, tm_q, p, pieces, (cudaStream_t)stream) != cudaSuccess)
         return SHKV_ERR_CUDA;
     record_stream_use(stream,
                       {span_of(q, (size_t)((batch - 1) * q_request + (n_q - 1) * q_token + row) * 2),
                        span_of(lse, (size_t)((batch - 1) * lse_request + (n_q - 1) * lse_token + hq) * 4),
+                       span_of(workspace, workspace_bytes),
                        mass_span(p.mass.in, p.mass.in_request, p.mass.in_head, batch, c.num_kv_heads, len),
                        mass_span(p.mass.out, p.mass.out_request, p.mass.out_head, batch, c.num_kv_heads, len)});
     return SHKV_OK;
@@ -148,6 +251,14 @@ shkv_status add_mass(shkv_pool *pool, int32_t batch, int32_t n_q, int32_t hq, co
 }  // namespace
 
 extern "C" {
+
+shkv_status shkv_prefill_mass_workspace_size(const shkv_pool *pool, size_t *bytes)
+{
+    if (!pool || !bytes)
+        return SHKV_ERR_INVALID_ARG;
+    *bytes = piece_bytes(pool);
+    return SHKV_OK;
+}
 
 shkv_status shkv_decode_mass(shkv_pool *pool, int32_t batch, int32_t n_models, int32_t hq_per_model, const void *q,
                              float scale, const float *lse, float decay, const shkv_mass *mass, const shkv_mass *out,
@@ -160,7 +271,7 @@ try {
         return SHKV_ERR_UNSUPPORTED;
     const int64_t row = (int64_t)hq_per_model * pool->cfg.head_dim;
     return add_mass(pool, batch, n_models, hq_per_model, q, n_models * row, row, scale, lse,
-                    (int64_t)n_models * hq_per_model, hq_per_model, decay, mass, out, false, stream);
+                    (int64_t)n_models * hq_per_model, hq_per_model, decay, mass, out, false, nullptr, 0, stream);
 } catch (const std::exception &) {
     return SHKV_ERR_CUDA;                // no host memory
 }
@@ -168,9 +279,11 @@ try {
 shkv_status shkv_prefill_mass(shkv_pool *pool, int32_t batch, int32_t n_new, int32_t hq_per_model, const void *q,
                               int64_t q_request_stride, int64_t q_token_stride, float scale, const float *lse,
                               int64_t lse_request_stride, int64_t lse_token_stride, float decay,
-                              const shkv_mass *mass, const shkv_mass *out, void *stream)
+                              const shkv_mass *mass, const shkv_mass *out, void *workspace, size_t workspace_bytes,
+                              void *stream)
 try {
-    if (!callable(pool, batch) || batch < 1 || n_new < 1 || hq_per_model < 1)
+    if (!callable(pool, batch) || batch < 1 || n_new < 1 || hq_per_model < 1 || !workspace ||
+        !aligned(workspace, 16) || workspace_bytes < piece_bytes(pool))
         return SHKV_ERR_INVALID_ARG;
     const int32_t hkv = pool->cfg.num_kv_heads;
     if (hq_per_model % hkv || hq_per_model / hkv > 128)
@@ -179,7 +292,7 @@ try {
         if (pool->lens[b] < n_new)
             return SHKV_ERR_INVALID_ARG;     // the new tokens must already be in the pool
     return add_mass(pool, batch, n_new, hq_per_model, q, q_request_stride, q_token_stride, scale, lse,
-                    lse_request_stride, lse_token_stride, decay, mass, out, true, stream);
+                    lse_request_stride, lse_token_stride, decay, mass, out, true, workspace, workspace_bytes, stream);
 } catch (const std::exception &) {
     return SHKV_ERR_CUDA;                // no host memory
 }

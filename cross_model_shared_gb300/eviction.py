@@ -31,7 +31,7 @@ class EvictionCalls:
     named stream, or where a side stream is current, holds its tensors back:
     they may be dropped once it has returned.  A captured call's tensors, and
     the pool, have to live as long as the graph, which replays with the lengths
-    of the capture.  Calls take no workspace.
+    of the capture.
     """
 
     # -- arguments ------------------------------------------------------------
@@ -123,7 +123,8 @@ class EvictionCalls:
         token i weighs the tokens up to itself: q bf16 [B, n_new, hq, head_dim]
         and lse fp32 [B, n_new, hq] of the same ``prefill_attention``.  Slices
         of both (``q[:, -64:]``) make the chunk's last tokens a window of
-        voters: only a token's own rows have to be contiguous."""
+        voters: a token's own rows have to be contiguous, tokens a multiple of
+        head_dim elements apart and requests a multiple of the tokens' stride."""
         if q.dtype is not _BF16 or q.device != self.k_pages.device or q.dim() != 4 or q.shape[3] != self.head_dim:
             raise ValueError(f"q must be bfloat16 [B, n_new, hq, head_dim] on {self.k_pages.device}")
         B, T, H, D = q.shape
@@ -136,10 +137,12 @@ class EvictionCalls:
         ctx, s = self._enter(stream)
         with ctx:
             m, o, result = self._masses(mass, out, B, self._longest(B))
+            # scratch of this call alone: its memory goes back to the stream's (or a graph's) own
+            ws = torch.empty(N.shkv_prefill_mass_workspace_size(self.handle), dtype=torch.uint8, device=q.device)
             self._hold(s, stream, q, lse, mass, out)
             N.shkv_prefill_mass(self.handle, B, T, H, q.data_ptr(), q.stride(0), q.stride(1),
                                 D ** -0.5 if scale is None else float(scale), lse.data_ptr(), lse.stride(0),
-                                lse.stride(1), float(decay), m, o, s)
+                                lse.stride(1), float(decay), m, o, ws.data_ptr(), ws.numel(), s)
         return result
 
     def select_tokens(self, mass: torch.Tensor, keep, sink: int = 0, recent: int = 0,

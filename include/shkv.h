@@ -660,7 +660,7 @@ shkv_status shkv_q8_chunk_attention(shkv_q8_pool *pool, int32_t batch, const int
  * keep are host arrays [batch], read before the call returns, and requests may
  * be of any length from zero on.  A call captured into a CUDA graph replays
  * with the lengths of its capture; SHKV_ERRF_SEQ_LEN is set where the device
- * copy of a length then differs.  The calls take no workspace.
+ * copy of a length then differs.
  *
  * Masses: fp32, mass of token t of request b and KV head g at
  * data[b * request_stride + g * head_stride + t] (strides in elements, any
@@ -703,10 +703,15 @@ shkv_status shkv_decode_mass(shkv_pool *pool, int32_t batch, int32_t n_models, i
  * position L_b - n_new + i, and weighs the tokens up to its own.  The new tokens
  * of a larger chunk's end serve as a window of voters: q and lse may be slices.
  *   q    device bf16, token i's rows [hq_per_model, head_dim] at element
- *        b * q_request_stride + i * q_token_stride: multiples of 8, token
- *        stride at least hq_per_model * head_dim, request stride above 0
+ *        b * q_request_stride + i * q_token_stride: the token stride a multiple
+ *        of head_dim, at least hq_per_model * head_dim, the request stride a
+ *        multiple of the token stride, above 0
  *   lse  device fp32, token i's [hq_per_model] at element
  *        b * lse_request_stride + i * lse_token_stride, not negative
+ *   workspace, workspace_bytes
+ *        device scratch of at least shkv_prefill_mass_workspace_size() bytes
+ *        (the same for every shape), which may hold anything.  Calls sharing one
+ *        must not overlap on the GPU.
  * Supported: hq_per_model / num_kv_heads <= 128, head_dim 64 or 128.  Errors:
  * as shkv_decode_mass; SHKV_ERR_INVALID_ARG where a request is shorter than
  * n_new.
@@ -714,7 +719,9 @@ shkv_status shkv_decode_mass(shkv_pool *pool, int32_t batch, int32_t n_models, i
 shkv_status shkv_prefill_mass(shkv_pool *pool, int32_t batch, int32_t n_new, int32_t hq_per_model, const void *q,
                               int64_t q_request_stride, int64_t q_token_stride, float scale, const float *lse,
                               int64_t lse_request_stride, int64_t lse_token_stride, float decay,
-                              const shkv_mass *mass, const shkv_mass *out, void *stream);
+                              const shkv_mass *mass, const shkv_mass *out, void *workspace, size_t workspace_bytes,
+                              void *stream);
+shkv_status shkv_prefill_mass_workspace_size(const shkv_pool *pool, size_t *bytes);
 
 /*
  * The tokens to keep: for every request b and KV head g the positions of the
