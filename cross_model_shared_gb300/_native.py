@@ -92,6 +92,7 @@ class shkv_mass(ctypes.Structure):
         ("data", ctypes.c_void_p),
         ("request_stride", ctypes.c_int64),
         ("head_stride", ctypes.c_int64),
+        ("length", ctypes.c_int64),
     ]
 
 

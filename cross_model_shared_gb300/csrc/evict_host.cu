@@ -17,7 +17,7 @@
 namespace shkv {
 cudaError_t launch_mass(const CUtensorMap &tm_k, const CUtensorMap &tm_q, const MassParams &p, bool pieces,
                         cudaStream_t stream);
-cudaError_t launch_select(const SelectParams &p, cudaStream_t stream);
+cudaError_t launch_select(const SelectParams &p, int num_sms, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream);
 }  // namespace shkv
 
@@ -45,17 +45,19 @@ int64_t longest(int32_t batch, const int32_t *lens)
     return n;
 }
 
-// Masses that a call reads.
-bool readable(const shkv_mass *m)
+constexpr int32_t kMaxTokens = 1 << 30;   // of a request: the kernels step past its end in 32 bits
+
+// Masses of up to `len` tokens that a call reads.
+bool readable(const shkv_mass *m, int64_t len)
 {
-    return m && m->data && aligned(m->data, 4) && m->request_stride >= 0 && m->head_stride >= 0;
+    return m && m->data && aligned(m->data, 4) && m->request_stride >= 0 && m->head_stride >= 0 && m->length >= len;
 }
 
 // Masses that a call writes: the rows of `len` must not overlap, whichever of
 // requests and heads lies outside.
 bool writable(const shkv_mass *m, int32_t batch, int32_t hkv, int64_t len)
 {
-    if (!readable(m))
+    if (!readable(m, len))
         return false;
     const int64_t r = m->request_stride, h = m->head_stride;
     if (batch == 1 || hkv == 1)
@@ -188,9 +190,9 @@ shkv_status add_mass(shkv_pool *pool, int32_t batch, int32_t n_q, int32_t hq, co
     if (!q || !aligned(q, 16) || !lse || !aligned(lse, 4) || q_token < row || q_token % c.head_dim || q_request <= 0 ||
         q_request % q_token || lse_request < 0 || lse_token < 0 || !isfinite(scale_log2) || !isfinite(decay) ||
         !writable(out, batch, c.num_kv_heads, len) ||
-        (mass && (!readable(mass) || !same_layout(mass, out, batch, c.num_kv_heads))))
+        (mass && (!readable(mass, len) || !same_layout(mass, out, batch, c.num_kv_heads))))
         return SHKV_ERR_INVALID_ARG;
-    if (q_request >= (int64_t)1 << 39)   // a tensor map's strides are below 2^40 bytes
+    if (q_request >= (int64_t)1 << 39 || len > kMaxTokens)   // a tensor map's strides are below 2^40 bytes
         return SHKV_ERR_UNSUPPORTED;
     MassParams p;
     memset(&p, 0, sizeof p);
@@ -304,7 +306,8 @@ try {
         return SHKV_ERR_INVALID_ARG;
     if (batch == 0)
         return SHKV_OK;
-    if (!readable(mass) || !index || !aligned(index, 4) || index_stride < 1 || index_stride > INT32_MAX)
+    const int64_t len = longest(batch, pool->lens.data());
+    if (!readable(mass, len) || !index || !aligned(index, 4) || index_stride < 1)
         return SHKV_ERR_INVALID_ARG;
     const int32_t hkv = pool->cfg.num_kv_heads;
     SelectParams p;
@@ -317,7 +320,7 @@ try {
         p.lens[b] = L;
         p.keep[b] = keep[b];
     }
-    if ((int64_t)batch * hkv > INT32_MAX)
+    if ((int64_t)batch * hkv * 8 > INT32_MAX || len > kMaxTokens)
         return SHKV_ERR_UNSUPPORTED;
     p.mass = mass->data;
     p.mass_request = mass->request_stride;
@@ -330,9 +333,9 @@ try {
     p.hkv = hkv;
     p.sink = sink;
     p.recent = recent;
-    if (launch_select(p, (cudaStream_t)stream) != cudaSuccess)
+    if (launch_select(p, pool->num_sms, (cudaStream_t)stream) != cudaSuccess)
         return SHKV_ERR_CUDA;
-    record_stream_use(stream, {mass_span(p.mass, p.mass_request, p.mass_head, batch, hkv, longest(batch, p.lens)),
+    record_stream_use(stream, {mass_span(p.mass, p.mass_request, p.mass_head, batch, hkv, len),
                                span_of(index, (size_t)batch * hkv * index_stride * 4)});
     return SHKV_OK;
 } catch (const std::exception &) {
@@ -378,10 +381,10 @@ try {
         return SHKV_ERR_INVALID_ARG;
     if (table && !aligned(table, 4))
         return SHKV_ERR_INVALID_ARG;
-    if (out && (!readable(mass) || !writable(out, batch, c.num_kv_heads, len) ||
+    if (out && (!readable(mass, len) || !writable(out, batch, c.num_kv_heads, len) ||
                 !same_layout(mass, out, batch, c.num_kv_heads)))
         return SHKV_ERR_INVALID_ARG;
-    if ((pages + batch) * c.num_kv_heads > INT32_MAX)
+    if ((pages + batch) * c.num_kv_heads > INT32_MAX || len > kMaxTokens)
         return SHKV_ERR_UNSUPPORTED;
     p.k_pages = static_cast<uint4 *>(c.k_pages);
     p.v_pages = static_cast<uint4 *>(c.v_pages);

@@ -339,34 +339,85 @@ __device__ void issue(const MassParams &p, const Ctx<D> &c, uint32_t tmem)
     mbar_drain_bounded(c.fin(), 0u);
 }
 
+// Waits for the columns of S that were asked for.
+__device__ __forceinline__ void landed(uint32_t (&r)[64])
+{
+    // the operands keep the compiler from using a register before the wait
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 64; i += 16)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                     "+r"(r[i + 6]), "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]),
+                     "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15]));
+}
+
+// The weights of columns c0 .. c0 + 15 into four partial sums, two values an
+// instruction where there is one for it.
+template <bool kMasked>
+__device__ __forceinline__ void weigh16(const uint32_t *s, const float *lse, int c0, int rows, int first, float c,
+                                        float2 (&sum)[2])
+{
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+        const float4 l = *reinterpret_cast<const float4 *>(lse + c0 + j);
+        float2 x0 = __ffma2_rn(make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), make_float2(c, c),
+                               make_float2(l.x, l.y));
+        float2 x1 = __ffma2_rn(make_float2(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])), make_float2(c, c),
+                               make_float2(l.z, l.w));
+        if (kMasked) {
+            const int i = c0 + j;
+            x0.x = i >= first && i < rows ? x0.x : -INFINITY;
+            x0.y = i + 1 >= first && i + 1 < rows ? x0.y : -INFINITY;
+            x1.x = i + 2 >= first && i + 2 < rows ? x1.x : -INFINITY;
+            x1.y = i + 3 >= first && i + 3 < rows ? x1.y : -INFINITY;
+        }
+        sum[0] = __fadd2_rn(sum[0], make_float2(ex2_approx(x0.x), ex2_approx(x0.y)));
+        sum[1] = __fadd2_rn(sum[1], make_float2(ex2_approx(x1.x), ex2_approx(x1.y)));
+    }
+}
+
 // Sum of a thread's weights over the columns [first, rows) of S at taddr.  The
 // columns that the MMA rounds rows up to are zero queries, whose product with an
-// infinite key is no number; `latest` is the warp's largest `first`.
-__device__ __forceinline__ float weigh(uint32_t taddr, const float *lse, int rows, int first, int latest, float c)
+// infinite key is no number; `latest` is the warp's largest `first`.  S is in
+// registers half a buffer at a time; `empty` is arrived on as soon as all of it
+// is, so that the next product into the buffer runs beside the exponentials.
+__device__ __forceinline__ float weigh(uint32_t taddr, const float *lse, int rows, int first, int latest, float c,
+                                       uint32_t empty)
 {
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-    for (int c0 = 0; c0 < rows; c0 += 16) {
-        uint32_t s[16];
-        tmem_ld16_nowait(taddr + (uint32_t)c0, s);
-        float x[16];
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    uint32_t s[2][64];
+    tmem_ld32_nowait(taddr, s[0]);
+    if (rows > 32)
+        tmem_ld32_nowait(taddr + 32u, s[0] + 32);
+    landed(s[0]);
+    if (rows > 64)
+        tmem_ld32_nowait(taddr + 64u, s[1]);
+    if (rows > 96)
+        tmem_ld32_nowait(taddr + 96u, s[1] + 32);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<float4 *>(x + 4 * j) = *reinterpret_cast<const float4 *>(lse + c0 + 4 * j);
-        tmem_wait_ld();
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            x[j] = fmaf(__uint_as_float(s[j]), c, x[j]);
-        if (c0 < latest || c0 + 16 > rows) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                x[j] = c0 + j >= first && c0 + j < rows ? x[j] : -INFINITY;
+    for (int h = 0; h < 2; ++h) {
+        if (h)
+            landed(s[1]);
+        if (h || rows <= 64) {
+            tc_fence_before();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0)
+                mbar_arrive(empty);
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            sum[j & 3] += ex2_approx(x[j]);
+        for (int i = 0; i < 4; ++i) {
+            const int c0 = 64 * h + 16 * i;
+            if (c0 >= rows)
+                break;
+            if (c0 < latest || c0 + 16 > rows)
+                weigh16<true>(s[h] + 16 * i, lse, c0, rows, first, c, sum);
+            else
+                weigh16<false>(s[h] + 16 * i, lse, c0, rows, first, c, sum);
+        }
+        if (rows <= 64)
+            break;
     }
-    return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
 // The weights of tile x of every item, and its masses.
@@ -415,12 +466,10 @@ __device__ void add_up(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int 
                 // query tokens before t - past do not see the thread's token
                 const int first = t - w.past - i0, latest = first + 31 - lane;
                 sum += weigh(taddr + (uint32_t)st.slot * 128u, c.lse(qt.slot), rows, first * p.group, latest * p.group,
-                             p.scale_log2);
-                tc_fence_before();
-            }
-            __syncwarp();
-            if (lane == 0)
+                             p.scale_log2, c.s_empty(x, st.slot));
+            } else if (lane == 0) {
                 mbar_arrive(c.s_empty(x, st.slot));
+            }
             st.next(2);
         }
         if (!inside)

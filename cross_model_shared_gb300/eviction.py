@@ -7,14 +7,14 @@ mass, and ``evict_tokens`` moves them into new pages.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 from typing import Dict, Optional
 
-import numpy as np
 import torch
 
 from . import _native as N
-from .q8 import _HostInts
+from .q8 import _HostInts, _current_device, _raw_stream
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _HERE = contextlib.nullcontext()
@@ -37,13 +37,13 @@ class EvictionCalls:
     # -- arguments ------------------------------------------------------------
     def _enter(self, stream: Optional[torch.cuda.Stream]):
         """(context that makes the stream and the pool's device current, raw stream)."""
-        device = self.k_pages.device
         if stream is None:
-            stream = torch.cuda.current_stream(device)
-            if torch.cuda.current_device() == device.index:
-                return _HERE, int(stream.cuda_stream)
-        elif stream.device != device:
-            raise ValueError(f"stream must be one of {device}")
+            index = self.k_pages.device.index
+            if _raw_stream is not None and _current_device() == index:
+                return _HERE, _raw_stream(index)
+            stream = torch.cuda.current_stream(self.k_pages.device)
+        elif stream.device != self.k_pages.device:
+            raise ValueError(f"stream must be one of {self.k_pages.device}")
         return torch.cuda.stream(stream), int(stream.cuda_stream)
 
     def _hold(self, raw: int, named: Optional[torch.cuda.Stream], *tensors: Optional[torch.Tensor]) -> None:
@@ -67,29 +67,34 @@ class EvictionCalls:
                 t.record_stream(stream)
 
     def _mass_of(self, t: torch.Tensor, batch: int, name: str) -> N.shkv_mass:
-        if t.dtype is not _F32 or t.device != self.k_pages.device or t.dim() != 3:
-            raise ValueError(f"{name} must be float32 [B, num_kv_heads, T] on {self.k_pages.device}")
-        if t.shape[0] < batch or t.shape[1] != self.num_kv_heads or (t.shape[2] > 1 and t.stride(2) != 1):
-            raise ValueError(f"{name} must be [B, {self.num_kv_heads}, T] of at least {batch} requests, "
-                             "its last dimension contiguous")
-        return N.shkv_mass(t.data_ptr(), t.stride(0), t.stride(1))
+        if t.dtype is not _F32 or t.device != self.k_pages.device:
+            raise ValueError(f"{name} must be float32 on {self.k_pages.device}")
+        shape = t.shape
+        if len(shape) != 3 or shape[0] < batch or shape[1] != self.num_kv_heads:
+            raise ValueError(f"{name} must be [B, {self.num_kv_heads}, T] of at least {batch} requests")
+        request, head, token = t.stride()
+        if token != 1 and shape[2] > 1:
+            raise ValueError(f"{name}: a row's masses must be contiguous")
+        return N.shkv_mass(t.data_ptr(), request, head, shape[2])
 
-    def _masses(self, mass: Optional[torch.Tensor], out: Optional[torch.Tensor], batch: int, longest: int):
-        """Views of the masses read (or None) and written, and the tensor written."""
-        if out is None:
-            out = mass if mass is not None else torch.zeros((batch, self.num_kv_heads, longest), dtype=_F32,
-                                                            device=self.k_pages.device)
-        views = []
-        for t, name in ((mass, "mass"), (out, "out")):
-            if t is not None and t.dim() == 3 and t.shape[2] < longest:
-                raise ValueError(f"{name} must hold the longest request's {longest} tokens")
-            views.append(self._mass_of(t, batch, name) if t is not None else None)
-        return views[0], views[1], out
+    def _mass_workspace(self) -> int:
+        n = self.__dict__.get("_mass_workspace_bytes")
+        if n is None:
+            n = self._mass_workspace_bytes = N.shkv_prefill_mass_workspace_size(self.handle)
+        return n
 
-    def _longest(self, batch: int) -> int:
-        if batch > self.max_batch:
-            raise ValueError(f"at most {self.max_batch} requests")
-        return int(self.host_seq_lens(batch).max(initial=0))
+    def _masses(self, mass: Optional[torch.Tensor], out: Optional[torch.Tensor], batch: int):
+        """Masses read (or None) and written, for the C call, and the tensor written."""
+        m = self._mass_of(mass, batch, "mass") if mass is not None else None
+        if out is not None:
+            return m, self._mass_of(out, batch, "out"), out
+        if mass is None:
+            if batch > self.max_batch:
+                raise ValueError(f"at most {self.max_batch} requests")
+            longest = int(self.host_seq_lens(batch).max(initial=0))
+            mass = torch.zeros((batch, self.num_kv_heads, longest), dtype=_F32, device=self.k_pages.device)
+            return None, self._mass_of(mass, batch, "out"), mass
+        return m, m, mass
 
     # -- the path -------------------------------------------------------------
     def decode_mass(self, q: torch.Tensor, lse: torch.Tensor, n_models: int, mass: Optional[torch.Tensor],
@@ -111,7 +116,7 @@ class EvictionCalls:
             raise ValueError(f"lse must be a contiguous float32 tensor {[B, rows]} on {q.device}")
         ctx, s = self._enter(stream)
         with ctx:
-            m, o, result = self._masses(mass, out, B, self._longest(B))
+            m, o, result = self._masses(mass, out, B)
             self._hold(s, stream, q, lse, mass, out)
             N.shkv_decode_mass(self.handle, B, n_models, rows // n_models, q.data_ptr(),
                                D ** -0.5 if scale is None else float(scale), lse.data_ptr(), float(decay), m, o, s)
@@ -136,9 +141,9 @@ class EvictionCalls:
             raise ValueError("lse: a token's values must be contiguous")
         ctx, s = self._enter(stream)
         with ctx:
-            m, o, result = self._masses(mass, out, B, self._longest(B))
+            m, o, result = self._masses(mass, out, B)
             # scratch of this call alone: its memory goes back to the stream's (or a graph's) own
-            ws = torch.empty(N.shkv_prefill_mass_workspace_size(self.handle), dtype=torch.uint8, device=q.device)
+            ws = torch.empty(self._mass_workspace(), dtype=torch.uint8, device=q.device)
             self._hold(s, stream, q, lse, mass, out)
             N.shkv_prefill_mass(self.handle, B, T, H, q.data_ptr(), q.stride(0), q.stride(1),
                                 D ** -0.5 if scale is None else float(scale), lse.data_ptr(), lse.stride(0),
@@ -153,26 +158,27 @@ class EvictionCalls:
         int32 [B, num_kv_heads, most kept], ascending, -1 behind a request's
         kept tokens; a request of at most ``keep[b]`` tokens keeps them all."""
         k = _HostInts(keep, "keep")
-        longest = self._longest(k.n)
-        lens = self.host_seq_lens(k.n)
-        most = int(np.minimum(lens, np.asarray(k._keep, dtype=np.int64)).max(initial=0))
+        sink, recent = int(sink), int(recent)
+        if not (0 <= sink < 2 ** 31 and 0 <= recent < 2 ** 31):
+            raise ValueError("sink and recent must lie in [0, 2**31)")
         ctx, s = self._enter(stream)
         with ctx:
-            if mass.dim() == 3 and mass.shape[2] < longest:
-                raise ValueError(f"mass must hold the longest request's {longest} tokens")
             m = self._mass_of(mass, k.n, "mass")
-            shape = (k.n, self.num_kv_heads, max(most, 1))
+            index = out
             if out is None:
-                index = torch.empty(shape, dtype=_I32, device=self.k_pages.device)
-            else:
-                index = out
-                if out.dtype is not _I32 or out.device != self.k_pages.device or out.dim() != 3 or \
-                        not out.is_contiguous() or out.shape[:2] != shape[:2] or out.shape[2] < most:
-                    raise ValueError(f"out must be a contiguous int32 tensor [{shape[0]}, {shape[1]}, at least {most}]")
+                if k.n > self.max_batch:
+                    raise ValueError(f"at most {self.max_batch} requests")
+                lens = array.array("i", bytes(4 * k.n))
+                if k.n:
+                    N.shkv_pool_get_seq_lens(self.handle, k.n, lens.buffer_info()[0])
+                most = max(map(min, k._keep, lens), default=0)
+                index = torch.empty((k.n, self.num_kv_heads, max(most, 1)), dtype=_I32, device=self.k_pages.device)
+            elif out.dtype is not _I32 or out.device != self.k_pages.device or out.dim() != 3 or \
+                    not out.is_contiguous() or out.shape[0] != k.n or out.shape[1] != self.num_kv_heads:
+                raise ValueError(f"out must be a contiguous int32 tensor [{k.n}, {self.num_kv_heads}, K]")
             if k.n:
                 self._hold(s, stream, mass, out)
-                N.shkv_select_tokens(self.handle, k.n, m, k.ptr, int(sink), int(recent), index.data_ptr(),
-                                     index.shape[2], s)
+                N.shkv_select_tokens(self.handle, k.n, m, k.ptr, sink, recent, index.data_ptr(), index.shape[2], s)
         return index
 
     def evict_tokens(self, index: torch.Tensor, keep, new_table: torch.Tensor, mass: Optional[torch.Tensor] = None,
@@ -207,10 +213,9 @@ class EvictionCalls:
         for t, name in tables:
             if t.dtype is not _I32 or t.device != device or t.dim() != 2 or not t.is_contiguous() or t.shape[0] < k.n:
                 raise ValueError(f"{name} must be a contiguous int32 tensor [{k.n}, pages] on {device}")
-        longest = max(lens._keep, default=0) if lens is not None else self._longest(k.n)
         ctx, s = self._enter(stream)
         with ctx:
-            m, o, _ = self._masses(mass, out, k.n, longest) if mass is not None else (None, None, None)
+            m, o, _ = self._masses(mass, out, k.n) if mass is not None else (None, None, None)
             if k.n:
                 self._hold(s, stream, index, new_table, table, mass, out)
                 N.shkv_evict_tokens(self.handle, k.n, k.ptr, index.data_ptr(), index.shape[2], new_table.data_ptr(),

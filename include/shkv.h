@@ -662,13 +662,14 @@ shkv_status shkv_q8_chunk_attention(shkv_q8_pool *pool, int32_t batch, const int
  * with the lengths of its capture; SHKV_ERRF_SEQ_LEN is set where the device
  * copy of a length then differs.
  *
- * Masses: fp32, mass of token t of request b and KV head g at
+ * Masses: fp32, mass of token t < length of request b and KV head g at
  * data[b * request_stride + g * head_stride + t] (strides in elements, any
- * alignment of 4 bytes).
+ * alignment of 4 bytes).  A call whose longest request has more than `length`
+ * tokens, or more than 2^30, is refused.
  */
 typedef struct {
     float *data;
-    int64_t request_stride, head_stride;
+    int64_t request_stride, head_stride, length;
 } shkv_mass;
 
 /*
