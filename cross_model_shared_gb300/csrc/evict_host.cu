@@ -99,7 +99,7 @@ bool make_q_map(CUtensorMap *tm, const void *q, const shkv_pool_config &c, int32
 // Bytes of the cut items' sums.
 size_t piece_bytes(const shkv_pool *pool)
 {
-    return (size_t)2 * std::min(pool->num_sms, kMassMaxCtas) * kMassItem * sizeof(float);
+    return (size_t)2 * std::min(pool->num_sms, kMassMaxCtas) * kMassSpan * kMassTile * sizeof(float);
 }
 
 // Cuts the items into at most `limit` ranges of about equal cost, counted in
@@ -110,27 +110,29 @@ constexpr int64_t kItemCost = 1, kMinPiece = 2;
 
 bool plan_mass(MassParams &p, int limit)
 {
-    // cost of tile pair `pair` of a request, and of all of its pairs of one head
-    auto cost = [&](int L, int pair) -> int64_t {
-        const int past = mass_past(L, p.n_q, p.causal), t = pair * kMassItem;
-        int64_t k = kItemCost + p.blocks - mass_block0(t, past, p.tpt);
-        if (t + kMassTile < L)
-            k += p.blocks - mass_block0(t + kMassTile, past, p.tpt);
+    const int tokens = p.span * kMassTile;
+    // cost of item `at` of a request's head, and of all of the head's
+    auto cost = [&](int L, int at) -> int64_t {
+        const int past = mass_past(L, p.n_q, p.causal);
+        int64_t k = kItemCost;
+        for (int t = at * tokens; t < std::min(L, (at + 1) * tokens); t += kMassTile)
+            k += p.blocks - mass_block0(t, past, p.tpt);
         return k;
     };
-    // the first `even` pairs take part in every block
-    auto even = [&](int L) -> int64_t { return std::max(0, std::min(L / kMassItem, mass_past(L, p.n_q, p.causal) / kMassItem)); };
-    const int64_t full = kItemCost + 2 * (int64_t)p.blocks;
+    // the first `even` items take part in every block
+    auto even = [&](int L) -> int64_t { return std::max(0, std::min(L, mass_past(L, p.n_q, p.causal)) / tokens); };
+    const int64_t full = kItemCost + (int64_t)p.span * p.blocks;
     auto head = [&](int L) -> int64_t {
         int64_t k = even(L) * full;
-        for (int pair = (int)even(L); pair * kMassItem < L; ++pair)
-            k += cost(L, pair);
+        for (int at = (int)even(L); at * tokens < L; ++at)
+            k += cost(L, at);
         return k;
     };
     int64_t total = 0;
     for (int b = 0; b < p.batch; ++b)
         total += p.hkv * head(p.lens[b]);
-    const int64_t C = std::max<int64_t>(1, std::min<int64_t>(limit, p.blocks > 1 ? total / (4 * kMinPiece) : p.item0[p.batch]));
+    const int64_t C = std::max<int64_t>(
+        1, std::min<int64_t>(limit, p.blocks > 1 ? total / (p.span * kMinPiece) : p.item0[p.batch]));
     int n = 0, b = 0;
     int64_t before = 0, h = head(p.lens[0]);
     bool cut = false;
@@ -143,20 +145,20 @@ bool plan_mass(MassParams &p, int limit)
         }
         const int L = p.lens[b], g = (int)((target - before) / h);
         int64_t rest = (target - before) % h;
-        int pair = (int)std::min(rest / full, even(L));
-        rest -= pair * full;
-        int64_t k = cost(L, pair);
+        int at = (int)std::min(rest / full, even(L));
+        rest -= at * full;
+        int64_t k = cost(L, at);
         while (rest >= k) {
             rest -= k;
-            k = cost(L, ++pair);
+            k = cost(L, ++at);
         }
-        int item = p.item0[b] + g * ((L + kMassItem - 1) / kMassItem) + pair;
-        const int block0 = mass_block0(pair * kMassItem, mass_past(L, p.n_q, p.causal), p.tpt);
-        const int64_t steps = p.blocks - block0, at = steps * rest / k;
+        int item = p.item0[b] + g * ((L + tokens - 1) / tokens) + at;
+        const int block0 = mass_block0(at * tokens, mass_past(L, p.n_q, p.causal), p.tpt);
+        const int64_t steps = p.blocks - block0, done = steps * rest / k;
         int block = 0;
-        if (steps >= 2 * kMinPiece && at >= kMinPiece && steps - at >= kMinPiece)
-            block = block0 + (int)at;
-        else if (2 * at >= steps)
+        if (steps >= 2 * kMinPiece && done >= kMinPiece && steps - done >= kMinPiece)
+            block = block0 + (int)done;
+        else if (2 * done >= steps)
             ++item;
         if (item > p.cut_item[n] || (item == p.cut_item[n] && block > p.cut_block[n])) {
             if (item >= p.item0[p.batch])
@@ -171,6 +173,21 @@ bool plan_mass(MassParams &p, int limit)
     p.cut_item[n + 1] = p.item0[p.batch];
     p.cut_block[n + 1] = 0;
     return cut;
+}
+
+// Tiles of an item: four share a block's rows, fewer where that leaves the CTAs
+// less than four (item, block) steps each.
+int32_t item_span(int32_t batch, const int32_t *lens, int32_t hkv, int32_t blocks, int ctas)
+{
+    int32_t span = kMassSpan;
+    for (; span > 1; span /= 2) {
+        int64_t items = 0;
+        for (int b = 0; b < batch; ++b)
+            items += ((int64_t)lens[b] + span * kMassTile - 1) / (span * kMassTile);
+        if (items * hkv * blocks >= 4 * ctas)
+            break;
+    }
+    return span;
 }
 
 // Both forms: the n_q query tokens of every request.
@@ -196,11 +213,16 @@ shkv_status add_mass(shkv_pool *pool, int32_t batch, int32_t n_q, int32_t hq, co
         return SHKV_ERR_UNSUPPORTED;
     MassParams p;
     memset(&p, 0, sizeof p);
+    p.group = hq / c.num_kv_heads;
+    p.tpt = std::min(kMassRows / p.group, n_q);
+    p.blocks = (n_q + p.tpt - 1) / p.tpt;
+    const int ctas = std::min(pool->num_sms, kMassMaxCtas);
+    p.span = item_span(batch, pool->lens.data(), c.num_kv_heads, p.blocks, ctas);
     int64_t items = 0;
     for (int b = 0; b < batch; ++b) {
         p.lens[b] = pool->lens[b];
         p.item0[b] = (int32_t)items;
-        items += ((int64_t)pool->lens[b] + kMassItem - 1) / kMassItem * c.num_kv_heads;
+        items += ((int64_t)pool->lens[b] + p.span * kMassTile - 1) / (p.span * kMassTile) * c.num_kv_heads;
         if (items > INT32_MAX)
             return SHKV_ERR_UNSUPPORTED;
     }
@@ -225,20 +247,17 @@ shkv_status add_mass(shkv_pool *pool, int32_t batch, int32_t n_q, int32_t hq, co
     p.batch = batch;
     p.n_q = n_q;
     p.hkv = c.num_kv_heads;
-    p.group = hq / c.num_kv_heads;
     p.head_dim = c.head_dim;
     p.page_size = c.page_size;
     p.max_pages = c.max_pages_per_seq;
     p.num_pages = c.num_pages;
     p.causal = causal;
-    p.tpt = std::min(kMassRows / p.group, n_q);
-    p.blocks = (n_q + p.tpt - 1) / p.tpt;
     p.scale_log2 = scale_log2;
     p.decay = decay;
     CUtensorMap tm_q;
     if (!make_q_map(&tm_q, q, c, batch, n_q, hq, q_request, q_token, p.tpt))
         return SHKV_ERR_CUDA;
-    const bool pieces = plan_mass(p, std::min(pool->num_sms, kMassMaxCtas));
+    const bool pieces = plan_mass(p, ctas);
     if (launch_mass(pool->tm_k2, tm_q, p, pieces, (cudaStream_t)stream) != cudaSuccess)
         return SHKV_ERR_CUDA;
     record_stream_use(stream,

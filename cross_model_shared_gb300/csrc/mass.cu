@@ -13,12 +13,20 @@
 // lane) and adds up its row of weights in a register, without a word between
 // threads: no atomics, the same bits every time.  K is read once per call; the
 // rows of a decode step stay in shared memory while a CTA walks along the tokens
-// of a head, those of a chunk stream past the two K tiles of an item (a Q block
-// of 32 KB feeds two MMAs of 128 x 128 x D).
+// of a head, those of a chunk stream past the K tiles of an item (a Q block of
+// 32 KB feeds up to four MMAs of 128 x 128 x D).
 //
-// Warps 0-3 and 4-7 take the weights of the item's first and second tile, each
-// with two S buffers; warp 8 copies K, warp 9 Q (and the log-sum-exps), one lane
-// of warp 10 issues the MMAs.
+// Warps 0-15 take the weights, warp 16 copies K, warp 17 Q (and the log-sum-exps),
+// one lane of warp 18 issues the MMAs, in one of two ways:
+//
+// * few blocks (a decode step, a short window): both operands from shared memory,
+//   four warps a tile of an item, four S buffers.  Bound by the bytes of K.
+// * many blocks: at M = N = 128 two operands from shared memory take 120 of its 128
+//   bytes a cycle and leave none for the log-sum-exps, so an item's K goes from
+//   shared memory to TMEM (64 columns a tile) once, and two S buffers remain, one
+//   for the even tiles and one for the odd ones, each emptied into the registers
+//   of eight warps, 64 columns a thread, before the exponentials begin.  Bound by
+//   the tensor cores and the exponentials alike (512 cycles a product each).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -32,9 +40,9 @@ namespace shkv {
 
 namespace {
 
-constexpr int kThreads = 352;
-constexpr int kKWarp = 8, kQWarp = 9, kMmaWarp = 10;
-constexpr uint32_t kTmemCols = 512;          // S[tile][buffer], 128 columns each
+constexpr int kThreads = 608;
+constexpr int kKWarp = 16, kQWarp = 17, kMmaWarp = 18;
+constexpr uint32_t kTmemCols = 512;          // four S buffers of 128 columns
 constexpr uint32_t kHalfBytes = 128u * 128u; // 64 columns of 128 tokens or rows
 
 // Ring slots: at D = 128 seven of 32 KB fill shared memory (K four, a decode's
@@ -43,8 +51,8 @@ template <int D>
 struct Ring {
     static constexpr int kK = D == 128 ? 4 : 8, kQ = D == 128 ? 3 : 5;
     static constexpr uint32_t kSlot = (uint32_t)(D / 64) * kHalfBytes;
-    // barriers: K full, K empty, Q full, Q empty, S full [tile][buffer], S empty, fin
-    static constexpr int kBars = 2 * kK + 2 * kQ + 9;
+    // barriers: K full, K empty, Q full, Q empty, S full, S empty, K in TMEM, fin
+    static constexpr int kBars = 2 * kK + 2 * kQ + 13;
     static constexpr uint32_t kQ0 = kK * kSlot, kLse = kQ0 + kQ * kSlot, kBar0 = kLse + kQ * kMassRows * 4,
                               kMisc = kBar0 + 8 * kBars, kBytes = kMisc + 16 + 1024;
 };
@@ -61,12 +69,13 @@ struct Ctx {
     __device__ uint32_t k_empty(int s) const { return bar(Ring<D>::kK + s); }
     __device__ uint32_t q_full(int s) const { return bar(2 * Ring<D>::kK + s); }
     __device__ uint32_t q_empty(int s) const { return bar(2 * Ring<D>::kK + Ring<D>::kQ + s); }
-    __device__ uint32_t s_full(int x, int i) const { return bar(2 * Ring<D>::kK + 2 * Ring<D>::kQ + 2 * x + i); }
-    __device__ uint32_t s_empty(int x, int i) const { return s_full(x, i) + 32u; }
-    __device__ uint32_t fin() const { return s_full(0, 0) + 64u; }
+    __device__ uint32_t s_full(int i) const { return bar(2 * Ring<D>::kK + 2 * Ring<D>::kQ + i); }
+    __device__ uint32_t s_empty(int i) const { return s_full(i) + 32u; }
+    __device__ uint32_t k_in_tmem(int x) const { return s_full(x) + 64u; }
+    __device__ uint32_t fin() const { return s_full(0) + 96u; }
     __device__ uint32_t k_slot(int s) const { return base + (uint32_t)s * Ring<D>::kSlot; }
     __device__ uint32_t q_slot(int s) const { return base + Ring<D>::kQ0 + (uint32_t)s * Ring<D>::kSlot; }
-    __device__ float *lse(int s) const { return reinterpret_cast<float *>(smem + Ring<D>::kLse) + s * kMassRows; }
+    __device__ uint32_t lse(int s) const { return base + Ring<D>::kLse + (uint32_t)(s * kMassRows * 4); }
     __device__ bool wait(uint32_t b, uint32_t parity) const { return q8_wait<true>(b, parity, abort_flag, err); }
 };
 
@@ -85,29 +94,39 @@ struct Turn {
 
 // The items of a CTA's range, one after another; every role walks them alike.
 struct Walk {
-    int item, last, b, g, pair, pairs;   // `last`: one past the range's last item
+    int item, last, b, g, at, items;     // `last`: one past the range's last item; item `at` of the head's `items`
     int L, past, t0;
     int begin, end;                      // blocks of this item in the range
-    int block0[2];                       // first block that a tile takes part in; beyond all if it is empty
     bool fresh;                          // another (request, KV head) than the item before
+    // whether block k has a row that sees a token of tile x
+    __device__ bool sees(const MassParams &p, int k, int x) const
+    {
+        return t0 + x * kMassTile - past < min((k + 1) * p.tpt, p.n_q);
+    }
+    __device__ bool whole(const MassParams &p) const { return begin == mass_block0(t0, past, p.tpt) && end == p.blocks; }
 };
 
 __device__ __forceinline__ void walk_request(const MassParams &p, Walk &w)
 {
     w.L = p.lens[w.b];
     w.past = mass_past(w.L, p.n_q, p.causal);
-    w.pairs = (w.L + kMassItem - 1) / kMassItem;
+    w.items = (w.L + p.span * kMassTile - 1) / (p.span * kMassTile);
 }
 
 __device__ __forceinline__ void walk_item(const MassParams &p, Walk &w)
 {
-    w.t0 = w.pair * kMassItem;
-    w.block0[0] = mass_block0(w.t0, w.past, p.tpt);
-    w.block0[1] = w.t0 + kMassTile < w.L ? mass_block0(w.t0 + kMassTile, w.past, p.tpt) : INT32_MAX;
-    w.begin = w.block0[0];
+    w.t0 = w.at * p.span * kMassTile;
+    w.begin = mass_block0(w.t0, w.past, p.tpt);
     if (w.item == p.cut_item[blockIdx.x])
         w.begin = max(w.begin, p.cut_block[blockIdx.x]);
     w.end = w.item == p.cut_item[blockIdx.x + 1] ? p.cut_block[blockIdx.x + 1] : p.blocks;
+}
+
+// Where the sums of a cut item go: of a range's cut items the first has its
+// beginning in the range before, the last only its end cut off.
+__device__ __forceinline__ int piece_of(const MassParams &p, const Walk &w)
+{
+    return 2 * blockIdx.x + (w.item != p.cut_item[blockIdx.x] || p.cut_block[blockIdx.x] == 0);
 }
 
 // Whether the CTA has an item at all.
@@ -127,8 +146,8 @@ __device__ __forceinline__ bool walk_first(const MassParams &p, Walk &w)
     }
     w.b = lo;
     walk_request(p, w);
-    w.g = (w.item - p.item0[lo]) / w.pairs;
-    w.pair = (w.item - p.item0[lo]) % w.pairs;
+    w.g = (w.item - p.item0[lo]) / w.items;
+    w.at = (w.item - p.item0[lo]) % w.items;
     w.fresh = true;
     walk_item(p, w);
     return true;
@@ -139,8 +158,8 @@ __device__ __forceinline__ bool walk_next(const MassParams &p, Walk &w)
     if (++w.item >= w.last)
         return false;
     w.fresh = false;
-    if (++w.pair == w.pairs) {
-        w.pair = 0;
+    if (++w.at == w.items) {
+        w.at = 0;
         w.fresh = true;
         if (++w.g == p.hkv) {
             w.g = 0;
@@ -157,9 +176,9 @@ __device__ __forceinline__ bool walk_next(const MassParams &p, Walk &w)
 // A block of rows is copied again for every item, unless it is a head's only one.
 __device__ __forceinline__ bool new_rows(const MassParams &p, const Walk &w) { return p.blocks > 1 || w.fresh; }
 
-// K tiles: a lane per (column half, page) of a tile.  A page outside the pool
-// is left out and flagged; the tile's threads look at their table entries
-// themselves.
+// K tiles, a lane per (column half, page) of a tile.  A lane also holds one of the
+// item's table entries, read an item ahead.  A page outside the pool is left out
+// and flagged; the tile's threads look at their table entries themselves.
 template <int D>
 __device__ void copy_k(const CUtensorMap *tm, const MassParams &p, const Ctx<D> &c)
 {
@@ -167,48 +186,46 @@ __device__ void copy_k(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
     const int half = lane / RB, rb = lane % RB;
     const bool copier = half < D / 64;
     const uint64_t pol = l2_evict_first_policy();
+    auto entry = [&](const Walk &w) {
+        const int pg = w.t0 / P + lane;
+        return lane < p.span * RB && pg * P < w.L ? __ldg(p.block_table + (int64_t)w.b * p.max_pages + pg) : -1;
+    };
     Walk w;
     Turn turn;
-    bool alive = true;
-    int issued = 0;
-    if (!walk_first(p, w))
-        return;
-    do {
-        const int32_t *row = p.block_table + (int64_t)w.b * p.max_pages;
-        if (lane == 0 && w.fresh && w.pair == 0 && w.g == 0 && __ldg(p.seq_lens + w.b) != w.L)
+    bool alive = true, more = walk_first(p, w);
+    int issued = 0, id = more ? entry(w) : -1;
+    while (more) {
+        Walk next = w;
+        more = walk_next(p, next);
+        const int next_id = more ? entry(next) : -1;
+        if (lane == 0 && w.fresh && w.at == 0 && w.g == 0 && __ldg(p.seq_lens + w.b) != w.L)
             atomicOr(p.err, SHKV_ERRF_SEQ_LEN);
-        const int pages = (w.L + P - 1) / P;
-        int id[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int pg = (w.t0 + x * kMassTile) / P + rb;
-            id[x] = copier && pg < pages ? __ldg(row + pg) : -1;
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int pg = (w.t0 + x * kMassTile) / P + rb;
-            if (w.t0 + x * kMassTile >= w.L)
-                break;
-            bool ok = true;
-            if (alive && lane == 0)
-                ok = c.wait(c.k_empty(turn.slot), turn.parity ^ 1u);
-            alive = alive && __all_sync(0xffffffffu, ok);
-            const bool inside = copier && (uint32_t)id[x] < (uint32_t)p.num_pages;
-            if (copier && pg < pages && !inside)
+#pragma unroll 1
+        for (int x = 0; x < p.span && w.t0 + x * kMassTile < w.L; ++x) {
+            const int page = __shfl_sync(0xffffffffu, id, (x * RB + rb) & 31);
+            const bool there = copier && w.t0 + x * kMassTile + rb * P < w.L;
+            const bool inside = there && (uint32_t)page < (uint32_t)p.num_pages;
+            if (there && !inside)
                 atomicOr(p.err, SHKV_ERRF_PAGE_OOB);
             const uint32_t mask = __ballot_sync(0xffffffffu, inside);
-            if (alive && lane == 0)
-                mbar_arrive_expect_tx(c.k_full(turn.slot), (uint32_t)__popc(mask) * (uint32_t)P * 128u);
-            __syncwarp();
-            if (alive && inside)
-                tma_load_2d(c.k_slot(turn.slot) + (uint32_t)half * kHalfBytes + (uint32_t)(rb * P) * 128u, tm, half * 64,
-                            (id[x] * p.hkv + w.g) * P, c.k_full(turn.slot), pol);
-            if (alive) {
-                ++issued;
-                turn.next(Ring<D>::kK);
+            bool ok = true;
+            if (alive && lane == 0) {
+                ok = c.wait(c.k_empty(turn.slot), turn.parity ^ 1u);
+                if (ok)
+                    mbar_arrive_expect_tx(c.k_full(turn.slot), (uint32_t)__popc(mask) * (uint32_t)P * 128u);
             }
+            alive = __all_sync(0xffffffffu, alive && ok);
+            if (!alive)
+                continue;
+            if (inside)
+                tma_load_2d(c.k_slot(turn.slot) + (uint32_t)half * kHalfBytes + (uint32_t)(rb * P) * 128u, tm, half * 64,
+                            (page * p.hkv + w.g) * P, c.k_full(turn.slot), pol);
+            ++issued;
+            turn.next(Ring<D>::kK);
         }
-    } while (walk_next(p, w));
+        w = next;
+        id = next_id;
+    }
     if (!alive && lane == 0)                 // wait for the copies in flight
         for (int i = max(0, issued - Ring<D>::kK); i < issued; ++i)
             mbar_drain_bounded(c.k_full(i % Ring<D>::kK), (uint32_t)(i / Ring<D>::kK) & 1u);
@@ -225,6 +242,12 @@ __device__ void copy_q(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
     Turn turn;
     bool alive = true;
     int issued = 0;
+    int tok[kMassRows / 32], head[kMassRows / 32];       // of the lane's rows in a block
+#pragma unroll
+    for (int j = 0; j < kMassRows / 32; ++j) {
+        tok[j] = (lane + 32 * j) / p.group;
+        head[j] = lane + 32 * j - tok[j] * p.group;
+    }
     if (!walk_first(p, w))
         return;
     do {
@@ -239,7 +262,7 @@ __device__ void copy_q(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
                 const int r = lane + 32 * j;
                 off[j] = INFINITY;
                 if (r < rows)
-                    off[j] = lse_base2(__ldg(src + (i0 + r / p.group) * p.lse_token + r % p.group));
+                    off[j] = lse_base2(__ldg(src + (i0 + tok[j]) * p.lse_token + head[j]));
             }
             bool ok = true;
             if (alive && lane == 0)
@@ -249,7 +272,8 @@ __device__ void copy_q(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
                 continue;
 #pragma unroll
             for (int j = 0; j < kMassRows / 32; ++j)
-                c.lse(turn.slot)[lane + 32 * j] = -off[j];
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(c.lse(turn.slot) + 4u * (uint32_t)(lane + 32 * j)), "f"(-off[j])
+                             : "memory");
             __syncwarp();
             if (lane == 0)
                 mbar_arrive_expect_tx(c.q_full(turn.slot), bytes);
@@ -270,28 +294,39 @@ __device__ void copy_q(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
             mbar_drain_bounded(c.q_full(i % Ring<D>::kQ), (uint32_t)(i / Ring<D>::kQ) & 1u);
 }
 
+// Which of the S buffers x, x + span, .. a tile's next product goes to: four bits
+// a tile count the products, modulo twice the tile's buffers.
+struct SRing {
+    uint32_t counts = 0u;
+    int span, log2n;                         // 4 / span buffers a tile
+    __device__ explicit SRing(int span_) : span(span_), log2n(span_ == 4 ? 0 : span_ == 2 ? 1 : 2) {}
+    __device__ int buffer(int x) const { return x + span * (int)(counts >> 4 * x & ((1u << log2n) - 1u)); }
+    __device__ uint32_t parity(int x) const { return counts >> (4 * x + log2n) & 1u; }
+    __device__ void next(int x)
+    {
+        const uint32_t n = (counts >> 4 * x & 15u) + 1u & (2u << log2n) - 1u;
+        counts = (counts & ~(15u << 4 * x)) | n << 4 * x;
+    }
+};
+
 // S = K Q^T for every (block, tile) of the range.  A slot of K is free after the
-// item's last block, one of Q when the next block's rows are needed.
+// item's last block, one of Q when the next block's rows are needed.  (Loops are
+// kept rolled: the roles of an SM sub-partition share its instruction cache.)
 template <int D>
 __device__ void issue(const MassParams &p, const Ctx<D> &c, uint32_t tmem)
 {
     const uint64_t kd0 = umma_sdesc_sw128(c.k_slot(0), 16u, 1024u), qd0 = umma_sdesc_sw128(c.q_slot(0), 16u, 1024u);
     Walk w;
-    Turn kt, qt, st[2];
+    Turn kt, qt;
+    SRing st(p.span);
     bool alive = true, rows_in = false;
     if (!walk_first(p, w))
         return;
     do {
-        bool k_in[2] = {false, false};
-        int kslot[2];
-        uint32_t kpar[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            kslot[x] = kt.slot;
-            kpar[x] = kt.parity;
-            if (w.block0[x] < INT32_MAX)
-                kt.next(Ring<D>::kK);
-        }
+        const int tiles = min(p.span, (w.L - w.t0 + kMassTile - 1) / kMassTile);
+        uint32_t k_in = 0u;                  // tiles whose K has been waited for
+        Turn kx;
+#pragma unroll 1
         for (int k = w.begin; k < w.end; ++k) {
             if (new_rows(p, w)) {
                 if (rows_in) {
@@ -305,117 +340,123 @@ __device__ void issue(const MassParams &p, const Ctx<D> &c, uint32_t tmem)
             const int rows = min(p.tpt, p.n_q - k * p.tpt) * p.group;
             const uint32_t idesc = umma_idesc_bf16(kMassTile, (rows + 15) & ~15, false, false);
             const uint64_t qd = qd0 + (((uint32_t)qt.slot * Ring<D>::kSlot) >> 4);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (k < w.block0[x])
+            kx = kt;
+#pragma unroll 1
+            for (int x = 0; x < tiles; ++x, kx.next(Ring<D>::kK)) {
+                if (!w.sees(p, k, x))
                     continue;
-                if (alive && !k_in[x])
-                    alive = c.wait(c.k_full(kslot[x]), kpar[x]);
-                k_in[x] = true;
+                const int s = st.buffer(x);
+                if (alive && !(k_in >> x & 1u))
+                    alive = c.wait(c.k_full(kx.slot), kx.parity);
+                k_in |= 1u << x;
                 if (alive)
-                    alive = c.wait(c.s_empty(x, st[x].slot), st[x].parity ^ 1u);
+                    alive = c.wait(c.s_empty(s), st.parity(x) ^ 1u);
                 if (alive) {
                     tc_fence_after();
-                    const uint64_t kd = kd0 + (((uint32_t)kslot[x] * Ring<D>::kSlot) >> 4);
+                    const uint64_t kd = kd0 + (((uint32_t)kx.slot * Ring<D>::kSlot) >> 4);
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
                         const uint32_t off = ((uint32_t)(i >> 2) * kHalfBytes + (uint32_t)(i & 3) * 32u) >> 4;
-                        umma_bf16(tmem + (uint32_t)(2 * x + st[x].slot) * 128u, kd + off, qd + off, idesc, i ? 1u : 0u);
+                        umma_bf16(tmem + (uint32_t)s * 128u, kd + off, qd + off, idesc, i ? 1u : 0u);
                     }
                 }
-                umma_commit(c.s_full(x, st[x].slot));
-                st[x].next(2);
+                umma_commit(c.s_full(s));
+                st.next(x);
+                if (k == w.end - 1)
+                    umma_commit(c.k_empty(kx.slot));
             }
         }
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-            if (w.block0[x] < INT32_MAX) {
-                if (alive && !k_in[x])       // a range that ends before the tile's first block
-                    alive = c.wait(c.k_full(kslot[x]), kpar[x]);
-                umma_commit(c.k_empty(kslot[x]));
+        kx = kt;
+#pragma unroll 1
+        for (int x = 0; x < tiles; ++x, kx.next(Ring<D>::kK))
+            if (!(k_in >> x & 1u)) {         // a range that ends before the tile's first block
+                if (alive)
+                    alive = c.wait(c.k_full(kx.slot), kx.parity);
+                umma_commit(c.k_empty(kx.slot));
             }
+        kt = kx;
     } while (walk_next(p, w));
     umma_commit(c.fin());
     mbar_drain_bounded(c.fin(), 0u);
 }
 
-// Waits for the columns of S that were asked for.
-__device__ __forceinline__ void landed(uint32_t (&r)[64])
+__device__ __forceinline__ float4 load_lse(uint32_t addr)
 {
-    // the operands keep the compiler from using a register before the wait
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 64; i += 16)
-        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
-                     "+r"(r[i + 6]), "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]),
-                     "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15]));
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
 }
 
-// The weights of columns c0 .. c0 + 15 into four partial sums, two values an
-// instruction where there is one for it.
+// The weights of 16 columns into partial sums, two values an instruction where
+// there is one for it; kMasked: of the columns [first, end) of them.
 template <bool kMasked>
-__device__ __forceinline__ void weigh16(const uint32_t *s, const float *lse, int c0, int rows, int first, float c,
-                                        float2 (&sum)[2])
+__device__ __forceinline__ void weigh16(const uint32_t *s, uint32_t lse, int first, int end, float c, float2 (&sum)[2])
 {
 #pragma unroll
     for (int j = 0; j < 16; j += 4) {
-        const float4 l = *reinterpret_cast<const float4 *>(lse + c0 + j);
+        const float4 l = load_lse(lse + 4u * j);
         float2 x0 = __ffma2_rn(make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), make_float2(c, c),
                                make_float2(l.x, l.y));
         float2 x1 = __ffma2_rn(make_float2(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])), make_float2(c, c),
                                make_float2(l.z, l.w));
         if (kMasked) {
-            const int i = c0 + j;
-            x0.x = i >= first && i < rows ? x0.x : -INFINITY;
-            x0.y = i + 1 >= first && i + 1 < rows ? x0.y : -INFINITY;
-            x1.x = i + 2 >= first && i + 2 < rows ? x1.x : -INFINITY;
-            x1.y = i + 3 >= first && i + 3 < rows ? x1.y : -INFINITY;
+            x0.x = j >= first && j < end ? x0.x : -INFINITY;
+            x0.y = j + 1 >= first && j + 1 < end ? x0.y : -INFINITY;
+            x1.x = j + 2 >= first && j + 2 < end ? x1.x : -INFINITY;
+            x1.y = j + 3 >= first && j + 3 < end ? x1.y : -INFINITY;
         }
         sum[0] = __fadd2_rn(sum[0], make_float2(ex2_approx(x0.x), ex2_approx(x0.y)));
         sum[1] = __fadd2_rn(sum[1], make_float2(ex2_approx(x1.x), ex2_approx(x1.y)));
     }
 }
 
-// Sum of a thread's weights over the columns [first, rows) of S at taddr.  The
-// columns that the MMA rounds rows up to are zero queries, whose product with an
-// infinite key is no number; `latest` is the warp's largest `first`.  S is in
-// registers half a buffer at a time; `empty` is arrived on as soon as all of it
-// is, so that the next product into the buffer runs beside the exponentials.
-__device__ __forceinline__ float weigh(uint32_t taddr, const float *lse, int rows, int first, int latest, float c,
+// A warp has read an S buffer to its end.
+__device__ __forceinline__ void leave(uint32_t empty)
+{
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(empty);
+}
+
+// Sum of a thread's weights over columns [first, n) of S at taddr, n <= 64;
+// `latest` is the warp's largest `first`.  The columns that the MMA rounds rows up
+// to are zero queries, whose product with an infinite key is no number, so they
+// are left out.  `last`: the buffer is arrived on as empty as soon as its values
+// are in registers, and the next product into it runs beside the exponentials.
+// (No use of a score can move before its wait: it needs a log-sum-exp that is read
+// after it.)
+__device__ __forceinline__ float weigh(uint32_t taddr, uint32_t lse, int n, int first, int latest, float c, bool last,
                                        uint32_t empty)
 {
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    uint32_t s[2][64];
-    tmem_ld32_nowait(taddr, s[0]);
-    if (rows > 32)
-        tmem_ld32_nowait(taddr + 32u, s[0] + 32);
-    landed(s[0]);
-    if (rows > 64)
-        tmem_ld32_nowait(taddr + 64u, s[1]);
-    if (rows > 96)
-        tmem_ld32_nowait(taddr + 96u, s[1] + 32);
+    if (n > 48 && latest <= 0) {             // nearly all blocks of a chunk: straight code
+        uint32_t s[64];
+        tmem_ld32_nowait(taddr, s);
+        tmem_ld32_nowait(taddr + 32u, s + 32);
+        tmem_wait_ld();
+        if (last)
+            leave(empty);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (h)
-            landed(s[1]);
-        if (h || rows <= 64) {
-            tc_fence_before();
-            __syncwarp();
-            if ((threadIdx.x & 31) == 0)
-                mbar_arrive(empty);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c0 = 64 * h + 16 * i;
-            if (c0 >= rows)
-                break;
-            if (c0 < latest || c0 + 16 > rows)
-                weigh16<true>(s[h] + 16 * i, lse, c0, rows, first, c, sum);
+        for (int i = 0; i < 3; ++i)
+            weigh16<false>(s + 16 * i, lse + 64u * i, 0, 16, c, sum);
+        if (n < 64)
+            weigh16<true>(s + 48, lse + 192u, 0, n - 48, c, sum);
+        else
+            weigh16<false>(s + 48, lse + 192u, 0, 16, c, sum);
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < n; i += 16) {
+            uint32_t s[16];
+            tmem_ld16_nowait(taddr + (uint32_t)i, s);
+            tmem_wait_ld();
+            if (i < latest || i + 16 > n)
+                weigh16<true>(s, lse + 4u * i, first - i, n - i, c, sum);
             else
-                weigh16<false>(s[h] + 16 * i, lse, c0, rows, first, c, sum);
+                weigh16<false>(s, lse + 4u * i, 0, 16, c, sum);
         }
-        if (rows <= 64)
-            break;
+        if (last)
+            leave(empty);
     }
     return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
@@ -424,25 +465,25 @@ __device__ __forceinline__ float weigh(uint32_t taddr, const float *lse, int row
 template <int D>
 __device__ void add_up(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int x)
 {
-    const int lane = threadIdx.x & 31;
-    const uint32_t taddr = tmem + (uint32_t)x * 256u + ((uint32_t)(threadIdx.x & 96) << 16);
+    const int lane = threadIdx.x & 31, row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;
     Walk w;
-    Turn qt, st;
+    Turn qt;
+    SRing st(p.span);
     bool alive = true, rows_in = false;
     if (!walk_first(p, w))
         return;
     do {
-        const int t = w.t0 + x * kMassTile + (threadIdx.x & 127);
-        const bool whole = w.begin == w.block0[0] && w.end == p.blocks;
-        const int64_t at = w.b * p.mass.in_request + w.g * p.mass.in_head + t;
-        float old = 0.f;
+        const bool whole = w.whole(p), mine = x < p.span && w.t0 + x * kMassTile < w.L;
+        const int t = w.t0 + x * kMassTile + row;
+        float old = 0.f, sum = 0.f;
         bool inside = false;
-        if (t < w.L) {
+        if (mine && t < w.L) {
             inside = (uint32_t)__ldg(p.block_table + (int64_t)w.b * p.max_pages + t / p.page_size) < (uint32_t)p.num_pages;
             if (whole && p.mass.in)
-                old = p.mass.in[at];
+                old = p.mass.in[w.b * p.mass.in_request + w.g * p.mass.in_head + t];
         }
-        float sum = 0.f;
+#pragma unroll 1
         for (int k = w.begin; k < w.end; ++k) {
             if (new_rows(p, w)) {
                 if (rows_in) {
@@ -455,36 +496,223 @@ __device__ void add_up(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int 
                 if (alive)
                     alive = c.wait(c.q_full(qt.slot), qt.parity);
             }
-            if (k < w.block0[x])
+            if (!mine || !w.sees(p, k, x))
                 continue;
-            if (alive)
-                alive = c.wait(c.s_full(x, st.slot), st.parity);
-            alive = __all_sync(0xffffffffu, alive);
             const int i0 = k * p.tpt, rows = min(p.tpt, p.n_q - i0) * p.group;
+            const int s = st.buffer(x);
+            if (alive)
+                alive = c.wait(c.s_full(s), st.parity(x));
+            alive = __all_sync(0xffffffffu, alive);
             if (alive) {
                 tc_fence_after();
                 // query tokens before t - past do not see the thread's token
-                const int first = t - w.past - i0, latest = first + 31 - lane;
-                sum += weigh(taddr + (uint32_t)st.slot * 128u, c.lse(qt.slot), rows, first * p.group, latest * p.group,
-                             p.scale_log2, c.s_empty(x, st.slot));
+                const int first = (t - w.past - i0) * p.group, latest = first + (31 - lane) * p.group;
+                const uint32_t taddr = tmem + lanes + (uint32_t)s * 128u;
+#pragma unroll 1
+                for (int h = 0; h < rows; h += 64)
+                    sum += weigh(taddr + (uint32_t)h, c.lse(qt.slot) + 4u * h, min(64, rows - h), first - h, latest - h,
+                                 p.scale_log2, h + 64 >= rows, c.s_empty(s));
             } else if (lane == 0) {
-                mbar_arrive(c.s_empty(x, st.slot));
+                mbar_arrive(c.s_empty(s));
             }
-            st.next(2);
+            st.next(x);
         }
+        if (!mine || t >= w.L)
+            continue;
         if (!inside)
             sum = 0.f;
-        if (!whole) {
-            // of a range's cut items the first has its end cut off or both, the last its beginning left
-            const int i = 2 * blockIdx.x + (w.item != p.cut_item[blockIdx.x] || p.cut_block[blockIdx.x] == 0);
-            p.pieces[(int64_t)i * kMassItem + threadIdx.x] = sum;
-        } else if (t < w.L) {
-            p.mass.out[w.b * p.mass.out_request + w.g * p.mass.out_head + t] = p.mass.in ? fmaf(p.decay, old, sum) : sum;
+        if (!whole)
+            p.pieces[(int64_t)piece_of(p, w) * (kMassSpan * kMassTile) + t - w.t0] = sum;
+        else
+            p.mass.out[w.b * p.mass.out_request + w.g * p.mass.out_head + t] =
+                p.mass.in ? fmaf(p.decay, old, sum) : sum;
+    } while (walk_next(p, w));
+}
+
+// ---------------------------------------------------------------------------
+// many blocks: K in TMEM
+// ---------------------------------------------------------------------------
+constexpr uint32_t kStreamS = 256u;          // first column of the two S buffers; tile x's K is at 64 x
+
+template <int D>
+__device__ void issue_stream(const MassParams &p, const Ctx<D> &c, uint32_t tmem)
+{
+    const uint64_t qd0 = umma_sdesc_sw128(c.q_slot(0), 16u, 1024u);
+    Walk w;
+    Turn qt;
+    uint32_t s_use = 0u, k_use = 0u;         // parities of the S buffers' and the tiles' next use
+    bool alive = true, rows_in = false;
+    if (!walk_first(p, w))
+        return;
+    do {
+        const int tiles = min(p.span, (w.L - w.t0 + kMassTile - 1) / kMassTile);
+        uint32_t k_in = 0u;                  // tiles whose K has been waited for
+#pragma unroll 1
+        for (int k = w.begin; k < w.end; ++k) {
+            if (rows_in) {
+                umma_commit(c.q_empty(qt.slot));
+                qt.next(Ring<D>::kQ);
+            }
+            rows_in = true;
+            if (alive)
+                alive = c.wait(c.q_full(qt.slot), qt.parity);
+            const int rows = min(p.tpt, p.n_q - k * p.tpt) * p.group;
+            const uint32_t idesc = umma_idesc_bf16(kMassTile, (rows + 15) & ~15, false, false);
+            const uint64_t qd = qd0 + (((uint32_t)qt.slot * Ring<D>::kSlot) >> 4);
+#pragma unroll 1
+            for (int x = 0; x < tiles; ++x) {
+                if (!w.sees(p, k, x))
+                    continue;
+                const int s = x & 1;
+                if (alive && !(k_in >> x & 1u))
+                    alive = c.wait(c.k_in_tmem(x), k_use >> x & 1u);
+                k_in |= 1u << x;
+                if (alive)
+                    alive = c.wait(c.s_empty(s), (s_use >> s & 1u) ^ 1u);
+                if (alive) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint32_t off = ((uint32_t)(i >> 2) * kHalfBytes + (uint32_t)(i & 3) * 32u) >> 4;
+                        umma_bf16_ts(tmem + kStreamS + (uint32_t)s * 128u, tmem + (uint32_t)(x * 64 + i * 8), qd + off,
+                                     idesc, i ? 1u : 0u);
+                    }
+                }
+                umma_commit(c.s_full(s));
+                s_use ^= 1u << s;
+            }
+        }
+        for (int x = 0; x < tiles; ++x)      // a range that ends before the tile's first block
+            if (alive && !(k_in >> x & 1u))
+                alive = c.wait(c.k_in_tmem(x), k_use >> x & 1u);
+        k_use ^= (1u << tiles) - 1u;
+    } while (walk_next(p, w));
+    umma_commit(c.fin());
+    mbar_drain_bounded(c.fin(), 0u);
+}
+
+// K of an item's tiles into TMEM, a tile of four warps each; the weights of the
+// even tiles by warps 0-7, of the odd ones by warps 8-15, each four warps of
+// them taking half of the columns; the halves joined, the masses.
+template <int D>
+__device__ void add_up_stream(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int four)
+{
+    const int lane = threadIdx.x & 31, row = threadIdx.x & 127, odd = four / 2, half = four % 2;
+    const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;
+    // this warp's columns of its S buffer; and the barrier of the two warps of the same tokens
+    const uint32_t s_mine = tmem + kStreamS + lanes + (uint32_t)(128 * odd + 64 * half);
+    const uint32_t pair_bar = 1u + (uint32_t)(4 * odd + row / 32);
+    Walk w;
+    Turn kt, qt;
+    uint32_t s_par = 0u;
+    bool alive = true, rows_in = false;
+    if (!walk_first(p, w))
+        return;
+    do {
+        const int tiles = min(p.span, (w.L - w.t0 + kMassTile - 1) / kMassTile);
+        // every product that read the tile's last K is done: the warps of its parity
+        // have waited for all of them
+#pragma unroll 1
+        for (int x = 0; x < tiles; ++x, kt.next(Ring<D>::kK)) {
+            if (x != 2 * half + odd)
+                continue;
+            if (alive)
+                alive = c.wait(c.k_full(kt.slot), kt.parity);
+            alive = __all_sync(0xffffffffu, alive);
+            if (alive) {
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h) {
+                    uint32_t v[32];
+                    const uint32_t src = c.k_slot(kt.slot) + (uint32_t)h * kHalfBytes + (uint32_t)row * 128u;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 f = load_lse(src + (uint32_t)((i ^ (row & 7)) << 4));
+                        v[4 * i] = __float_as_uint(f.x), v[4 * i + 1] = __float_as_uint(f.y);
+                        v[4 * i + 2] = __float_as_uint(f.z), v[4 * i + 3] = __float_as_uint(f.w);
+                    }
+                    tmem_st32(tmem + lanes + (uint32_t)(x * 64 + h * 32), v);
+                }
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(c.k_in_tmem(x));
+                mbar_arrive(c.k_empty(kt.slot));
+            }
+        }
+        float sum[2] = {0.f, 0.f};           // tiles odd and odd + 2
+#pragma unroll 1
+        for (int k = w.begin; k < w.end; ++k) {
+            if (rows_in) {
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(c.q_empty(qt.slot));
+                qt.next(Ring<D>::kQ);
+            }
+            rows_in = true;
+            if (alive)
+                alive = c.wait(c.q_full(qt.slot), qt.parity);
+            const int i0 = k * p.tpt, n = min(min(p.tpt, p.n_q - i0) * p.group - 64 * half, 64);
+#pragma unroll 1
+            for (int x = odd; x < tiles; x += 2) {
+                if (!w.sees(p, k, x))
+                    break;
+                if (alive)
+                    alive = c.wait(c.s_full(odd), s_par);
+                alive = __all_sync(0xffffffffu, alive);
+                if (alive) {
+                    tc_fence_after();
+                    // query tokens before t - past do not see token t
+                    const int first = (w.t0 + x * kMassTile + row - w.past - i0) * p.group - 64 * half;
+                    const float v = weigh(s_mine, c.lse(qt.slot) + 256u * half, n, first, first + (31 - lane) * p.group,
+                                          p.scale_log2, true, c.s_empty(odd));
+                    sum[0] += x < 2 ? v : 0.f;
+                    sum[1] += x < 2 ? 0.f : v;
+                } else if (lane == 0) {
+                    mbar_arrive(c.s_empty(odd));
+                }
+                s_par ^= 1u;
+            }
+        }
+        // the upper half's sums by way of its own columns of S, which no product
+        // writes before the next item's K is in TMEM
+        if (half) {
+            uint32_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = __float_as_uint(sum[i & 1]);
+            tmem_st8_nowait(s_mine, v);
+            tmem_wait_st();
+            tc_fence_before();
+        }
+        named_barrier(pair_bar, 64u);
+        if (half == 0) {
+            uint32_t v[8];
+            tc_fence_after();
+            tmem_ld8_nowait(s_mine + 64u, v);
+            tmem_wait_ld();
+            tc_fence_before();
+            const bool whole = w.whole(p);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int x = 2 * i + odd, t = w.t0 + x * kMassTile + row;
+                if (x >= tiles || t >= w.L)
+                    continue;
+                const bool inside = (uint32_t)__ldg(p.block_table + (int64_t)w.b * p.max_pages + t / p.page_size) <
+                                    (uint32_t)p.num_pages;
+                const float total = inside ? sum[i] + __uint_as_float(v[i]) : 0.f;
+                if (!whole)
+                    p.pieces[(int64_t)piece_of(p, w) * (kMassSpan * kMassTile) + t - w.t0] = total;
+                else
+                    p.mass.out[w.b * p.mass.out_request + w.g * p.mass.out_head + t] =
+                        p.mass.in ? fmaf(p.decay, p.mass.in[w.b * p.mass.in_request + w.g * p.mass.in_head + t], total)
+                                  : total;
+            }
         }
     } while (walk_next(p, w));
 }
 
-template <int D>
+template <int D, bool kStream>
 __global__ void __launch_bounds__(kThreads, 1)
     shkv_mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
                      const __grid_constant__ MassParams p)
@@ -500,17 +728,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < Ring<D>::kK; ++s) {
             mbar_init(c.k_full(s), 1u);
-            mbar_init(c.k_empty(s), 1u);
+            mbar_init(c.k_empty(s), kStream ? 4u : 1u);   // the warps that take it to TMEM, or the MMAs
         }
         for (int s = 0; s < Ring<D>::kQ; ++s) {
             mbar_init(c.q_full(s), 1u);
-            mbar_init(c.q_empty(s), 9u);     // the MMAs and the eight warps that read the log-sum-exps
+            mbar_init(c.q_empty(s), 17u);    // the MMAs and the warps that read the log-sum-exps
         }
-        for (int x = 0; x < 2; ++x)
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(c.s_full(x, i), 1u);
-                mbar_init(c.s_empty(x, i), 4u);
-            }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(c.s_full(i), 1u);
+            mbar_init(c.s_empty(i), kStream ? 8u : 4u);
+            mbar_init(c.k_in_tmem(i), 4u);
+        }
         mbar_init(c.fin(), 1u);
         *c.abort_flag = 0u;
         fence_barrier_init();
@@ -535,9 +763,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     else if (warp == kQWarp)
         copy_q<D>(&tm_q, p, c);
     else if (warp == kMmaWarp) {
-        if ((threadIdx.x & 31) == 0)
-            issue<D>(p, c, tmem);
-    } else
+        if ((threadIdx.x & 31) == 0) {
+            if (kStream)
+                issue_stream<D>(p, c, tmem);
+            else
+                issue<D>(p, c, tmem);
+        }
+    } else if (kStream)
+        add_up_stream<D>(p, c, tmem, warp / 4);
+    else
         add_up<D>(p, c, tmem, warp / 4);
     tc_fence_before();
     __syncthreads();
@@ -548,24 +782,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Items that ranges cut: the sums of the pieces, in the order of the blocks.
 // CTA c looks at the cut before range c and does an item's first.
-__global__ void __launch_bounds__(kMassItem) shkv_mass_join_kernel(const __grid_constant__ MassParams p)
+__global__ void __launch_bounds__(kMassSpan *kMassTile) shkv_mass_join_kernel(const __grid_constant__ MassParams p)
 {
     pdl_wait_prior();
     pdl_launch_dependents();
-    const int c = blockIdx.x + 1, item = p.cut_item[c];
+    const int c = blockIdx.x + 1, item = p.cut_item[c], u = threadIdx.x;
     if (p.cut_block[c] == 0 || (p.cut_item[c - 1] == item && p.cut_block[c - 1] > 0))
         return;
-    float sum = p.pieces[(int64_t)(2 * (c - 1) + 1) * kMassItem + threadIdx.x];
+    int b = 0, hi = p.batch;
+    while (hi - b > 1) {
+        const int mid = (b + hi) >> 1;
+        if (p.item0[mid] <= item)
+            b = mid;
+        else
+            hi = mid;
+    }
+    const int tokens = p.span * kMassTile, items = (p.lens[b] + tokens - 1) / tokens;
+    const int g = (item - p.item0[b]) / items, t = (item - p.item0[b]) % items * tokens + u;
+    if (u >= tokens || t >= p.lens[b])
+        return;
+    float sum = p.pieces[(int64_t)(2 * (c - 1) + 1) * (kMassSpan * kMassTile) + u];
     for (int i = c; i < p.num_ctas && p.cut_item[i] == item; ++i)
-        sum += p.pieces[(int64_t)(2 * i) * kMassItem + threadIdx.x];
-    int b = 0;
-    while (p.item0[b + 1] <= item)
-        ++b;
-    const int pairs = (p.lens[b] + kMassItem - 1) / kMassItem;
-    const int g = (item - p.item0[b]) / pairs, t = (item - p.item0[b]) % pairs * kMassItem + threadIdx.x;
-    if (t < p.lens[b])
-        p.mass.out[b * p.mass.out_request + g * p.mass.out_head + t] =
-            p.mass.in ? fmaf(p.decay, p.mass.in[b * p.mass.in_request + g * p.mass.in_head + t], sum) : sum;
+        sum += p.pieces[(int64_t)(2 * i) * (kMassSpan * kMassTile) + u];
+    p.mass.out[b * p.mass.out_request + g * p.mass.out_head + t] =
+        p.mass.in ? fmaf(p.decay, p.mass.in[b * p.mass.in_request + g * p.mass.in_head + t], sum) : sum;
 }
 
 }  // namespace
@@ -574,13 +814,15 @@ __global__ void __launch_bounds__(kMassItem) shkv_mass_join_kernel(const __grid_
 cudaError_t launch_mass(const CUtensorMap &tm_k, const CUtensorMap &tm_q, const MassParams &p, bool pieces,
                         cudaStream_t stream)
 {
-    auto kern = p.head_dim == 64 ? shkv_mass_kernel<64> : shkv_mass_kernel<128>;
+    const bool many = p.blocks >= kMassStream;
+    auto kern = p.head_dim == 64 ? (many ? shkv_mass_kernel<64, true> : shkv_mass_kernel<64, false>)
+                                 : (many ? shkv_mass_kernel<128, true> : shkv_mass_kernel<128, false>);
     const uint32_t smem = p.head_dim == 64 ? Ring<64>::kBytes : Ring<128>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess)
         e = launch_pdl(kern, p.num_ctas, kThreads, smem, stream, tm_k, tm_q, p);
     if (e == cudaSuccess && pieces)
-        e = launch_pdl(shkv_mass_join_kernel, p.num_ctas - 1, kMassItem, 0u, stream, p);
+        e = launch_pdl(shkv_mass_join_kernel, p.num_ctas - 1, kMassSpan * kMassTile, 0u, stream, p);
     return e;
 }
 

@@ -93,17 +93,6 @@ __device__ __forceinline__ float max3f(float a, float b, float c)
     return y;
 }
 
-// D[tmem] (+)= A[tmem] . B[smem]^T, issued by one thread: A is 128 lanes
-// (rows) x K columns of packed bf16 pairs, the lower half the lower k.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_taddr, uint32_t a_taddr, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate)
-{
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_taddr),
-                 "r"(a_taddr), "l"(b_desc), "r"(idesc), "r"(accumulate)
-                 : "memory");
-}
-
 // Bounded wait that sleeps on the barrier instead of spinning: each try_wait
 // suspends the thread until the phase completes or ~20 us pass, so waiting
 // warps leave the issue slots to the softmax warps of their SM sub-partition.

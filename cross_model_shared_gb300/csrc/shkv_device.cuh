@@ -473,6 +473,17 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_taddr, uint64_t a_desc, uin
                  : "memory");
 }
 
+// D[tmem] (+)= A[tmem] . B[smem]^T, issued by one thread: A is 128 lanes
+// (rows) x K columns of packed bf16 pairs, the lower half the lower k.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_taddr, uint32_t a_taddr, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_taddr),
+                 "r"(a_taddr), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
 // Arrive on an mbarrier once every tcgen05.mma this thread issued so far has completed.
 __device__ __forceinline__ void umma_commit(uint32_t bar)
 {
