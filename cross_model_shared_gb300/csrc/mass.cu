@@ -17,7 +17,8 @@
 // 32 KB feeds up to four MMAs of 128 x 128 x D).
 //
 // Warps 0-15 take the weights, warp 16 copies K, warp 17 Q (and the log-sum-exps),
-// one lane of warp 18 issues the MMAs, in one of two ways:
+// warps 18 and 19 issue the MMAs of an item's even and odd tiles (one issuer alone
+// needs 1150 cycles a product, twice the product's time), in one of two ways:
 //
 // * few blocks (a decode step, a short window): both operands from shared memory,
 //   four warps a tile of an item, four S buffers.  Bound by the bytes of K.
@@ -40,7 +41,7 @@ namespace shkv {
 
 namespace {
 
-constexpr int kThreads = 608;
+constexpr int kThreads = 640;
 constexpr int kKWarp = 16, kQWarp = 17, kMmaWarp = 18;
 constexpr uint32_t kTmemCols = 512;          // four S buffers of 128 columns
 constexpr uint32_t kHalfBytes = 128u * 128u; // 64 columns of 128 tokens or rows
@@ -52,7 +53,7 @@ struct Ring {
     static constexpr int kK = D == 128 ? 4 : 8, kQ = D == 128 ? 3 : 5;
     static constexpr uint32_t kSlot = (uint32_t)(D / 64) * kHalfBytes;
     // barriers: K full, K empty, Q full, Q empty, S full, S empty, K in TMEM, fin
-    static constexpr int kBars = 2 * kK + 2 * kQ + 13;
+    static constexpr int kBars = 2 * kK + 2 * kQ + 14;
     static constexpr uint32_t kQ0 = kK * kSlot, kLse = kQ0 + kQ * kSlot, kBar0 = kLse + kQ * kMassRows * 4,
                               kMisc = kBar0 + 8 * kBars, kBytes = kMisc + 16 + 1024;
 };
@@ -72,7 +73,7 @@ struct Ctx {
     __device__ uint32_t s_full(int i) const { return bar(2 * Ring<D>::kK + 2 * Ring<D>::kQ + i); }
     __device__ uint32_t s_empty(int i) const { return s_full(i) + 32u; }
     __device__ uint32_t k_in_tmem(int x) const { return s_full(x) + 64u; }
-    __device__ uint32_t fin() const { return s_full(0) + 96u; }
+    __device__ uint32_t fin(int odd) const { return s_full(0) + 96u + 8u * (uint32_t)odd; }
     __device__ uint32_t k_slot(int s) const { return base + (uint32_t)s * Ring<D>::kSlot; }
     __device__ uint32_t q_slot(int s) const { return base + Ring<D>::kQ0 + (uint32_t)s * Ring<D>::kSlot; }
     __device__ uint32_t lse(int s) const { return base + Ring<D>::kLse + (uint32_t)(s * kMassRows * 4); }
@@ -89,6 +90,25 @@ struct Turn {
             slot = 0;
             parity ^= 1u;
         }
+    }
+};
+
+// A ring of n slots dealt to the tiles of an item: tile x uses x, x + span, ... in
+// turn, whatever the other tiles do.  So a slot is waited for by the same role every
+// time, in order: with slots handed round in one ring, an item of fewer tiles would
+// shift them, and a role that runs ahead could wait for a phase while the one before
+// is still open, which a parity wait takes for the phase before that.  Four bits a
+// tile count its uses, modulo twice its slots.
+struct TileRing {
+    uint32_t counts = 0u;
+    int span, log2n;
+    __device__ TileRing(int span_, int n) : span(span_), log2n(n >= 8 * span_ ? 3 : n >= 4 * span_ ? 2 : n >= 2 * span_) {}
+    __device__ int slot(int x) const { return x + span * (int)(counts >> 4 * x & ((1u << log2n) - 1u)); }
+    __device__ uint32_t parity(int x) const { return counts >> (4 * x + log2n) & 1u; }
+    __device__ void next(int x)
+    {
+        const uint32_t n = ((counts >> 4 * x & 15u) + 1u) & ((2u << log2n) - 1u);
+        counts = (counts & ~(15u << 4 * x)) | n << 4 * x;
     }
 };
 
@@ -191,9 +211,10 @@ __device__ void copy_k(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
         return lane < p.span * RB && pg * P < w.L ? __ldg(p.block_table + (int64_t)w.b * p.max_pages + pg) : -1;
     };
     Walk w;
-    Turn turn;
+    TileRing kt(p.span, Ring<D>::kK);
     bool alive = true, more = walk_first(p, w);
-    int issued = 0, id = more ? entry(w) : -1;
+    uint32_t armed = 0u, armed_parity = 0u;  // slots with a copy, and of which phase
+    int id = more ? entry(w) : -1;
     while (more) {
         Walk next = w;
         more = walk_next(p, next);
@@ -208,27 +229,30 @@ __device__ void copy_k(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
             if (there && !inside)
                 atomicOr(p.err, SHKV_ERRF_PAGE_OOB);
             const uint32_t mask = __ballot_sync(0xffffffffu, inside);
+            const int slot = kt.slot(x);
             bool ok = true;
             if (alive && lane == 0) {
-                ok = c.wait(c.k_empty(turn.slot), turn.parity ^ 1u);
+                ok = c.wait(c.k_empty(slot), kt.parity(x) ^ 1u);
                 if (ok)
-                    mbar_arrive_expect_tx(c.k_full(turn.slot), (uint32_t)__popc(mask) * (uint32_t)P * 128u);
+                    mbar_arrive_expect_tx(c.k_full(slot), (uint32_t)__popc(mask) * (uint32_t)P * 128u);
             }
             alive = __all_sync(0xffffffffu, alive && ok);
             if (!alive)
                 continue;
             if (inside)
-                tma_load_2d(c.k_slot(turn.slot) + (uint32_t)half * kHalfBytes + (uint32_t)(rb * P) * 128u, tm, half * 64,
-                            (page * p.hkv + w.g) * P, c.k_full(turn.slot), pol);
-            ++issued;
-            turn.next(Ring<D>::kK);
+                tma_load_2d(c.k_slot(slot) + (uint32_t)half * kHalfBytes + (uint32_t)(rb * P) * 128u, tm, half * 64,
+                            (page * p.hkv + w.g) * P, c.k_full(slot), pol);
+            armed |= 1u << slot;
+            armed_parity = (armed_parity & ~(1u << slot)) | kt.parity(x) << slot;
+            kt.next(x);
         }
         w = next;
         id = next_id;
     }
     if (!alive && lane == 0)                 // wait for the copies in flight
-        for (int i = max(0, issued - Ring<D>::kK); i < issued; ++i)
-            mbar_drain_bounded(c.k_full(i % Ring<D>::kK), (uint32_t)(i / Ring<D>::kK) & 1u);
+        for (int s = 0; s < Ring<D>::kK; ++s)
+            if (armed >> s & 1u)
+                mbar_drain_bounded(c.k_full(s), armed_parity >> s & 1u);
 }
 
 // Q blocks and what their rows' log-sum-exps take off the scores; a row beyond
@@ -294,93 +318,89 @@ __device__ void copy_q(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
             mbar_drain_bounded(c.q_full(i % Ring<D>::kQ), (uint32_t)(i / Ring<D>::kQ) & 1u);
 }
 
-// Which of the S buffers x, x + span, .. a tile's next product goes to: four bits
-// a tile count the products, modulo twice the tile's buffers.
-struct SRing {
-    uint32_t counts = 0u;
-    int span, log2n;                         // 4 / span buffers a tile
-    __device__ explicit SRing(int span_) : span(span_), log2n(span_ == 4 ? 0 : span_ == 2 ? 1 : 2) {}
-    __device__ int buffer(int x) const { return x + span * (int)(counts >> 4 * x & ((1u << log2n) - 1u)); }
-    __device__ uint32_t parity(int x) const { return counts >> (4 * x + log2n) & 1u; }
-    __device__ void next(int x)
-    {
-        const uint32_t n = (counts >> 4 * x & 15u) + 1u & (2u << log2n) - 1u;
-        counts = (counts & ~(15u << 4 * x)) | n << 4 * x;
-    }
-};
-
-// S = K Q^T for every (block, tile) of the range.  A slot of K is free after the
-// item's last block, one of Q when the next block's rows are needed.  (Loops are
-// kept rolled: the roles of an SM sub-partition share its instruction cache.)
+// The issuers' warps run converged, so that addresses and descriptors stay in
+// uniform registers; one lane issues.
 template <int D>
-__device__ void issue(const MassParams &p, const Ctx<D> &c, uint32_t tmem)
+__device__ __forceinline__ bool issuer_wait(const Ctx<D> &c, uint32_t bar, uint32_t parity, bool alive)
+{
+    return __all_sync(0xffffffffu, alive && c.wait(bar, parity));
+}
+
+// S = K Q^T for every block of the range and every tile of one parity.  A slot of K
+// is free after the item's last block, one of Q when the next block's rows are
+// needed.  (Loops are kept rolled: the roles of an SM sub-partition share its
+// instruction cache.)
+template <int D>
+__device__ void issue(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int odd)
 {
     const uint64_t kd0 = umma_sdesc_sw128(c.k_slot(0), 16u, 1024u), qd0 = umma_sdesc_sw128(c.q_slot(0), 16u, 1024u);
+    const bool one = (threadIdx.x & 31) == 0;
     Walk w;
-    Turn kt, qt;
-    SRing st(p.span);
+    Turn qt;
+    TileRing kt(p.span, Ring<D>::kK), st(p.span, 4);
     bool alive = true, rows_in = false;
     if (!walk_first(p, w))
         return;
     do {
         const int tiles = min(p.span, (w.L - w.t0 + kMassTile - 1) / kMassTile);
         uint32_t k_in = 0u;                  // tiles whose K has been waited for
-        Turn kx;
 #pragma unroll 1
         for (int k = w.begin; k < w.end; ++k) {
             if (new_rows(p, w)) {
                 if (rows_in) {
-                    umma_commit(c.q_empty(qt.slot));
+                    if (one)
+                        umma_commit(c.q_empty(qt.slot));
                     qt.next(Ring<D>::kQ);
                 }
                 rows_in = true;
-                if (alive)
-                    alive = c.wait(c.q_full(qt.slot), qt.parity);
+                alive = issuer_wait(c, c.q_full(qt.slot), qt.parity, alive);
             }
             const int rows = min(p.tpt, p.n_q - k * p.tpt) * p.group;
             const uint32_t idesc = umma_idesc_bf16(kMassTile, (rows + 15) & ~15, false, false);
             const uint64_t qd = qd0 + (((uint32_t)qt.slot * Ring<D>::kSlot) >> 4);
-            kx = kt;
 #pragma unroll 1
-            for (int x = 0; x < tiles; ++x, kx.next(Ring<D>::kK)) {
+            for (int x = odd; x < tiles; x += 2) {
                 if (!w.sees(p, k, x))
-                    continue;
-                const int s = st.buffer(x);
-                if (alive && !(k_in >> x & 1u))
-                    alive = c.wait(c.k_full(kx.slot), kx.parity);
+                    break;
+                const int s = st.slot(x), slot = kt.slot(x);
+                if (!(k_in >> x & 1u))
+                    alive = issuer_wait(c, c.k_full(slot), kt.parity(x), alive);
                 k_in |= 1u << x;
-                if (alive)
-                    alive = c.wait(c.s_empty(s), st.parity(x) ^ 1u);
-                if (alive) {
-                    tc_fence_after();
-                    const uint64_t kd = kd0 + (((uint32_t)kx.slot * Ring<D>::kSlot) >> 4);
+                alive = issuer_wait(c, c.s_empty(s), st.parity(x) ^ 1u, alive);
+                tc_fence_after();
+                const uint64_t kd = kd0 + (((uint32_t)slot * Ring<D>::kSlot) >> 4);
+                if (one) {
+                    if (alive) {
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        const uint32_t off = ((uint32_t)(i >> 2) * kHalfBytes + (uint32_t)(i & 3) * 32u) >> 4;
-                        umma_bf16(tmem + (uint32_t)s * 128u, kd + off, qd + off, idesc, i ? 1u : 0u);
+                        for (int i = 0; i < D / 16; ++i) {
+                            const uint32_t off = ((uint32_t)(i >> 2) * kHalfBytes + (uint32_t)(i & 3) * 32u) >> 4;
+                            umma_bf16(tmem + (uint32_t)s * 128u, kd + off, qd + off, idesc, i ? 1u : 0u);
+                        }
                     }
+                    umma_commit(c.s_full(s));
+                    if (k == w.end - 1)
+                        umma_commit(c.k_empty(slot));
                 }
-                umma_commit(c.s_full(s));
+                __syncwarp();
                 st.next(x);
-                if (k == w.end - 1)
-                    umma_commit(c.k_empty(kx.slot));
             }
         }
-        kx = kt;
-#pragma unroll 1
-        for (int x = 0; x < tiles; ++x, kx.next(Ring<D>::kK))
+        for (int x = odd; x < tiles; x += 2) {
             if (!(k_in >> x & 1u)) {         // a range that ends before the tile's first block
-                if (alive)
-                    alive = c.wait(c.k_full(kx.slot), kx.parity);
-                umma_commit(c.k_empty(kx.slot));
+                alive = issuer_wait(c, c.k_full(kt.slot(x)), kt.parity(x), alive);
+                if (one)
+                    umma_commit(c.k_empty(kt.slot(x)));
             }
-        kt = kx;
+            kt.next(x);
+        }
     } while (walk_next(p, w));
-    umma_commit(c.fin());
-    mbar_drain_bounded(c.fin(), 0u);
+    if (one) {
+        umma_commit(c.fin(odd));
+        mbar_drain_bounded(c.fin(odd), 0u);
+    }
 }
 
-__device__ __forceinline__ float4 load_lse(uint32_t addr)
+__device__ __forceinline__ float4 load_shared4(uint32_t addr)
 {
     float4 v;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
@@ -394,7 +414,7 @@ __device__ __forceinline__ void weigh16(const uint32_t *s, uint32_t lse, int fir
 {
 #pragma unroll
     for (int j = 0; j < 16; j += 4) {
-        const float4 l = load_lse(lse + 4u * j);
+        const float4 l = load_shared4(lse + 4u * j);
         float2 x0 = __ffma2_rn(make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), make_float2(c, c),
                                make_float2(l.x, l.y));
         float2 x1 = __ffma2_rn(make_float2(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])), make_float2(c, c),
@@ -469,7 +489,7 @@ __device__ void add_up(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int 
     const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;
     Walk w;
     Turn qt;
-    SRing st(p.span);
+    TileRing st(p.span, 4);
     bool alive = true, rows_in = false;
     if (!walk_first(p, w))
         return;
@@ -499,7 +519,7 @@ __device__ void add_up(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int 
             if (!mine || !w.sees(p, k, x))
                 continue;
             const int i0 = k * p.tpt, rows = min(p.tpt, p.n_q - i0) * p.group;
-            const int s = st.buffer(x);
+            const int s = st.slot(x);
             if (alive)
                 alive = c.wait(c.s_full(s), st.parity(x));
             alive = __all_sync(0xffffffffu, alive);
@@ -535,12 +555,14 @@ __device__ void add_up(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int 
 constexpr uint32_t kStreamS = 256u;          // first column of the two S buffers; tile x's K is at 64 x
 
 template <int D>
-__device__ void issue_stream(const MassParams &p, const Ctx<D> &c, uint32_t tmem)
+__device__ void issue_stream(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int odd)
 {
     const uint64_t qd0 = umma_sdesc_sw128(c.q_slot(0), 16u, 1024u);
+    const uint32_t d = tmem + kStreamS + (uint32_t)odd * 128u, empty = c.s_empty(odd), full = c.s_full(odd);
+    const bool one = (threadIdx.x & 31) == 0;
     Walk w;
     Turn qt;
-    uint32_t s_use = 0u, k_use = 0u;         // parities of the S buffers' and the tiles' next use
+    uint32_t s_par = 1u, k_par = 0u;         // of the S buffer's next wait; of the tiles' (odd, odd + 2), a bit each
     bool alive = true, rows_in = false;
     if (!walk_first(p, w))
         return;
@@ -550,45 +572,48 @@ __device__ void issue_stream(const MassParams &p, const Ctx<D> &c, uint32_t tmem
 #pragma unroll 1
         for (int k = w.begin; k < w.end; ++k) {
             if (rows_in) {
-                umma_commit(c.q_empty(qt.slot));
+                if (one)
+                    umma_commit(c.q_empty(qt.slot));
                 qt.next(Ring<D>::kQ);
             }
             rows_in = true;
-            if (alive)
-                alive = c.wait(c.q_full(qt.slot), qt.parity);
             const int rows = min(p.tpt, p.n_q - k * p.tpt) * p.group;
             const uint32_t idesc = umma_idesc_bf16(kMassTile, (rows + 15) & ~15, false, false);
             const uint64_t qd = qd0 + (((uint32_t)qt.slot * Ring<D>::kSlot) >> 4);
+            alive = issuer_wait(c, c.q_full(qt.slot), qt.parity, alive);
 #pragma unroll 1
-            for (int x = 0; x < tiles; ++x) {
+            for (int x = odd; x < tiles; x += 2) {
                 if (!w.sees(p, k, x))
-                    continue;
-                const int s = x & 1;
-                if (alive && !(k_in >> x & 1u))
-                    alive = c.wait(c.k_in_tmem(x), k_use >> x & 1u);
+                    break;
+                const uint32_t a = tmem + (uint32_t)(x * 64);
+                if (!(k_in >> x & 1u))
+                    alive = issuer_wait(c, c.k_in_tmem(x), k_par >> x & 1u, alive);
                 k_in |= 1u << x;
-                if (alive)
-                    alive = c.wait(c.s_empty(s), (s_use >> s & 1u) ^ 1u);
-                if (alive) {
-                    tc_fence_after();
+                alive = issuer_wait(c, empty, s_par, alive);
+                tc_fence_after();
+                if (one) {
+                    if (alive) {
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        const uint32_t off = ((uint32_t)(i >> 2) * kHalfBytes + (uint32_t)(i & 3) * 32u) >> 4;
-                        umma_bf16_ts(tmem + kStreamS + (uint32_t)s * 128u, tmem + (uint32_t)(x * 64 + i * 8), qd + off,
-                                     idesc, i ? 1u : 0u);
+                        for (int i = 0; i < D / 16; ++i) {
+                            const uint32_t off = ((uint32_t)(i >> 2) * kHalfBytes + (uint32_t)(i & 3) * 32u) >> 4;
+                            umma_bf16_ts(d, a + (uint32_t)(i * 8), qd + off, idesc, i ? 1u : 0u);
+                        }
                     }
+                    umma_commit(full);
                 }
-                umma_commit(c.s_full(s));
-                s_use ^= 1u << s;
+                __syncwarp();
+                s_par ^= 1u;
             }
         }
-        for (int x = 0; x < tiles; ++x)      // a range that ends before the tile's first block
-            if (alive && !(k_in >> x & 1u))
-                alive = c.wait(c.k_in_tmem(x), k_use >> x & 1u);
-        k_use ^= (1u << tiles) - 1u;
+        for (int x = odd; x < tiles; x += 2) // a range that ends before the tile's first block
+            if (!(k_in >> x & 1u))
+                alive = issuer_wait(c, c.k_in_tmem(x), k_par >> x & 1u, alive);
+        k_par ^= (1u << tiles) - 1u;
     } while (walk_next(p, w));
-    umma_commit(c.fin());
-    mbar_drain_bounded(c.fin(), 0u);
+    if (one) {
+        umma_commit(c.fin(odd));
+        mbar_drain_bounded(c.fin(odd), 0u);
+    }
 }
 
 // K of an item's tiles into TMEM, a tile of four warps each; the weights of the
@@ -603,7 +628,9 @@ __device__ void add_up_stream(const MassParams &p, const Ctx<D> &c, uint32_t tme
     const uint32_t s_mine = tmem + kStreamS + lanes + (uint32_t)(128 * odd + 64 * half);
     const uint32_t pair_bar = 1u + (uint32_t)(4 * odd + row / 32);
     Walk w;
-    Turn kt, qt;
+    Turn qt;
+    TileRing kt(p.span, Ring<D>::kK);
+    const int own = 2 * half + odd;          // the tile that this warp takes to TMEM
     uint32_t s_par = 0u;
     bool alive = true, rows_in = false;
     if (!walk_first(p, w))
@@ -612,33 +639,32 @@ __device__ void add_up_stream(const MassParams &p, const Ctx<D> &c, uint32_t tme
         const int tiles = min(p.span, (w.L - w.t0 + kMassTile - 1) / kMassTile);
         // every product that read the tile's last K is done: the warps of its parity
         // have waited for all of them
-#pragma unroll 1
-        for (int x = 0; x < tiles; ++x, kt.next(Ring<D>::kK)) {
-            if (x != 2 * half + odd)
-                continue;
+        if (own < tiles) {
+            const int slot = kt.slot(own);
             if (alive)
-                alive = c.wait(c.k_full(kt.slot), kt.parity);
+                alive = c.wait(c.k_full(slot), kt.parity(own));
             alive = __all_sync(0xffffffffu, alive);
             if (alive) {
 #pragma unroll
                 for (int h = 0; h < D / 64; ++h) {
                     uint32_t v[32];
-                    const uint32_t src = c.k_slot(kt.slot) + (uint32_t)h * kHalfBytes + (uint32_t)row * 128u;
+                    const uint32_t src = c.k_slot(slot) + (uint32_t)h * kHalfBytes + (uint32_t)row * 128u;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float4 f = load_lse(src + (uint32_t)((i ^ (row & 7)) << 4));
+                        const float4 f = load_shared4(src + (uint32_t)((i ^ (row & 7)) << 4));
                         v[4 * i] = __float_as_uint(f.x), v[4 * i + 1] = __float_as_uint(f.y);
                         v[4 * i + 2] = __float_as_uint(f.z), v[4 * i + 3] = __float_as_uint(f.w);
                     }
-                    tmem_st32(tmem + lanes + (uint32_t)(x * 64 + h * 32), v);
+                    tmem_st32(tmem + lanes + (uint32_t)(own * 64 + h * 32), v);
                 }
                 tc_fence_before();
             }
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(c.k_in_tmem(x));
-                mbar_arrive(c.k_empty(kt.slot));
+                mbar_arrive(c.k_in_tmem(own));
+                mbar_arrive(c.k_empty(slot));
             }
+            kt.next(own);
         }
         float sum[2] = {0.f, 0.f};           // tiles odd and odd + 2
 #pragma unroll 1
@@ -732,14 +758,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < Ring<D>::kQ; ++s) {
             mbar_init(c.q_full(s), 1u);
-            mbar_init(c.q_empty(s), 17u);    // the MMAs and the warps that read the log-sum-exps
+            mbar_init(c.q_empty(s), 18u);    // both issuers' MMAs and the warps that read the log-sum-exps
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(c.s_full(i), 1u);
             mbar_init(c.s_empty(i), kStream ? 8u : 4u);
             mbar_init(c.k_in_tmem(i), 4u);
         }
-        mbar_init(c.fin(), 1u);
+        mbar_init(c.fin(0), 1u);
+        mbar_init(c.fin(1), 1u);
         *c.abort_flag = 0u;
         fence_barrier_init();
     }
@@ -762,13 +789,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         copy_k<D>(&tm_k, p, c);
     else if (warp == kQWarp)
         copy_q<D>(&tm_q, p, c);
-    else if (warp == kMmaWarp) {
-        if ((threadIdx.x & 31) == 0) {
-            if (kStream)
-                issue_stream<D>(p, c, tmem);
-            else
-                issue<D>(p, c, tmem);
-        }
+    else if (warp >= kMmaWarp) {
+        if (kStream)
+            issue_stream<D>(p, c, tmem, warp - kMmaWarp);
+        else
+            issue<D>(p, c, tmem, warp - kMmaWarp);
     } else if (kStream)
         add_up_stream<D>(p, c, tmem, warp / 4);
     else
