@@ -20,7 +20,9 @@ constexpr int kMassMaxCtas = 256;
 constexpr int kMassTile = 128;       // tokens of a tile: rows of an MMA
 constexpr int kMassSpan = 4;         // tiles of an item, at most
 constexpr int kMassRows = 128;       // query rows of a block, at most
-constexpr int kMassStream = 4;       // blocks from which an item's K goes to TMEM
+
+// Blocks of rows from which rows lie on the MMA's M dimension.
+inline bool mass_wide(int32_t blocks) { return blocks >= 4; }
 
 // A decode step or a chunk: row r = i * G + j of a (request, KV head g) is
 // query token i, head g * G + j.  Causal: query token i sits at position

@@ -175,10 +175,12 @@ bool plan_mass(MassParams &p, int limit)
     return cut;
 }
 
-// Tiles of an item: four share a block's rows, fewer where that leaves the CTAs
-// less than four (item, block) steps each.
+// Tiles of an item: two with many blocks; else four share a block's rows, fewer
+// where that leaves the CTAs less than four (item, block) steps each.
 int32_t item_span(int32_t batch, const int32_t *lens, int32_t hkv, int32_t blocks, int ctas)
 {
+    if (mass_wide(blocks))
+        return 2;
     int32_t span = kMassSpan;
     for (; span > 1; span /= 2) {
         int64_t items = 0;

@@ -8,26 +8,26 @@
 // so there is no running maximum and nothing to rescale: a weight is final as
 // soon as its score is there.
 //
-// Tokens lie on the MMA's M dimension, S[t, r] = K Q^T with M = 128 tokens and
-// N = up to 128 rows in a TMEM buffer, so that a thread owns a token (its TMEM
-// lane) and adds up its row of weights in a register, without a word between
-// threads: no atomics, the same bits every time.  K is read once per call; the
-// rows of a decode step stay in shared memory while a CTA walks along the tokens
-// of a head, those of a chunk stream past the K tiles of an item (a Q block of
-// 32 KB feeds up to four MMAs of 128 x 128 x D).
+// K is read once per call.  Nothing is added across threads but in a fixed order:
+// no atomics, the same bits every time.  Two ways:
+//
+// * Few blocks of rows (a decode step, a short window): tokens on the MMA's M
+//   dimension, S[t, r] = K Q^T with M = 128 tokens and N = up to 128 rows in one of
+//   four TMEM buffers.  A thread owns a token (its TMEM lane) and adds up its row of
+//   weights in a register.  The rows stay in shared memory while a CTA walks along
+//   the tokens of a head.  Bound by the bytes of K.
+// * Many blocks: rows on M, S[r, t] = Q K^T with N = the 256 tokens of an item, whose
+//   K stays while the blocks stream past.  A thread owns a row and 64 tokens, for
+//   which it adds up the weights of its row in every block in 64 registers; the
+//   threads' sums are joined at the item's end.  A row's log-sum-exp is one register
+//   then: with tokens on M every weight needs one from shared memory, and at 512
+//   cycles a product of 128 x 128 those reads alone take as long as the product
+//   (2048 new tokens of 40 heads behind 38k: 774 us).  Bound by the tensor cores and
+//   the exponentials alike, 512 cycles each.
 //
 // Warps 0-15 take the weights, warp 16 copies K, warp 17 Q (and the log-sum-exps),
-// warps 18 and 19 issue the MMAs of an item's even and odd tiles (one issuer alone
-// needs 1150 cycles a product, twice the product's time), in one of two ways:
-//
-// * few blocks (a decode step, a short window): both operands from shared memory,
-//   four warps a tile of an item, four S buffers.  Bound by the bytes of K.
-// * many blocks: at M = N = 128 two operands from shared memory take 120 of its 128
-//   bytes a cycle and leave none for the log-sum-exps, so an item's K goes from
-//   shared memory to TMEM (64 columns a tile) once, and two S buffers remain, one
-//   for the even tiles and one for the odd ones, each emptied into the registers
-//   of eight warps, 64 columns a thread, before the exponentials begin.  Bound by
-//   the tensor cores and the exponentials alike (512 cycles a product each).
+// warps 18 and 19 issue the MMAs: of the even and of the odd tiles with few blocks
+// (one issuer alone needs about 1150 cycles a product), warp 18 all with many.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -43,7 +43,10 @@ namespace {
 
 constexpr int kThreads = 640;
 constexpr int kKWarp = 16, kQWarp = 17, kMmaWarp = 18;
-constexpr uint32_t kTmemCols = 512;          // four S buffers of 128 columns
+constexpr uint32_t kTmemCols = 512;          // four S buffers of 128 columns, or two of 256
+// Registers a thread, many blocks (setmaxnreg): 104 * 512 + 64 * 128 = 96 * 640.
+constexpr uint32_t kLaunchRegs = 96, kWeightRegs = 104, kOtherRegs = 64;
+static_assert(kWeightRegs * 512 + kOtherRegs * 128 == kLaunchRegs * kThreads, "register split");
 constexpr uint32_t kHalfBytes = 128u * 128u; // 64 columns of 128 tokens or rows
 
 // Ring slots: at D = 128 seven of 32 KB fill shared memory (K four, a decode's
@@ -52,8 +55,8 @@ template <int D>
 struct Ring {
     static constexpr int kK = D == 128 ? 4 : 8, kQ = D == 128 ? 3 : 5;
     static constexpr uint32_t kSlot = (uint32_t)(D / 64) * kHalfBytes;
-    // barriers: K full, K empty, Q full, Q empty, S full, S empty, K in TMEM, fin
-    static constexpr int kBars = 2 * kK + 2 * kQ + 14;
+    // barriers: K full, K empty, Q full, Q empty, S full, S empty, fin
+    static constexpr int kBars = 2 * kK + 2 * kQ + 10;
     static constexpr uint32_t kQ0 = kK * kSlot, kLse = kQ0 + kQ * kSlot, kBar0 = kLse + kQ * kMassRows * 4,
                               kMisc = kBar0 + 8 * kBars, kBytes = kMisc + 16 + 1024;
 };
@@ -72,8 +75,7 @@ struct Ctx {
     __device__ uint32_t q_empty(int s) const { return bar(2 * Ring<D>::kK + Ring<D>::kQ + s); }
     __device__ uint32_t s_full(int i) const { return bar(2 * Ring<D>::kK + 2 * Ring<D>::kQ + i); }
     __device__ uint32_t s_empty(int i) const { return s_full(i) + 32u; }
-    __device__ uint32_t k_in_tmem(int x) const { return s_full(x) + 64u; }
-    __device__ uint32_t fin(int odd) const { return s_full(0) + 96u + 8u * (uint32_t)odd; }
+    __device__ uint32_t fin(int odd) const { return s_full(0) + 64u + 8u * (uint32_t)odd; }
     __device__ uint32_t k_slot(int s) const { return base + (uint32_t)s * Ring<D>::kSlot; }
     __device__ uint32_t q_slot(int s) const { return base + Ring<D>::kQ0 + (uint32_t)s * Ring<D>::kSlot; }
     __device__ uint32_t lse(int s) const { return base + Ring<D>::kLse + (uint32_t)(s * kMassRows * 4); }
@@ -277,17 +279,22 @@ __device__ void copy_q(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
     do {
         if (!new_rows(p, w))
             continue;
+        const float *src = p.lse + w.b * p.lse_request + w.g * p.group;
+        float ahead[kMassRows / 32];         // of the next block
+        auto load = [&](int k) {
+            const int i0 = k * p.tpt, rows = k < w.end ? min(p.tpt, p.n_q - i0) * p.group : 0;
+#pragma unroll
+            for (int j = 0; j < kMassRows / 32; ++j)
+                ahead[j] = lane + 32 * j < rows ? lse_base2(__ldg(src + (i0 + tok[j]) * p.lse_token + head[j])) : INFINITY;
+        };
+        load(w.begin);
+#pragma unroll 1
         for (int k = w.begin; k < w.end; ++k) {
-            const int i0 = k * p.tpt, rows = min(p.tpt, p.n_q - i0) * p.group;
-            const float *src = p.lse + w.b * p.lse_request + w.g * p.group;
             float off[kMassRows / 32];
 #pragma unroll
-            for (int j = 0; j < kMassRows / 32; ++j) {
-                const int r = lane + 32 * j;
-                off[j] = INFINITY;
-                if (r < rows)
-                    off[j] = lse_base2(__ldg(src + (i0 + tok[j]) * p.lse_token + head[j]));
-            }
+            for (int j = 0; j < kMassRows / 32; ++j)
+                off[j] = ahead[j];
+            load(k + 1);
             bool ok = true;
             if (alive && lane == 0)
                 ok = c.wait(c.q_empty(turn.slot), turn.parity ^ 1u);
@@ -306,7 +313,7 @@ __device__ void copy_q(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
                 asm volatile(
                     "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
                     " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(c.q_slot(turn.slot) + (uint32_t)lane * kHalfBytes),
-                    "l"(reinterpret_cast<uint64_t>(tm)), "r"(lane * 64), "r"(w.g * p.group), "r"(i0), "r"(w.b),
+                    "l"(reinterpret_cast<uint64_t>(tm)), "r"(lane * 64), "r"(w.g * p.group), "r"(k * p.tpt), "r"(w.b),
                     "r"(c.q_full(turn.slot))
                     : "memory");
             ++issued;
@@ -550,195 +557,227 @@ __device__ void add_up(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int 
 }
 
 // ---------------------------------------------------------------------------
-// many blocks: K in TMEM
+// many blocks: rows on M, 256 tokens on N
 // ---------------------------------------------------------------------------
-constexpr uint32_t kStreamS = 256u;          // first column of the two S buffers; tile x's K is at 64 x
+constexpr int kWide = 2 * kMassTile;         // tokens of an item
+
+// An item's K, [column half][256 tokens][128 B], a lane per (half, page); pages as
+// in copy_k().
+template <int D>
+__device__ void copy_k_wide(const CUtensorMap *tm, const MassParams &p, const Ctx<D> &c)
+{
+    constexpr int kSlots = Ring<D>::kK / 2;
+    const int lane = threadIdx.x & 31, P = p.page_size, RB = kWide / P;
+    const uint64_t pol = l2_evict_first_policy();
+    auto entry = [&](const Walk &w) {
+        const int pg = w.t0 / P + lane;
+        return lane < RB && pg * P < w.L ? __ldg(p.block_table + (int64_t)w.b * p.max_pages + pg) : -1;
+    };
+    Walk w;
+    Turn turn;
+    bool alive = true, more = walk_first(p, w);
+    int issued = 0, id = more ? entry(w) : -1;
+    while (more) {
+        Walk next = w;
+        more = walk_next(p, next);
+        const int next_id = more ? entry(next) : -1;
+        if (lane == 0 && w.fresh && w.at == 0 && w.g == 0 && __ldg(p.seq_lens + w.b) != w.L)
+            atomicOr(p.err, SHKV_ERRF_SEQ_LEN);
+        const bool there = lane < RB && w.t0 + lane * P < w.L, inside = there && (uint32_t)id < (uint32_t)p.num_pages;
+        if (there && !inside)
+            atomicOr(p.err, SHKV_ERRF_PAGE_OOB);
+        const uint32_t mask = __ballot_sync(0xffffffffu, inside);
+        bool ok = true;
+        if (alive && lane == 0) {
+            ok = c.wait(c.k_empty(turn.slot), turn.parity ^ 1u);
+            if (ok)
+                mbar_arrive_expect_tx(c.k_full(turn.slot), (uint32_t)(__popc(mask) * P * D * 2));
+        }
+        alive = __all_sync(0xffffffffu, alive && ok);
+        if (alive) {
+            if (inside)
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h)
+                    tma_load_2d(c.k_slot(2 * turn.slot) + (uint32_t)(h * kWide + lane * P) * 128u, tm, h * 64,
+                                (id * p.hkv + w.g) * P, c.k_full(turn.slot), pol);
+            ++issued;
+            turn.next(kSlots);
+        }
+        w = next;
+        id = next_id;
+    }
+    if (!alive && lane == 0)
+        for (int i = max(0, issued - kSlots); i < issued; ++i)
+            mbar_drain_bounded(c.k_full(i % kSlots), (uint32_t)(i / kSlots) & 1u);
+}
 
 template <int D>
-__device__ void issue_stream(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int odd)
+__device__ void issue_wide(const MassParams &p, const Ctx<D> &c, uint32_t tmem)
 {
-    const uint64_t qd0 = umma_sdesc_sw128(c.q_slot(0), 16u, 1024u);
-    const uint32_t d = tmem + kStreamS + (uint32_t)odd * 128u, empty = c.s_empty(odd), full = c.s_full(odd);
+    const uint64_t kd0 = umma_sdesc_sw128(c.k_slot(0), 16u, 1024u), qd0 = umma_sdesc_sw128(c.q_slot(0), 16u, 1024u);
     const bool one = (threadIdx.x & 31) == 0;
     Walk w;
-    Turn qt;
-    uint32_t s_par = 1u, k_par = 0u;         // of the S buffer's next wait; of the tiles' (odd, odd + 2), a bit each
-    bool alive = true, rows_in = false;
+    Turn kt, qt, st;
+    bool alive = true;
     if (!walk_first(p, w))
         return;
     do {
-        const int tiles = min(p.span, (w.L - w.t0 + kMassTile - 1) / kMassTile);
-        uint32_t k_in = 0u;                  // tiles whose K has been waited for
+        const uint32_t idesc = umma_idesc_bf16(128, w.t0 + kMassTile < w.L ? kWide : kMassTile, false, false);
+        const uint64_t kd = kd0 + ((2u * (uint32_t)kt.slot * Ring<D>::kSlot) >> 4);
+        alive = issuer_wait(c, c.k_full(kt.slot), kt.parity, alive);
 #pragma unroll 1
         for (int k = w.begin; k < w.end; ++k) {
-            if (rows_in) {
-                if (one)
-                    umma_commit(c.q_empty(qt.slot));
-                qt.next(Ring<D>::kQ);
-            }
-            rows_in = true;
-            const int rows = min(p.tpt, p.n_q - k * p.tpt) * p.group;
-            const uint32_t idesc = umma_idesc_bf16(kMassTile, (rows + 15) & ~15, false, false);
             const uint64_t qd = qd0 + (((uint32_t)qt.slot * Ring<D>::kSlot) >> 4);
             alive = issuer_wait(c, c.q_full(qt.slot), qt.parity, alive);
-#pragma unroll 1
-            for (int x = odd; x < tiles; x += 2) {
-                if (!w.sees(p, k, x))
-                    break;
-                const uint32_t a = tmem + (uint32_t)(x * 64);
-                if (!(k_in >> x & 1u))
-                    alive = issuer_wait(c, c.k_in_tmem(x), k_par >> x & 1u, alive);
-                k_in |= 1u << x;
-                alive = issuer_wait(c, empty, s_par, alive);
-                tc_fence_after();
-                if (one) {
-                    if (alive) {
+            alive = issuer_wait(c, c.s_empty(st.slot), st.parity ^ 1u, alive);
+            tc_fence_after();
+            if (one) {
+                if (alive) {
 #pragma unroll
-                        for (int i = 0; i < D / 16; ++i) {
-                            const uint32_t off = ((uint32_t)(i >> 2) * kHalfBytes + (uint32_t)(i & 3) * 32u) >> 4;
-                            umma_bf16_ts(d, a + (uint32_t)(i * 8), qd + off, idesc, i ? 1u : 0u);
-                        }
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint32_t in = (uint32_t)(i & 3) * 32u;
+                        umma_bf16(tmem + (uint32_t)st.slot * 256u, qd + (((uint32_t)(i >> 2) * kHalfBytes + in) >> 4),
+                                  kd + (((uint32_t)(i >> 2) * 2u * kHalfBytes + in) >> 4), idesc, i ? 1u : 0u);
                     }
-                    umma_commit(full);
                 }
-                __syncwarp();
-                s_par ^= 1u;
+                umma_commit(c.s_full(st.slot));
+                umma_commit(c.q_empty(qt.slot));
             }
+            __syncwarp();
+            st.next(2);
+            qt.next(Ring<D>::kQ);
         }
-        for (int x = odd; x < tiles; x += 2) // a range that ends before the tile's first block
-            if (!(k_in >> x & 1u))
-                alive = issuer_wait(c, c.k_in_tmem(x), k_par >> x & 1u, alive);
-        k_par ^= (1u << tiles) - 1u;
+        kt.next(Ring<D>::kK / 2);
     } while (walk_next(p, w));
     if (one) {
-        umma_commit(c.fin(odd));
-        mbar_drain_bounded(c.fin(odd), 0u);
+        umma_commit(c.fin(0));
+        mbar_drain_bounded(c.fin(0), 0u);
     }
 }
 
-// K of an item's tiles into TMEM, a tile of four warps each; the weights of the
-// even tiles by warps 0-7, of the odd ones by warps 8-15, each four warps of
-// them taking half of the columns; the halves joined, the masses.
-template <int D>
-__device__ void add_up_stream(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int four)
+// Adds to acc the weights of 16 tokens for the thread's row; kMasked: of the first
+// `seen` ones.
+template <bool kMasked>
+__device__ __forceinline__ void weigh_row16(const uint32_t *s, float c, float l, int seen, float2 *acc)
 {
-    const int lane = threadIdx.x & 31, row = threadIdx.x & 127, odd = four / 2, half = four % 2;
-    const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;
-    // this warp's columns of its S buffer; and the barrier of the two warps of the same tokens
-    const uint32_t s_mine = tmem + kStreamS + lanes + (uint32_t)(128 * odd + 64 * half);
-    const uint32_t pair_bar = 1u + (uint32_t)(4 * odd + row / 32);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), make_float2(c, c),
+                              make_float2(l, l));
+        if (kMasked) {
+            x.x = 2 * j < seen ? x.x : -INFINITY;
+            x.y = 2 * j + 1 < seen ? x.y : -INFINITY;
+        }
+        acc[j] = __fadd2_rn(acc[j], make_float2(ex2_approx(x.x), ex2_approx(x.y)));
+    }
+}
+
+// The weights of columns 64 group .. 64 group + 63 of every item; at its end the
+// warps' sums by way of the item's K, which has been used, and the masses.
+template <int D>
+__device__ void add_up_wide(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int group)
+{
+    const int lane = threadIdx.x & 31, quad = threadIdx.x / 32 % 4, row = 32 * quad + lane;
+    const int tok = row / p.group, tok0 = 32 * quad / p.group;       // query token of the row, and of the warp's first
+    const uint32_t s_mine = tmem + ((uint32_t)(32 * quad) << 16) + 64u * (uint32_t)group;
     Walk w;
-    Turn qt;
-    TileRing kt(p.span, Ring<D>::kK);
-    const int own = 2 * half + odd;          // the tile that this warp takes to TMEM
-    uint32_t s_par = 0u;
-    bool alive = true, rows_in = false;
+    Turn kt, qt, st;
+    bool alive = true;
     if (!walk_first(p, w))
         return;
     do {
-        const int tiles = min(p.span, (w.L - w.t0 + kMassTile - 1) / kMassTile);
-        // every product that read the tile's last K is done: the warps of its parity
-        // have waited for all of them
-        if (own < tiles) {
-            const int slot = kt.slot(own);
-            if (alive)
-                alive = c.wait(c.k_full(slot), kt.parity(own));
-            alive = __all_sync(0xffffffffu, alive);
-            if (alive) {
+        const int tokens = min(kWide, w.L - w.t0), mine = tokens - 64 * group;      // of the warp's 64
+        float2 acc[32];
 #pragma unroll
-                for (int h = 0; h < D / 64; ++h) {
-                    uint32_t v[32];
-                    const uint32_t src = c.k_slot(slot) + (uint32_t)h * kHalfBytes + (uint32_t)row * 128u;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 f = load_shared4(src + (uint32_t)((i ^ (row & 7)) << 4));
-                        v[4 * i] = __float_as_uint(f.x), v[4 * i + 1] = __float_as_uint(f.y);
-                        v[4 * i + 2] = __float_as_uint(f.z), v[4 * i + 3] = __float_as_uint(f.w);
-                    }
-                    tmem_st32(tmem + lanes + (uint32_t)(own * 64 + h * 32), v);
-                }
-                tc_fence_before();
-            }
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(c.k_in_tmem(own));
-                mbar_arrive(c.k_empty(slot));
-            }
-            kt.next(own);
-        }
-        float sum[2] = {0.f, 0.f};           // tiles odd and odd + 2
+        for (int j = 0; j < 32; ++j)
+            acc[j] = make_float2(0.f, 0.f);
 #pragma unroll 1
         for (int k = w.begin; k < w.end; ++k) {
-            if (rows_in) {
+            const int i0 = k * p.tpt;
+            // tokens of the warp's that the row sees; a row behind the block's last sees
+            // none (its zero query and an infinite key make no number)
+            const int base = w.past + i0 + 1 - w.t0 - 64 * group;
+            const int seen = row < min(p.tpt, p.n_q - i0) * p.group ? base + tok : 0;
+            const bool plain = base + tok0 >= 64;
+            alive = alive && c.wait(c.q_full(qt.slot), qt.parity);
+            float l;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(l) : "r"(c.lse(qt.slot) + 4u * (uint32_t)row)
+                         : "memory");
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(c.q_empty(qt.slot));
+            qt.next(Ring<D>::kQ);
+            alive = __all_sync(0xffffffffu, alive && c.wait(c.s_full(st.slot), st.parity));
+            if (alive && mine > 0) {
+                tc_fence_after();
+                const uint32_t s = s_mine + 256u * (uint32_t)st.slot;
+                uint32_t a[2][16];
+                tmem_ld16_nowait(s, a[0]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    tmem_wait_ld();
+                    if (i < 3)
+                        tmem_ld16_nowait(s + 16u * (uint32_t)(i + 1), a[(i + 1) & 1]);
+                    else
+                        leave(c.s_empty(st.slot));
+                    // (no use of a score moves before its wait: `seen` passes through it)
+                    int n = seen;
+                    asm volatile("" : "+r"(n)::"memory");
+                    if (plain) {
+                        if (n > 0)
+                            weigh_row16<false>(a[i & 1], p.scale_log2, l, 16, acc + 8 * i);
+                    } else if (n > 16 * i) {
+                        weigh_row16<true>(a[i & 1], p.scale_log2, l, n - 16 * i, acc + 8 * i);
+                    }
+                }
+            } else {
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(c.q_empty(qt.slot));
-                qt.next(Ring<D>::kQ);
+                    mbar_arrive(c.s_empty(st.slot));
             }
-            rows_in = true;
-            if (alive)
-                alive = c.wait(c.q_full(qt.slot), qt.parity);
-            const int i0 = k * p.tpt, n = min(min(p.tpt, p.n_q - i0) * p.group - 64 * half, 64);
-#pragma unroll 1
-            for (int x = odd; x < tiles; x += 2) {
-                if (!w.sees(p, k, x))
-                    break;
-                if (alive)
-                    alive = c.wait(c.s_full(odd), s_par);
-                alive = __all_sync(0xffffffffu, alive);
-                if (alive) {
-                    tc_fence_after();
-                    // query tokens before t - past do not see token t
-                    const int first = (w.t0 + x * kMassTile + row - w.past - i0) * p.group - 64 * half;
-                    const float v = weigh(s_mine, c.lse(qt.slot) + 256u * half, n, first, first + (31 - lane) * p.group,
-                                          p.scale_log2, true, c.s_empty(odd));
-                    sum[0] += x < 2 ? v : 0.f;
-                    sum[1] += x < 2 ? 0.f : v;
-                } else if (lane == 0) {
-                    mbar_arrive(c.s_empty(odd));
-                }
-                s_par ^= 1u;
-            }
+            st.next(2);
         }
-        // the upper half's sums by way of its own columns of S, which no product
-        // writes before the next item's K is in TMEM
-        if (half) {
-            uint32_t v[8];
+        // over the warp's rows: halves of the columns change hands, until a lane has two
+        // (columns 2 r, 2 r + 1, the bits of r being the lane's from the top)
+        const uint32_t full = 0xffffffffu;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = __float_as_uint(sum[i & 1]);
-            tmem_st8_nowait(s_mine, v);
-            tmem_wait_st();
-            tc_fence_before();
-        }
-        named_barrier(pair_bar, 64u);
-        if (half == 0) {
-            uint32_t v[8];
-            tc_fence_after();
-            tmem_ld8_nowait(s_mine + 64u, v);
-            tmem_wait_ld();
-            tc_fence_before();
-            const bool whole = w.whole(p);
+        for (int o = 16, n = 16; o; o >>= 1, n >>= 1)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int x = 2 * i + odd, t = w.t0 + x * kMassTile + row;
-                if (x >= tiles || t >= w.L)
-                    continue;
-                const bool inside = (uint32_t)__ldg(p.block_table + (int64_t)w.b * p.max_pages + t / p.page_size) <
-                                    (uint32_t)p.num_pages;
-                const float total = inside ? sum[i] + __uint_as_float(v[i]) : 0.f;
-                if (!whole)
-                    p.pieces[(int64_t)piece_of(p, w) * (kMassSpan * kMassTile) + t - w.t0] = total;
-                else
-                    p.mass.out[w.b * p.mass.out_request + w.g * p.mass.out_head + t] =
-                        p.mass.in ? fmaf(p.decay, p.mass.in[w.b * p.mass.in_request + w.g * p.mass.in_head + t], total)
-                                  : total;
+            for (int j = 0; j < n; ++j) {
+                const bool up = lane & o;
+                const float2 send = up ? acc[j] : acc[j + n], keep = up ? acc[j + n] : acc[j];
+                acc[j] = make_float2(keep.x + __shfl_xor_sync(full, send.x, o), keep.y + __shfl_xor_sync(full, send.y, o));
             }
+        const uint32_t sums = c.k_slot(2 * kt.slot);     // [4 warps][256 tokens]
+        if (mine > 0)
+            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sums + (uint32_t)(quad * kWide + 64 * group + 2 * lane) * 4u),
+                         "f"(acc[0].x), "f"(acc[0].y)
+                         : "memory");
+        named_barrier(1u, 512u);
+        if (threadIdx.x < tokens) {
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i]) : "r"(sums + (uint32_t)(i * kWide + threadIdx.x) * 4u));
+            const int t = w.t0 + threadIdx.x;
+            const bool inside = (uint32_t)__ldg(p.block_table + (int64_t)w.b * p.max_pages + t / p.page_size) <
+                                (uint32_t)p.num_pages;
+            const float sum = inside ? (v[0] + v[1]) + (v[2] + v[3]) : 0.f;
+            if (!w.whole(p))
+                p.pieces[(int64_t)piece_of(p, w) * (kMassSpan * kMassTile) + threadIdx.x] = sum;
+            else
+                p.mass.out[w.b * p.mass.out_request + w.g * p.mass.out_head + t] =
+                    p.mass.in ? fmaf(p.decay, p.mass.in[w.b * p.mass.in_request + w.g * p.mass.in_head + t], sum) : sum;
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(c.k_empty(kt.slot));
+        kt.next(Ring<D>::kK / 2);
     } while (walk_next(p, w));
 }
 
-template <int D, bool kStream>
+template <int D, bool kManyRows>
 __global__ void __launch_bounds__(kThreads, 1)
     shkv_mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
                      const __grid_constant__ MassParams p)
@@ -754,16 +793,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < Ring<D>::kK; ++s) {
             mbar_init(c.k_full(s), 1u);
-            mbar_init(c.k_empty(s), kStream ? 4u : 1u);   // the warps that take it to TMEM, or the MMAs
+            mbar_init(c.k_empty(s), kManyRows ? 16u : 1u);   // the weights' warps, or the MMAs
         }
         for (int s = 0; s < Ring<D>::kQ; ++s) {
             mbar_init(c.q_full(s), 1u);
-            mbar_init(c.q_empty(s), 18u);    // both issuers' MMAs and the warps that read the log-sum-exps
+            mbar_init(c.q_empty(s), kManyRows ? 17u : 18u);  // the issuers' MMAs and the warps that read the log-sum-exps
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(c.s_full(i), 1u);
-            mbar_init(c.s_empty(i), kStream ? 8u : 4u);
-            mbar_init(c.k_in_tmem(i), 4u);
+            mbar_init(c.s_empty(i), kManyRows ? 16u : 4u);
         }
         mbar_init(c.fin(0), 1u);
         mbar_init(c.fin(1), 1u);
@@ -785,17 +823,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(c.smem + Ring<D>::kMisc + 4u);
     pdl_wait_prior();
     pdl_launch_dependents();
-    if (warp == kKWarp)
+    if (kManyRows) {
+        if (warp < kKWarp) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWeightRegs));
+            add_up_wide<D>(p, c, tmem, warp / 4);
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+            if (warp == kKWarp)
+                copy_k_wide<D>(&tm_k, p, c);
+            else if (warp == kQWarp)
+                copy_q<D>(&tm_q, p, c);
+            else if (warp == kMmaWarp)
+                issue_wide<D>(p, c, tmem);
+        }
+    } else if (warp == kKWarp)
         copy_k<D>(&tm_k, p, c);
     else if (warp == kQWarp)
         copy_q<D>(&tm_q, p, c);
-    else if (warp >= kMmaWarp) {
-        if (kStream)
-            issue_stream<D>(p, c, tmem, warp - kMmaWarp);
-        else
-            issue<D>(p, c, tmem, warp - kMmaWarp);
-    } else if (kStream)
-        add_up_stream<D>(p, c, tmem, warp / 4);
+    else if (warp >= kMmaWarp)
+        issue<D>(p, c, tmem, warp - kMmaWarp);
     else
         add_up<D>(p, c, tmem, warp / 4);
     tc_fence_before();
@@ -839,11 +885,18 @@ __global__ void __launch_bounds__(kMassSpan *kMassTile) shkv_mass_join_kernel(co
 cudaError_t launch_mass(const CUtensorMap &tm_k, const CUtensorMap &tm_q, const MassParams &p, bool pieces,
                         cudaStream_t stream)
 {
-    const bool many = p.blocks >= kMassStream;
-    auto kern = p.head_dim == 64 ? (many ? shkv_mass_kernel<64, true> : shkv_mass_kernel<64, false>)
-                                 : (many ? shkv_mass_kernel<128, true> : shkv_mass_kernel<128, false>);
+    const bool wide = mass_wide(p.blocks);
+    auto kern = p.head_dim == 64 ? (wide ? shkv_mass_kernel<64, true> : shkv_mass_kernel<64, false>)
+                                 : (wide ? shkv_mass_kernel<128, true> : shkv_mass_kernel<128, false>);
     const uint32_t smem = p.head_dim == 64 ? Ring<64>::kBytes : Ring<128>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // a build whose launch has other registers than setmaxnreg hands out could wait
+    // for some forever: it is refused
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+    if (e == cudaSuccess && wide && fa.numRegs != (int)kLaunchRegs)
+        e = cudaErrorInvalidConfiguration;
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess)
         e = launch_pdl(kern, p.num_ctas, kThreads, smem, stream, tm_k, tm_q, p);
     if (e == cudaSuccess && pieces)
