@@ -44,8 +44,9 @@ namespace {
 constexpr int kThreads = 640;
 constexpr int kKWarp = 16, kQWarp = 17, kMmaWarp = 18;
 constexpr uint32_t kTmemCols = 512;          // four S buffers of 128 columns, or two of 256
-// Registers a thread, many blocks (setmaxnreg): 104 * 512 + 64 * 128 = 96 * 640.
-constexpr uint32_t kLaunchRegs = 96, kWeightRegs = 104, kOtherRegs = 64;
+// Registers a thread, many blocks (setmaxnreg): 112 * 512 + 32 * 128 = 96 * 640.  (At
+// 104 for the weights their inner loop spills: half as fast again.)
+constexpr uint32_t kLaunchRegs = 96, kWeightRegs = 112, kOtherRegs = 32;
 static_assert(kWeightRegs * 512 + kOtherRegs * 128 == kLaunchRegs * kThreads, "register split");
 constexpr uint32_t kHalfBytes = 128u * 128u; // 64 columns of 128 tokens or rows
 
@@ -260,10 +261,26 @@ __device__ void copy_k(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
 // Q blocks and what their rows' log-sum-exps take off the scores; a row beyond
 // the block's, or one that attends nothing, gets -inf and so weighs nothing.
 template <int D>
+__device__ __forceinline__ void copy_block(const CUtensorMap *tm, const MassParams &p, const Ctx<D> &c, const Walk &w, int k,
+                                           int slot)
+{
+    const int lane = threadIdx.x & 31;
+    if (lane == 0)
+        mbar_arrive_expect_tx(c.q_full(slot), (uint32_t)(p.tpt * p.group * D * 2));
+    __syncwarp();
+    if (lane < D / 64)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(c.q_slot(slot) + (uint32_t)lane * kHalfBytes),
+            "l"(reinterpret_cast<uint64_t>(tm)), "r"(lane * 64), "r"(w.g * p.group), "r"(k * p.tpt), "r"(w.b),
+            "r"(c.q_full(slot))
+            : "memory");
+}
+
+template <int D>
 __device__ void copy_q(const CUtensorMap *tm, const MassParams &p, const Ctx<D> &c)
 {
     const int lane = threadIdx.x & 31;
-    const uint32_t bytes = (uint32_t)(p.tpt * p.group * D * 2);
     Walk w;
     Turn turn;
     bool alive = true;
@@ -306,16 +323,7 @@ __device__ void copy_q(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
                 asm volatile("st.shared.f32 [%0], %1;" ::"r"(c.lse(turn.slot) + 4u * (uint32_t)(lane + 32 * j)), "f"(-off[j])
                              : "memory");
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive_expect_tx(c.q_full(turn.slot), bytes);
-            __syncwarp();
-            if (lane < D / 64)
-                asm volatile(
-                    "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-                    " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(c.q_slot(turn.slot) + (uint32_t)lane * kHalfBytes),
-                    "l"(reinterpret_cast<uint64_t>(tm)), "r"(lane * 64), "r"(w.g * p.group), "r"(k * p.tpt), "r"(w.b),
-                    "r"(c.q_full(turn.slot))
-                    : "memory");
+            copy_block<D>(tm, p, c, w, k, turn.slot);
             ++issued;
             turn.next(Ring<D>::kQ);
         }
@@ -612,6 +620,31 @@ __device__ void copy_k_wide(const CUtensorMap *tm, const MassParams &p, const Ct
 }
 
 template <int D>
+__device__ void copy_q_wide(const CUtensorMap *tm, const MassParams &p, const Ctx<D> &c)
+{
+    Walk w;
+    Turn turn;
+    bool alive = true;
+    int issued = 0;
+    if (!walk_first(p, w))
+        return;
+    do {
+#pragma unroll 1
+        for (int k = w.begin; k < w.end; ++k) {
+            alive = issuer_wait(c, c.q_empty(turn.slot), turn.parity ^ 1u, alive);
+            if (!alive)
+                continue;
+            copy_block<D>(tm, p, c, w, k, turn.slot);
+            ++issued;
+            turn.next(Ring<D>::kQ);
+        }
+    } while (walk_next(p, w));
+    if (!alive && (threadIdx.x & 31) == 0)
+        for (int i = max(0, issued - Ring<D>::kQ); i < issued; ++i)
+            mbar_drain_bounded(c.q_full(i % Ring<D>::kQ), (uint32_t)(i / Ring<D>::kQ) & 1u);
+}
+
+template <int D>
 __device__ void issue_wide(const MassParams &p, const Ctx<D> &c, uint32_t tmem)
 {
     const uint64_t kd0 = umma_sdesc_sw128(c.k_slot(0), 16u, 1024u), qd0 = umma_sdesc_sw128(c.q_slot(0), 16u, 1024u);
@@ -655,13 +688,13 @@ __device__ void issue_wide(const MassParams &p, const Ctx<D> &c, uint32_t tmem)
     }
 }
 
-// Adds to acc the weights of 16 tokens for the thread's row; kMasked: of the first
+// Adds to acc the weights of 32 tokens for the thread's row; kMasked: of the first
 // `seen` ones.
 template <bool kMasked>
-__device__ __forceinline__ void weigh_row16(const uint32_t *s, float c, float l, int seen, float2 *acc)
+__device__ __forceinline__ void weigh_row32(const uint32_t *s, float c, float l, int seen, float2 *acc)
 {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 16; ++j) {
         float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), make_float2(c, c),
                               make_float2(l, l));
         if (kMasked) {
@@ -673,15 +706,17 @@ __device__ __forceinline__ void weigh_row16(const uint32_t *s, float c, float l,
 }
 
 // The weights of columns 64 group .. 64 group + 63 of every item; at its end the
-// warps' sums by way of the item's K, which has been used, and the masses.
+// warps' sums by way of the item's K, which has been used, and the masses.  (TMEM is
+// read 32 columns at a time: 16 at a time took a fifth longer in all.)
 template <int D>
 __device__ void add_up_wide(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int group)
 {
     const int lane = threadIdx.x & 31, quad = threadIdx.x / 32 % 4, row = 32 * quad + lane;
     const int tok = row / p.group, tok0 = 32 * quad / p.group;       // query token of the row, and of the warp's first
     const uint32_t s_mine = tmem + ((uint32_t)(32 * quad) << 16) + 64u * (uint32_t)group;
+    const int n_mine = row < p.tpt * p.group ? p.n_q : 0;            // the row's query tokens lie before this
     Walk w;
-    Turn kt, qt, st;
+    Turn kt, st;
     bool alive = true;
     if (!walk_first(p, w))
         return;
@@ -691,44 +726,42 @@ __device__ void add_up_wide(const MassParams &p, const Ctx<D> &c, uint32_t tmem,
 #pragma unroll
         for (int j = 0; j < 32; ++j)
             acc[j] = make_float2(0.f, 0.f);
+        // the row's query token in the next block, and the log-sum-exp, read a block
+        // ahead; a row behind the last weighs nothing (+inf is taken off)
+        int i = w.begin * p.tpt + tok;
+        const float *src = p.lse + w.b * p.lse_request + i * p.lse_token + w.g * p.group + row - tok * p.group;
+        float lse = i < n_mine ? __ldg(src) : -INFINITY;
+        // blocks from which on all of the warp's rows see all of its tokens
+        const int rest = w.t0 + 64 * group + 63 - w.past - tok0;
+        const int plain = rest > 0 ? (rest + p.tpt - 1) / p.tpt : 0;
 #pragma unroll 1
         for (int k = w.begin; k < w.end; ++k) {
-            const int i0 = k * p.tpt;
-            // tokens of the warp's that the row sees; a row behind the block's last sees
-            // none (its zero query and an infinite key make no number)
-            const int base = w.past + i0 + 1 - w.t0 - 64 * group;
-            const int seen = row < min(p.tpt, p.n_q - i0) * p.group ? base + tok : 0;
-            const bool plain = base + tok0 >= 64;
-            alive = alive && c.wait(c.q_full(qt.slot), qt.parity);
-            float l;
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(l) : "r"(c.lse(qt.slot) + 4u * (uint32_t)row)
-                         : "memory");
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(c.q_empty(qt.slot));
-            qt.next(Ring<D>::kQ);
+            const float l = -lse_base2(lse);
+            const bool row_in = i < n_mine;
+            i += p.tpt;
+            src += p.tpt * p.lse_token;
+            lse = i < n_mine ? __ldg(src) : -INFINITY;
             alive = __all_sync(0xffffffffu, alive && c.wait(c.s_full(st.slot), st.parity));
             if (alive && mine > 0) {
                 tc_fence_after();
-                const uint32_t s = s_mine + 256u * (uint32_t)st.slot;
-                uint32_t a[2][16];
-                tmem_ld16_nowait(s, a[0]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t s[32];
+                    tmem_ld32_nowait(s_mine + 256u * (uint32_t)st.slot + 32u * h, s);
                     tmem_wait_ld();
-                    if (i < 3)
-                        tmem_ld16_nowait(s + 16u * (uint32_t)(i + 1), a[(i + 1) & 1]);
-                    else
+                    if (h)
                         leave(c.s_empty(st.slot));
-                    // (no use of a score moves before its wait: `seen` passes through it)
-                    int n = seen;
-                    asm volatile("" : "+r"(n)::"memory");
-                    if (plain) {
-                        if (n > 0)
-                            weigh_row16<false>(a[i & 1], p.scale_log2, l, 16, acc + 8 * i);
-                    } else if (n > 16 * i) {
-                        weigh_row16<true>(a[i & 1], p.scale_log2, l, n - 16 * i, acc + 8 * i);
-                    }
+                    // (no use of a score moves before its wait: the condition passes through it)
+                    int in = row_in;
+                    asm volatile("" : "+r"(in)::"memory");
+                    // a zero query of a row that is none and an infinite key make no number
+                    if (!in)
+                        continue;
+                    if (k >= plain)
+                        weigh_row32<false>(s, p.scale_log2, l, 32, acc + 16 * h);
+                    else                     // tokens up to past + the row's query token
+                        weigh_row32<true>(s, p.scale_log2, l, w.past + i - p.tpt + 1 - w.t0 - 64 * group - 32 * h,
+                                          acc + 16 * h);
                 }
             } else {
                 __syncwarp();
@@ -797,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < Ring<D>::kQ; ++s) {
             mbar_init(c.q_full(s), 1u);
-            mbar_init(c.q_empty(s), kManyRows ? 17u : 18u);  // the issuers' MMAs and the warps that read the log-sum-exps
+            mbar_init(c.q_empty(s), kManyRows ? 1u : 18u);   // the issuers' MMAs, and the warps that read the log-sum-exps
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(c.s_full(i), 1u);
@@ -832,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (warp == kKWarp)
                 copy_k_wide<D>(&tm_k, p, c);
             else if (warp == kQWarp)
-                copy_q<D>(&tm_q, p, c);
+                copy_q_wide<D>(&tm_q, p, c);
             else if (warp == kMmaWarp)
                 issue_wide<D>(p, c, tmem);
         }
