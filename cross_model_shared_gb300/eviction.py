@@ -31,7 +31,8 @@ class EvictionCalls:
     named stream, or where a side stream is current, holds its tensors back:
     they may be dropped once it has returned.  A captured call's tensors, and
     the pool, have to live as long as the graph, which replays with the lengths
-    of the capture.
+    of the capture.  Scratch memory is the pool's, one per stream; a captured call
+    takes its own from the graph's memory.
     """
 
     # -- arguments ------------------------------------------------------------
@@ -77,11 +78,18 @@ class EvictionCalls:
             raise ValueError(f"{name}: a row's masses must be contiguous")
         return N.shkv_mass(t.data_ptr(), request, head, shape[2])
 
-    def _mass_workspace(self) -> int:
-        n = self.__dict__.get("_mass_workspace_bytes")
-        if n is None:
-            n = self._mass_workspace_bytes = N.shkv_prefill_mass_workspace_size(self.handle)
-        return n
+    def _mass_workspace(self, raw: int) -> torch.Tensor:
+        """Scratch of the calls on a stream, or of a captured call alone (from
+        the graph's memory, so graphs share none)."""
+        ws: Dict[int, torch.Tensor] = self.__dict__.setdefault("_mass_workspaces", {})
+        t = ws.get(raw)
+        capturing = torch.cuda.is_current_stream_capturing()
+        if t is None or capturing:
+            t = torch.empty(N.shkv_prefill_mass_workspace_size(self.handle), dtype=torch.uint8,
+                            device=self.k_pages.device)
+            if not capturing:
+                ws[raw] = t
+        return t
 
     def _masses(self, mass: Optional[torch.Tensor], out: Optional[torch.Tensor], batch: int):
         """Masses read (or None) and written, for the C call, and the tensor written."""
@@ -130,24 +138,25 @@ class EvictionCalls:
         of both (``q[:, -64:]``) make the chunk's last tokens a window of
         voters: a token's own rows have to be contiguous, tokens a multiple of
         head_dim elements apart and requests a multiple of the tokens' stride."""
-        if q.dtype is not _BF16 or q.device != self.k_pages.device or q.dim() != 4 or q.shape[3] != self.head_dim:
+        shape, stride = q.shape, q.stride()
+        if q.dtype is not _BF16 or q.device != self.k_pages.device or len(shape) != 4 or shape[3] != self.head_dim:
             raise ValueError(f"q must be bfloat16 [B, n_new, hq, head_dim] on {self.k_pages.device}")
-        B, T, H, D = q.shape
-        if (D > 1 and q.stride(3) != 1) or (H > 1 and q.stride(2) != D):
+        B, T, H, D = shape
+        if stride[3] != 1 or (stride[2] != D and H > 1):
             raise ValueError("q: a token's rows must be contiguous")
-        if lse.dtype is not _F32 or lse.device != q.device or tuple(lse.shape) != (B, T, H):
+        if lse.dtype is not _F32 or lse.device != q.device or lse.shape != shape[:3]:
             raise ValueError(f"lse must be float32 {[B, T, H]} on {q.device}")
-        if H > 1 and lse.stride(2) != 1:
+        ls = lse.stride()
+        if ls[2] != 1 and H > 1:
             raise ValueError("lse: a token's values must be contiguous")
         ctx, s = self._enter(stream)
         with ctx:
             m, o, result = self._masses(mass, out, B)
-            # scratch of this call alone: its memory goes back to the stream's (or a graph's) own
-            ws = torch.empty(self._mass_workspace(), dtype=torch.uint8, device=q.device)
+            ws = self._mass_workspace(s)
             self._hold(s, stream, q, lse, mass, out)
-            N.shkv_prefill_mass(self.handle, B, T, H, q.data_ptr(), q.stride(0), q.stride(1),
-                                D ** -0.5 if scale is None else float(scale), lse.data_ptr(), lse.stride(0),
-                                lse.stride(1), float(decay), m, o, ws.data_ptr(), ws.numel(), s)
+            N.shkv_prefill_mass(self.handle, B, T, H, q.data_ptr(), stride[0], stride[1],
+                                D ** -0.5 if scale is None else float(scale), lse.data_ptr(), ls[0], ls[1], float(decay),
+                                m, o, ws.data_ptr(), ws.numel(), s)
         return result
 
     def select_tokens(self, mass: torch.Tensor, keep, sink: int = 0, recent: int = 0,
