@@ -512,9 +512,9 @@ __device__ void add_up(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int 
         const bool whole = w.whole(p), mine = x < p.span && w.t0 + x * kMassTile < w.L;
         const int t = w.t0 + x * kMassTile + row;
         float old = 0.f, sum = 0.f;
-        bool inside = false;
-        if (mine && t < w.L) {
-            inside = (uint32_t)__ldg(p.block_table + (int64_t)w.b * p.max_pages + t / p.page_size) < (uint32_t)p.num_pages;
+        int page = -1;
+        if (mine && t < w.L) {               // looked at when the sum is there
+            page = __ldg(p.block_table + (int64_t)w.b * p.max_pages + t / p.page_size);
             if (whole && p.mass.in)
                 old = p.mass.in[w.b * p.mass.in_request + w.g * p.mass.in_head + t];
         }
@@ -554,7 +554,7 @@ __device__ void add_up(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int 
         }
         if (!mine || t >= w.L)
             continue;
-        if (!inside)
+        if ((uint32_t)page >= (uint32_t)p.num_pages)
             sum = 0.f;
         if (!whole)
             p.pieces[(int64_t)piece_of(p, w) * (kMassSpan * kMassTile) + t - w.t0] = sum;
