@@ -11,19 +11,19 @@ namespace shkv {
 
 namespace {
 
-constexpr int kSelectThreads = 512;
-constexpr int kBins = 2048;                              // of an 11-bit digit
-constexpr int kBinsPerThread = kBins / kSelectThreads;
-constexpr int kHistBytes = 2 * kBins * 4;
+constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
+constexpr int kBins = 2048, kCoarse = 256;               // of an 11-bit digit, and by its upper 8 bits
+constexpr int kHist = kBins + kCoarse;                   // words of a histogram
 constexpr int kSelectKeys = 49152;                       // keys of a CTA's slice that it holds in shared memory
 
-// A mass as an unsigned key of the same order: -0 as 0, every NaN on top.
+// A mass as an unsigned key of the same order: -0 as 0, every NaN on top.  Sinks and
+// recent tokens have a key above all, no token the key 0.
+constexpr uint32_t kAlways = 0xffffffffu, kNanKey = 0xfffffffeu;
+
 __device__ __forceinline__ uint32_t mass_key(float m)
 {
-    if (m != m)
-        return 0xffffffffu;
-    const uint32_t u = __float_as_uint(m == 0.f ? 0.f : m);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    const uint32_t u = __float_as_uint(m + 0.f);         // -0 + 0 = 0
+    return m != m ? kNanKey : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 // Barrier of the row's CTAs; their shared memory is ordered by it.
@@ -43,19 +43,10 @@ __device__ __forceinline__ uint32_t of_rank(const void *p, uint32_t rank)
     return a;
 }
 
-__device__ __forceinline__ uint4 load_of_rank4(uint32_t addr)
+__device__ __forceinline__ uint32_t load_of_rank(const uint32_t *p, uint32_t rank)
 {
-    uint4 v;
-    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr));
-    return v;
-}
-
-__device__ __forceinline__ uint2 load_of_rank2(uint32_t addr)
-{
-    uint2 v;
-    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(of_rank(p, rank)));
     return v;
 }
 
@@ -65,16 +56,20 @@ __device__ __forceinline__ uint2 load_of_rank2(uint32_t addr)
 // The n-th largest key of the candidates (the tokens between the sinks and the
 // recent ones) is found digit by digit, 11 bits, 11 and 10 from the top: the CTAs
 // count the candidates that share the digits found so far in a histogram each,
-// read all of them and find the digit, every one for itself.  Then all keys
-// above and, by position, as many of the equal ones as still fit are written.
-// A slice's keys stay in shared memory between the passes.
-__global__ void __launch_bounds__(kSelectThreads) shkv_select_kernel(const __grid_constant__ SelectParams p, int cached)
+// and every one of them finds the digit from all: first by its upper 8 bits, then
+// among 8 bins (reading all 2048 bins of 8 CTAs took 2.5 us a digit).  Then all
+// keys above and, by position, as many of the equal ones as still fit are written.
+// A slice's keys stay in shared memory between the passes, four of a thread side by
+// side.  Bound by the latency of its steps.
+template <int kMinCtas>
+__global__ void __launch_bounds__(kSelectThreads, kMinCtas)
+    shkv_select_kernel(const __grid_constant__ SelectParams p, int cached)
 {
     extern __shared__ __align__(16) uint32_t dyn[];
-    __shared__ uint32_t warp_sum[kSelectThreads / 32], found[3][2];      // found: digit and rest of each pass
-    __shared__ __align__(8) uint32_t totals[2];
-    __shared__ uint2 warp_counts[kSelectThreads / 32];
-    uint32_t *const keys = dyn + 2 * kBins;
+    __shared__ uint32_t warp_sum[kSelectWarps], found[2];            // found: coarse bin, keys in higher ones
+    __shared__ uint32_t totals[2];
+    __shared__ uint2 warp_counts[kSelectWarps];
+    uint32_t *const keys = dyn + 2 * kHist;
     uint32_t rank, ctas;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ctas));
@@ -95,117 +90,161 @@ __global__ void __launch_bounds__(kSelectThreads) shkv_select_kernel(const __gri
         return;
     }
     // this CTA's positions, and the candidates among them
-    const int per = (L + ctas - 1) / ctas, t0 = min(L, (int)rank * per), t1 = min(L, t0 + per);
+    const int per = ((L + (int)ctas - 1) / (int)ctas + 3) & ~3, t0 = min(L, (int)rank * per), t1 = min(L, t0 + per);
     const int lo = max(t0, p.sink), hi = min(t1, L - p.recent);
     const float *m = p.mass + b * p.mass_request + g * p.mass_head;
     const uint32_t zero_key = mass_key(0.f);
     uint32_t prefix = 0u, need = (uint32_t)(keep - p.sink - p.recent);   // of the keys with this prefix
-    const bool any = need > 0u;
-    if (tid < 6)
-        found[tid / 2][tid % 2] = 0u;
-    if (any)
+    // keys of positions t .. t + 3, t - t0 a multiple of 4; 0 outside the slice
+    auto four = [&](int t) -> uint4 {
+        if (cached)
+            return *reinterpret_cast<const uint4 *>(keys + (t - t0));
+        uint32_t k[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            k[i] = t + i >= t1 ? 0u : t + i < lo || t + i >= hi ? kAlways : mass_key(__ldg(m + t + i));
+        return make_uint4(k[0], k[1], k[2], k[3]);
+    };
+    for (int i = tid; i < 2 * kHist / 4; i += kSelectThreads)
+        reinterpret_cast<uint4 *>(dyn)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid < 2)
+        found[tid] = 0u;
+    __syncthreads();
+    if (need == 0u)
+        prefix = kNanKey;                    // no candidate is above, none of the equal ones stays
 #pragma unroll 1
-        for (int pass = 0; pass < 3; ++pass) {
-            uint32_t *hist = dyn + (pass & 1) * kBins;
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-            reinterpret_cast<uint4 *>(hist)[tid] = make_uint4(0u, 0u, 0u, 0u);
-            __syncthreads();
-            if (pass == 0) {
-                // masses that are exactly 0 are many: counted in a register
-                uint32_t zeros = 0u;
-                constexpr int kU = 8;
-                for (int t = lo + tid; t < hi; t += kU * kSelectThreads) {
-                    float x[kU];
+    for (int pass = 0; pass < (need ? 3 : 1); ++pass) {
+        uint32_t *hist = dyn + (pass & 1) * kHist;
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const uint32_t mask = pass == 2 ? 1023u : 2047u;
+        // masses that are exactly 0 are many: counted in a register
+        uint32_t zeros = 0u;
+        if (pass == 0) {
+            constexpr int kU = kMinCtas > 2 ? 8 : 16;
+#pragma unroll 1
+            for (int t = t0 + tid; t < t1; t += kU * kSelectThreads) {
+                float x[kU];
 #pragma unroll
-                    for (int u = 0; u < kU; ++u)
-                        x[u] = t + u * kSelectThreads < hi ? __ldg(m + t + u * kSelectThreads) : 0.f;
+                for (int u = 0; u < kU; ++u)
+                    x[u] = t + u * kSelectThreads < t1 ? __ldg(m + t + u * kSelectThreads) : 0.f;
 #pragma unroll
-                    for (int u = 0; u < kU; ++u)
-                        if (t + u * kSelectThreads < hi) {
-                            const uint32_t k = mass_key(x[u]);
-                            if (cached)
-                                keys[t + u * kSelectThreads - t0] = k;
-                            if (k == zero_key)
-                                ++zeros;
-                            else
-                                atomicAdd(hist + (k >> 21), 1u);
-                        }
+                for (int u = 0; u < kU; ++u) {
+                    const int at = t + u * kSelectThreads;
+                    if (at >= t1)
+                        break;
+                    uint32_t k = mass_key(x[u]);
+                    if (at < lo || at >= hi)
+                        k = kAlways;
+                    else if (k == zero_key)
+                        ++zeros;
+                    else
+                        atomicAdd(hist + (k >> 21), 1u);
+                    if (cached)
+                        keys[at - t0] = k;
                 }
-                zeros = __reduce_add_sync(0xffffffffu, zeros);
-                if (lane == 0 && zeros)
-                    atomicAdd(hist + (zero_key >> 21), zeros);
-            } else {
-                const int above = shift + bits;
-                uint32_t zeros = 0u;
-                for (int t = lo + tid; t < hi; t += kSelectThreads) {
-                    const uint32_t k = cached ? keys[t - t0] : mass_key(__ldg(m + t));
-                    if ((k ^ prefix) >> above == 0u) {
-                        if (k == zero_key)
+            }
+            if (tid < 3 && cached && t1 + tid - t0 < ((t1 - t0 + 3) & ~3))
+                keys[t1 + tid - t0] = 0u;
+        } else {
+            // keys base .. base + width share the digits found (the topmost is kAlways)
+            const uint32_t width = min((1u << (pass == 1 ? 21 : 10)) - 1u, kNanKey - prefix);
+#pragma unroll 2
+            for (int t = t0 + 4 * tid; t < t1; t += 4 * kSelectThreads) {
+                const uint4 v = four(t);
+                const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (k[i] - prefix <= width) {
+                        if (k[i] == zero_key)
                             ++zeros;
                         else
-                            atomicAdd(hist + (k >> shift & ((1u << bits) - 1u)), 1u);
+                            atomicAdd(hist + (k[i] >> shift & mask), 1u);
                     }
-                }
-                zeros = __reduce_add_sync(0xffffffffu, zeros);
-                if (lane == 0 && zeros)
-                    atomicAdd(hist + (zero_key >> shift & ((1u << bits) - 1u)), zeros);
             }
-            row_sync(ctas);
-            // thread i: the four bins from the top, over all CTAs
-            const int bin = kBins - kBinsPerThread * (tid + 1);
-            uint4 n = make_uint4(0u, 0u, 0u, 0u);
-            for (uint32_t r = 0; r < ctas; ++r) {
-                const uint4 v = ctas == 1 ? *reinterpret_cast<const uint4 *>(hist + bin) : load_of_rank4(of_rank(hist + bin, r));
-                n.x += v.x, n.y += v.y, n.z += v.z, n.w += v.w;
-            }
-            const uint32_t mine = n.x + n.y + n.z + n.w;
-            uint32_t upto = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
-                upto += lane >= o ? v : 0u;
-            }
-            if (lane == 31)
-                warp_sum[warp] = upto;
-            __syncthreads();
-            for (int w = 0; w < warp; ++w)
-                upto += warp_sum[w];
-            uint32_t before = upto - mine;               // keys in higher bins
-            if (before < need && need <= upto) {
-                const uint32_t c[4] = {n.w, n.z, n.y, n.x};
-                int d = bin + 3;
-#pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    if (before + c[i] < need && d == bin + 3 - i) {
-                        before += c[i];
-                        --d;
-                    }
-                found[pass][0] = (uint32_t)d;
-                found[pass][1] = need - before;
-            }
-            __syncthreads();
-            prefix |= found[pass][0] << shift;
-            need = found[pass][1];
         }
+        zeros = __reduce_add_sync(0xffffffffu, zeros);
+        if (lane == 0 && zeros)
+            atomicAdd(hist + (zero_key >> shift & mask), zeros);
+        __syncthreads();
+        if (need == 0u)
+            break;                                   // the keys are there, that was all
+        // the coarse bins, half of one a thread
+        {
+            const uint4 v = reinterpret_cast<const uint4 *>(hist)[tid];
+            uint32_t n = v.x + v.y + v.z + v.w;
+            n += __shfl_xor_sync(0xffffffffu, n, 1);
+            if (!(tid & 1))
+                hist[kBins + tid / 2] = n;
+        }
+        row_sync(ctas);
+        // thread i < 256: coarse bin 255 - i of all CTAs
+        uint32_t n = 0u;
+        if (tid < kCoarse) {
+            const uint32_t *bin = hist + kBins + kCoarse - 1 - tid;
+            if (ctas == 1)
+                n = *bin;
+            else
+#pragma unroll 4
+                for (uint32_t r = 0; r < ctas; ++r)
+                    n += load_of_rank(bin, r);
+        }
+        uint32_t upto = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            upto += lane >= o ? v : 0u;
+        }
+        if (lane == 31)
+            warp_sum[warp] = upto;
+        __syncthreads();
+        if (tid < kCoarse) {
+#pragma unroll
+            for (int w = 0; w < kCoarse / 32; ++w)
+                upto += w < warp ? warp_sum[w] : 0u;
+            if (upto - n < need && need <= upto) {
+                found[0] = (uint32_t)(kCoarse - 1 - tid);
+                found[1] = upto - n;              // keys in higher coarse bins
+            }
+        }
+        __syncthreads();
+        // every warp finds the digit among the 8 bins: lane = 4 ranks x 8 bins, from the top
+        {
+            const uint32_t coarse = found[0];
+            const uint32_t *bin = hist + coarse * 8u + 7u - (lane & 7);
+            uint32_t v = 0u;
+            for (uint32_t r = lane >> 3; r < ctas; r += 4)
+                v += ctas == 1 ? *bin : load_of_rank(bin, r);
+            v += __shfl_xor_sync(0xffffffffu, v, 8);
+            v += __shfl_xor_sync(0xffffffffu, v, 16);
+            uint32_t sum = v;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o, 8);
+                sum += (lane & 7) >= o ? x : 0u;
+            }
+            const uint32_t before = found[1] + sum - v;
+            const uint32_t here = __ballot_sync(0xffffffffu, before < need && need <= before + v) & 255u;
+            const int at = here ? __ffs(here) - 1 : 0;
+            need -= __shfl_sync(0xffffffffu, before, at);
+            prefix |= (coarse * 8u + 7u - (uint32_t)at) << shift;
+        }
+        if (pass == 1) {                             // the first histogram serves again: all have read it
+            for (int i = tid; i < kHist / 4; i += kSelectThreads)
+                reinterpret_cast<uint4 *>(dyn)[i] = make_uint4(0u, 0u, 0u, 0u);
+            __syncthreads();
+        }
+    }
     // `need` of the keys equal to `prefix` stay, all larger ones do.  A warp takes
-    // a run of the slice; first how many of each lie before it.
-    const int run = ((t1 - t0 + kSelectThreads - 1) / kSelectThreads) * 32;
+    // a run of the slice, a lane four positions at a time; first how many of each lie
+    // before it.
+    const int run = (((t1 - t0) + 128 * kSelectWarps - 1) / (128 * kSelectWarps)) * 128;
     const int w0 = min(t1, t0 + warp * run), w1 = min(t1, w0 + run);
-    auto look = [&](int t, bool &above, bool &equal) {
-        above = t < lo || t >= hi;                       // the slice's sinks and recent tokens
-        equal = false;
-        if (!above && any) {
-            const uint32_t k = cached ? keys[t - t0] : mass_key(__ldg(m + t));
-            above = k > prefix;
-            equal = k == prefix;
-        }
-    };
     uint32_t na = 0u, ne = 0u;
-    for (int t = w0 + lane; t < w1; t += 32) {
-        bool above, equal;
-        look(t, above, equal);
-        na += above;
-        ne += equal;
+#pragma unroll 2
+    for (int t = w0 + 4 * lane; t < w1; t += 128) {
+        const uint4 k = four(t);
+        na += (k.x > prefix) + (k.y > prefix) + (k.z > prefix) + (k.w > prefix);
+        ne += (k.x == prefix) + (k.y == prefix) + (k.z == prefix) + (k.w == prefix);
     }
     na = __reduce_add_sync(0xffffffffu, na);
     ne = __reduce_add_sync(0xffffffffu, ne);
@@ -213,7 +252,8 @@ __global__ void __launch_bounds__(kSelectThreads) shkv_select_kernel(const __gri
         warp_counts[warp] = make_uint2(na, ne);
     __syncthreads();
     uint32_t a = 0u, e = 0u;
-    for (int w = 0; w < kSelectThreads / 32; ++w) {
+#pragma unroll
+    for (int w = 0; w < kSelectWarps; ++w) {
         if (w == warp)
             na = a, ne = e;
         a += warp_counts[w].x;
@@ -223,22 +263,45 @@ __global__ void __launch_bounds__(kSelectThreads) shkv_select_kernel(const __gri
         if (tid == 0)
             totals[0] = a, totals[1] = e;
         row_sync(ctas);
-        for (uint32_t r = 0; r < rank; ++r) {
-            const uint2 v = load_of_rank2(of_rank(totals, r));
-            na += v.x, ne += v.y;
+        if (lane < 2) {                                  // lane 0: above, lane 1: equal, of the CTAs before
+            uint32_t v = 0u;
+#pragma unroll 4
+            for (uint32_t r = 0; r < rank; ++r)
+                v += load_of_rank(totals + lane, r);
+            a = v;
         }
+        na += __shfl_sync(0xffffffffu, a, 0);
+        ne += __shfl_sync(0xffffffffu, a, 1);
     }
-    for (int t = w0 + lane; t - lane < w1; t += 32) {
-        bool above = false, equal = false;
-        if (t < w1)
-            look(t, above, equal);
-        const uint32_t ba = __ballot_sync(0xffffffffu, above), be = __ballot_sync(0xffffffffu, equal);
-        const uint32_t left = (1u << lane) - 1u, ea = ne + __popc(be & left);
-        const uint32_t at = na + __popc(ba & left) + min(ea, need);
-        if ((above || (equal && ea < need)) && at < (uint32_t)keep)      // always, unless masses change under the call
-            out[at] = t;
-        na += __popc(ba);
-        ne += __popc(be);
+    for (int t = w0 + 4 * lane; t - 4 * lane < w1; t += 128) {
+        const uint4 v = t < w1 ? four(t) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+        // above in the lower half, equal in the upper half of a word
+        uint32_t mine = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            mine += k[i] > prefix ? 1u : k[i] == prefix ? 1u << 16 : 0u;
+        uint32_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+            upto += lane >= o ? x : 0u;
+        }
+        const uint32_t sum = __shfl_sync(0xffffffffu, upto, 31);
+        if (mine) {
+            uint32_t pa = na + (upto - mine & 0xffffu), pe = ne + (upto - mine >> 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool up = k[i] > prefix, eq = k[i] == prefix;
+                const uint32_t at = pa + min(pe, need);
+                if ((up || (eq && pe < need)) && at < (uint32_t)keep)    // always, unless masses change under the call
+                    out[at] = t + i;
+                pa += up;
+                pe += eq;
+            }
+        }
+        na += sum & 0xffffu;
+        ne += sum >> 16;
     }
     if (ctas > 1)
         row_sync(ctas);                                  // nobody leaves while its counts are read
@@ -256,11 +319,13 @@ cudaError_t launch_select(const SelectParams &p, int num_sms, cudaStream_t strea
     int ctas = 1;
     while (ctas < 8 && 2 * ctas * rows <= 2 * num_sms && longest > 4096 * ctas)
         ctas *= 2;
-    const int64_t slice = (longest + ctas - 1) / ctas;
+    const int64_t slice = ((longest + ctas - 1) / ctas + 3) & ~3;
     const int cached = slice <= kSelectKeys;
-    const uint32_t smem = (uint32_t)(kHistBytes + (cached ? slice * 4 : 0));
-    cudaError_t e = cudaFuncSetAttribute(shkv_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kHistBytes + kSelectKeys * 4);
+    const uint32_t smem = (uint32_t)(2 * kHist * 4 + (cached ? slice * 4 : 0));
+    // two CTAs an SM, or four with fewer registers and loads in flight
+    auto kern = rows * ctas > 2 * num_sms ? shkv_select_kernel<4> : shkv_select_kernel<2>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         2 * kHist * 4 + kSelectKeys * 4);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
@@ -276,7 +341,7 @@ cudaError_t launch_select(const SelectParams &p, int num_sms, cudaStream_t strea
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = ctas > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, shkv_select_kernel, p, cached);
+    return cudaLaunchKernelEx(&cfg, kern, p, cached);
 }
 
 namespace {
