@@ -18,7 +18,7 @@ struct MassIo {
 
 constexpr int kMassMaxCtas = 256;
 constexpr int kMassTile = 128;       // tokens of a tile: rows of an MMA
-constexpr int kMassSpan = 4;         // tiles of an item, at most
+constexpr int kWide = 2 * kMassTile; // tokens of an item with many blocks
 constexpr int kMassRows = 128;       // query rows of a block, at most
 
 // Blocks of rows from which rows lie on the MMA's M dimension.
@@ -26,9 +26,9 @@ inline bool mass_wide(int32_t blocks) { return blocks >= 4; }
 
 // A decode step or a chunk: row r = i * G + j of a (request, KV head g) is
 // query token i, head g * G + j.  Causal: query token i sits at position
-// L_b - n_q + i.  Blocks of `tpt` query tokens, `blocks` in all; an item is `span`
-// (1, 2 or 4) consecutive 128-token tiles of a (request, KV head), items are
-// numbered request-major, then by head.  CTA c takes the blocks from (cut_item[c],
+// L_b - n_q + i.  Blocks of `tpt` query tokens, `blocks` in all; an item is
+// kMassTile (few blocks) or kWide consecutive tokens of a (request, KV head), items
+// are numbered request-major, then by head.  CTA c takes the blocks from (cut_item[c],
 // cut_block[c]) up to (cut_item[c + 1], cut_block[c + 1]); block 0 stands for
 // the item's first.
 struct MassParams {
@@ -37,9 +37,9 @@ struct MassParams {
     MassIo mass;
     const int32_t *block_table, *seq_lens;
     uint32_t *err;
-    float *pieces;                   // [2 * CTAs, kMassSpan * kMassTile]: sums of a range's first and last, cut item
+    float *pieces;                   // [2 * CTAs, kWide]: sums of a range's first and last, cut item
     int32_t batch, n_q, hkv, group, head_dim, page_size, max_pages, num_pages, causal;
-    int32_t tpt, blocks, span, num_ctas;
+    int32_t tpt, blocks, item_tokens, num_ctas;
     float scale_log2, decay;
     int32_t cut_item[kMassMaxCtas + 1];
     int32_t cut_block[kMassMaxCtas + 1];

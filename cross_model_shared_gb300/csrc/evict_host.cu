@@ -99,7 +99,7 @@ bool make_q_map(CUtensorMap *tm, const void *q, const shkv_pool_config &c, int32
 // Bytes of the cut items' sums.
 size_t piece_bytes(const shkv_pool *pool)
 {
-    return (size_t)2 * std::min(pool->num_sms, kMassMaxCtas) * kMassSpan * kMassTile * sizeof(float);
+    return (size_t)2 * std::min(pool->num_sms, kMassMaxCtas) * kWide * sizeof(float);
 }
 
 // Cuts the items into at most `limit` ranges of about equal cost, counted in
@@ -110,7 +110,7 @@ constexpr int64_t kItemCost = 1, kMinPiece = 2;
 
 bool plan_mass(MassParams &p, int limit)
 {
-    const int tokens = p.span * kMassTile;
+    const int tokens = p.item_tokens;
     // cost of item `at` of a request's head, and of all of the head's
     auto cost = [&](int L, int at) -> int64_t {
         const int past = mass_past(L, p.n_q, p.causal);
@@ -121,7 +121,7 @@ bool plan_mass(MassParams &p, int limit)
     };
     // the first `even` items take part in every block
     auto even = [&](int L) -> int64_t { return std::max(0, std::min(L, mass_past(L, p.n_q, p.causal)) / tokens); };
-    const int64_t full = kItemCost + (int64_t)p.span * p.blocks;
+    const int64_t full = kItemCost + (int64_t)(tokens / kMassTile) * p.blocks;
     auto head = [&](int L) -> int64_t {
         int64_t k = even(L) * full;
         for (int at = (int)even(L); at * tokens < L; ++at)
@@ -132,7 +132,7 @@ bool plan_mass(MassParams &p, int limit)
     for (int b = 0; b < p.batch; ++b)
         total += p.hkv * head(p.lens[b]);
     const int64_t C = std::max<int64_t>(
-        1, std::min<int64_t>(limit, p.blocks > 1 ? total / (p.span * kMinPiece) : p.item0[p.batch]));
+        1, std::min<int64_t>(limit, mass_wide(p.blocks) ? total / (2 * kMinPiece) : p.item0[p.batch]));
     int n = 0, b = 0;
     int64_t before = 0, h = head(p.lens[0]);
     bool cut = false;
@@ -175,23 +175,6 @@ bool plan_mass(MassParams &p, int limit)
     return cut;
 }
 
-// Tiles of an item: two with many blocks; else four share a block's rows, fewer
-// where that leaves the CTAs less than four (item, block) steps each.
-int32_t item_span(int32_t batch, const int32_t *lens, int32_t hkv, int32_t blocks, int ctas)
-{
-    if (mass_wide(blocks))
-        return 2;
-    int32_t span = kMassSpan;
-    for (; span > 1; span /= 2) {
-        int64_t items = 0;
-        for (int b = 0; b < batch; ++b)
-            items += ((int64_t)lens[b] + span * kMassTile - 1) / (span * kMassTile);
-        if (items * hkv * blocks >= 4 * ctas)
-            break;
-    }
-    return span;
-}
-
 // Both forms: the n_q query tokens of every request.
 shkv_status add_mass(shkv_pool *pool, int32_t batch, int32_t n_q, int32_t hq, const void *q, int64_t q_request,
                      int64_t q_token, float scale, const float *lse, int64_t lse_request, int64_t lse_token,
@@ -219,12 +202,12 @@ shkv_status add_mass(shkv_pool *pool, int32_t batch, int32_t n_q, int32_t hq, co
     p.tpt = std::min(kMassRows / p.group, n_q);
     p.blocks = (n_q + p.tpt - 1) / p.tpt;
     const int ctas = std::min(pool->num_sms, kMassMaxCtas);
-    p.span = item_span(batch, pool->lens.data(), c.num_kv_heads, p.blocks, ctas);
+    p.item_tokens = mass_wide(p.blocks) ? kWide : kMassTile;
     int64_t items = 0;
     for (int b = 0; b < batch; ++b) {
         p.lens[b] = pool->lens[b];
         p.item0[b] = (int32_t)items;
-        items += ((int64_t)pool->lens[b] + p.span * kMassTile - 1) / (p.span * kMassTile) * c.num_kv_heads;
+        items += ((int64_t)pool->lens[b] + p.item_tokens - 1) / p.item_tokens * c.num_kv_heads;
         if (items > INT32_MAX)
             return SHKV_ERR_UNSUPPORTED;
     }

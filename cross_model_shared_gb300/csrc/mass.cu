@@ -96,32 +96,14 @@ struct Turn {
     }
 };
 
-// A ring of n slots dealt to the tiles of an item: tile x uses x, x + span, ... in
-// turn, whatever the other tiles do.  So a slot is waited for by the same role every
-// time, in order: with slots handed round in one ring, an item of fewer tiles would
-// shift them, and a role that runs ahead could wait for a phase while the one before
-// is still open, which a parity wait takes for the phase before that.  Four bits a
-// tile count its uses, modulo twice its slots.
-struct TileRing {
-    uint32_t counts = 0u;
-    int span, log2n;
-    __device__ TileRing(int span_, int n) : span(span_), log2n(n >= 8 * span_ ? 3 : n >= 4 * span_ ? 2 : n >= 2 * span_) {}
-    __device__ int slot(int x) const { return x + span * (int)(counts >> 4 * x & ((1u << log2n) - 1u)); }
-    __device__ uint32_t parity(int x) const { return counts >> (4 * x + log2n) & 1u; }
-    __device__ void next(int x)
-    {
-        const uint32_t n = ((counts >> 4 * x & 15u) + 1u) & ((2u << log2n) - 1u);
-        counts = (counts & ~(15u << 4 * x)) | n << 4 * x;
-    }
-};
-
 // The items of a CTA's range, one after another; every role walks them alike.
 struct Walk {
     int item, last, b, g, at, items;     // `last`: one past the range's last item; item `at` of the head's `items`
+    int step;                            // items taken together: with few blocks up to four tiles of a head
     int L, past, t0;
     int begin, end;                      // blocks of this item in the range
     bool fresh;                          // another (request, KV head) than the item before
-    // whether block k has a row that sees a token of tile x
+    // whether block k has a row that sees a token of the step's tile x
     __device__ bool sees(const MassParams &p, int k, int x) const
     {
         return t0 + x * kMassTile - past < min((k + 1) * p.tpt, p.n_q);
@@ -133,12 +115,13 @@ __device__ __forceinline__ void walk_request(const MassParams &p, Walk &w)
 {
     w.L = p.lens[w.b];
     w.past = mass_past(w.L, p.n_q, p.causal);
-    w.items = (w.L + p.span * kMassTile - 1) / (p.span * kMassTile);
+    w.items = (w.L + p.item_tokens - 1) / (p.item_tokens);
 }
 
 __device__ __forceinline__ void walk_item(const MassParams &p, Walk &w)
 {
-    w.t0 = w.at * p.span * kMassTile;
+    w.t0 = w.at * p.item_tokens;
+    w.step = p.item_tokens == kWide ? 1 : min(4, min(w.items - w.at, w.last - w.item));
     w.begin = mass_block0(w.t0, w.past, p.tpt);
     if (w.item == p.cut_item[blockIdx.x])
         w.begin = max(w.begin, p.cut_block[blockIdx.x]);
@@ -178,10 +161,12 @@ __device__ __forceinline__ bool walk_first(const MassParams &p, Walk &w)
 
 __device__ __forceinline__ bool walk_next(const MassParams &p, Walk &w)
 {
-    if (++w.item >= w.last)
+    w.item += w.step;
+    if (w.item >= w.last)
         return false;
     w.fresh = false;
-    if (++w.at == w.items) {
+    w.at += w.step;
+    if (w.at == w.items) {
         w.at = 0;
         w.fresh = true;
         if (++w.g == p.hkv) {
@@ -196,12 +181,19 @@ __device__ __forceinline__ bool walk_next(const MassParams &p, Walk &w)
     return true;
 }
 
-// A block of rows is copied again for every item, unless it is a head's only one.
-__device__ __forceinline__ bool new_rows(const MassParams &p, const Walk &w) { return p.blocks > 1 || w.fresh; }
+// ---------------------------------------------------------------------------
+// few blocks: tokens on M, an item is a tile, up to four are taken together
+// ---------------------------------------------------------------------------
+// Tile n of a range (n = 0, 1, ..) uses K slot n mod kK, S buffer n mod 4, and belongs
+// to issuer n mod 2 and to the four warps n mod 4.  As kK is a multiple of 4, a slot
+// is waited for by the same role every time, in order: a role that waited only for
+// some of a slot's phases could look at the slot while the phase before is still
+// open, and a parity wait takes that for the phase before it, which is over.
+__device__ __forceinline__ int tile_of(const MassParams &p, const Walk &w) { return w.item - p.cut_item[blockIdx.x]; }
 
 // K tiles, a lane per (column half, page) of a tile.  A lane also holds one of the
-// item's table entries, read an item ahead.  A page outside the pool is left out
-// and flagged; the tile's threads look at their table entries themselves.
+// table entries of up to four tiles, read four tiles ahead.  A page outside the pool
+// is left out and flagged; the tile's threads look at their table entries themselves.
 template <int D>
 __device__ void copy_k(const CUtensorMap *tm, const MassParams &p, const Ctx<D> &c)
 {
@@ -211,13 +203,12 @@ __device__ void copy_k(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
     const uint64_t pol = l2_evict_first_policy();
     auto entry = [&](const Walk &w) {
         const int pg = w.t0 / P + lane;
-        return lane < p.span * RB && pg * P < w.L ? __ldg(p.block_table + (int64_t)w.b * p.max_pages + pg) : -1;
+        return lane < w.step * RB && pg * P < w.L ? __ldg(p.block_table + (int64_t)w.b * p.max_pages + pg) : -1;
     };
     Walk w;
-    TileRing kt(p.span, Ring<D>::kK);
     bool alive = true, more = walk_first(p, w);
-    uint32_t armed = 0u, armed_parity = 0u;  // slots with a copy, and of which phase
-    int id = more ? entry(w) : -1;
+    int issued = 0, id = more ? entry(w) : -1;
+#pragma unroll 1
     while (more) {
         Walk next = w;
         more = walk_next(p, next);
@@ -225,17 +216,16 @@ __device__ void copy_k(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
         if (lane == 0 && w.fresh && w.at == 0 && w.g == 0 && __ldg(p.seq_lens + w.b) != w.L)
             atomicOr(p.err, SHKV_ERRF_SEQ_LEN);
 #pragma unroll 1
-        for (int x = 0; x < p.span && w.t0 + x * kMassTile < w.L; ++x) {
-            const int page = __shfl_sync(0xffffffffu, id, (x * RB + rb) & 31);
+        for (int x = 0; x < w.step; ++x) {
+            const int slot = issued % Ring<D>::kK, page = __shfl_sync(0xffffffffu, id, (x * RB + rb) & 31);
             const bool there = copier && w.t0 + x * kMassTile + rb * P < w.L;
             const bool inside = there && (uint32_t)page < (uint32_t)p.num_pages;
             if (there && !inside)
                 atomicOr(p.err, SHKV_ERRF_PAGE_OOB);
             const uint32_t mask = __ballot_sync(0xffffffffu, inside);
-            const int slot = kt.slot(x);
             bool ok = true;
             if (alive && lane == 0) {
-                ok = c.wait(c.k_empty(slot), kt.parity(x) ^ 1u);
+                ok = c.wait(c.k_empty(slot), ((uint32_t)(issued / Ring<D>::kK) & 1u) ^ 1u);
                 if (ok)
                     mbar_arrive_expect_tx(c.k_full(slot), (uint32_t)__popc(mask) * (uint32_t)P * 128u);
             }
@@ -245,21 +235,17 @@ __device__ void copy_k(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
             if (inside)
                 tma_load_2d(c.k_slot(slot) + (uint32_t)half * kHalfBytes + (uint32_t)(rb * P) * 128u, tm, half * 64,
                             (page * p.hkv + w.g) * P, c.k_full(slot), pol);
-            armed |= 1u << slot;
-            armed_parity = (armed_parity & ~(1u << slot)) | kt.parity(x) << slot;
-            kt.next(x);
+            ++issued;
         }
         w = next;
         id = next_id;
     }
     if (!alive && lane == 0)                 // wait for the copies in flight
-        for (int s = 0; s < Ring<D>::kK; ++s)
-            if (armed >> s & 1u)
-                mbar_drain_bounded(c.k_full(s), armed_parity >> s & 1u);
+        for (int i = max(0, issued - Ring<D>::kK); i < issued; ++i)
+            mbar_drain_bounded(c.k_full(i % Ring<D>::kK), (uint32_t)(i / Ring<D>::kK) & 1u);
 }
 
-// Q blocks and what their rows' log-sum-exps take off the scores; a row beyond
-// the block's, or one that attends nothing, gets -inf and so weighs nothing.
+// Block k of the rows of an item's head into a Q slot.
 template <int D>
 __device__ __forceinline__ void copy_block(const CUtensorMap *tm, const MassParams &p, const Ctx<D> &c, const Walk &w, int k,
                                            int slot)
@@ -277,6 +263,9 @@ __device__ __forceinline__ void copy_block(const CUtensorMap *tm, const MassPara
             : "memory");
 }
 
+// The blocks of every head that the range comes to, and what their rows'
+// log-sum-exps take off the scores; a row beyond the block's, or one that attends
+// nothing, gets -inf and so weighs nothing.
 template <int D>
 __device__ void copy_q(const CUtensorMap *tm, const MassParams &p, const Ctx<D> &c)
 {
@@ -285,33 +274,21 @@ __device__ void copy_q(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
     Turn turn;
     bool alive = true;
     int issued = 0;
-    int tok[kMassRows / 32], head[kMassRows / 32];       // of the lane's rows in a block
-#pragma unroll
-    for (int j = 0; j < kMassRows / 32; ++j) {
-        tok[j] = (lane + 32 * j) / p.group;
-        head[j] = lane + 32 * j - tok[j] * p.group;
-    }
     if (!walk_first(p, w))
         return;
     do {
-        if (!new_rows(p, w))
+        if (!w.fresh)
             continue;
         const float *src = p.lse + w.b * p.lse_request + w.g * p.group;
-        float ahead[kMassRows / 32];         // of the next block
-        auto load = [&](int k) {
-            const int i0 = k * p.tpt, rows = k < w.end ? min(p.tpt, p.n_q - i0) * p.group : 0;
-#pragma unroll
-            for (int j = 0; j < kMassRows / 32; ++j)
-                ahead[j] = lane + 32 * j < rows ? lse_base2(__ldg(src + (i0 + tok[j]) * p.lse_token + head[j])) : INFINITY;
-        };
-        load(w.begin);
 #pragma unroll 1
-        for (int k = w.begin; k < w.end; ++k) {
+        for (int k = 0; k < p.blocks; ++k) {
+            const int i0 = k * p.tpt, rows = min(p.tpt, p.n_q - i0) * p.group;
             float off[kMassRows / 32];
 #pragma unroll
-            for (int j = 0; j < kMassRows / 32; ++j)
-                off[j] = ahead[j];
-            load(k + 1);
+            for (int j = 0; j < kMassRows / 32; ++j) {
+                const int r = lane + 32 * j;
+                off[j] = r < rows ? lse_base2(__ldg(src + (i0 + r / p.group) * p.lse_token + r % p.group)) : INFINITY;
+            }
             bool ok = true;
             if (alive && lane == 0)
                 ok = c.wait(c.q_empty(turn.slot), turn.parity ^ 1u);
@@ -333,6 +310,26 @@ __device__ void copy_q(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
             mbar_drain_bounded(c.q_full(i % Ring<D>::kQ), (uint32_t)(i / Ring<D>::kQ) & 1u);
 }
 
+// The next head's blocks: leaves the last one's (`done` on each of their slots) and
+// waits for these.  `turn` is the first one's.
+template <int D, typename Done>
+__device__ __forceinline__ bool next_blocks(const MassParams &p, const Ctx<D> &c, Turn &turn, bool first, bool alive, Done done)
+{
+    if (!first)
+#pragma unroll 1
+        for (int k = 0; k < p.blocks; ++k) {
+            done(turn.slot);
+            turn.next(Ring<D>::kQ);
+        }
+    Turn t = turn;
+#pragma unroll 1
+    for (int k = 0; k < p.blocks; ++k) {
+        alive = __all_sync(0xffffffffu, alive && c.wait(c.q_full(t.slot), t.parity));
+        t.next(Ring<D>::kQ);
+    }
+    return alive;
+}
+
 // The issuers' warps run converged, so that addresses and descriptors stay in
 // uniform registers; one lane issues.
 template <int D>
@@ -341,10 +338,7 @@ __device__ __forceinline__ bool issuer_wait(const Ctx<D> &c, uint32_t bar, uint3
     return __all_sync(0xffffffffu, alive && c.wait(bar, parity));
 }
 
-// S = K Q^T for every block of the range and every tile of one parity.  A slot of K
-// is free after the item's last block, one of Q when the next block's rows are
-// needed.  (Loops are kept rolled: the roles of an SM sub-partition share its
-// instruction cache.)
+// S = K Q^T for the range's tiles of one parity and every block that sees them.
 template <int D>
 __device__ void issue(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int odd)
 {
@@ -352,38 +346,35 @@ __device__ void issue(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int o
     const bool one = (threadIdx.x & 31) == 0;
     Walk w;
     Turn qt;
-    TileRing kt(p.span, Ring<D>::kK), st(p.span, 4);
-    bool alive = true, rows_in = false;
+    uint32_t s_par = 0xfu;                   // of the S buffers' next waits
+    bool alive = true, first = true;
     if (!walk_first(p, w))
         return;
     do {
-        const int tiles = min(p.span, (w.L - w.t0 + kMassTile - 1) / kMassTile);
-        uint32_t k_in = 0u;                  // tiles whose K has been waited for
+        if (w.fresh) {
+            alive = next_blocks<D>(p, c, qt, first, alive, [&](int slot) {
+                if (one)
+                    umma_commit(c.q_empty(slot));
+            });
+            first = false;
+        }
+        const int n0 = tile_of(p, w);
 #pragma unroll 1
-        for (int k = w.begin; k < w.end; ++k) {
-            if (new_rows(p, w)) {
-                if (rows_in) {
-                    if (one)
-                        umma_commit(c.q_empty(qt.slot));
-                    qt.next(Ring<D>::kQ);
-                }
-                rows_in = true;
-                alive = issuer_wait(c, c.q_full(qt.slot), qt.parity, alive);
-            }
-            const int rows = min(p.tpt, p.n_q - k * p.tpt) * p.group;
-            const uint32_t idesc = umma_idesc_bf16(kMassTile, (rows + 15) & ~15, false, false);
-            const uint64_t qd = qd0 + (((uint32_t)qt.slot * Ring<D>::kSlot) >> 4);
+        for (int x = (n0 ^ odd) & 1; x < w.step; x += 2) {
+            const int n = n0 + x, s = n & 3, slot = n % Ring<D>::kK;
+            const uint64_t kd = kd0 + (((uint32_t)slot * Ring<D>::kSlot) >> 4);
+            alive = issuer_wait(c, c.k_full(slot), (uint32_t)(n / Ring<D>::kK) & 1u, alive);
+            Turn t = qt;
 #pragma unroll 1
-            for (int x = odd; x < tiles; x += 2) {
+            for (int k = 0; k < p.blocks; ++k, t.next(Ring<D>::kQ)) {
                 if (!w.sees(p, k, x))
-                    break;
-                const int s = st.slot(x), slot = kt.slot(x);
-                if (!(k_in >> x & 1u))
-                    alive = issuer_wait(c, c.k_full(slot), kt.parity(x), alive);
-                k_in |= 1u << x;
-                alive = issuer_wait(c, c.s_empty(s), st.parity(x) ^ 1u, alive);
+                    continue;
+                const int rows = min(p.tpt, p.n_q - k * p.tpt) * p.group;
+                const uint32_t idesc = umma_idesc_bf16(kMassTile, (rows + 15) & ~15, false, false);
+                const uint64_t qd = qd0 + (((uint32_t)t.slot * Ring<D>::kSlot) >> 4);
+                alive = issuer_wait(c, c.s_empty(s), s_par >> s & 1u, alive);
+                s_par ^= 1u << s;
                 tc_fence_after();
-                const uint64_t kd = kd0 + (((uint32_t)slot * Ring<D>::kSlot) >> 4);
                 if (one) {
                     if (alive) {
 #pragma unroll
@@ -393,20 +384,11 @@ __device__ void issue(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int o
                         }
                     }
                     umma_commit(c.s_full(s));
-                    if (k == w.end - 1)
+                    if (k == p.blocks - 1)
                         umma_commit(c.k_empty(slot));
                 }
                 __syncwarp();
-                st.next(x);
             }
-        }
-        for (int x = odd; x < tiles; x += 2) {
-            if (!(k_in >> x & 1u)) {         // a range that ends before the tile's first block
-                alive = issuer_wait(c, c.k_full(kt.slot(x)), kt.parity(x), alive);
-                if (one)
-                    umma_commit(c.k_empty(kt.slot(x)));
-            }
-            kt.next(x);
         }
     } while (walk_next(p, w));
     if (one) {
@@ -496,78 +478,69 @@ __device__ __forceinline__ float weigh(uint32_t taddr, uint32_t lse, int n, int 
     return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
-// The weights of tile x of every item, and its masses.
+// The weights of every fourth tile, and its masses.
 template <int D>
-__device__ void add_up(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int x)
+__device__ void add_up(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int four)
 {
-    const int lane = threadIdx.x & 31, row = threadIdx.x & 127;
-    const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;
+    const int lane = threadIdx.x & 31;
+    const uint32_t taddr = tmem + ((uint32_t)(threadIdx.x & 96) << 16) + 128u * (uint32_t)four;
     Walk w;
     Turn qt;
-    TileRing st(p.span, 4);
-    bool alive = true, rows_in = false;
+    uint32_t s_par = 0u;
+    bool alive = true, first = true;
     if (!walk_first(p, w))
         return;
     do {
-        const bool whole = w.whole(p), mine = x < p.span && w.t0 + x * kMassTile < w.L;
-        const int t = w.t0 + x * kMassTile + row;
+        if (w.fresh) {
+            alive = next_blocks<D>(p, c, qt, first, alive, [&](int slot) {
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(c.q_empty(slot));
+            });
+            first = false;
+        }
+        const int x = (four - tile_of(p, w)) & 3;
+        if (x >= w.step)
+            continue;
+        const int t = w.t0 + x * kMassTile + (threadIdx.x & 127);
         float old = 0.f, sum = 0.f;
         int page = -1;
-        if (mine && t < w.L) {               // looked at when the sum is there
+        if (t < w.L) {                       // looked at when the sum is there
             page = __ldg(p.block_table + (int64_t)w.b * p.max_pages + t / p.page_size);
-            if (whole && p.mass.in)
+            if (p.mass.in)
                 old = p.mass.in[w.b * p.mass.in_request + w.g * p.mass.in_head + t];
         }
+        Turn q = qt;
 #pragma unroll 1
-        for (int k = w.begin; k < w.end; ++k) {
-            if (new_rows(p, w)) {
-                if (rows_in) {
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(c.q_empty(qt.slot));
-                    qt.next(Ring<D>::kQ);
-                }
-                rows_in = true;
-                if (alive)
-                    alive = c.wait(c.q_full(qt.slot), qt.parity);
-            }
-            if (!mine || !w.sees(p, k, x))
+        for (int k = 0; k < p.blocks; ++k, q.next(Ring<D>::kQ)) {
+            if (!w.sees(p, k, x))
                 continue;
             const int i0 = k * p.tpt, rows = min(p.tpt, p.n_q - i0) * p.group;
-            const int s = st.slot(x);
-            if (alive)
-                alive = c.wait(c.s_full(s), st.parity(x));
-            alive = __all_sync(0xffffffffu, alive);
+            alive = __all_sync(0xffffffffu, alive && c.wait(c.s_full(four), s_par));
+            s_par ^= 1u;
             if (alive) {
                 tc_fence_after();
                 // query tokens before t - past do not see the thread's token
-                const int first = (t - w.past - i0) * p.group, latest = first + (31 - lane) * p.group;
-                const uint32_t taddr = tmem + lanes + (uint32_t)s * 128u;
+                const int first_row = (t - w.past - i0) * p.group, latest = first_row + (31 - lane) * p.group;
 #pragma unroll 1
                 for (int h = 0; h < rows; h += 64)
-                    sum += weigh(taddr + (uint32_t)h, c.lse(qt.slot) + 4u * h, min(64, rows - h), first - h, latest - h,
-                                 p.scale_log2, h + 64 >= rows, c.s_empty(s));
+                    sum += weigh(taddr + (uint32_t)h, c.lse(q.slot) + 4u * h, min(64, rows - h), first_row - h, latest - h,
+                                 p.scale_log2, h + 64 >= rows, c.s_empty(four));
             } else if (lane == 0) {
-                mbar_arrive(c.s_empty(s));
+                mbar_arrive(c.s_empty(four));
             }
-            st.next(x);
         }
-        if (!mine || t >= w.L)
+        if (t >= w.L)
             continue;
         if ((uint32_t)page >= (uint32_t)p.num_pages)
             sum = 0.f;
-        if (!whole)
-            p.pieces[(int64_t)piece_of(p, w) * (kMassSpan * kMassTile) + t - w.t0] = sum;
-        else
-            p.mass.out[w.b * p.mass.out_request + w.g * p.mass.out_head + t] =
-                p.mass.in ? fmaf(p.decay, old, sum) : sum;
+        p.mass.out[w.b * p.mass.out_request + w.g * p.mass.out_head + t] = p.mass.in ? fmaf(p.decay, old, sum) : sum;
     } while (walk_next(p, w));
 }
 
 // ---------------------------------------------------------------------------
 // many blocks: rows on M, 256 tokens on N
 // ---------------------------------------------------------------------------
-constexpr int kWide = 2 * kMassTile;         // tokens of an item
 
 // An item's K, [column half][256 tokens][128 B], a lane per (half, page); pages as
 // in copy_k().
@@ -797,7 +770,7 @@ __device__ void add_up_wide(const MassParams &p, const Ctx<D> &c, uint32_t tmem,
                                 (uint32_t)p.num_pages;
             const float sum = inside ? (v[0] + v[1]) + (v[2] + v[3]) : 0.f;
             if (!w.whole(p))
-                p.pieces[(int64_t)piece_of(p, w) * (kMassSpan * kMassTile) + threadIdx.x] = sum;
+                p.pieces[(int64_t)piece_of(p, w) * kWide + threadIdx.x] = sum;
             else
                 p.mass.out[w.b * p.mass.out_request + w.g * p.mass.out_head + t] =
                     p.mass.in ? fmaf(p.decay, p.mass.in[w.b * p.mass.in_request + w.g * p.mass.in_head + t], sum) : sum;
@@ -886,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Items that ranges cut: the sums of the pieces, in the order of the blocks.
 // CTA c looks at the cut before range c and does an item's first.
-__global__ void __launch_bounds__(kMassSpan *kMassTile) shkv_mass_join_kernel(const __grid_constant__ MassParams p)
+__global__ void __launch_bounds__(kWide) shkv_mass_join_kernel(const __grid_constant__ MassParams p)
 {
     pdl_wait_prior();
     pdl_launch_dependents();
@@ -901,13 +874,13 @@ __global__ void __launch_bounds__(kMassSpan *kMassTile) shkv_mass_join_kernel(co
         else
             hi = mid;
     }
-    const int tokens = p.span * kMassTile, items = (p.lens[b] + tokens - 1) / tokens;
+    const int tokens = p.item_tokens, items = (p.lens[b] + tokens - 1) / tokens;
     const int g = (item - p.item0[b]) / items, t = (item - p.item0[b]) % items * tokens + u;
     if (u >= tokens || t >= p.lens[b])
         return;
-    float sum = p.pieces[(int64_t)(2 * (c - 1) + 1) * (kMassSpan * kMassTile) + u];
+    float sum = p.pieces[(int64_t)(2 * (c - 1) + 1) * (kWide) + u];
     for (int i = c; i < p.num_ctas && p.cut_item[i] == item; ++i)
-        sum += p.pieces[(int64_t)(2 * i) * (kMassSpan * kMassTile) + u];
+        sum += p.pieces[(int64_t)(2 * i) * (kWide) + u];
     p.mass.out[b * p.mass.out_request + g * p.mass.out_head + t] =
         p.mass.in ? fmaf(p.decay, p.mass.in[b * p.mass.in_request + g * p.mass.in_head + t], sum) : sum;
 }
@@ -940,7 +913,7 @@ cudaError_t launch_mass(const CUtensorMap &tm_k, const CUtensorMap &tm_q, const 
     if (e == cudaSuccess)
         e = launch_pdl(kern, p.num_ctas, kThreads, smem, stream, tm_k, tm_q, p);
     if (e == cudaSuccess && pieces)
-        e = launch_pdl(shkv_mass_join_kernel, p.num_ctas - 1, kMassSpan * kMassTile, 0u, stream, p);
+        e = launch_pdl(shkv_mass_join_kernel, p.num_ctas - 1, kWide, 0u, stream, p);
     return e;
 }
 
