@@ -41,7 +41,7 @@ EXPORTS = [
     "shkv_partition_requests", "shkv_selftest_bounded_wait", "shkv_q8_pool_create", "shkv_q8_pool_destroy",
     "shkv_q8_pool_set_seq_lens", "shkv_q8_pool_get_seq_lens", "shkv_q8_check_errors", "shkv_q8_append_kv",
     "shkv_q8_read_kv", "shkv_q8_workspace_size", "shkv_q8_decode_attention", "shkv_q8_chunk_attention",
-    "shkv_decode_mass", "shkv_prefill_mass", "shkv_prefill_mass_workspace_size", "shkv_select_tokens", "shkv_evict_tokens",
+    "shkv_decode_mass", "shkv_prefill_mass", "shkv_prefill_mass_workspace_size", "shkv_select_tokens", "shkv_select_width", "shkv_evict_tokens",
 ]
 
 SHKV_CONSUMER_AUTO = -1
@@ -188,6 +188,7 @@ def load() -> ctypes.CDLL:
                               mass, vp, ctypes.c_size_t, vp],
         "shkv_prefill_mass_workspace_size": [vp, ctypes.POINTER(ctypes.c_size_t)],
         "shkv_select_tokens": [vp, i32, mass, i32p, i32, i32, vp, i64, vp],
+        "shkv_select_width": [vp, i32, i32p, ctypes.POINTER(i32)],
         "shkv_evict_tokens": [vp, i32, i32p, vp, i64, vp, i64, vp, i64, i32p, mass, mass, vp],
     }
     for name, args in sig.items():
@@ -448,6 +449,12 @@ def shkv_select_tokens(pool: int, batch: int, mass: shkv_mass, keep: int, sink: 
                        index_stride: int, stream: int) -> None:
     _check(load().shkv_select_tokens(pool, batch, _ref(mass), keep, sink, recent, index, index_stride, stream),
            "shkv_select_tokens")
+
+
+def shkv_select_width(pool: int, batch: int, keep: int) -> int:
+    n = ctypes.c_int32()
+    _check(load().shkv_select_width(pool, batch, keep, ctypes.byref(n)), "shkv_select_width")
+    return n.value
 
 
 def shkv_evict_tokens(pool: int, batch: int, keep: int, index: int, index_stride: int, new_table: int,

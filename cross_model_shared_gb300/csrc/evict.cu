@@ -11,7 +11,7 @@ namespace shkv {
 
 namespace {
 
-constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
+constexpr int kSelectThreads = 256;                      // 512: a batch of 512 rows of 1K to 8K tokens takes 20.7 us, not 18.9
 constexpr int kBins = 2048, kCoarse = 256;               // of an 11-bit digit, and by its upper 8 bits
 constexpr int kHist = kBins + kCoarse;                   // words of a histogram
 constexpr int kSelectKeys = 49152;                       // keys of a CTA's slice that it holds in shared memory
@@ -61,14 +61,14 @@ __device__ __forceinline__ uint32_t load_of_rank(const uint32_t *p, uint32_t ran
 // keys above and, by position, as many of the equal ones as still fit are written.
 // A slice's keys stay in shared memory between the passes, four of a thread side by
 // side.  Bound by the latency of its steps.
-template <int kMinCtas>
-__global__ void __launch_bounds__(kSelectThreads, kMinCtas)
+__global__ void __launch_bounds__(kSelectThreads, 4)
     shkv_select_kernel(const __grid_constant__ SelectParams p, int cached)
 {
+    constexpr int kThreads = kSelectThreads, kWarps = kThreads / 32;
     extern __shared__ __align__(16) uint32_t dyn[];
-    __shared__ uint32_t warp_sum[kSelectWarps], found[2];            // found: coarse bin, keys in higher ones
+    __shared__ uint32_t warp_sum[kWarps], found[2];            // found: coarse bin, keys in higher ones
     __shared__ uint32_t totals[2];
-    __shared__ uint2 warp_counts[kSelectWarps];
+    __shared__ uint2 warp_counts[kWarps];
     uint32_t *const keys = dyn + 2 * kHist;
     uint32_t rank, ctas;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kSelectThreads, kMinCtas)
     const int row = blockIdx.x / ctas, b = row / p.hkv, g = row % p.hkv;
     const int L = p.lens[b], keep = min(p.keep[b], L);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
-    const int all = rank * kSelectThreads + tid, step = ctas * kSelectThreads;
+    const int all = rank * kThreads + tid, step = ctas * kThreads;
     int32_t *out = p.index + (int64_t)row * p.index_stride;
     if (g == 0 && all == 0 && p.seq_lens[b] != L)
         atomicOr(p.err, SHKV_ERRF_SEQ_LEN);
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kSelectThreads, kMinCtas)
             k[i] = t + i >= t1 ? 0u : t + i < lo || t + i >= hi ? kAlways : mass_key(__ldg(m + t + i));
         return make_uint4(k[0], k[1], k[2], k[3]);
     };
-    for (int i = tid; i < 2 * kHist / 4; i += kSelectThreads)
+    for (int i = tid; i < 2 * kHist / 4; i += kThreads)
         reinterpret_cast<uint4 *>(dyn)[i] = make_uint4(0u, 0u, 0u, 0u);
     if (tid < 2)
         found[tid] = 0u;
@@ -120,16 +120,16 @@ __global__ void __launch_bounds__(kSelectThreads, kMinCtas)
         // masses that are exactly 0 are many: counted in a register
         uint32_t zeros = 0u;
         if (pass == 0) {
-            constexpr int kU = kMinCtas > 2 ? 8 : 16;
+            constexpr int kU = 16;
 #pragma unroll 1
-            for (int t = t0 + tid; t < t1; t += kU * kSelectThreads) {
+            for (int t = t0 + tid; t < t1; t += kU * kThreads) {
                 float x[kU];
 #pragma unroll
                 for (int u = 0; u < kU; ++u)
-                    x[u] = t + u * kSelectThreads < t1 ? __ldg(m + t + u * kSelectThreads) : 0.f;
+                    x[u] = t + u * kThreads < t1 ? __ldg(m + t + u * kThreads) : 0.f;
 #pragma unroll
                 for (int u = 0; u < kU; ++u) {
-                    const int at = t + u * kSelectThreads;
+                    const int at = t + u * kThreads;
                     if (at >= t1)
                         break;
                     uint32_t k = mass_key(x[u]);
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kSelectThreads, kMinCtas)
             // keys base .. base + width share the digits found (the topmost is kAlways)
             const uint32_t width = min((1u << (pass == 1 ? 21 : 10)) - 1u, kNanKey - prefix);
 #pragma unroll 2
-            for (int t = t0 + 4 * tid; t < t1; t += 4 * kSelectThreads) {
+            for (int t = t0 + 4 * tid; t < t1; t += 4 * kThreads) {
                 const uint4 v = four(t);
                 const uint32_t k[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -168,13 +168,9 @@ __global__ void __launch_bounds__(kSelectThreads, kMinCtas)
         __syncthreads();
         if (need == 0u)
             break;                                   // the keys are there, that was all
-        // the coarse bins, half of one a thread
-        {
-            const uint4 v = reinterpret_cast<const uint4 *>(hist)[tid];
-            uint32_t n = v.x + v.y + v.z + v.w;
-            n += __shfl_xor_sync(0xffffffffu, n, 1);
-            if (!(tid & 1))
-                hist[kBins + tid / 2] = n;
+        if (tid < kCoarse) {
+            const uint4 v = reinterpret_cast<const uint4 *>(hist)[2 * tid], x = reinterpret_cast<const uint4 *>(hist)[2 * tid + 1];
+            hist[kBins + tid] = (v.x + v.y + v.z + v.w) + (x.x + x.y + x.z + x.w);
         }
         row_sync(ctas);
         // thread i < 256: coarse bin 255 - i of all CTAs
@@ -229,7 +225,7 @@ __global__ void __launch_bounds__(kSelectThreads, kMinCtas)
             prefix |= (coarse * 8u + 7u - (uint32_t)at) << shift;
         }
         if (pass == 1) {                             // the first histogram serves again: all have read it
-            for (int i = tid; i < kHist / 4; i += kSelectThreads)
+            for (int i = tid; i < kHist / 4; i += kThreads)
                 reinterpret_cast<uint4 *>(dyn)[i] = make_uint4(0u, 0u, 0u, 0u);
             __syncthreads();
         }
@@ -237,7 +233,7 @@ __global__ void __launch_bounds__(kSelectThreads, kMinCtas)
     // `need` of the keys equal to `prefix` stay, all larger ones do.  A warp takes
     // a run of the slice, a lane four positions at a time; first how many of each lie
     // before it.
-    const int run = (((t1 - t0) + 128 * kSelectWarps - 1) / (128 * kSelectWarps)) * 128;
+    const int run = (((t1 - t0) + 128 * kWarps - 1) / (128 * kWarps)) * 128;
     const int w0 = min(t1, t0 + warp * run), w1 = min(t1, w0 + run);
     uint32_t na = 0u, ne = 0u;
 #pragma unroll 2
@@ -253,7 +249,7 @@ __global__ void __launch_bounds__(kSelectThreads, kMinCtas)
     __syncthreads();
     uint32_t a = 0u, e = 0u;
 #pragma unroll
-    for (int w = 0; w < kSelectWarps; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
         if (w == warp)
             na = a, ne = e;
         a += warp_counts[w].x;
@@ -322,9 +318,7 @@ cudaError_t launch_select(const SelectParams &p, int num_sms, cudaStream_t strea
     const int64_t slice = ((longest + ctas - 1) / ctas + 3) & ~3;
     const int cached = slice <= kSelectKeys;
     const uint32_t smem = (uint32_t)(2 * kHist * 4 + (cached ? slice * 4 : 0));
-    // two CTAs an SM, or four with fewer registers and loads in flight
-    auto kern = rows * ctas > 2 * num_sms ? shkv_select_kernel<4> : shkv_select_kernel<2>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(shkv_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          2 * kHist * 4 + kSelectKeys * 4);
     if (e != cudaSuccess)
         return e;
@@ -341,7 +335,7 @@ cudaError_t launch_select(const SelectParams &p, int num_sms, cudaStream_t strea
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = ctas > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, p, cached);
+    return cudaLaunchKernelEx(&cfg, shkv_select_kernel, p, cached);
 }
 
 namespace {

@@ -346,6 +346,16 @@ try {
     return SHKV_ERR_CUDA;                // no host memory
 }
 
+shkv_status shkv_select_width(const shkv_pool *pool, int32_t batch, const int32_t *keep, int32_t *width)
+{
+    if (!pool || !width || batch < 0 || batch > pool->cfg.max_batch || (batch > 0 && !keep))
+        return SHKV_ERR_INVALID_ARG;
+    *width = 0;
+    for (int b = 0; b < batch; ++b)
+        *width = std::max(*width, std::min(keep[b], pool->lens[b]));
+    return SHKV_OK;
+}
+
 shkv_status shkv_evict_tokens(shkv_pool *pool, int32_t batch, const int32_t *keep, const int32_t *index,
                               int64_t index_stride, const int32_t *new_table, int64_t new_table_stride,
                               const int32_t *table, int64_t table_stride, const int32_t *lens, const shkv_mass *mass,

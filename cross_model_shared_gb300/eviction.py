@@ -7,7 +7,6 @@ mass, and ``evict_tokens`` moves them into new pages.
 """
 from __future__ import annotations
 
-import array
 import contextlib
 from typing import Dict, Optional
 
@@ -177,10 +176,7 @@ class EvictionCalls:
             if out is None:
                 if k.n > self.max_batch:
                     raise ValueError(f"at most {self.max_batch} requests")
-                lens = array.array("i", bytes(4 * k.n))
-                if k.n:
-                    N.shkv_pool_get_seq_lens(self.handle, k.n, lens.buffer_info()[0])
-                most = max(map(min, k._keep, lens), default=0)
+                most = N.shkv_select_width(self.handle, k.n, k.ptr)
                 index = torch.empty((k.n, self.num_kv_heads, max(most, 1)), dtype=_I32, device=self.k_pages.device)
             elif out.dtype is not _I32 or out.device != self.k_pages.device or out.dim() != 3 or \
                     not out.is_contiguous() or out.shape[0] != k.n or out.shape[1] != self.num_kv_heads:

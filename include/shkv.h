@@ -738,6 +738,9 @@ shkv_status shkv_prefill_mass_workspace_size(const shkv_pool *pool, size_t *byte
  */
 shkv_status shkv_select_tokens(shkv_pool *pool, int32_t batch, const shkv_mass *mass, const int32_t *keep,
                                int32_t sink, int32_t recent, int32_t *index, int64_t index_stride, void *stream);
+/* The tokens that the longest row of a selection keeps (0 if none): the least
+ * index_stride, host only. */
+shkv_status shkv_select_width(const shkv_pool *pool, int32_t batch, const int32_t *keep, int32_t *width);
 
 /*
  * Move the kept tokens of every request longer than keep[b] into new pages:

@@ -28,6 +28,7 @@ def test_null_pools(lib):
     assert lib.shkv_decode_mass(None, 1, 1, 1, 16, 1.0, 16, 1.0, r, r, None) == bad
     assert lib.shkv_prefill_mass(None, 1, 1, 1, 16, 64, 64, 1.0, 16, 1, 1, 1.0, r, r, 16, 1 << 20, None) == bad
     assert lib.shkv_prefill_mass_workspace_size(None, ctypes.byref(n)) == bad
+    assert lib.shkv_select_width(None, 1, None, ctypes.byref(ctypes.c_int32())) == bad
     assert lib.shkv_select_tokens(None, 1, r, None, 0, 0, 16, 1, None) == bad
     assert lib.shkv_evict_tokens(None, 1, None, 16, 1, 16, 1, None, 0, None, None, None, None) == bad
 
@@ -63,10 +64,7 @@ def fake(monkeypatch):
         monkeypatch.setattr(eviction.N, f"shkv_{name}", f.entry(name))
     monkeypatch.setattr(eviction.N, "shkv_prefill_mass_workspace_size", lambda pool: 64)
 
-    def lens(pool, n, ptr):
-        (ctypes.c_int32 * n).from_address(ptr)[:] = [20] * n
-
-    monkeypatch.setattr(eviction.N, "shkv_pool_get_seq_lens", lens)
+    monkeypatch.setattr(eviction.N, "shkv_select_width", lambda pool, n, keep: 9)
     monkeypatch.setattr(eviction, "_raw_stream", lambda index: f.raw)
     monkeypatch.setattr(eviction, "_current_device", lambda: None)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: f"stream {f.raw}")
