@@ -107,8 +107,8 @@ size_t piece_bytes(const shkv_pool *pool)
 // K's copy, the join of its threads' sums; 1, 4, 8, 12: a document 592, 588, 581,
 // 575 us, ten drawn chunks 24.7, 23.9, 23.9, 23.9 us in the mean).  An item of many
 // blocks may be cut between two of them, but not into pieces of under kMinPiece
-// blocks.  (Leaving items whole where that costs less than the second kernel seemed
-// to gained nothing: 24.2 us.)  True if an item is cut.
+// blocks.  (Leaving items whole where a cut seemed dearer than the second kernel
+// gained nothing: 24.2 us.)  True if an item is cut.
 constexpr int64_t kItemCost = 8, kMinPiece = 2;
 
 bool plan_mass(MassParams &p, int limit)
@@ -188,6 +188,8 @@ shkv_status add_mass(shkv_pool *pool, int32_t batch, int32_t n_q, int32_t hq, co
     const int64_t row = (int64_t)hq * c.head_dim;
     if (n_q == 1)                        // a stride that no step is taken along
         q_token = row, lse_token = 0;
+    if (q_token >= (int64_t)1 << 39)     // a tensor map's strides are below 2^40 bytes
+        return SHKV_ERR_UNSUPPORTED;
     if (batch == 1)
         q_request = n_q * q_token, lse_request = 0;
     const float scale_log2 = (float)((double)scale * 1.4426950408889634);
@@ -197,7 +199,7 @@ shkv_status add_mass(shkv_pool *pool, int32_t batch, int32_t n_q, int32_t hq, co
         !writable(out, batch, c.num_kv_heads, len) ||
         (mass && (!readable(mass, len) || !same_layout(mass, out, batch, c.num_kv_heads))))
         return SHKV_ERR_INVALID_ARG;
-    if (q_request >= (int64_t)1 << 39 || len > kMaxTokens)   // a tensor map's strides are below 2^40 bytes
+    if (q_request >= (int64_t)1 << 39 || len > kMaxTokens)
         return SHKV_ERR_UNSUPPORTED;
     MassParams p;
     memset(&p, 0, sizeof p);
@@ -394,7 +396,11 @@ try {
     p.page0[batch] = (int32_t)pages;     // at most SHKV_MAX_BATCH * max_pages_per_seq; checked below
     if (!moves)
         return SHKV_OK;
-    if (pages > 0 && (!index || !new_table || !aligned(index, 4) || !aligned(new_table, 4) || new_table == c.block_table))
+    // the pool's table is written from new_table: no byte of one may be the other's
+    const Span own = span_of(c.block_table, (size_t)c.max_batch * c.max_pages_per_seq * 4);
+    const Span given = span_of(new_table, (size_t)batch * new_table_stride * 4);
+    if (!new_table || !aligned(new_table, 4) || (given.lo < own.hi && own.lo < given.hi) ||
+        (pages > 0 && (!index || !aligned(index, 4))))
         return SHKV_ERR_INVALID_ARG;
     if (table && !aligned(table, 4))
         return SHKV_ERR_INVALID_ARG;

@@ -659,8 +659,9 @@ shkv_status shkv_q8_chunk_attention(shkv_q8_pool *pool, int32_t batch, const int
  * each call must be the pool's (SHKV_ERR_INVALID_ARG), arrays named lens and
  * keep are host arrays [batch], read before the call returns, and requests may
  * be of any length from zero on.  A call captured into a CUDA graph replays
- * with the lengths of its capture; SHKV_ERRF_SEQ_LEN is set where the device
- * copy of a length then differs.
+ * with the lengths of its capture (the host copy of a length changes with the
+ * call, as an append's does); SHKV_ERRF_SEQ_LEN is set where the device copy of
+ * a length then differs.
  *
  * Masses: fp32, mass of token t < length of request b and KV head g at
  * data[b * request_stride + g * head_stride + t] (strides in elements, any
@@ -755,7 +756,7 @@ shkv_status shkv_select_width(const shkv_pool *pool, int32_t batch, const int32_
  * move masses in place it must ascend.
  *   index      device int32 [batch, num_kv_heads, index_stride]
  *   new_table  device int32 [batch, new_table_stride]: pages that no request of
- *              the call reads, each named once; not the pool's block table
+ *              the call reads, each named once; no part of the pool's block table
  *   table, table_stride, lens
  *              where the tokens are: NULL, 0, NULL for the pool's own table and
  *              lengths, else device int32 [batch, table_stride] and host [batch]

@@ -279,6 +279,7 @@ def test_eviction_refusals():
         lambda: pool.evict_tokens(index, [-1, 40], new),
         lambda: pool.evict_tokens(index, [40, 40, 40], new),
         lambda: pool.evict_tokens(index, keep, pool.block_table),
+        lambda: pool.evict_tokens(index[:1].contiguous(), keep[:1], pool.block_table[1:]),   # a part of the pool's own
         lambda: pool.evict_tokens(index, keep, new, out=mass),
         lambda: pool.evict_tokens(index, keep, new, mass=mass[:, :, :99]),
         lambda: pool.evict_tokens(index, keep, new, mass=mass, out=mass[:1].expand(2, 2, 100)),

@@ -129,6 +129,44 @@ def test_nan_and_infinities_reach_their_own_tokens_and_rows():
     assert torch.isnan(run_decode(pool, q, lse, None)).all()
 
 
+@pytest.mark.parametrize("n,group", [(1, 3), (1, 17), (7, 1), (40, 5), (100, 5), (300, 3), (300, 9)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_infinite_keys_meet_the_rows_that_there_are(n, group, d):
+    """A key whose product with every row is -inf gets 0: the zeros that fill up a block of rows would give NaN."""
+    c = Cache([700, 333], 1, d, 16, seed=n + group)
+    for b, t in ((0, 5), (0, 399), (1, 30)):
+        row = c.k[int(c.table[b, t // 16]), 0, t % 16]
+        row.zero_()
+        row[0] = float("inf")
+    pool = c.pool()
+    q = c.randn(2, n, group, d)
+    q[..., 0] = -q[..., 0].abs() - 1
+    lse = torch.zeros(2, n, group, device="cuda")
+    for f in (lambda: run_decode(pool, q, lse, None, scale=0.01), lambda: pool.prefill_mass(q, lse, None, scale=0.01)):
+        if n * group > 64 and "run_decode" in f.__code__.co_names:
+            continue
+        got = f()
+        assert pool.check_errors() == 0 and not torch.isnan(got).any()
+        assert got[0, 0, 5] == 0 and got[0, 0, 399] == 0 and got[1, 0, 30] == 0 and int((got[0, 0, :400] == 0).sum()) == 2
+
+
+@pytest.mark.parametrize("lens,n,hq,hkv", [([900, 2000], 700, 10, 2), ([256, 300], 256, 4, 1), ([3000], 64, 8, 2)])
+def test_prefill_in_place(lens, n, hq, hkv):
+    """Also where an item's blocks are shared out and joined by the second kernel."""
+    c = Cache(lens, hkv, 128, 16, seed=n)
+    pool = c.pool()
+    q = c.randn(len(lens), n, hq, 128)
+    lse = lse_of(c, q, 0.05, True)
+    old = c.mass(extra=7)
+    mass = old.clone()
+    for decay in (1.0, 0.5):
+        before = mass.clone()
+        assert pool.prefill_mass(q, lse, mass, decay=decay, scale=0.05) is mass
+        check_mass(c, q, lse, 0.05, True, decay, before, mass)
+    for b, L in enumerate(lens):
+        assert torch.equal(mass[b, :, L:], old[b, :, L:])
+
+
 def test_scale_and_large_scores():
     """Scores of some thousand, negative scales, a scale of zero."""
     c = Cache([500, 129], 1, 64, 32, seed=7, big=40.0)
