@@ -11,9 +11,10 @@ namespace shkv {
 
 namespace {
 
-constexpr int kSelectThreads = 256;                      // 512: a batch of 512 rows of 1K to 8K tokens takes 20.7 us, not 18.9
 constexpr int kBins = 2048, kCoarse = 256;               // of an 11-bit digit, and by its upper 8 bits
 constexpr int kHist = kBins + kCoarse;                   // words of a histogram
+// Words before the keys: two histograms, then 256 positions a warp.
+constexpr int select_front(int threads) { return threads * 8 > 2 * kHist ? threads * 8 : 2 * kHist; }
 constexpr int kSelectKeys = 49152;                       // keys of a CTA's slice that it holds in shared memory
 
 // A mass as an unsigned key of the same order: -0 as 0, every NaN on top.  Sinks and
@@ -61,15 +62,16 @@ __device__ __forceinline__ uint32_t load_of_rank(const uint32_t *p, uint32_t ran
 // keys above and, by position, as many of the equal ones as still fit are written.
 // A slice's keys stay in shared memory between the passes, four of a thread side by
 // side.  Bound by the latency of its steps.
-__global__ void __launch_bounds__(kSelectThreads, 4)
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     shkv_select_kernel(const __grid_constant__ SelectParams p, int cached)
 {
-    constexpr int kThreads = kSelectThreads, kWarps = kThreads / 32;
+    constexpr int kWarps = kThreads / 32;
     extern __shared__ __align__(16) uint32_t dyn[];
     __shared__ uint32_t warp_sum[kWarps], found[2];            // found: coarse bin, keys in higher ones
     __shared__ uint32_t totals[2];
     __shared__ uint2 warp_counts[kWarps];
-    uint32_t *const keys = dyn + 2 * kHist;
+    uint32_t *const keys = dyn + select_front(kThreads);
     uint32_t rank, ctas;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ctas));
@@ -154,12 +156,12 @@ __global__ void __launch_bounds__(kSelectThreads, 4)
                 const uint32_t k[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (k[i] - prefix <= width) {
-                        if (k[i] == zero_key)
-                            ++zeros;
-                        else
-                            atomicAdd(hist + (k[i] >> shift & mask), 1u);
-                    }
+                {
+                    const bool in = k[i] - prefix <= width, zero = k[i] == zero_key;
+                    zeros += in && zero;
+                    if (in && !zero)
+                        atomicAdd(hist + (k[i] >> shift & mask), 1u);
+                }
             }
         }
         zeros = __reduce_add_sync(0xffffffffu, zeros);
@@ -231,9 +233,9 @@ __global__ void __launch_bounds__(kSelectThreads, 4)
         }
     }
     // `need` of the keys equal to `prefix` stay, all larger ones do.  A warp takes
-    // a run of the slice, a lane four positions at a time; first how many of each lie
+    // a run of the slice, a lane eight positions at a time; first how many of each lie
     // before it.
-    const int run = (((t1 - t0) + 128 * kWarps - 1) / (128 * kWarps)) * 128;
+    const int run = (((t1 - t0) + 256 * kWarps - 1) / (256 * kWarps)) * 256;
     const int w0 = min(t1, t0 + warp * run), w1 = min(t1, w0 + run);
     uint32_t na = 0u, ne = 0u;
 #pragma unroll 2
@@ -269,42 +271,51 @@ __global__ void __launch_bounds__(kSelectThreads, 4)
         na += __shfl_sync(0xffffffffu, a, 0);
         ne += __shfl_sync(0xffffffffu, a, 1);
     }
-    for (int t = w0 + 4 * lane; t - 4 * lane < w1; t += 128) {
-        const uint4 v = t < w1 ? four(t) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+    uint32_t *const stage = dyn + warp * 256;            // the histograms have been read
+    for (int t = w0 + 8 * lane; t - 8 * lane < w1; t += 256) {
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u), v = t < w1 ? four(t) : none, x = t + 4 < w1 ? four(t + 4) : none;
+        const uint32_t k[8] = {v.x, v.y, v.z, v.w, x.x, x.y, x.z, x.w};
         // above in the lower half, equal in the upper half of a word
         uint32_t mine = 0u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 8; ++i)
             mine += k[i] > prefix ? 1u : k[i] == prefix ? 1u << 16 : 0u;
         uint32_t upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
-            upto += lane >= o ? x : 0u;
+            const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+            upto += lane >= o ? y : 0u;
         }
         const uint32_t sum = __shfl_sync(0xffffffffu, upto, 31);
-        if (mine) {
-            uint32_t pa = na + (upto - mine & 0xffffu), pe = ne + (upto - mine >> 16);
+        // side by side in shared memory first: written from here, a position at a time,
+        // they take 6 us of a long row
+        const uint32_t base = na + min(ne, need);
+        uint32_t pa = na + (upto - mine & 0xffffu), pe = ne + (upto - mine >> 16);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool up = k[i] > prefix, eq = k[i] == prefix;
-                const uint32_t at = pa + min(pe, need);
-                if ((up || (eq && pe < need)) && at < (uint32_t)keep)    // always, unless masses change under the call
-                    out[at] = t + i;
-                pa += up;
-                pe += eq;
-            }
+        for (int i = 0; i < 8; ++i) {
+            const bool up = k[i] > prefix, eq = k[i] == prefix;
+            if (up || (eq && pe < need))
+                stage[pa + min(pe, need) - base] = t + i;
+            pa += up;
+            pe += eq;
         }
         na += sum & 0xffffu;
         ne += sum >> 16;
+        const uint32_t n = na + min(ne, need) - base;
+        __syncwarp();
+        for (uint32_t j = lane; j < n; j += 32)
+            if (base + j < (uint32_t)keep)               // always, unless masses change under the call
+                out[base + j] = (int32_t)stage[j];
+        __syncwarp();
     }
     if (ctas > 1)
         row_sync(ctas);                                  // nobody leaves while its counts are read
 }
 
-// A row gets more CTAs (a cluster of up to 8) as long as all of them find room
-// at once and a slice keeps 4096 tokens.
+// A row gets more CTAs (a cluster of up to 8), of more threads, as long as each has
+// an SM to itself and a slice keeps 4096 tokens (32 rows of 131584: 2 CTAs 69 us, 4
+// 26 us, 8, two on some SMs, 30 us; 512 threads 27 us).  Alone a CTA has 256 threads:
+// 512 take 20.7 us for a batch of 512 rows of 1K to 8K tokens, 256 18 us.
 cudaError_t launch_select(const SelectParams &p, int num_sms, cudaStream_t stream)
 {
     int64_t longest = 0;
@@ -313,18 +324,20 @@ cudaError_t launch_select(const SelectParams &p, int num_sms, cudaStream_t strea
             longest = p.lens[b] > longest ? p.lens[b] : longest;
     const int64_t rows = (int64_t)p.batch * p.hkv;
     int ctas = 1;
-    while (ctas < 8 && 2 * ctas * rows <= 2 * num_sms && longest > 4096 * ctas)
+    while (ctas < 8 && 2 * ctas * rows <= num_sms && longest > 4096 * ctas)
         ctas *= 2;
+    const int threads = ctas > 1 ? 1024 : 256;
+    auto kern = ctas > 1 ? shkv_select_kernel<1024> : shkv_select_kernel<256>;
     const int64_t slice = ((longest + ctas - 1) / ctas + 3) & ~3;
     const int cached = slice <= kSelectKeys;
-    const uint32_t smem = (uint32_t)(2 * kHist * 4 + (cached ? slice * 4 : 0));
-    cudaError_t e = cudaFuncSetAttribute(shkv_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         2 * kHist * 4 + kSelectKeys * 4);
+    const uint32_t front = (uint32_t)select_front(threads) * 4, smem = front + (uint32_t)(cached ? slice * 4 : 0);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)front + kSelectKeys * 4);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * ctas));
-    cfg.blockDim = dim3(kSelectThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -335,7 +348,7 @@ cudaError_t launch_select(const SelectParams &p, int num_sms, cudaStream_t strea
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = ctas > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, shkv_select_kernel, p, cached);
+    return cudaLaunchKernelEx(&cfg, kern, p, cached);
 }
 
 namespace {
