@@ -312,10 +312,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
         row_sync(ctas);                                  // nobody leaves while its counts are read
 }
 
-// A row gets more CTAs (a cluster of up to 8), of more threads, as long as each has
-// an SM to itself and a slice keeps 4096 tokens (32 rows of 131584: 2 CTAs 69 us, 4
-// 26 us, 8, two on some SMs, 30 us; 512 threads 27 us).  Alone a CTA has 256 threads:
-// 512 take 20.7 us for a batch of 512 rows of 1K to 8K tokens, 256 18 us.
+// A row gets more CTAs (a cluster of up to 8) as long as each has an SM to itself and
+// a slice keeps 4096 tokens (32 rows of 131584: 2 CTAs 69 us, 4 26 us, 8, two on some
+// SMs, 30 us), and where its keys fit no shared memory otherwise (192 rows of 131000:
+// 256 us from global memory with a CTA a row).  Long rows and slices have 1024
+// threads a CTA, short ones 256: 128 rows of 20K to 40K tokens 41 us with 256, 27 us
+// with 1024; 512 rows of 1K to 8K 19 and 30; 1024 rows of 2K to 4K 23 and 53.
 cudaError_t launch_select(const SelectParams &p, int num_sms, cudaStream_t stream)
 {
     int64_t longest = 0;
@@ -324,10 +326,11 @@ cudaError_t launch_select(const SelectParams &p, int num_sms, cudaStream_t strea
             longest = p.lens[b] > longest ? p.lens[b] : longest;
     const int64_t rows = (int64_t)p.batch * p.hkv;
     int ctas = 1;
-    while (ctas < 8 && 2 * ctas * rows <= num_sms && longest > 4096 * ctas)
+    while (ctas < 8 && longest > 4096 * ctas && (2 * ctas * rows <= num_sms || longest > (int64_t)kSelectKeys * ctas))
         ctas *= 2;
-    const int threads = ctas > 1 ? 1024 : 256;
-    auto kern = ctas > 1 ? shkv_select_kernel<1024> : shkv_select_kernel<256>;
+    const bool wide = ctas > 1 || longest > 12288;
+    const int threads = wide ? 1024 : 256;
+    auto kern = wide ? shkv_select_kernel<1024> : shkv_select_kernel<256>;
     const int64_t slice = ((longest + ctas - 1) / ctas + 3) & ~3;
     const int cached = slice <= kSelectKeys;
     const uint32_t front = (uint32_t)select_front(threads) * 4, smem = front + (uint32_t)(cached ? slice * 4 : 0);
