@@ -13,18 +13,16 @@ namespace {
 
 constexpr int kBins = 2048, kCoarse = 256;               // of an 11-bit digit, and by its upper 8 bits
 constexpr int kHist = kBins + kCoarse;                   // words of a histogram
-// Words before the keys: two histograms, then 256 positions a warp.
-constexpr int select_front(int threads) { return threads * 8 > 2 * kHist ? threads * 8 : 2 * kHist; }
 constexpr int kSelectKeys = 49152;                       // keys of a CTA's slice that it holds in shared memory
+constexpr int kSmemSm = 228 * 1024;                      // of an SM, 1 KB a CTA among it
+constexpr int kGroup = 128;                              // keys that a warp reads at once, four of a lane
 
-// A mass as an unsigned key of the same order: -0 as 0, every NaN on top.  Sinks and
-// recent tokens have a key above all, no token the key 0.
-constexpr uint32_t kAlways = 0xffffffffu, kNanKey = 0xfffffffeu;
-
+// A mass as an unsigned key of the same order: -0 as 0, every NaN (a sum's result is
+// the one with all bits set) on top.
 __device__ __forceinline__ uint32_t mass_key(float m)
 {
     const uint32_t u = __float_as_uint(m + 0.f);         // -0 + 0 = 0
-    return m != m ? kNanKey : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 // Barrier of the row's CTAs; their shared memory is ordered by it.
@@ -53,37 +51,46 @@ __device__ __forceinline__ uint32_t load_of_rank(const uint32_t *p, uint32_t ran
 
 }  // namespace
 
-// A cluster of CTAs per (request, KV head), each with a slice of its positions.
-// The n-th largest key of the candidates (the tokens between the sinks and the
-// recent ones) is found digit by digit, 11 bits, 11 and 10 from the top: the CTAs
-// count the candidates that share the digits found so far in a histogram each,
+// A cluster of CTAs per (request, KV head), each with a slice of its candidates, the
+// tokens between the sinks and the recent ones; in it every warp has a run.
+// The n-th largest key is found digit by digit, 11 bits, 11 and 10 from the top: the
+// CTAs count the candidates that share the digits found so far in a histogram each,
 // and every one of them finds the digit from all: first by its upper 8 bits, then
 // among 8 bins (reading all 2048 bins of 8 CTAs took 2.5 us a digit).  Then all
-// keys above and, by position, as many of the equal ones as still fit are written.
-// A slice's keys stay in shared memory between the passes, four of a thread side by
-// side.  Bound by the latency of its steps.
+// keys above and, by position, as many of the equal ones as still fit are written:
+// a warp puts its positions side by side where its keys were, and copies them out
+// once it knows how many lie before them (written from the scan, a position at a
+// time, they took 6 us of a long row).  Candidates behind the row's last, up to a
+// whole group, count as -infinity: they come last of all by key and position.
+// Bound by instructions (a long row takes about 70 for a key of each lane) and the
+// latency of its steps alike: half of the issue slots are taken.
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     shkv_select_kernel(const __grid_constant__ SelectParams p, int cached)
 {
     constexpr int kWarps = kThreads / 32;
     extern __shared__ __align__(16) uint32_t dyn[];
-    __shared__ uint32_t warp_sum[kWarps], found[2];            // found: coarse bin, keys in higher ones
+    __shared__ uint32_t warp_sum[kCoarse / 32], found[2];      // found: coarse bin, keys in higher ones
     __shared__ uint32_t totals[2];
     __shared__ uint2 warp_counts[kWarps];
-    uint32_t *const keys = dyn + select_front(kThreads);
     uint32_t rank, ctas;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ctas));
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
+    for (int i = tid; i < 2 * kHist / 4; i += kThreads)
+        reinterpret_cast<uint4 *>(dyn)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid < 2)
+        found[tid] = 0u;
     pdl_wait_prior();
     pdl_launch_dependents();
-    const int row = blockIdx.x / ctas, b = row / p.hkv, g = row % p.hkv;
+    const int log_ctas = 31 - __clz((int)ctas);          // a power of two
+    const int b = blockIdx.y, g = blockIdx.x >> log_ctas;
     const int L = p.lens[b], keep = min(p.keep[b], L);
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
     const int all = rank * kThreads + tid, step = ctas * kThreads;
-    int32_t *out = p.index + (int64_t)row * p.index_stride;
+    int32_t *out = p.index + ((int64_t)b * p.hkv + g) * p.index_stride;
     if (g == 0 && all == 0 && p.seq_lens[b] != L)
         atomicOr(p.err, SHKV_ERRF_SEQ_LEN);
+#pragma unroll 4
     for (int64_t j = keep + all; j < p.index_stride; j += step)
         out[j] = -1;
     if (keep == L) {
@@ -91,117 +98,116 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
             out[j] = j;
         return;
     }
-    // this CTA's positions, and the candidates among them
-    const int per = ((L + (int)ctas - 1) / (int)ctas + 3) & ~3, t0 = min(L, (int)rank * per), t1 = min(L, t0 + per);
-    const int lo = max(t0, p.sink), hi = min(t1, L - p.recent);
-    const float *m = p.mass + b * p.mass_request + g * p.mass_head;
-    const uint32_t zero_key = mass_key(0.f);
-    uint32_t prefix = 0u, need = (uint32_t)(keep - p.sink - p.recent);   // of the keys with this prefix
-    // keys of positions t .. t + 3, t - t0 a multiple of 4; 0 outside the slice
+    for (int j = all; j < p.sink + p.recent; j += step) {
+        const int from_end = p.sink + p.recent - j;
+        out[j < p.sink ? j : keep - from_end] = j < p.sink ? j : L - from_end;
+    }
+    out += p.sink;
+    const uint32_t chosen = (uint32_t)(keep - p.sink - p.recent);
+    if (chosen == 0u)
+        return;
+    const int cand = L - p.sink - p.recent;
+    const int per = ((cand + (int)ctas - 1 >> log_ctas) + kGroup - 1) & ~(kGroup - 1);
+    const int c0 = min(cand, (int)rank * per), n = min(cand - c0, per);
+    const int run = (n + kGroup * kWarps - 1) / (kGroup * kWarps) * kGroup;
+    const int w0 = min(n, warp * run), w1 = min(n, w0 + run);
+    const float *m = p.mass + b * p.mass_request + g * p.mass_head + p.sink + c0;
+    uint32_t *const own = dyn + 2 * kHist + warp * run - w0;   // a run's keys, from w0 on
+    // keys t .. t + 3 of the run
     auto four = [&](int t) -> uint4 {
         if (cached)
-            return *reinterpret_cast<const uint4 *>(keys + (t - t0));
+            return *reinterpret_cast<const uint4 *>(own + t);
         uint32_t k[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            k[i] = t + i >= t1 ? 0u : t + i < lo || t + i >= hi ? kAlways : mass_key(__ldg(m + t + i));
+            k[i] = mass_key(t + i < w1 ? __ldg(m + t + i) : -INFINITY);
         return make_uint4(k[0], k[1], k[2], k[3]);
     };
-    for (int i = tid; i < 2 * kHist / 4; i += kThreads)
-        reinterpret_cast<uint4 *>(dyn)[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (tid < 2)
-        found[tid] = 0u;
-    __syncthreads();
-    if (need == 0u)
-        prefix = kNanKey;                    // no candidate is above, none of the equal ones stays
+    uint32_t prefix = 0u, need = chosen, equal = 0u;     // of the keys with this prefix; keys with all its digits
 #pragma unroll 1
-    for (int pass = 0; pass < (need ? 3 : 1); ++pass) {
+    for (int pass = 0; pass < 3; ++pass) {
         uint32_t *hist = dyn + (pass & 1) * kHist;
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-        const uint32_t mask = pass == 2 ? 1023u : 2047u;
-        // masses that are exactly 0 are many: counted in a register
-        uint32_t zeros = 0u;
         if (pass == 0) {
             constexpr int kU = 16;
-#pragma unroll 1
-            for (int t = t0 + tid; t < t1; t += kU * kThreads) {
-                float x[kU];
+            float x[kU];
+            auto load = [&](int t) {
 #pragma unroll
                 for (int u = 0; u < kU; ++u)
-                    x[u] = t + u * kThreads < t1 ? __ldg(m + t + u * kThreads) : 0.f;
+                    x[u] = t + u * 32 + lane < w1 ? __ldg(m + t + u * 32 + lane) : -INFINITY;
+            };
+            load(w0);
+            __syncthreads();                             // the histograms are empty
+#pragma unroll 1
+            for (int t = w0; t < w1;) {
 #pragma unroll
                 for (int u = 0; u < kU; ++u) {
-                    const int at = t + u * kThreads;
-                    if (at >= t1)
+                    if (u % 4 == 0 && t + u * 32 >= w1)
                         break;
-                    uint32_t k = mass_key(x[u]);
-                    if (at < lo || at >= hi)
-                        k = kAlways;
-                    else if (k == zero_key)
-                        ++zeros;
-                    else
-                        atomicAdd(hist + (k >> 21), 1u);
+                    const uint32_t k = mass_key(x[u]);
+                    atomicAdd(hist + (k >> 21), 1u);
                     if (cached)
-                        keys[at - t0] = k;
+                        own[t + u * 32 + lane] = k;
                 }
+                t += kU * 32;
+                if (t < w1)
+                    load(t);
             }
-            if (tid < 3 && cached && t1 + tid - t0 < ((t1 - t0 + 3) & ~3))
-                keys[t1 + tid - t0] = 0u;
+            __syncwarp();
         } else {
-            // keys base .. base + width share the digits found (the topmost is kAlways)
-            const uint32_t width = min((1u << (pass == 1 ? 21 : 10)) - 1u, kNanKey - prefix);
+            // keys prefix .. prefix + width share the digits found
+            const uint32_t width = (1u << (pass == 1 ? 21 : 10)) - 1u;
 #pragma unroll 2
-            for (int t = t0 + 4 * tid; t < t1; t += 4 * kThreads) {
-                const uint4 v = four(t);
+            for (int t = w0; t < w1; t += kGroup) {
+                const uint4 v = four(t + 4 * lane);
                 const uint32_t k[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                {
-                    const bool in = k[i] - prefix <= width, zero = k[i] == zero_key;
-                    zeros += in && zero;
-                    if (in && !zero)
-                        atomicAdd(hist + (k[i] >> shift & mask), 1u);
-                }
+                    if (k[i] - prefix <= width)
+                        atomicAdd(hist + (k[i] - prefix >> shift), 1u);
             }
         }
-        zeros = __reduce_add_sync(0xffffffffu, zeros);
-        if (lane == 0 && zeros)
-            atomicAdd(hist + (zero_key >> shift & mask), zeros);
         __syncthreads();
-        if (need == 0u)
-            break;                                   // the keys are there, that was all
+        // thread i < 256: coarse bin 255 - i, of all CTAs
+        uint32_t count = 0u;
         if (tid < kCoarse) {
-            const uint4 v = reinterpret_cast<const uint4 *>(hist)[2 * tid], x = reinterpret_cast<const uint4 *>(hist)[2 * tid + 1];
-            hist[kBins + tid] = (v.x + v.y + v.z + v.w) + (x.x + x.y + x.z + x.w);
+            const uint4 *bin = reinterpret_cast<const uint4 *>(hist) + 2 * (kCoarse - 1 - tid);
+            const uint4 v = bin[0], x = bin[1];
+            count = (v.x + v.y + v.z + v.w) + (x.x + x.y + x.z + x.w);
         }
-        row_sync(ctas);
-        // thread i < 256: coarse bin 255 - i of all CTAs
-        uint32_t n = 0u;
-        if (tid < kCoarse) {
-            const uint32_t *bin = hist + kBins + kCoarse - 1 - tid;
-            if (ctas == 1)
-                n = *bin;
-            else
+        if (ctas > 1) {
+            uint32_t *bin = hist + kBins + tid;
+            if (tid < kCoarse)
+                *bin = count;
+            row_sync(ctas);
+            if (tid < kCoarse) {
+                count = 0u;
 #pragma unroll 4
                 for (uint32_t r = 0; r < ctas; ++r)
-                    n += load_of_rank(bin, r);
+                    count += load_of_rank(bin, r);
+            }
         }
-        uint32_t upto = n;
+        if (pass == 1)                               // the first histogram serves again: all have read it
+            for (int i = tid; i < kHist / 4; i += kThreads)
+                reinterpret_cast<uint4 *>(dyn)[i] = make_uint4(0u, 0u, 0u, 0u);
+        uint32_t upto = count;
+        if (tid < kCoarse) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
-            upto += lane >= o ? v : 0u;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+                upto += lane >= o ? v : 0u;
+            }
+            if (lane == 31)
+                warp_sum[warp] = upto;
         }
-        if (lane == 31)
-            warp_sum[warp] = upto;
         __syncthreads();
         if (tid < kCoarse) {
 #pragma unroll
             for (int w = 0; w < kCoarse / 32; ++w)
                 upto += w < warp ? warp_sum[w] : 0u;
-            if (upto - n < need && need <= upto) {
+            if (upto - count < need && need <= upto) {
                 found[0] = (uint32_t)(kCoarse - 1 - tid);
-                found[1] = upto - n;              // keys in higher coarse bins
+                found[1] = upto - count;              // keys in higher coarse bins
             }
         }
         __syncthreads();
@@ -224,38 +230,65 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
             const uint32_t here = __ballot_sync(0xffffffffu, before < need && need <= before + v) & 255u;
             const int at = here ? __ffs(here) - 1 : 0;
             need -= __shfl_sync(0xffffffffu, before, at);
+            equal = __shfl_sync(0xffffffffu, v, at);
             prefix |= (coarse * 8u + 7u - (uint32_t)at) << shift;
         }
-        if (pass == 1) {                             // the first histogram serves again: all have read it
-            for (int i = tid; i < kHist / 4; i += kThreads)
-                reinterpret_cast<uint4 *>(dyn)[i] = make_uint4(0u, 0u, 0u, 0u);
-            __syncthreads();
-        }
     }
-    // `need` of the keys equal to `prefix` stay, all larger ones do.  A warp takes
-    // a run of the slice, a lane eight positions at a time; first how many of each lie
-    // before it.
-    const int run = (((t1 - t0) + 256 * kWarps - 1) / (256 * kWarps)) * 256;
-    const int w0 = min(t1, t0 + warp * run), w1 = min(t1, w0 + run);
-    uint32_t na = 0u, ne = 0u;
-#pragma unroll 2
-    for (int t = w0 + 4 * lane; t < w1; t += 128) {
-        const uint4 k = four(t);
-        na += (k.x > prefix) + (k.y > prefix) + (k.z > prefix) + (k.w > prefix);
-        ne += (k.x == prefix) + (k.y == prefix) + (k.z == prefix) + (k.w == prefix);
-    }
-    na = __reduce_add_sync(0xffffffffu, na);
-    ne = __reduce_add_sync(0xffffffffu, ne);
-    if (lane == 0)
-        warp_counts[warp] = make_uint2(na, ne);
-    __syncthreads();
-    uint32_t a = 0u, e = 0u;
+    // All larger keys stay, and `need` of the `equal` keys that are `prefix`: all of
+    // them, as a rule.  Then a run's positions take the place of its keys, four groups
+    // at a time, their counts in a byte each (up to 128).
+    const bool listed = cached && equal == need;
+    uint32_t *const list = own + w0;
+    uint32_t some = 0u, same = 0u;                       // that stay; equal ones where not all do
+    for (int t = w0; t < w1; t += 4 * kGroup) {
+        uint32_t k[16], mine = 0u;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w == warp)
-            na = a, ne = e;
-        a += warp_counts[w].x;
-        e += warp_counts[w].y;
+        for (int v = 0; v < 4; ++v) {
+            const uint4 x = t + v * kGroup < w1 ? four(t + v * kGroup + 4 * lane) : make_uint4(0u, 0u, 0u, 0u);
+            k[4 * v] = x.x, k[4 * v + 1] = x.y, k[4 * v + 2] = x.z, k[4 * v + 3] = x.w;
+#pragma unroll
+            for (int i = 4 * v; i < 4 * v + 4; ++i)
+                mine += k[i] >= prefix ? 1u << 8 * v : 0u;
+        }
+        uint32_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+            upto += lane >= o ? y : 0u;
+        }
+        const uint32_t sum = __shfl_sync(0xffffffffu, upto, 31);
+        if (listed) {
+            upto -= mine;
+            __syncwarp();                                // the keys have been read
+            uint32_t first = some;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                uint32_t *to = list + first + (upto >> 8 * v & 255u);
+#pragma unroll
+                for (int i = 4 * v; i < 4 * v + 4; ++i)
+                    if (k[i] >= prefix)
+                        *to++ = (uint32_t)(t + v * kGroup + 4 * lane + (i & 3));
+                first += sum >> 8 * v & 255u;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                same += k[i] == prefix;
+        }
+        some += (sum & 255u) + (sum >> 8 & 255u) + (sum >> 16 & 255u) + (sum >> 24);
+    }
+    same = __reduce_add_sync(0xffffffffu, same);
+    if (lane == 0)
+        warp_counts[warp] = make_uint2(some - same, same);
+    __syncthreads();
+    // those above (and equal ones, where listed) and equal ones: before this warp's, of the CTA
+    uint32_t na, ne, a, e;
+    {
+        const uint2 c = lane < kWarps ? warp_counts[lane] : make_uint2(0u, 0u);
+        na = __reduce_add_sync(0xffffffffu, lane < warp ? c.x : 0u);
+        ne = __reduce_add_sync(0xffffffffu, lane < warp ? c.y : 0u);
+        a = __reduce_add_sync(0xffffffffu, c.x);
+        e = __reduce_add_sync(0xffffffffu, c.y);
     }
     if (ctas > 1) {
         if (tid == 0)
@@ -271,53 +304,40 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
         na += __shfl_sync(0xffffffffu, a, 0);
         ne += __shfl_sync(0xffffffffu, a, 1);
     }
-    uint32_t *const stage = dyn + warp * 256;            // the histograms have been read
-    for (int t = w0 + 8 * lane; t - 8 * lane < w1; t += 256) {
-        const uint4 none = make_uint4(0u, 0u, 0u, 0u), v = t < w1 ? four(t) : none, x = t + 4 < w1 ? four(t + 4) : none;
-        const uint32_t k[8] = {v.x, v.y, v.z, v.w, x.x, x.y, x.z, x.w};
-        // above in the lower half, equal in the upper half of a word
-        uint32_t mine = 0u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            mine += k[i] > prefix ? 1u : k[i] == prefix ? 1u << 16 : 0u;
-        uint32_t upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
-            upto += lane >= o ? y : 0u;
+    // (a place of `chosen` and above: only if masses change under the call)
+    const int base = p.sink + c0;
+    const uint32_t below = (1u << lane) - 1u;
+    if (listed) {
+        for (uint32_t j = lane; j < some; j += 32)
+            if (na + j < chosen)
+                out[na + j] = base + (int32_t)list[j];
+    } else {
+        for (int t0 = w0; t0 < w1; t0 += 32) {
+            const int t = t0 + lane;
+            const uint32_t k = t >= w1 ? 0u : cached ? own[t] : mass_key(__ldg(m + t));
+            const bool up = k > prefix, eq = k == prefix;
+            const uint32_t ups = __ballot_sync(0xffffffffu, up), eqs = __ballot_sync(0xffffffffu, eq);
+            const uint32_t pe = ne + __popc(eqs & below), at = na + __popc(ups & below) + min(pe, need);
+            if ((up || (eq && pe < need)) && at < chosen)
+                out[at] = base + t;
+            na += __popc(ups);
+            ne += __popc(eqs);
         }
-        const uint32_t sum = __shfl_sync(0xffffffffu, upto, 31);
-        // side by side in shared memory first: written from here, a position at a time,
-        // they take 6 us of a long row
-        const uint32_t base = na + min(ne, need);
-        uint32_t pa = na + (upto - mine & 0xffffu), pe = ne + (upto - mine >> 16);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const bool up = k[i] > prefix, eq = k[i] == prefix;
-            if (up || (eq && pe < need))
-                stage[pa + min(pe, need) - base] = t + i;
-            pa += up;
-            pe += eq;
-        }
-        na += sum & 0xffffu;
-        ne += sum >> 16;
-        const uint32_t n = na + min(ne, need) - base;
-        __syncwarp();
-        for (uint32_t j = lane; j < n; j += 32)
-            if (base + j < (uint32_t)keep)               // always, unless masses change under the call
-                out[base + j] = (int32_t)stage[j];
-        __syncwarp();
     }
     if (ctas > 1)
         row_sync(ctas);                                  // nobody leaves while its counts are read
 }
 
-// A row gets more CTAs (a cluster of up to 8) as long as each has an SM to itself and
-// a slice keeps 4096 tokens (32 rows of 131584: 2 CTAs 69 us, 4 26 us, 8, two on some
-// SMs, 30 us), and where its keys fit no shared memory otherwise (192 rows of 131000:
-// 256 us from global memory with a CTA a row).  Long rows and slices have 1024
-// threads a CTA, short ones 256: 128 rows of 20K to 40K tokens 41 us with 256, 27 us
-// with 1024; 512 rows of 1K to 8K 19 and 30; 1024 rows of 2K to 4K 23 and 53.
+// A row gets more CTAs (a cluster of up to 8) as long as a slice keeps 16384 tokens
+// and each has an SM to itself (32 rows of 131584: 4 CTAs 17 us, 8, two on some SMs, 45;
+// 8 rows of 12000: 1 CTA 9.0 us, 4 10.5; of 40000: 4 CTAs 12.4 us, 8 14.1), and more than
+// there are SMs where its keys fit shared memory only then (192 rows of 131000: 4 CTAs
+// 105 us, one that reads its masses from global memory in every pass 202).
+//
+// Threads: as many as make 1024 an SM, by the CTAs that its shared memory takes, 512 a
+// row where rows do not fill the SMs.  (256 / 512 / 1024 threads: 512 rows of 1K to 8K
+// 13.6 / 15.8 / 22.3 us; 320 rows of 8K to 12K 16.9 / 14.8 / 19.0; 320 of 14K to 16K
+// 18.5 / 17.3 / 21.8; 128 of 20K to 40K 26.2 / 19.3 / 18.1; 128 of 8000 9.2 / 7.9 / 9.1.)
 cudaError_t launch_select(const SelectParams &p, int num_sms, cudaStream_t stream)
 {
     int64_t longest = 0;
@@ -326,20 +346,25 @@ cudaError_t launch_select(const SelectParams &p, int num_sms, cudaStream_t strea
             longest = p.lens[b] > longest ? p.lens[b] : longest;
     const int64_t rows = (int64_t)p.batch * p.hkv;
     int ctas = 1;
-    while (ctas < 8 && longest > 4096 * ctas && (2 * ctas * rows <= num_sms || longest > (int64_t)kSelectKeys * ctas))
+    while (ctas < 8 && longest > 16384 * ctas &&
+           (2 * ctas * rows <= num_sms || (longest > (int64_t)kSelectKeys * ctas && longest <= 8 * kSelectKeys)))
         ctas *= 2;
-    const bool wide = ctas > 1 || longest > 12288;
-    const int threads = wide ? 1024 : 256;
-    auto kern = wide ? shkv_select_kernel<1024> : shkv_select_kernel<256>;
-    const int64_t slice = ((longest + ctas - 1) / ctas + 3) & ~3;
+    const int64_t room = kSmemSm / (2 * kHist * 4 + 1024 + 4 * longest);
+    const int threads = ctas > 1 || room < 2 ? 1024 : room < 4 || (rows <= num_sms && longest > 4096) ? 512 : 256;
+    auto kern = threads == 1024  ? shkv_select_kernel<1024>
+                : threads == 512 ? shkv_select_kernel<512>
+                                 : shkv_select_kernel<256>;
+    // runs of whole groups
+    const int64_t part = (longest + ctas - 1) / ctas, unit = kGroup * (threads / 32);
+    const int64_t slice = (part + unit - 1) / unit * unit;
     const int cached = slice <= kSelectKeys;
-    const uint32_t front = (uint32_t)select_front(threads) * 4, smem = front + (uint32_t)(cached ? slice * 4 : 0);
+    const uint32_t front = 2 * kHist * 4, smem = front + (uint32_t)(cached ? slice * 4 : 0);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)front + kSelectKeys * 4);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(rows * ctas));
+    cfg.gridDim = dim3((unsigned)(p.hkv * ctas), (unsigned)p.batch);
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;

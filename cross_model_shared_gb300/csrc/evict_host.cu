@@ -27,8 +27,6 @@ namespace {
 
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-shkv_status status_of(cudaError_t e) { return e == cudaSuccess ? SHKV_OK : SHKV_ERR_CUDA; }
-
 // A pool, a batch that it takes, and its device current.
 bool callable(const shkv_pool *pool, int32_t batch)
 {
