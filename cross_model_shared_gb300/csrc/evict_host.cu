@@ -405,7 +405,7 @@ try {
     if (out && (!readable(mass, len) || !writable(out, batch, c.num_kv_heads, len) ||
                 !same_layout(mass, out, batch, c.num_kv_heads)))
         return SHKV_ERR_INVALID_ARG;
-    if ((pages + batch) * c.num_kv_heads > INT32_MAX || len > kMaxTokens)
+    if ((pages + batch) * c.num_kv_heads > INT32_MAX - 64 || len > kMaxTokens)   // warps, whole CTAs of them
         return SHKV_ERR_UNSUPPORTED;
     p.k_pages = static_cast<uint4 *>(c.k_pages);
     p.v_pages = static_cast<uint4 *>(c.v_pages);

@@ -64,6 +64,23 @@ def test_selection_of_long_requests(lens, kind):
     assert pool.check_errors() == 0
 
 
+@pytest.mark.parametrize("lens,hkv", [
+    ([49152], 1), ([49153, 17], 1), ([393216], 1), ([393217, 1], 1),        # keys that just fit, and that do not
+    ([50000, 98305, 1, 60000] * 6, 8),                                      # more rows than SMs, in clusters all the same
+    ([12000, 30, 4097, 9000] * 6, 8), ([15000, 16000] * 12, 8),             # 512 threads: two or three rows an SM
+    ([5000, 4097, 1] * 2, 8), ([16384, 300], 8), ([16385, 300], 8)])        # few rows, short and just long enough
+@pytest.mark.parametrize("kind", ["octaves", "few values", "-inf"])
+def test_selection_in_every_launch_shape(lens, hkv, kind):
+    pool = select_pool(lens, hkv)
+    mass = draw_masses("few values" if kind == "-inf" else kind, len(lens), hkv, max(lens), seed=7)
+    if kind == "-inf":                       # below every number, and equal to nothing behind the row's end
+        mass[mass < 4] = -float("inf")
+    for f, sink, recent in ((0.3, 5, 33), (0.9, 0, 0)):
+        keep = [max(int(f * L), min(L, sink + recent)) for L in lens]
+        check_selection(mass, lens, keep, sink, recent, pool.select_tokens(mass, keep, sink=sink, recent=recent))
+    assert pool.check_errors() == 0
+
+
 def test_selection_of_many_rows_and_every_keep():
     lens = np.random.default_rng(1).integers(0, 90, 1024).tolist()
     pool = select_pool(lens, 2)
