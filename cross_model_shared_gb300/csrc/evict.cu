@@ -423,25 +423,51 @@ __device__ __forceinline__ void move_masses(const EvictParams &p, int row)
                 dst[j0 + u * kMoveThreads] = 0.f;
 }
 
+// The request's table row and length, by a CTA.
+__device__ __forceinline__ void commit_request(const EvictParams &p, int b)
+{
+    const int keep = p.keep[b];
+    if (p.check_lens && threadIdx.x == 0 && p.seq_lens[b] != p.lens[b])
+        atomicOr(p.err, SHKV_ERRF_SEQ_LEN);
+    if (keep >= p.lens[b])
+        return;
+    for (int i = threadIdx.x; i < p.max_pages; i += kMoveThreads)
+        p.block_table[(int64_t)b * p.max_pages + i] = i < p.new_stride ? p.new_table[b * p.new_stride + i] : -1;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        p.seq_lens[b] = keep;
+}
+
 }  // namespace
 
-// The first CTAs move masses.  The others copy rows, a warp per (new page, KV
-// head): K's and V's rows of 32 / (2 D / 8) tokens an instruction, eight
-// instructions' loads before their stores.
+// The first CTAs write tables and lengths, where the move reads a table of the
+// caller's (one launch less: 4.2 -> 2.8 us for a short request, 3 us of the host), the
+// next ones move masses.  The others copy rows, a warp per (new page, KV head): K's
+// and V's rows of 32 / (2 D / 8) tokens an instruction, eight instructions' loads
+// before their stores.  Bound by HBM: 48 requests to half, 491 MB, 78 us (94% of a
+// copy's rate).  The eight loads need 72 registers, three CTAs an SM: left to itself the
+// compiler took 56 and loaded fewer at once (104 us; 16 loads of a thread 90, 4 and five
+// CTAs 81); stores that stay longer in L2 81 us.
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads) shkv_evict_kernel(const __grid_constant__ EvictParams p)
+__global__ void __launch_bounds__(kMoveThreads, 3) shkv_evict_kernel(const __grid_constant__ EvictParams p)
 {
     constexpr int V = D / 8, kTok = 32 / (2 * V);        // vectors of a row, tokens an instruction
     constexpr int kU = 8;
     pdl_wait_prior();
-    pdl_launch_dependents();
-    const int mass_blocks = p.mass.out ? p.batch * p.hkv : 0;
-    if ((int)blockIdx.x < mass_blocks) {
-        move_masses(p, blockIdx.x);
+    if (!p.at_once)                  // as in the kernel below
+        pdl_launch_dependents();
+    const int commits = p.at_once ? p.batch : 0, mass_blocks = p.mass.out ? p.batch * p.hkv : 0;
+    const int block = (int)blockIdx.x - commits - mass_blocks;
+    if ((int)blockIdx.x < commits) {
+        commit_request(p, blockIdx.x);
+        return;
+    }
+    if (block < 0) {
+        move_masses(p, blockIdx.x - commits);
         return;
     }
     const int lane = threadIdx.x & 31, P = p.page_size;
-    const int w = (blockIdx.x - mass_blocks) * (kMoveThreads / 32) + threadIdx.x / 32;
+    const int w = block * (kMoveThreads / 32) + threadIdx.x / 32;
     if (w >= p.page0[p.batch] * p.hkv)
         return;
     const int page = w / p.hkv, g = w % p.hkv;
@@ -489,37 +515,27 @@ __global__ void __launch_bounds__(kMoveThreads) shkv_evict_kernel(const __grid_c
         for (int u = 0; u < kU; ++u) {
             const int t = j + u * kTok + tok;
             if (t < n && good >> t & 1u)
-                dst[(int64_t)t * V] = x[u];
+                __stcs(dst + (int64_t)t * V, x[u]);
         }
     }
 }
 
-// After the move: the requests' tables and lengths.  Lets no dependent start
-// early: the unit kernel of a decode with tails reads the table without waiting
-// for its predecessor.
+// After a move that read the pool's own table: the requests' tables and lengths.
+// Lets no dependent start early: the unit kernel of a decode with tails reads the
+// table without waiting for its predecessor.
 __global__ void __launch_bounds__(kMoveThreads) shkv_evict_commit_kernel(const __grid_constant__ EvictParams p)
 {
     pdl_wait_prior();
-    const int b = blockIdx.x;
-    const int keep = p.keep[b];
-    if (p.check_lens && threadIdx.x == 0 && p.seq_lens[b] != p.lens[b])
-        atomicOr(p.err, SHKV_ERRF_SEQ_LEN);
-    if (keep >= p.lens[b])
-        return;
-    for (int i = threadIdx.x; i < p.max_pages; i += kMoveThreads)
-        p.block_table[(int64_t)b * p.max_pages + i] = i < p.new_stride ? p.new_table[b * p.new_stride + i] : -1;
-    __syncthreads();
-    if (threadIdx.x == 0)
-        p.seq_lens[b] = keep;
+    commit_request(p, blockIdx.x);
 }
 
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream)
 {
     const int64_t warps = (int64_t)p.page0[p.batch] * p.hkv;
-    const int64_t grid = (p.mass.out ? (int64_t)p.batch * p.hkv : 0) + (warps + kMoveThreads / 32 - 1) / (kMoveThreads / 32);
+    const int64_t grid = (p.at_once ? p.batch : 0) + (p.mass.out ? (int64_t)p.batch * p.hkv : 0) + (warps + kMoveThreads / 32 - 1) / (kMoveThreads / 32);
     auto kern = p.head_dim == 64 ? shkv_evict_kernel<64> : shkv_evict_kernel<128>;
     cudaError_t e = grid ? launch_pdl(kern, (int)grid, kMoveThreads, 0u, stream, p) : cudaSuccess;
-    if (e == cudaSuccess)
+    if (e == cudaSuccess && !p.at_once)
         e = launch_pdl(shkv_evict_commit_kernel, p.batch, kMoveThreads, 0u, stream, p);
     return e;
 }

@@ -75,6 +75,7 @@ struct EvictParams {
     int32_t *block_table, *seq_lens;
     uint32_t *err;
     int32_t batch, hkv, head_dim, page_size, max_pages, num_pages, check_lens;
+    int32_t at_once;                 // tables and lengths beside the move: it reads neither
     int32_t lens[SHKV_MAX_BATCH];
     int32_t keep[SHKV_MAX_BATCH];
     int32_t page0[SHKV_MAX_BATCH + 1];   // new pages before each request

@@ -405,7 +405,7 @@ try {
     if (out && (!readable(mass, len) || !writable(out, batch, c.num_kv_heads, len) ||
                 !same_layout(mass, out, batch, c.num_kv_heads)))
         return SHKV_ERR_INVALID_ARG;
-    if ((pages + batch) * c.num_kv_heads > INT32_MAX - 64 || len > kMaxTokens)   // warps, whole CTAs of them
+    if ((pages + batch) * c.num_kv_heads > INT32_MAX - 64 - batch || len > kMaxTokens)   // warps, whole CTAs of them
         return SHKV_ERR_UNSUPPORTED;
     p.k_pages = static_cast<uint4 *>(c.k_pages);
     p.v_pages = static_cast<uint4 *>(c.v_pages);
@@ -433,6 +433,9 @@ try {
     p.max_pages = c.max_pages_per_seq;
     p.num_pages = c.num_pages;
     p.check_lens = !lens;
+    // a source of the caller's that is no part of the pool's own table
+    const Span source = span_of(table, (size_t)batch * table_stride * 4);
+    p.at_once = table && (source.hi <= own.lo || own.hi <= source.lo);
     if (launch_evict(p, (cudaStream_t)stream) != cudaSuccess)
         return SHKV_ERR_CUDA;
     for (int b = 0; b < batch; ++b)

@@ -214,6 +214,42 @@ def test_an_index_in_no_order_into_other_masses():
         assert torch.equal(out[b, :, :60], old[b].gather(1, index[b].long()))
 
 
+@pytest.mark.parametrize("source", ["a copy", "the pool's own", "part of a wider one"])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 32)])
+@pytest.mark.parametrize("masses", [False, True])
+def test_a_named_source(source, d, page, masses):
+    """The table that the call reads may be the one that it writes."""
+    lens, keep = [700, 33, 0, 512, 90], [300, 40, 3, 511, 0]
+    c = Cache(lens, 3, d, page, seed=31, spare=70)
+    pool = c.pool()
+    if source == "the pool's own":
+        table = pool.block_table[:5]
+    else:
+        table = torch.full((5, c.table.shape[1] + 7), -1, dtype=torch.int32, device="cuda")
+        table[:, : c.table.shape[1]] = c.table.cuda()
+        table = table if source == "part of a wider one" else table[:, : c.table.shape[1]].contiguous()
+    index, new = drawn_index(c, keep, lens, seed=5), spare_table(c, keep, lens, width=2)
+    want_k, want_v = evicted(c, index, keep, new)
+    old = c.mass(extra=2)
+    mass = old.clone()
+    pool.evict_tokens(index, keep, new, mass=mass if masses else None, source=(table, lens))
+    assert pool.check_errors() == 0
+    assert torch.equal(c.k, want_k) and torch.equal(c.v, want_v)
+    assert pool.seq_lens.tolist() == pool.host_seq_lens().tolist() == [300, 33, 0, 511, 0]
+    for b, (L, n) in enumerate(zip(lens, keep)):
+        row = c.table[b].clone()
+        if n < L:
+            row[:] = -1
+            w = min(new.shape[1], len(row))
+            row[:w] = new[b, :w].cpu()
+        assert torch.equal(pool.block_table[b].cpu(), row)
+        if masses and n < L:
+            assert torch.equal(mass[b, :, :n], old[b].gather(1, index[b, :, :n].long()))
+            assert not mass[b, :, n:L].any() and torch.equal(mass[b, :, L:], old[b, :, L:])
+        else:
+            assert torch.equal(mass[b], old[b])
+
+
 def test_from_a_table_and_lengths_put_aside():
     """A shared prompt's pages, read for two requests at once, stay intact; a call may be repeated."""
     c = Cache([300], 2, 128, 16, seed=4, spare=30)
@@ -405,7 +441,8 @@ def test_a_session_within_a_budget_of_pages(d, page, hkv, group):
     assert pool.check_errors() == 0
 
 
-def test_a_decode_with_tails_right_behind_an_eviction():
+@pytest.mark.parametrize("aside", [False, True])
+def test_a_decode_with_tails_right_behind_an_eviction(aside):
     """Its unit kernel reads the block table that the eviction has just written."""
     c = Cache([3000, 2500], 2, 128, 16, seed=21, spare=400)
     pool = c.pool()
@@ -421,7 +458,7 @@ def test_a_decode_with_tails_right_behind_an_eviction():
         pool.block_table.copy_(old)
         pool.set_seq_lens(c.lens)
         tails.decode_attention(q)
-        pool.evict_tokens(index, keep, new)
+        pool.evict_tokens(index, keep, new, source=(old, c.lens) if aside else None)
         got = tails.decode_attention(q)
         torch.cuda.synchronize()
         if want is None:
