@@ -720,6 +720,7 @@ __device__ void add_up_wide(const MassParams &p, const Ctx<D> &c, uint32_t tmem,
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t s[32];
+                    __syncwarp();            // the load is the whole warp's, and lanes without a row skip a half
                     tmem_ld32_nowait(s_mine + 256u * (uint32_t)st.slot + 32u * h, s);
                     tmem_wait_ld();
                     if (h)
@@ -728,13 +729,13 @@ __device__ void add_up_wide(const MassParams &p, const Ctx<D> &c, uint32_t tmem,
                     int in = row_in;
                     asm volatile("" : "+r"(in)::"memory");
                     // a zero query of a row that is none and an infinite key make no number
-                    if (!in)
-                        continue;
-                    if (k >= plain)
-                        weigh_row32<false>(s, p.scale_log2, l, 32, acc + 16 * h);
-                    else                     // tokens up to past + the row's query token
-                        weigh_row32<true>(s, p.scale_log2, l, w.past + i - p.tpt + 1 - w.t0 - 64 * group - 32 * h,
-                                          acc + 16 * h);
+                    if (in) {
+                        if (k >= plain)
+                            weigh_row32<false>(s, p.scale_log2, l, 32, acc + 16 * h);
+                        else                 // tokens up to past + the row's query token
+                            weigh_row32<true>(s, p.scale_log2, l, w.past + i - p.tpt + 1 - w.t0 - 64 * group - 32 * h,
+                                              acc + 16 * h);
+                    }
                 }
             } else {
                 __syncwarp();
