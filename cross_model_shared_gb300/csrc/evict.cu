@@ -25,13 +25,16 @@ __device__ __forceinline__ uint32_t mass_key(float m)
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
-// Barrier of the row's CTAs; their shared memory is ordered by it.
+// Barrier of the row's CTAs; their shared memory is ordered by it.  (The cluster's
+// is a whole warp's instruction; lanes come from loops of different length.)
 __device__ __forceinline__ void row_sync(uint32_t ctas)
 {
-    if (ctas == 1)
+    if (ctas == 1) {
         __syncthreads();
-    else
-        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        return;
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Address of the same shared variable in CTA `rank` of the cluster.
