@@ -55,6 +55,15 @@ __host__ __device__ inline int mass_past(int len, int n_q, int causal) { return 
 // First block with a row that sees token t.
 __host__ __device__ inline int mass_block0(int t, int past, int tpt) { return t > past ? (t - past) / tpt : 0; }
 
+// First row of the block of query tokens i0 .. that sees token t of a tile that the
+// block sees.  0 where all rows do: the distance to a token far back, times the
+// group, would not fit 32 bits (34M tokens and 64 rows).
+__host__ __device__ inline int mass_first_row(int t, int past, int i0, int group)
+{
+    const int tokens = t - past - i0;
+    return tokens > 0 ? tokens * group : 0;
+}
+
 struct SelectParams {
     const float *mass;
     int64_t mass_request, mass_head, index_stride;

@@ -520,8 +520,9 @@ __device__ void add_up(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int 
             s_par ^= 1u;
             if (alive) {
                 tc_fence_after();
-                // query tokens before t - past do not see the thread's token
-                const int first_row = (t - w.past - i0) * p.group, latest = first_row + (31 - lane) * p.group;
+                // of the thread's token, and of the warp's last
+                const int first_row = mass_first_row(t, w.past, i0, p.group);
+                const int latest = mass_first_row(t + 31 - lane, w.past, i0, p.group);
 #pragma unroll 1
                 for (int h = 0; h < rows; h += 64)
                     sum += weigh(taddr + (uint32_t)h, c.lse(q.slot) + 4u * h, min(64, rows - h), first_row - h, latest - h,

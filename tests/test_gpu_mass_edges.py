@@ -1,6 +1,8 @@
-"""Masses at the edges of what the calls allow, against the definition in 64 bits: blocks that rows do not fill."""
+"""Masses at the edges of what the calls allow, against the definition in 64 bits."""
 import pytest
 import torch
+
+from cross_model_shared_gb300 import SharedKVPool
 
 from .eviction_common import Cache, check_mass, lse_of
 
@@ -19,3 +21,37 @@ def test_blocks_of_rows_that_end_inside_a_warp(n, group, d):
     got = pool.prefill_mass(q, lse, old, decay=0.5, scale=0.08, out=torch.zeros_like(old))
     assert pool.check_errors() == 0
     check_mass(c, q, lse, 0.08, True, 0.5, old, got)
+
+
+class Window:
+    """Tokens [t0, t1) of a long cache as a request of their own, for check_mass."""
+
+    def __init__(self, k, t0, t1):
+        self.lens, self.hkv, self.k = [t1 - t0], 1, k.view(-1, k.shape[-1])[t0:t1]
+
+    def rows(self, b):
+        return self.k.double()[None]
+
+
+def test_requests_whose_rows_times_tokens_pass_32_bits():
+    """34 million tokens of one KV head: 64 stacked rows of a decode, and two new tokens of 128 heads."""
+    d, P, L = 64, 32, 34_000_001
+    pages = -(-L // P)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k = torch.empty(pages, 1, P, d, dtype=torch.bfloat16, device="cuda")
+    for i in range(0, pages, 1 << 17):
+        k[i: i + (1 << 17)] = torch.randn(k[i: i + (1 << 17)].shape, generator=g, device="cuda", dtype=torch.bfloat16)
+    pool = SharedKVPool(pages, P, 1, d, max_batch=1, max_pages_per_seq=pages, k_pages=k, v_pages=k, initial_seq_lens=[L])
+    pool.block_table.copy_(torch.arange(pages, dtype=torch.int32)[None])
+    windows = [(0, 300_000), (L // 3, L // 3 + 1000), (33_554_432 - 400_000, L)]
+    windows += [(t, t + 1000) for t in (L - (1 << 25) - 500, L - (1 << 24) - 500, L // 2)]
+    for n, hq, causal in ((8, 8, False), (1, 64, False), (2, 128, True), (1, 128, True)):
+        q = torch.randn(1, n, hq, d, generator=g, device="cuda").to(torch.bfloat16)
+        lse = torch.full((1, n, hq), 3.0, device="cuda")
+        if causal:
+            got = pool.prefill_mass(q, lse, None, scale=0.1)
+        else:
+            got = pool.decode_mass(q.view(1, n * hq, d), lse.view(1, -1), n, None, scale=0.1)
+        assert pool.check_errors() == 0
+        for t0, t1 in windows:
+            check_mass(Window(k, t0, t1), q, lse, 0.1, causal and t1 == L, 1.0, None, got[:, :, t0:t1])
