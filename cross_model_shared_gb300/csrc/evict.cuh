@@ -90,11 +90,16 @@ struct EvictParams {
     int32_t page0[SHKV_MAX_BATCH + 1];   // new pages before each request
 };
 
-// What a row's log-sum-exp takes off its scores, in base 2: +inf for a row
-// that attends nothing, so that all its weights are 0.
-__device__ __forceinline__ float lse_base2(float lse)
+// What is added to a row's scores in base 2: its log-sum-exp off, at most the
+// largest number; kRowOut for a row that attends nothing.  Such a row is left out by
+// this mark: its scores may be infinite or no number, which adding -inf would not
+// make a weight of 0.
+constexpr float kRowOut = INFINITY, kLargest = 3.402823466e38f;
+
+__device__ __forceinline__ float lse_offset(float lse)
 {
-    return lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
+    const float l = lse * -1.4426950408889634f;
+    return lse == -INFINITY ? kRowOut : l == INFINITY ? kLargest : l;
 }
 
 }  // namespace shkv

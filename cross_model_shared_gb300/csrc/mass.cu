@@ -80,6 +80,8 @@ struct Ctx {
     __device__ uint32_t k_slot(int s) const { return base + (uint32_t)s * Ring<D>::kSlot; }
     __device__ uint32_t q_slot(int s) const { return base + Ring<D>::kQ0 + (uint32_t)s * Ring<D>::kSlot; }
     __device__ uint32_t lse(int s) const { return base + Ring<D>::kLse + (uint32_t)(s * kMassRows * 4); }
+    // a byte: whether a row of the block in slot s attends nothing
+    __device__ uint32_t outs(int s) const { return base + Ring<D>::kMisc + 8u + (uint32_t)s; }
     __device__ bool wait(uint32_t b, uint32_t parity) const { return q8_wait<true>(b, parity, abort_flag, err); }
 };
 
@@ -263,9 +265,8 @@ __device__ __forceinline__ void copy_block(const CUtensorMap *tm, const MassPara
             : "memory");
 }
 
-// The blocks of every head that the range comes to, and what their rows'
-// log-sum-exps take off the scores; a row beyond the block's, or one that attends
-// nothing, gets -inf and so weighs nothing.
+// The blocks of every head that the range comes to, what their rows' log-sum-exps
+// add to the scores, and whether one of the rows attends nothing.
 template <int D>
 __device__ void copy_q(const CUtensorMap *tm, const MassParams &p, const Ctx<D> &c)
 {
@@ -283,12 +284,15 @@ __device__ void copy_q(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
 #pragma unroll 1
         for (int k = 0; k < p.blocks; ++k) {
             const int i0 = k * p.tpt, rows = min(p.tpt, p.n_q - i0) * p.group;
-            float off[kMassRows / 32];
+            float l[kMassRows / 32];
+            bool out = false;
 #pragma unroll
             for (int j = 0; j < kMassRows / 32; ++j) {
                 const int r = lane + 32 * j;
-                off[j] = r < rows ? lse_base2(__ldg(src + (i0 + r / p.group) * p.lse_token + r % p.group)) : INFINITY;
+                l[j] = r < rows ? lse_offset(__ldg(src + (i0 + r / p.group) * p.lse_token + r % p.group)) : 0.f;
+                out = out || l[j] == kRowOut;
             }
+            out = __any_sync(0xffffffffu, out);
             bool ok = true;
             if (alive && lane == 0)
                 ok = c.wait(c.q_empty(turn.slot), turn.parity ^ 1u);
@@ -297,8 +301,10 @@ __device__ void copy_q(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
                 continue;
 #pragma unroll
             for (int j = 0; j < kMassRows / 32; ++j)
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(c.lse(turn.slot) + 4u * (uint32_t)(lane + 32 * j)), "f"(-off[j])
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(c.lse(turn.slot) + 4u * (uint32_t)(lane + 32 * j)), "f"(l[j])
                              : "memory");
+            if (lane == 0)
+                asm volatile("st.shared.u8 [%0], %1;" ::"r"(c.outs(turn.slot)), "r"((uint32_t)out) : "memory");
             __syncwarp();
             copy_block<D>(tm, p, c, w, k, turn.slot);
             ++issued;
@@ -405,8 +411,9 @@ __device__ __forceinline__ float4 load_shared4(uint32_t addr)
 }
 
 // The weights of 16 columns into partial sums, two values an instruction where
-// there is one for it; kMasked: of the columns [first, end) of them.
-template <bool kMasked>
+// there is one for it; kMasked: of the columns [first, end) of them; kOuts: of those
+// whose rows are not out.
+template <bool kMasked, bool kOuts = false>
 __device__ __forceinline__ void weigh16(const uint32_t *s, uint32_t lse, int first, int end, float c, float2 (&sum)[2])
 {
 #pragma unroll
@@ -421,6 +428,12 @@ __device__ __forceinline__ void weigh16(const uint32_t *s, uint32_t lse, int fir
             x0.y = j + 1 >= first && j + 1 < end ? x0.y : -INFINITY;
             x1.x = j + 2 >= first && j + 2 < end ? x1.x : -INFINITY;
             x1.y = j + 3 >= first && j + 3 < end ? x1.y : -INFINITY;
+        }
+        if (kOuts) {
+            x0.x = l.x != kRowOut ? x0.x : -INFINITY;
+            x0.y = l.y != kRowOut ? x0.y : -INFINITY;
+            x1.x = l.z != kRowOut ? x1.x : -INFINITY;
+            x1.y = l.w != kRowOut ? x1.y : -INFINITY;
         }
         sum[0] = __fadd2_rn(sum[0], make_float2(ex2_approx(x0.x), ex2_approx(x0.y)));
         sum[1] = __fadd2_rn(sum[1], make_float2(ex2_approx(x1.x), ex2_approx(x1.y)));
@@ -439,15 +452,15 @@ __device__ __forceinline__ void leave(uint32_t empty)
 // Sum of a thread's weights over columns [first, n) of S at taddr, n <= 64;
 // `latest` is the warp's largest `first`.  The columns that the MMA rounds rows up
 // to are zero queries, whose product with an infinite key is no number, so they
-// are left out.  `last`: the buffer is arrived on as empty as soon as its values
+// are left out, as are rows that attend nothing where there are some (`outs`).  `last`: the buffer is arrived on as empty as soon as its values
 // are in registers, and the next product into it runs beside the exponentials.
 // (No use of a score can move before its wait: it needs a log-sum-exp that is read
 // after it.)
-__device__ __forceinline__ float weigh(uint32_t taddr, uint32_t lse, int n, int first, int latest, float c, bool last,
-                                       uint32_t empty)
+__device__ __forceinline__ float weigh(uint32_t taddr, uint32_t lse, int n, int first, int latest, float c, bool outs,
+                                       bool last, uint32_t empty)
 {
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    if (n > 48 && latest <= 0) {             // nearly all blocks of a chunk: straight code
+    if (n > 48 && latest <= 0 && !outs) {    // nearly all blocks of a chunk: straight code
         uint32_t s[64];
         tmem_ld32_nowait(taddr, s);
         tmem_ld32_nowait(taddr + 32u, s + 32);
@@ -467,7 +480,9 @@ __device__ __forceinline__ float weigh(uint32_t taddr, uint32_t lse, int n, int 
             uint32_t s[16];
             tmem_ld16_nowait(taddr + (uint32_t)i, s);
             tmem_wait_ld();
-            if (i < latest || i + 16 > n)
+            if (outs)
+                weigh16<true, true>(s, lse + 4u * i, first - i, n - i, c, sum);
+            else if (i < latest || i + 16 > n)
                 weigh16<true>(s, lse + 4u * i, first - i, n - i, c, sum);
             else
                 weigh16<false>(s, lse + 4u * i, 0, 16, c, sum);
@@ -516,6 +531,8 @@ __device__ void add_up(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int 
             if (!w.sees(p, k, x))
                 continue;
             const int i0 = k * p.tpt, rows = min(p.tpt, p.n_q - i0) * p.group;
+            uint32_t outs;
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(outs) : "r"(c.outs(q.slot)));
             alive = __all_sync(0xffffffffu, alive && c.wait(c.s_full(four), s_par));
             s_par ^= 1u;
             if (alive) {
@@ -526,7 +543,7 @@ __device__ void add_up(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int 
 #pragma unroll 1
                 for (int h = 0; h < rows; h += 64)
                     sum += weigh(taddr + (uint32_t)h, c.lse(q.slot) + 4u * h, min(64, rows - h), first_row - h, latest - h,
-                                 p.scale_log2, h + 64 >= rows, c.s_empty(four));
+                                 p.scale_log2, outs != 0u, h + 64 >= rows, c.s_empty(four));
             } else if (lane == 0) {
                 mbar_arrive(c.s_empty(four));
             }
@@ -701,7 +718,7 @@ __device__ void add_up_wide(const MassParams &p, const Ctx<D> &c, uint32_t tmem,
         for (int j = 0; j < 32; ++j)
             acc[j] = make_float2(0.f, 0.f);
         // the row's query token in the next block, and the log-sum-exp, read a block
-        // ahead; a row behind the last weighs nothing (+inf is taken off)
+        // ahead; a row behind the last is out
         int i = w.begin * p.tpt + tok;
         const float *src = p.lse + w.b * p.lse_request + i * p.lse_token + w.g * p.group + row - tok * p.group;
         float lse = i < n_mine ? __ldg(src) : -INFINITY;
@@ -710,8 +727,8 @@ __device__ void add_up_wide(const MassParams &p, const Ctx<D> &c, uint32_t tmem,
         const int plain = rest > 0 ? (rest + p.tpt - 1) / p.tpt : 0;
 #pragma unroll 1
         for (int k = w.begin; k < w.end; ++k) {
-            const float l = -lse_base2(lse);
-            const bool row_in = i < n_mine;
+            const float l = lse_offset(lse);
+            const bool row_in = l != kRowOut;
             i += p.tpt;
             src += p.tpt * p.lse_token;
             lse = i < n_mine ? __ldg(src) : -INFINITY;
@@ -729,7 +746,7 @@ __device__ void add_up_wide(const MassParams &p, const Ctx<D> &c, uint32_t tmem,
                     // (no use of a score moves before its wait: the condition passes through it)
                     int in = row_in;
                     asm volatile("" : "+r"(in)::"memory");
-                    // a zero query of a row that is none and an infinite key make no number
+                    // (a zero query of a row that is none and an infinite key make no number)
                     if (in) {
                         if (k >= plain)
                             weigh_row32<false>(s, p.scale_log2, l, 32, acc + 16 * h);

@@ -55,3 +55,57 @@ def test_requests_whose_rows_times_tokens_pass_32_bits():
         assert pool.check_errors() == 0
         for t0, t1 in windows:
             check_mass(Window(k, t0, t1), q, lse, 0.1, causal and t1 == L, 1.0, None, got[:, :, t0:t1])
+
+
+@pytest.mark.parametrize("n,group", [(1, 5), (2, 16), (7, 4), (40, 5), (64, 3), (300, 3), (150, 9)])
+@pytest.mark.parametrize("what", ["nan", "inf", "inf key", "nan key"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_that_attend_nothing_add_nothing_whatever_they_hold(n, group, what, d):
+    """An lse of -inf takes a row out, also where its scores are no number or infinite: an inactive decoder's queries
+    may hold anything, and a key may be infinite."""
+    c = Cache([n + 500, n + 77], 2, d, 16, seed=n + group)
+    q = c.randn(2, n, 2 * group, d)
+    q[..., 0] = -q[..., 0].abs() - 1         # an infinite key below is -inf to the rows that attend
+    pool = c.pool()
+    scale = 0.05
+    lse = lse_of(c, q, scale, True)
+    dead = torch.rand(2, n, 2 * group, generator=c.g).cuda() < 0.3
+    dead[0, 0], dead[0, 0, 1] = True, False
+    dead[1, :, group:] = True                # a KV head that nobody attends
+    lse[dead] = -float("inf")
+    if what in ("nan", "inf"):
+        q[dead] = float(what)
+    else:
+        q[..., 0] = torch.where(dead, q[..., 0].abs(), q[..., 0])
+        for b, t in ((0, 5), (0, n + 499), (1, 30)):
+            row = c.k[int(c.table[b, t // 16]), :, t % 16]
+            row[:] = 0
+            row[:, 0] = float("inf")
+            if what == "nan key":            # of a head whose rows are all out
+                c.k[int(c.table[1, 1]), 1, 3] = float("nan")
+    old = c.mass()
+    for form in ("decode", "prefill"):
+        if form == "decode":
+            if n * group > 64:
+                continue
+            got = pool.decode_mass(q.view(2, -1, d), lse.view(2, -1), n, old, scale=scale, out=torch.zeros_like(old))
+        else:
+            got = pool.prefill_mass(q, lse, old, scale=scale, out=torch.zeros_like(old))
+        assert pool.check_errors() == 0 and not torch.isnan(got).any()
+        check_mass(c, q, lse, scale, form == "prefill", 1.0, old, got)
+        assert torch.equal(got[1, 1, : c.lens[1]], old[1, 1, : c.lens[1]])
+
+
+@pytest.mark.parametrize("n,group", [(2, 8), (60, 4), (300, 3)])
+def test_a_row_of_an_infinite_sum_weighs_its_infinite_key_as_no_number(n, group):
+    """An lse of +inf is that of a row with an infinite score: exp(inf - inf) there, 0 elsewhere."""
+    c = Cache([n + 100], 1, 128, 16, seed=n)
+    c.k[int(c.table[0, 0]), 0, 7] = 0
+    c.k[int(c.table[0, 0]), 0, 7, 0] = float("inf")
+    q = c.randn(1, n, group, 128)
+    q[..., 0] = q[..., 0].abs() + 1
+    pool = c.pool()
+    lse = torch.full((1, n, group), float("inf"), device="cuda")
+    lse[0, 0, 0] = -float("inf")
+    nan = torch.isnan(pool.prefill_mass(q, lse, None, scale=0.05))
+    assert nan[0, 0, 7] and int(nan.sum()) == 1
