@@ -389,7 +389,11 @@ constexpr int kMassPer = 16;         // masses of a thread and pass
 constexpr int kMassZeros = 8;
 
 // Masses of one (request, KV head), a CTA: a pass reads its masses before any is
-// written, and as positions ascend it writes only below what later passes read.
+// written, and as positions ascend it writes only below what later passes read.  A
+// token whose row is not copied gets 0: what its slot holds is not its own.  (The
+// tables are looked through first, and token by token only if a page is none: asked
+// of every token, 128K of them, the masses took longer than the rows: 143 us where
+// 125.)
 __device__ __forceinline__ void move_masses(const EvictParams &p, int row)
 {
     const int b = row / p.hkv, g = row % p.hkv;
@@ -399,6 +403,17 @@ __device__ __forceinline__ void move_masses(const EvictParams &p, int row)
     const int32_t *index = p.index + (int64_t)row * p.index_stride;
     const float *src = p.mass.in + b * p.mass.in_request + g * p.mass.in_head;
     float *dst = p.mass.out + b * p.mass.out_request + g * p.mass.out_head;
+    const int32_t *from = p.table + b * p.table_stride, *to = p.new_table + b * p.new_stride;
+    const int shift = p.page_size == 16 ? 4 : 5;
+    auto inside = [&](const int32_t *page) { return (uint32_t)__ldg(page) < (uint32_t)p.num_pages; };
+    bool bad = false;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < (L + p.page_size - 1) >> shift; i += kMoveThreads)
+        bad |= !inside(from + i);
+#pragma unroll 8
+    for (int i = threadIdx.x; i < (keep + p.page_size - 1) >> shift; i += kMoveThreads)
+        bad |= !inside(to + i);
+    bad = __syncthreads_or(bad);
     for (int j0 = 0; j0 < keep; j0 += kMassPer * kMoveThreads) {
         int i[kMassPer];
         float x[kMassPer];
@@ -410,6 +425,12 @@ __device__ __forceinline__ void move_masses(const EvictParams &p, int row)
 #pragma unroll
         for (int u = 0; u < kMassPer; ++u)
             x[u] = (uint32_t)i[u] < (uint32_t)L ? src[i[u]] : 0.f;
+        if (bad)
+#pragma unroll
+            for (int u = 0; u < kMassPer; ++u)
+                if ((uint32_t)i[u] < (uint32_t)L &&
+                    !(inside(from + (i[u] >> shift)) && inside(to + (j0 + u * kMoveThreads + threadIdx.x >> shift))))
+                    x[u] = 0.f;
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < kMassPer; ++u) {

@@ -2,8 +2,10 @@
 import pytest
 import torch
 
-from .eviction_common import check_selection
-from .test_gpu_evict import draw_masses, select_pool
+from cross_model_shared_gb300 import _native as N
+
+from .eviction_common import Cache, check_selection
+from .test_gpu_evict import draw_masses, drawn_index, select_pool, spare_table
 
 pytestmark = pytest.mark.gpu
 
@@ -19,3 +21,38 @@ def test_clusters_whose_lanes_write_unequally_many(lens, kind):
         keep = [min(L - 1, few + 3) for L in lens]
         check_selection(mass, lens, keep, 2, 1, pool.select_tokens(mass, keep, sink=2, recent=1))
     assert pool.check_errors() == 0
+
+
+@pytest.mark.parametrize("where", ["in place", "out"])
+@pytest.mark.parametrize("aside", [False, True])
+def test_a_token_that_is_not_copied_has_no_mass(where, aside):
+    """Its slot still holds what was there before: a mass beside it would have the next selection keep that."""
+    c = Cache([5000, 100], 2, 128, 16, seed=5, spare=330)
+    keep = [4500, 40]
+    index, new = drawn_index(c, keep, c.lens), spare_table(c, keep, c.lens)
+    k0, v0 = c.k.clone(), c.v.clone()
+    for bad in (-1, c.num, 2 ** 31 - 1, -2 ** 31):
+        for which in ("source", "new"):
+            c.k.copy_(k0), c.v.copy_(v0)
+            pool = c.pool()
+            table, to = c.table.cuda(), new.clone()
+            lost = torch.zeros(2, 2, 4500, dtype=torch.bool, device="cuda")
+            if which == "source":
+                table[0, 2], table[0, 300], table[1, 1] = bad, bad, bad
+                pool.block_table.copy_(table)
+                for b, pages in ((0, (2, 300)), (1, (1,))):
+                    for pg in pages:
+                        lost[b, :, : keep[b]] |= index[b, :, : keep[b]] // 16 == pg
+            else:
+                to[0, 0], to[0, 281], to[1, 1] = bad, bad, bad
+                lost[0, :, :16], lost[0, :, 281 * 16: 4500], lost[1, :, 16:32] = True, True, True
+            old = torch.rand(2, 2, 5000, generator=c.g).cuda() + 0.5
+            mass, out = old.clone(), torch.full_like(old, 7.0)
+            pool.evict_tokens(index, keep, to, mass=mass, out=out if where == "out" else None,
+                              source=(table, c.lens) if aside else None)
+            assert pool.check_errors() == N.SHKV_ERRF_PAGE_OOB
+            got = mass if where == "in place" else out
+            for b, n in enumerate(keep):
+                want = old[b].gather(1, index[b, :, :n].long()).masked_fill(lost[b, :, :n], 0.0)
+                assert lost[b].any() and torch.equal(got[b, :, :n], want)
+                assert not got[b, :, n: c.lens[b]].any()
