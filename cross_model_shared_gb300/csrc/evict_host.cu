@@ -214,9 +214,7 @@ shkv_status add_mass(shkv_pool *pool, int32_t batch, int32_t n_q, int32_t hq, co
         if (items > INT32_MAX)
             return SHKV_ERR_UNSUPPORTED;
     }
-    p.item0[batch] = (int32_t)items;
-    if (items == 0)
-        return SHKV_OK;
+    p.item0[batch] = (int32_t)items;     // 0: one CTA that looks at the lengths
     p.lse = lse;
     p.lse_request = lse_request;
     p.lse_token = lse_token;

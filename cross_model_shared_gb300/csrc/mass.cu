@@ -193,6 +193,15 @@ __device__ __forceinline__ bool walk_next(const MassParams &p, Walk &w)
 // open, and a parity wait takes that for the phase before it, which is over.
 __device__ __forceinline__ int tile_of(const MassParams &p, const Walk &w) { return w.item - p.cut_item[blockIdx.x]; }
 
+// Every request's length against the device's, requests without a token among them (in
+// the warp that copies K, behind its copies).
+__device__ __forceinline__ void check_lens(const MassParams &p)
+{
+    for (int b = 32 * blockIdx.x + (threadIdx.x & 31); b < p.batch; b += 32 * gridDim.x)
+        if (__ldg(p.seq_lens + b) != p.lens[b])
+            atomicOr(p.err, SHKV_ERRF_SEQ_LEN);
+}
+
 // K tiles, a lane per (column half, page) of a tile.  A lane also holds one of the
 // table entries of up to four tiles, read four tiles ahead.  A page outside the pool
 // is left out and flagged; the tile's threads look at their table entries themselves.
@@ -215,8 +224,6 @@ __device__ void copy_k(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
         Walk next = w;
         more = walk_next(p, next);
         const int next_id = more ? entry(next) : -1;
-        if (lane == 0 && w.fresh && w.at == 0 && w.g == 0 && __ldg(p.seq_lens + w.b) != w.L)
-            atomicOr(p.err, SHKV_ERRF_SEQ_LEN);
 #pragma unroll 1
         for (int x = 0; x < w.step; ++x) {
             const int slot = issued % Ring<D>::kK, page = __shfl_sync(0xffffffffu, id, (x * RB + rb) & 31);
@@ -580,8 +587,6 @@ __device__ void copy_k_wide(const CUtensorMap *tm, const MassParams &p, const Ct
         Walk next = w;
         more = walk_next(p, next);
         const int next_id = more ? entry(next) : -1;
-        if (lane == 0 && w.fresh && w.at == 0 && w.g == 0 && __ldg(p.seq_lens + w.b) != w.L)
-            atomicOr(p.err, SHKV_ERRF_SEQ_LEN);
         const bool there = lane < RB && w.t0 + lane * P < w.L, inside = there && (uint32_t)id < (uint32_t)p.num_pages;
         if (there && !inside)
             atomicOr(p.err, SHKV_ERRF_PAGE_OOB);
@@ -854,21 +859,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             add_up_wide<D>(p, c, tmem, warp / 4);
         } else {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-            if (warp == kKWarp)
+            if (warp == kKWarp) {
                 copy_k_wide<D>(&tm_k, p, c);
-            else if (warp == kQWarp)
+                check_lens(p);
+            } else if (warp == kQWarp) {
                 copy_q_wide<D>(&tm_q, p, c);
-            else if (warp == kMmaWarp)
+            } else if (warp == kMmaWarp) {
                 issue_wide<D>(p, c, tmem);
+            }
         }
-    } else if (warp == kKWarp)
+    } else if (warp == kKWarp) {
         copy_k<D>(&tm_k, p, c);
-    else if (warp == kQWarp)
+        check_lens(p);
+    } else if (warp == kQWarp) {
         copy_q<D>(&tm_q, p, c);
-    else if (warp >= kMmaWarp)
+    } else if (warp >= kMmaWarp) {
         issue<D>(p, c, tmem, warp - kMmaWarp);
-    else
+    } else {
         add_up<D>(p, c, tmem, warp / 4);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -3,6 +3,7 @@ import pytest
 import torch
 
 from cross_model_shared_gb300 import SharedKVPool
+from cross_model_shared_gb300 import _native as N
 
 from .eviction_common import Cache, check_mass, lse_of
 
@@ -109,3 +110,24 @@ def test_a_row_of_an_infinite_sum_weighs_its_infinite_key_as_no_number(n, group)
     lse[0, 0, 0] = -float("inf")
     nan = torch.isnan(pool.prefill_mass(q, lse, None, scale=0.05))
     assert nan[0, 0, 7] and int(nan.sum()) == 1
+
+
+@pytest.mark.parametrize("lens", [[300, 0, 20], [0, 0, 0], [0, 300, 0]])
+def test_a_replay_after_empty_requests_have_grown_is_flagged(lens):
+    c = Cache([300, 300, 300], 2, 128, 16, seed=4)
+    pool = c.pool(lens=lens)
+    q, lse = c.randn(3, 8, 128), torch.full((3, 8), 4.0, device="cuda")
+    mass = torch.zeros(3, 2, 300, device="cuda")
+    pool.decode_mass(q, lse, 1, mass)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pool.decode_mass(q, lse, 1, mass)
+    g.replay()
+    torch.cuda.synchronize()
+    assert pool.check_errors() == 0
+    for b in range(3):
+        pool.set_seq_lens([L + (1 if L < 300 else -1) * (i == b) for i, L in enumerate(lens)])
+        g.replay()
+        torch.cuda.synchronize()
+        assert pool.check_errors() == N.SHKV_ERRF_SEQ_LEN, b
