@@ -35,6 +35,12 @@ bool callable(const shkv_pool *pool, int32_t batch)
            cudaGetDevice(&dev) == cudaSuccess && dev == pool->device;
 }
 
+bool capturing(void *stream)
+{
+    cudaStreamCaptureStatus s = cudaStreamCaptureStatusNone;
+    return cudaStreamIsCapturing((cudaStream_t)stream, &s) == cudaSuccess && s == cudaStreamCaptureStatusActive;
+}
+
 int64_t longest(int32_t batch, const int32_t *lens)
 {
     int64_t n = 0;
@@ -390,8 +396,22 @@ try {
         pages += n;
     }
     p.page0[batch] = (int32_t)pages;     // at most SHKV_MAX_BATCH * max_pages_per_seq; checked below
-    if (!moves)
-        return SHKV_OK;
+    p.block_table = c.block_table;
+    p.seq_lens = c.seq_lens;
+    p.err = c.error_word;
+    p.batch = batch;
+    p.hkv = c.num_kv_heads;
+    p.head_dim = c.head_dim;
+    p.page_size = c.page_size;
+    p.max_pages = c.max_pages_per_seq;
+    p.num_pages = c.num_pages;
+    p.check_lens = !lens;
+    if (!moves) {
+        // nothing to launch, but a replay has to find out about lengths that it was not captured with
+        if (batch == 0 || lens || !capturing(stream))
+            return SHKV_OK;
+        return launch_evict(p, (cudaStream_t)stream) == cudaSuccess ? SHKV_OK : SHKV_ERR_CUDA;
+    }
     // the pool's table is written from new_table: no byte of one may be the other's
     const Span own = span_of(c.block_table, (size_t)c.max_batch * c.max_pages_per_seq * 4);
     const Span given = span_of(new_table, (size_t)batch * new_table_stride * 4);
@@ -421,16 +441,6 @@ try {
         p.mass.out_request = out->request_stride;
         p.mass.out_head = out->head_stride;
     }
-    p.block_table = c.block_table;
-    p.seq_lens = c.seq_lens;
-    p.err = c.error_word;
-    p.batch = batch;
-    p.hkv = c.num_kv_heads;
-    p.head_dim = c.head_dim;
-    p.page_size = c.page_size;
-    p.max_pages = c.max_pages_per_seq;
-    p.num_pages = c.num_pages;
-    p.check_lens = !lens;
     // a source of the caller's that is no part of the pool's own table
     const Span source = span_of(table, (size_t)batch * table_stride * 4);
     p.at_once = table && (source.hi <= own.lo || own.hi <= source.lo);

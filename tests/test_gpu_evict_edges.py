@@ -56,3 +56,23 @@ def test_a_token_that_is_not_copied_has_no_mass(where, aside):
                 want = old[b].gather(1, index[b, :, :n].long()).masked_fill(lost[b, :, :n], 0.0)
                 assert lost[b].any() and torch.equal(got[b, :, :n], want)
                 assert not got[b, :, n: c.lens[b]].any()
+
+
+def test_a_replay_that_moves_nobody_flags_requests_that_have_grown():
+    c = Cache([300, 77], 2, 128, 16, seed=3)
+    pool = c.pool(lens=[30, 0])
+    index = torch.zeros(2, 2, 40, dtype=torch.int32, device="cuda")
+    new = torch.full((2, 3), -1, dtype=torch.int32, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pool.evict_tokens(index, [40, 40], new)
+    g.replay()
+    torch.cuda.synchronize()
+    assert pool.check_errors() == 0
+    table = pool.block_table.clone()
+    for lens in ([200, 0], [30, 1], [29, 0]):
+        pool.set_seq_lens(lens)
+        g.replay()
+        torch.cuda.synchronize()
+        assert pool.check_errors() == N.SHKV_ERRF_SEQ_LEN, lens
+        assert torch.equal(pool.block_table, table) and pool.seq_lens.tolist() == lens
