@@ -76,3 +76,15 @@ def test_a_replay_that_moves_nobody_flags_requests_that_have_grown():
         torch.cuda.synchronize()
         assert pool.check_errors() == N.SHKV_ERRF_SEQ_LEN, lens
         assert torch.equal(pool.block_table, table) and pool.seq_lens.tolist() == lens
+
+
+def test_a_batch_of_empty_requests():
+    pool = Cache([0, 0, 0], 2, 64, 16).pool()
+    mass = torch.zeros(3, 2, 0, device="cuda")
+    index = pool.select_tokens(mass, [4, 4, 4], sink=1, recent=2)
+    assert index.shape == (3, 2, 1) and (index == -1).all()
+    index = torch.full((3, 2, 5), 9, dtype=torch.int32, device="cuda")
+    pool.select_tokens(mass, [4, 0, 4], out=index)
+    assert (index == -1).all()
+    pool.evict_tokens(index, [4, 0, 4], torch.zeros(3, 1, dtype=torch.int32, device="cuda"), mass=mass)
+    assert pool.host_seq_lens().tolist() == [0, 0, 0] and pool.check_errors() == 0

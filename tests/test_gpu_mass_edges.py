@@ -131,3 +131,14 @@ def test_a_replay_after_empty_requests_have_grown_is_flagged(lens):
         g.replay()
         torch.cuda.synchronize()
         assert pool.check_errors() == N.SHKV_ERRF_SEQ_LEN, b
+
+
+def test_a_batch_of_empty_requests():
+    pool = Cache([0, 0, 0], 2, 64, 16).pool()
+    q, lse = torch.zeros(3, 8, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(3, 8, device="cuda")
+    got = pool.decode_mass(q, lse, 2, None)
+    assert got.shape == (3, 2, 0)
+    assert pool.decode_mass(q, lse, 2, got) is got
+    out = torch.full((3, 2, 5), 7.0, device="cuda")
+    pool.decode_mass(q, lse, 2, got, out=out)
+    assert (out == 7).all() and pool.check_errors() == 0
