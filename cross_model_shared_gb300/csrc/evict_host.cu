@@ -190,16 +190,17 @@ shkv_status add_mass(shkv_pool *pool, int32_t batch, int32_t n_q, int32_t hq, co
 {
     const shkv_pool_config &c = pool->cfg;
     const int64_t row = (int64_t)hq * c.head_dim;
-    if (n_q == 1)                        // a stride that no step is taken along
-        q_token = row, lse_token = 0;
+    if (n_q == 1)                        // a stride that no step is taken along: one that divides the requests'
+        q_token = c.head_dim, lse_token = 0;
     if (q_token >= (int64_t)1 << 39)     // a tensor map's strides are below 2^40 bytes
         return SHKV_ERR_UNSUPPORTED;
     if (batch == 1)
         q_request = n_q * q_token, lse_request = 0;
     const float scale_log2 = (float)((double)scale * 1.4426950408889634);
     const int64_t len = longest(batch, pool->lens.data());
-    if (!q || !aligned(q, 16) || !lse || !aligned(lse, 4) || q_token < row || q_token % c.head_dim || q_request <= 0 ||
-        q_request % q_token || lse_request < 0 || lse_token < 0 || !isfinite(scale_log2) || !isfinite(decay) ||
+    if (!q || !aligned(q, 16) || !lse || !aligned(lse, 4) || (n_q > 1 && q_token < row) || q_token % c.head_dim ||
+        q_request <= 0 || q_request % q_token || lse_request < 0 || lse_token < 0 || !isfinite(scale_log2) ||
+        !isfinite(decay) ||
         !writable(out, batch, c.num_kv_heads, len) ||
         (mass && (!readable(mass, len) || (len > 0 && !same_layout(mass, out, batch, c.num_kv_heads)))))
         return SHKV_ERR_INVALID_ARG;

@@ -136,7 +136,8 @@ class EvictionCalls:
         and lse fp32 [B, n_new, hq] of the same ``prefill_attention``.  Slices
         of both (``q[:, -64:]``) make the chunk's last tokens a window of
         voters: a token's own rows have to be contiguous, tokens a multiple of
-        head_dim elements apart and requests a multiple of the tokens' stride."""
+        head_dim elements apart and requests a multiple of the tokens' stride
+        (of head_dim, for one token each)."""
         shape, stride = q.shape, q.stride()
         if q.dtype is not _BF16 or q.device != self.k_pages.device or len(shape) != 4 or shape[3] != self.head_dim:
             raise ValueError(f"q must be bfloat16 [B, n_new, hq, head_dim] on {self.k_pages.device}")

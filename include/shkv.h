@@ -707,7 +707,9 @@ shkv_status shkv_decode_mass(shkv_pool *pool, int32_t batch, int32_t n_models, i
  *   q    device bf16, token i's rows [hq_per_model, head_dim] at element
  *        b * q_request_stride + i * q_token_stride: the token stride a multiple
  *        of head_dim, at least hq_per_model * head_dim, the request stride a
- *        multiple of the token stride, above 0
+ *        multiple of the token stride, above 0.  With n_new = 1 the token
+ *        stride is not looked at and the request stride a multiple of head_dim.
+ *        With batch = 1 the request stride is not looked at
  *   lse  device fp32, token i's [hq_per_model] at element
  *        b * lse_request_stride + i * lse_token_stride, not negative
  *   workspace, workspace_bytes

@@ -142,3 +142,22 @@ def test_a_batch_of_empty_requests():
     out = torch.full((3, 2, 5), 7.0, device="cuda")
     pool.decode_mass(q, lse, 2, got, out=out)
     assert (out == 7).all() and pool.check_errors() == 0
+
+
+@pytest.mark.parametrize("T", [1, 5, 8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_new_token_out_of_a_fused_projection(T, d):
+    """q, k and v heads of a token side by side: the token stride is no multiple of its query heads'."""
+    c = Cache([100, 450, 33], 8, d, 16, seed=T)
+    pool = c.pool()
+    qkv = c.randn(3, T, 48, d)
+    q = qkv[:, -1:, :32]
+    lse = lse_of(c, q, 0.07, True)
+    fused = torch.zeros(3, T, 48, device="cuda")
+    fused[:, -1:, :32] = lse
+    got = pool.prefill_mass(q, fused[:, -1:, :32], None, scale=0.07)
+    assert pool.check_errors() == 0
+    check_mass(c, q, lse, 0.07, True, 1.0, None, got)
+    assert torch.equal(pool.prefill_mass(q.contiguous(), lse, None, scale=0.07), got)
+    one = pool.prefill_mass(q[:1], lse[:1], None, scale=0.07)
+    check_mass(c, q[:1], lse[:1], 0.07, True, 1.0, None, one, requests=[0])
