@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 namespace shkv {
@@ -32,6 +33,23 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), int grid, int block, uint32_t sme
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+// Registers a thread of a kernel's build, asked for once and kept in `known`
+// (0: not yet).  Pools of several host threads may come here at once.
+template <typename Kernel>
+cudaError_t kernel_registers(Kernel *kern, std::atomic<int> &known, int *regs)
+{
+    *regs = known.load(std::memory_order_relaxed);
+    if (*regs != 0)
+        return cudaSuccess;
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+    if (e == cudaSuccess) {
+        *regs = fa.numRegs;
+        known.store(fa.numRegs, std::memory_order_relaxed);
+    }
+    return e;
 }
 
 }  // namespace shkv

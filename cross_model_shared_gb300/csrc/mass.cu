@@ -925,16 +925,10 @@ cudaError_t launch_mass(const CUtensorMap &tm_k, const CUtensorMap &tm_q, const 
     const uint32_t smem = p.head_dim == 64 ? Ring<64>::kBytes : Ring<128>::kBytes;
     // a build whose launch has other registers than setmaxnreg hands out could wait
     // for some forever: it is refused
-    static int regs[2] = {0, 0};
-    int &r = regs[p.head_dim == 64];
-    cudaError_t e = cudaSuccess;
-    if (wide && r == 0) {
-        cudaFuncAttributes fa;
-        e = cudaFuncGetAttributes(&fa, kern);
-        if (e == cudaSuccess)
-            r = fa.numRegs;
-    }
-    if (e == cudaSuccess && wide && r != (int)kLaunchRegs)
+    static std::atomic<int> known[2];
+    int regs = (int)kLaunchRegs;
+    cudaError_t e = wide ? kernel_registers(kern, known[p.head_dim == 64], &regs) : cudaSuccess;
+    if (e == cudaSuccess && regs != (int)kLaunchRegs)
         e = cudaErrorInvalidConfiguration;
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

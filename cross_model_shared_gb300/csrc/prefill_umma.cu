@@ -39,6 +39,7 @@
 #include <stdint.h>
 
 #include "shkv_device.cuh"
+#include "launch.cuh"
 #include "prefill.cuh"
 
 namespace shkv {
@@ -703,18 +704,14 @@ cudaError_t launch_prefill_umma(const CUtensorMap &tmK, const CUtensorMap &tmV, 
     // The setmaxnreg split hands out exactly the registers the CTA is launched
     // with (168 a thread): a build with another count is refused rather than
     // launched, since its setmaxnreg.inc could wait for registers forever.
-    static int num_regs = -1;
-    if (num_regs < 0) {
-        cudaFuncAttributes fa;
-        cudaError_t e = cudaFuncGetAttributes(&fa, shkv_prefill_umma_kernel);
-        if (e != cudaSuccess)
-            return e;
-        num_regs = fa.numRegs;
-    }
+    static std::atomic<int> known;
+    int num_regs;
+    cudaError_t e = kernel_registers(shkv_prefill_umma_kernel, known, &num_regs);
+    if (e != cudaSuccess)
+        return e;
     if ((uint32_t)num_regs * kPThreads != kPSoftmaxRegs * 256 + kPOtherRegs * 128)
         return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaFuncSetAttribute(shkv_prefill_umma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    e = cudaFuncSetAttribute(shkv_prefill_umma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return e;
     shkv_prefill_umma_kernel<<<grid, kPThreads, smem, stream>>>(tmK, tmV, p);

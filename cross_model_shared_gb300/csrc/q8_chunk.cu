@@ -1041,18 +1041,15 @@ __global__ void __launch_bounds__(256) shkv_q8_chunk_join_kernel(const __grid_co
 cudaError_t launch_q8_chunk(const CUtensorMap &tmK, const CUtensorMap &tmV, const Q8ChunkParams &p, bool splits,
                             cudaStream_t stream)
 {
-    static int regs = -1;      // the register split hands out exactly the launch's 128 a thread
-    if (regs < 0) {
-        cudaFuncAttributes fa;
-        const cudaError_t e = cudaFuncGetAttributes(&fa, shkv_q8_chunk_kernel);
-        if (e != cudaSuccess)
-            return e;
-        regs = fa.numRegs;
-    }
+    static std::atomic<int> known;
+    int regs;                  // the register split hands out exactly the launch's 128 a thread
+    cudaError_t e = kernel_registers(shkv_q8_chunk_kernel, known, &regs);
+    if (e != cudaSuccess)
+        return e;
     if ((uint32_t)regs * kThreads != kSoftmaxRegs * 256 + kOtherRegs * 256)
         return cudaErrorInvalidConfiguration;
     const uint32_t smem = smem_layout().total;
-    cudaError_t e = cudaFuncSetAttribute(shkv_q8_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(shkv_q8_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess)
         e = launch_pdl(shkv_q8_chunk_kernel, p.num_ctas, kThreads, smem, stream, tmK, tmV, p);
     if (e != cudaSuccess || !splits)

@@ -1461,19 +1461,15 @@ namespace {
 template <int NR>
 cudaError_t launch_nr(const CUtensorMap &tmK, const CUtensorMap &tmV, const Q8DecodeParams &q, cudaStream_t stream)
 {
-    static int regs = -1;      // the register split hands out exactly the launch's 128 a thread
-    if (regs < 0) {
-        cudaFuncAttributes fa;
-        const cudaError_t e = cudaFuncGetAttributes(&fa, shkv_q8_decode_kernel<NR>);
-        if (e != cudaSuccess)
-            return e;
-        regs = fa.numRegs;
-    }
+    static std::atomic<int> known;
+    int regs;                  // the register split hands out exactly the launch's 128 a thread
+    cudaError_t e = kernel_registers(shkv_q8_decode_kernel<NR>, known, &regs);
+    if (e != cudaSuccess)
+        return e;
     if ((uint32_t)regs * kThreads != kSoftmaxRegs * 256 + kOtherRegs * 256)
         return cudaErrorInvalidConfiguration;
     constexpr uint32_t smem = smem_layout(NR).total;
-    const cudaError_t e =
-        cudaFuncSetAttribute(shkv_q8_decode_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(shkv_q8_decode_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return e;
     return launch_pdl(shkv_q8_decode_kernel<NR>, q.d.num_ctas, kThreads, smem, stream, tmK, tmV, q);
