@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
         uint32_t k[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            k[i] = mass_key(t + i < w1 ? __ldg(m + t + i) : -INFINITY);
+            k[i] = mass_key(t + i < w1 ? m[t + i] : -INFINITY);
         return make_uint4(k[0], k[1], k[2], k[3]);
     };
     uint32_t prefix = 0u, need = chosen, equal = 0u;     // of the keys with this prefix; keys with all its digits
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
             auto load = [&](int t) {
 #pragma unroll
                 for (int u = 0; u < kU; ++u)
-                    x[u] = t + u * 32 + lane < w1 ? __ldg(m + t + u * 32 + lane) : -INFINITY;
+                    x[u] = t + u * 32 + lane < w1 ? m[t + u * 32 + lane] : -INFINITY;
             };
             load(w0);
             __syncthreads();                             // the histograms are empty
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     } else {
         for (int t0 = w0; t0 < w1; t0 += 32) {
             const int t = t0 + lane;
-            const uint32_t k = t >= w1 ? 0u : cached ? own[t] : mass_key(__ldg(m + t));
+            const uint32_t k = t >= w1 ? 0u : cached ? own[t] : mass_key(m[t]);
             const bool up = k > prefix, eq = k == prefix;
             const uint32_t ups = __ballot_sync(0xffffffffu, up), eqs = __ballot_sync(0xffffffffu, eq);
             const uint32_t pe = ne + __popc(eqs & below), at = na + __popc(ups & below) + min(pe, need);
@@ -405,7 +405,7 @@ __device__ __forceinline__ void move_masses(const EvictParams &p, int row)
     float *dst = p.mass.out + b * p.mass.out_request + g * p.mass.out_head;
     const int32_t *from = p.table + b * p.table_stride, *to = p.new_table + b * p.new_stride;
     const int shift = p.page_size == 16 ? 4 : 5;
-    auto inside = [&](const int32_t *page) { return (uint32_t)__ldg(page) < (uint32_t)p.num_pages; };
+    auto inside = [&](const int32_t *page) { return (uint32_t)*page < (uint32_t)p.num_pages; };
     bool bad = false;
 #pragma unroll 8
     for (int i = threadIdx.x; i < (L + p.page_size - 1) >> shift; i += kMoveThreads)
@@ -420,7 +420,7 @@ __device__ __forceinline__ void move_masses(const EvictParams &p, int row)
 #pragma unroll
         for (int u = 0; u < kMassPer; ++u) {
             const int j = j0 + u * kMoveThreads + threadIdx.x;
-            i[u] = j < keep ? __ldg(index + j) : -1;
+            i[u] = j < keep ? index[j] : -1;
         }
 #pragma unroll
         for (int u = 0; u < kMassPer; ++u)
@@ -504,18 +504,18 @@ __global__ void __launch_bounds__(kMoveThreads, 3) shkv_evict_kernel(const __gri
             hi = mid;
     }
     const int j0 = (page - p.page0[b]) * P, n = min(P, p.keep[b] - j0);
-    const int to = __ldg(p.new_table + b * p.new_stride + j0 / P);
+    const int to = p.new_table[b * p.new_stride + j0 / P];
     bool ok = (uint32_t)to < (uint32_t)p.num_pages;
     int row = 0;                                         // of the lane's token (a pool's rows fit 32 bits)
     if (!ok) {
         atomicOr(p.err, SHKV_ERRF_PAGE_OOB);
     } else if (lane < n) {
-        const int i = __ldg(p.index + ((int64_t)b * p.hkv + g) * p.index_stride + j0 + lane);
+        const int i = p.index[((int64_t)b * p.hkv + g) * p.index_stride + j0 + lane];
         ok = (uint32_t)i < (uint32_t)p.lens[b];
         if (!ok) {
             atomicOr(p.err, SHKV_ERRF_INDEX);
         } else {
-            const int from = __ldg(p.table + b * p.table_stride + i / P);
+            const int from = p.table[b * p.table_stride + i / P];
             ok = (uint32_t)from < (uint32_t)p.num_pages;
             if (!ok)
                 atomicOr(p.err, SHKV_ERRF_PAGE_OOB);

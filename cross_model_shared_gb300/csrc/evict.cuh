@@ -9,6 +9,10 @@
 
 namespace shkv {
 
+// These kernels may start while the one before them in the stream still writes what
+// they read after their wait (log-sum-exps, masses, indexes, tables), so they read
+// it by ordinary loads: __ldg wants data that stays as it is for a kernel's lifetime.
+
 // Masses read and written; `in` may be null (nothing to read).
 struct MassIo {
     const float *in;

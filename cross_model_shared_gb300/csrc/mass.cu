@@ -198,7 +198,7 @@ __device__ __forceinline__ int tile_of(const MassParams &p, const Walk &w) { ret
 __device__ __forceinline__ void check_lens(const MassParams &p)
 {
     for (int b = 32 * blockIdx.x + (threadIdx.x & 31); b < p.batch; b += 32 * gridDim.x)
-        if (__ldg(p.seq_lens + b) != p.lens[b])
+        if (p.seq_lens[b] != p.lens[b])
             atomicOr(p.err, SHKV_ERRF_SEQ_LEN);
 }
 
@@ -214,7 +214,7 @@ __device__ void copy_k(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
     const uint64_t pol = l2_evict_first_policy();
     auto entry = [&](const Walk &w) {
         const int pg = w.t0 / P + lane;
-        return lane < w.step * RB && pg * P < w.L ? __ldg(p.block_table + (int64_t)w.b * p.max_pages + pg) : -1;
+        return lane < w.step * RB && pg * P < w.L ? p.block_table[(int64_t)w.b * p.max_pages + pg] : -1;
     };
     Walk w;
     bool alive = true, more = walk_first(p, w);
@@ -296,7 +296,7 @@ __device__ void copy_q(const CUtensorMap *tm, const MassParams &p, const Ctx<D> 
 #pragma unroll
             for (int j = 0; j < kMassRows / 32; ++j) {
                 const int r = lane + 32 * j;
-                l[j] = r < rows ? lse_offset(__ldg(src + (i0 + r / p.group) * p.lse_token + r % p.group)) : 0.f;
+                l[j] = r < rows ? lse_offset(src[(i0 + r / p.group) * p.lse_token + r % p.group]) : 0.f;
                 out = out || l[j] == kRowOut;
             }
             out = __any_sync(0xffffffffu, out);
@@ -528,7 +528,7 @@ __device__ void add_up(const MassParams &p, const Ctx<D> &c, uint32_t tmem, int 
         float old = 0.f, sum = 0.f;
         int page = -1;
         if (t < w.L) {                       // looked at when the sum is there
-            page = __ldg(p.block_table + (int64_t)w.b * p.max_pages + t / p.page_size);
+            page = p.block_table[(int64_t)w.b * p.max_pages + t / p.page_size];
             if (p.mass.in)
                 old = p.mass.in[w.b * p.mass.in_request + w.g * p.mass.in_head + t];
         }
@@ -577,7 +577,7 @@ __device__ void copy_k_wide(const CUtensorMap *tm, const MassParams &p, const Ct
     const uint64_t pol = l2_evict_first_policy();
     auto entry = [&](const Walk &w) {
         const int pg = w.t0 / P + lane;
-        return lane < RB && pg * P < w.L ? __ldg(p.block_table + (int64_t)w.b * p.max_pages + pg) : -1;
+        return lane < RB && pg * P < w.L ? p.block_table[(int64_t)w.b * p.max_pages + pg] : -1;
     };
     Walk w;
     Turn turn;
@@ -726,7 +726,7 @@ __device__ void add_up_wide(const MassParams &p, const Ctx<D> &c, uint32_t tmem,
         // ahead; a row behind the last is out
         int i = w.begin * p.tpt + tok;
         const float *src = p.lse + w.b * p.lse_request + i * p.lse_token + w.g * p.group + row - tok * p.group;
-        float lse = i < n_mine ? __ldg(src) : -INFINITY;
+        float lse = i < n_mine ? *src : -INFINITY;
         // blocks from which on all of the warp's rows see all of its tokens
         const int rest = w.t0 + 64 * group + 63 - w.past - tok0;
         const int plain = rest > 0 ? (rest + p.tpt - 1) / p.tpt : 0;
@@ -736,7 +736,7 @@ __device__ void add_up_wide(const MassParams &p, const Ctx<D> &c, uint32_t tmem,
             const bool row_in = l != kRowOut;
             i += p.tpt;
             src += p.tpt * p.lse_token;
-            lse = i < n_mine ? __ldg(src) : -INFINITY;
+            lse = i < n_mine ? *src : -INFINITY;
             alive = __all_sync(0xffffffffu, alive && c.wait(c.s_full(st.slot), st.parity));
             if (alive && mine > 0) {
                 tc_fence_after();
@@ -790,7 +790,7 @@ __device__ void add_up_wide(const MassParams &p, const Ctx<D> &c, uint32_t tmem,
             for (int i = 0; i < 4; ++i)
                 asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i]) : "r"(sums + (uint32_t)(i * kWide + threadIdx.x) * 4u));
             const int t = w.t0 + threadIdx.x;
-            const bool inside = (uint32_t)__ldg(p.block_table + (int64_t)w.b * p.max_pages + t / p.page_size) <
+            const bool inside = (uint32_t)p.block_table[(int64_t)w.b * p.max_pages + t / p.page_size] <
                                 (uint32_t)p.num_pages;
             const float sum = inside ? (v[0] + v[1]) + (v[2] + v[3]) : 0.f;
             if (!w.whole(p))
