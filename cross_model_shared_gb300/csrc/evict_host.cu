@@ -38,7 +38,10 @@ bool callable(const shkv_pool *pool, int32_t batch)
 bool capturing(void *stream)
 {
     cudaStreamCaptureStatus s = cudaStreamCaptureStatusNone;
-    return cudaStreamIsCapturing((cudaStream_t)stream, &s) == cudaSuccess && s == cudaStreamCaptureStatusActive;
+    if (cudaStreamIsCapturing((cudaStream_t)stream, &s) == cudaSuccess)
+        return s == cudaStreamCaptureStatusActive;
+    cudaGetLastError();                  // the default stream beside a capture: no error of this call's
+    return false;
 }
 
 int64_t longest(int32_t batch, const int32_t *lens)
