@@ -391,9 +391,10 @@ constexpr int kMassZeros = 8;
 // Masses of one (request, KV head), a CTA: a pass reads its masses before any is
 // written, and as positions ascend it writes only below what later passes read.  A
 // token whose row is not copied gets 0: what its slot holds is not its own.  (The
-// tables are looked through first, and token by token only if a page is none: asked
-// of every token, 128K of them, the masses took longer than the rows: 143 us where
-// 125.)
+// tables are looked through first, and token by token only if a page is none, in a
+// walk of its own: one row of 131072 to half 43 us (d 64) and 40 (d 128), 37 and 40
+// without the look;
+// asked in the passes 54: their 16 masses were no longer loaded together.)
 __device__ __forceinline__ void move_masses(const EvictParams &p, int row)
 {
     const int b = row / p.hkv, g = row % p.hkv;
@@ -405,14 +406,21 @@ __device__ __forceinline__ void move_masses(const EvictParams &p, int row)
     float *dst = p.mass.out + b * p.mass.out_request + g * p.mass.out_head;
     const int32_t *from = p.table + b * p.table_stride, *to = p.new_table + b * p.new_stride;
     const int shift = p.page_size == 16 ? 4 : 5;
-    auto inside = [&](const int32_t *page) { return (uint32_t)*page < (uint32_t)p.num_pages; };
+    auto inside = [&](int page) { return (uint32_t)page < (uint32_t)p.num_pages; };
     bool bad = false;
-#pragma unroll 8
-    for (int i = threadIdx.x; i < (L + p.page_size - 1) >> shift; i += kMoveThreads)
-        bad |= !inside(from + i);
-#pragma unroll 8
-    for (int i = threadIdx.x; i < (keep + p.page_size - 1) >> shift; i += kMoveThreads)
-        bad |= !inside(to + i);
+    auto look = [&](const int32_t *pages, int n) {
+        for (int i0 = threadIdx.x; i0 < n; i0 += kMassPer * kMoveThreads) {
+            int x[kMassPer];
+#pragma unroll
+            for (int u = 0; u < kMassPer; ++u)
+                x[u] = i0 + u * kMoveThreads < n ? pages[i0 + u * kMoveThreads] : 0;
+#pragma unroll
+            for (int u = 0; u < kMassPer; ++u)
+                bad = bad || !inside(x[u]);
+        }
+    };
+    look(from, (L + p.page_size - 1) >> shift);
+    look(to, (keep + p.page_size - 1) >> shift);
     bad = __syncthreads_or(bad);
     for (int j0 = 0; j0 < keep; j0 += kMassPer * kMoveThreads) {
         int i[kMassPer];
@@ -425,12 +433,6 @@ __device__ __forceinline__ void move_masses(const EvictParams &p, int row)
 #pragma unroll
         for (int u = 0; u < kMassPer; ++u)
             x[u] = (uint32_t)i[u] < (uint32_t)L ? src[i[u]] : 0.f;
-        if (bad)
-#pragma unroll
-            for (int u = 0; u < kMassPer; ++u)
-                if ((uint32_t)i[u] < (uint32_t)L &&
-                    !(inside(from + (i[u] >> shift)) && inside(to + (j0 + u * kMoveThreads + threadIdx.x >> shift))))
-                    x[u] = 0.f;
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < kMassPer; ++u) {
@@ -440,6 +442,12 @@ __device__ __forceinline__ void move_masses(const EvictParams &p, int row)
         }
     }
     __syncthreads();
+    if (bad)
+        for (int j = threadIdx.x; j < keep; j += kMoveThreads) {
+            const int i = index[j];
+            if ((uint32_t)i < (uint32_t)L && !(inside(from[i >> shift]) && inside(to[j >> shift])))
+                dst[j] = 0.f;
+        }
     for (int j0 = keep + threadIdx.x; j0 < L; j0 += kMassZeros * kMoveThreads)
 #pragma unroll
         for (int u = 0; u < kMassZeros; ++u)
