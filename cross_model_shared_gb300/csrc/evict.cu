@@ -392,9 +392,9 @@ constexpr int kMassZeros = 8;
 // written, and as positions ascend it writes only below what later passes read.  A
 // token whose row is not copied gets 0: what its slot holds is not its own.  (The
 // tables are looked through first, and token by token only if a page is none, in a
-// walk of its own: one row of 131072 to half 43 us (d 64) and 40 (d 128), 37 and 40
-// without the look;
-// asked in the passes 54: their 16 masses were no longer loaded together.)
+// walk of its own: one row of 131072 to half 43 us (d 64) and 40 (d 128), without the
+// look 37 and 40; asked in the passes 54, whose 16 masses were then not loaded
+// together.)
 __device__ __forceinline__ void move_masses(const EvictParams &p, int row)
 {
     const int b = row / p.hkv, g = row % p.hkv;
@@ -473,11 +473,11 @@ __device__ __forceinline__ void commit_request(const EvictParams &p, int b)
 }  // namespace
 
 // The first CTAs write tables and lengths, where the move reads a table of the
-// caller's (one launch less: 4.2 -> 2.8 us for a short request, 3 us of the host), the
-// next ones move masses.  The others copy rows, a warp per (new page, KV head): K's
+// caller's (one launch less than from the pool's own: 1 to 2 us of the GPU, up to 2 of
+// the host), the next ones move masses.  The others copy rows, a warp per (new page, KV head): K's
 // and V's rows of 32 / (2 D / 8) tokens an instruction, eight instructions' loads
 // before their stores.  Bound by HBM: 48 requests to half, 491 MB, 78 us (94% of a
-// copy's rate).  The eight loads need 72 registers, three CTAs an SM: left to itself the
+// copy's rate).  The eight loads need 72 to 76 registers, three CTAs an SM: left to itself the
 // compiler took 56 and loaded fewer at once (104 us; 16 loads of a thread 90, 4 and five
 // CTAs 81); stores that stay longer in L2 81 us.
 template <int D>

@@ -111,8 +111,11 @@ size_t piece_bytes(const shkv_pool *pool)
 
 // Cuts the items into at most `limit` ranges of about equal cost, counted in
 // products of a tile and a block of rows (0.3 us); an item costs kItemCost more (its
-// K's copy, the join of its threads' sums; 1, 4, 8, 12: a document 592, 588, 581,
-// 575 us, ten drawn chunks 24.7, 23.9, 23.9, 23.9 us in the mean).  An item of many
+// K's copy, the join of its threads' sums).  A compromise: at 1 and 4 a document takes
+// 2 and 1% more; at 12 and 16 it takes 1 and 2% less (573, 566, 560 us at 8, 12, 16),
+// as do a few requests of 8K (29.2, 28.0, 27.4), but chunks without much before them
+// up to 6% more (283 tokens 11.6, 12.3, 12.3; 1889 tokens 16.0, 16.5, 16.6); ten drawn
+// chunks are the same in the mean.  An item of many
 // blocks may be cut between two of them, but not into pieces of under kMinPiece
 // blocks.  (Leaving items whole where a cut seemed dearer than the second kernel
 // gained nothing: 24.2 us.)  True if an item is cut.

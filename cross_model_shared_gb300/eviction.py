@@ -199,9 +199,11 @@ class EvictionCalls:
         request of the call reads; its row becomes the request's, with the pages
         it names for tokens to come
         mass: masses that move along: to the front of the request's row, zeros
-        behind them up to the old length, into ``out`` (``mass`` itself if None)
+        behind them up to the old length, into ``out`` (``mass`` itself if None:
+        the index must ascend then; another ``out`` must not overlap ``mass``)
         source: (table, lens) that say where the tokens are, instead of the
-        pool's own: int32 [B, W'] on the device, and a host list."""
+        pool's own: int32 [B, W'] on the device, and a host list.  A table that
+        is no part of the pool's saves the call its second launch."""
         k = _HostInts(keep, "keep")
         device = self.k_pages.device
         if index.dtype is not _I32 or index.device != device or index.dim() != 3 or not index.is_contiguous() or \

@@ -661,7 +661,8 @@ shkv_status shkv_q8_chunk_attention(shkv_q8_pool *pool, int32_t batch, const int
  * be of any length from zero on.  A call captured into a CUDA graph replays
  * with the lengths of its capture (the host copy of a length changes with the
  * call, as an append's does); SHKV_ERRF_SEQ_LEN is set where the device copy of
- * a length then differs.
+ * a length then differs, of empty requests as of others (a move that is given the
+ * lengths compares none).
  *
  * Masses: fp32, mass of token t < length of request b and KV head g at
  * data[b * request_stride + g * head_stride + t] (strides in elements, any
