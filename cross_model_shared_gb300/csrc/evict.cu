@@ -474,12 +474,12 @@ __device__ __forceinline__ void commit_request(const EvictParams &p, int b)
 
 // The first CTAs write tables and lengths, where the move reads a table of the
 // caller's (one launch less than from the pool's own: 1 to 2 us of the GPU, up to 2 of
-// the host), the next ones move masses.  The others copy rows, a warp per (new page, KV head): K's
-// and V's rows of 32 / (2 D / 8) tokens an instruction, eight instructions' loads
-// before their stores.  Bound by HBM: 48 requests to half, 491 MB, 78 us (94% of a
-// copy's rate).  The eight loads need 72 to 76 registers, three CTAs an SM: left to itself the
-// compiler took 56 and loaded fewer at once (104 us; 16 loads of a thread 90, 4 and five
-// CTAs 81); stores that stay longer in L2 81 us.
+// the host), the next ones move masses.  The others copy rows, a warp per (new page,
+// KV head): K's and V's rows of 32 / (2 D / 8) tokens an instruction, eight
+// instructions' loads before their stores.  Bound by HBM: 48 requests to half, 491 MB,
+// 79 us (93% of a copy's rate).  The eight loads need 72 to 76 registers, three CTAs an
+// SM: left to itself the compiler took 56 and loaded fewer at once (104 us; 16 loads of
+// a thread 90, 4 and five CTAs 81); stores that stay longer in L2 81 us.
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads, 3) shkv_evict_kernel(const __grid_constant__ EvictParams p)
 {

@@ -57,7 +57,8 @@ constexpr int32_t kMaxTokens = 1 << 30;   // of a request: the kernels step past
 // Masses of up to `len` tokens that a call reads; of none they may be anywhere.
 bool readable(const shkv_mass *m, int64_t len)
 {
-    return m && (len == 0 || (m->data && aligned(m->data, 4))) && m->request_stride >= 0 && m->head_stride >= 0 && m->length >= len;
+    return m && (len == 0 || (m->data && aligned(m->data, 4))) && m->request_stride >= 0 && m->head_stride >= 0 &&
+           m->length >= len;
 }
 
 // Masses that a call writes: the rows of `len` must not overlap, whichever of
@@ -206,8 +207,7 @@ shkv_status add_mass(shkv_pool *pool, int32_t batch, int32_t n_q, int32_t hq, co
     const int64_t len = longest(batch, pool->lens.data());
     if (!q || !aligned(q, 16) || !lse || !aligned(lse, 4) || (n_q > 1 && q_token < row) || q_token % c.head_dim ||
         q_request <= 0 || q_request % q_token || lse_request < 0 || lse_token < 0 || !isfinite(scale_log2) ||
-        !isfinite(decay) ||
-        !writable(out, batch, c.num_kv_heads, len) ||
+        !isfinite(decay) || !writable(out, batch, c.num_kv_heads, len) ||
         (mass && (!readable(mass, len) || (len > 0 && !same_layout(mass, out, batch, c.num_kv_heads)))))
         return SHKV_ERR_INVALID_ARG;
     if (q_request >= (int64_t)1 << 39 || len > kMaxTokens)
